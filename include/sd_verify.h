@@ -39,6 +39,10 @@
  * sd_fanout_schedule (host), sd_fanout_topk, sd_fanout_hits,
  * sd_verify_linear_fanout, sd_presto_init, sd_presto_expand,
  * sd_branch_fork; each call with a workspace has a *_workspace query.
+ * Around the verify step: sd_kv_append and sd_paged_attention (the target's
+ * forward pass over a chunk of drafts and its paged cache) and
+ * sd_distill_topk (and _backward, _step: training the drafter on the
+ * target's top logits).
  *
  * Conventions shared by every call:
  *  - Every tensor argument is a DEVICE pointer owned by the caller, row-major
@@ -78,7 +82,12 @@ typedef enum {
   SD_ERR_CUDA = 3         /* a CUDA runtime call failed */
 } sd_status;
 
-typedef enum { SD_F32 = 0, SD_BF16 = 1 } sd_dtype;
+typedef enum {
+  SD_F32 = 0,
+  SD_BF16 = 1,
+  SD_F16 = 2 /* queries, keys and values only (sd_kv_append,
+                sd_paged_attention) */
+} sd_dtype;
 
 /* device status bits */
 #define SD_DEV_BAD_TOKEN 1  /* a draft token outside [0, V): that test rejects */
@@ -89,6 +98,11 @@ typedef enum { SD_F32 = 0, SD_BF16 = 1 } sd_dtype;
 #define SD_DEV_ZERO_MASS 8  /* a residual had zero mass: drawn from p instead */
 #define SD_DEV_TIMEOUT 16   /* a bounded wait on an asynchronous copy gave up:
                                the call's outputs are not to be trusted */
+#define SD_DEV_BAD_LENGTH 32 /* paged cache: a sequence's chunk or key count
+                                is impossible (see sd_paged_kv) */
+#define SD_DEV_BAD_PAGE 64   /* paged cache: a page the sequence needs is
+                                outside [0, num_pages) */
+#define SD_DEV_BAD_POSITION 128 /* append: a position outside the table */
 
 /* Limits (SD_ERR_UNSUPPORTED beyond them). */
 #define SD_MAX_V (1 << 24)     /* vocabulary size */
@@ -96,6 +110,7 @@ typedef enum { SD_F32 = 0, SD_BF16 = 1 } sd_dtype;
 #define SD_MAX_K 32            /* candidates (kcand); lookahead positions - 1 (fan-out) */
 #define SD_MAX_TREE_NODES 1024 /* nodes per tree */
 #define SD_MAX_FANOUT 64       /* F_k per position */
+#define SD_MAX_DISTILL_K 256   /* teacher entries per row (distillation) */
 
 const char *sd_version(void);
 const char *sd_last_error(void);
@@ -520,6 +535,165 @@ sd_status sd_verify_linear_fanout(
  * ------------------------------------------------------------------- */
 sd_status sd_selftest_bounded_wait(int polls, int32_t *dev_status,
                                    int32_t *out, void *stream);
+
+/* ---------------------------------------------------------------------
+ * Paged cache of keys and values (the state that the target model's
+ * forward pass keeps between rounds), and chunks of new tokens over it.
+ *
+ * The pages of a cache hold page_size tokens each.  Element d of head h of
+ * token t of page p lies at p page_stride + t token_stride + h head_stride
+ * + d (strides in elements, the same for k and v), so both the token-major
+ * and the head-major order of a page are described by the strides.
+ * Sequence b's key j lies at token j % page_size of page
+ * block_table[b][j / page_size].
+ *
+ * A call takes the new tokens of B sequences packed one sequence after the
+ * other: those of sequence b are rows q_start[b] .. q_start[b+1] - 1 of the
+ * call's tensors (q_start [B+1], q_start[0] = 0), n = q_start[b+1] -
+ * q_start[b] >= 0 of them, and they are the last n of its kv_len[b] keys:
+ * token i has index kv_len[b] - n + i.  Lengths of zero are allowed.
+ * A sequence is unusable, and sets SD_DEV_BAD_LENGTH if a call has rows of
+ * it, unless 0 <= q_start[b] <= q_start[b+1] <= total and n <= kv_len[b] <=
+ * max_pages page_size.
+ * ------------------------------------------------------------------- */
+typedef struct {
+  void *k, *v;              /* device */
+  sd_dtype dt;              /* SD_BF16 or SD_F16 */
+  int num_pages, page_size; /* page_size: a multiple of 8 */
+  int heads, head_dim;      /* of keys and values */
+  long long page_stride, token_stride, head_stride;
+  const int32_t *block_table; /* device [B, max_pages] */
+  int max_pages;
+} sd_paged_kv;
+
+/* ---------------------------------------------------------------------
+ * Append the new tokens' keys and values to the cache, with the rotary
+ * position embedding applied to the keys (and to the queries) on the way.
+ *
+ * k, v [total, heads, head_dim] and q [total, q_heads, head_dim]
+ *     (nullable), of the cache's type: a token's heads are contiguous, the
+ *     tokens k_stride, v_stride, q_stride elements apart (so all three may
+ *     be parts of one projection's output).
+ * cos_sin [max_pos, rot_dim] float (nullable: no rotation): row `pos`
+ *     holds the cosines, then the sines, of the rot_dim / 2 angles of
+ *     position pos.  Pair i of a head, (x_i, y_i), becomes (x_i c_i - y_i
+ *     s_i, x_i s_i + y_i c_i); its elements are (i, i + rot_dim / 2), or
+ *     (2 i, 2 i + 1) when `interleaved`.  Elements from rot_dim on are
+ *     copied.  rot_dim is even and at most head_dim.  fp32 arithmetic, one
+ *     rounding.
+ * positions [total] int32 (nullable): each token's row of cos_sin.  The
+ *     default is its index in the sequence; a token tree passes its nodes'
+ *     depths added to the prefix length.
+ * q_out [total, q_heads, head_dim], contiguous: the rotated queries (must
+ *     not overlap q).  The keys and values go to the cache.
+ * A token of an unusable sequence, or whose page is not in [0, num_pages)
+ * (SD_DEV_BAD_PAGE), or whose position is outside [0, max_pos)
+ * (SD_DEV_BAD_POSITION), writes nothing to the cache; its q_out is zero.
+ * Rows that belong to no sequence are left as they are.
+ * ------------------------------------------------------------------- */
+sd_status sd_kv_append(const sd_paged_kv *cache, const void *k,
+                       long long k_stride, const void *v, long long v_stride,
+                       const void *q, long long q_stride, int q_heads,
+                       const int32_t *q_start, const int32_t *kv_len,
+                       const int32_t *positions, const float *cos_sin,
+                       int max_pos, int rot_dim, int interleaved, int B,
+                       int total, void *q_out, int32_t *dev_status,
+                       void *stream);
+
+/* ---------------------------------------------------------------------
+ * Attention of the new tokens over the paged cache (their own keys and
+ * values included: append first).
+ *
+ * q [total, q_heads, head_dim] of the cache's type, a token's heads
+ *     contiguous, tokens q_stride elements apart; q_heads is a multiple of
+ *     the cache's heads, query head h reads cache head h / (q_heads /
+ *     heads).  head_dim is 64 or 128.
+ * out[t, h] = sum_j w_j v_j / sum_j w_j, w_j = exp(scale q.k_j), over the
+ *     keys j that token t sees: every key before the chunk, and of the
+ *     chunk either the tokens up to itself (tree_mask null) or those whose
+ *     bit is set: bit (i & 31) of tree_mask[t][i / 32] is token i of the
+ *     sequence's chunk.  tree_mask [total, mask_words] int32; chunks longer
+ *     than 32 mask_words are unusable (SD_DEV_BAD_LENGTH).  scale > 0.
+ * out [total, q_heads, head_dim], contiguous, of the cache's type.
+ * lse [total, q_heads] float (nullable): log sum_j w_j.
+ * A token that sees no key gets out = 0 and lse = -inf.  The tokens of an
+ * unusable sequence whose q_start is usable, and of a sequence with a
+ * page outside [0, num_pages) among the ones it reads (SD_DEV_BAD_PAGE),
+ * get NaN.  Rows of no sequence are left as they are.  What the cache holds
+ * at and past kv_len never reaches a result.  A NaN or an infinity in a
+ * key or value before kv_len reaches the tokens that see it, and may reach
+ * others of the sequence.
+ * Products are of the cache's type with fp32 sums; the weights w_j are
+ * rounded to the cache's type before they multiply v; maxima, sums and the
+ * output's sum are fp32.
+ *
+ * max_q: the longest chunk, a hint: it picks the tile shape and never
+ *     changes which results are computed.
+ * Workspace: sd_paged_attention_workspace(...) bytes with the same max_q.
+ * ------------------------------------------------------------------- */
+size_t sd_paged_attention_workspace(int q_heads, int heads, int head_dim,
+                                    int max_q);
+
+sd_status sd_paged_attention(const void *q, long long q_stride, int q_heads,
+                             const sd_paged_kv *cache, const int32_t *q_start,
+                             const int32_t *kv_len, const int32_t *tree_mask,
+                             int mask_words, int B, int total, int max_q,
+                             float scale, void *out, float *lse,
+                             int32_t *dev_status, void *workspace,
+                             size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------
+ * Distillation of a drafter from the target's top logits.
+ *
+ * Row n has K teacher entries: ids teacher_id[n][k] and the target's
+ * logits teacher_logit[n][k] (for instance sd_fanout_topk's out_tokens and
+ * out_logit).  With p_k = exp(z_k / T) normalised over the row's entries,
+ * or, when teacher_lse [N] is given, p_k = exp(z_k / T - teacher_lse[n])
+ * (teacher_lse: log sum exp(z / T) over the target's whole row, so the p_k
+ * are the target's own probabilities), P = sum_k p_k, and q =
+ * softmax(student row / T) over all V columns:
+ *
+ *   loss[n] = sum_k p_k (log p_k - log q_{id_k})
+ *   grad[n][j] = grad_loss[n] / T (P q_j - sum_{k: id_k = j} p_k)
+ *
+ * which is d(sum_n grad_loss[n] loss[n]) / d student[n][j].
+ * student [N, V], fp32 or bf16, rows row_stride >= V elements apart; grad
+ * likewise with grad_stride, of the student's type.  teacher_logit float,
+ * teacher_id int32 [N, K], 1 <= K <= SD_MAX_DISTILL_K.  T > 0.
+ * lse [N]: log sum_j exp(student_j / T), an output of the forward calls and
+ * an input of the backward one.
+ * An entry with id < 0 is padding; one with id >= V is treated as padding
+ * and sets SD_DEV_BAD_TOKEN.  An entry with logit -inf has p = 0 and adds
+ * nothing, whatever the student's logit.  Repeated ids each count.  A row
+ * without usable entries has loss 0 and gradient 0.  A student logit of
+ * -inf has q = 0.  A row (student's or teacher's) that holds NaN or +inf, or
+ * a student row of only -inf, has loss and lse NaN, gradient NaN and sets
+ * SD_DEV_NONFINITE.  A row with grad_loss exactly 0 gets a gradient of
+ * exactly 0 (its student row is not read by the backward call).
+ * grad may be the student's own buffer (same pointer and stride).
+ * sd_distill_topk_step is the forward and the backward call together; it
+ * reads the student's rows once where they are 16-byte aligned and fit
+ * on chip.
+ * ------------------------------------------------------------------- */
+sd_status sd_distill_topk(const void *student, long long row_stride,
+                          sd_dtype dt, const float *teacher_logit,
+                          const int32_t *teacher_id, const float *teacher_lse,
+                          int N, int V, int K, float T, float *loss,
+                          float *lse, int32_t *dev_status, void *stream);
+
+sd_status sd_distill_topk_backward(
+    const void *student, long long row_stride, sd_dtype dt, const float *lse,
+    const float *teacher_logit, const int32_t *teacher_id,
+    const float *teacher_lse, const float *grad_loss, int N, int V, int K,
+    float T, void *grad, long long grad_stride, int32_t *dev_status,
+    void *stream);
+
+sd_status sd_distill_topk_step(
+    const void *student, long long row_stride, sd_dtype dt,
+    const float *teacher_logit, const int32_t *teacher_id,
+    const float *teacher_lse, const float *grad_loss, int N, int V, int K,
+    float T, float *loss, float *lse, void *grad, long long grad_stride,
+    int32_t *dev_status, void *stream);
 
 #ifdef __cplusplus
 }

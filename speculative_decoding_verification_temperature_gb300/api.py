@@ -17,9 +17,10 @@ import torch
 from . import build as _build
 
 SD_OK, SD_ERR_INVALID_ARG, SD_ERR_UNSUPPORTED, SD_ERR_CUDA = 0, 1, 2, 3
-SD_F32, SD_BF16 = 0, 1
+SD_F32, SD_BF16, SD_F16 = 0, 1, 2
 DEV_BAD_TOKEN, DEV_NONFINITE, DEV_BAD_PARENT, DEV_ZERO_MASS = 1, 2, 4, 8
 DEV_TIMEOUT = 16
+DEV_BAD_LENGTH, DEV_BAD_PAGE, DEV_BAD_POSITION = 32, 64, 128
 
 _lock = threading.Lock()
 _lib = None
@@ -50,6 +51,7 @@ def lib() -> ctypes.CDLL:
 def _declare(L):
     P, I, F, D, Z = (ctypes.c_void_p, ctypes.c_int, ctypes.c_float,
                      ctypes.c_double, ctypes.c_size_t)
+    LL = ctypes.c_longlong
     sig = {
         "sd_version": ([], ctypes.c_char_p),
         "sd_last_error": ([], ctypes.c_char_p),
@@ -86,6 +88,16 @@ def _declare(L):
         "sd_verify_linear_fanout_workspace": ([I, I, I, I], Z),
         "sd_verify_linear_fanout": ([P, P, I, P, P, I, I, I, F, P, P, P, P,
                                      P, P, P, P, Z, P], I),
+        "sd_kv_append": ([P, P, LL, P, LL, P, LL, I, P, P, P, P, I, I, I, I,
+                          I, P, P, P], I),
+        "sd_paged_attention_workspace": ([I, I, I, I], Z),
+        "sd_paged_attention": ([P, LL, I, P, P, P, P, I, I, I, I, F, P, P, P,
+                                P, Z, P], I),
+        "sd_distill_topk": ([P, LL, I, P, P, P, I, I, I, F, P, P, P, P], I),
+        "sd_distill_topk_backward": ([P, LL, I, P, P, P, P, P, I, I, I, F, P,
+                                      LL, P, P], I),
+        "sd_distill_topk_step": ([P, LL, I, P, P, P, P, I, I, I, F, P, P, P,
+                                  LL, P, P], I),
         "sd_tune_set": ([I, I], I),
         "sd_selftest_bounded_wait": ([I, P, P, P], I),
         "sd_tune_get": ([I], I),
@@ -594,3 +606,269 @@ def verify_linear_fanout(target, draft, tokens, uniforms, T, F, *,
         ws.numel(), _stream(dev)))
     return {"n": n, "tokens": toks, "prob": prob,
             "fan_tokens": ftok[:, :total], "fan_logit": flog[:, :total]}
+
+
+class _PagedKVStruct(ctypes.Structure):
+    """sd_paged_kv of include/sd_verify.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("dt", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int),
+                ("page_stride", ctypes.c_longlong),
+                ("token_stride", ctypes.c_longlong),
+                ("head_stride", ctypes.c_longlong),
+                ("block_table", ctypes.c_void_p),
+                ("max_pages", ctypes.c_int)]
+
+
+_CACHE_DT = {torch.bfloat16: SD_BF16, torch.float16: SD_F16}
+
+
+class PagedKV:
+    """A paged cache of keys and values (sd_paged_kv).
+
+    k, v [num_pages, page_size, heads, head_dim], bfloat16 or float16, the
+    last dimension contiguous and the others strided alike in both (a
+    head-major page is ``t.transpose(1, 2)`` of [num_pages, heads,
+    page_size, head_dim]); block_table [B, max_pages] int32, the page of
+    each page_size keys of a sequence.  The tensors are kept, not copied:
+    the program may change them between calls."""
+
+    def __init__(self, k, v, block_table):
+        dev = k.device
+        for t, name in ((k, "k"), (v, "v")):
+            if not t.is_cuda:
+                raise ValueError("%s must be a CUDA tensor (there is no CPU "
+                                 "path)" % name)
+            if t.dtype not in _CACHE_DT:
+                raise TypeError("%s must be bfloat16 or float16, got %s" %
+                                (name, t.dtype))
+            if t.dim() != 4 or t.stride(3) != 1:
+                raise ValueError("%s must be [pages, page_size, heads, "
+                                 "head_dim] with a contiguous last dimension"
+                                 % name)
+        if v.device != dev or v.dtype != k.dtype or v.shape != k.shape or \
+                v.stride() != k.stride():
+            raise ValueError("k and v must have one device, dtype, shape and "
+                             "strides")
+        _dev(block_table, dev, "block_table", torch.int32)
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [B, max_pages]")
+        self.k, self.v, self.block_table = k, v, block_table
+        n, page, heads, dim = k.shape
+        self.B, self.heads, self.head_dim = block_table.shape[0], heads, dim
+        self._struct = _PagedKVStruct(
+            k.data_ptr(), v.data_ptr(), _CACHE_DT[k.dtype], n, page, heads,
+            dim, k.stride(0), k.stride(1), k.stride(2),
+            block_table.data_ptr(), block_table.shape[1])
+        self._addr = ctypes.addressof(self._struct)
+
+
+def _rows(t, cache, name, heads=None):
+    """Packed rows [total, heads, head_dim] of the cache's type, a row's
+    heads contiguous; returns the stride between rows."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor (there is no CPU path)"
+                         % name)
+    if t.device != cache.k.device:
+        raise ValueError("%s must live on %s" % (name, cache.k.device))
+    if t.dtype != cache.k.dtype:
+        raise TypeError("%s must be %s" % (name, cache.k.dtype))
+    d = cache.head_dim
+    if t.dim() != 3 or t.shape[2] != d or \
+            (heads is not None and t.shape[1] != heads):
+        raise ValueError("%s must be [total, %s, %d]" %
+                         (name, heads or "heads", d))
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (s1 != d and t.shape[1] > 1):
+        raise ValueError("%s: a row's heads must be contiguous" % name)
+    return s0 if t.shape[0] > 1 else max(s0, t.shape[1] * d)
+
+
+def _lengths(cache, q_start, kv_len):
+    dev = cache.k.device
+    _dev(q_start, dev, "q_start", torch.int32)
+    _dev(kv_len, dev, "kv_len", torch.int32)
+    B = kv_len.numel()
+    if q_start.numel() != B + 1:
+        raise ValueError("q_start must have one entry more than kv_len")
+    if B > cache.B:
+        raise ValueError("block_table has %d rows for %d sequences" %
+                         (cache.B, B))
+    return B
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def kv_append(cache, k, v, q_start, kv_len, *, q=None, cos_sin=None,
+              positions=None, interleaved=False, status=None):
+    """Append new tokens' keys and values to a PagedKV, rotated by position
+    (sd_kv_append).
+
+    k, v [total, heads, D] and q [total, q_heads, D] (optional), rows may be
+    strided; q_start [B+1] and kv_len [B] int32 (kv_len counts the new
+    tokens); cos_sin [max_pos, rot_dim] float32, cosines then sines (None:
+    no rotation); positions [total] int32 (None: the index in the sequence).
+    Returns the rotated queries (None without q)."""
+    dev = cache.k.device
+    ks, vs = _rows(k, cache, "k", cache.heads), _rows(v, cache, "v",
+                                                      cache.heads)
+    total = k.shape[0]
+    if v.shape[0] != total:
+        raise ValueError("k and v must have the same number of rows")
+    B = _lengths(cache, q_start, kv_len)
+    qs = Hq = max_pos = rot = 0
+    out = None
+    if q is not None:
+        qs, Hq = _rows(q, cache, "q"), q.shape[1]
+        if q.shape[0] != total:
+            raise ValueError("q and k must have the same number of rows")
+        out = torch.empty((total, Hq, cache.head_dim), dtype=q.dtype,
+                          device=dev)
+    if cos_sin is not None:
+        _dev(cos_sin, dev, "cos_sin", torch.float32)
+        max_pos, rot = cos_sin.shape
+    if positions is not None:
+        _dev(positions, dev, "positions", torch.int32)
+        if positions.numel() != total:
+            raise ValueError("positions must be [total]")
+    _check(lib().sd_kv_append(
+        cache._addr, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q), qs, Hq,
+        q_start.data_ptr(), kv_len.data_ptr(), _ptr(positions),
+        _ptr(cos_sin), max_pos, rot, 1 if interleaved else 0, B, total,
+        _ptr(out), _ptr(status), _stream(dev)))
+    return out
+
+
+def paged_attention(q, cache, q_start, kv_len, *, max_q=None, scale=None,
+                    tree_mask=None, want_lse=False, status=None,
+                    workspace=None):
+    """Attention of a chunk of new tokens per sequence over a PagedKV
+    (sd_paged_attention); their keys and values are appended before.
+
+    q [total, q_heads, D], rows may be strided; q_start [B+1], kv_len [B]
+    int32.  tree_mask [total, words] int32 (None: causal): the tokens of its
+    own chunk that each token sees, as bits.  max_q: the longest chunk, a
+    hint that only picks the tile shape (default: the mean chunk).  scale
+    defaults to D ** -0.5.  Returns out [total, q_heads, D] (and lse [total,
+    q_heads] float32 when want_lse)."""
+    dev = cache.k.device
+    qs = _rows(q, cache, "q")
+    total, Hq, D = q.shape
+    B = _lengths(cache, q_start, kv_len)
+    words = 0
+    if tree_mask is not None:
+        _dev(tree_mask, dev, "tree_mask", torch.int32)
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != total:
+            raise ValueError("tree_mask must be [total, words]")
+        words = tree_mask.shape[1]
+    if max_q is None:
+        max_q = -(-total // max(B, 1))
+    out = torch.empty((total, Hq, D), dtype=q.dtype, device=dev)
+    lse = torch.empty((total, Hq), dtype=torch.float32,
+                      device=dev) if want_lse else None
+    L = lib()
+    nbytes = L.sd_paged_attention_workspace(Hq, cache.heads, D, max_q)
+    ws = (workspace or _default_ws).get(dev, nbytes)
+    _check(L.sd_paged_attention(
+        q.data_ptr(), qs, Hq, cache._addr, q_start.data_ptr(),
+        kv_len.data_ptr(), _ptr(tree_mask), words, B, total, max_q,
+        D ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse),
+        _ptr(status), ws.data_ptr(), ws.numel(), _stream(dev)))
+    return {"out": out, "lse": lse} if want_lse else {"out": out}
+
+
+def _distill_rows(student, teacher_logit, teacher_id, teacher_lse):
+    dev = student.device
+    if not student.is_cuda:
+        raise ValueError("student must be a CUDA tensor (there is no CPU "
+                         "path)")
+    if student.dim() != 2 or student.stride(1) != 1:
+        raise ValueError("student must be [N, V] rows with unit stride")
+    N, V = student.shape
+    _dev(teacher_logit, dev, "teacher_logit", torch.float32)
+    _dev(teacher_id, dev, "teacher_id", torch.int32)
+    if teacher_logit.dim() != 2 or teacher_logit.shape[0] != N or \
+            teacher_id.shape != teacher_logit.shape:
+        raise ValueError("teacher_logit and teacher_id must be [N, K]")
+    _dev(teacher_lse, dev, "teacher_lse", torch.float32)
+    if teacher_lse is not None and teacher_lse.numel() != N:
+        raise ValueError("teacher_lse must be [N]")
+    return dev, N, V, teacher_logit.shape[1], \
+        student.stride(0) if N > 1 else max(student.stride(0), V)
+
+
+def _row_vector(t, dev, name, N):
+    _dev(t, dev, name, torch.float32)
+    if t.numel() != N:
+        raise ValueError("%s must be [N]" % name)
+
+
+def _grad_out(out, student, dev, N, V):
+    """The gradient's buffer and row stride (a new one without `out`)."""
+    if out is None:
+        return torch.empty((N, V), dtype=student.dtype, device=dev), V
+    if not out.is_cuda or out.device != dev or out.dtype != student.dtype \
+            or tuple(out.shape) != (N, V) or out.stride(1) != 1:
+        raise ValueError("out must be [N, V] rows with unit stride, of the "
+                         "student's type and device")
+    return out, out.stride(0) if N > 1 else max(out.stride(0), V)
+
+
+def distill_topk(student, teacher_logit, teacher_id, T=1.0, *,
+                 teacher_lse=None, status=None):
+    """KL from the target's top-K logits to the drafter's softmax
+    (sd_distill_topk): student [N, V] float32 or bfloat16 (rows may be
+    strided), teacher_logit [N, K] float32, teacher_id [N, K] int32 (-1:
+    padding), teacher_lse [N] float32 (None: the K probabilities are
+    normalised among themselves).  Returns loss [N] and lse [N] (log sum
+    exp(student / T), which the backward call takes)."""
+    dev, N, V, K, rs = _distill_rows(student, teacher_logit, teacher_id,
+                                     teacher_lse)
+    loss = torch.empty(N, dtype=torch.float32, device=dev)
+    lse = torch.empty(N, dtype=torch.float32, device=dev)
+    _check(lib().sd_distill_topk(
+        student.data_ptr(), rs, _dt(student), teacher_logit.data_ptr(),
+        teacher_id.data_ptr(), _ptr(teacher_lse), N, V, K, T,
+        loss.data_ptr(), lse.data_ptr(), _ptr(status), _stream(dev)))
+    return {"loss": loss, "lse": lse}
+
+
+def distill_topk_backward(student, lse, teacher_logit, teacher_id, grad_loss,
+                          T=1.0, *, teacher_lse=None, out=None, status=None):
+    """Gradient of sum_n grad_loss[n] loss[n] of distill_topk with respect to
+    the student's logits (sd_distill_topk_backward); lse as distill_topk
+    returned it.  ``out`` may be the student itself.  Returns grad [N, V] of
+    the student's type."""
+    dev, N, V, K, rs = _distill_rows(student, teacher_logit, teacher_id,
+                                     teacher_lse)
+    _row_vector(lse, dev, "lse", N)
+    _row_vector(grad_loss, dev, "grad_loss", N)
+    grad, gs = _grad_out(out, student, dev, N, V)
+    _check(lib().sd_distill_topk_backward(
+        student.data_ptr(), rs, _dt(student), lse.data_ptr(),
+        teacher_logit.data_ptr(), teacher_id.data_ptr(), _ptr(teacher_lse),
+        grad_loss.data_ptr(), N, V, K, T, grad.data_ptr(), gs, _ptr(status),
+        _stream(dev)))
+    return grad
+
+
+def distill_topk_step(student, teacher_logit, teacher_id, grad_loss, T=1.0,
+                      *, teacher_lse=None, out=None, status=None):
+    """distill_topk and its gradient in one call (sd_distill_topk_step), for
+    a training step that knows the rows' weights beforehand.  Returns loss,
+    lse and grad."""
+    dev, N, V, K, rs = _distill_rows(student, teacher_logit, teacher_id,
+                                     teacher_lse)
+    _row_vector(grad_loss, dev, "grad_loss", N)
+    loss = torch.empty(N, dtype=torch.float32, device=dev)
+    lse = torch.empty(N, dtype=torch.float32, device=dev)
+    grad, gs = _grad_out(out, student, dev, N, V)
+    _check(lib().sd_distill_topk_step(
+        student.data_ptr(), rs, _dt(student), teacher_logit.data_ptr(),
+        teacher_id.data_ptr(), _ptr(teacher_lse), grad_loss.data_ptr(), N, V,
+        K, T, loss.data_ptr(), lse.data_ptr(), grad.data_ptr(), gs,
+        _ptr(status), _stream(dev)))
+    return {"loss": loss, "lse": lse, "grad": grad}

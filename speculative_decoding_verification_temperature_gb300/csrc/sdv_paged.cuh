@@ -1,0 +1,84 @@
+// sdv_paged.cuh -- what the paged-cache kernels share: 16-bit element
+// types, the sequence a packed row belongs to, and the host's checks of a
+// cache description.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "sdv_device.cuh"
+#include "sdv_host.cuh"
+
+namespace sdv {
+
+// fp32 <-> the cache's 16-bit types (round to nearest even).
+__device__ __forceinline__ float widen(__nv_bfloat16 x) {
+  return __bfloat162float(x);
+}
+__device__ __forceinline__ float widen(__half x) { return __half2float(x); }
+template <class T> __device__ __forceinline__ T narrow(float x);
+template <> __device__ __forceinline__ __nv_bfloat16 narrow(float x) {
+  return __float2bfloat16_rn(x);
+}
+template <> __device__ __forceinline__ __half narrow(float x) {
+  return __float2half_rn(x);
+}
+
+// A sequence's chunk: n new tokens from packed row `start`, the last n of
+// its kv keys.  usable: see sd_paged_kv; rows_ok: start and n are.
+struct Chunk {
+  int start, n, kv;
+  bool rows_ok, usable;
+};
+
+__device__ __forceinline__ Chunk load_chunk(const int32_t *q_start,
+                                            const int32_t *kv_len, int b,
+                                            int total, long long max_kv) {
+  Chunk c;
+  c.start = __ldg(q_start + b);
+  const int end = __ldg(q_start + b + 1);
+  c.kv = __ldg(kv_len + b);
+  c.rows_ok = c.start >= 0 && c.start <= end && end <= total;
+  c.n = c.rows_ok ? end - c.start : 0;
+  c.usable = c.rows_ok && c.n <= c.kv && c.kv <= max_kv;
+  return c;
+}
+
+// The last sequence whose q_start is at most `row` (the row's own, where it
+// has one: empty sequences before it share its q_start).
+__device__ __forceinline__ int find_sequence(const int32_t *q_start, int B,
+                                             int row) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(q_start + mid) <= row) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Host checks of a cache description.
+inline sd_status check_cache(const sd_paged_kv *c) {
+  SDV_REQUIRE(c != nullptr, "cache is null");
+  SDV_REQUIRE(c->dt == SD_BF16 || c->dt == SD_F16, "bad cache dtype %d",
+              (int)c->dt);
+  SDV_REQUIRE(c->num_pages >= 0, "num_pages < 0");
+  SDV_REQUIRE(c->page_size >= 1, "page_size < 1");
+  SDV_REQUIRE(c->max_pages >= 0, "max_pages < 0");
+  SDV_REQUIRE((long long)c->max_pages * c->page_size < (1LL << 31),
+              "max_pages page_size = %lld does not fit 31 bits",
+              (long long)c->max_pages * c->page_size);
+  SDV_REQUIRE(c->heads >= 1 && c->heads <= 65535, "heads=%d outside [1, 65535]",
+              c->heads);
+  SDV_REQUIRE(c->head_dim >= 1 && c->head_dim <= 1024,
+              "head_dim=%d outside [1, 1024]", c->head_dim);
+  SDV_REQUIRE(c->page_stride >= 0 && c->token_stride >= 0 &&
+                  c->head_stride >= 0,
+              "a cache stride is negative");
+  if (c->page_size % 8 != 0)
+    return fail(SD_ERR_UNSUPPORTED, "page_size=%d is not a multiple of 8",
+                c->page_size);
+  return SD_OK;
+}
+
+}  // namespace sdv

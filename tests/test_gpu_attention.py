@@ -1,0 +1,279 @@
+"""sd_paged_attention against the 64-bit formula, under bounds derived from
+the types' roundings (tests/operators_ref.py).  The caches hold NaN wherever
+no key of a sequence lies."""
+import numpy as np
+import pytest
+import torch
+
+from speculative_decoding_verification_temperature_gb300 import api
+from tests import operators_ref as ref
+from tests.test_gpu_canaries import GuardedTorch
+
+pytestmark = pytest.mark.gpu
+
+BF, HF = torch.bfloat16, torch.float16
+
+
+def random_trees(n, seed):
+    r = np.random.default_rng(seed)
+    see = []
+    for m in n:
+        t = np.zeros((m, m), bool)
+        for i in range(m):
+            if i:
+                t[i] = t[r.integers(max(0, i - 6), i)]
+            t[i, i] = True
+        see.append(t)
+    return see
+
+
+def run(P, Hq, *, see=None, max_q=None, scale=None, by=2.0, ws=None):
+    cache = api.PagedKV(P.to_gpu(P.k), P.to_gpu(P.v), P.table.cuda())
+    q = P.rows(Hq, by=by)
+    start, kv = P.lengths()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = api.paged_attention(
+        q.cuda(), cache, start, kv, max_q=max_q, scale=scale,
+        tree_mask=None if see is None else ref.pack_mask(see), want_lse=True,
+        status=st, workspace=ws or api.Workspace())
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    out, lse, tol, ltol = ref.attention(P, q, scale or P.dim ** -0.5, see)
+    g, gl = ref.f64(got["out"]), ref.f64(got["lse"])
+    assert np.isfinite(g).all()
+    assert (np.abs(g - out) <= tol).all(), np.abs(g - out).max()
+    fine = np.isfinite(lse)
+    assert (gl[~fine] == lse[~fine]).all()
+    assert (np.abs(gl - lse)[fine] <= ltol[fine]).all()
+    return got
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,kv", [
+    ([1], [1]), ([1], [2]), ([5], [100]), ([1, 1, 1], [129, 128, 127]),
+    ([0, 3, 0], [5, 3, 0]), ([9, 9], [300, 9]), ([17, 1, 40], [140, 513, 40]),
+    ([130], [257]), ([1], [1000])])
+def test_lengths(dtype, D, n, kv):
+    run(ref.Paged(n, kv, 2, D, 16, dtype, seed=sum(kv) + D), 4,
+        max_q=max(n))
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 1), (5, 5), (10, 2), (16, 1),
+                                    (71, 1), (130, 1), (14, 2)])
+@pytest.mark.parametrize("n", [1, 4])
+def test_head_layouts(Hq, Hkv, n):
+    run(ref.Paged([n, n], [n, 200], Hkv, 64, 8, BF, seed=Hq), Hq, max_q=n)
+
+
+@pytest.mark.parametrize("page", [8, 24, 48, 64, 128, 256, 320])
+@pytest.mark.parametrize("head_major", [False, True])
+def test_pages(page, head_major):
+    """Pages that end inside a key tile, tiles that end inside a page."""
+    P = ref.Paged([3, 1], [401, 130], 2, 128, page, HF, seed=page,
+                  head_major=head_major)
+    run(P, 8, max_q=3)
+
+
+@pytest.mark.parametrize("hint", [None, 0, 1, 5, 64, 4096])
+def test_the_hint_changes_no_result(hint):
+    """Any max_q: the chunk lengths are what q_start says."""
+    run(ref.Paged([40, 1, 3], [170, 300, 3], 2, 64, 16, BF, seed=3), 6,
+        max_q=hint)
+
+
+@pytest.mark.parametrize("n,kv,Hq", [([64, 64], [300, 64], 8),
+                                     ([31, 33, 1], [200, 40, 9], 2),
+                                     ([130], [300], 2), ([1, 2], [1, 2], 4)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_token_trees(n, kv, Hq, D):
+    run(ref.Paged(n, kv, 2, D, 32, HF, seed=sum(kv)), Hq, max_q=max(n),
+        see=random_trees(n, 5))
+
+
+def test_masks_that_leave_rows_empty():
+    """No prefix and no bit: out 0, lse -inf; rows beside them as ever.  Bits
+    past the chunk count for nothing."""
+    see = random_trees([5, 40, 3], 7)
+    see[0][2] = False
+    see[1][:, :] = False
+    see[1][3, 0] = see[1][39, 38] = True
+    P = ref.Paged([5, 40, 3], [5, 40, 20], 2, 64, 16, BF, seed=11)
+    got = run(P, 4, max_q=40, see=see)
+    assert bool((got["out"][2] == 0).all())
+    assert bool((got["lse"][2] == -float("inf")).all())
+    assert bool((got["out"][5:8] == 0).all())
+    # a mask that looks ahead, and one past the chunk
+    ahead = [np.ones((3, 3), bool)]
+    P = ref.Paged([3], [130], 1, 64, 8, BF, seed=12)
+    want = run(P, 2, max_q=3, see=ahead)["out"]
+    cache = api.PagedKV(P.k.cuda(), P.v.cuda(), P.table.cuda())
+    P.gen.manual_seed(1)
+    q = P.rows(2).cuda()
+    start, kv = P.lengths()
+    full = torch.full((3, 2), -1, dtype=torch.int32, device="cuda")
+    a = api.paged_attention(q, cache, start, kv, tree_mask=full)["out"]
+    b = api.paged_attention(q, cache, start, kv,
+                            tree_mask=ref.pack_mask(ahead))["out"]
+    assert torch.equal(a, b) and want.shape == a.shape
+
+
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 8, 2), (64, 6, 2)])
+def test_parts_of_prompts(D, Hq, Hkv):
+    """Chunks of several hundred tokens: many row tiles, causal limits inside
+    key tiles, work shared between several CTAs."""
+    run(ref.Paged([300, 257, 1], [300, 700, 650], Hkv, D, 64, BF, seed=21),
+        Hq, max_q=300)
+
+
+def test_long_prefixes_are_split_and_joined():
+    run(ref.Paged([1, 2], [6000, 150], 1, 64, 32, BF, seed=31), 4, max_q=2)
+    run(ref.Paged([9], [5000], 2, 128, 16, HF, seed=32), 8, max_q=9)
+
+
+@pytest.mark.parametrize("by", [0.0, 20.0])
+def test_flat_and_steep_scores(by):
+    """Equal weights, and maxima that move by hundreds along the keys."""
+    run(ref.Paged([2, 3], [700, 40], 2, 64, 16, BF, seed=41), 4, by=by)
+    run(ref.Paged([40], [200], 1, 128, 16, HF, seed=42), 4, by=by)
+
+
+def test_rising_maximum():
+    """Every key tile's scores lie above the last one's."""
+    P = ref.Paged([1], [640], 1, 64, 16, BF, seed=43)
+    d = torch.randn(64, generator=P.gen)
+    for j in range(640):
+        p, t = P.slot(0, j)
+        P.k[p, t, 0] = (d * (j / 64.0) / d.norm()).to(BF)
+    q = (d * 8).to(BF).view(1, 1, 64).repeat(1, 2, 1)
+    P.rows = lambda *a, **k: q
+    run(P, 2, scale=1.0)
+
+
+def test_scale_and_strided_queries():
+    P = ref.Paged([4, 2], [90, 33], 2, 64, 16, BF, seed=51)
+    run(P, 4, scale=0.3)
+    cache = api.PagedKV(P.k.cuda(), P.v.cuda(), P.table.cuda())
+    start, kv = P.lengths()
+    wide = P.rows(9).cuda()
+    a = api.paged_attention(wide[:, 2:6], cache, start, kv)["out"]
+    b = api.paged_attention(wide[:, 2:6].contiguous(), cache, start,
+                            kv)["out"]
+    assert torch.equal(a, b)
+
+
+def test_unusable_sequences():
+    """A key count below the chunk, one above the table, a bad page among
+    those read, a mask too short: NaN for that sequence, bits set, the other
+    sequences the same bits as without them."""
+    n, kv = [2, 2, 2, 2, 40], [40, 50, 60, 30, 40]
+    P = ref.Paged(n, kv, 1, 64, 16, BF, seed=61)
+    q = P.rows(4).cuda()
+    start, kvt = P.lengths()
+
+    def call(table, kvt, mask=None):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        r = api.paged_attention(
+            q, api.PagedKV(P.k.cuda(), P.v.cuda(), table.cuda()), start, kvt,
+            tree_mask=mask, want_lse=True, status=st, max_q=40)
+        return r["out"], r["lse"], int(st.item())
+
+    out, lse, st = call(P.table, kvt)
+    assert st == 0 and bool(torch.isfinite(out).all())
+    bad_kv = kvt.clone()
+    bad_kv[0], bad_kv[1] = 1, 10 ** 6
+    table = P.table.clone()
+    table[2, 1] = -1
+    table[3, 0] = 10 ** 6
+    table[4, 3] = 10 ** 6  # past its 40 keys: never read
+    o2, l2, st = call(table, bad_kv)
+    assert st == api.DEV_BAD_LENGTH | api.DEV_BAD_PAGE
+    assert bool(torch.isnan(o2[:8]).all()) and bool(torch.isnan(l2[:8]).all())
+    assert torch.equal(o2[8:], out[8:]) and torch.equal(l2[8:], lse[8:])
+    mask = torch.full((48, 1), -1, dtype=torch.int32, device="cuda")
+    o3, _, st = call(P.table, kvt, mask)
+    assert st == api.DEV_BAD_LENGTH
+    assert bool(torch.isnan(o3[8:]).all())
+    assert bool(torch.isfinite(o3[:8]).all())
+
+
+def test_a_nan_key_reaches_who_sees_it():
+    P = ref.Paged([2, 2], [150, 150], 2, 64, 16, BF, seed=71)
+    p, t = P.slot(0, 7)
+    P.k[p, t, 1] = np.nan
+    cache = api.PagedKV(P.k.cuda(), P.v.cuda(), P.table.cuda())
+    q = P.rows(4).cuda()
+    o = api.paged_attention(q, cache, *P.lengths())["out"]
+    assert bool(torch.isnan(o[:2, 2:]).all())
+    assert bool(torch.isfinite(o[:2, :2]).all())
+    assert bool(torch.isfinite(o[2:]).all())
+
+
+def test_same_bits_twice_and_on_another_stream():
+    P = ref.Paged([9, 1, 30], [3000, 700, 900], 2, 128, 16, BF, seed=81)
+    cache = api.PagedKV(P.k.cuda(), P.v.cuda(), P.table.cuda())
+    q = P.rows(8).cuda()
+    start, kv = P.lengths()
+    ws = api.Workspace()
+    a = api.paged_attention(q, cache, start, kv, workspace=ws)["out"]
+    for _ in range(3):
+        b = api.paged_attention(q, cache, start, kv, workspace=ws)["out"]
+        assert torch.equal(a, b)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        b = api.paged_attention(q, cache, start, kv,
+                                workspace=api.Workspace())["out"]
+    s.synchronize()
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n,kv,hint", [([9, 1], [3000, 70], 9),
+                                       ([200], [300], 200)])
+def test_no_write_outside_the_buffers(monkeypatch, n, kv, hint):
+    guard = GuardedTorch()
+    monkeypatch.setattr(api, "torch", guard)
+    P = ref.Paged(n, kv, 2, 64, 16, BF, seed=91)
+    cache = api.PagedKV(P.k.cuda(), P.v.cuda(), P.table.cuda())
+    api.paged_attention(P.rows(6).cuda(), cache, *P.lengths(), max_q=hint,
+                        want_lse=True, workspace=api.Workspace())
+    assert guard.check() >= 2
+
+
+def test_rows_of_no_sequence_are_left_alone(monkeypatch):
+    """total above q_start[B]: those rows keep what they held."""
+    guard = GuardedTorch()  # its buffers start as the sentinel
+    monkeypatch.setattr(api, "torch", guard)
+    P = ref.Paged([2, 1], [20, 300], 2, 64, 16, BF, seed=95)
+    cache = api.PagedKV(P.k.cuda(), P.v.cuda(), P.table.cuda())
+    q = torch.cat([P.rows(4), torch.ones(3, 4, 64, dtype=BF)]).cuda()
+    out = api.paged_attention(q, cache, *P.lengths(),
+                              workspace=api.Workspace())["out"]
+    torch.cuda.synchronize()
+    assert bool((out[3:].view(torch.uint8) == 0xA5).all())
+    assert bool(torch.isfinite(out[:3]).all())
+
+
+def test_cache_offsets_past_32_bits():
+    """Pages whose element offsets do not fit 32 bits (a strided view of a
+    larger buffer): the last pages of a cache of 2^32 + elements."""
+    page, H, D = 16, 1, 64
+    pages = 2
+    stride = (1 << 32) // 1 + 1024  # elements between the two pages
+    free = torch.cuda.mem_get_info()[0]
+    if free < 40 << 30:
+        pytest.skip("needs 40 GB")
+    n = stride + page * H * D
+    kb = torch.empty(n, dtype=BF, device="cuda")
+    vb = torch.empty(n, dtype=BF, device="cuda")
+    view = (pages, page, H, D), (stride, H * D, D, 1)
+    k, v = kb.as_strided(*view), vb.as_strided(*view)
+    g = torch.Generator().manual_seed(1)
+    P = ref.Paged([1], [30], H, D, page, BF, seed=1, extra_cols=0)
+    P.table = torch.tensor([[1, 0]], dtype=torch.int32)
+    P.k = torch.randn(pages, page, H, D, generator=g).to(BF)
+    P.v = torch.randn(pages, page, H, D, generator=g).to(BF)
+    k.copy_(P.k)
+    v.copy_(P.v)
+    P.to_gpu = lambda t: k if t is P.k else v
+    run(P, 2)
