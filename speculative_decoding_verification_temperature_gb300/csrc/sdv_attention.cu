@@ -3,109 +3,988 @@
 //
 //   out = sum_j w_j v_j / sum_j w_j,  w_j = exp(scale q.k_j)
 //
-// in one pass over the keys with a running maximum m and sum l: a new
-// maximum m' scales what is summed so far by exp(m - m').
+// in one pass over the keys with a running reference m and sum l: a new
+// reference m' scales what is summed so far by exp(m - m').
+//
+// A row is one (token, query head); the rows of a sequence that read one
+// cache head are token-major, so the G query heads of a group share each key
+// tile.  A unit of work is (sequence, cache head, 128 or 256 rows), its
+// length the tiles of 128 keys its rows see.  All units laid end to end are
+// cut into equal shares, one per SM, whatever the lengths are; a unit that
+// is cut leaves partial sums in the workspace, which a second kernel joins
+// in key order.
+//
+// In a CTA, one warp loads key and value tiles by TMA through the block
+// table, one issues the tensor-core products, and two warpgroups ("streams")
+// turn scores into weights, a thread per row.  S = Q K^T goes to tensor
+// memory; the weights, rounded to 16 bits, go back there over S and are the
+// first operand of O += W V.  The streams take turns on the tensor cores:
+// with 256 rows each stream has 128 of them; with up to 128 rows (a few
+// drafts) both have the same rows and every other key tile, and their sums
+// are joined at the end of the unit.
+#include <cuda.h>
+
+#include <atomic>
+
 #include "sdv_paged.cuh"
+#include "sdv_tcgen05.cuh"
 
 namespace sdv {
 namespace {
 
+constexpr int kTile = 128;       // keys per tile, rows per stream
+constexpr int kMaxGrid = 160;    // CTAs the workspace is laid out for
+constexpr int kAttnThreads = 320;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kBadRing = 64;     // units whose bad-page mark is kept
+constexpr float kLn2 = 0.693147180559945f;
+// A row's reference moves only when its maximum is 2^8 above it: weights
+// stay below 2^8, far inside 16-bit range, and most tiles rescale nothing.
+constexpr float kSlack = 8.f;
+
 struct AttnParams {
-  const void *q, *k, *v;
+  const void *q;
   long long q_stride;
   const int32_t *q_start, *kv_len, *block_table, *mask;
   int mask_words;
-  int B, total, Hq, Hkv;
+  int B, total, Hq, Hkv, G;
   int num_pages, page_size, max_pages;
-  long long page_stride, token_stride, head_stride;
+  int box;  // rows of one TMA box: a power of two that divides the page
   float scale_log2;  // scale x log2(e)
   void *out;
   float *lse;
   int32_t *dev_status;
+  // workspace: records of cut units, (m, l) and O of the parts
+  struct CutUnit *cut;
+  float2 *part_ml;
+  float *part_o;
 };
 
-// One warp per (token, query head); a lane holds D / 32 elements.
-template <class T, int D>
-__global__ void __launch_bounds__(kThreads)
-attention_row_kernel(const __grid_constant__ AttnParams p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long w =
-      (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (w >= (long long)p.total * p.Hq) return;
-  const int row = (int)(w / p.Hq), h = (int)(w % p.Hq);
-  const int b = find_sequence(p.q_start, p.B, row);
+// A unit whose key range is cut: part 0 is slot 1 of the CTA that starts
+// it, part k slot 0 of the k-th CTA after it.
+struct CutUnit {
+  int parts, rows;     // rows: valid rows of the tile
+  int start, head;     // packed row of the sequence, cache head
+  long long first;     // first row of the tile in (token, group) order
+};
+
+// ------------------------------------------------------------ work units
+__device__ __forceinline__ Chunk attn_chunk(const AttnParams &p, int b) {
   Chunk c = load_chunk(p.q_start, p.kv_len, b, p.total,
                        (long long)p.max_pages * p.page_size);
-  if (c.usable && p.mask && c.n > 32 * p.mask_words) c.usable = false;
-  if (!c.usable && lane == 0) status_or(p.dev_status, SD_DEV_BAD_LENGTH);
-  if (!c.rows_ok || row < c.start || row >= c.start + c.n) return;
-  T *out = (T *)p.out + ((long long)row * p.Hq + h) * D;
-  float *lse = p.lse ? p.lse + (long long)row * p.Hq + h : nullptr;
-  const float nan = __int_as_float(0x7fc00000);
-  const int i = row - c.start, ctx = c.kv - c.n;
-  const T *q = (const T *)p.q + row * p.q_stride + (long long)h * D;
-  const int kh = h / (p.Hq / p.Hkv);
-  float qv[E], o[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    qv[e] = widen(q[lane + 32 * e]);
-    o[e] = 0.f;
+  if (p.mask && c.n > 32LL * p.mask_words) c.usable = false;
+  return c;
+}
+
+template <int ROWS>
+__device__ __forceinline__ int row_tiles(const AttnParams &p,
+                                         const Chunk &c) {
+  return c.usable ? (int)(((long long)c.n * p.G + ROWS - 1) / ROWS) : 0;
+}
+
+// Key tiles that row tile t sees.
+template <int ROWS>
+__device__ __forceinline__ int key_tiles(const AttnParams &p, const Chunk &c,
+                                         int t) {
+  int last = c.kv - 1;
+  if (!p.mask) {
+    const long long i = ((long long)(t + 1) * ROWS - 1) / p.G;
+    if (i < c.n - 1) last = c.kv - c.n + (int)i;
   }
-  float m = -kInf, l = 0.f;
-  bool bad = !c.usable;
-  const int last = bad ? 0 : p.mask ? c.kv : ctx + i + 1;
-  for (int j = 0; j < last; ++j) {
-    const int page = __ldg(p.block_table + (long long)b * p.max_pages +
-                           j / p.page_size);
-    if (page < 0 || page >= p.num_pages) {
-      bad = true;
-      if (lane == 0) status_or(p.dev_status, SD_DEV_BAD_PAGE);
-      break;
+  return last / kTile + 1;
+}
+
+template <int ROWS>
+__device__ unsigned long long head_tiles(const AttnParams &p,
+                                         const Chunk &c) {
+  const int T = row_tiles<ROWS>(p, c);
+  unsigned long long s = 0;
+  for (int t = 0; t < T; ++t) s += key_tiles<ROWS>(p, c, t);
+  return s;
+}
+
+// The plan of one CTA: its share [x0, x1) of all tiles, and where x0 lies.
+struct Plan {
+  unsigned long long total, x0, x1, rem;  // rem: x0 within sequence b
+  unsigned long long warp_sum[8];
+  int n, b;
+  int any_unusable;
+};
+
+template <int ROWS>
+__device__ void make_plan(const AttnParams &p, Plan &s) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  unsigned long long first = 0, sum = 0;
+  bool unusable = false;
+  if (tid < 256)
+    for (int b = tid; b < p.B; b += 256) {
+      const Chunk c = attn_chunk(p, b);
+      if (c.n > 0 && !c.usable) unusable = true;
+      if (!c.rows_ok) {
+        unusable = true;
+        if (blockIdx.x == 0) status_or(p.dev_status, SD_DEV_BAD_LENGTH);
+      }
+      const unsigned long long w = head_tiles<ROWS>(p, c) * p.Hkv;
+      if (b == tid) first = w;
+      sum += w;
     }
-    if (p.mask && j >= ctx) {
-      const int x = j - ctx;
-      const int32_t word =
-          __ldg(p.mask + (long long)row * p.mask_words + (x >> 5));
-      if (!((word >> (x & 31)) & 1)) continue;
+  // inclusive scan of `first` and total of `sum`
+  unsigned long long tot = sum;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) tot += __shfl_xor_sync(~0u, tot, d);
+  if (lane == 0 && warp < 8) s.warp_sum[warp] = tot;
+  if (tid == 0) s.b = -1;
+  const int any = __syncthreads_or(unusable);
+  if (tid == 0) {
+    unsigned long long w = 0;
+    for (int i = 0; i < 8; ++i) w += s.warp_sum[i];
+    s.total = w;
+    s.any_unusable = any;
+    s.n = w < gridDim.x ? (int)w : (int)gridDim.x;
+    s.x0 = s.x1 = 0;
+    if ((int)blockIdx.x < s.n) {
+      s.x0 = w * blockIdx.x / s.n;
+      s.x1 = w * (blockIdx.x + 1) / s.n;
     }
-    const long long at = page * p.page_stride +
-                         (j % p.page_size) * p.token_stride +
-                         kh * p.head_stride;
-    const T *k = (const T *)p.k + at, *v = (const T *)p.v + at;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(qv[e], widen(k[lane + 32 * e]), s);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= p.scale_log2;
-    const float mn = fmaxf(m, s);
-    const float f = m == -kInf ? 0.f : ex2(m - mn);
-    const float wgt = ex2(s - mn);
-    m = mn;
-    l = l * f + wgt;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      o[e] = fmaf(o[e], f, wgt * widen(v[lane + 32 * e]));
   }
-  const float inv = bad ? nan : l > 0.f ? 1.f / l : l != l ? l : 0.f;
+  __syncthreads();
+  if (s.x0 == s.x1) return;
+  unsigned long long carry = 0;
+  for (int base = 0; base < p.B; base += 256) {
+    unsigned long long w = 0;
+    if (tid < 256 && base + tid < p.B)
+      w = base == 0 ? first
+                    : head_tiles<ROWS>(p, attn_chunk(p, base + tid)) * p.Hkv;
+    unsigned long long inc = w;
 #pragma unroll
-  for (int e = 0; e < E; ++e)
-    out[lane + 32 * e] = narrow<T>(bad ? nan : o[e] * inv);
-  if (lse && lane == 0)
-    *lse = bad ? nan : l == 0.f ? -kInf : (m + log2f(l)) * 0.69314718f;
+    for (int d = 1; d < 32; d <<= 1) {
+      const unsigned long long o = __shfl_up_sync(~0u, inc, d);
+      if (lane >= d) inc += o;
+    }
+    if (lane == 31 && warp < 8) s.warp_sum[warp] = inc;
+    __syncthreads();
+    unsigned long long all = 0, before = carry;
+    for (int i = 0; i < 8; ++i) {
+      if (i < warp) before += s.warp_sum[i];
+      all += s.warp_sum[i];
+    }
+    const unsigned long long lo = before + inc - w;
+    if (tid < 256 && s.x0 >= lo && s.x0 < lo + w) {
+      s.b = base + tid;
+      s.rem = s.x0 - lo;
+    }
+    carry += all;
+    __syncthreads();
+    if (s.b >= 0) break;
+  }
+}
+
+// Walks the units of a CTA's share; every warp walks the same ones.
+template <int ROWS> struct Units {
+  const AttnParams &p;
+  unsigned long long left;
+  Chunk c;
+  int b, h, t, T;
+  int j0, j1, nk;   // key tiles [j0, j1) of the unit's nk
+  int rows;         // valid rows of the tile
+  int count;        // units begun
+
+  __device__ Units(const AttnParams &p_, const Plan &s)
+      : p(p_), left(s.x1 - s.x0), b(s.b), h(0), t(0), T(0), j0(0), count(0) {
+    if (!left) return;
+    c = attn_chunk(p, b);
+    T = row_tiles<ROWS>(p, c);
+    const unsigned long long per = head_tiles<ROWS>(p, c);
+    h = (int)(s.rem / per);
+    unsigned long long r = s.rem % per;
+    for (;;) {
+      const int k = key_tiles<ROWS>(p, c, t);
+      if (r < (unsigned long long)k) break;
+      r -= k;
+      ++t;
+    }
+    j0 = (int)r;
+    set();
+  }
+  __device__ void set() {
+    ++count;
+    nk = key_tiles<ROWS>(p, c, t);
+    j1 = (unsigned long long)(nk - j0) < left ? nk : j0 + (int)left;
+    const long long r = (long long)c.n * p.G - (long long)t * ROWS;
+    rows = r < ROWS ? (int)r : ROWS;
+  }
+  __device__ void next() {
+    left -= j1 - j0;
+    if (!left) return;
+    j0 = 0;
+    if (++t == T) {
+      t = 0;
+      if (++h == p.Hkv) {
+        h = 0;
+        do {  // left > 0: a later sequence has tiles
+          c = attn_chunk(p, ++b);
+          T = row_tiles<ROWS>(p, c);
+        } while (T == 0);
+      }
+    }
+    set();
+  }
+};
+
+// --------------------------------------------------------- shared memory
+// PAIR: 256 rows a unit, 128 a stream; otherwise both streams share 128.
+template <int D, bool PAIR> struct Layout {
+  static constexpr int kRows = PAIR ? 256 : 128;
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int kQTiles = PAIR ? 2 : 1;
+  // as many stages as fit: what is in flight covers the latency of HBM
+  static constexpr int kK = D == 128 ? 3 : PAIR ? 4 : 5;
+  static constexpr int kV = D == 128 ? (PAIR ? 2 : 3) : PAIR ? 4 : 5;
+  static constexpr size_t kTiles =
+      (size_t)kTileBytes * (kQTiles + kK + kV);
+};
+
+template <int D, bool PAIR> struct Shared {
+  using L = Layout<D, PAIR>;
+  uint64_t k_full[L::kK], k_empty[L::kK], v_full[L::kV], v_empty[L::kV];
+  uint64_t q_full[2], s_full[2], w_full[2], o_full[2], drain;
+  uint32_t tmem;
+  volatile int abort;
+  int bad[kBadRing];  // unit count whose pages were bad
+  float2 ml[2][PAIR ? 1 : kTile];
+  Plan plan;
+};
+template <int D, bool PAIR> constexpr size_t attn_smem() {
+  return Layout<D, PAIR>::kTiles + sizeof(Shared<D, PAIR>);
+}
+
+// A bounded wait; after a failure anywhere in the CTA every wait gives up.
+constexpr unsigned kAttnWaitLimit = 1u << 22;
+__device__ __forceinline__ bool attn_wait(uint64_t *bar, uint32_t parity,
+                                          volatile int *abort,
+                                          int32_t *dev_status) {
+  for (unsigned it = 0; it < kAttnWaitLimit; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 255) == 255 && *abort) return false;
+  }
+  *abort = 1;
+  status_or(dev_status, SD_DEV_TIMEOUT);
+  return false;
+}
+
+// A barrier of the two softmax warpgroups alone.
+__device__ __forceinline__ void streams_sync() {
+  asm volatile("bar.sync 1, 256;" ::: "memory");
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t &>(d))
+      : "l"(reinterpret_cast<uint64_t &>(a)),
+        "l"(reinterpret_cast<uint64_t &>(b)),
+        "l"(reinterpret_cast<uint64_t &>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t &>(d))
+      : "l"(reinterpret_cast<uint64_t &>(a)),
+        "l"(reinterpret_cast<uint64_t &>(b)));
+  return d;
+}
+
+template <class T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+  uint32_t u;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
+  return u;
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
+  uint32_t u;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
+  return u;
+}
+
+// Bits of the 32 keys from `key` on that a row sees.  Causal: keys up to
+// `limit`.  Tree: the prefix, and the chunk's tokens in its mask.
+__device__ __forceinline__ uint32_t seen_bits(const AttnParams &p,
+                                              const Chunk &c, int token,
+                                              int limit, int key) {
+  const int ctx = c.kv - c.n;
+  const int end = (p.mask ? c.kv - 1 : limit) - key;  // last bit in range
+  if (end < 0) return 0;
+  const uint32_t in = end >= 31 ? ~0u : (2u << end) - 1;
+  if (!p.mask) return in;
+  const int x = key - ctx;  // the chunk's token at bit 0
+  if (x <= -32) return in;
+  const int32_t *m = p.mask + (long long)(c.start + token) * p.mask_words;
+  uint32_t bits;
+  if (x < 0) {
+    bits = ((1u << -x) - 1) | (uint32_t)__ldg(m) << -x;
+  } else {
+    const int w = x >> 5;
+    const uint32_t lo = w < p.mask_words ? (uint32_t)__ldg(m + w) : 0;
+    const uint32_t hi = w + 1 < p.mask_words ? (uint32_t)__ldg(m + w + 1) : 0;
+    bits = __funnelshift_r(lo, hi, x & 31);
+  }
+  return bits & in;
+}
+
+// ------------------------------------------------------------- the kernel
+template <class T, int D, bool PAIR>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+attention_kernel(const __grid_constant__ AttnParams p,
+                 const __grid_constant__ CUtensorMap k_map,
+                 const __grid_constant__ CUtensorMap v_map) {
+  using L = Layout<D, PAIR>;
+  constexpr int ROWS = L::kRows;
+  constexpr bool BF16 = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ __align__(1024) char dyn[];  // swizzled tiles first
+  Shared<D, PAIR> &s = *reinterpret_cast<Shared<D, PAIR> *>(dyn + L::kTiles);
+  char *q_tile = dyn;
+  char *k_tile = q_tile + L::kQTiles * L::kTileBytes;
+  char *v_tile = k_tile + L::kK * L::kTileBytes;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < L::kK; ++i) {
+      mbar_init(&s.k_full[i], 1);
+      mbar_init(&s.k_empty[i], 1);
+    }
+    for (int i = 0; i < L::kV; ++i) {
+      mbar_init(&s.v_full[i], 1);
+      mbar_init(&s.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.q_full[i], PAIR ? 4 : 8);
+      mbar_init(&s.s_full[i], 1);
+      mbar_init(&s.w_full[i], 4);
+      mbar_init(&s.o_full[i], 1);
+    }
+    mbar_init(&s.drain, 1);
+    s.abort = 0;
+    fence_mbar_init();
+  }
+  if (tid < kBadRing) s.bad[tid] = 0;
+  if (warp == kMmaWarp) tmem_alloc_all(&s.tmem);
+  if (warp == kLoadWarp && lane == 0) {
+    tma_prefetch_map(&k_map);
+    tma_prefetch_map(&v_map);
+  }
+  griddep_wait();  // nothing before this reads or writes what a grid before
+                   // this one may still write or read
+  make_plan<ROWS>(p, s.plan);
+  tmem_fence_before();
+  __syncthreads();
+  tmem_fence_after();
+  const uint32_t tmem = s.tmem;
+  Units<ROWS> u(p, s.plan);
+  bool fine = true;
+
+  if (warp == kLoadWarp) {
+    // ---- key and value tiles, a box of page rows at a time
+    const int per = kTile / p.box;  // boxes of a tile and column half
+    constexpr int HALVES = D / 64;
+    unsigned kn = 0, vn = 0;  // tiles issued
+    for (; u.left && fine; u.next()) {
+      const int32_t *table = p.block_table + (long long)u.b * p.max_pages;
+      for (int j = u.j0; j < u.j1 && fine; ++j) {
+        const int ks = kn % L::kK, vs = vn % L::kV;
+        // lane i has boxes i and i + 32 (box = 8: 16 boxes a half)
+        int page = 0, tok = 0;
+        bool bad = false;
+        const int a = lane % per;
+        if (lane < per * HALVES) {
+          const int key = j * kTile + a * p.box;
+          page = p.num_pages > 0 ? p.num_pages : 1;  // out of range: zeros
+          if (key < u.c.kv) {
+            const int id = __ldg(table + key / p.page_size);
+            if (id >= 0 && id < p.num_pages) page = id;
+            else bad = true;
+          }
+          tok = key % p.page_size;
+        }
+        if (__any_sync(~0u, bad) && lane == 0) {
+          s.bad[u.count % kBadRing] = u.count;
+          status_or(p.dev_status, SD_DEV_BAD_PAGE);
+        }
+        fine = attn_wait(&s.k_empty[ks], (kn / L::kK & 1) ^ 1, &s.abort,
+                         p.dev_status);
+        if (!__all_sync(~0u, fine)) { fine = false; break; }
+        if (lane == 0) mbar_expect_tx(&s.k_full[ks], L::kTileBytes);
+        __syncwarp();
+        if (lane < per * HALVES)
+          tma_load_4d(k_tile + ks * L::kTileBytes + (lane / per) * (kTile * 128) +
+                          a * p.box * 128,
+                      &k_map, (lane / per) * 64, tok, u.h, page,
+                      &s.k_full[ks]);
+        ++kn;
+        fine = attn_wait(&s.v_empty[vs], (vn / L::kV & 1) ^ 1, &s.abort,
+                         p.dev_status);
+        if (!__all_sync(~0u, fine)) { fine = false; break; }
+        if (lane == 0) mbar_expect_tx(&s.v_full[vs], L::kTileBytes);
+        __syncwarp();
+        if (lane < per * HALVES)
+          tma_load_4d(v_tile + vs * L::kTileBytes + (lane / per) * (kTile * 128) +
+                          a * p.box * 128,
+                      &v_map, (lane / per) * 64, tok, u.h, page,
+                      &s.v_full[vs]);
+        ++vn;
+      }
+    }
+    if (!fine) {
+      // give up: let the copies in flight land before the CTA ends
+      for (int i = 0; i < L::kK; ++i)
+        if (kn > (unsigned)i) {
+          const unsigned last = (kn - 1 - i) / L::kK;
+          for (unsigned it = 0; it < (1u << 20); ++it)
+            if (mbar_try_wait(&s.k_full[i], last & 1)) break;
+        }
+      for (int i = 0; i < L::kV; ++i)
+        if (vn > (unsigned)i) {
+          const unsigned last = (vn - 1 - i) / L::kV;
+          for (unsigned it = 0; it < (1u << 20); ++it)
+            if (mbar_try_wait(&s.v_full[i], last & 1)) break;
+        }
+    }
+  } else if (warp == kMmaWarp) {
+    // ---- tensor-core products, issued by lane 0
+    constexpr uint32_t S_DESC = umma_idesc(BF16, false, kTile, kTile);
+    constexpr uint32_t O_DESC = umma_idesc(BF16, true, kTile, D);
+    unsigned kn = 0, vn = 0;          // tiles consumed
+    unsigned wn[2] = {0, 0}, un = 0;  // weight tiles of a stream, units
+    // S of stream st against the key tile in stage kn (not yet released)
+    auto scores = [&](int st) {
+      if (lane == 0) {
+        const char *a = q_tile + (PAIR ? st : 0) * L::kTileBytes;
+        const char *b = k_tile + (kn % L::kK) * L::kTileBytes;
+        tmem_fence_after();
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const int at = (i / 4) * (kTile * 128) + (i % 4) * 32;
+          umma_ss(tmem + st * kTile, umma_desc(a + at, 16),
+                  umma_desc(b + at, 16), S_DESC, i > 0);
+        }
+        umma_commit(&s.s_full[st]);
+      }
+    };
+    auto wait_k = [&] {
+      fine = fine && attn_wait(&s.k_full[kn % L::kK], kn / L::kK & 1,
+                               &s.abort, p.dev_status);
+    };
+    auto release_k = [&] {
+      if (lane == 0) umma_commit(&s.k_empty[kn % L::kK]);
+      ++kn;
+    };
+    // O of stream st with the value tile in stage vn
+    auto values = [&](int st, bool first) {
+      fine = fine && attn_wait(&s.w_full[st], wn[st] & 1, &s.abort,
+                               p.dev_status);
+      ++wn[st];
+      if (lane == 0 && fine) {
+        const char *b = v_tile + (vn % L::kV) * L::kTileBytes;
+        tmem_fence_after();
+#pragma unroll
+        for (int i = 0; i < kTile / 16; ++i)
+          umma_ts(tmem + 2 * kTile + st * D, tmem + st * kTile + i * 8,
+                  umma_desc(b + i * 16 * 128, kTile * 128), O_DESC,
+                  !first || i > 0);
+        umma_commit(&s.o_full[st]);
+      }
+    };
+    // Wait for value tile j; what lies past the sequence's keys becomes
+    // zero, so that 0 x NaN of a stale page cannot reach the sums.
+    auto wait_v = [&](int j) {
+      fine = fine && attn_wait(&s.v_full[vn % L::kV], vn / L::kV & 1,
+                               &s.abort, p.dev_status);
+      const int from = u.c.kv - j * kTile;
+      if (from < kTile) {
+        const int to = (from + p.box - 1) / p.box * p.box;
+        char *v = v_tile + (vn % L::kV) * L::kTileBytes;
+        for (int i = lane; i < (to - from) * 8 * (D / 64); i += 32) {
+          const int row = from + i / 8 % (to - from);
+          const int half = i / 8 / (to - from);
+          *reinterpret_cast<uint4 *>(v + half * (kTile * 128) + row * 128 +
+                                     (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async();
+        __syncwarp();
+      }
+    };
+    auto release_v = [&] {
+      if (lane == 0) umma_commit(&s.v_empty[vn % L::kV]);
+      ++vn;
+    };
+    for (; u.left && fine; u.next(), ++un) {
+      const int cnt = u.j1 - u.j0;
+      fine = attn_wait(&s.q_full[0], un & 1, &s.abort, p.dev_status);
+      if (PAIR) {
+        const int ns = u.rows > kTile ? 2 : 1;
+        if (fine)
+          fine = attn_wait(&s.q_full[1], un & 1, &s.abort, p.dev_status);
+        wait_k();
+        if (!fine) break;
+        for (int st = 0; st < ns; ++st) scores(st);
+        release_k();
+        for (int i = 0; i < cnt && fine; ++i) {
+          wait_v(u.j0 + i);
+          for (int st = 0; st < ns && fine; ++st) {
+            values(st, i == 0);
+            if (i + 1 < cnt) {
+              if (st == 0) wait_k();
+              if (fine) scores(st);
+            }
+          }
+          release_v();
+          if (i + 1 < cnt) release_k();
+        }
+      } else {
+        for (int i = 0; i < 2 && i < cnt && fine; ++i) {
+          wait_k();
+          if (fine) scores(i);
+          release_k();
+        }
+        for (int i = 0; i < cnt && fine; ++i) {
+          wait_v(u.j0 + i);
+          values(i & 1, i < 2);
+          release_v();
+          if (i + 2 < cnt && fine) {
+            wait_k();
+            if (fine) scores(i & 1);
+            release_k();
+          }
+        }
+      }
+    }
+    if (!fine) {  // tensor memory is freed below: let products in flight end
+      if (lane == 0) umma_commit(&s.drain);
+      for (unsigned it = 0; it < (1u << 20); ++it)
+        if (mbar_try_wait(&s.drain, 0)) break;
+    }
+  } else {
+    // ---- softmax: stream st, a thread per row
+    const int st = warp >> 2, r = tid & (kTile - 1);
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes << 16
+    const uint32_t s_addr = tmem + lanes + st * kTile;
+    const float sl = p.scale_log2;
+    unsigned tn = 0;  // tiles of this stream seen
+    if (tid == 0) p.cut[blockIdx.x].parts = 0;
+    for (; u.left && fine; u.next()) {
+      if (tid == 0 && u.j0 == 0 && u.j1 < u.nk) {
+        // this CTA's last unit goes on in the CTAs up to the one whose
+        // share holds the unit's last tile
+        const unsigned long long end = s.plan.x1 + (u.nk - u.j1);
+        CutUnit cut;
+        cut.parts = (int)((end * s.plan.n - 1) / s.plan.total) -
+                    (int)blockIdx.x + 1;
+        cut.rows = u.rows;
+        cut.start = u.c.start;
+        cut.head = u.h;
+        cut.first = (long long)u.t * ROWS;
+        p.cut[blockIdx.x] = cut;
+      }
+      const int cnt_all = u.j1 - u.j0;
+      const int cnt = PAIR ? cnt_all : (cnt_all - st + 1) / 2;
+      const int base_row = PAIR ? st * kTile : 0;
+      const long long first_row = (long long)u.t * ROWS;
+      // a stream without rows only keeps the unit count
+      const bool active = !PAIR || u.rows > base_row;
+      const bool mine = base_row + r < u.rows;
+      const bool warp_rows = base_row + (warp & 3) * 32 < u.rows;
+      const int token =
+          mine ? (int)((first_row + base_row + r) / p.G) : 0;
+      const int ctx = u.c.kv - u.c.n, limit = ctx + token;
+      if (active) {
+        // the unit's queries, in the tiles' swizzle
+        constexpr int CH = D / 8;
+        constexpr int NT = PAIR ? 128 : 256;
+        const int me = PAIR ? r : tid;
+        char *dst = q_tile + (PAIR ? st : 0) * L::kTileBytes;
+#pragma unroll 4
+        for (int i = me; i < kTile * CH; i += NT) {
+          const int row = i / CH, ch = i % CH;
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (base_row + row < u.rows) {
+            const long long at = first_row + base_row + row;
+            const int tok = (int)(at / p.G), g = (int)(at % p.G);
+            x = __ldg(reinterpret_cast<const uint4 *>(
+                    (const T *)p.q + (u.c.start + tok) * p.q_stride +
+                    (long long)(u.h * p.G + g) * D) +
+                ch);
+          }
+          *reinterpret_cast<uint4 *>(dst + (ch >> 3) * (kTile * 128) +
+                                     row * 128 +
+                                     (((ch & 7) ^ (row & 7)) << 4)) = x;
+        }
+        fence_proxy_async();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.q_full[PAIR ? st : 0]);
+      float m = -kInf, l = 0.f;
+      for (int i = 0; active && i < cnt; ++i, ++tn) {
+        const int j = u.j0 + (PAIR ? i : 2 * i + st);
+        fine = attn_wait(&s.s_full[st], tn & 1, &s.abort, p.dev_status);
+        if (!__all_sync(~0u, fine)) { fine = false; break; }
+        if (warp_rows) {
+          uint32_t x[kTile];
+          tmem_fence_after();
+#pragma unroll
+          for (int c = 0; c < kTile; c += 32) tmem_ld32(s_addr + c, x + c);
+          tmem_wait_ld();
+          // only tiles past the first row's last key hide anything
+          const int key = j * kTile;
+          const bool cuts = key + kTile - 1 > (p.mask ? ctx - 1 : limit);
+          if (__any_sync(~0u, cuts)) {
+#pragma unroll
+            for (int c = 0; c < kTile; c += 32) {
+              const uint32_t seen =
+                  mine ? seen_bits(p, u.c, token, limit, key + c) : 0;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(seen >> e & 1)) x[c + e] = 0xff800000u;
+            }
+          }
+          float top[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float *f = reinterpret_cast<const float *>(x) + 32 * c;
+            float a = fmaxf(f[0], f[1]);
+#pragma unroll
+            for (int e = 2; e < 32; e += 2) a = max3f(a, f[e], f[e + 1]);
+            top[c] = a;
+          }
+          const float mt = fmaxf(max3f(top[0], top[1], top[2]), top[3]);
+          // a new reference where the maximum has risen enough
+          const bool raise = mt > -kInf && !((mt - m) * sl <= kSlack);
+          float f = 1.f;
+          if (raise) {
+            f = m == -kInf ? 1.f : ex2((m - mt) * sl);
+            m = mt;
+            l *= f;
+          }
+          if (__any_sync(~0u, raise) && i > 0) {
+            fine = attn_wait(&s.o_full[st], (tn - 1) & 1, &s.abort,
+                             p.dev_status);
+            if (!__all_sync(~0u, fine)) { fine = false; break; }
+            tmem_fence_after();
+            const uint32_t o_addr = tmem + lanes + 2 * kTile + st * D;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(o_addr + c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(o_addr + c, o);
+            }
+          }
+          const float off = m == -kInf ? 0.f : -m * sl;
+          const float2 k2 = make_float2(sl, sl), o2 = make_float2(off, off);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < kTile; c += 32) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              float2 z = make_float2(__uint_as_float(x[c + e]),
+                                     __uint_as_float(x[c + e + 1]));
+              z = fma2(z, k2, o2);
+              z.x = ex2(z.x);
+              z.y = ex2(z.y);
+              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], z);
+              w[e >> 1] = pack2<T>(z.x, z.y);
+            }
+            tmem_st16(s_addr + c / 2, w);
+          }
+          const float2 t2 = add2(sum[0], sum[1]);
+          l += t2.x + t2.y;
+          tmem_wait_st();
+          tmem_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.w_full[st]);
+      }
+      if (!fine) break;
+      // ---- the end of the unit: O is complete
+      if (active && cnt > 0) {
+        fine = attn_wait(&s.o_full[st], (tn - 1) & 1, &s.abort, p.dev_status);
+        if (!__all_sync(~0u, fine)) { fine = false; break; }
+        tmem_fence_after();
+      }
+      // the two streams' sums of the same rows are joined; stream st then
+      // writes column half st.  256 rows: each its own rows, all columns.
+      float f0 = 1.f, f1 = 0.f;
+      if (!PAIR) {
+        s.ml[st][r] = make_float2(m, l);
+        tmem_fence_before();
+        streams_sync();
+        tmem_fence_after();
+        const float2 other = s.ml[st ^ 1][r];
+        const float mj = fmaxf(m, other.x);
+        const float fm = m == -kInf ? 0.f : ex2((m - mj) * sl);
+        const float fo = other.x == -kInf ? 0.f : ex2((other.x - mj) * sl);
+        l = l * fm + other.y * fo;
+        m = mj;
+        f0 = st ? fo : fm;
+        f1 = st ? fm : fo;
+      }
+      if (s.bad[u.count % kBadRing] == u.count) l = __int_as_float(0x7fc00000);
+      const bool whole = u.j0 == 0 && u.j1 == u.nk;
+      const int c_lo = PAIR ? 0 : st * (D / 2), c_n = PAIR ? D : D / 2;
+      const uint32_t o_addr =
+          tmem + lanes + 2 * kTile + (PAIR ? st * D : 0) + c_lo;
+      const bool second = !PAIR && cnt_all > 1;
+      if (warp_rows) {
+        const long long at = first_row + base_row + r;
+        const int g = mine ? (int)(at % p.G) : 0;
+        const long long row =
+            ((long long)(u.c.start + token) * p.Hq + u.h * p.G + g);
+        const long long part =
+            ((long long)blockIdx.x * 2 + (u.j0 == 0 ? 1 : 0)) * ROWS +
+            base_row + r;
+        // no key seen: 0; a NaN sum stays NaN
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (whole) f0 *= inv, f1 *= inv;
+        if (mine && (PAIR || st == 0)) {
+          if (!whole) p.part_ml[part] = make_float2(m * sl, l);
+          else if (p.lse)
+            p.lse[row] = l == 0.f ? -kInf : (m * sl + log2f(l)) * kLn2;
+        }
+        for (int c = 0; c < c_n; c += 32) {
+          uint32_t a[32];
+          tmem_ld32(o_addr + c, a);
+          tmem_wait_ld();
+          float o[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(a[e]) * f0;
+          if (second) {
+            tmem_ld32(o_addr + D + c, a);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = fmaf(__uint_as_float(a[e]), f1, o[e]);
+          }
+          if (!mine) continue;
+          if (whole) {
+            uint4 *dst = reinterpret_cast<uint4 *>((T *)p.out + row * D +
+                                                   c_lo + c);
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              dst[e / 8] = make_uint4(
+                  pack2<T>(o[e], o[e + 1]), pack2<T>(o[e + 2], o[e + 3]),
+                  pack2<T>(o[e + 4], o[e + 5]), pack2<T>(o[e + 6], o[e + 7]));
+          } else {
+            float4 *dst =
+                reinterpret_cast<float4 *>(p.part_o + part * D + c_lo + c);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              dst[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+      }
+      tmem_fence_before();
+      if (!PAIR) streams_sync();  // O, m, l and Q may be overwritten
+    }
+  }
+
+  if (s.plan.any_unusable) {
+    // NaN for the sequences that cannot be read
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+      const Chunk c = attn_chunk(p, b);
+      if (c.usable || c.n == 0) continue;
+      if (tid == 0) status_or(p.dev_status, SD_DEV_BAD_LENGTH);
+      const long long lo = (long long)c.start * p.Hq,
+                      n = (long long)c.n * p.Hq;
+      for (long long i = tid; i < n * D; i += kAttnThreads)
+        ((T *)p.out)[lo * D + i] = narrow<T>(__int_as_float(0x7fc00000));
+      if (p.lse)
+        for (long long i = tid; i < n; i += kAttnThreads)
+          p.lse[lo + i] = __int_as_float(0x7fc00000);
+    }
+  }
+  tmem_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_free_all(tmem);
+}
+
+// Joins the parts of cut units: a warp per row.  Block (x, y): the unit
+// that CTA x began, rows 8 y ...
+template <class T, int D, int ROWS>
+__global__ void __launch_bounds__(kThreads)
+attention_join_kernel(const __grid_constant__ AttnParams p) {
+  griddep_wait();
+  const CutUnit cut = p.cut[blockIdx.x];
+  const int r = blockIdx.y * kWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (cut.parts < 2 || r >= cut.rows) return;
+  auto slot = [&](int k) {
+    return ((long long)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * ROWS + r;
+  };
+  float m = -kInf;
+  for (int k = lane; k < cut.parts; k += 32)
+    m = fmaxf(m, p.part_ml[slot(k)].x);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
+  constexpr int E = D / 32;
+  float l = 0.f, o[E] = {};
+#pragma unroll 4
+  for (int k = 0; k < cut.parts; ++k) {
+    const long long at = slot(k);
+    const float2 ml = p.part_ml[at];
+    const float w = ml.x == -kInf ? (ml.y == ml.y ? 0.f : ml.y)
+                                  : ex2(ml.x - m);
+    l = fmaf(ml.y, w, l);
+    const float *src = p.part_o + at * D + lane * E;
+    if constexpr (E == 4) {
+      const float4 x = *reinterpret_cast<const float4 *>(src);
+      o[0] = fmaf(x.x, w, o[0]);
+      o[1] = fmaf(x.y, w, o[1]);
+      o[2] = fmaf(x.z, w, o[2]);
+      o[3] = fmaf(x.w, w, o[3]);
+    } else {
+      const float2 x = *reinterpret_cast<const float2 *>(src);
+      o[0] = fmaf(x.x, w, o[0]);
+      o[1] = fmaf(x.y, w, o[1]);
+    }
+  }
+  const long long at = cut.first + r;
+  const long long row = (cut.start + at / p.G) * p.Hq +
+                        (long long)cut.head * p.G + at % p.G;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t *dst = reinterpret_cast<uint32_t *>((T *)p.out + row * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2)
+    dst[e / 2] = pack2<T>(o[e] * inv, o[e + 1] * inv);
+  if (p.lse && lane == 0)
+    p.lse[row] = l == 0.f ? -kInf : (m + log2f(l)) * kLn2;
+}
+
+// ------------------------------------------------------------------- host
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType,
+                                 cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *,
+                                 const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion,
+                                 CUtensorMapFloatOOBfill);
+
+sd_status encoder(EncodeTiled *out) {
+  static std::atomic<EncodeTiled> known{nullptr};
+  EncodeTiled f = known.load(std::memory_order_acquire);
+  if (!f) {
+    void *fn = nullptr;
+    cudaDriverEntryPointQueryResult res;
+    SDV_CUDA(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn,
+                                              12000, cudaEnableDefault, &res));
+    if (!fn || res != cudaDriverEntryPointSuccess)
+      return fail(SD_ERR_UNSUPPORTED, "the driver has no tensor maps");
+    f = reinterpret_cast<EncodeTiled>(fn);
+    known.store(f, std::memory_order_release);
+  }
+  *out = f;
+  return SD_OK;
+}
+
+// The cache as (head_dim, token of a page, head, page), in boxes of 64
+// columns (128 bytes) x `box` tokens, swizzled; what lies outside is zero.
+sd_status cache_map(const sd_paged_kv *c, void *base, int box,
+                    CUtensorMap *map) {
+  EncodeTiled enc = nullptr;
+  const sd_status st = encoder(&enc);
+  if (st != SD_OK) return st;
+  const cuuint64_t pages = c->num_pages > 0 ? c->num_pages : 1;
+  const cuuint64_t dims[4] = {(cuuint64_t)c->head_dim,
+                              (cuuint64_t)c->page_size,
+                              (cuuint64_t)c->heads, pages};
+  // a dimension of one element has no stride of its own
+  const cuuint64_t any = (cuuint64_t)c->head_dim * 2;
+  const cuuint64_t strides[3] = {
+      (cuuint64_t)c->token_stride * 2,
+      c->heads > 1 ? (cuuint64_t)c->head_stride * 2 : any,
+      pages > 1 ? (cuuint64_t)c->page_stride * 2 : any};
+  const cuuint32_t boxes[4] = {64, (cuuint32_t)box, 1, 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  const CUresult r = enc(
+      map,
+      c->dt == SD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+      4, base, dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(SD_ERR_INVALID_ARG,
+                "no tensor map for the cache's strides (%lld, %lld, %lld)",
+                c->page_stride, c->token_stride, c->head_stride);
+  return SD_OK;
+}
+
+struct WsLayout {
+  size_t cut, ml, o, bytes;
+};
+WsLayout ws_layout(int rows, int D) {
+  WsLayout w;
+  w.cut = 0;
+  w.ml = (kMaxGrid * sizeof(CutUnit) + 255) / 256 * 256;
+  w.o = w.ml + (size_t)kMaxGrid * 2 * rows * sizeof(float2);
+  w.bytes = w.o + (size_t)kMaxGrid * 2 * rows * D * sizeof(float);
+  return w;
+}
+
+// 256 rows a unit where a chunk has more than 128 of them.
+bool pair_rows(int max_q, int G) { return (long long)max_q * G > kTile; }
+
+template <class T, int D, bool PAIR>
+sd_status launch(AttnParams &p, const CUtensorMap &k_map,
+                 const CUtensorMap &v_map, int sms, char *ws,
+                 cudaStream_t s) {
+  using L = Layout<D, PAIR>;
+  const WsLayout w = ws_layout(L::kRows, D);
+  p.cut = reinterpret_cast<CutUnit *>(ws + w.cut);
+  p.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
+  p.part_o = reinterpret_cast<float *>(ws + w.o);
+  const void *kernel = (const void *)attention_kernel<T, D, PAIR>;
+  int dev = 0;
+  SDV_CUDA(cudaGetDevice(&dev));
+  static std::atomic<unsigned long long> ready{0};
+  if (dev >= 64 || !(ready.load() >> dev & 1)) {
+    SDV_CUDA(cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        (int)attn_smem<D, PAIR>()));
+    if (dev < 64) ready.fetch_or(1ull << dev);
+  }
+  const unsigned grid = sms < kMaxGrid ? sms : kMaxGrid;
+  void *args[] = {&p, const_cast<CUtensorMap *>(&k_map),
+                  const_cast<CUtensorMap *>(&v_map)};
+  sd_status st = launch_pdl(kernel, grid, kAttnThreads,
+                            attn_smem<D, PAIR>(), s, args);
+  if (st != SD_OK) return st;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, L::kRows / kWarps, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void *jargs[] = {&p};
+  SDV_CUDA(cudaLaunchKernelExC(
+      &cfg, (const void *)attention_join_kernel<T, D, L::kRows>, jargs));
+  return SD_OK;
 }
 
 template <class T>
-sd_status launch(const AttnParams &p, int D, cudaStream_t s) {
-  const long long blocks = ((long long)p.total * p.Hq + kWarps - 1) / kWarps;
-  SDV_REQUIRE(blocks < (1LL << 31), "too many rows");
+sd_status dispatch(AttnParams &p, int D, bool pair, const CUtensorMap &km,
+                   const CUtensorMap &vm, int sms, char *ws, cudaStream_t s) {
   if (D == 64)
-    attention_row_kernel<T, 64><<<(unsigned)blocks, kThreads, 0, s>>>(p);
-  else
-    attention_row_kernel<T, 128><<<(unsigned)blocks, kThreads, 0, s>>>(p);
-  SDV_CUDA(cudaGetLastError());
-  return SD_OK;
+    return pair ? launch<T, 64, true>(p, km, vm, sms, ws, s)
+                : launch<T, 64, false>(p, km, vm, sms, ws, s);
+  return pair ? launch<T, 128, true>(p, km, vm, sms, ws, s)
+              : launch<T, 128, false>(p, km, vm, sms, ws, s);
 }
 
 }  // namespace
@@ -115,11 +994,10 @@ using namespace sdv;
 
 extern "C" size_t sd_paged_attention_workspace(int q_heads, int heads,
                                                int head_dim, int max_q) {
-  (void)q_heads;
-  (void)heads;
-  (void)head_dim;
-  (void)max_q;
-  return 0;
+  if (heads < 1 || q_heads < heads || (head_dim != 64 && head_dim != 128))
+    return 256;
+  return ws_layout(pair_rows(max_q, q_heads / heads) ? 256 : 128, head_dim)
+      .bytes;
 }
 
 extern "C" sd_status sd_paged_attention(
@@ -128,8 +1006,6 @@ extern "C" sd_status sd_paged_attention(
     int mask_words, int B, int total, int max_q, float scale, void *out,
     float *lse, int32_t *dev_status, void *workspace, size_t ws_bytes,
     void *stream) {
-  (void)workspace;
-  (void)ws_bytes;
   sd_status st = check_cache(cache);
   if (st != SD_OK) return st;
   const int D = cache->head_dim;
@@ -157,13 +1033,17 @@ extern "C" sd_status sd_paged_attention(
                   cache->page_stride % 8 == 0 &&
                   cache->token_stride % 8 == 0 && cache->head_stride % 8 == 0,
               "the cache must be 16-byte aligned, its strides multiples of 8");
+  SDV_REQUIRE((long long)total * q_heads < (1LL << 31),
+              "total x q_heads does not fit 31 bits");
+  const size_t need = sd_paged_attention_workspace(q_heads, cache->heads, D,
+                                                   max_q);
+  SDV_REQUIRE(workspace && ws_bytes >= need && aligned16(workspace),
+              "a 16-byte aligned workspace of >= %zu bytes required", need);
   int sms = 0;
   st = check_device(&sms);
   if (st != SD_OK) return st;
   AttnParams p;
   p.q = q;
-  p.k = cache->k;
-  p.v = cache->v;
   p.q_stride = q_stride;
   p.q_start = q_start;
   p.kv_len = kv_len;
@@ -177,14 +1057,21 @@ extern "C" sd_status sd_paged_attention(
   p.num_pages = cache->num_pages;
   p.page_size = cache->page_size;
   p.max_pages = cache->max_pages;
-  p.page_stride = cache->page_stride;
-  p.token_stride = cache->token_stride;
-  p.head_stride = cache->head_stride;
+  p.G = q_heads / cache->heads;
+  for (p.box = 8; p.box < kTile && cache->page_size % (2 * p.box) == 0;)
+    p.box *= 2;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.out = out;
   p.lse = lse;
   p.dev_status = dev_status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return cache->dt == SD_BF16 ? launch<__nv_bfloat16>(p, D, s)
-                              : launch<__half>(p, D, s);
+  CUtensorMap k_map, v_map;
+  st = cache_map(cache, cache->k, p.box, &k_map);
+  if (st == SD_OK) st = cache_map(cache, cache->v, p.box, &v_map);
+  if (st != SD_OK) return st;
+  const bool pair = pair_rows(max_q, p.G);
+  char *ws = static_cast<char *>(workspace);
+  return cache->dt == SD_BF16
+             ? dispatch<__nv_bfloat16>(p, D, pair, k_map, v_map, sms, ws, s)
+             : dispatch<__half>(p, D, pair, k_map, v_map, sms, ws, s);
 }
