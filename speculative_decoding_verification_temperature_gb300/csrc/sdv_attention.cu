@@ -34,7 +34,7 @@ namespace {
 
 constexpr int kTile = 128;       // keys per tile, rows per stream
 constexpr int kMaxGrid = 160;    // CTAs the workspace is laid out for
-constexpr int kAttnThreads = 320;
+constexpr int kAttnThreads = 384;  // two warpgroups of softmax, one of roles
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr int kBadRing = 64;     // units whose bad-page mark is kept
 constexpr float kLn2 = 0.693147180559945f;
@@ -48,6 +48,7 @@ struct AttnParams {
   const int32_t *q_start, *kv_len, *block_table, *mask;
   int mask_words;
   int B, total, Hq, Hkv, G;
+  FastDiv by_G, by_page;
   int num_pages, page_size, max_pages;
   int box;  // rows of one TMA box: a power of two that divides the page
   float scale_log2;  // scale x log2(e)
@@ -65,7 +66,7 @@ struct AttnParams {
 struct CutUnit {
   int parts, rows;     // rows: valid rows of the tile
   int start, head;     // packed row of the sequence, cache head
-  long long first;     // first row of the tile in (token, group) order
+  int first;           // first row of the tile in (token, group) order
 };
 
 // ------------------------------------------------------------ work units
@@ -79,7 +80,7 @@ __device__ __forceinline__ Chunk attn_chunk(const AttnParams &p, int b) {
 template <int ROWS>
 __device__ __forceinline__ int row_tiles(const AttnParams &p,
                                          const Chunk &c) {
-  return c.usable ? (int)(((long long)c.n * p.G + ROWS - 1) / ROWS) : 0;
+  return c.usable ? (c.n * p.G + ROWS - 1) / ROWS : 0;
 }
 
 // Key tiles that row tile t sees.
@@ -88,8 +89,8 @@ __device__ __forceinline__ int key_tiles(const AttnParams &p, const Chunk &c,
                                          int t) {
   int last = c.kv - 1;
   if (!p.mask) {
-    const long long i = ((long long)(t + 1) * ROWS - 1) / p.G;
-    if (i < c.n - 1) last = c.kv - c.n + (int)i;
+    const int i = div_by((t + 1) * ROWS - 1, p.by_G);
+    if (i < c.n - 1) last = c.kv - c.n + i;
   }
   return last / kTile + 1;
 }
@@ -105,9 +106,9 @@ __device__ unsigned long long head_tiles(const AttnParams &p,
 
 // The plan of one CTA: its share [x0, x1) of all tiles, and where x0 lies.
 struct Plan {
-  unsigned long long total, x0, x1, rem;  // rem: x0 within sequence b
+  unsigned long long total, x0, x1;
   unsigned long long warp_sum[8];
-  int n, b;
+  int n, b, h, t, j;  // shares; the unit and key tile where x0 lies
   int any_unusable;
 };
 
@@ -170,8 +171,20 @@ __device__ void make_plan(const AttnParams &p, Plan &s) {
     }
     const unsigned long long lo = before + inc - w;
     if (tid < 256 && s.x0 >= lo && s.x0 < lo + w) {
+      const Chunk c = attn_chunk(p, base + tid);
+      const unsigned long long per = head_tiles<ROWS>(p, c);
+      unsigned long long r = s.x0 - lo;
+      s.h = (int)(r / per);
+      r %= per;
+      int t = 0;
+      for (;; ++t) {
+        const int k = key_tiles<ROWS>(p, c, t);
+        if (r < (unsigned long long)k) break;
+        r -= k;
+      }
       s.b = base + tid;
-      s.rem = s.x0 - lo;
+      s.t = t;
+      s.j = (int)r;
     }
     carry += all;
     __syncthreads();
@@ -190,28 +203,18 @@ template <int ROWS> struct Units {
   int count;        // units begun
 
   __device__ Units(const AttnParams &p_, const Plan &s)
-      : p(p_), left(s.x1 - s.x0), b(s.b), h(0), t(0), T(0), j0(0), count(0) {
+      : p(p_), left(s.x1 - s.x0), b(s.b), h(s.h), t(s.t), T(0), j0(s.j),
+        count(0) {
     if (!left) return;
     c = attn_chunk(p, b);
     T = row_tiles<ROWS>(p, c);
-    const unsigned long long per = head_tiles<ROWS>(p, c);
-    h = (int)(s.rem / per);
-    unsigned long long r = s.rem % per;
-    for (;;) {
-      const int k = key_tiles<ROWS>(p, c, t);
-      if (r < (unsigned long long)k) break;
-      r -= k;
-      ++t;
-    }
-    j0 = (int)r;
     set();
   }
   __device__ void set() {
     ++count;
     nk = key_tiles<ROWS>(p, c, t);
     j1 = (unsigned long long)(nk - j0) < left ? nk : j0 + (int)left;
-    const long long r = (long long)c.n * p.G - (long long)t * ROWS;
-    rows = r < ROWS ? (int)r : ROWS;
+    rows = min(c.n * p.G - t * ROWS, ROWS);
   }
   __device__ void next() {
     left -= j1 - j0;
@@ -382,9 +385,14 @@ attention_kernel(const __grid_constant__ AttnParams p,
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = s.tmem;
-  Units<ROWS> u(p, s.plan);
   bool fine = true;
 
+  // 384 threads start with 168 registers each; a softmax thread holds a row
+  // of 128 scores, a role next to nothing: 256 x 224 + 128 x 56 = 384 x 168
+  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  else asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+  if (warp >= 8) {
+  Units<ROWS> u(p, s.plan);
   if (warp == kLoadWarp) {
     // ---- key and value tiles, a box of page rows at a time
     const int per = kTile / p.box;  // boxes of a tile and column half
@@ -402,11 +410,12 @@ attention_kernel(const __grid_constant__ AttnParams p,
           const int key = j * kTile + a * p.box;
           page = p.num_pages > 0 ? p.num_pages : 1;  // out of range: zeros
           if (key < u.c.kv) {
-            const int id = __ldg(table + key / p.page_size);
+            const int at = div_by(key, p.by_page);
+            const int id = __ldg(table + at);
             if (id >= 0 && id < p.num_pages) page = id;
             else bad = true;
+            tok = key - at * p.page_size;
           }
-          tok = key % p.page_size;
         }
         if (__any_sync(~0u, bad) && lane == 0) {
           s.bad[u.count % kBadRing] = u.count;
@@ -457,27 +466,29 @@ attention_kernel(const __grid_constant__ AttnParams p,
     constexpr uint32_t O_DESC = umma_idesc(BF16, true, kTile, D);
     unsigned kn = 0, vn = 0;          // tiles consumed
     unsigned wn[2] = {0, 0}, un = 0;  // weight tiles of a stream, units
+    const uint32_t lead = lane == 0;
+    constexpr uint32_t HI = umma_desc_hi(1024);
     // S of stream st against the key tile in stage kn (not yet released)
     auto scores = [&](int st) {
-      if (lane == 0) {
-        const char *a = q_tile + (PAIR ? st : 0) * L::kTileBytes;
-        const char *b = k_tile + (kn % L::kK) * L::kTileBytes;
-        tmem_fence_after();
+      const uint32_t a = uniform(
+          umma_desc_lo(q_tile + (PAIR ? st : 0) * L::kTileBytes, 16));
+      const uint32_t b = uniform(
+          umma_desc_lo(k_tile + (kn % L::kK) * L::kTileBytes, 16));
+      const uint32_t d = uniform(tmem + st * kTile);
+      tmem_fence_after();
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const int at = (i / 4) * (kTile * 128) + (i % 4) * 32;
-          umma_ss(tmem + st * kTile, umma_desc(a + at, 16),
-                  umma_desc(b + at, 16), S_DESC, i > 0);
-        }
-        umma_commit(&s.s_full[st]);
+      for (int i = 0; i < D / 16; ++i) {
+        const int at = ((i / 4) * (kTile * 128) + (i % 4) * 32) / 16;
+        umma_ss<HI>(d, a + at, b + at, S_DESC, i > 0, lead);
       }
+      umma_commit(&s.s_full[st], lead);
     };
     auto wait_k = [&] {
       fine = fine && attn_wait(&s.k_full[kn % L::kK], kn / L::kK & 1,
                                &s.abort, p.dev_status);
     };
     auto release_k = [&] {
-      if (lane == 0) umma_commit(&s.k_empty[kn % L::kK]);
+      umma_commit(&s.k_empty[kn % L::kK], lead);
       ++kn;
     };
     // O of stream st with the value tile in stage vn
@@ -485,16 +496,18 @@ attention_kernel(const __grid_constant__ AttnParams p,
       fine = fine && attn_wait(&s.w_full[st], wn[st] & 1, &s.abort,
                                p.dev_status);
       ++wn[st];
-      if (lane == 0 && fine) {
-        const char *b = v_tile + (vn % L::kV) * L::kTileBytes;
-        tmem_fence_after();
+      if (!fine) return;
+      const uint32_t b = uniform(umma_desc_lo(
+          v_tile + (vn % L::kV) * L::kTileBytes, kTile * 128));
+      const uint32_t w = uniform(tmem + st * kTile);
+      const uint32_t d = uniform(tmem + 2 * kTile + st * D);
+      const bool add = uniform(!first);
+      tmem_fence_after();
 #pragma unroll
-        for (int i = 0; i < kTile / 16; ++i)
-          umma_ts(tmem + 2 * kTile + st * D, tmem + st * kTile + i * 8,
-                  umma_desc(b + i * 16 * 128, kTile * 128), O_DESC,
-                  !first || i > 0);
-        umma_commit(&s.o_full[st]);
-      }
+      for (int i = 0; i < kTile / 16; ++i)
+        umma_ts<HI>(d, w + i * 8, b + i * 16 * 128 / 16, O_DESC, add || i > 0,
+                    lead);
+      umma_commit(&s.o_full[st], lead);
     };
     // Wait for value tile j; what lies past the sequence's keys becomes
     // zero, so that 0 x NaN of a stale page cannot reach the sums.
@@ -516,7 +529,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
       }
     };
     auto release_v = [&] {
-      if (lane == 0) umma_commit(&s.v_empty[vn % L::kV]);
+      umma_commit(&s.v_empty[vn % L::kV], lead);
       ++vn;
     };
     for (; u.left && fine; u.next(), ++un) {
@@ -561,11 +574,13 @@ attention_kernel(const __grid_constant__ AttnParams p,
       }
     }
     if (!fine) {  // tensor memory is freed below: let products in flight end
-      if (lane == 0) umma_commit(&s.drain);
+      umma_commit(&s.drain, lead);
       for (unsigned it = 0; it < (1u << 20); ++it)
         if (mbar_try_wait(&s.drain, 0)) break;
     }
+  }
   } else {
+    Units<ROWS> u(p, s.plan);
     // ---- softmax: stream st, a thread per row
     const int st = warp >> 2, r = tid & (kTile - 1);
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes << 16
@@ -584,19 +599,19 @@ attention_kernel(const __grid_constant__ AttnParams p,
         cut.rows = u.rows;
         cut.start = u.c.start;
         cut.head = u.h;
-        cut.first = (long long)u.t * ROWS;
+        cut.first = u.t * ROWS;
         p.cut[blockIdx.x] = cut;
       }
       const int cnt_all = u.j1 - u.j0;
       const int cnt = PAIR ? cnt_all : (cnt_all - st + 1) / 2;
       const int base_row = PAIR ? st * kTile : 0;
-      const long long first_row = (long long)u.t * ROWS;
+      const int first_row = u.t * ROWS;
       // a stream without rows only keeps the unit count
       const bool active = !PAIR || u.rows > base_row;
       const bool mine = base_row + r < u.rows;
       const bool warp_rows = base_row + (warp & 3) * 32 < u.rows;
       const int token =
-          mine ? (int)((first_row + base_row + r) / p.G) : 0;
+          mine ? div_by(first_row + base_row + r, p.by_G) : 0;
       const int ctx = u.c.kv - u.c.n, limit = ctx + token;
       if (active) {
         // the unit's queries, in the tiles' swizzle
@@ -604,20 +619,21 @@ attention_kernel(const __grid_constant__ AttnParams p,
         constexpr int NT = PAIR ? 128 : 256;
         const int me = PAIR ? r : tid;
         char *dst = q_tile + (PAIR ? st : 0) * L::kTileBytes;
-#pragma unroll 4
-        for (int i = me; i < kTile * CH; i += NT) {
-          const int row = i / CH, ch = i % CH;
+        const int ch = me % CH;
+        const T *src = (const T *)p.q + u.c.start * p.q_stride +
+                       (long long)u.h * p.G * D + ch * 8;
+        dst += (ch >> 3) * (kTile * 128);
+#pragma unroll
+        for (int i = 0; i < kTile * CH / NT; ++i) {
+          const int row = me / CH + i * (NT / CH);
           uint4 x = make_uint4(0, 0, 0, 0);
           if (base_row + row < u.rows) {
-            const long long at = first_row + base_row + row;
-            const int tok = (int)(at / p.G), g = (int)(at % p.G);
+            const int at = first_row + base_row + row;
+            const int tok = div_by(at, p.by_G);
             x = __ldg(reinterpret_cast<const uint4 *>(
-                    (const T *)p.q + (u.c.start + tok) * p.q_stride +
-                    (long long)(u.h * p.G + g) * D) +
-                ch);
+                src + tok * p.q_stride + (at - tok * p.G) * D));
           }
-          *reinterpret_cast<uint4 *>(dst + (ch >> 3) * (kTile * 128) +
-                                     row * 128 +
+          *reinterpret_cast<uint4 *>(dst + row * 128 +
                                      (((ch & 7) ^ (row & 7)) << 4)) = x;
         }
         fence_proxy_async();
@@ -740,8 +756,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
           tmem + lanes + 2 * kTile + (PAIR ? st * D : 0) + c_lo;
       const bool second = !PAIR && cnt_all > 1;
       if (warp_rows) {
-        const long long at = first_row + base_row + r;
-        const int g = mine ? (int)(at % p.G) : 0;
+        const int g = mine ? first_row + base_row + r - token * p.G : 0;
         const long long row =
             ((long long)(u.c.start + token) * p.Hq + u.h * p.G + g);
         const long long part =
@@ -852,9 +867,9 @@ attention_join_kernel(const __grid_constant__ AttnParams p) {
       o[1] = fmaf(x.y, w, o[1]);
     }
   }
-  const long long at = cut.first + r;
-  const long long row = (cut.start + at / p.G) * p.Hq +
-                        (long long)cut.head * p.G + at % p.G;
+  const int at = cut.first + r, tok = div_by(at, p.by_G);
+  const long long row = (long long)(cut.start + tok) * p.Hq +
+                        cut.head * p.G + (at - tok * p.G);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint32_t *dst = reinterpret_cast<uint32_t *>((T *)p.out + row * D + lane * E);
 #pragma unroll
@@ -1033,7 +1048,7 @@ extern "C" sd_status sd_paged_attention(
                   cache->page_stride % 8 == 0 &&
                   cache->token_stride % 8 == 0 && cache->head_stride % 8 == 0,
               "the cache must be 16-byte aligned, its strides multiples of 8");
-  SDV_REQUIRE((long long)total * q_heads < (1LL << 31),
+  SDV_REQUIRE((long long)total * q_heads < (1LL << 31) - 256,
               "total x q_heads does not fit 31 bits");
   const size_t need = sd_paged_attention_workspace(q_heads, cache->heads, D,
                                                    max_q);
@@ -1058,6 +1073,8 @@ extern "C" sd_status sd_paged_attention(
   p.page_size = cache->page_size;
   p.max_pages = cache->max_pages;
   p.G = q_heads / cache->heads;
+  p.by_G = fast_div(p.G);
+  p.by_page = fast_div(cache->page_size);
   for (p.box = 8; p.box < kTile && cache->page_size % (2 * p.box) == 0;)
     p.box *= 2;
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);

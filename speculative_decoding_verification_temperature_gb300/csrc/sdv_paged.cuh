@@ -57,6 +57,23 @@ __device__ __forceinline__ int find_sequence(const int32_t *q_start, int B,
   return lo;
 }
 
+// Division of 0 <= x < 2^31 by a fixed d >= 1 as a multiplication (Granlund
+// and Montgomery, "Division by invariant integers using multiplication",
+// 1994): with l = ceil(log2 d) and mul = floor(2^32 (2^l - d) / d) + 1 the
+// quotient is (hi(mul x) + x) >> l.
+struct FastDiv {
+  uint32_t mul, shift;
+};
+inline FastDiv fast_div(uint32_t d) {
+  FastDiv f = {0, 0};
+  while (f.shift < 31 && (1u << f.shift) < d) ++f.shift;
+  f.mul = (uint32_t)(((1ull << 32) * ((1ull << f.shift) - d)) / d + 1);
+  return f;
+}
+__device__ __forceinline__ int div_by(int x, FastDiv f) {
+  return (int)((__umulhi((uint32_t)x, f.mul) + (uint32_t)x) >> f.shift);
+}
+
 // Host checks of a cache description.
 inline sd_status check_cache(const sd_paged_kv *c) {
   SDV_REQUIRE(c != nullptr, "cache is null");

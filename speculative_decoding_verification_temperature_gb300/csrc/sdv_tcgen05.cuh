@@ -81,15 +81,24 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
 }
 
 // Shared-memory matrix descriptor of a tile of 128-byte rows in the
-// 128-byte swizzle (16-byte chunk c of row r lies at chunk c ^ (r & 7)):
-// groups of eight rows are 1024 bytes apart; lead_bytes is the distance
-// between 64-element column blocks where the operand runs along its rows
-// (MN-major), and unused where it runs along the reduction (K-major).
-__device__ __forceinline__ uint64_t umma_desc(const void *tile,
-                                              uint32_t lead_bytes) {
-  return (uint64_t)((smem_addr(tile) & 0x3ffff) >> 4) |
-         (uint64_t)(lead_bytes >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// 128-byte swizzle (16-byte chunk c of row r lies at chunk c ^ (r & 7)).
+// Low word: address, and lead_bytes, the distance between 64-element column
+// blocks where the operand runs along its rows (MN-major; unused where it
+// runs along the reduction, K-major).  High word: the distance between
+// groups of eight rows, the version and the swizzle.  Moving along the tile
+// adds bytes / 16 to the low word.
+__device__ __forceinline__ uint32_t umma_desc_lo(const void *tile,
+                                                 uint32_t lead_bytes) {
+  return (smem_addr(tile) & 0x3ffff) >> 4 | (lead_bytes >> 4) << 16;
+}
+__host__ __device__ constexpr uint32_t umma_desc_hi(uint32_t group_bytes) {
+  return group_bytes >> 4 | 1u << 14 | 2u << 29;
+}
+
+// A value that is the same in every lane, known to be so by the compiler:
+// tcgen05 operands live in uniform registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) {
+  return __shfl_sync(~0u, x, 0);
 }
 
 // Instruction descriptor: fp32 sums, both operands bf16 or fp16, A with the
@@ -102,30 +111,42 @@ __host__ __device__ constexpr uint32_t umma_idesc(bool bf16, bool b_mn_major,
 }
 
 // One step of 16 along the reduction: D (+)= A B, A in shared memory or in
-// tensor memory (two elements a column).  One thread issues; steps run in
-// the order issued.
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b,
-                                        uint32_t idesc, bool add) {
+// tensor memory (two elements a column).  The whole warp calls these with
+// the same operands and the lane with `lead` set issues: a predicate, not a
+// branch, keeps the operands in uniform registers (in a branch each product
+// took ~125 cycles to issue).  Products run in the order issued.
+template <uint32_t HI>
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo,
+                                        uint32_t b_lo, uint32_t idesc,
+                                        bool add, uint32_t lead) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
-}
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b,
-                                        uint32_t idesc, bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(
           d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)add), "n"(HI), "r"(lead)
       : "memory");
 }
-// Arrive on `bar` when every tcgen05.mma this thread issued is complete.
-__device__ __forceinline__ void umma_commit(uint64_t *bar) {
+template <uint32_t HI>
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b_lo,
+                                        uint32_t idesc, bool add,
+                                        uint32_t lead) {
   asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 "
-      "[%0];" ::"r"(smem_addr(bar))
+      "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %6, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(
+          d),
+      "r"(a), "r"(b_lo), "r"(idesc), "r"((uint32_t)add), "n"(HI), "r"(lead)
+      : "memory");
+}
+// Arrive on `bar` when every tcgen05.mma the lead lane issued is complete.
+__device__ __forceinline__ void umma_commit(uint64_t *bar, uint32_t lead) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster"
+      ".b64 [%0];\n\t}" ::"r"(smem_addr(bar)), "r"(lead)
       : "memory");
 }
 
