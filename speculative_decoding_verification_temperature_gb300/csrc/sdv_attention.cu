@@ -337,6 +337,34 @@ __device__ __forceinline__ uint32_t seen_bits(const AttnParams &p,
   return bits & in;
 }
 
+__device__ __forceinline__ float max32(const uint32_t *x) {
+  const float *f = reinterpret_cast<const float *>(x);
+  float a = fmaxf(f[0], f[1]), b = fmaxf(f[2], f[3]);
+#pragma unroll
+  for (int e = 4; e < 32; e += 4) {
+    a = max3f(a, f[e], f[e + 1]);
+    b = max3f(b, f[e + 2], f[e + 3]);
+  }
+  return fmaxf(a, b);
+}
+
+// The largest of a row's 128 scores after hide(chunk, column).
+template <class Hide>
+__device__ __forceinline__ float row_max(uint32_t s_addr, Hide hide) {
+  float m = -kInf;
+#pragma unroll
+  for (int c = 0; c < kTile; c += 64) {
+    uint32_t x[64];
+    tmem_ld32(s_addr + c, x);
+    tmem_ld32(s_addr + c + 32, x + 32);
+    tmem_wait_ld();
+    hide(x, c);
+    hide(x + 32, c + 32);
+    m = max3f(m, max32(x), max32(x + 32));
+  }
+  return m;
+}
+
 // ------------------------------------------------------------- the kernel
 template <class T, int D, bool PAIR>
 __global__ void __launch_bounds__(kAttnThreads, 1)
@@ -461,53 +489,55 @@ attention_kernel(const __grid_constant__ AttnParams p,
         }
     }
   } else if (warp == kMmaWarp) {
-    // ---- tensor-core products, issued by lane 0
+    // ---- tensor-core products
     constexpr uint32_t S_DESC = umma_idesc(BF16, false, kTile, kTile);
     constexpr uint32_t O_DESC = umma_idesc(BF16, true, kTile, D);
     unsigned kn = 0, vn = 0;          // tiles consumed
     unsigned wn[2] = {0, 0}, un = 0;  // weight tiles of a stream, units
-    const uint32_t lead = lane == 0;
     constexpr uint32_t HI = umma_desc_hi(1024);
-    // S of stream st against the key tile in stage kn (not yet released)
-    auto scores = [&](int st) {
-      const uint32_t a = uniform(
-          umma_desc_lo(q_tile + (PAIR ? st : 0) * L::kTileBytes, 16));
-      const uint32_t b = uniform(
-          umma_desc_lo(k_tile + (kn % L::kK) * L::kTileBytes, 16));
-      const uint32_t d = uniform(tmem + st * kTile);
-      tmem_fence_after();
+    // S of stream st against key tile kn; `last`: nothing else reads the tile
+    auto scores = [&](int st, bool last) {
+      const uint32_t a =
+          umma_desc_lo(q_tile + (PAIR ? st : 0) * L::kTileBytes, 16);
+      const uint32_t b =
+          umma_desc_lo(k_tile + (kn % L::kK) * L::kTileBytes, 16);
+      if (elect_one()) {
+        tmem_fence_after();
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const int at = ((i / 4) * (kTile * 128) + (i % 4) * 32) / 16;
-        umma_ss<HI>(d, a + at, b + at, S_DESC, i > 0, lead);
+        for (int i = 0; i < D / 16; ++i) {
+          const int at = ((i / 4) * (kTile * 128) + (i % 4) * 32) / 16;
+          umma_ss<HI>(tmem + st * kTile, a + at, b + at, S_DESC, i > 0);
+        }
+        umma_commit(&s.s_full[st]);
+        if (last) umma_commit(&s.k_empty[kn % L::kK]);
       }
-      umma_commit(&s.s_full[st], lead);
+      __syncwarp();
+      if (last) ++kn;
     };
     auto wait_k = [&] {
       fine = fine && attn_wait(&s.k_full[kn % L::kK], kn / L::kK & 1,
                                &s.abort, p.dev_status);
     };
-    auto release_k = [&] {
-      umma_commit(&s.k_empty[kn % L::kK], lead);
-      ++kn;
-    };
-    // O of stream st with the value tile in stage vn
-    auto values = [&](int st, bool first) {
+    // O of stream st with value tile vn
+    auto values = [&](int st, bool first, bool last) {
+      const uint32_t b = umma_desc_lo(
+          v_tile + (vn % L::kV) * L::kTileBytes, kTile * 128);
+      const uint32_t w = tmem + st * kTile, d = tmem + 2 * kTile + st * D;
       fine = fine && attn_wait(&s.w_full[st], wn[st] & 1, &s.abort,
                                p.dev_status);
       ++wn[st];
       if (!fine) return;
-      const uint32_t b = uniform(umma_desc_lo(
-          v_tile + (vn % L::kV) * L::kTileBytes, kTile * 128));
-      const uint32_t w = uniform(tmem + st * kTile);
-      const uint32_t d = uniform(tmem + 2 * kTile + st * D);
-      const bool add = uniform(!first);
-      tmem_fence_after();
+      if (elect_one()) {
+        tmem_fence_after();
 #pragma unroll
-      for (int i = 0; i < kTile / 16; ++i)
-        umma_ts<HI>(d, w + i * 8, b + i * 16 * 128 / 16, O_DESC, add || i > 0,
-                    lead);
-      umma_commit(&s.o_full[st], lead);
+        for (int i = 0; i < kTile / 16; ++i)
+          umma_ts<HI>(d, w + i * 8, b + i * 16 * 128 / 16, O_DESC,
+                      !first || i > 0);
+        umma_commit(&s.o_full[st]);
+        if (last) umma_commit(&s.v_empty[vn % L::kV]);
+      }
+      __syncwarp();
+      if (last) ++vn;
     };
     // Wait for value tile j; what lies past the sequence's keys becomes
     // zero, so that 0 x NaN of a stale page cannot reach the sums.
@@ -528,10 +558,6 @@ attention_kernel(const __grid_constant__ AttnParams p,
         __syncwarp();
       }
     };
-    auto release_v = [&] {
-      umma_commit(&s.v_empty[vn % L::kV], lead);
-      ++vn;
-    };
     for (; u.left && fine; u.next(), ++un) {
       const int cnt = u.j1 - u.j0;
       fine = attn_wait(&s.q_full[0], un & 1, &s.abort, p.dev_status);
@@ -541,40 +567,35 @@ attention_kernel(const __grid_constant__ AttnParams p,
           fine = attn_wait(&s.q_full[1], un & 1, &s.abort, p.dev_status);
         wait_k();
         if (!fine) break;
-        for (int st = 0; st < ns; ++st) scores(st);
-        release_k();
+        for (int st = 0; st < ns; ++st) scores(st, st == ns - 1);
         for (int i = 0; i < cnt && fine; ++i) {
+          // both tiles first: between a stream's weights and its next
+          // scores nothing is waited for
           wait_v(u.j0 + i);
+          if (i + 1 < cnt) wait_k();
           for (int st = 0; st < ns && fine; ++st) {
-            values(st, i == 0);
-            if (i + 1 < cnt) {
-              if (st == 0) wait_k();
-              if (fine) scores(st);
-            }
+            values(st, i == 0, st == ns - 1);
+            if (i + 1 < cnt && fine) scores(st, st == ns - 1);
           }
-          release_v();
-          if (i + 1 < cnt) release_k();
         }
       } else {
         for (int i = 0; i < 2 && i < cnt && fine; ++i) {
           wait_k();
-          if (fine) scores(i);
-          release_k();
+          if (fine) scores(i, true);
         }
         for (int i = 0; i < cnt && fine; ++i) {
           wait_v(u.j0 + i);
-          values(i & 1, i < 2);
-          release_v();
+          values(i & 1, i < 2, true);
           if (i + 2 < cnt && fine) {
             wait_k();
-            if (fine) scores(i & 1);
-            release_k();
+            if (fine) scores(i & 1, true);
           }
         }
       }
     }
     if (!fine) {  // tensor memory is freed below: let products in flight end
-      umma_commit(&s.drain, lead);
+      if (elect_one()) umma_commit(&s.drain);
+      __syncwarp();
       for (unsigned it = 0; it < (1u << 20); ++it)
         if (mbar_try_wait(&s.drain, 0)) break;
     }
@@ -646,43 +667,60 @@ attention_kernel(const __grid_constant__ AttnParams p,
         fine = attn_wait(&s.s_full[st], tn & 1, &s.abort, p.dev_status);
         if (!__all_sync(~0u, fine)) { fine = false; break; }
         if (warp_rows) {
-          uint32_t x[kTile];
           tmem_fence_after();
-#pragma unroll
-          for (int c = 0; c < kTile; c += 32) tmem_ld32(s_addr + c, x + c);
-          tmem_wait_ld();
-          // only tiles past the first row's last key hide anything
+          // only tiles past the row's last key hide anything
           const int key = j * kTile;
-          const bool cuts = key + kTile - 1 > (p.mask ? ctx - 1 : limit);
-          if (__any_sync(~0u, cuts)) {
+          const bool cuts = __any_sync(
+              ~0u, key + kTile - 1 > (p.mask ? ctx - 1 : limit));
+          auto hide = [&](uint32_t *x, int c) {
+            if (!cuts) return;
+            const uint32_t seen =
+                mine ? seen_bits(p, u.c, token, limit, key + c) : 0;
 #pragma unroll
-            for (int c = 0; c < kTile; c += 32) {
-              const uint32_t seen =
-                  mine ? seen_bits(p, u.c, token, limit, key + c) : 0;
+            for (int e = 0; e < 32; ++e)
+              if (!(seen >> e & 1)) x[e] = 0xff800000u;
+          };
+          float f = 1.f;  // what the row's earlier sums are scaled by
+          if (i == 0) m = row_max(s_addr, hide);
+          // weights against the reference at hand; where the tile's maximum
+          // turns out too far above it (rare), once more against a new one
+          uint32_t w[kTile / 2];
+          float2 sum[2];
+          for (bool moved = false;; moved = true) {
+            const float off = m == -kInf ? 0.f : -m * sl;
+            const float2 k2 = make_float2(sl, sl), o2 = make_float2(off, off);
+            sum[0] = sum[1] = make_float2(0.f, 0.f);
+            float mt = -kInf;
+            uint32_t x[2][32];
+            tmem_ld32(s_addr, x[0]);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(seen >> e & 1)) x[c + e] = 0xff800000u;
+            for (int c = 0; c < kTile / 32; ++c) {
+              uint32_t *xc = x[c & 1];
+              tmem_wait_ld();
+              if (c + 1 < kTile / 32)
+                tmem_ld32(s_addr + 32 * (c + 1), x[(c + 1) & 1]);
+              hide(xc, 32 * c);
+              mt = fmaxf(mt, max32(xc));
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float2 z = make_float2(__uint_as_float(xc[e]),
+                                       __uint_as_float(xc[e + 1]));
+                z = fma2(z, k2, o2);
+                z.x = ex2(z.x);
+                z.y = ex2(z.y);
+                sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], z);
+                w[16 * c + (e >> 1)] = pack2<T>(z.x, z.y);
+              }
+            }
+            if (moved) break;
+            const bool raise = mt > -kInf && !((mt - m) * sl <= kSlack);
+            if (!__any_sync(~0u, raise)) break;
+            if (raise) {
+              f = m == -kInf ? 1.f : ex2((m - mt) * sl);
+              m = mt;
             }
           }
-          float top[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const float *f = reinterpret_cast<const float *>(x) + 32 * c;
-            float a = fmaxf(f[0], f[1]);
-#pragma unroll
-            for (int e = 2; e < 32; e += 2) a = max3f(a, f[e], f[e + 1]);
-            top[c] = a;
-          }
-          const float mt = fmaxf(max3f(top[0], top[1], top[2]), top[3]);
-          // a new reference where the maximum has risen enough
-          const bool raise = mt > -kInf && !((mt - m) * sl <= kSlack);
-          float f = 1.f;
-          if (raise) {
-            f = m == -kInf ? 1.f : ex2((m - mt) * sl);
-            m = mt;
-            l *= f;
-          }
-          if (__any_sync(~0u, raise) && i > 0) {
+          if (__any_sync(~0u, f != 1.f)) {
             fine = attn_wait(&s.o_full[st], (tn - 1) & 1, &s.abort,
                              p.dev_status);
             if (!__all_sync(~0u, fine)) { fine = false; break; }
@@ -699,26 +737,10 @@ attention_kernel(const __grid_constant__ AttnParams p,
               tmem_st32(o_addr + c, o);
             }
           }
-          const float off = m == -kInf ? 0.f : -m * sl;
-          const float2 k2 = make_float2(sl, sl), o2 = make_float2(off, off);
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int c = 0; c < kTile; c += 32) {
-            uint32_t w[16];
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float2 z = make_float2(__uint_as_float(x[c + e]),
-                                     __uint_as_float(x[c + e + 1]));
-              z = fma2(z, k2, o2);
-              z.x = ex2(z.x);
-              z.y = ex2(z.y);
-              sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], z);
-              w[e >> 1] = pack2<T>(z.x, z.y);
-            }
-            tmem_st16(s_addr + c / 2, w);
-          }
+          tmem_st32(s_addr, w);
+          tmem_st32(s_addr + 32, w + 32);
           const float2 t2 = add2(sum[0], sum[1]);
-          l += t2.x + t2.y;
+          l = fmaf(l, f, t2.x + t2.y);
           tmem_wait_st();
           tmem_fence_before();
         }

@@ -95,10 +95,17 @@ __host__ __device__ constexpr uint32_t umma_desc_hi(uint32_t group_bytes) {
   return group_bytes >> 4 | 1u << 14 | 2u << 29;
 }
 
-// A value that is the same in every lane, known to be so by the compiler:
-// tcgen05 operands live in uniform registers.
-__device__ __forceinline__ uint32_t uniform(uint32_t x) {
-  return __shfl_sync(~0u, x, 0);
+// One lane of the (converged) warp, always the same one.  The products are
+// issued in a branch on this: 64 cycles apart at N = 128, the tensor cores'
+// own rate; in a branch on the lane number they took 125, under a predicate
+// 66 and more.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
 }
 
 // Instruction descriptor: fp32 sums, both operands bf16 or fp16, A with the
@@ -111,42 +118,36 @@ __host__ __device__ constexpr uint32_t umma_idesc(bool bf16, bool b_mn_major,
 }
 
 // One step of 16 along the reduction: D (+)= A B, A in shared memory or in
-// tensor memory (two elements a column).  The whole warp calls these with
-// the same operands and the lane with `lead` set issues: a predicate, not a
-// branch, keeps the operands in uniform registers (in a branch each product
-// took ~125 cycles to issue).  Products run in the order issued.
+// tensor memory (two elements a column).  One thread issues; products run in
+// the order issued.
 template <uint32_t HI>
 __device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo,
                                         uint32_t b_lo, uint32_t idesc,
-                                        bool add, uint32_t lead) {
+                                        bool add) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t.reg .b64 a, b;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
       "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %6, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(
-          d),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)add), "n"(HI), "r"(lead)
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)add), "n"(HI)
       : "memory");
 }
 template <uint32_t HI>
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b_lo,
-                                        uint32_t idesc, bool add,
-                                        uint32_t lead) {
+                                        uint32_t idesc, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p, e;\n\t.reg .b64 b;\n\t"
-      "mov.b64 b, {%2, %5};\n\t"
-      "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %6, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(
           d),
-      "r"(a), "r"(b_lo), "r"(idesc), "r"((uint32_t)add), "n"(HI), "r"(lead)
+      "r"(a), "r"(b_lo), "r"(idesc), "r"((uint32_t)add), "n"(HI)
       : "memory");
 }
-// Arrive on `bar` when every tcgen05.mma the lead lane issued is complete.
-__device__ __forceinline__ void umma_commit(uint64_t *bar, uint32_t lead) {
+// Arrive on `bar` when every tcgen05.mma this thread issued is complete.
+__device__ __forceinline__ void umma_commit(uint64_t *bar) {
   asm volatile(
-      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
-      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster"
-      ".b64 [%0];\n\t}" ::"r"(smem_addr(bar)), "r"(lead)
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 "
+      "[%0];" ::"r"(smem_addr(bar))
       : "memory");
 }
 
