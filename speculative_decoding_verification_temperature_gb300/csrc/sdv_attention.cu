@@ -35,7 +35,7 @@ namespace {
 constexpr int kTile = 128;       // keys per tile, rows per stream
 constexpr int kMaxGrid = 160;    // CTAs the workspace is laid out for
 constexpr int kAttnThreads = 384;  // two warpgroups of softmax, one of roles
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kMmaWarp = 9;  // and 10; warps 8 and 11 load
 constexpr int kBadRing = 64;     // units whose bad-page mark is kept
 constexpr float kLn2 = 0.693147180559945f;
 // A row's reference moves only when its maximum is 2^8 above it: weights
@@ -239,18 +239,24 @@ template <int ROWS> struct Units {
 template <int D, bool PAIR> struct Layout {
   static constexpr int kRows = PAIR ? 256 : 128;
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int kQTiles = PAIR ? 2 : 1;
-  // as many stages as fit: what is in flight covers the latency of HBM
-  static constexpr int kK = D == 128 ? 3 : PAIR ? 4 : 5;
-  static constexpr int kV = D == 128 ? (PAIR ? 2 : 3) : PAIR ? 4 : 5;
+  // the queries; at the end of a unit, staging for its rows (4 KB a warp)
+  static constexpr int kQBytes = PAIR ? 2 * kTileBytes : 32768;
+  // Two rings of tiles, as many as fit: what is in flight covers the latency
+  // of HBM.  PAIR: ring 0 holds the key tiles, ring 1 the value tiles, read
+  // by both streams.  Otherwise ring st holds stream st's tiles in the order
+  // it uses them (key, value, key, ...): a ring with one writer and one
+  // reader, so that a stream that is ahead never takes a slot's earlier
+  // filling for its own.
+  static constexpr int kN0 = D == 128 ? 3 : PAIR ? 4 : 5;
+  static constexpr int kN1 = D == 128 ? (PAIR ? 2 : 3) : PAIR ? 4 : 5;
   static constexpr size_t kTiles =
-      (size_t)kTileBytes * (kQTiles + kK + kV);
+      kQBytes + (size_t)kTileBytes * (kN0 + kN1);
 };
 
 template <int D, bool PAIR> struct Shared {
   using L = Layout<D, PAIR>;
-  uint64_t k_full[L::kK], k_empty[L::kK], v_full[L::kV], v_empty[L::kV];
-  uint64_t q_full[2], s_full[2], w_full[2], o_full[2], drain;
+  uint64_t full[2][L::kN0], empty[2][L::kN0];
+  uint64_t q_full[2], s_full[2], w_full[2], o_full[2], drain[2];
   uint32_t tmem;
   volatile int abort;
   int bad[kBadRing];  // unit count whose pages were bad
@@ -275,9 +281,23 @@ __device__ __forceinline__ bool attn_wait(uint64_t *bar, uint32_t parity,
   return false;
 }
 
+// A position in a ring of n slots: the slot, and the parity of its filling.
+struct RingAt {
+  int slot, n;
+  uint32_t parity;
+  __device__ RingAt(int n_) : slot(0), n(n_), parity(0) {}
+  __device__ void next() {
+    if (++slot == n) slot = 0, parity ^= 1;
+  }
+};
+
 // A barrier of the two softmax warpgroups alone.
 __device__ __forceinline__ void streams_sync() {
   asm volatile("bar.sync 1, 256;" ::: "memory");
+}
+
+__device__ __forceinline__ void stream_sync(int st) {
+  asm volatile("bar.sync %0, 128;" ::"r"(2 + st) : "memory");
 }
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -348,6 +368,13 @@ __device__ __forceinline__ float max32(const uint32_t *x) {
   return fmaxf(a, b);
 }
 
+// 16-byte piece `piece` of row `row` in a warp's 32 rows of 128 bytes,
+// swizzled: rows written by a lane each are read along without conflicts.
+__device__ __forceinline__ uint4 *stage_at(char *stage, int row, int piece) {
+  return reinterpret_cast<uint4 *>(stage + row * 128 +
+                                   ((piece ^ (row & 7)) << 4));
+}
+
 // The largest of a row's 128 scores after hide(chunk, column).
 template <class Hide>
 __device__ __forceinline__ float row_max(uint32_t s_addr, Hide hide) {
@@ -377,32 +404,30 @@ attention_kernel(const __grid_constant__ AttnParams p,
   extern __shared__ __align__(1024) char dyn[];  // swizzled tiles first
   Shared<D, PAIR> &s = *reinterpret_cast<Shared<D, PAIR> *>(dyn + L::kTiles);
   char *q_tile = dyn;
-  char *k_tile = q_tile + L::kQTiles * L::kTileBytes;
-  char *v_tile = k_tile + L::kK * L::kTileBytes;
+  char *ring[2] = {q_tile + L::kQBytes,
+                   q_tile + L::kQBytes + L::kN0 * L::kTileBytes};
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int i = 0; i < L::kK; ++i) {
-      mbar_init(&s.k_full[i], 1);
-      mbar_init(&s.k_empty[i], 1);
-    }
-    for (int i = 0; i < L::kV; ++i) {
-      mbar_init(&s.v_full[i], 1);
-      mbar_init(&s.v_empty[i], 1);
-    }
+    for (int i = 0; i < 2; ++i)
+      for (int k = 0; k < L::kN0; ++k) {
+        mbar_init(&s.full[i][k], 1);
+        mbar_init(&s.empty[i][k], PAIR ? 2 : 1);  // the streams that read it
+      }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.q_full[i], PAIR ? 4 : 8);
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.w_full[i], 4);
       mbar_init(&s.o_full[i], 1);
     }
-    mbar_init(&s.drain, 1);
+    mbar_init(&s.drain[0], 1);
+    mbar_init(&s.drain[1], 1);
     s.abort = 0;
     fence_mbar_init();
   }
   if (tid < kBadRing) s.bad[tid] = 0;
   if (warp == kMmaWarp) tmem_alloc_all(&s.tmem);
-  if (warp == kLoadWarp && lane == 0) {
+  if (warp == 8 && lane == 0) {
     tma_prefetch_map(&k_map);
     tma_prefetch_map(&v_map);
   }
@@ -420,134 +445,114 @@ attention_kernel(const __grid_constant__ AttnParams p,
   if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   else asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
   if (warp >= 8) {
-  Units<ROWS> u(p, s.plan);
-  if (warp == kLoadWarp) {
-    // ---- key and value tiles, a box of page rows at a time
-    const int per = kTile / p.box;  // boxes of a tile and column half
-    constexpr int HALVES = D / 64;
-    unsigned kn = 0, vn = 0;  // tiles issued
-    for (; u.left && fine; u.next()) {
-      const int32_t *table = p.block_table + (long long)u.b * p.max_pages;
-      for (int j = u.j0; j < u.j1 && fine; ++j) {
-        const int ks = kn % L::kK, vs = vn % L::kV;
-        // lane i has boxes i and i + 32 (box = 8: 16 boxes a half)
-        int page = 0, tok = 0;
-        bool bad = false;
-        const int a = lane % per;
-        if (lane < per * HALVES) {
-          const int key = j * kTile + a * p.box;
-          page = p.num_pages > 0 ? p.num_pages : 1;  // out of range: zeros
-          if (key < u.c.kv) {
-            const int at = div_by(key, p.by_page);
-            const int id = __ldg(table + at);
-            if (id >= 0 && id < p.num_pages) page = id;
-            else bad = true;
-            tok = key - at * p.page_size;
+    Units<ROWS> u(p, s.plan);
+    if (warp == 8 || warp == 11) {
+      // ---- ring `me`, a box of page rows at a time
+      const int me = warp == 8 ? 0 : 1;
+      const int per = kTile / p.box;  // boxes of a tile and column half
+      const bool has = lane < per * (D / 64);
+      const int a = lane % per, half = lane / per;
+      const uint32_t to = half * (kTile * 128) + a * p.box * 128;
+      RingAt at(me ? L::kN1 : L::kN0);
+      unsigned filled = 0;
+      int page = 0, tok = 0;
+      auto load = [&](const CUtensorMap *map) {
+        fine = attn_wait(&s.empty[me][at.slot], at.parity ^ 1, &s.abort,
+                         p.dev_status);
+        if (!__all_sync(~0u, fine)) {
+          fine = false;
+          return;
+        }
+        uint64_t *full = &s.full[me][at.slot];
+        if (lane == 0) mbar_expect_tx(full, L::kTileBytes);
+        __syncwarp();
+        if (has)
+          tma_load_4d(ring[me] + at.slot * L::kTileBytes + to, map, half * 64,
+                      tok, u.h, page, full);
+        at.next();
+        ++filled;
+      };
+      for (; u.left && fine; u.next()) {
+        const int32_t *table = p.block_table + (long long)u.b * p.max_pages;
+        const int step = PAIR ? 1 : 2;
+        for (int j = u.j0 + (PAIR ? 0 : me); j < u.j1 && fine; j += step) {
+          bool bad = false;
+          if (has) {
+            const int key = j * kTile + a * p.box;
+            page = p.num_pages > 0 ? p.num_pages : 1;  // out of range: zeros
+            tok = 0;
+            if (key < u.c.kv) {
+              const int n = div_by(key, p.by_page);
+              const int id = __ldg(table + n);
+              if (id >= 0 && id < p.num_pages) page = id;
+              else bad = true;
+              tok = key - n * p.page_size;
+            }
           }
+          if (__any_sync(~0u, bad) && lane == 0) {
+            s.bad[u.count % kBadRing] = u.count;
+            status_or(p.dev_status, SD_DEV_BAD_PAGE);
+          }
+          if (!PAIR || me == 0) load(&k_map);
+          if ((!PAIR || me == 1) && fine) load(&v_map);
         }
-        if (__any_sync(~0u, bad) && lane == 0) {
-          s.bad[u.count % kBadRing] = u.count;
-          status_or(p.dev_status, SD_DEV_BAD_PAGE);
-        }
-        fine = attn_wait(&s.k_empty[ks], (kn / L::kK & 1) ^ 1, &s.abort,
-                         p.dev_status);
-        if (!__all_sync(~0u, fine)) { fine = false; break; }
-        if (lane == 0) mbar_expect_tx(&s.k_full[ks], L::kTileBytes);
-        __syncwarp();
-        if (lane < per * HALVES)
-          tma_load_4d(k_tile + ks * L::kTileBytes + (lane / per) * (kTile * 128) +
-                          a * p.box * 128,
-                      &k_map, (lane / per) * 64, tok, u.h, page,
-                      &s.k_full[ks]);
-        ++kn;
-        fine = attn_wait(&s.v_empty[vs], (vn / L::kV & 1) ^ 1, &s.abort,
-                         p.dev_status);
-        if (!__all_sync(~0u, fine)) { fine = false; break; }
-        if (lane == 0) mbar_expect_tx(&s.v_full[vs], L::kTileBytes);
-        __syncwarp();
-        if (lane < per * HALVES)
-          tma_load_4d(v_tile + vs * L::kTileBytes + (lane / per) * (kTile * 128) +
-                          a * p.box * 128,
-                      &v_map, (lane / per) * 64, tok, u.h, page,
-                      &s.v_full[vs]);
-        ++vn;
       }
-    }
-    if (!fine) {
-      // give up: let the copies in flight land before the CTA ends
-      for (int i = 0; i < L::kK; ++i)
-        if (kn > (unsigned)i) {
-          const unsigned last = (kn - 1 - i) / L::kK;
-          for (unsigned it = 0; it < (1u << 20); ++it)
-            if (mbar_try_wait(&s.k_full[i], last & 1)) break;
-        }
-      for (int i = 0; i < L::kV; ++i)
-        if (vn > (unsigned)i) {
-          const unsigned last = (vn - 1 - i) / L::kV;
-          for (unsigned it = 0; it < (1u << 20); ++it)
-            if (mbar_try_wait(&s.v_full[i], last & 1)) break;
-        }
-    }
-  } else if (warp == kMmaWarp) {
-    // ---- tensor-core products
+      if (!fine) {  // give up: let the copies in flight land first
+        for (int i = 0; i < at.n; ++i)
+          if (filled > (unsigned)i) {
+            const unsigned last = (filled - 1 - i) / at.n;
+            for (unsigned it = 0; it < (1u << 20); ++it)
+              if (mbar_try_wait(&s.full[me][i], last & 1)) break;
+          }
+      }
+    } else {
+    // ---- tensor-core products of stream st, a warp each: while one is held
+    // up issuing (products queue some 200 cycles deep) the other waits for
+    // its weights
+    const int st = warp - kMmaWarp;
     constexpr uint32_t S_DESC = umma_idesc(BF16, false, kTile, kTile);
     constexpr uint32_t O_DESC = umma_idesc(BF16, true, kTile, D);
-    unsigned kn = 0, vn = 0;          // tiles consumed
-    unsigned wn[2] = {0, 0}, un = 0;  // weight tiles of a stream, units
     constexpr uint32_t HI = umma_desc_hi(1024);
-    // S of stream st against key tile kn; `last`: nothing else reads the tile
-    auto scores = [&](int st, bool last) {
-      const uint32_t a =
-          umma_desc_lo(q_tile + (PAIR ? st : 0) * L::kTileBytes, 16);
-      const uint32_t b =
-          umma_desc_lo(k_tile + (kn % L::kK) * L::kTileBytes, 16);
-      if (elect_one()) {
+    const uint32_t s_addr = tmem + st * kTile;
+    const uint32_t o_addr = tmem + 2 * kTile + st * D;
+    const uint32_t q_lo =
+        umma_desc_lo(q_tile + (PAIR ? st : 0) * L::kTileBytes, 16);
+    // where the stream reads keys and values next
+    const int kr = PAIR ? 0 : st, vr = PAIR ? 1 : st;
+    const uint32_t k_lo = umma_desc_lo(ring[kr], 16);
+    const uint32_t v_lo = umma_desc_lo(ring[vr], kTile * 128);
+    RingAt ring_k(kr ? L::kN1 : L::kN0), ring_v(L::kN1);
+    RingAt &k_at = ring_k, &v_at = PAIR ? ring_v : ring_k;
+    uint32_t wp = 0, qp = 0;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      fine = fine && attn_wait(bar, parity, &s.abort, p.dev_status);
+    };
+    // S against the next key tile
+    auto scores = [&] {
+      wait(&s.full[kr][k_at.slot], k_at.parity);
+      if (fine && elect_one()) {
+        const uint32_t b = k_lo + k_at.slot * (L::kTileBytes / 16);
         tmem_fence_after();
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const int at = ((i / 4) * (kTile * 128) + (i % 4) * 32) / 16;
-          umma_ss<HI>(tmem + st * kTile, a + at, b + at, S_DESC, i > 0);
+          umma_ss<HI>(s_addr, q_lo + at, b + at, S_DESC, i > 0);
         }
         umma_commit(&s.s_full[st]);
-        if (last) umma_commit(&s.k_empty[kn % L::kK]);
+        umma_commit(&s.empty[kr][k_at.slot]);
       }
       __syncwarp();
-      if (last) ++kn;
+      k_at.next();
     };
-    auto wait_k = [&] {
-      fine = fine && attn_wait(&s.k_full[kn % L::kK], kn / L::kK & 1,
-                               &s.abort, p.dev_status);
-    };
-    // O of stream st with value tile vn
-    auto values = [&](int st, bool first, bool last) {
-      const uint32_t b = umma_desc_lo(
-          v_tile + (vn % L::kV) * L::kTileBytes, kTile * 128);
-      const uint32_t w = tmem + st * kTile, d = tmem + 2 * kTile + st * D;
-      fine = fine && attn_wait(&s.w_full[st], wn[st] & 1, &s.abort,
-                               p.dev_status);
-      ++wn[st];
-      if (!fine) return;
-      if (elect_one()) {
-        tmem_fence_after();
-#pragma unroll
-        for (int i = 0; i < kTile / 16; ++i)
-          umma_ts<HI>(d, w + i * 8, b + i * 16 * 128 / 16, O_DESC,
-                      !first || i > 0);
-        umma_commit(&s.o_full[st]);
-        if (last) umma_commit(&s.v_empty[vn % L::kV]);
-      }
-      __syncwarp();
-      if (last) ++vn;
-    };
-    // Wait for value tile j; what lies past the sequence's keys becomes
-    // zero, so that 0 x NaN of a stale page cannot reach the sums.
+    // Wait for the value tile of key tile j.  What lies past the sequence's
+    // keys becomes zero, so that 0 x NaN of a stale page cannot reach the
+    // sums (both streams may write the same zeros).
     auto wait_v = [&](int j) {
-      fine = fine && attn_wait(&s.v_full[vn % L::kV], vn / L::kV & 1,
-                               &s.abort, p.dev_status);
+      wait(&s.full[vr][v_at.slot], v_at.parity);
       const int from = u.c.kv - j * kTile;
       if (from < kTile) {
         const int to = (from + p.box - 1) / p.box * p.box;
-        char *v = v_tile + (vn % L::kV) * L::kTileBytes;
+        char *v = ring[vr] + v_at.slot * L::kTileBytes;
         for (int i = lane; i < (to - from) * 8 * (D / 64); i += 32) {
           const int row = from + i / 8 % (to - from);
           const int half = i / 8 / (to - from);
@@ -558,48 +563,54 @@ attention_kernel(const __grid_constant__ AttnParams p,
         __syncwarp();
       }
     };
-    for (; u.left && fine; u.next(), ++un) {
+    // O with that tile
+    auto values = [&](bool first) {
+      wait(&s.w_full[st], wp);
+      wp ^= 1;
+      if (fine && elect_one()) {
+        const uint32_t b = v_lo + v_at.slot * (L::kTileBytes / 16);
+        tmem_fence_after();
+#pragma unroll
+        for (int i = 0; i < kTile / 16; ++i)
+          umma_ts<HI>(o_addr, s_addr + i * 8, b + i * 16 * 128 / 16, O_DESC,
+                      !first || i > 0);
+        umma_commit(&s.o_full[st]);
+        umma_commit(&s.empty[vr][v_at.slot]);
+      }
+      __syncwarp();
+      v_at.next();
+    };
+    for (; u.left && fine; u.next()) {
       const int cnt = u.j1 - u.j0;
-      fine = attn_wait(&s.q_full[0], un & 1, &s.abort, p.dev_status);
-      if (PAIR) {
-        const int ns = u.rows > kTile ? 2 : 1;
-        if (fine)
-          fine = attn_wait(&s.q_full[1], un & 1, &s.abort, p.dev_status);
-        wait_k();
-        if (!fine) break;
-        for (int st = 0; st < ns; ++st) scores(st, st == ns - 1);
+      wait(&s.q_full[PAIR ? st : 0], qp);
+      qp ^= 1;
+      if (PAIR && st == 1 && u.rows <= kTile) {
+        // no rows: let go of every tile as it comes
         for (int i = 0; i < cnt && fine; ++i) {
-          // both tiles first: between a stream's weights and its next
-          // scores nothing is waited for
-          wait_v(u.j0 + i);
-          if (i + 1 < cnt) wait_k();
-          for (int st = 0; st < ns && fine; ++st) {
-            values(st, i == 0, st == ns - 1);
-            if (i + 1 < cnt && fine) scores(st, st == ns - 1);
-          }
+          wait(&s.full[kr][k_at.slot], k_at.parity);
+          if (fine && lane == 0) mbar_arrive(&s.empty[kr][k_at.slot]);
+          k_at.next();
+          wait(&s.full[vr][v_at.slot], v_at.parity);
+          if (fine && lane == 0) mbar_arrive(&s.empty[vr][v_at.slot]);
+          v_at.next();
         }
-      } else {
-        for (int i = 0; i < 2 && i < cnt && fine; ++i) {
-          wait_k();
-          if (fine) scores(i, true);
-        }
-        for (int i = 0; i < cnt && fine; ++i) {
-          wait_v(u.j0 + i);
-          values(i & 1, i < 2, true);
-          if (i + 2 < cnt && fine) {
-            wait_k();
-            if (fine) scores(i & 1, true);
-          }
-        }
+        continue;
+      }
+      const int i0 = PAIR ? 0 : st, step = PAIR ? 1 : 2;
+      if (i0 < cnt) scores();
+      for (int i = i0; i < cnt && fine; i += step) {
+        wait_v(u.j0 + i);
+        values(i == i0);
+        if (i + step < cnt && fine) scores();
       }
     }
     if (!fine) {  // tensor memory is freed below: let products in flight end
-      if (elect_one()) umma_commit(&s.drain);
+      if (elect_one()) umma_commit(&s.drain[st]);
       __syncwarp();
       for (unsigned it = 0; it < (1u << 20); ++it)
-        if (mbar_try_wait(&s.drain, 0)) break;
+        if (mbar_try_wait(&s.drain[st], 0)) break;
     }
-  }
+    }
   } else {
     Units<ROWS> u(p, s.plan);
     // ---- softmax: stream st, a thread per row
@@ -672,14 +683,20 @@ attention_kernel(const __grid_constant__ AttnParams p,
           const int key = j * kTile;
           const bool cuts = __any_sync(
               ~0u, key + kTile - 1 > (p.mask ? ctx - 1 : limit));
+          uint32_t seen[kTile / 32];
+          if (cuts) {
+#pragma unroll
+            for (int c = 0; c < kTile / 32; ++c)
+              seen[c] =
+                  mine ? seen_bits(p, u.c, token, limit, key + 32 * c) : 0;
+          }
           auto hide = [&](uint32_t *x, int c) {
             if (!cuts) return;
-            const uint32_t seen =
-                mine ? seen_bits(p, u.c, token, limit, key + c) : 0;
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (!(seen >> e & 1)) x[e] = 0xff800000u;
+              if (!(seen[c / 32] >> e & 1)) x[e] = 0xff800000u;
           };
+          __syncwarp();
           float f = 1.f;  // what the row's earlier sums are scaled by
           if (i == 0) m = row_max(s_addr, hide);
           // weights against the reference at hand; where the tile's maximum
@@ -719,6 +736,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
               f = m == -kInf ? 1.f : ex2((m - mt) * sl);
               m = mt;
             }
+            __syncwarp();
           }
           if (__any_sync(~0u, f != 1.f)) {
             fine = attn_wait(&s.o_full[st], (tn - 1) & 1, &s.abort,
@@ -737,6 +755,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
               tmem_st32(o_addr + c, o);
             }
           }
+          __syncwarp();
           tmem_st32(s_addr, w);
           tmem_st32(s_addr + 32, w + 32);
           const float2 t2 = add2(sum[0], sum[1]);
@@ -792,40 +811,69 @@ attention_kernel(const __grid_constant__ AttnParams p,
           else if (p.lse)
             p.lse[row] = l == 0.f ? -kInf : (m * sl + log2f(l)) * kLn2;
         }
-        for (int c = 0; c < c_n; c += 32) {
-          uint32_t a[32];
+        // through this warp's part of the query tile (its queries are
+        // used up), so that the stores run along the rows
+        char *stage = PAIR ? q_tile + st * L::kTileBytes + (warp & 3) * 4096
+                           : q_tile + warp * 4096;
+        constexpr int COLS = 32;
+#pragma unroll
+        for (int c = 0; c < c_n; c += COLS) {
+          __syncwarp();  // tcgen05.ld wants the whole warp; the staging is free
+          uint32_t a[COLS];
           tmem_ld32(o_addr + c, a);
           tmem_wait_ld();
-          float o[32];
+          float o[COLS];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(a[e]) * f0;
+          for (int e = 0; e < COLS; ++e) o[e] = __uint_as_float(a[e]) * f0;
           if (second) {
             tmem_ld32(o_addr + D + c, a);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
+            for (int e = 0; e < COLS; ++e)
               o[e] = fmaf(__uint_as_float(a[e]), f1, o[e]);
           }
-          if (!mine) continue;
           if (whole) {
-            uint4 *dst = reinterpret_cast<uint4 *>((T *)p.out + row * D +
-                                                   c_lo + c);
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              dst[e / 8] = make_uint4(
+            for (int e = 0; e < COLS; e += 8)
+              *stage_at(stage, lane, e / 8) = make_uint4(
                   pack2<T>(o[e], o[e + 1]), pack2<T>(o[e + 2], o[e + 3]),
                   pack2<T>(o[e + 4], o[e + 5]), pack2<T>(o[e + 6], o[e + 7]));
           } else {
-            float4 *dst =
-                reinterpret_cast<float4 *>(p.part_o + part * D + c_lo + c);
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              dst[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < COLS; e += 4)
+              *stage_at(stage, lane, e / 4) = make_uint4(
+                  __float_as_uint(o[e]), __float_as_uint(o[e + 1]),
+                  __float_as_uint(o[e + 2]), __float_as_uint(o[e + 3]));
+          }
+          __syncwarp();
+          const int per = whole ? 4 : 8;  // 16-byte pieces of a row
+          const int first = base_row + (warp & 3) * 32;
+#pragma unroll
+          for (int i = lane; i < 32 * per; i += 32) {
+            const int rr = i / per, pc = i % per;
+            const uint4 x = *stage_at(stage, rr, pc);
+            if (first + rr >= u.rows) {
+              // no such row
+            } else if (whole) {
+              const int at = first_row + first + rr;
+              const int tok = div_by(at, p.by_G);
+              const long long to = (long long)(u.c.start + tok) * p.Hq +
+                                   u.h * p.G + (at - tok * p.G);
+              reinterpret_cast<uint4 *>((T *)p.out + to * D + c_lo + c)[pc] =
+                  x;
+            } else {
+              reinterpret_cast<uint4 *>(
+                  p.part_o + (part - r + (warp & 3) * 32 + rr) * D + c_lo +
+                  c)[pc] = x;
+            }
           }
         }
       }
+      __syncwarp();
       tmem_fence_before();
-      if (!PAIR) streams_sync();  // O, m, l and Q may be overwritten
+      // O, m, l and the queries may be overwritten
+      if (PAIR) stream_sync(st);
+      else streams_sync();
     }
   }
 

@@ -277,3 +277,36 @@ def test_cache_offsets_past_32_bits():
     v.copy_(P.v)
     P.to_gpu = lambda t: k if t is P.k else v
     run(P, 2)
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_many_calls_in_a_row_keep_their_bits(page):
+    """A ragged verify round over long prefixes (72 rows a unit, units cut
+    between CTAs), queued a hundred times without waiting: the tile rings of
+    the two streams stay in step whatever order the copies land in."""
+    g = torch.Generator(device="cuda").manual_seed(page)
+    B, n, Hkv, G, D, kv = 24, 9, 8, 8, 128, 4096
+    per = kv // page
+    k = torch.randn(B * per, page, Hkv, D, generator=g, device="cuda").to(BF)
+    v = torch.randn(B * per, page, Hkv, D, generator=g, device="cuda").to(BF)
+    table = torch.randperm(B * per, generator=g, device="cuda").to(
+        torch.int32).view(B, per)
+    cache = api.PagedKV(k, v, table)
+    start = torch.arange(0, B * n + 1, n, dtype=torch.int32, device="cuda")
+    kvl = (torch.rand(B, generator=g, device="cuda") * (kv - n) + n).to(
+        torch.int32)
+    q = torch.randn(B * n, G * Hkv, D, generator=g, device="cuda").to(BF)
+    ws = api.Workspace()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    outs = [api.paged_attention(q, cache, start, kvl, max_q=n, workspace=ws,
+                                status=st)["out"] for _ in range(100)]
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    b, t, h = 3, 4, 11  # one row against 64 bits
+    last = int(kvl[b]) - n + t + 1
+    kk = k[table[b].long()].flatten(0, 1)[:last, h // G].double()
+    vv = v[table[b].long()].flatten(0, 1)[:last, h // G].double()
+    p = torch.softmax(kk @ q[b * n + t, h].double() * D ** -0.5, 0)
+    err = (outs[0][b * n + t, h].double() - p @ vv).abs()
+    assert bool((err <= 2.0 ** -7 * (p @ vv.abs()) + 1e-4).all())
