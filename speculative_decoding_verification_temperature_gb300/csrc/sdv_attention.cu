@@ -256,7 +256,7 @@ template <int D, bool PAIR> struct Layout {
 template <int D, bool PAIR> struct Shared {
   using L = Layout<D, PAIR>;
   uint64_t full[2][L::kN0], empty[2][L::kN0];
-  uint64_t q_full[2], s_full[2], w_full[2], o_full[2], drain[2];
+  uint64_t q_full[2], s_full[2], w_full[2], o_full[2], turn[2], drain[2];
   uint32_t tmem;
   volatile int abort;
   int bad[kBadRing];  // unit count whose pages were bad
@@ -375,9 +375,16 @@ __device__ __forceinline__ uint4 *stage_at(char *stage, int row, int piece) {
                                    ((piece ^ (row & 7)) << 4));
 }
 
-// The largest of a row's 128 scores after hide(chunk, column).
-template <class Hide>
-__device__ __forceinline__ float row_max(uint32_t s_addr, Hide hide) {
+// Scores a row does not see become -inf.
+__device__ __forceinline__ void hide32(uint32_t *x, uint32_t seen) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (!(seen >> e & 1)) x[e] = 0xff800000u;
+}
+
+// The largest of a row's 128 scores (of those it sees, where `cuts`).
+__device__ __forceinline__ float row_max(uint32_t s_addr, bool cuts,
+                                         const uint32_t *seen) {
   float m = -kInf;
 #pragma unroll
   for (int c = 0; c < kTile; c += 64) {
@@ -385,11 +392,50 @@ __device__ __forceinline__ float row_max(uint32_t s_addr, Hide hide) {
     tmem_ld32(s_addr + c, x);
     tmem_ld32(s_addr + c + 32, x + 32);
     tmem_wait_ld();
-    hide(x, c);
-    hide(x + 32, c + 32);
+    if (cuts) {
+      hide32(x, seen[c / 32]);
+      hide32(x + 32, seen[c / 32 + 1]);
+    }
     m = max3f(m, max32(x), max32(x + 32));
   }
   return m;
+}
+
+// A row's weights 2^(s sl + off), rounded and packed, their sum before the
+// rounding, and the largest score.  One warp on a scheduler takes ~810
+// cycles for a tile, two ~1440: the issue slots, not the exponentials, are
+// what it runs on, so hidden scores have a copy of their own.
+template <class T, bool HIDE>
+__device__ __forceinline__ float weigh(uint32_t s_addr, float sl, float off,
+                                       const uint32_t *seen, uint32_t *w,
+                                       float &total) {
+  const float2 k2 = make_float2(sl, sl), o2 = make_float2(off, off);
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  float mt = -kInf;
+  uint32_t x[2][32];
+  tmem_ld32(s_addr, x[0]);
+#pragma unroll
+  for (int c = 0; c < kTile / 32; ++c) {
+    uint32_t *xc = x[c & 1];
+    tmem_wait_ld();
+    if (c + 1 < kTile / 32)
+      tmem_ld32(s_addr + 32 * (c + 1), x[(c + 1) & 1]);
+    if (HIDE) hide32(xc, seen[c]);
+    mt = fmaxf(mt, max32(xc));
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      float2 z = make_float2(__uint_as_float(xc[e]),
+                             __uint_as_float(xc[e + 1]));
+      z = fma2(z, k2, o2);
+      z.x = ex2(z.x);
+      z.y = ex2(z.y);
+      sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], z);
+      w[16 * c + (e >> 1)] = pack2<T>(z.x, z.y);
+    }
+  }
+  const float2 t = add2(sum[0], sum[1]);
+  total = t.x + t.y;
+  return mt;
 }
 
 // ------------------------------------------------------------- the kernel
@@ -419,6 +465,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
       mbar_init(&s.s_full[i], 1);
       mbar_init(&s.w_full[i], 4);
       mbar_init(&s.o_full[i], 1);
+      mbar_init(&s.turn[i], 1);
     }
     mbar_init(&s.drain[0], 1);
     mbar_init(&s.drain[1], 1);
@@ -441,9 +488,9 @@ attention_kernel(const __grid_constant__ AttnParams p,
   bool fine = true;
 
   // 384 threads start with 168 registers each; a softmax thread holds a row
-  // of 128 scores, a role next to nothing: 256 x 224 + 128 x 56 = 384 x 168
-  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-  else asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+  // of 128 scores, a role next to nothing: 256 x 208 + 128 x 88 = 384 x 168
+  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
   if (warp >= 8) {
     Units<ROWS> u(p, s.plan);
     if (warp == 8 || warp == 11) {
@@ -528,11 +575,10 @@ attention_kernel(const __grid_constant__ AttnParams p,
       fine = fine && attn_wait(bar, parity, &s.abort, p.dev_status);
     };
     // S against the next key tile
+    auto wait_k = [&] { wait(&s.full[kr][k_at.slot], k_at.parity); };
     auto scores = [&] {
-      wait(&s.full[kr][k_at.slot], k_at.parity);
       if (fine && elect_one()) {
         const uint32_t b = k_lo + k_at.slot * (L::kTileBytes / 16);
-        tmem_fence_after();
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           const int at = ((i / 4) * (kTile * 128) + (i % 4) * 32) / 16;
@@ -564,12 +610,13 @@ attention_kernel(const __grid_constant__ AttnParams p,
       }
     };
     // O with that tile
-    auto values = [&](bool first) {
+    auto wait_w = [&] {
       wait(&s.w_full[st], wp);
       wp ^= 1;
+    };
+    auto values = [&](bool first) {
       if (fine && elect_one()) {
         const uint32_t b = v_lo + v_at.slot * (L::kTileBytes / 16);
-        tmem_fence_after();
 #pragma unroll
         for (int i = 0; i < kTile / 16; ++i)
           umma_ts<HI>(o_addr, s_addr + i * 8, b + i * 16 * 128 / 16, O_DESC,
@@ -579,6 +626,18 @@ attention_kernel(const __grid_constant__ AttnParams p,
       }
       __syncwarp();
       v_at.next();
+    };
+    // 256 rows: the streams take strict turns, a value and a score product
+    // at a time, so that one's softmax runs under the other's products
+    // (left to themselves they fall into step, and both wait for both)
+    uint32_t tp = st ^ 1;
+    auto take_turn = [&] {
+      wait(&s.turn[st], tp);
+      tp ^= 1;
+    };
+    auto pass_turn = [&] {
+      if (fine && elect_one()) mbar_arrive(&s.turn[st ^ 1]);
+      __syncwarp();
     };
     for (; u.left && fine; u.next()) {
       const int cnt = u.j1 - u.j0;
@@ -597,11 +656,25 @@ attention_kernel(const __grid_constant__ AttnParams p,
         continue;
       }
       const int i0 = PAIR ? 0 : st, step = PAIR ? 1 : 2;
-      if (i0 < cnt) scores();
+      const bool turns = PAIR && u.rows > kTile;
+      if (i0 < cnt) {
+        wait_k();
+        if (turns) take_turn();
+        tmem_fence_after();
+        scores();
+        if (turns) pass_turn();
+      }
       for (int i = i0; i < cnt && fine; i += step) {
+        const bool more = i + step < cnt;
         wait_v(u.j0 + i);
+        if (PAIR && more) wait_k();
+        wait_w();
+        if (turns) take_turn();
+        tmem_fence_after();
         values(i == i0);
-        if (i + step < cnt && fine) scores();
+        if (!PAIR && more) wait_k();
+        if (more) scores();
+        if (turns) pass_turn();
       }
     }
     if (!fine) {  // tensor memory is freed below: let products in flight end
@@ -683,52 +756,26 @@ attention_kernel(const __grid_constant__ AttnParams p,
           const int key = j * kTile;
           const bool cuts = __any_sync(
               ~0u, key + kTile - 1 > (p.mask ? ctx - 1 : limit));
-          uint32_t seen[kTile / 32];
+          uint32_t seen[kTile / 32] = {};
           if (cuts) {
 #pragma unroll
             for (int c = 0; c < kTile / 32; ++c)
               seen[c] =
                   mine ? seen_bits(p, u.c, token, limit, key + 32 * c) : 0;
           }
-          auto hide = [&](uint32_t *x, int c) {
-            if (!cuts) return;
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(seen[c / 32] >> e & 1)) x[e] = 0xff800000u;
-          };
           __syncwarp();
           float f = 1.f;  // what the row's earlier sums are scaled by
-          if (i == 0) m = row_max(s_addr, hide);
+          if (i == 0) m = row_max(s_addr, cuts, seen);
           // weights against the reference at hand; where the tile's maximum
           // turns out too far above it (rare), once more against a new one
           uint32_t w[kTile / 2];
-          float2 sum[2];
+          float sum;
+#pragma unroll 1
           for (bool moved = false;; moved = true) {
             const float off = m == -kInf ? 0.f : -m * sl;
-            const float2 k2 = make_float2(sl, sl), o2 = make_float2(off, off);
-            sum[0] = sum[1] = make_float2(0.f, 0.f);
-            float mt = -kInf;
-            uint32_t x[2][32];
-            tmem_ld32(s_addr, x[0]);
-#pragma unroll
-            for (int c = 0; c < kTile / 32; ++c) {
-              uint32_t *xc = x[c & 1];
-              tmem_wait_ld();
-              if (c + 1 < kTile / 32)
-                tmem_ld32(s_addr + 32 * (c + 1), x[(c + 1) & 1]);
-              hide(xc, 32 * c);
-              mt = fmaxf(mt, max32(xc));
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float2 z = make_float2(__uint_as_float(xc[e]),
-                                       __uint_as_float(xc[e + 1]));
-                z = fma2(z, k2, o2);
-                z.x = ex2(z.x);
-                z.y = ex2(z.y);
-                sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], z);
-                w[16 * c + (e >> 1)] = pack2<T>(z.x, z.y);
-              }
-            }
+            const float mt = cuts ? weigh<T, true>(s_addr, sl, off, seen, w, sum)
+                                  : weigh<T, false>(s_addr, sl, off, seen, w,
+                                                    sum);
             if (moved) break;
             const bool raise = mt > -kInf && !((mt - m) * sl <= kSlack);
             if (!__any_sync(~0u, raise)) break;
@@ -758,8 +805,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
           __syncwarp();
           tmem_st32(s_addr, w);
           tmem_st32(s_addr + 32, w + 32);
-          const float2 t2 = add2(sum[0], sum[1]);
-          l = fmaf(l, f, t2.x + t2.y);
+          l = fmaf(l, f, sum);
           tmem_wait_st();
           tmem_fence_before();
         }
