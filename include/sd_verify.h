@@ -614,7 +614,9 @@ sd_status sd_kv_append(const sd_paged_kv *cache, const void *k,
  *     bit is set: bit (i & 31) of tree_mask[t][i / 32] is token i of the
  *     sequence's chunk.  tree_mask [total, mask_words] int32; chunks longer
  *     than 32 mask_words are unusable (SD_DEV_BAD_LENGTH).  scale > 0.
- * out [total, q_heads, head_dim], contiguous, of the cache's type.
+ * out [total, q_heads, head_dim], contiguous, of the cache's type, 32-byte
+ *     aligned (the workspace too); q, k and v 16-byte aligned, their strides
+ *     multiples of 8 elements.
  * lse [total, q_heads] float (nullable): log sum_j w_j.
  * A token that sees no key gets out = 0 and lse = -inf.  The tokens of an
  * unusable sequence whose q_start is usable, and of a sequence with a

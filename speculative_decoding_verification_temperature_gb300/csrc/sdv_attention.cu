@@ -33,6 +33,7 @@ namespace sdv {
 namespace {
 
 constexpr int kTile = 128;       // keys per tile, rows per stream
+constexpr int kHalf = kTile / 2;  // keys a softmax thread weighs at a time
 constexpr int kMaxGrid = 160;    // CTAs the workspace is laid out for
 constexpr int kAttnThreads = 384;  // two warpgroups of softmax, one of roles
 constexpr int kMmaWarp = 9;  // and 10; warps 8 and 11 load
@@ -210,6 +211,10 @@ template <int ROWS> struct Units {
     T = row_tiles<ROWS>(p, c);
     set();
   }
+  __device__ void to(const Units &o) {  // o walks the same share
+    left = o.left, c = o.c, b = o.b, h = o.h, t = o.t, T = o.T;
+    j0 = o.j0, j1 = o.j1, nk = o.nk, rows = o.rows, count = o.count;
+  }
   __device__ void set() {
     ++count;
     nk = key_tiles<ROWS>(p, c, t);
@@ -239,8 +244,7 @@ template <int ROWS> struct Units {
 template <int D, bool PAIR> struct Layout {
   static constexpr int kRows = PAIR ? 256 : 128;
   static constexpr int kTileBytes = kTile * D * 2;
-  // the queries; at the end of a unit, staging for its rows (4 KB a warp)
-  static constexpr int kQBytes = PAIR ? 2 * kTileBytes : 32768;
+  static constexpr int kQBytes = (PAIR ? 2 : 1) * kTileBytes;
   // Two rings of tiles, as many as fit: what is in flight covers the latency
   // of HBM.  PAIR: ring 0 holds the key tiles, ring 1 the value tiles, read
   // by both streams.  Otherwise ring st holds stream st's tiles in the order
@@ -256,7 +260,8 @@ template <int D, bool PAIR> struct Layout {
 template <int D, bool PAIR> struct Shared {
   using L = Layout<D, PAIR>;
   uint64_t full[2][L::kN0], empty[2][L::kN0];
-  uint64_t q_full[2], s_full[2], w_full[2], o_full[2], turn[2], drain[2];
+  uint64_t q_full[2], s_full[2], turn[2], drain[2];
+  uint64_t w_full[2][2], o_full[2][2];  // of a stream's tile halves
   uint32_t tmem;
   volatile int abort;
   int bad[kBadRing];  // unit count whose pages were bad
@@ -296,8 +301,14 @@ __device__ __forceinline__ void streams_sync() {
   asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 
-__device__ __forceinline__ void stream_sync(int st) {
-  asm volatile("bar.sync %0, 128;" ::"r"(2 + st) : "memory");
+
+// 32 bytes, at a multiple of 32: whole sectors even where each lane writes
+// a row of its own.
+__device__ __forceinline__ void st_v8(void *to, const uint32_t *x) {
+  asm volatile(
+      "st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to),
+      SDV_I8(x, 0)
+      : "memory");
 }
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -368,13 +379,6 @@ __device__ __forceinline__ float max32(const uint32_t *x) {
   return fmaxf(a, b);
 }
 
-// 16-byte piece `piece` of row `row` in a warp's 32 rows of 128 bytes,
-// swizzled: rows written by a lane each are read along without conflicts.
-__device__ __forceinline__ uint4 *stage_at(char *stage, int row, int piece) {
-  return reinterpret_cast<uint4 *>(stage + row * 128 +
-                                   ((piece ^ (row & 7)) << 4));
-}
-
 // Scores a row does not see become -inf.
 __device__ __forceinline__ void hide32(uint32_t *x, uint32_t seen) {
 #pragma unroll
@@ -401,41 +405,108 @@ __device__ __forceinline__ float row_max(uint32_t s_addr, bool cuts,
   return m;
 }
 
-// A row's weights 2^(s sl + off), rounded and packed, their sum before the
-// rounding, and the largest score.  One warp on a scheduler takes ~810
-// cycles for a tile, two ~1440: the issue slots, not the exponentials, are
-// what it runs on, so hidden scores have a copy of their own.
-template <class T, bool HIDE>
-__device__ __forceinline__ float weigh(uint32_t s_addr, float sl, float off,
-                                       const uint32_t *seen, uint32_t *w,
-                                       float &total) {
+// 32 weights 2^(s sl + off), rounded and packed; their sums before the
+// rounding are added to `sum`.
+template <class T>
+__device__ __forceinline__ void weigh32(const uint32_t *x, float sl,
+                                        float off, uint32_t *w,
+                                        float2 (&sum)[2]) {
   const float2 k2 = make_float2(sl, sl), o2 = make_float2(off, off);
-  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  float mt = -kInf;
-  uint32_t x[2][32];
-  tmem_ld32(s_addr, x[0]);
 #pragma unroll
-  for (int c = 0; c < kTile / 32; ++c) {
-    uint32_t *xc = x[c & 1];
-    tmem_wait_ld();
-    if (c + 1 < kTile / 32)
-      tmem_ld32(s_addr + 32 * (c + 1), x[(c + 1) & 1]);
-    if (HIDE) hide32(xc, seen[c]);
-    mt = fmaxf(mt, max32(xc));
-#pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-      float2 z = make_float2(__uint_as_float(xc[e]),
-                             __uint_as_float(xc[e + 1]));
-      z = fma2(z, k2, o2);
-      z.x = ex2(z.x);
-      z.y = ex2(z.y);
-      sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], z);
-      w[16 * c + (e >> 1)] = pack2<T>(z.x, z.y);
-    }
+  for (int e = 0; e < 32; e += 2) {
+    float2 z = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+    z = fma2(z, k2, o2);
+    z.x = ex2(z.x);
+    z.y = ex2(z.y);
+    sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], z);
+    w[e >> 1] = pack2<T>(z.x, z.y);
   }
-  const float2 t = add2(sum[0], sum[1]);
-  total = t.x + t.y;
-  return mt;
+}
+
+// A softmax thread's row: where its scores and sums lie, its reference m
+// and sum l.
+struct Row {
+  uint32_t s_addr, o_addr;
+  float sl, m, l;
+};
+
+// The weights of one row in one tile, half a tile at a time, so that the
+// values of one half are summed while the other is weighed.  They are taken
+// against the reference at hand while the scores' maximum is still being
+// found; where it turns out too far above (rare), the sums are scaled down
+// and the half is weighed once more.  Chunks of 32 scores are fetched one
+// ahead.  first: nothing is summed yet; parity: of the tile in the stream;
+// w_full, o_full: of the tile's halves.  Tiles that hide scores have a copy
+// of their own: a warp here runs on its scheduler's issue slots.
+template <class T, int D, bool HIDE>
+__device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
+                                           uint64_t *w_full, uint64_t *o_full,
+                                           bool first, uint32_t parity,
+                                           volatile int *abort,
+                                           int32_t *dev_status) {
+  uint32_t x[2][32];
+  tmem_ld32(row.s_addr, x[0]);
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    uint32_t w[kHalf / 2];
+    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    float mt = -kInf;
+    const float off = row.m == -kInf ? 0.f : -row.m * row.sl;
+#pragma unroll
+    for (int c = 2 * hf; c < 2 * hf + 2; ++c) {
+      uint32_t *xc = x[c & 1];
+      tmem_wait_ld();
+      if (c < 3) tmem_ld32(row.s_addr + 32 * (c + 1), x[(c + 1) & 1]);
+      if (HIDE) hide32(xc, seen[c]);
+      mt = fmaxf(mt, max32(xc));
+      weigh32<T>(xc, row.sl, off, w + 16 * (c & 1), sum);
+    }
+    const bool raise = mt > -kInf && !((mt - row.m) * row.sl <= kSlack);
+    if (__any_sync(~0u, raise)) {
+      float f = 1.f;
+      if (raise) {
+        f = row.m == -kInf ? 1.f : ex2((row.m - mt) * row.sl);
+        row.m = mt;
+      }
+      row.l *= f;
+      if (hf || !first) {
+        // a half's sums are complete when the last half's before it are
+        const bool fine =
+            attn_wait(&o_full[hf ^ 1], parity ^ (hf ^ 1), abort, dev_status);
+        if (!__all_sync(~0u, fine)) return false;
+        tmem_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(row.o_addr + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+          tmem_st32(row.o_addr + c, o);
+        }
+      }
+      const float to = row.m == -kInf ? 0.f : -row.m * row.sl;
+      sum[0] = sum[1] = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int c = 2 * hf; c < 2 * hf + 2; ++c) {
+        uint32_t y[32];
+        tmem_ld32(row.s_addr + 32 * c, y);
+        tmem_wait_ld();
+        if (HIDE) hide32(y, seen[c]);
+        weigh32<T>(y, row.sl, to, w + 16 * (c & 1), sum);
+      }
+      __syncwarp();
+    }
+    tmem_st32(row.s_addr + hf * (kHalf / 2), w);
+    const float2 t = add2(sum[0], sum[1]);
+    row.l += t.x + t.y;
+    tmem_wait_st();
+    tmem_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&w_full[hf]);
+  }
+  return true;
 }
 
 // ------------------------------------------------------------- the kernel
@@ -463,8 +534,10 @@ attention_kernel(const __grid_constant__ AttnParams p,
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.q_full[i], PAIR ? 4 : 8);
       mbar_init(&s.s_full[i], 1);
-      mbar_init(&s.w_full[i], 4);
-      mbar_init(&s.o_full[i], 1);
+      for (int hf = 0; hf < 2; ++hf) {
+        mbar_init(&s.w_full[i][hf], 4);
+        mbar_init(&s.o_full[i][hf], 1);
+      }
       mbar_init(&s.turn[i], 1);
     }
     mbar_init(&s.drain[0], 1);
@@ -610,22 +683,21 @@ attention_kernel(const __grid_constant__ AttnParams p,
       }
     };
     // O with that tile
-    auto wait_w = [&] {
-      wait(&s.w_full[st], wp);
-      wp ^= 1;
-    };
-    auto values = [&](bool first) {
+    // half hf of the tile's keys
+    auto values = [&](int hf, bool first) {
       if (fine && elect_one()) {
-        const uint32_t b = v_lo + v_at.slot * (L::kTileBytes / 16);
+        const uint32_t b = v_lo + v_at.slot * (L::kTileBytes / 16) +
+                           hf * (kHalf * 128 / 16);
+        tmem_fence_after();
 #pragma unroll
-        for (int i = 0; i < kTile / 16; ++i)
-          umma_ts<HI>(o_addr, s_addr + i * 8, b + i * 16 * 128 / 16, O_DESC,
-                      !first || i > 0);
-        umma_commit(&s.o_full[st]);
-        umma_commit(&s.empty[vr][v_at.slot]);
+        for (int i = 0; i < kHalf / 16; ++i)
+          umma_ts<HI>(o_addr, s_addr + hf * (kHalf / 2) + i * 8,
+                      b + i * 16 * 128 / 16, O_DESC, !first || i > 0);
+        umma_commit(&s.o_full[st][hf]);
+        if (hf) umma_commit(&s.empty[vr][v_at.slot]);
       }
       __syncwarp();
-      v_at.next();
+      if (hf) v_at.next();
     };
     // 256 rows: the streams take strict turns, a value and a score product
     // at a time, so that one's softmax runs under the other's products
@@ -641,8 +713,6 @@ attention_kernel(const __grid_constant__ AttnParams p,
     };
     for (; u.left && fine; u.next()) {
       const int cnt = u.j1 - u.j0;
-      wait(&s.q_full[PAIR ? st : 0], qp);
-      qp ^= 1;
       if (PAIR && st == 1 && u.rows <= kTile) {
         // no rows: let go of every tile as it comes
         for (int i = 0; i < cnt && fine; ++i) {
@@ -655,6 +725,8 @@ attention_kernel(const __grid_constant__ AttnParams p,
         }
         continue;
       }
+      wait(&s.q_full[PAIR ? st : 0], qp);
+      qp ^= 1;
       const int i0 = PAIR ? 0 : st, step = PAIR ? 1 : 2;
       const bool turns = PAIR && u.rows > kTile;
       if (i0 < cnt) {
@@ -668,10 +740,12 @@ attention_kernel(const __grid_constant__ AttnParams p,
         const bool more = i + step < cnt;
         wait_v(u.j0 + i);
         if (PAIR && more) wait_k();
-        wait_w();
+        wait(&s.w_full[st][0], wp);
         if (turns) take_turn();
-        tmem_fence_after();
-        values(i == i0);
+        values(0, i == i0);
+        wait(&s.w_full[st][1], wp);
+        wp ^= 1;
+        values(1, false);
         if (!PAIR && more) wait_k();
         if (more) scores();
         if (turns) pass_turn();
@@ -689,11 +763,46 @@ attention_kernel(const __grid_constant__ AttnParams p,
     // ---- softmax: stream st, a thread per row
     const int st = warp >> 2, r = tid & (kTile - 1);
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes << 16
-    const uint32_t s_addr = tmem + lanes + st * kTile;
     const float sl = p.scale_log2;
     unsigned tn = 0;  // tiles of this stream seen
     if (tid == 0) p.cut[blockIdx.x].parts = 0;
-    for (; u.left && fine; u.next()) {
+    const int base_row = PAIR ? st * kTile : 0;
+    // a stream without rows takes no part in a unit
+    auto active = [&](const Units<ROWS> &v) {
+      return !PAIR || v.rows > base_row;
+    };
+    // a unit's queries, in the tiles' swizzle
+    auto load_q = [&](const Units<ROWS> &v) {
+      if (!active(v)) return;
+      constexpr int CH = D / 8, NT = PAIR ? 128 : 256;
+      const int me = PAIR ? r : tid, ch = me % CH;
+      const T *src = (const T *)p.q + v.c.start * p.q_stride +
+                     (long long)v.h * p.G * D + ch * 8;
+      char *dst = q_tile + (PAIR ? st : 0) * L::kTileBytes +
+                  (ch >> 3) * (kTile * 128);
+      uint4 x[kTile * CH / NT];
+#pragma unroll
+      for (int i = 0; i < kTile * CH / NT; ++i) {
+        const int n = base_row + me / CH + i * (NT / CH);
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (n < v.rows) {
+          const int at = v.t * ROWS + n, tok = div_by(at, p.by_G);
+          x[i] = __ldg(reinterpret_cast<const uint4 *>(
+              src + tok * p.q_stride + (at - tok * p.G) * D));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kTile * CH / NT; ++i) {
+        const int n = me / CH + i * (NT / CH);
+        *reinterpret_cast<uint4 *>(dst + n * 128 +
+                                   (((ch & 7) ^ (n & 7)) << 4)) = x[i];
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.q_full[PAIR ? st : 0]);
+    };
+    if (u.left) load_q(u);
+    while (u.left && fine) {
       if (tid == 0 && u.j0 == 0 && u.j1 < u.nk) {
         // this CTA's last unit goes on in the CTAs up to the one whose
         // share holds the unit's last tile
@@ -707,46 +816,19 @@ attention_kernel(const __grid_constant__ AttnParams p,
         cut.first = u.t * ROWS;
         p.cut[blockIdx.x] = cut;
       }
+      Units<ROWS> next(u);
+      next.next();
       const int cnt_all = u.j1 - u.j0;
-      const int cnt = PAIR ? cnt_all : (cnt_all - st + 1) / 2;
-      const int base_row = PAIR ? st * kTile : 0;
-      const int first_row = u.t * ROWS;
-      // a stream without rows only keeps the unit count
-      const bool active = !PAIR || u.rows > base_row;
+      const int cnt =
+          !active(u) ? 0 : PAIR ? cnt_all : (cnt_all - st + 1) / 2;
+      const int row_at = u.t * ROWS + base_row + r;
       const bool mine = base_row + r < u.rows;
       const bool warp_rows = base_row + (warp & 3) * 32 < u.rows;
-      const int token =
-          mine ? div_by(first_row + base_row + r, p.by_G) : 0;
+      const int token = mine ? div_by(row_at, p.by_G) : 0;
       const int ctx = u.c.kv - u.c.n, limit = ctx + token;
-      if (active) {
-        // the unit's queries, in the tiles' swizzle
-        constexpr int CH = D / 8;
-        constexpr int NT = PAIR ? 128 : 256;
-        const int me = PAIR ? r : tid;
-        char *dst = q_tile + (PAIR ? st : 0) * L::kTileBytes;
-        const int ch = me % CH;
-        const T *src = (const T *)p.q + u.c.start * p.q_stride +
-                       (long long)u.h * p.G * D + ch * 8;
-        dst += (ch >> 3) * (kTile * 128);
-#pragma unroll
-        for (int i = 0; i < kTile * CH / NT; ++i) {
-          const int row = me / CH + i * (NT / CH);
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (base_row + row < u.rows) {
-            const int at = first_row + base_row + row;
-            const int tok = div_by(at, p.by_G);
-            x = __ldg(reinterpret_cast<const uint4 *>(
-                src + tok * p.q_stride + (at - tok * p.G) * D));
-          }
-          *reinterpret_cast<uint4 *>(dst + row * 128 +
-                                     (((ch & 7) ^ (row & 7)) << 4)) = x;
-        }
-        fence_proxy_async();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.q_full[PAIR ? st : 0]);
-      float m = -kInf, l = 0.f;
-      for (int i = 0; active && i < cnt; ++i, ++tn) {
+      Row row = {tmem + lanes + st * kTile,
+                 tmem + lanes + 2 * kTile + st * D, sl, -kInf, 0.f};
+      for (int i = 0; i < cnt; ++i, ++tn) {
         const int j = u.j0 + (PAIR ? i : 2 * i + st);
         fine = attn_wait(&s.s_full[st], tn & 1, &s.abort, p.dev_status);
         if (!__all_sync(~0u, fine)) { fine = false; break; }
@@ -764,69 +846,39 @@ attention_kernel(const __grid_constant__ AttnParams p,
                   mine ? seen_bits(p, u.c, token, limit, key + 32 * c) : 0;
           }
           __syncwarp();
-          float f = 1.f;  // what the row's earlier sums are scaled by
-          if (i == 0) m = row_max(s_addr, cuts, seen);
-          // weights against the reference at hand; where the tile's maximum
-          // turns out too far above it (rare), once more against a new one
-          uint32_t w[kTile / 2];
-          float sum;
-#pragma unroll 1
-          for (bool moved = false;; moved = true) {
-            const float off = m == -kInf ? 0.f : -m * sl;
-            const float mt = cuts ? weigh<T, true>(s_addr, sl, off, seen, w, sum)
-                                  : weigh<T, false>(s_addr, sl, off, seen, w,
-                                                    sum);
-            if (moved) break;
-            const bool raise = mt > -kInf && !((mt - m) * sl <= kSlack);
-            if (!__any_sync(~0u, raise)) break;
-            if (raise) {
-              f = m == -kInf ? 1.f : ex2((m - mt) * sl);
-              m = mt;
-            }
-            __syncwarp();
-          }
-          if (__any_sync(~0u, f != 1.f)) {
-            fine = attn_wait(&s.o_full[st], (tn - 1) & 1, &s.abort,
-                             p.dev_status);
-            if (!__all_sync(~0u, fine)) { fine = false; break; }
-            tmem_fence_after();
-            const uint32_t o_addr = tmem + lanes + 2 * kTile + st * D;
-#pragma unroll
-            for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(o_addr + c, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(o_addr + c, o);
-            }
-          }
-          __syncwarp();
-          tmem_st32(s_addr, w);
-          tmem_st32(s_addr + 32, w + 32);
-          l = fmaf(l, f, sum);
-          tmem_wait_st();
-          tmem_fence_before();
+          if (i == 0) row.m = row_max(row.s_addr, cuts, seen);
+          fine = cuts ? weigh_tile<T, D, true>(row, seen, s.w_full[st],
+                                               s.o_full[st], i == 0, tn & 1,
+                                               &s.abort, p.dev_status)
+                      : weigh_tile<T, D, false>(row, seen, s.w_full[st],
+                                                s.o_full[st], i == 0, tn & 1,
+                                                &s.abort, p.dev_status);
+          if (!fine) break;
+        } else if (lane == 0) {
+          mbar_arrive(&s.w_full[st][0]);
+          mbar_arrive(&s.w_full[st][1]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.w_full[st]);
       }
       if (!fine) break;
-      // ---- the end of the unit: O is complete
-      if (active && cnt > 0) {
-        fine = attn_wait(&s.o_full[st], (tn - 1) & 1, &s.abort, p.dev_status);
+      // ---- the end of the unit.  The last scores are out, so the next
+      // unit's queries may replace this one's: its first scores are under
+      // way while this one's rows are written
+      if (PAIR && next.left) load_q(next);
+      if (cnt > 0) {
+        fine = attn_wait(&s.o_full[st][1], (tn - 1) & 1, &s.abort,
+                         p.dev_status);
         if (!__all_sync(~0u, fine)) { fine = false; break; }
         tmem_fence_after();
       }
       // the two streams' sums of the same rows are joined; stream st then
       // writes column half st.  256 rows: each its own rows, all columns.
-      float f0 = 1.f, f1 = 0.f;
+      float f0 = 1.f, f1 = 0.f, m = row.m, l = row.l;
       if (!PAIR) {
         s.ml[st][r] = make_float2(m, l);
         tmem_fence_before();
         streams_sync();
         tmem_fence_after();
+        if (next.left) load_q(next);
         const float2 other = s.ml[st ^ 1][r];
         const float mj = fmaxf(m, other.x);
         const float fm = m == -kInf ? 0.f : ex2((m - mj) * sl);
@@ -843,9 +895,8 @@ attention_kernel(const __grid_constant__ AttnParams p,
           tmem + lanes + 2 * kTile + (PAIR ? st * D : 0) + c_lo;
       const bool second = !PAIR && cnt_all > 1;
       if (warp_rows) {
-        const int g = mine ? first_row + base_row + r - token * p.G : 0;
-        const long long row =
-            ((long long)(u.c.start + token) * p.Hq + u.h * p.G + g);
+        const long long to = (long long)(u.c.start + token) * p.Hq +
+                             u.h * p.G + (mine ? row_at - token * p.G : 0);
         const long long part =
             ((long long)blockIdx.x * 2 + (u.j0 == 0 ? 1 : 0)) * ROWS +
             base_row + r;
@@ -855,71 +906,47 @@ attention_kernel(const __grid_constant__ AttnParams p,
         if (mine && (PAIR || st == 0)) {
           if (!whole) p.part_ml[part] = make_float2(m * sl, l);
           else if (p.lse)
-            p.lse[row] = l == 0.f ? -kInf : (m * sl + log2f(l)) * kLn2;
+            p.lse[to] = l == 0.f ? -kInf : (m * sl + log2f(l)) * kLn2;
         }
-        // through this warp's part of the query tile (its queries are
-        // used up), so that the stores run along the rows
-        char *stage = PAIR ? q_tile + st * L::kTileBytes + (warp & 3) * 4096
-                           : q_tile + warp * 4096;
-        constexpr int COLS = 32;
+        T *out = (T *)p.out + to * D + c_lo;
+        float *part_o = p.part_o + part * D + c_lo;
 #pragma unroll
-        for (int c = 0; c < c_n; c += COLS) {
-          __syncwarp();  // tcgen05.ld wants the whole warp; the staging is free
-          uint32_t a[COLS];
+        for (int c = 0; c < c_n; c += 32) {
+          __syncwarp();  // tcgen05.ld wants the whole warp
+          uint32_t a[32];
           tmem_ld32(o_addr + c, a);
           tmem_wait_ld();
-          float o[COLS];
+          float o[32];
 #pragma unroll
-          for (int e = 0; e < COLS; ++e) o[e] = __uint_as_float(a[e]) * f0;
+          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(a[e]) * f0;
           if (second) {
             tmem_ld32(o_addr + D + c, a);
             tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < COLS; ++e)
+            for (int e = 0; e < 32; ++e)
               o[e] = fmaf(__uint_as_float(a[e]), f1, o[e]);
           }
-          if (whole) {
+          if (!mine) {
+            // no such row
+          } else if (whole) {
+            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < COLS; e += 8)
-              *stage_at(stage, lane, e / 8) = make_uint4(
-                  pack2<T>(o[e], o[e + 1]), pack2<T>(o[e + 2], o[e + 3]),
-                  pack2<T>(o[e + 4], o[e + 5]), pack2<T>(o[e + 6], o[e + 7]));
+            for (int e = 0; e < 16; ++e)
+              w[e] = pack2<T>(o[2 * e], o[2 * e + 1]);
+            st_v8(out + c, w);
+            st_v8(out + c + 16, w + 8);
           } else {
 #pragma unroll
-            for (int e = 0; e < COLS; e += 4)
-              *stage_at(stage, lane, e / 4) = make_uint4(
-                  __float_as_uint(o[e]), __float_as_uint(o[e + 1]),
-                  __float_as_uint(o[e + 2]), __float_as_uint(o[e + 3]));
-          }
-          __syncwarp();
-          const int per = whole ? 4 : 8;  // 16-byte pieces of a row
-          const int first = base_row + (warp & 3) * 32;
+            for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(o[e]);
 #pragma unroll
-          for (int i = lane; i < 32 * per; i += 32) {
-            const int rr = i / per, pc = i % per;
-            const uint4 x = *stage_at(stage, rr, pc);
-            if (first + rr >= u.rows) {
-              // no such row
-            } else if (whole) {
-              const int at = first_row + first + rr;
-              const int tok = div_by(at, p.by_G);
-              const long long to = (long long)(u.c.start + tok) * p.Hq +
-                                   u.h * p.G + (at - tok * p.G);
-              reinterpret_cast<uint4 *>((T *)p.out + to * D + c_lo + c)[pc] =
-                  x;
-            } else {
-              reinterpret_cast<uint4 *>(
-                  p.part_o + (part - r + (warp & 3) * 32 + rr) * D + c_lo +
-                  c)[pc] = x;
-            }
+            for (int e = 0; e < 32; e += 8) st_v8(part_o + c + e, a + e);
           }
         }
       }
       __syncwarp();
       tmem_fence_before();
-      // O, m, l and the queries may be overwritten
-      if (PAIR) stream_sync(st);
-      else streams_sync();
+      if (!PAIR) streams_sync();  // O, m and l may be overwritten
+      u.to(next);
     }
   }
 
@@ -1158,8 +1185,10 @@ extern "C" sd_status sd_paged_attention(
               "block_table is null");
   SDV_REQUIRE(q_stride >= (long long)q_heads * D,
               "tokens overlap: q_stride is below q_heads x head_dim");
-  SDV_REQUIRE(aligned16(q) && q_stride % 8 == 0 && aligned16(out),
-              "q and out must be 16-byte aligned, q_stride a multiple of 8");
+  SDV_REQUIRE(aligned16(q) && q_stride % 8 == 0,
+              "q must be 16-byte aligned, q_stride a multiple of 8");
+  SDV_REQUIRE((reinterpret_cast<uintptr_t>(out) & 31) == 0,
+              "out must be 32-byte aligned");
   SDV_REQUIRE(aligned16(cache->k) && aligned16(cache->v) &&
                   cache->page_stride % 8 == 0 &&
                   cache->token_stride % 8 == 0 && cache->head_stride % 8 == 0,
@@ -1168,8 +1197,9 @@ extern "C" sd_status sd_paged_attention(
               "total x q_heads does not fit 31 bits");
   const size_t need = sd_paged_attention_workspace(q_heads, cache->heads, D,
                                                    max_q);
-  SDV_REQUIRE(workspace && ws_bytes >= need && aligned16(workspace),
-              "a 16-byte aligned workspace of >= %zu bytes required", need);
+  SDV_REQUIRE(workspace && ws_bytes >= need &&
+                  (reinterpret_cast<uintptr_t>(workspace) & 31) == 0,
+              "a 32-byte aligned workspace of >= %zu bytes required", need);
   int sms = 0;
   st = check_device(&sms);
   if (st != SD_OK) return st;
