@@ -39,9 +39,11 @@ constexpr int kAttnThreads = 384;  // two warpgroups of softmax, one of roles
 constexpr int kMmaWarp = 9;  // and 10; warps 8 and 11 load
 constexpr int kBadRing = 64;     // units whose bad-page mark is kept
 constexpr float kLn2 = 0.693147180559945f;
-// A row's reference moves only when its maximum is 2^8 above it: weights
-// stay below 2^8, far inside 16-bit range, and most tiles rescale nothing.
-constexpr float kSlack = 8.f;
+// A row's reference moves only when its maximum is 2^15 above it: weights
+// stay inside fp16's range (bf16's is wider), their relative rounding is the
+// same at any scale, and hardly a tile rescales anything.  (At 2^8 the rows
+// of a prompt tile did so in one tile of ten, for half a tile's time each.)
+constexpr float kSlack = 15.f;
 
 struct AttnParams {
   const void *q;
@@ -105,18 +107,29 @@ __device__ unsigned long long head_tiles(const AttnParams &p,
   return s;
 }
 
-// The plan of one CTA: its share [x0, x1) of all tiles, and where x0 lies.
+// Starting and ending a unit costs a CTA about as much as this many key
+// tiles: it counts into the shares, so that many short units and few long
+// ones take the same time (two prompt chunks, one over 8192 cached keys and
+// one over 2385: 589 us by tiles alone, 549 with 8, 554 with 12).  Not where
+// the shares are themselves short: there every tile that another SM takes is
+// time saved.
+template <int ROWS> constexpr int unit_cost() { return ROWS == 256 ? 8 : 1; }
+
+// The plan of one CTA.  All units are laid end to end, each `extra` places
+// for itself and then one for each key tile; the CTA's share is [x0, x1).
 struct Plan {
   unsigned long long total, x0, x1;
-  unsigned long long warp_sum[8];
-  int n, b, h, t, j;  // shares; the unit and key tile where x0 lies
+  unsigned long long warp_sum[8], warp_units[8];
+  int n, b, h, t, at;  // shares; the unit where x0 lies, and the place in it
+  int extra;
   int any_unusable;
 };
 
 template <int ROWS>
 __device__ void make_plan(const AttnParams &p, Plan &s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  unsigned long long first = 0, sum = 0;
+  // key tiles and units of this thread's sequences; of its first one
+  unsigned long long tiles = 0, units = 0, first_tiles = 0, first_units = 0;
   bool unusable = false;
   if (tid < 256)
     for (int b = tid; b < p.B; b += 256) {
@@ -127,19 +140,31 @@ __device__ void make_plan(const AttnParams &p, Plan &s) {
         if (blockIdx.x == 0) status_or(p.dev_status, SD_DEV_BAD_LENGTH);
       }
       const unsigned long long w = head_tiles<ROWS>(p, c) * p.Hkv;
-      if (b == tid) first = w;
-      sum += w;
+      const unsigned long long k =
+          (unsigned long long)row_tiles<ROWS>(p, c) * p.Hkv;
+      if (b == tid) first_tiles = w, first_units = k;
+      tiles += w;
+      units += k;
     }
-  // inclusive scan of `first` and total of `sum`
-  unsigned long long tot = sum;
 #pragma unroll
-  for (int d = 16; d; d >>= 1) tot += __shfl_xor_sync(~0u, tot, d);
-  if (lane == 0 && warp < 8) s.warp_sum[warp] = tot;
+  for (int d = 16; d; d >>= 1) {
+    tiles += __shfl_xor_sync(~0u, tiles, d);
+    units += __shfl_xor_sync(~0u, units, d);
+  }
+  if (lane == 0 && warp < 8) {
+    s.warp_sum[warp] = tiles;
+    s.warp_units[warp] = units;
+  }
   if (tid == 0) s.b = -1;
   const int any = __syncthreads_or(unusable);
   if (tid == 0) {
-    unsigned long long w = 0;
-    for (int i = 0; i < 8; ++i) w += s.warp_sum[i];
+    unsigned long long w = 0, k = 0;
+    for (int i = 0; i < 8; ++i) {
+      w += s.warp_sum[i];
+      k += s.warp_units[i];
+    }
+    s.extra = w >= 16ull * gridDim.x ? unit_cost<ROWS>() : 0;
+    w += k * s.extra;
     s.total = w;
     s.any_unusable = any;
     s.n = w < gridDim.x ? (int)w : (int)gridDim.x;
@@ -151,12 +176,17 @@ __device__ void make_plan(const AttnParams &p, Plan &s) {
   }
   __syncthreads();
   if (s.x0 == s.x1) return;
+  const unsigned long long extra = s.extra;
   unsigned long long carry = 0;
   for (int base = 0; base < p.B; base += 256) {
-    unsigned long long w = 0;
-    if (tid < 256 && base + tid < p.B)
-      w = base == 0 ? first
-                    : head_tiles<ROWS>(p, attn_chunk(p, base + tid)) * p.Hkv;
+    unsigned long long w = first_tiles + extra * first_units;
+    if (base > 0) {
+      w = 0;
+      if (tid < 256 && base + tid < p.B) {
+        const Chunk c = attn_chunk(p, base + tid);
+        w = (head_tiles<ROWS>(p, c) + extra * row_tiles<ROWS>(p, c)) * p.Hkv;
+      }
+    }
     unsigned long long inc = w;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -173,19 +203,20 @@ __device__ void make_plan(const AttnParams &p, Plan &s) {
     const unsigned long long lo = before + inc - w;
     if (tid < 256 && s.x0 >= lo && s.x0 < lo + w) {
       const Chunk c = attn_chunk(p, base + tid);
-      const unsigned long long per = head_tiles<ROWS>(p, c);
+      const unsigned long long per =
+          head_tiles<ROWS>(p, c) + extra * row_tiles<ROWS>(p, c);
       unsigned long long r = s.x0 - lo;
       s.h = (int)(r / per);
       r %= per;
       int t = 0;
       for (;; ++t) {
-        const int k = key_tiles<ROWS>(p, c, t);
+        const int k = key_tiles<ROWS>(p, c, t) + (int)extra;
         if (r < (unsigned long long)k) break;
         r -= k;
       }
       s.b = base + tid;
       s.t = t;
-      s.j = (int)r;
+      s.at = (int)r;
     }
     carry += all;
     __syncthreads();
@@ -193,49 +224,58 @@ __device__ void make_plan(const AttnParams &p, Plan &s) {
   }
 }
 
-// Walks the units of a CTA's share; every warp walks the same ones.
+// Walks the units of a CTA's share that it has key tiles of; every warp
+// walks the same ones.
 template <int ROWS> struct Units {
   const AttnParams &p;
-  unsigned long long left;
+  unsigned long long left;  // places of the share from `at` on
   Chunk c;
-  int b, h, t, T;
+  int b, h, t, T, at, extra;
   int j0, j1, nk;   // key tiles [j0, j1) of the unit's nk
   int rows;         // valid rows of the tile
   int count;        // units begun
 
   __device__ Units(const AttnParams &p_, const Plan &s)
-      : p(p_), left(s.x1 - s.x0), b(s.b), h(s.h), t(s.t), T(0), j0(s.j),
-        count(0) {
+      : p(p_), left(s.x1 - s.x0), b(s.b), h(s.h), t(s.t), T(0), at(s.at),
+        extra(s.extra), count(0) {
     if (!left) return;
     c = attn_chunk(p, b);
     T = row_tiles<ROWS>(p, c);
     set();
+    if (j0 == j1) next();
   }
   __device__ void to(const Units &o) {  // o walks the same share
-    left = o.left, c = o.c, b = o.b, h = o.h, t = o.t, T = o.T;
+    left = o.left, c = o.c, b = o.b, h = o.h, t = o.t, T = o.T, at = o.at;
     j0 = o.j0, j1 = o.j1, nk = o.nk, rows = o.rows, count = o.count;
+  }
+  __device__ int places() const {  // of the unit that are in the share
+    const int n = nk + extra - at;
+    return (unsigned long long)n < left ? n : (int)left;
   }
   __device__ void set() {
     ++count;
     nk = key_tiles<ROWS>(p, c, t);
-    j1 = (unsigned long long)(nk - j0) < left ? nk : j0 + (int)left;
+    j0 = max(0, at - extra);
+    j1 = max(0, at + places() - extra);
     rows = min(c.n * p.G - t * ROWS, ROWS);
   }
   __device__ void next() {
-    left -= j1 - j0;
-    if (!left) return;
-    j0 = 0;
-    if (++t == T) {
-      t = 0;
-      if (++h == p.Hkv) {
-        h = 0;
-        do {  // left > 0: a later sequence has tiles
-          c = attn_chunk(p, ++b);
-          T = row_tiles<ROWS>(p, c);
-        } while (T == 0);
+    do {  // past units of which the share has no tile
+      left -= places();
+      if (!left) return;
+      at = 0;
+      if (++t == T) {
+        t = 0;
+        if (++h == p.Hkv) {
+          h = 0;
+          do {  // left > 0: a later sequence has units
+            c = attn_chunk(p, ++b);
+            T = row_tiles<ROWS>(p, c);
+          } while (T == 0);
+        }
       }
-    }
-    set();
+      set();
+    } while (j0 == j1);
   }
 };
 
@@ -806,7 +846,8 @@ attention_kernel(const __grid_constant__ AttnParams p,
       if (tid == 0 && u.j0 == 0 && u.j1 < u.nk) {
         // this CTA's last unit goes on in the CTAs up to the one whose
         // share holds the unit's last tile
-        const unsigned long long end = s.plan.x1 + (u.nk - u.j1);
+        const unsigned long long end =
+            s.plan.x1 + (unsigned)(u.nk - u.j1);
         CutUnit cut;
         cut.parts = (int)((end * s.plan.n - 1) / s.plan.total) -
                     (int)blockIdx.x + 1;
@@ -818,6 +859,17 @@ attention_kernel(const __grid_constant__ AttnParams p,
       }
       Units<ROWS> next(u);
       next.next();
+      if (next.left && active(next)) {  // its queries on their way to L2
+        const int n = base_row + r, at = next.t * ROWS + n;
+        if (n < next.rows && (PAIR || st == 0)) {
+          const int tok = div_by(at, p.by_G);
+          const T *q = (const T *)p.q + (next.c.start + tok) * p.q_stride +
+                       (next.h * p.G + at - tok * p.G) * D;
+#pragma unroll
+          for (int e = 0; e < D; e += 64)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(q + e));
+        }
+      }
       const int cnt_all = u.j1 - u.j0;
       const int cnt =
           !active(u) ? 0 : PAIR ? cnt_all : (cnt_all - st + 1) / 2;
