@@ -674,8 +674,8 @@ sd_status sd_paged_attention(const void *q, long long q_stride, int q_heads,
  * exactly 0 (its student row is not read by the backward call).
  * grad may be the student's own buffer (same pointer and stride).
  * sd_distill_topk_step is the forward and the backward call together; it
- * reads the student's rows once where they are 16-byte aligned and fit
- * on chip.
+ * reads the student's rows once where one fits the shared memory of 16 SMs
+ * (573,000 bf16 columns), and twice above.
  * ------------------------------------------------------------------- */
 sd_status sd_distill_topk(const void *student, long long row_stride,
                           sd_dtype dt, const float *teacher_logit,

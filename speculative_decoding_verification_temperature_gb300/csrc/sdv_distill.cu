@@ -5,20 +5,33 @@
 // softmax(z / T) of the student's row,
 //   loss = sum_k p_k (log p_k - log q_k)
 //   d loss / d z_j = (P q_j - sum_{k: id_k = j} p_k) / T.
+//
+// All three calls stream vocabulary rows and are bound by HBM: the forward
+// call reads a row once, the backward call reads and writes it once, and so
+// does the step, which keeps a row in the shared memory of a cluster between
+// the pass that finds log sum exp and the pass that writes the gradient.
+//
+// A row is cut into 16-byte slots by address, whatever its own alignment:
+// only its first and last slot can be partial, and those alone are read and
+// written by the element.
 #include "sdv_device.cuh"
 #include "sdv_host.cuh"
+#include "sdv_tma.cuh"
 
 namespace sdv {
 namespace {
 
 constexpr float kLn2 = 0.693147180559945f;
+constexpr int kSlotsPerCopy = 1024;  // 16 KB a bulk copy
+constexpr int kMaxCopies = 5;        // a step's slice of a row
+constexpr int kBatch = 8;            // slots a thread has in flight
 
 struct DistillParams {
   const void *student;
   long long row_stride;
   const float *logit, *teacher_lse, *grad_loss;
   const int32_t *id;
-  int N, V, K;
+  int N, V, K, CL;
   float k2;     // log2(e) / T
   float inv_T;
   float *loss, *lse;
@@ -28,25 +41,135 @@ struct DistillParams {
   int32_t *dev_status;
 };
 
+// A row as 16-byte slots from the aligned address at or before its start:
+// column j is element head + j.
+template <int DT> struct SlotRow {
+  static constexpr int VW = vec_width<DT>();
+  const char *base;
+  int head, V, slots;
+  __device__ SlotRow(const void *rows, long long stride, int row, int V_)
+      : V(V_) {
+    const char *start =
+        (const char *)rows + (long long)row * stride * elt_bytes<DT>();
+    head = (int)(reinterpret_cast<uintptr_t>(start) & 15) / elt_bytes<DT>();
+    base = start - head * elt_bytes<DT>();
+    slots = (head + V + VW - 1) / VW;
+  }
+  __device__ bool full(int s) const {
+    return (s > 0 || head == 0) && (s + 1) * VW <= head + V;
+  }
+  __device__ int first_col(int s) const { return s * VW - head; }
+};
+
+__device__ __forceinline__ uint4 ld_v4(const void *p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+
+// A partial slot by the element; columns outside the row are -inf.
+template <int DT>
+__device__ Raw<DT, vec_width<DT>()> load_partial(const SlotRow<DT> &r, int s) {
+  uint32_t w[4] = {};
+  const int c0 = r.first_col(s);
+  for (int e = 0; e < r.VW; ++e) {
+    const bool in = c0 + e >= 0 && c0 + e < r.V;
+    const char *at = r.base + (s * r.VW + e) * (long long)elt_bytes<DT>();
+    if (DT == 0) {
+      w[e] = in ? *reinterpret_cast<const uint32_t *>(at) : 0xff800000u;
+    } else {
+      const uint32_t h =
+          in ? *reinterpret_cast<const unsigned short *>(at) : 0xff80u;
+      w[e >> 1] |= h << (16 * (e & 1));
+    }
+  }
+  Raw<DT, vec_width<DT>()> x;
+  x.w = make_uint4(w[0], w[1], w[2], w[3]);
+  return x;
+}
+
+template <int DT>
+__device__ __forceinline__ Raw<DT, vec_width<DT>()> load_slot(
+    const SlotRow<DT> &r, int s) {
+  if (r.full(s)) {
+    Raw<DT, vec_width<DT>()> x;
+    x.w = ld_v4(r.base + (long long)s * 16);
+    return x;
+  }
+  return load_partial(r, s);
+}
+
+// One logit (a plain load: the row may be written in this kernel, later).
+template <int DT>
+__device__ __forceinline__ float load_col(const SlotRow<DT> &r, int j) {
+  const char *at = r.base + (long long)(r.head + j) * elt_bytes<DT>();
+  if constexpr (DT == 0) return *reinterpret_cast<const float *>(at);
+  const uint32_t h = *reinterpret_cast<const unsigned short *>(at);
+  return __uint_as_float(h << 16);
+}
+
+template <int DT>
+__device__ __forceinline__ void store_elt(void *row, int j, float x) {
+  if constexpr (DT == 0) {
+    ((float *)row)[j] = x;
+  } else {
+    uint32_t u;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(u) : "f"(x));
+    ((unsigned short *)row)[j] = (unsigned short)u;
+  }
+}
+
+// Gradients of a slot: c 2^(z k2 + nl2) of its columns (c alone scales).
+template <int DT>
+__device__ __forceinline__ void store_slot(
+    const SlotRow<DT> &r, char *grad, bool aligned, int s,
+    const Raw<DT, vec_width<DT>()> &x, float c, float k2, float nl2) {
+  float g[SlotRow<DT>::VW];
+#pragma unroll
+  for (int e = 0; e < r.VW; ++e)
+    g[e] = c * ex2(fmaf(elt<DT, SlotRow<DT>::VW>(x, e), k2, nl2));
+  const int c0 = r.first_col(s);
+  if (aligned && r.full(s)) {
+    uint4 w;
+    if constexpr (DT == 0) {
+      w = make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]),
+                     __float_as_uint(g[2]), __float_as_uint(g[3]));
+    } else {
+      uint32_t u[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+            : "=r"(u[e])
+            : "f"(g[2 * e + 1]), "f"(g[2 * e]));
+      w = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+    *reinterpret_cast<uint4 *>(grad + (long long)c0 * elt_bytes<DT>()) = w;
+  } else {
+    for (int e = 0; e < r.VW; ++e)
+      if (c0 + e >= 0 && c0 + e < r.V) store_elt<DT>(grad, c0 + e, g[e]);
+  }
+}
+
 // The teacher's entries of one row, in shared memory: id (-1: padding or
-// p = 0 by a logit of -inf), p and log2 p.
+// p = 0 by a logit of -inf), p, log2 p, and P (NaN: unusable entries).
 struct Teacher {
   int id[SD_MAX_DISTILL_K];
   float p[SD_MAX_DISTILL_K];
   float log2p[SD_MAX_DISTILL_K];
+  float P;
 };
 
-// Reads a row's entries and normalises them (all threads of the CTA call
-// it); returns P, NaN when the entries are unusable.
-__device__ float load_teacher(const DistillParams &p, int row, Teacher &t,
-                              float *scratch) {
-  const int tid = threadIdx.x;
+// Read and normalise a row's entries (one warp).
+__device__ void load_teacher(const DistillParams &p, int row, Teacher &t) {
+  const int lane = threadIdx.x & 31;
   int st = 0;
   float m = -kInf;
   bool bad = false;
-  for (int k = tid; k < p.K; k += kThreads) {
-    int id = p.id[(long long)row * p.K + k];
-    const float z = p.logit[(long long)row * p.K + k];
+  for (int k = lane; k < p.K; k += 32) {
+    int id = __ldg(p.id + (long long)row * p.K + k);
+    const float z = __ldg(p.logit + (long long)row * p.K + k);
     if (id >= p.V) {
       st |= SD_DEV_BAD_TOKEN;
       id = -1;
@@ -60,141 +183,47 @@ __device__ float load_teacher(const DistillParams &p, int row, Teacher &t,
     if (id >= 0) m = fmaxf(m, z);
   }
   status_or(p.dev_status, st);
-  const bool any_bad = __syncthreads_or(bad);
-  scratch[tid] = m;
-  __syncthreads();
-  for (int i = kThreads / 2; i; i >>= 1) {
-    if (tid < i) scratch[tid] = fmaxf(scratch[tid], scratch[tid + i]);
-    __syncthreads();
-  }
-  m = scratch[0];
-  __syncthreads();
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
   // sum of 2^((z - m) k2) over the entries
   float s = 0.f;
-  for (int k = tid; k < p.K; k += kThreads)
+  for (int k = lane; k < p.K; k += 32)
     if (t.id[k] >= 0) s += ex2((t.log2p[k] - m) * p.k2);
-  scratch[tid] = s;
-  __syncthreads();
-  for (int i = kThreads / 2; i; i >>= 1) {
-    if (tid < i) scratch[tid] += scratch[tid + i];
-    __syncthreads();
-  }
-  s = scratch[0];
-  __syncthreads();
+#pragma unroll
+  for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
   float tl = 0.f;
-  bool tl_bad = false;
   if (p.teacher_lse) {
-    tl = p.teacher_lse[row];
-    tl_bad = !(fabsf(tl) < kInf);
+    tl = __ldg(p.teacher_lse + row);
+    if (!(fabsf(tl) < kInf)) bad = true;
   }
   const float ls = log2f(s);
-  for (int k = tid; k < p.K; k += kThreads) {
+  float P = 0.f;
+  for (int k = lane; k < p.K; k += 32) {
     const float z = t.log2p[k];
-    float l2 = p.teacher_lse ? (z * p.inv_T - tl) * (1.f / kLn2)
-                             : (z - m) * p.k2 - ls;
+    const float l2 = p.teacher_lse ? (z * p.inv_T - tl) * (1.f / kLn2)
+                                   : (z - m) * p.k2 - ls;
+    const float pk = t.id[k] >= 0 ? ex2(l2) : 0.f;
     t.log2p[k] = l2;
-    t.p[k] = t.id[k] >= 0 ? ex2(l2) : 0.f;
+    t.p[k] = pk;
+    P += pk;
   }
-  __syncthreads();
-  float P = 1.f;
-  if (m == -kInf) P = 0.f;  // no usable entry
-  else if (p.teacher_lse) {
-    P = 0.f;
-    for (int k = 0; k < p.K; ++k) P += t.p[k];
-  }
-  return any_bad || tl_bad ? __int_as_float(0x7fc00000) : P;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) P += __shfl_xor_sync(~0u, P, d);
+  if (!p.teacher_lse) P = m == -kInf ? 0.f : 1.f;
+  if (__any_sync(~0u, bad)) P = __int_as_float(0x7fc00000);
+  if (lane == 0) t.P = P;
 }
 
-// One CTA per row.
+// The columns of the entries with ids in [lo, hi), over what the pass over
+// the row wrote: the first entry of an id writes for all that repeat it.
+// at: the student's logits at the ids.
 template <int DT>
-__global__ void __launch_bounds__(kThreads)
-distill_forward_kernel(const __grid_constant__ DistillParams p) {
-  __shared__ Teacher t;
-  __shared__ float scratch[kThreads];
-  const int row = blockIdx.x, tid = threadIdx.x;
-  const char *z = (const char *)p.student +
-                  (long long)row * p.row_stride * elt_bytes<DT>();
-  const float P = load_teacher(p, row, t, scratch);
-  MS st = ms_empty();
-  float vmax;
-  for (int j = tid; j < p.V; j += kThreads)
-    ms_add_v<DT, 1>(st, load_vec<DT, 1>(z, j), p.k2, vmax);
-  __shared__ MS part[kThreads];
-  part[tid] = st;
-  __syncthreads();
-  for (int i = kThreads / 2; i; i >>= 1) {
-    if (tid < i) part[tid] = ms_merge(part[tid], part[tid + i], p.k2);
-    __syncthreads();
-  }
-  st = part[0];
-  const bool ok = ms_valid(st) && P == P;
-  const float lse2 = st.m * p.k2 + log2f(st.s);
-  float a = 0.f;
-  if (ok)
-    for (int k = tid; k < p.K; k += kThreads)
-      if (t.id[k] >= 0 && t.p[k] > 0.f)
-        a += t.p[k] *
-             (t.log2p[k] - ((load_logit<DT>(z, t.id[k]) - st.m) * p.k2 -
-                            log2f(st.s)));
-  __syncthreads();
-  scratch[tid] = a;
-  __syncthreads();
-  for (int i = kThreads / 2; i; i >>= 1) {
-    if (tid < i) scratch[tid] += scratch[tid + i];
-    __syncthreads();
-  }
-  if (tid == 0) {
-    const float nan = __int_as_float(0x7fc00000);
-    p.loss[row] = ok ? scratch[0] * kLn2 : nan;
-    p.lse[row] = ok ? lse2 * kLn2 : nan;
-    if (!ok) status_or(p.dev_status, SD_DEV_NONFINITE);
-  }
-}
-
-template <int DT>
-__device__ __forceinline__ void store_elt(void *row, int j, float x) {
-  if constexpr (DT == 0) ((float *)row)[j] = x;
-  else {
-    uint32_t u;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(u) : "f"(x));
-    ((unsigned short *)row)[j] = (unsigned short)u;
-  }
-}
-
-template <int DT>
-__global__ void __launch_bounds__(kThreads)
-distill_backward_kernel(const __grid_constant__ DistillParams p) {
-  __shared__ Teacher t;
-  __shared__ float scratch[kThreads];
-  __shared__ float at[SD_MAX_DISTILL_K];
-  const int row = blockIdx.x, tid = threadIdx.x;
-  const char *z = (const char *)p.student +
-                  (long long)row * p.row_stride * elt_bytes<DT>();
-  char *g = (char *)p.grad + (long long)row * p.grad_stride * elt_bytes<DT>();
-  const float w = p.grad_loss[row];
-  if (w == 0.f) {
-    for (int j = tid; j < p.V; j += kThreads) store_elt<DT>(g, j, 0.f);
-    return;
-  }
-  const float P = load_teacher(p, row, t, scratch);
-  const float lse = p.lse_in[row];
-  const bool ok = P == P && fabsf(lse) < kInf;
-  const float c = ok ? w * p.inv_T : __int_as_float(0x7fc00000);
-  const float nl2 = -lse * (1.f / kLn2);
-  if (!ok && tid == 0) status_or(p.dev_status, SD_DEV_NONFINITE);
-  for (int k = tid; k < p.K; k += kThreads)
-    at[k] = t.id[k] >= 0 ? load_logit<DT>(z, t.id[k]) : 0.f;
-  __syncthreads();
-  for (int j = tid; j < p.V; j += kThreads) {
-    const float x = elt<DT, 1>(load_vec<DT, 1>(z, j), 0);
-    store_elt<DT>(g, j, c * P * ex2(fmaf(x, p.k2, nl2)));
-  }
-  __syncthreads();
-  // the entries' columns again, with the teacher's probabilities: the first
-  // entry of an id writes for all that repeat it
-  for (int k = tid; k < p.K; k += kThreads) {
+__device__ void store_entries(const DistillParams &p, const Teacher &t,
+                              char *grad, int lo, int hi, const float *at,
+                              float c, float P, float nl2) {
+  for (int k = threadIdx.x; k < p.K; k += kThreads) {
     const int id = t.id[k];
-    if (id < 0) continue;
+    if (id < lo || id >= hi) continue;
     float sum = 0.f;
     bool first = true;
     for (int i = 0; i < p.K; ++i)
@@ -203,8 +232,191 @@ distill_backward_kernel(const __grid_constant__ DistillParams p) {
         sum += t.p[i];
       }
     if (first)
-      store_elt<DT>(g, id, c * (P * ex2(fmaf(at[k], p.k2, nl2)) - sum));
+      store_elt<DT>(grad, id, c * (P * ex2(fmaf(at[k], p.k2, nl2)) - sum));
   }
+}
+
+// The forward call and the step: a cluster of CL CTAs per row, a contiguous
+// run of its slots each.  STEP: the run is kept in shared memory (bulk
+// copies, a barrier each) and read from there again for the gradient.
+template <int DT, bool STEP>
+__global__ void __launch_bounds__(kThreads)
+distill_row_kernel(const __grid_constant__ DistillParams p) {
+  constexpr int VW = vec_width<DT>();
+  extern __shared__ __align__(16) char kept[];
+  __shared__ Teacher t;
+  __shared__ float at[SD_MAX_DISTILL_K];
+  __shared__ MS part[kWarps], mine;
+  __shared__ uint64_t bar[kMaxCopies];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster.block_rank();
+  const int row = blockIdx.x / p.CL;
+  const SlotRow<DT> r(p.student, p.row_stride, row, p.V);
+  const int s0 = (int)((long long)r.slots * rank / p.CL);
+  const int s1 = (int)((long long)r.slots * (rank + 1) / p.CL);
+  const int n = s1 - s0;
+  const float k2 = p.k2;
+  uint4 *slot = reinterpret_cast<uint4 *>(kept);
+  if constexpr (STEP) {
+    // only a row's first and last slot can be partial
+    const int f0 = s0 + (n > 0 && !r.full(s0));
+    const int f1 = s1 - (n > 0 && s1 - 1 >= f0 && !r.full(s1 - 1));
+    if (tid == 0) {
+      for (int i = 0; i < kMaxCopies; ++i) mbar_init(&bar[i], 1);
+      fence_mbar_init();
+      for (int i = 0; i * kSlotsPerCopy < n; ++i) {
+        const int a = max(s0 + i * kSlotsPerCopy, f0);
+        const int b = min(s0 + (i + 1) * kSlotsPerCopy, f1);
+        const uint32_t bytes = b > a ? (uint32_t)(b - a) * 16 : 0;
+        mbar_expect_tx(&bar[i], bytes);
+        if (bytes)
+          bulk_g2s_hint(slot + (a - s0), r.base + (long long)a * 16, bytes,
+                        &bar[i], l2_evict_first_policy());
+      }
+    }
+    if (tid == 32 && f0 > s0) slot[0] = load_partial(r, s0).w;
+    if (tid == 64 && f1 < s1) slot[n - 1] = load_partial(r, s1 - 1).w;
+  }
+  if (warp == kWarps - 1) load_teacher(p, row, t);
+  __syncthreads();
+  // the student's logits at the ids, before anything is written (the
+  // gradient may go to the student's own rows)
+  if (rank == 0 || STEP) {
+    for (int k = tid; k < p.K; k += kThreads)
+      at[k] = t.id[k] >= 0 ? load_col(r, t.id[k]) : 0.f;
+  }
+  MS st = ms_empty();
+  float vmax;
+  bool fine = true;
+  if constexpr (STEP) {
+    for (int i = 0; i * kSlotsPerCopy < n; ++i) {
+      fine = mbar_wait(&bar[i], 0, p.dev_status) && fine;
+      const int b = min((i + 1) * kSlotsPerCopy, n);
+#pragma unroll 4
+      for (int s = i * kSlotsPerCopy + tid; s < b; s += kThreads) {
+        Raw<DT, VW> x;
+        x.w = slot[s];
+        ms_add_v<DT, VW>(st, x, k2, vmax);
+      }
+    }
+  } else {
+    for (int s = s0 + tid; s < s1; s += kThreads * kBatch) {
+      Raw<DT, VW> x[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (s + i * kThreads < s1) x[i] = load_slot(r, s + i * kThreads);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (s + i * kThreads < s1) ms_add_v<DT, VW>(st, x[i], k2, vmax);
+    }
+  }
+  st = warp_down_ms(st, k2);
+  if (lane == 0) part[warp] = st;
+  __syncthreads();
+  if (tid == 0) {
+    st = part[0];
+    for (int i = 1; i < kWarps; ++i) st = ms_merge(st, part[i], k2);
+    mine = st;
+  }
+  cluster.sync();
+  st = ms_empty();
+  for (int i = 0; i < p.CL; ++i)
+    st = ms_merge(st, *cluster.map_shared_rank(&mine, i), k2);
+  cg::cluster_group::arrival_token token = cluster.barrier_arrive();
+  const float P = t.P, nan = __int_as_float(0x7fc00000);
+  const bool ok = ms_valid(st) && P == P;
+  const float ls = log2f(st.s);
+  if (rank == 0 && warp == 0) {
+    float a = 0.f;
+    for (int k = lane; k < p.K; k += 32)
+      if (t.id[k] >= 0 && t.p[k] > 0.f)
+        a += t.p[k] * (t.log2p[k] - ((at[k] - st.m) * k2 - ls));
+    a = warp_down_sum(a);
+    if (lane == 0) {
+      p.loss[row] = ok ? a * kLn2 : nan;
+      p.lse[row] = ok ? (st.m * k2 + ls) * kLn2 : nan;
+      if (!ok) status_or(p.dev_status, SD_DEV_NONFINITE);
+    }
+  }
+  if constexpr (STEP) {
+    const float w = __ldg(p.grad_loss + row);
+    const float c = w == 0.f ? 0.f : ok ? w * p.inv_T : nan;
+    const float nl2 = -(st.m * k2 + ls);
+    char *grad =
+        (char *)p.grad + (long long)row * p.grad_stride * elt_bytes<DT>();
+    const bool aligned = ((reinterpret_cast<uintptr_t>(grad) & 15) /
+                          elt_bytes<DT>()) == (unsigned)r.head;
+    // c = 0 and nothing usable: zeros, not 0 x NaN
+    const float scale = c * P, kz = w == 0.f ? 0.f : k2;
+#pragma unroll 4
+    for (int s = tid; s < n; s += kThreads) {
+      Raw<DT, VW> x;
+      x.w = w == 0.f ? make_uint4(0, 0, 0, 0) : slot[s];
+      store_slot<DT>(r, grad, aligned, s0 + s, x, w == 0.f ? 0.f : scale, kz,
+                     w == 0.f ? 0.f : nl2);
+    }
+    if (w != 0.f) {
+      __syncthreads();
+      store_entries<DT>(p, t, grad, max(0, r.first_col(s0)),
+                        min(p.V, r.first_col(s1)), at, c, P, nl2);
+    }
+  }
+  cluster.barrier_wait(std::move(token));  // peers have read `mine`
+}
+
+// The backward call: a CTA per row and run of kThreads kBatch slots.
+template <int DT>
+__global__ void __launch_bounds__(kThreads)
+distill_backward_kernel(const __grid_constant__ DistillParams p) {
+  constexpr int VW = vec_width<DT>();
+  __shared__ Teacher t;
+  __shared__ float at[SD_MAX_DISTILL_K];
+  const int row = blockIdx.x, tid = threadIdx.x;
+  const SlotRow<DT> r(p.student, p.row_stride, row, p.V);
+  const int s0 = blockIdx.y * (kThreads * kBatch);
+  const int s1 = min(s0 + kThreads * kBatch, r.slots);
+  if (s0 >= s1) return;
+  char *grad =
+      (char *)p.grad + (long long)row * p.grad_stride * elt_bytes<DT>();
+  const bool aligned = ((reinterpret_cast<uintptr_t>(grad) & 15) /
+                        elt_bytes<DT>()) == (unsigned)r.head;
+  const float w = __ldg(p.grad_loss + row);
+  Raw<DT, VW> x[kBatch];
+  if (w != 0.f) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (s0 + tid + i * kThreads < s1)
+        x[i] = load_slot(r, s0 + tid + i * kThreads);
+  }
+  const int lo = max(0, r.first_col(s0)), hi = min(p.V, r.first_col(s1));
+  float P = 0.f, c = 0.f, nl2 = 0.f;
+  if (w != 0.f) {
+    if (tid < 32) load_teacher(p, row, t);
+    __syncthreads();
+    P = t.P;
+    const float lse = __ldg(p.lse_in + row);
+    const bool ok = P == P && fabsf(lse) < kInf;
+    if (!ok && tid == 0) status_or(p.dev_status, SD_DEV_NONFINITE);
+    c = ok ? w * p.inv_T : __int_as_float(0x7fc00000);
+    nl2 = -lse * (1.f / kLn2);
+    // before any of this CTA's columns is written
+    for (int k = tid; k < p.K; k += kThreads)
+      if (t.id[k] >= lo && t.id[k] < hi)
+        at[k] = load_col(r, t.id[k]);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < kBatch; ++i) {
+    const int s = s0 + tid + i * kThreads;
+    if (s >= s1) continue;
+    if (w == 0.f) x[i].w = make_uint4(0, 0, 0, 0);
+    store_slot<DT>(r, grad, aligned, s, x[i], c * P, w == 0.f ? 0.f : p.k2,
+                   nl2);
+  }
+  if (w == 0.f) return;
+  __syncthreads();
+  store_entries<DT>(p, t, grad, lo, hi, at, c, P, nl2);
 }
 
 sd_status check_distill(const void *student, long long row_stride,
@@ -219,6 +431,46 @@ sd_status check_distill(const void *student, long long row_stride,
   SDV_REQUIRE(row_stride >= V, "row_stride < V");
   SDV_REQUIRE(N == 0 || (student && logit && id), "null pointer");
   return SD_OK;
+}
+
+// Slots a row of V columns can take, wherever it starts.
+int max_slots(int V, sd_dtype dt) {
+  const int vw = dt == SD_F32 ? 4 : 8;
+  return (V + 2 * vw - 2) / vw;
+}
+
+// CTAs per row of the forward call: enough for some eight on every SM, each
+// with at least 512 slots.
+int forward_cluster(int N, int slots, int sms) {
+  int cl = 1;
+  while (cl < 8 && (long long)N * cl < 4LL * sms && slots / (2 * cl) >= 512)
+    cl *= 2;
+  return cl;
+}
+
+// CTAs per row of the step, 0 where a row does not fit their shared memory:
+// slices of at most 70 KB (three CTAs on an SM: one loads while another
+// writes), smaller ones while there are too few rows to fill the GPU.
+int step_cluster(int N, int slots, int sms) {
+  constexpr int kMost = 4480;
+  int cl = (slots + kMost - 1) / kMost;
+  if (cl > 16) return 0;
+  if (cl > 8) return 16;
+  while (cl <= 4 && (long long)N * cl < sms && slots / (2 * cl) >= 512) cl *= 2;
+  return cl;
+}
+
+template <bool STEP>
+sd_status launch_rows(DistillParams &p, sd_dtype dt, int cl, size_t smem,
+                      cudaStream_t s) {
+  const void *kernel = dt == SD_F32 ? (const void *)distill_row_kernel<0, STEP>
+                                    : (const void *)distill_row_kernel<1, STEP>;
+  int resident = 0;  // also lets the kernel have its shared memory
+  const sd_status st = max_active_clusters(kernel, cl, smem, &resident);
+  if (st != SD_OK) return st;
+  p.CL = cl;
+  void *args[] = {&p};
+  return launch_clusters(kernel, p.N, cl, smem, s, args);
 }
 
 DistillParams distill_params(const void *student, long long row_stride,
@@ -264,10 +516,8 @@ extern "C" sd_status sd_distill_topk(
   p.loss = loss;
   p.lse = lse;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dt == SD_F32) distill_forward_kernel<0><<<N, kThreads, 0, s>>>(p);
-  else distill_forward_kernel<1><<<N, kThreads, 0, s>>>(p);
-  SDV_CUDA(cudaGetLastError());
-  return SD_OK;
+  return launch_rows<false>(p, dt, forward_cluster(N, max_slots(V, dt), sms),
+                            0, s);
 }
 
 extern "C" sd_status sd_distill_topk_backward(
@@ -293,8 +543,10 @@ extern "C" sd_status sd_distill_topk_backward(
   p.grad = grad;
   p.grad_stride = grad_stride;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dt == SD_F32) distill_backward_kernel<0><<<N, kThreads, 0, s>>>(p);
-  else distill_backward_kernel<1><<<N, kThreads, 0, s>>>(p);
+  const int run = kThreads * kBatch;
+  const dim3 grid(N, (max_slots(V, dt) + run - 1) / run);
+  if (dt == SD_F32) distill_backward_kernel<0><<<grid, kThreads, 0, s>>>(p);
+  else distill_backward_kernel<1><<<grid, kThreads, 0, s>>>(p);
   SDV_CUDA(cudaGetLastError());
   return SD_OK;
 }
@@ -305,13 +557,33 @@ extern "C" sd_status sd_distill_topk_step(
     const float *teacher_lse, const float *grad_loss, int N, int V, int K,
     float T, float *loss, float *lse, void *grad, long long grad_stride,
     int32_t *dev_status, void *stream) {
-  SDV_REQUIRE(N <= 0 || (grad_loss && grad), "null pointer");
-  SDV_REQUIRE(grad_stride >= V, "grad_stride < V");
-  sd_status st = sd_distill_topk(student, row_stride, dt, teacher_logit,
-                                 teacher_id, teacher_lse, N, V, K, T, loss,
-                                 lse, dev_status, stream);
+  sd_status st = check_distill(student, row_stride, dt, teacher_logit,
+                               teacher_id, N, V, K, T);
   if (st != SD_OK) return st;
-  return sd_distill_topk_backward(student, row_stride, dt, lse, teacher_logit,
-                                  teacher_id, teacher_lse, grad_loss, N, V, K,
-                                  T, grad, grad_stride, dev_status, stream);
+  SDV_REQUIRE(grad_stride >= V, "grad_stride < V");
+  if (N == 0) return SD_OK;
+  SDV_REQUIRE(loss && lse && grad_loss && grad, "null pointer");
+  int sms = 0;
+  st = check_device(&sms);
+  if (st != SD_OK) return st;
+  const int slots = max_slots(V, dt), cl = step_cluster(N, slots, sms);
+  if (cl == 0) {  // rows too long to keep: read them twice
+    st = sd_distill_topk(student, row_stride, dt, teacher_logit, teacher_id,
+                         teacher_lse, N, V, K, T, loss, lse, dev_status,
+                         stream);
+    if (st != SD_OK) return st;
+    return sd_distill_topk_backward(
+        student, row_stride, dt, lse, teacher_logit, teacher_id, teacher_lse,
+        grad_loss, N, V, K, T, grad, grad_stride, dev_status, stream);
+  }
+  DistillParams p =
+      distill_params(student, row_stride, teacher_logit, teacher_id,
+                     teacher_lse, N, V, K, T, dev_status);
+  p.loss = loss;
+  p.lse = lse;
+  p.grad_loss = grad_loss;
+  p.grad = grad;
+  p.grad_stride = grad_stride;
+  return launch_rows<true>(p, dt, cl, (size_t)(slots / cl + 2) * 16,
+                           static_cast<cudaStream_t>(stream));
 }
