@@ -161,28 +161,33 @@ struct Teacher {
   float P;
 };
 
-// Read and normalise a row's entries (one warp).
-__device__ void load_teacher(const DistillParams &p, int row, Teacher &t) {
+// An entry as read: padding and logits of -inf lose their id, NaN and +inf
+// become NaN.
+__device__ __forceinline__ void put_entry(const DistillParams &p, Teacher &t,
+                                          int k, int id, float z) {
+  bool bad = false;
+  if (id >= p.V) {
+    status_or(p.dev_status, SD_DEV_BAD_TOKEN);
+    id = -1;
+  }
+  if (id >= 0) {
+    bad = z != z || z == kInf;
+    if (z == -kInf) id = -1;
+  }
+  t.id[k] = id < 0 ? -1 : id;
+  t.log2p[k] = bad ? __int_as_float(0x7fc00000) : z;
+}
+
+// Normalise a row's entries as put_entry left them (one warp).
+__device__ void normalise(const DistillParams &p, int row, Teacher &t) {
   const int lane = threadIdx.x & 31;
-  int st = 0;
   float m = -kInf;
   bool bad = false;
-  for (int k = lane; k < p.K; k += 32) {
-    int id = __ldg(p.id + (long long)row * p.K + k);
-    const float z = __ldg(p.logit + (long long)row * p.K + k);
-    if (id >= p.V) {
-      st |= SD_DEV_BAD_TOKEN;
-      id = -1;
+  for (int k = lane; k < p.K; k += 32)
+    if (t.id[k] >= 0) {
+      m = fmaxf(m, t.log2p[k]);
+      bad = bad || t.log2p[k] != t.log2p[k];
     }
-    if (id >= 0) {
-      if (z != z || z == kInf) bad = true;
-      if (z == -kInf) id = -1;
-    }
-    t.id[k] = id < 0 ? -1 : id;
-    t.log2p[k] = z;
-    if (id >= 0) m = fmaxf(m, z);
-  }
-  status_or(p.dev_status, st);
 #pragma unroll
   for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
   // sum of 2^((z - m) k2) over the entries
@@ -214,6 +219,15 @@ __device__ void load_teacher(const DistillParams &p, int row, Teacher &t) {
   if (lane == 0) t.P = P;
 }
 
+// Read and normalise a row's entries (one warp).
+__device__ void load_teacher(const DistillParams &p, int row, Teacher &t) {
+  for (int k = threadIdx.x & 31; k < p.K; k += 32)
+    put_entry(p, t, k, __ldg(p.id + (long long)row * p.K + k),
+              __ldg(p.logit + (long long)row * p.K + k));
+  __syncwarp();
+  normalise(p, row, t);
+}
+
 // The columns of the entries with ids in [lo, hi), over what the pass over
 // the row wrote: the first entry of an id writes for all that repeat it.
 // at: the student's logits at the ids.
@@ -236,18 +250,40 @@ __device__ void store_entries(const DistillParams &p, const Teacher &t,
   }
 }
 
-// The forward call and the step: a cluster of CL CTAs per row, a contiguous
-// run of its slots each.  STEP: the run is kept in shared memory (bulk
-// copies, a barrier each) and read from there again for the gradient.
-template <int DT, bool STEP>
+// (max, sum) of a row's slots: this thread's part in, the cluster's out.
+// Every CTA merges the parts in rank order.  A CTA that is a row ahead may
+// not change what a peer still reads: rows alternate between the two `mine`.
+struct RowReduce {
+  MS part[kWarps], mine[2];
+};
+__device__ __forceinline__ MS reduce_row(MS st, float k2, int CL,
+                                         RowReduce &red, int which,
+                                         cg::cluster_group &cluster) {
+  const int tid = threadIdx.x;
+  st = warp_down_ms(st, k2);
+  if ((tid & 31) == 0) red.part[tid >> 5] = st;
+  __syncthreads();
+  if (tid == 0) {
+    st = red.part[0];
+    for (int i = 1; i < kWarps; ++i) st = ms_merge(st, red.part[i], k2);
+    red.mine[which] = st;
+  }
+  cluster.sync();
+  st = ms_empty();
+  for (int i = 0; i < CL; ++i)
+    st = ms_merge(st, *cluster.map_shared_rank(&red.mine[which], i), k2);
+  return st;
+}
+
+// The forward call: a cluster of CL CTAs per row, a contiguous run of its
+// slots each.
+template <int DT>
 __global__ void __launch_bounds__(kThreads)
-distill_row_kernel(const __grid_constant__ DistillParams p) {
+distill_forward_kernel(const __grid_constant__ DistillParams p) {
   constexpr int VW = vec_width<DT>();
-  extern __shared__ __align__(16) char kept[];
   __shared__ Teacher t;
   __shared__ float at[SD_MAX_DISTILL_K];
-  __shared__ MS part[kWarps], mine;
-  __shared__ uint64_t bar[kMaxCopies];
+  __shared__ RowReduce red;
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster.block_rank();
@@ -255,79 +291,28 @@ distill_row_kernel(const __grid_constant__ DistillParams p) {
   const SlotRow<DT> r(p.student, p.row_stride, row, p.V);
   const int s0 = (int)((long long)r.slots * rank / p.CL);
   const int s1 = (int)((long long)r.slots * (rank + 1) / p.CL);
-  const int n = s1 - s0;
   const float k2 = p.k2;
-  uint4 *slot = reinterpret_cast<uint4 *>(kept);
-  if constexpr (STEP) {
-    // only a row's first and last slot can be partial
-    const int f0 = s0 + (n > 0 && !r.full(s0));
-    const int f1 = s1 - (n > 0 && s1 - 1 >= f0 && !r.full(s1 - 1));
-    if (tid == 0) {
-      for (int i = 0; i < kMaxCopies; ++i) mbar_init(&bar[i], 1);
-      fence_mbar_init();
-      for (int i = 0; i * kSlotsPerCopy < n; ++i) {
-        const int a = max(s0 + i * kSlotsPerCopy, f0);
-        const int b = min(s0 + (i + 1) * kSlotsPerCopy, f1);
-        const uint32_t bytes = b > a ? (uint32_t)(b - a) * 16 : 0;
-        mbar_expect_tx(&bar[i], bytes);
-        if (bytes)
-          bulk_g2s_hint(slot + (a - s0), r.base + (long long)a * 16, bytes,
-                        &bar[i], l2_evict_first_policy());
-      }
-    }
-    if (tid == 32 && f0 > s0) slot[0] = load_partial(r, s0).w;
-    if (tid == 64 && f1 < s1) slot[n - 1] = load_partial(r, s1 - 1).w;
-  }
-  if (warp == kWarps - 1) load_teacher(p, row, t);
-  __syncthreads();
-  // the student's logits at the ids, before anything is written (the
-  // gradient may go to the student's own rows)
-  if (rank == 0 || STEP) {
-    for (int k = tid; k < p.K; k += kThreads)
+  if (rank == 0 && warp == kWarps - 1) {
+    load_teacher(p, row, t);
+    __syncwarp();
+    for (int k = lane; k < p.K; k += 32)
       at[k] = t.id[k] >= 0 ? load_col(r, t.id[k]) : 0.f;
   }
   MS st = ms_empty();
   float vmax;
-  bool fine = true;
-  if constexpr (STEP) {
-    for (int i = 0; i * kSlotsPerCopy < n; ++i) {
-      fine = mbar_wait(&bar[i], 0, p.dev_status) && fine;
-      const int b = min((i + 1) * kSlotsPerCopy, n);
-#pragma unroll 4
-      for (int s = i * kSlotsPerCopy + tid; s < b; s += kThreads) {
-        Raw<DT, VW> x;
-        x.w = slot[s];
-        ms_add_v<DT, VW>(st, x, k2, vmax);
-      }
-    }
-  } else {
-    for (int s = s0 + tid; s < s1; s += kThreads * kBatch) {
-      Raw<DT, VW> x[kBatch];
+  for (int s = s0 + tid; s < s1; s += kThreads * kBatch) {
+    Raw<DT, VW> x[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (s + i * kThreads < s1) x[i] = load_slot(r, s + i * kThreads);
+    for (int i = 0; i < kBatch; ++i)
+      if (s + i * kThreads < s1) x[i] = load_slot(r, s + i * kThreads);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        if (s + i * kThreads < s1) ms_add_v<DT, VW>(st, x[i], k2, vmax);
-    }
+    for (int i = 0; i < kBatch; ++i)
+      if (s + i * kThreads < s1) ms_add_v<DT, VW>(st, x[i], k2, vmax);
   }
-  st = warp_down_ms(st, k2);
-  if (lane == 0) part[warp] = st;
-  __syncthreads();
-  if (tid == 0) {
-    st = part[0];
-    for (int i = 1; i < kWarps; ++i) st = ms_merge(st, part[i], k2);
-    mine = st;
-  }
-  cluster.sync();
-  st = ms_empty();
-  for (int i = 0; i < p.CL; ++i)
-    st = ms_merge(st, *cluster.map_shared_rank(&mine, i), k2);
-  cg::cluster_group::arrival_token token = cluster.barrier_arrive();
-  const float P = t.P, nan = __int_as_float(0x7fc00000);
-  const bool ok = ms_valid(st) && P == P;
-  const float ls = log2f(st.s);
+  st = reduce_row(st, k2, p.CL, red, 0, cluster);
   if (rank == 0 && warp == 0) {
+    const float ls = log2f(st.s), nan = __int_as_float(0x7fc00000);
+    const bool ok = ms_valid(st) && t.P == t.P;
     float a = 0.f;
     for (int k = lane; k < p.K; k += 32)
       if (t.id[k] >= 0 && t.p[k] > 0.f)
@@ -339,7 +324,138 @@ distill_row_kernel(const __grid_constant__ DistillParams p) {
       if (!ok) status_or(p.dev_status, SD_DEV_NONFINITE);
     }
   }
-  if constexpr (STEP) {
+  cluster.sync();  // peers have read `red`
+}
+
+// The step: clusters of CL CTAs take rows in turn and keep a row in their
+// shared memory (bulk copies of up to 16 KB, a barrier each) from the pass
+// that finds log sum exp to the pass that writes the gradient.  The second
+// pass hands a copy's space to the next row as soon as it has used it, so
+// loads and stores overlap within a CTA as well as between the three on an
+// SM; the next row's teacher entries are fetched a row ahead.
+template <int DT>
+__global__ void __launch_bounds__(kThreads)
+distill_step_kernel(const __grid_constant__ DistillParams p) {
+  constexpr int VW = vec_width<DT>();
+  extern __shared__ __align__(16) char kept[];
+  __shared__ Teacher t;
+  __shared__ float at[SD_MAX_DISTILL_K], entry_loss[2];
+  __shared__ RowReduce red;
+  __shared__ uint64_t bar[kMaxCopies];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster.block_rank();
+  const int clusters = gridDim.x / p.CL;
+  const float k2 = p.k2, nan = __int_as_float(0x7fc00000);
+  uint4 *slot = reinterpret_cast<uint4 *>(kept);
+  // this CTA's run of a row's slots; [f0, f1) are whole
+  struct Run {
+    int s0, s1, f0, f1;
+  };
+  auto run_of = [&](const SlotRow<DT> &r) {
+    Run u;
+    u.s0 = (int)((long long)r.slots * rank / p.CL);
+    u.s1 = (int)((long long)r.slots * (rank + 1) / p.CL);
+    u.f0 = u.s0 + (u.s1 > u.s0 && !r.full(u.s0));
+    u.f1 = u.s1 - (u.s1 > u.f0 && !r.full(u.s1 - 1));
+    return u;
+  };
+  // copy i of a row (thread 0)
+  auto fetch = [&](const SlotRow<DT> &r, const Run &u, int i) {
+    const int a = max(u.s0 + i * kSlotsPerCopy, u.f0);
+    const int b = min(u.s0 + (i + 1) * kSlotsPerCopy, u.f1);
+    const uint32_t bytes = b > a ? (uint32_t)(b - a) * 16 : 0;
+    mbar_expect_tx(&bar[i], bytes);
+    if (bytes)
+      bulk_g2s_hint(slot + (a - u.s0), r.base + (long long)a * 16, bytes,
+                    &bar[i], l2_evict_first_policy());
+  };
+  if (tid == 0) {
+    for (int i = 0; i < kMaxCopies; ++i) mbar_init(&bar[i], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  int row = blockIdx.x / p.CL;
+  SlotRow<DT> r(p.student, p.row_stride, row, p.V);
+  Run u = run_of(r);
+  if (tid == 0)
+    for (int i = 0; i < kMaxCopies; ++i) fetch(r, u, i);
+  auto entry_of = [&](int n, int &id, float &z) {
+    id = -1;
+    z = 0.f;
+    if (n < p.N && tid < p.K) {
+      id = __ldg(p.id + (long long)n * p.K + tid);
+      z = __ldg(p.logit + (long long)n * p.K + tid);
+    }
+  };
+  static_assert(SD_MAX_DISTILL_K <= kThreads, "an entry a thread");
+  int id;
+  float z;
+  entry_of(row, id, z);
+  uint32_t parity = 0;
+  int last = -1;  // the row whose loss is being added up
+  bool last_ok = false;
+  // rank 0, after a cluster barrier: the loss of row `last`
+  auto finish_loss = [&] {
+    if (rank == 0 && warp == 0 && last >= 0) {
+      float a = lane < p.CL
+                    ? *cluster.map_shared_rank(&entry_loss[parity ^ 1], lane)
+                    : 0.f;
+      a = warp_down_sum(a);
+      if (lane == 0) p.loss[last] = last_ok ? a * kLn2 : nan;
+    }
+  };
+  for (; row < p.N; row += clusters) {
+    const int n = u.s1 - u.s0;
+    if (tid < p.K) put_entry(p, t, tid, id, z);
+    entry_of(row + clusters, id, z);
+    if (tid == 32 && u.f0 > u.s0) slot[0] = load_partial(r, u.s0).w;
+    if (tid == 64 && u.f1 < u.s1) slot[n - 1] = load_partial(r, u.s1 - 1).w;
+    __syncthreads();
+    if (warp == kWarps - 1) normalise(p, row, t);
+    MS st = ms_empty();
+    float vmax;
+    for (int i = 0; i < kMaxCopies; ++i) {
+      mbar_wait(&bar[i], parity, p.dev_status);
+      const int b = min((i + 1) * kSlotsPerCopy, n);
+#pragma unroll 4
+      for (int s = i * kSlotsPerCopy + tid; s < b; s += kThreads) {
+        Raw<DT, VW> x;
+        x.w = slot[s];
+        ms_add_v<DT, VW>(st, x, k2, vmax);
+      }
+    }
+    st = reduce_row(st, k2, p.CL, red, parity, cluster);
+    finish_loss();
+    const float P = t.P;
+    const bool ok = ms_valid(st) && P == P;
+    const float ls = log2f(st.s);
+    const int lo = max(0, r.first_col(u.s0));
+    const int hi = min(p.V, r.first_col(u.s1));
+    // the entries in this run: their logits and their part of the loss
+    float a = 0.f;
+    if (tid < p.K && t.id[tid] >= lo && t.id[tid] < hi) {
+      const int c = t.id[tid] - r.first_col(u.s0);
+      const char *src = kept + (long long)c * elt_bytes<DT>();
+      const float x =
+          DT == 0 ? *reinterpret_cast<const float *>(src)
+                  : __uint_as_float(
+                        (uint32_t)*reinterpret_cast<const unsigned short *>(src)
+                        << 16);
+      at[tid] = x;
+      if (t.p[tid] > 0.f)
+        a = t.p[tid] * (t.log2p[tid] - ((x - st.m) * k2 - ls));
+    }
+    __shared__ float loss_part[kWarps];
+    a = warp_down_sum(a);
+    if (lane == 0) loss_part[warp] = a;
+    if (rank == 0 && tid == 0) {
+      p.lse[row] = ok ? (st.m * k2 + ls) * kLn2 : nan;
+      if (!ok) status_or(p.dev_status, SD_DEV_NONFINITE);
+    }
+    last = row;
+    last_ok = ok;
+    // the gradient, and the next row into the space of the copies used up
     const float w = __ldg(p.grad_loss + row);
     const float c = w == 0.f ? 0.f : ok ? w * p.inv_T : nan;
     const float nl2 = -(st.m * k2 + ls);
@@ -347,22 +463,37 @@ distill_row_kernel(const __grid_constant__ DistillParams p) {
         (char *)p.grad + (long long)row * p.grad_stride * elt_bytes<DT>();
     const bool aligned = ((reinterpret_cast<uintptr_t>(grad) & 15) /
                           elt_bytes<DT>()) == (unsigned)r.head;
-    // c = 0 and nothing usable: zeros, not 0 x NaN
-    const float scale = c * P, kz = w == 0.f ? 0.f : k2;
+    const SlotRow<DT> next(p.student, p.row_stride,
+                           min(row + clusters, p.N - 1), p.V);
+    const Run nu = run_of(next);
+    for (int i = 0; i < kMaxCopies; ++i) {
+      const int b = min((i + 1) * kSlotsPerCopy, n);
 #pragma unroll 4
-    for (int s = tid; s < n; s += kThreads) {
-      Raw<DT, VW> x;
-      x.w = w == 0.f ? make_uint4(0, 0, 0, 0) : slot[s];
-      store_slot<DT>(r, grad, aligned, s0 + s, x, w == 0.f ? 0.f : scale, kz,
-                     w == 0.f ? 0.f : nl2);
-    }
-    if (w != 0.f) {
+      for (int s = i * kSlotsPerCopy + tid; s < b; s += kThreads) {
+        Raw<DT, VW> x;
+        // a weight of 0: zeros, whatever the row holds
+        x.w = w == 0.f ? make_uint4(0, 0, 0, 0) : slot[s];
+        store_slot<DT>(r, grad, aligned, u.s0 + s, x, w == 0.f ? 0.f : c * P,
+                       w == 0.f ? 0.f : k2, w == 0.f ? 0.f : nl2);
+      }
+      fence_proxy_async();
       __syncthreads();
-      store_entries<DT>(p, t, grad, max(0, r.first_col(s0)),
-                        min(p.V, r.first_col(s1)), at, c, P, nl2);
+      if (tid == 0 && row + clusters < p.N) fetch(next, nu, i);
     }
+    if (tid == 0) {
+      float sum = 0.f;
+      for (int i = 0; i < kWarps; ++i) sum += loss_part[i];
+      entry_loss[parity] = sum;
+    }
+    if (w != 0.f) store_entries<DT>(p, t, grad, lo, hi, at, c, P, nl2);
+    __syncthreads();  // t, at and the parts may change
+    r = next;
+    u = nu;
+    parity ^= 1;
   }
-  cluster.barrier_wait(std::move(token));  // peers have read `mine`
+  cluster.sync();
+  finish_loss();
+  cluster.sync();  // peers have read entry_loss
 }
 
 // The backward call: a CTA per row and run of kThreads kBatch slots.
@@ -460,19 +591,6 @@ int step_cluster(int N, int slots, int sms) {
   return cl;
 }
 
-template <bool STEP>
-sd_status launch_rows(DistillParams &p, sd_dtype dt, int cl, size_t smem,
-                      cudaStream_t s) {
-  const void *kernel = dt == SD_F32 ? (const void *)distill_row_kernel<0, STEP>
-                                    : (const void *)distill_row_kernel<1, STEP>;
-  int resident = 0;  // also lets the kernel have its shared memory
-  const sd_status st = max_active_clusters(kernel, cl, smem, &resident);
-  if (st != SD_OK) return st;
-  p.CL = cl;
-  void *args[] = {&p};
-  return launch_clusters(kernel, p.N, cl, smem, s, args);
-}
-
 DistillParams distill_params(const void *student, long long row_stride,
                              const float *logit, const int32_t *id,
                              const float *teacher_lse, int N, int V, int K,
@@ -516,8 +634,11 @@ extern "C" sd_status sd_distill_topk(
   p.loss = loss;
   p.lse = lse;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return launch_rows<false>(p, dt, forward_cluster(N, max_slots(V, dt), sms),
-                            0, s);
+  const void *kernel = dt == SD_F32 ? (const void *)distill_forward_kernel<0>
+                                    : (const void *)distill_forward_kernel<1>;
+  p.CL = forward_cluster(N, max_slots(V, dt), sms);
+  void *args[] = {&p};
+  return launch_clusters(kernel, N, p.CL, 0, s, args);
 }
 
 extern "C" sd_status sd_distill_topk_backward(
@@ -584,6 +705,14 @@ extern "C" sd_status sd_distill_topk_step(
   p.grad_loss = grad_loss;
   p.grad = grad;
   p.grad_stride = grad_stride;
-  return launch_rows<true>(p, dt, cl, (size_t)(slots / cl + 2) * 16,
-                           static_cast<cudaStream_t>(stream));
+  const void *kernel = dt == SD_F32 ? (const void *)distill_step_kernel<0>
+                                    : (const void *)distill_step_kernel<1>;
+  const size_t smem = (size_t)(slots / cl + 2) * 16;
+  int resident = 0;
+  st = max_active_clusters(kernel, cl, smem, &resident);
+  if (st != SD_OK) return st;
+  p.CL = cl;
+  void *args[] = {&p};
+  return launch_clusters(kernel, N < resident ? N : resident, cl, smem,
+                         static_cast<cudaStream_t>(stream), args);
 }
