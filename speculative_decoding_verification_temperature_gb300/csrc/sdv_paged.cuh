@@ -45,14 +45,20 @@ __device__ __forceinline__ Chunk load_chunk(const int32_t *q_start,
 }
 
 // The last sequence whose q_start is at most `row` (the row's own, where it
-// has one: empty sequences before it share its q_start).
-__device__ __forceinline__ int find_sequence(const int32_t *q_start, int B,
-                                             int row) {
-  int lo = 0, hi = B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(q_start + mid) <= row) lo = mid;
-    else hi = mid - 1;
+// has one: empty sequences before it share its q_start).  The whole warp
+// looks, a 32nd of the range a lane.
+__device__ __forceinline__ int warp_find_sequence(const int32_t *q_start,
+                                                  int B, int row) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;  // in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = lo + lane * step;
+    const unsigned below =
+        __ballot_sync(~0u, lane * step < n && __ldg(q_start + at) <= row);
+    const int last = below ? 31 - __clz(below) : 0;
+    n = min(step, n - last * step);
+    lo += last * step;
   }
   return lo;
 }
