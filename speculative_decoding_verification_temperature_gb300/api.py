@@ -24,6 +24,7 @@ DEV_BAD_LENGTH, DEV_BAD_PAGE, DEV_BAD_POSITION = 32, 64, 128
 
 _lock = threading.Lock()
 _lib = None
+_get_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 class SdError(RuntimeError):
@@ -35,6 +36,8 @@ class SdError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load libsdverify.so (compiling it first if it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             # SDV_LIB selects another build of the same library
@@ -657,6 +660,7 @@ class PagedKV:
         self.k, self.v, self.block_table = k, v, block_table
         n, page, heads, dim = k.shape
         self.B, self.heads, self.head_dim = block_table.shape[0], heads, dim
+        self.device, self.dtype = dev, k.dtype
         self._struct = _PagedKVStruct(
             k.data_ptr(), v.data_ptr(), _CACHE_DT[k.dtype], n, page, heads,
             dim, k.stride(0), k.stride(1), k.stride(2),
@@ -664,38 +668,54 @@ class PagedKV:
         self._addr = ctypes.addressof(self._struct)
 
 
+# The checks below look at each property once: a call on a few tokens takes
+# less time on the GPU than its checks can take here.
+
 def _rows(t, cache, name, heads=None):
     """Packed rows [total, heads, head_dim] of the cache's type, a row's
-    heads contiguous; returns the stride between rows."""
+    heads contiguous; returns their number, the heads and the row stride."""
+    d, shape, st = cache.head_dim, t.shape, t.stride()
+    if t.dtype is cache.dtype and t.device == cache.device and \
+            len(shape) == 3 and shape[2] == d and st[2] == 1:
+        n, h, _ = shape
+        if (st[1] == d or h == 1) and (h == heads or heads is None):
+            return n, h, st[0] if n > 1 else h * d
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor (there is no CPU path)"
                          % name)
-    if t.device != cache.k.device:
-        raise ValueError("%s must live on %s" % (name, cache.k.device))
-    if t.dtype != cache.k.dtype:
-        raise TypeError("%s must be %s" % (name, cache.k.dtype))
-    d = cache.head_dim
-    if t.dim() != 3 or t.shape[2] != d or \
-            (heads is not None and t.shape[1] != heads):
-        raise ValueError("%s must be [total, %s, %d]" %
-                         (name, heads or "heads", d))
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (s1 != d and t.shape[1] > 1):
-        raise ValueError("%s: a row's heads must be contiguous" % name)
-    return s0 if t.shape[0] > 1 else max(s0, t.shape[1] * d)
+    if t.device != cache.device:
+        raise ValueError("%s must live on %s" % (name, cache.device))
+    if t.dtype != cache.dtype:
+        raise TypeError("%s must be %s" % (name, cache.dtype))
+    raise ValueError("%s must be [total, %s, %d] with a row's heads "
+                     "contiguous" % (name, heads or "heads", d))
+
+
+def _vec(t, device, dtype, name):
+    """A contiguous tensor of this type and device; returns its address."""
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        _dev(t, device, name, dtype)
+    return t.data_ptr()
 
 
 def _lengths(cache, q_start, kv_len):
-    dev = cache.k.device
-    _dev(q_start, dev, "q_start", torch.int32)
-    _dev(kv_len, dev, "kv_len", torch.int32)
+    qp = _vec(q_start, cache.device, torch.int32, "q_start")
+    kp = _vec(kv_len, cache.device, torch.int32, "kv_len")
     B = kv_len.numel()
     if q_start.numel() != B + 1:
         raise ValueError("q_start must have one entry more than kv_len")
     if B > cache.B:
         raise ValueError("block_table has %d rows for %d sequences" %
                          (cache.B, B))
-    return B
+    return B, qp, kp
+
+
+def _raw_stream(device):
+    """The current stream's handle (without a Stream object around it where
+    torch has a call for that: 2 us less)."""
+    if _get_raw_stream is not None and device.index is not None:
+        return _get_raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _ptr(t):
@@ -712,33 +732,33 @@ def kv_append(cache, k, v, q_start, kv_len, *, q=None, cos_sin=None,
     tokens); cos_sin [max_pos, rot_dim] float32, cosines then sines (None:
     no rotation); positions [total] int32 (None: the index in the sequence).
     Returns the rotated queries (None without q)."""
-    dev = cache.k.device
-    ks, vs = _rows(k, cache, "k", cache.heads), _rows(v, cache, "v",
-                                                      cache.heads)
-    total = k.shape[0]
-    if v.shape[0] != total:
+    dev, D = cache.device, cache.head_dim
+    total, _, ks = _rows(k, cache, "k", cache.heads)
+    nv, _, vs = _rows(v, cache, "v", cache.heads)
+    if nv != total:
         raise ValueError("k and v must have the same number of rows")
-    B = _lengths(cache, q_start, kv_len)
+    B, start, lens = _lengths(cache, q_start, kv_len)
     qs = Hq = max_pos = rot = 0
-    out = None
+    qp = op = cp = pp = out = None
     if q is not None:
-        qs, Hq = _rows(q, cache, "q"), q.shape[1]
-        if q.shape[0] != total:
+        nq, Hq, qs = _rows(q, cache, "q")
+        if nq != total:
             raise ValueError("q and k must have the same number of rows")
-        out = torch.empty((total, Hq, cache.head_dim), dtype=q.dtype,
-                          device=dev)
+        out = torch.empty((total, Hq, D), dtype=cache.dtype, device=dev)
+        qp, op = q.data_ptr(), out.data_ptr()
     if cos_sin is not None:
-        _dev(cos_sin, dev, "cos_sin", torch.float32)
+        cp = _vec(cos_sin, dev, torch.float32, "cos_sin")
         max_pos, rot = cos_sin.shape
     if positions is not None:
-        _dev(positions, dev, "positions", torch.int32)
+        pp = _vec(positions, dev, torch.int32, "positions")
         if positions.numel() != total:
             raise ValueError("positions must be [total]")
-    _check(lib().sd_kv_append(
-        cache._addr, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q), qs, Hq,
-        q_start.data_ptr(), kv_len.data_ptr(), _ptr(positions),
-        _ptr(cos_sin), max_pos, rot, 1 if interleaved else 0, B, total,
-        _ptr(out), _ptr(status), _stream(dev)))
+    rc = lib().sd_kv_append(
+        cache._addr, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, Hq, start,
+        lens, pp, cp, max_pos, rot, 1 if interleaved else 0, B, total, op,
+        _ptr(status), _raw_stream(dev))
+    if rc != SD_OK:
+        _check(rc)
     return out
 
 
@@ -754,67 +774,72 @@ def paged_attention(q, cache, q_start, kv_len, *, max_q=None, scale=None,
     hint that only picks the tile shape (default: the mean chunk).  scale
     defaults to D ** -0.5.  Returns out [total, q_heads, D] (and lse [total,
     q_heads] float32 when want_lse)."""
-    dev = cache.k.device
-    qs = _rows(q, cache, "q")
-    total, Hq, D = q.shape
-    B = _lengths(cache, q_start, kv_len)
-    words = 0
+    dev, D = cache.device, cache.head_dim
+    total, Hq, qs = _rows(q, cache, "q")
+    B, start, lens = _lengths(cache, q_start, kv_len)
+    words, mp = 0, None
     if tree_mask is not None:
-        _dev(tree_mask, dev, "tree_mask", torch.int32)
+        mp = _vec(tree_mask, dev, torch.int32, "tree_mask")
         if tree_mask.dim() != 2 or tree_mask.shape[0] != total:
             raise ValueError("tree_mask must be [total, words]")
         words = tree_mask.shape[1]
     if max_q is None:
         max_q = -(-total // max(B, 1))
-    out = torch.empty((total, Hq, D), dtype=q.dtype, device=dev)
+    out = torch.empty((total, Hq, D), dtype=cache.dtype, device=dev)
     lse = torch.empty((total, Hq), dtype=torch.float32,
                       device=dev) if want_lse else None
     L = lib()
     nbytes = L.sd_paged_attention_workspace(Hq, cache.heads, D, max_q)
     ws = (workspace or _default_ws).get(dev, nbytes)
-    _check(L.sd_paged_attention(
-        q.data_ptr(), qs, Hq, cache._addr, q_start.data_ptr(),
-        kv_len.data_ptr(), _ptr(tree_mask), words, B, total, max_q,
-        D ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(lse),
-        _ptr(status), ws.data_ptr(), ws.numel(), _stream(dev)))
+    rc = L.sd_paged_attention(
+        q.data_ptr(), qs, Hq, cache._addr, start, lens, mp, words, B, total,
+        max_q, D ** -0.5 if scale is None else scale, out.data_ptr(),
+        _ptr(lse), _ptr(status), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+    if rc != SD_OK:
+        _check(rc)
     return {"out": out, "lse": lse} if want_lse else {"out": out}
 
 
-def _distill_rows(student, teacher_logit, teacher_id, teacher_lse):
+_LOGIT_DT = {torch.float32: SD_F32, torch.bfloat16: SD_BF16}
+
+
+def _distill_rows(student, logit, ids, lse):
+    """Checks the rows; returns the arguments that every call shares."""
     dev = student.device
-    if not student.is_cuda:
+    if dev.type != "cuda":
         raise ValueError("student must be a CUDA tensor (there is no CPU "
                          "path)")
-    if student.dim() != 2 or student.stride(1) != 1:
+    shape, st = student.shape, student.stride()
+    if len(shape) != 2 or st[1] != 1:
         raise ValueError("student must be [N, V] rows with unit stride")
-    N, V = student.shape
-    _dev(teacher_logit, dev, "teacher_logit", torch.float32)
-    _dev(teacher_id, dev, "teacher_id", torch.int32)
-    if teacher_logit.dim() != 2 or teacher_logit.shape[0] != N or \
-            teacher_id.shape != teacher_logit.shape:
+    dt = _LOGIT_DT.get(student.dtype)
+    if dt is None:
+        dt = _dt(student)
+    N, V = shape
+    lp = _vec(logit, dev, torch.float32, "teacher_logit")
+    ip = _vec(ids, dev, torch.int32, "teacher_id")
+    if logit.dim() != 2 or logit.shape[0] != N or ids.shape != logit.shape:
         raise ValueError("teacher_logit and teacher_id must be [N, K]")
-    _dev(teacher_lse, dev, "teacher_lse", torch.float32)
-    if teacher_lse is not None and teacher_lse.numel() != N:
-        raise ValueError("teacher_lse must be [N]")
-    return dev, N, V, teacher_logit.shape[1], \
-        student.stride(0) if N > 1 else max(student.stride(0), V)
+    tp = None if lse is None else _row_vector(lse, dev, "teacher_lse", N)
+    return dev, N, V, logit.shape[1], dt, st[0] if N > 1 else V, lp, ip, tp
 
 
 def _row_vector(t, dev, name, N):
-    _dev(t, dev, name, torch.float32)
+    p = _vec(t, dev, torch.float32, name)
     if t.numel() != N:
         raise ValueError("%s must be [N]" % name)
+    return p
 
 
 def _grad_out(out, student, dev, N, V):
     """The gradient's buffer and row stride (a new one without `out`)."""
     if out is None:
         return torch.empty((N, V), dtype=student.dtype, device=dev), V
-    if not out.is_cuda or out.device != dev or out.dtype != student.dtype \
+    if out.device != dev or out.dtype != student.dtype \
             or tuple(out.shape) != (N, V) or out.stride(1) != 1:
         raise ValueError("out must be [N, V] rows with unit stride, of the "
                          "student's type and device")
-    return out, out.stride(0) if N > 1 else max(out.stride(0), V)
+    return out, out.stride(0) if N > 1 else V
 
 
 def distill_topk(student, teacher_logit, teacher_id, T=1.0, *,
@@ -825,14 +850,15 @@ def distill_topk(student, teacher_logit, teacher_id, T=1.0, *,
     padding), teacher_lse [N] float32 (None: the K probabilities are
     normalised among themselves).  Returns loss [N] and lse [N] (log sum
     exp(student / T), which the backward call takes)."""
-    dev, N, V, K, rs = _distill_rows(student, teacher_logit, teacher_id,
-                                     teacher_lse)
+    dev, N, V, K, dt, rs, lp, ip, tp = _distill_rows(
+        student, teacher_logit, teacher_id, teacher_lse)
     loss = torch.empty(N, dtype=torch.float32, device=dev)
     lse = torch.empty(N, dtype=torch.float32, device=dev)
-    _check(lib().sd_distill_topk(
-        student.data_ptr(), rs, _dt(student), teacher_logit.data_ptr(),
-        teacher_id.data_ptr(), _ptr(teacher_lse), N, V, K, T,
-        loss.data_ptr(), lse.data_ptr(), _ptr(status), _stream(dev)))
+    rc = lib().sd_distill_topk(
+        student.data_ptr(), rs, dt, lp, ip, tp, N, V, K, T, loss.data_ptr(),
+        lse.data_ptr(), _ptr(status), _raw_stream(dev))
+    if rc != SD_OK:
+        _check(rc)
     return {"loss": loss, "lse": lse}
 
 
@@ -842,16 +868,16 @@ def distill_topk_backward(student, lse, teacher_logit, teacher_id, grad_loss,
     the student's logits (sd_distill_topk_backward); lse as distill_topk
     returned it.  ``out`` may be the student itself.  Returns grad [N, V] of
     the student's type."""
-    dev, N, V, K, rs = _distill_rows(student, teacher_logit, teacher_id,
-                                     teacher_lse)
-    _row_vector(lse, dev, "lse", N)
-    _row_vector(grad_loss, dev, "grad_loss", N)
+    dev, N, V, K, dt, rs, lp, ip, tp = _distill_rows(
+        student, teacher_logit, teacher_id, teacher_lse)
+    sp = _row_vector(lse, dev, "lse", N)
+    wp = _row_vector(grad_loss, dev, "grad_loss", N)
     grad, gs = _grad_out(out, student, dev, N, V)
-    _check(lib().sd_distill_topk_backward(
-        student.data_ptr(), rs, _dt(student), lse.data_ptr(),
-        teacher_logit.data_ptr(), teacher_id.data_ptr(), _ptr(teacher_lse),
-        grad_loss.data_ptr(), N, V, K, T, grad.data_ptr(), gs, _ptr(status),
-        _stream(dev)))
+    rc = lib().sd_distill_topk_backward(
+        student.data_ptr(), rs, dt, sp, lp, ip, tp, wp, N, V, K, T,
+        grad.data_ptr(), gs, _ptr(status), _raw_stream(dev))
+    if rc != SD_OK:
+        _check(rc)
     return grad
 
 
@@ -860,15 +886,16 @@ def distill_topk_step(student, teacher_logit, teacher_id, grad_loss, T=1.0,
     """distill_topk and its gradient in one call (sd_distill_topk_step), for
     a training step that knows the rows' weights beforehand.  Returns loss,
     lse and grad."""
-    dev, N, V, K, rs = _distill_rows(student, teacher_logit, teacher_id,
-                                     teacher_lse)
-    _row_vector(grad_loss, dev, "grad_loss", N)
+    dev, N, V, K, dt, rs, lp, ip, tp = _distill_rows(
+        student, teacher_logit, teacher_id, teacher_lse)
+    wp = _row_vector(grad_loss, dev, "grad_loss", N)
     loss = torch.empty(N, dtype=torch.float32, device=dev)
     lse = torch.empty(N, dtype=torch.float32, device=dev)
     grad, gs = _grad_out(out, student, dev, N, V)
-    _check(lib().sd_distill_topk_step(
-        student.data_ptr(), rs, _dt(student), teacher_logit.data_ptr(),
-        teacher_id.data_ptr(), _ptr(teacher_lse), grad_loss.data_ptr(), N, V,
-        K, T, loss.data_ptr(), lse.data_ptr(), grad.data_ptr(), gs,
-        _ptr(status), _stream(dev)))
+    rc = lib().sd_distill_topk_step(
+        student.data_ptr(), rs, dt, lp, ip, tp, wp, N, V, K, T,
+        loss.data_ptr(), lse.data_ptr(), grad.data_ptr(), gs, _ptr(status),
+        _raw_stream(dev))
+    if rc != SD_OK:
+        _check(rc)
     return {"loss": loss, "lse": lse, "grad": grad}

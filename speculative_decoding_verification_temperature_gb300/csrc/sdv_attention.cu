@@ -1035,33 +1035,48 @@ attention_join_kernel(const __grid_constant__ AttnParams p) {
   auto slot = [&](int k) {
     return ((long long)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * ROWS + r;
   };
-  float m = -kInf;
-  for (int k = lane; k < cut.parts; k += 32)
-    m = fmaxf(m, p.part_ml[slot(k)].x);
+  constexpr int E = D / 32;
+  auto part = [&](int k) {
+    return k < cut.parts ? p.part_ml[slot(k)] : make_float2(-kInf, 0.f);
+  };
+  float2 ml = part(lane);
+  float m = ml.x;
+  for (int k = lane + 32; k < cut.parts; k += 32) m = fmaxf(m, part(k).x);
 #pragma unroll
   for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-  constexpr int E = D / 32;
   float l = 0.f, o[E] = {};
-#pragma unroll 4
-  for (int k = 0; k < cut.parts; ++k) {
-    const long long at = slot(k);
-    const float2 ml = p.part_ml[at];
+  for (int k0 = 0; k0 < cut.parts; k0 += 32) {
+    if (k0) ml = part(k0 + lane);
+    // lane k has the weight of part k0 + k: 0 for one that saw nothing (or
+    // is none), NaN for one with a NaN sum
     const float w = ml.x == -kInf ? (ml.y == ml.y ? 0.f : ml.y)
                                   : ex2(ml.x - m);
-    l = fmaf(ml.y, w, l);
-    const float *src = p.part_o + at * D + lane * E;
-    if constexpr (E == 4) {
-      const float4 x = *reinterpret_cast<const float4 *>(src);
-      o[0] = fmaf(x.x, w, o[0]);
-      o[1] = fmaf(x.y, w, o[1]);
-      o[2] = fmaf(x.z, w, o[2]);
-      o[3] = fmaf(x.w, w, o[3]);
-    } else {
-      const float2 x = *reinterpret_cast<const float2 *>(src);
-      o[0] = fmaf(x.x, w, o[0]);
-      o[1] = fmaf(x.y, w, o[1]);
+    l += ml.y * w;
+    const int n = min(cut.parts - k0, 32);
+    for (int k = 0; k < n; k += 2) {
+      float x[2][E];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float *src =
+            p.part_o + slot(min(k0 + k + i, cut.parts - 1)) * D + lane * E;
+        if constexpr (E == 4) {
+          const float4 v = *reinterpret_cast<const float4 *>(src);
+          x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2 *>(src);
+          x[i][0] = v.x, x[i][1] = v.y;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float wk = __shfl_sync(~0u, w, k + i);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(x[i][e], wk, o[e]);
+      }
     }
   }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
   const int at = cut.first + r, tok = div_by(at, p.by_G);
   const long long row = (long long)(cut.start + tok) * p.Hq +
                         cut.head * p.G + (at - tok * p.G);
@@ -1172,6 +1187,8 @@ sd_status launch(AttnParams &p, const CUtensorMap &k_map,
   sd_status st = launch_pdl(kernel, grid, kAttnThreads,
                             attn_smem<D, PAIR>(), s, args);
   if (st != SD_OK) return st;
+  // a sequence whose table holds one key tile has no unit that can be cut
+  if ((long long)p.max_pages * p.page_size <= kTile) return SD_OK;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, L::kRows / kWarps, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
