@@ -312,30 +312,6 @@ template <int D, bool PAIR> constexpr size_t attn_smem() {
   return Layout<D, PAIR>::kTiles + sizeof(Shared<D, PAIR>);
 }
 
-// A bounded wait; after a failure anywhere in the CTA every wait gives up.
-constexpr unsigned kAttnWaitLimit = 1u << 22;
-__device__ __forceinline__ bool attn_wait(uint64_t *bar, uint32_t parity,
-                                          volatile int *abort,
-                                          int32_t *dev_status) {
-  for (unsigned it = 0; it < kAttnWaitLimit; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 255) == 255 && *abort) return false;
-  }
-  *abort = 1;
-  status_or(dev_status, SD_DEV_TIMEOUT);
-  return false;
-}
-
-// A position in a ring of n slots: the slot, and the parity of its filling.
-struct RingAt {
-  int slot, n;
-  uint32_t parity;
-  __device__ RingAt(int n_) : slot(0), n(n_), parity(0) {}
-  __device__ void next() {
-    if (++slot == n) slot = 0, parity ^= 1;
-  }
-};
-
 // A barrier of the two softmax warpgroups alone.
 __device__ __forceinline__ void streams_sync() {
   asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -349,24 +325,6 @@ __device__ __forceinline__ void st_v8(void *to, const uint32_t *x) {
       "st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to),
       SDV_I8(x, 0)
       : "memory");
-}
-
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
-      : "=l"(reinterpret_cast<uint64_t &>(d))
-      : "l"(reinterpret_cast<uint64_t &>(a)),
-        "l"(reinterpret_cast<uint64_t &>(b)),
-        "l"(reinterpret_cast<uint64_t &>(c)));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<uint64_t &>(d))
-      : "l"(reinterpret_cast<uint64_t &>(a)),
-        "l"(reinterpret_cast<uint64_t &>(b)));
-  return d;
 }
 
 template <class T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
@@ -512,7 +470,7 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
       if (hf || !first) {
         // a half's sums are complete when the last half's before it are
         const bool fine =
-            attn_wait(&o_full[hf ^ 1], parity ^ (hf ^ 1), abort, dev_status);
+            role_wait(&o_full[hf ^ 1], parity ^ (hf ^ 1), abort, dev_status);
         if (!__all_sync(~0u, fine)) return false;
         tmem_fence_after();
 #pragma unroll 1
@@ -617,7 +575,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
       unsigned filled = 0;
       int page = 0, tok = 0;
       auto load = [&](const CUtensorMap *map) {
-        fine = attn_wait(&s.empty[me][at.slot], at.parity ^ 1, &s.abort,
+        fine = role_wait(&s.empty[me][at.slot], at.parity ^ 1, &s.abort,
                          p.dev_status);
         if (!__all_sync(~0u, fine)) {
           fine = false;
@@ -685,7 +643,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
     RingAt &k_at = ring_k, &v_at = PAIR ? ring_v : ring_k;
     uint32_t wp = 0, qp = 0;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-      fine = fine && attn_wait(bar, parity, &s.abort, p.dev_status);
+      fine = fine && role_wait(bar, parity, &s.abort, p.dev_status);
     };
     // S against the next key tile
     auto wait_k = [&] { wait(&s.full[kr][k_at.slot], k_at.parity); };
@@ -882,7 +840,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
                  tmem + lanes + 2 * kTile + st * D, sl, -kInf, 0.f};
       for (int i = 0; i < cnt; ++i, ++tn) {
         const int j = u.j0 + (PAIR ? i : 2 * i + st);
-        fine = attn_wait(&s.s_full[st], tn & 1, &s.abort, p.dev_status);
+        fine = role_wait(&s.s_full[st], tn & 1, &s.abort, p.dev_status);
         if (!__all_sync(~0u, fine)) { fine = false; break; }
         if (warp_rows) {
           tmem_fence_after();
@@ -917,7 +875,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
       // way while this one's rows are written
       if (PAIR && next.left) load_q(next);
       if (cnt > 0) {
-        fine = attn_wait(&s.o_full[st][1], (tn - 1) & 1, &s.abort,
+        fine = role_wait(&s.o_full[st][1], (tn - 1) & 1, &s.abort,
                          p.dev_status);
         if (!__all_sync(~0u, fine)) { fine = false; break; }
         tmem_fence_after();

@@ -14,6 +14,8 @@
 // A row is cut into 16-byte slots by address, whatever its own alignment:
 // only its first and last slot can be partial, and those alone are read and
 // written by the element.
+#include <atomic>
+
 #include "sdv_device.cuh"
 #include "sdv_host.cuh"
 #include "sdv_tma.cuh"
@@ -22,9 +24,7 @@ namespace sdv {
 namespace {
 
 constexpr float kLn2 = 0.693147180559945f;
-constexpr int kSlotsPerCopy = 1024;  // 16 KB a bulk copy
-constexpr int kMaxCopies = 5;        // a step's slice of a row
-constexpr int kBatch = 8;            // slots a thread has in flight
+constexpr int kBatch = 8;         // slots a thread has in flight
 
 struct DistillParams {
   const void *student;
@@ -42,11 +42,11 @@ struct DistillParams {
 };
 
 // A row as 16-byte slots from the aligned address at or before its start:
-// column j is element head + j.
+// column j is element head + j; slots [f0, f1) are whole.
 template <int DT> struct SlotRow {
   static constexpr int VW = vec_width<DT>();
   const char *base;
-  int head, V, slots;
+  int head, V, slots, f0, f1;
   __device__ SlotRow(const void *rows, long long stride, int row, int V_)
       : V(V_) {
     const char *start =
@@ -54,9 +54,11 @@ template <int DT> struct SlotRow {
     head = (int)(reinterpret_cast<uintptr_t>(start) & 15) / elt_bytes<DT>();
     base = start - head * elt_bytes<DT>();
     slots = (head + V + VW - 1) / VW;
+    f0 = head > 0;
+    f1 = max((head + V) / VW, f0);
   }
   __device__ bool full(int s) const {
-    return (s > 0 || head == 0) && (s + 1) * VW <= head + V;
+    return (unsigned)(s - f0) < (unsigned)(f1 - f0);
   }
   __device__ int first_col(int s) const { return s * VW - head; }
 };
@@ -71,7 +73,7 @@ __device__ __forceinline__ uint4 ld_v4(const void *p) {
 
 // A partial slot by the element; columns outside the row are -inf.
 template <int DT>
-__device__ Raw<DT, vec_width<DT>()> load_partial(const SlotRow<DT> &r, int s) {
+__device__ __noinline__ Raw<DT, vec_width<DT>()> load_partial(const SlotRow<DT> &r, int s) {
   uint32_t w[4] = {};
   const int c0 = r.first_col(s);
   for (int e = 0; e < r.VW; ++e) {
@@ -121,43 +123,80 @@ __device__ __forceinline__ void store_elt(void *row, int j, float x) {
   }
 }
 
-// Gradients of a slot: c 2^(z k2 + nl2) of its columns (c alone scales).
+// c 2^(z k2 + nl2) of a slot's columns, as the row's type.
 template <int DT>
-__device__ __forceinline__ void store_slot(
-    const SlotRow<DT> &r, char *grad, bool aligned, int s,
+__device__ __forceinline__ uint4 slot_grad(
     const Raw<DT, vec_width<DT>()> &x, float c, float k2, float nl2) {
-  float g[SlotRow<DT>::VW];
+  constexpr int VW = vec_width<DT>();
+  const uint32_t in[4] = {x.w.x, x.w.y, x.w.z, x.w.w};
+  uint32_t out[4];
+  const float2 kk = make_float2(k2, k2), nn = make_float2(nl2, nl2),
+               cc = make_float2(c, c);
 #pragma unroll
-  for (int e = 0; e < r.VW; ++e)
-    g[e] = c * ex2(fmaf(elt<DT, SlotRow<DT>::VW>(x, e), k2, nl2));
-  const int c0 = r.first_col(s);
-  if (aligned && r.full(s)) {
-    uint4 w;
+  for (int e = 0; e < VW; e += 2) {
+    float2 z = DT == 0 ? make_float2(__uint_as_float(in[e % 4]),
+                                     __uint_as_float(in[(e + 1) % 4]))
+                       : make_float2(__uint_as_float(in[e / 2] << 16),
+                                     __uint_as_float(in[e / 2] & 0xffff0000u));
+    z = fma2(z, kk, nn);
+    z.x = ex2(z.x);
+    z.y = ex2(z.y);
+    z = mul2(z, cc);
     if constexpr (DT == 0) {
-      w = make_uint4(__float_as_uint(g[0]), __float_as_uint(g[1]),
-                     __float_as_uint(g[2]), __float_as_uint(g[3]));
+      out[e % 4] = __float_as_uint(z.x);
+      out[(e + 1) % 4] = __float_as_uint(z.y);
     } else {
-      uint32_t u[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-            : "=r"(u[e])
-            : "f"(g[2 * e + 1]), "f"(g[2 * e]));
-      w = make_uint4(u[0], u[1], u[2], u[3]);
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
+          : "=r"(out[e / 2])
+          : "f"(z.y), "f"(z.x));
     }
-    *reinterpret_cast<uint4 *>(grad + (long long)c0 * elt_bytes<DT>()) = w;
-  } else {
-    for (int e = 0; e < r.VW; ++e)
-      if (c0 + e >= 0 && c0 + e < r.V) store_elt<DT>(grad, c0 + e, g[e]);
+  }
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// The columns of slot s that lie in the row, by the element.
+template <int DT>
+__device__ __noinline__ void store_partial(const SlotRow<DT> &r, char *grad,
+                                           int s, uint4 g) {
+  const uint32_t w[4] = {g.x, g.y, g.z, g.w};
+  const int c0 = r.first_col(s);
+  for (int e = 0; e < r.VW; ++e) {
+    if (c0 + e < 0 || c0 + e >= r.V) continue;
+    if (DT == 0) ((uint32_t *)grad)[c0 + e] = w[e % 4];
+    else
+      ((unsigned short *)grad)[c0 + e] =
+          (unsigned short)(w[e / 2] >> (16 * (e & 1)));
   }
 }
 
+// Where a row's gradient goes: slot by slot where it lies like the student's
+// row (`like`), else by the element.
+template <int DT> struct GradRow {
+  char *row, *slots;
+  bool like;
+  __device__ GradRow(void *grad, long long stride, int n,
+                     const SlotRow<DT> &r) {
+    row = (char *)grad + (long long)n * stride * elt_bytes<DT>();
+    slots = row - r.head * elt_bytes<DT>();
+    like = (reinterpret_cast<uintptr_t>(slots) & 15) == 0;
+  }
+  __device__ __forceinline__ void store(const SlotRow<DT> &r, int s,
+                                        uint4 g) const {
+    if (like && r.full(s))
+      *reinterpret_cast<uint4 *>(slots + (long long)s * 16) = g;
+    else
+      store_partial(r, row, s, g);
+  }
+};
+
 // The teacher's entries of one row, in shared memory: id (-1: padding or
-// p = 0 by a logit of -inf), p, log2 p, and P (NaN: unusable entries).
+// p = 0 by a logit of -inf), p, log2 p, the student's logit at the id, and P
+// (NaN: unusable entries).
 struct Teacher {
   int id[SD_MAX_DISTILL_K];
   float p[SD_MAX_DISTILL_K];
   float log2p[SD_MAX_DISTILL_K];
+  float at[SD_MAX_DISTILL_K];
   float P;
 };
 
@@ -219,23 +258,37 @@ __device__ void normalise(const DistillParams &p, int row, Teacher &t) {
   if (lane == 0) t.P = P;
 }
 
-// Read and normalise a row's entries (one warp).
-__device__ void load_teacher(const DistillParams &p, int row, Teacher &t) {
-  for (int k = threadIdx.x & 31; k < p.K; k += 32)
+// Read and normalise a row's entries, and fetch the student's logits at the
+// ids in [lo, hi) (one warp).
+template <int DT>
+__device__ void load_teacher(const DistillParams &p, int row, Teacher &t,
+                             const SlotRow<DT> &r, int lo, int hi) {
+  const int lane = threadIdx.x & 31;
+  for (int k = lane; k < p.K; k += 32)
     put_entry(p, t, k, __ldg(p.id + (long long)row * p.K + k),
               __ldg(p.logit + (long long)row * p.K + k));
   __syncwarp();
+  constexpr int MOST = SD_MAX_DISTILL_K / 32;
+  float z[MOST];  // on their way while the entries are normalised
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    const int k = lane + 32 * i;
+    const int id = k < p.K ? t.id[k] : -1;
+    z[i] = id >= lo && id < hi ? load_col(r, id) : 0.f;
+  }
   normalise(p, row, t);
+#pragma unroll
+  for (int i = 0; i < MOST; ++i)
+    if (lane + 32 * i < p.K) t.at[lane + 32 * i] = z[i];
 }
 
 // The columns of the entries with ids in [lo, hi), over what the pass over
 // the row wrote: the first entry of an id writes for all that repeat it.
-// at: the student's logits at the ids.
 template <int DT>
 __device__ void store_entries(const DistillParams &p, const Teacher &t,
-                              char *grad, int lo, int hi, const float *at,
-                              float c, float P, float nl2) {
-  for (int k = threadIdx.x; k < p.K; k += kThreads) {
+                              char *grad, int lo, int hi, float c, float P,
+                              float nl2, int threads) {
+  for (int k = threadIdx.x; k < p.K; k += threads) {
     const int id = t.id[k];
     if (id < lo || id >= hi) continue;
     float sum = 0.f;
@@ -246,77 +299,83 @@ __device__ void store_entries(const DistillParams &p, const Teacher &t,
         sum += t.p[i];
       }
     if (first)
-      store_elt<DT>(grad, id, c * (P * ex2(fmaf(at[k], p.k2, nl2)) - sum));
+      store_elt<DT>(grad, id, c * (P * ex2(fmaf(t.at[k], p.k2, nl2)) - sum));
   }
 }
 
-// (max, sum) of a row's slots: this thread's part in, the cluster's out.
-// Every CTA merges the parts in rank order.  A CTA that is a row ahead may
-// not change what a peer still reads: rows alternate between the two `mine`.
-struct RowReduce {
-  MS part[kWarps], mine[2];
-};
-__device__ __forceinline__ MS reduce_row(MS st, float k2, int CL,
-                                         RowReduce &red, int which,
-                                         cg::cluster_group &cluster) {
-  const int tid = threadIdx.x;
-  st = warp_down_ms(st, k2);
-  if ((tid & 31) == 0) red.part[tid >> 5] = st;
-  __syncthreads();
-  if (tid == 0) {
-    st = red.part[0];
-    for (int i = 1; i < kWarps; ++i) st = ms_merge(st, red.part[i], k2);
-    red.mine[which] = st;
-  }
-  cluster.sync();
-  st = ms_empty();
-  for (int i = 0; i < CL; ++i)
-    st = ms_merge(st, *cluster.map_shared_rank(&red.mine[which], i), k2);
-  return st;
-}
+// The forward call and the step: a cluster of CL CTAs per row, a contiguous
+// run of its slots each, in batches of kRowThreads kBatch slots.
+//
+// The step goes over its run twice and keeps what it can of it in between:
+// the first kKept slots in shared memory and the last batch in registers
+// (each thread its own, so nothing is waited for), and it reads the rest,
+// newest first, once more.  Two CTAs on an SM, each with a row, keep HBM
+// busy through each other's reductions.
+constexpr int kRowThreads = 512;
+constexpr int kKept = 6272;  // 98 KB a CTA
 
-// The forward call: a cluster of CL CTAs per row, a contiguous run of its
-// slots each.
-template <int DT>
-__global__ void __launch_bounds__(kThreads)
-distill_forward_kernel(const __grid_constant__ DistillParams p) {
-  constexpr int VW = vec_width<DT>();
+template <int DT, bool STEP>
+__global__ void __launch_bounds__(kRowThreads, 2)
+distill_row_kernel(const __grid_constant__ DistillParams p) {
+  constexpr int VW = vec_width<DT>(), WARPS = kRowThreads / 32;
+  constexpr int RUN = kRowThreads * kBatch;
+  extern __shared__ __align__(16) char dyn[];
   __shared__ Teacher t;
-  __shared__ float at[SD_MAX_DISTILL_K];
-  __shared__ RowReduce red;
+  __shared__ MS part[WARPS], mine;
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = (int)cluster.block_rank();
+  const int rank = p.CL > 1 ? (int)cluster.block_rank() : 0;
   const int row = blockIdx.x / p.CL;
   const SlotRow<DT> r(p.student, p.row_stride, row, p.V);
   const int s0 = (int)((long long)r.slots * rank / p.CL);
   const int s1 = (int)((long long)r.slots * (rank + 1) / p.CL);
-  const float k2 = p.k2;
-  if (rank == 0 && warp == kWarps - 1) {
-    load_teacher(p, row, t);
-    __syncwarp();
-    for (int k = lane; k < p.K; k += 32)
-      at[k] = t.id[k] >= 0 ? load_col(r, t.id[k]) : 0.f;
-  }
+  const float k2 = p.k2, nan = __int_as_float(0x7fc00000);
+  uint4 *kept = reinterpret_cast<uint4 *>(dyn);
+  const int batches = (s1 - s0 + RUN - 1) / RUN;
+  Raw<DT, VW> x[kBatch];
+  // before anything is written (the gradient may go to the student's rows)
+  if (warp == WARPS - 1 && (rank == 0 || STEP))
+    load_teacher(p, row, t, r, 0, p.V);
   MS st = ms_empty();
   float vmax;
-  for (int s = s0 + tid; s < s1; s += kThreads * kBatch) {
-    Raw<DT, VW> x[kBatch];
+  for (int b = 0; b < batches; ++b) {
+    const int n = b * RUN + tid;
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      if (s + i * kThreads < s1) x[i] = load_slot(r, s + i * kThreads);
+      if (s0 + n + i * kRowThreads < s1)
+        x[i] = load_slot(r, s0 + n + i * kRowThreads);
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      if (s + i * kThreads < s1) ms_add_v<DT, VW>(st, x[i], k2, vmax);
+      if (s0 + n + i * kRowThreads < s1) {
+        ms_add_v<DT, VW>(st, x[i], k2, vmax);
+        if (STEP && n + i * kRowThreads < kKept && b + 1 < batches)
+          kept[n + i * kRowThreads] = x[i].w;
+      }
   }
-  st = reduce_row(st, k2, p.CL, red, 0, cluster);
+  st = warp_down_ms(st, k2);
+  if (lane == 0) part[warp] = st;
+  __syncthreads();
+  if (p.CL == 1) {
+    st = part[0];
+    for (int i = 1; i < WARPS; ++i) st = ms_merge(st, part[i], k2);
+  } else {
+    if (tid == 0) {
+      st = part[0];
+      for (int i = 1; i < WARPS; ++i) st = ms_merge(st, part[i], k2);
+      mine = st;
+    }
+    cluster.sync();
+    st = ms_empty();
+    for (int i = 0; i < p.CL; ++i)
+      st = ms_merge(st, *cluster.map_shared_rank(&mine, i), k2);
+  }
+  const float ls = log2f(st.s);
   if (rank == 0 && warp == 0) {
-    const float ls = log2f(st.s), nan = __int_as_float(0x7fc00000);
     const bool ok = ms_valid(st) && t.P == t.P;
     float a = 0.f;
     for (int k = lane; k < p.K; k += 32)
       if (t.id[k] >= 0 && t.p[k] > 0.f)
-        a += t.p[k] * (t.log2p[k] - ((at[k] - st.m) * k2 - ls));
+        a += t.p[k] * (t.log2p[k] - ((t.at[k] - st.m) * k2 - ls));
     a = warp_down_sum(a);
     if (lane == 0) {
       p.loss[row] = ok ? a * kLn2 : nan;
@@ -324,230 +383,283 @@ distill_forward_kernel(const __grid_constant__ DistillParams p) {
       if (!ok) status_or(p.dev_status, SD_DEV_NONFINITE);
     }
   }
-  cluster.sync();  // peers have read `red`
+  if constexpr (STEP) {
+    const float w = __ldg(p.grad_loss + row), P = t.P;
+    const bool ok = ms_valid(st) && P == P;
+    const float c = ok ? w * p.inv_T : nan, nl2 = -(st.m * k2 + ls);
+    const GradRow<DT> grad(p.grad, p.grad_stride, row, r);
+    for (int b = batches - 1; b >= 0; --b) {
+      const int n = b * RUN + tid;
+      if (b + 1 < batches) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int at = n + i * kRowThreads;
+          if (at < kKept) x[i].w = kept[at];
+          else if (s0 + at < s1) x[i] = load_slot(r, s0 + at);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int s = s0 + n + i * kRowThreads;
+        if (s >= s1) continue;
+        // a weight of 0: zeros, whatever the row holds
+        const uint4 g = slot_grad<DT>(x[i], c * P, k2, nl2);
+        grad.store(r, s, w == 0.f ? make_uint4(0, 0, 0, 0) : g);
+      }
+    }
+    if (w != 0.f) {
+      __syncthreads();
+      store_entries<DT>(p, t, grad.row, max(0, r.first_col(s0)),
+                        min(p.V, r.first_col(s1)), c, P, nl2, kRowThreads);
+    }
+  }
+  if (p.CL > 1) cluster.sync();  // peers have read `mine`
 }
 
-// The step: clusters of CL CTAs take rows in turn and keep a row in their
-// shared memory (bulk copies of up to 16 KB, a barrier each) from the pass
-// that finds log sum exp to the pass that writes the gradient.  The second
-// pass hands a copy's space to the next row as soon as it has used it, so
-// loads and stores overlap within a CTA as well as between the three on an
-// SM; the next row's teacher entries are fetched a row ahead.
+// The step where there are rows enough to fill the GPU: clusters of CL CTAs,
+// one CTA an SM, take rows in turn, a contiguous run of a row's slots each.
+// A row stays in shared memory from the pass that finds log sum exp to the
+// pass that writes the gradient, so HBM sees each byte once.  A loading warp
+// keeps a ring of 16 KB chunks full, across rows: while a row's sums are
+// exchanged and its gradient is written, the next one arrives.  A second
+// warp has the teacher's entries of the next row ready; sixteen warps do the
+// two passes.
+constexpr int kChunk = 1024;      // slots
+constexpr int kRing = 13;         // chunks, 208 KB
+constexpr int kMostChunks = 9;    // of a run: the rest of the ring runs ahead
+constexpr int kStepWarps = 16;
+constexpr int kStepThreads = 32 * (kStepWarps + 2);
+
+struct StepShared {
+  uint64_t full[kRing], empty[kRing];
+  uint64_t t_full[2], t_empty[2], sum_full[2];
+  volatile int abort;
+  MS part[kStepWarps];
+  alignas(8) MS sums[2][8];  // of the cluster's CTAs, two rows' worth
+  Teacher t[2];
+};
+
+__device__ __forceinline__ void step_sync() {  // the sixteen warps
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * kStepWarps) : "memory");
+}
+
 template <int DT>
-__global__ void __launch_bounds__(kThreads)
-distill_step_kernel(const __grid_constant__ DistillParams p) {
+__global__ void __launch_bounds__(kStepThreads, 1)
+distill_step_kernel(const __grid_constant__ DistillParams p, int chunks) {
   constexpr int VW = vec_width<DT>();
-  extern __shared__ __align__(16) char kept[];
-  __shared__ Teacher t;
-  __shared__ float at[SD_MAX_DISTILL_K], entry_loss[2];
-  __shared__ RowReduce red;
-  __shared__ uint64_t bar[kMaxCopies];
+  extern __shared__ __align__(16) char dyn[];
+  uint4 *ring = reinterpret_cast<uint4 *>(dyn);
+  StepShared &s =
+      *reinterpret_cast<StepShared *>(dyn + kRing * kChunk * 16);
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster.block_rank();
   const int clusters = gridDim.x / p.CL;
+  const int first = blockIdx.x / p.CL;
   const float k2 = p.k2, nan = __int_as_float(0x7fc00000);
-  uint4 *slot = reinterpret_cast<uint4 *>(kept);
-  // this CTA's run of a row's slots; [f0, f1) are whole
-  struct Run {
-    int s0, s1, f0, f1;
-  };
-  auto run_of = [&](const SlotRow<DT> &r) {
-    Run u;
-    u.s0 = (int)((long long)r.slots * rank / p.CL);
-    u.s1 = (int)((long long)r.slots * (rank + 1) / p.CL);
-    u.f0 = u.s0 + (u.s1 > u.s0 && !r.full(u.s0));
-    u.f1 = u.s1 - (u.s1 > u.f0 && !r.full(u.s1 - 1));
-    return u;
-  };
-  // copy i of a row (thread 0)
-  auto fetch = [&](const SlotRow<DT> &r, const Run &u, int i) {
-    const int a = max(u.s0 + i * kSlotsPerCopy, u.f0);
-    const int b = min(u.s0 + (i + 1) * kSlotsPerCopy, u.f1);
-    const uint32_t bytes = b > a ? (uint32_t)(b - a) * 16 : 0;
-    mbar_expect_tx(&bar[i], bytes);
-    if (bytes)
-      bulk_g2s_hint(slot + (a - u.s0), r.base + (long long)a * 16, bytes,
-                    &bar[i], l2_evict_first_policy());
-  };
   if (tid == 0) {
-    for (int i = 0; i < kMaxCopies; ++i) mbar_init(&bar[i], 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&s.full[i], 1);
+      mbar_init(&s.empty[i], kStepWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s.t_full[i], 1);
+      mbar_init(&s.t_empty[i], kStepWarps);
+      mbar_init(&s.sum_full[i], 1);
+    }
+    s.abort = 0;
     fence_mbar_init();
   }
-  __syncthreads();
-  int row = blockIdx.x / p.CL;
-  SlotRow<DT> r(p.student, p.row_stride, row, p.V);
-  Run u = run_of(r);
-  if (tid == 0)
-    for (int i = 0; i < kMaxCopies; ++i) fetch(r, u, i);
-  auto entry_of = [&](int n, int &id, float &z) {
-    id = -1;
-    z = 0.f;
-    if (n < p.N && tid < p.K) {
-      id = __ldg(p.id + (long long)n * p.K + tid);
-      z = __ldg(p.logit + (long long)n * p.K + tid);
-    }
+  cluster.sync();  // the peers' barriers are there
+  bool fine = true;
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    fine = __all_sync(~0u, fine && role_wait(bar, parity, &s.abort,
+                                             p.dev_status));
   };
-  static_assert(SD_MAX_DISTILL_K <= kThreads, "an entry a thread");
-  int id;
-  float z;
-  entry_of(row, id, z);
-  uint32_t parity = 0;
-  int last = -1;  // the row whose loss is being added up
-  bool last_ok = false;
-  // rank 0, after a cluster barrier: the loss of row `last`
-  auto finish_loss = [&] {
-    if (rank == 0 && warp == 0 && last >= 0) {
-      float a = lane < p.CL
-                    ? *cluster.map_shared_rank(&entry_loss[parity ^ 1], lane)
-                    : 0.f;
-      a = warp_down_sum(a);
-      if (lane == 0) p.loss[last] = last_ok ? a * kLn2 : nan;
-    }
-  };
-  for (; row < p.N; row += clusters) {
-    const int n = u.s1 - u.s0;
-    if (tid < p.K) put_entry(p, t, tid, id, z);
-    entry_of(row + clusters, id, z);
-    if (tid == 32 && u.f0 > u.s0) slot[0] = load_partial(r, u.s0).w;
-    if (tid == 64 && u.f1 < u.s1) slot[n - 1] = load_partial(r, u.s1 - 1).w;
-    __syncthreads();
-    if (warp == kWarps - 1) normalise(p, row, t);
-    MS st = ms_empty();
-    float vmax;
-    for (int i = 0; i < kMaxCopies; ++i) {
-      mbar_wait(&bar[i], parity, p.dev_status);
-      const int b = min((i + 1) * kSlotsPerCopy, n);
-#pragma unroll 4
-      for (int s = i * kSlotsPerCopy + tid; s < b; s += kThreads) {
-        Raw<DT, VW> x;
-        x.w = slot[s];
-        ms_add_v<DT, VW>(st, x, k2, vmax);
+
+  if (warp == kStepWarps) {
+    // ---- loads
+    RingAt at(kRing);
+    unsigned filled = 0;
+    for (int row = first; row < p.N && fine; row += clusters) {
+      const SlotRow<DT> r(p.student, p.row_stride, row, p.V);
+      const int s0 = (int)((long long)r.slots * rank / p.CL);
+      const int s1 = (int)((long long)r.slots * (rank + 1) / p.CL);
+      for (int i = 0; i < chunks; ++i) {
+        wait(&s.empty[at.slot], at.parity ^ 1);
+        if (!fine) break;
+        if (lane == 0) {
+          const int a = max(s0 + i * kChunk, r.f0);
+          const int b = min(min(s0 + (i + 1) * kChunk, s1), r.f1);
+          const uint32_t bytes = b > a ? (uint32_t)(b - a) * 16 : 0;
+          mbar_expect_tx(&s.full[at.slot], bytes);
+          if (bytes)
+            bulk_g2s_hint(ring + at.slot * kChunk + (a - s0 - i * kChunk),
+                          r.base + (long long)a * 16, bytes,
+                          &s.full[at.slot], l2_evict_first_policy());
+        }
+        at.next();
+        ++filled;
       }
     }
-    st = reduce_row(st, k2, p.CL, red, parity, cluster);
-    finish_loss();
-    const float P = t.P;
-    const bool ok = ms_valid(st) && P == P;
-    const float ls = log2f(st.s);
-    const int lo = max(0, r.first_col(u.s0));
-    const int hi = min(p.V, r.first_col(u.s1));
-    // the entries in this run: their logits and their part of the loss
-    float a = 0.f;
-    if (tid < p.K && t.id[tid] >= lo && t.id[tid] < hi) {
-      const int c = t.id[tid] - r.first_col(u.s0);
-      const char *src = kept + (long long)c * elt_bytes<DT>();
-      const float x =
-          DT == 0 ? *reinterpret_cast<const float *>(src)
-                  : __uint_as_float(
-                        (uint32_t)*reinterpret_cast<const unsigned short *>(src)
-                        << 16);
-      at[tid] = x;
-      if (t.p[tid] > 0.f)
-        a = t.p[tid] * (t.log2p[tid] - ((x - st.m) * k2 - ls));
-    }
-    __shared__ float loss_part[kWarps];
-    a = warp_down_sum(a);
-    if (lane == 0) loss_part[warp] = a;
-    if (rank == 0 && tid == 0) {
-      p.lse[row] = ok ? (st.m * k2 + ls) * kLn2 : nan;
-      if (!ok) status_or(p.dev_status, SD_DEV_NONFINITE);
-    }
-    last = row;
-    last_ok = ok;
-    // the gradient, and the next row into the space of the copies used up
-    const float w = __ldg(p.grad_loss + row);
-    const float c = w == 0.f ? 0.f : ok ? w * p.inv_T : nan;
-    const float nl2 = -(st.m * k2 + ls);
-    char *grad =
-        (char *)p.grad + (long long)row * p.grad_stride * elt_bytes<DT>();
-    const bool aligned = ((reinterpret_cast<uintptr_t>(grad) & 15) /
-                          elt_bytes<DT>()) == (unsigned)r.head;
-    const SlotRow<DT> next(p.student, p.row_stride,
-                           min(row + clusters, p.N - 1), p.V);
-    const Run nu = run_of(next);
-    for (int i = 0; i < kMaxCopies; ++i) {
-      const int b = min((i + 1) * kSlotsPerCopy, n);
-#pragma unroll 4
-      for (int s = i * kSlotsPerCopy + tid; s < b; s += kThreads) {
-        Raw<DT, VW> x;
-        // a weight of 0: zeros, whatever the row holds
-        x.w = w == 0.f ? make_uint4(0, 0, 0, 0) : slot[s];
-        store_slot<DT>(r, grad, aligned, u.s0 + s, x, w == 0.f ? 0.f : c * P,
-                       w == 0.f ? 0.f : k2, w == 0.f ? 0.f : nl2);
+    if (!fine)  // give up: let the copies in flight land first
+      for (unsigned i = 0; i < kRing && i < filled; ++i) {
+        const unsigned last = (filled - 1 - i) / kRing;
+        for (unsigned it = 0; it < (1u << 20); ++it)
+          if (mbar_try_wait(&s.full[i], last & 1)) break;
       }
-      fence_proxy_async();
-      __syncthreads();
-      if (tid == 0 && row + clusters < p.N) fetch(next, nu, i);
+  } else if (warp == kStepWarps + 1) {
+    // ---- the teacher's entries, and the student's logits at their ids:
+    // before the row's sums leave this CTA, so before any CTA writes to the
+    // row (the gradient may go to the student's own rows)
+    RingAt at(2);
+    for (int row = first; row < p.N; row += clusters) {
+      wait(&s.t_empty[at.slot], at.parity ^ 1);
+      if (!fine) break;
+      const SlotRow<DT> r(p.student, p.row_stride, row, p.V);
+      load_teacher(p, row, s.t[at.slot], r, 0, p.V);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.t_full[at.slot]);
+      at.next();
     }
-    if (tid == 0) {
-      float sum = 0.f;
-      for (int i = 0; i < kWarps; ++i) sum += loss_part[i];
-      entry_loss[parity] = sum;
+  } else {
+    RingAt read(kRing), write(kRing), two(2);
+    for (int row = first; row < p.N; row += clusters) {
+      const SlotRow<DT> r(p.student, p.row_stride, row, p.V);
+      const int s0 = (int)((long long)r.slots * rank / p.CL);
+      const int s1 = (int)((long long)r.slots * (rank + 1) / p.CL);
+      // ---- log sum exp
+      MS st = ms_empty();
+      float vmax;
+      for (int i = 0; i < chunks; ++i) {
+        wait(&s.full[read.slot], read.parity);
+        if (!fine) break;
+        const uint4 *src = ring + read.slot * kChunk;
+        const int n = min(kChunk, s1 - s0 - i * kChunk);
+#pragma unroll
+        for (int k = 0; k < kChunk / (32 * kStepWarps); ++k) {
+          const int j = tid + k * 32 * kStepWarps;
+          if (j >= n) continue;
+          Raw<DT, VW> x;
+          if (r.full(s0 + i * kChunk + j)) x.w = src[j];
+          else x = load_partial(r, s0 + i * kChunk + j);
+          ms_add_v<DT, VW>(st, x, k2, vmax);
+        }
+        read.next();
+      }
+      if (!fine) break;
+      st = warp_down_ms(st, k2);
+      if (lane == 0) s.part[warp] = st;
+      wait(&s.t_full[two.slot], two.parity);
+      if (!fine) break;
+      step_sync();
+      if (warp == 0) {
+        st = lane < kStepWarps ? s.part[lane] : ms_empty();
+        st = warp_down_ms(st, k2);
+        st.m = __shfl_sync(~0u, st.m, 0);
+        st.s = __shfl_sync(~0u, st.s, 0);
+        if (lane == 0) mbar_expect_tx(&s.sum_full[two.slot], 8 * p.CL);
+        if (lane < p.CL)
+          st_async_pair(&s.sums[two.slot][rank], &s.sum_full[two.slot], lane,
+                        st.m, st.s);
+        __syncwarp();
+      }
+      wait(&s.sum_full[two.slot], two.parity);
+      if (!fine) break;
+      st = ms_empty();
+      for (int i = 0; i < p.CL; ++i)
+        st = ms_merge(st, s.sums[two.slot][i], k2);
+      const Teacher &t = s.t[two.slot];
+      const float P = t.P, ls = log2f(st.s), w = __ldg(p.grad_loss + row);
+      const bool ok = ms_valid(st) && P == P;
+      if (rank == 0 && warp == 0) {
+        float a = 0.f;
+        for (int k = lane; k < p.K; k += 32)
+          if (t.id[k] >= 0 && t.p[k] > 0.f)
+            a += t.p[k] * (t.log2p[k] - ((t.at[k] - st.m) * k2 - ls));
+        a = warp_down_sum(a);
+        if (lane == 0) {
+          p.loss[row] = ok ? a * kLn2 : nan;
+          p.lse[row] = ok ? (st.m * k2 + ls) * kLn2 : nan;
+          if (!ok) status_or(p.dev_status, SD_DEV_NONFINITE);
+        }
+        __syncwarp();
+      }
+      // ---- the gradient; each chunk is handed back as soon as it is used
+      const float c = ok ? w * p.inv_T : nan, nl2 = -(st.m * k2 + ls);
+      const GradRow<DT> grad(p.grad, p.grad_stride, row, r);
+      for (int i = 0; i < chunks; ++i) {
+        const uint4 *src = ring + write.slot * kChunk;
+        const int n = min(kChunk, s1 - s0 - i * kChunk);
+#pragma unroll
+        for (int k = 0; k < kChunk / (32 * kStepWarps); ++k) {
+          const int j = tid + k * 32 * kStepWarps, at = s0 + i * kChunk + j;
+          if (j >= n) continue;
+          Raw<DT, VW> x;
+          if (r.full(at)) x.w = src[j];
+          else x = load_partial(r, at);
+          // a weight of 0: zeros, whatever the row holds
+          const uint4 g = slot_grad<DT>(x, c * P, k2, nl2);
+          grad.store(r, at, w == 0.f ? make_uint4(0, 0, 0, 0) : g);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.empty[write.slot]);
+        write.next();
+      }
+      step_sync();
+      if (w != 0.f)
+        store_entries<DT>(p, t, grad.row, max(0, r.first_col(s0)),
+                          min(p.V, r.first_col(s1)), c, P, nl2,
+                          32 * kStepWarps);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.t_empty[two.slot]);
+      two.next();
     }
-    if (w != 0.f) store_entries<DT>(p, t, grad, lo, hi, at, c, P, nl2);
-    __syncthreads();  // t, at and the parts may change
-    r = next;
-    u = nu;
-    parity ^= 1;
   }
-  cluster.sync();
-  finish_loss();
-  cluster.sync();  // peers have read entry_loss
+  __syncwarp();
+  cluster.sync();  // nothing is on its way to a CTA that has ended
 }
 
-// The backward call: a CTA per row and run of kThreads kBatch slots.
+// The backward call: a CTA per row and run of kThreads kBatch slots, all of
+// them on their way before the teacher's chain of loads.
 template <int DT>
 __global__ void __launch_bounds__(kThreads)
 distill_backward_kernel(const __grid_constant__ DistillParams p) {
-  constexpr int VW = vec_width<DT>();
+  constexpr int VW = vec_width<DT>(), RUN = kThreads * kBatch;
   __shared__ Teacher t;
-  __shared__ float at[SD_MAX_DISTILL_K];
   const int row = blockIdx.x, tid = threadIdx.x;
   const SlotRow<DT> r(p.student, p.row_stride, row, p.V);
-  const int s0 = blockIdx.y * (kThreads * kBatch);
-  const int s1 = min(s0 + kThreads * kBatch, r.slots);
+  const int s0 = blockIdx.y * RUN, s1 = min(s0 + RUN, r.slots);
   if (s0 >= s1) return;
-  char *grad =
-      (char *)p.grad + (long long)row * p.grad_stride * elt_bytes<DT>();
-  const bool aligned = ((reinterpret_cast<uintptr_t>(grad) & 15) /
-                        elt_bytes<DT>()) == (unsigned)r.head;
+  const GradRow<DT> grad(p.grad, p.grad_stride, row, r);
   const float w = __ldg(p.grad_loss + row);
+  if (w == 0.f) {  // the row is not read
+    for (int s = s0 + tid; s < s1; s += kThreads)
+      grad.store(r, s, make_uint4(0, 0, 0, 0));
+    return;
+  }
   Raw<DT, VW> x[kBatch];
-  if (w != 0.f) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (s0 + tid + i * kThreads < s1)
-        x[i] = load_slot(r, s0 + tid + i * kThreads);
-  }
+  for (int i = 0; i < kBatch; ++i)
+    if (s0 + tid + i * kThreads < s1)
+      x[i] = load_slot(r, s0 + tid + i * kThreads);
   const int lo = max(0, r.first_col(s0)), hi = min(p.V, r.first_col(s1));
-  float P = 0.f, c = 0.f, nl2 = 0.f;
-  if (w != 0.f) {
-    if (tid < 32) load_teacher(p, row, t);
-    __syncthreads();
-    P = t.P;
-    const float lse = __ldg(p.lse_in + row);
-    const bool ok = P == P && fabsf(lse) < kInf;
-    if (!ok && tid == 0) status_or(p.dev_status, SD_DEV_NONFINITE);
-    c = ok ? w * p.inv_T : __int_as_float(0x7fc00000);
-    nl2 = -lse * (1.f / kLn2);
-    // before any of this CTA's columns is written
-    for (int k = tid; k < p.K; k += kThreads)
-      if (t.id[k] >= lo && t.id[k] < hi)
-        at[k] = load_col(r, t.id[k]);
-    __syncthreads();
-  }
+  if (tid < 32) load_teacher(p, row, t, r, lo, hi);
+  const float lse = __ldg(p.lse_in + row);
+  __syncthreads();
+  const float P = t.P;
+  const bool ok = P == P && fabsf(lse) < kInf;
+  if (!ok && tid == 0) status_or(p.dev_status, SD_DEV_NONFINITE);
+  const float c = ok ? w * p.inv_T : __int_as_float(0x7fc00000);
+  const float nl2 = -lse * (1.f / kLn2);
 #pragma unroll
   for (int i = 0; i < kBatch; ++i) {
     const int s = s0 + tid + i * kThreads;
-    if (s >= s1) continue;
-    if (w == 0.f) x[i].w = make_uint4(0, 0, 0, 0);
-    store_slot<DT>(r, grad, aligned, s, x[i], c * P, w == 0.f ? 0.f : p.k2,
-                   nl2);
+    if (s < s1) grad.store(r, s, slot_grad<DT>(x[i], c * P, p.k2, nl2));
   }
-  if (w == 0.f) return;
   __syncthreads();
-  store_entries<DT>(p, t, grad, lo, hi, at, c, P, nl2);
+  store_entries<DT>(p, t, grad.row, lo, hi, c, P, nl2, kThreads);
 }
 
 sd_status check_distill(const void *student, long long row_stride,
@@ -570,25 +682,83 @@ int max_slots(int V, sd_dtype dt) {
   return (V + 2 * vw - 2) / vw;
 }
 
-// CTAs per row of the forward call: enough for some eight on every SM, each
-// with at least 512 slots.
-int forward_cluster(int N, int slots, int sms) {
-  int cl = 1;
-  while (cl < 8 && (long long)N * cl < 4LL * sms && slots / (2 * cl) >= 512)
-    cl *= 2;
-  return cl;
+// The ring kernel, where a run fits and there are rows for every SM; *done
+// says whether it took the call.
+sd_status launch_step(DistillParams &p, sd_dtype dt, int sms, cudaStream_t s,
+                      bool *done) {
+  *done = false;
+  const int slots = max_slots(p.V, dt);
+  const int cl = (slots + kMostChunks * kChunk - 2) / (kMostChunks * kChunk - 1);
+  if (cl > 8 || (long long)p.N * cl < sms) return SD_OK;
+  int chunks = (slots / cl + 1 + kChunk - 1) / kChunk;
+  const void *kernel = dt == SD_F32 ? (const void *)distill_step_kernel<0>
+                                    : (const void *)distill_step_kernel<1>;
+  const size_t smem = (size_t)kRing * kChunk * 16 + sizeof(StepShared);
+  int resident = 0;
+  const sd_status st = max_active_clusters(kernel, cl, smem, &resident);
+  if (st != SD_OK) return st;
+  p.CL = cl;
+  const int clusters = p.N < resident ? p.N : resident;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(clusters * cl), 1, 1);
+  cfg.blockDim = dim3(kStepThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cl;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void *args[] = {&p, &chunks};
+  SDV_CUDA(cudaLaunchKernelExC(&cfg, kernel, args));
+  *done = true;
+  return SD_OK;
 }
 
-// CTAs per row of the step, 0 where a row does not fit their shared memory:
-// slices of at most 70 KB (three CTAs on an SM: one loads while another
-// writes), smaller ones while there are too few rows to fill the GPU.
-int step_cluster(int N, int slots, int sms) {
-  constexpr int kMost = 4480;
-  int cl = (slots + kMost - 1) / kMost;
-  if (cl > 16) return 0;
-  if (cl > 8) return 16;
-  while (cl <= 4 && (long long)N * cl < sms && slots / (2 * cl) >= 512) cl *= 2;
-  return cl;
+// In clusters of as many CTAs per row as it takes to fill the GPU, each with
+// at least 512 slots.
+template <bool STEP>
+sd_status launch_rows(DistillParams &p, sd_dtype dt, int sms,
+                      cudaStream_t s) {
+  const int slots = max_slots(p.V, dt);
+  int cl = 1;
+  while (cl < 8 && (long long)p.N * cl < 2LL * sms && slots / (2 * cl) >= 512)
+    cl *= 2;
+  p.CL = cl;
+  const void *kernel = dt == SD_F32 ? (const void *)distill_row_kernel<0, STEP>
+                                    : (const void *)distill_row_kernel<1, STEP>;
+  // a run of one batch stays in registers
+  const int run = slots / cl + 1;
+  const size_t smem =
+      STEP && run > kRowThreads * kBatch ? kKept * 16 : 0;
+  if (smem) {
+    int dev = 0;
+    SDV_CUDA(cudaGetDevice(&dev));
+    static std::atomic<unsigned long long> ready[2];
+    std::atomic<unsigned long long> &have = ready[dt == SD_F32 ? 0 : 1];
+    if (dev >= 64 || !(have.load() >> dev & 1)) {
+      SDV_CUDA(cudaFuncSetAttribute(
+          kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+      if (dev < 64) have.fetch_or(1ull << dev);
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)p.N * (unsigned)cl, 1, 1);
+  cfg.blockDim = dim3(kRowThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cl;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void *args[] = {&p};
+  SDV_CUDA(cudaLaunchKernelExC(&cfg, kernel, args));
+  return SD_OK;
 }
 
 DistillParams distill_params(const void *student, long long row_stride,
@@ -634,11 +804,7 @@ extern "C" sd_status sd_distill_topk(
   p.loss = loss;
   p.lse = lse;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const void *kernel = dt == SD_F32 ? (const void *)distill_forward_kernel<0>
-                                    : (const void *)distill_forward_kernel<1>;
-  p.CL = forward_cluster(N, max_slots(V, dt), sms);
-  void *args[] = {&p};
-  return launch_clusters(kernel, N, p.CL, 0, s, args);
+  return launch_rows<false>(p, dt, sms, s);
 }
 
 extern "C" sd_status sd_distill_topk_backward(
@@ -663,9 +829,9 @@ extern "C" sd_status sd_distill_topk_backward(
   p.grad_loss = grad_loss;
   p.grad = grad;
   p.grad_stride = grad_stride;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int run = kThreads * kBatch;
   const dim3 grid(N, (max_slots(V, dt) + run - 1) / run);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (dt == SD_F32) distill_backward_kernel<0><<<grid, kThreads, 0, s>>>(p);
   else distill_backward_kernel<1><<<grid, kThreads, 0, s>>>(p);
   SDV_CUDA(cudaGetLastError());
@@ -687,16 +853,6 @@ extern "C" sd_status sd_distill_topk_step(
   int sms = 0;
   st = check_device(&sms);
   if (st != SD_OK) return st;
-  const int slots = max_slots(V, dt), cl = step_cluster(N, slots, sms);
-  if (cl == 0) {  // rows too long to keep: read them twice
-    st = sd_distill_topk(student, row_stride, dt, teacher_logit, teacher_id,
-                         teacher_lse, N, V, K, T, loss, lse, dev_status,
-                         stream);
-    if (st != SD_OK) return st;
-    return sd_distill_topk_backward(
-        student, row_stride, dt, lse, teacher_logit, teacher_id, teacher_lse,
-        grad_loss, N, V, K, T, grad, grad_stride, dev_status, stream);
-  }
   DistillParams p =
       distill_params(student, row_stride, teacher_logit, teacher_id,
                      teacher_lse, N, V, K, T, dev_status);
@@ -705,14 +861,8 @@ extern "C" sd_status sd_distill_topk_step(
   p.grad_loss = grad_loss;
   p.grad = grad;
   p.grad_stride = grad_stride;
-  const void *kernel = dt == SD_F32 ? (const void *)distill_step_kernel<0>
-                                    : (const void *)distill_step_kernel<1>;
-  const size_t smem = (size_t)(slots / cl + 2) * 16;
-  int resident = 0;
-  st = max_active_clusters(kernel, cl, smem, &resident);
-  if (st != SD_OK) return st;
-  p.CL = cl;
-  void *args[] = {&p};
-  return launch_clusters(kernel, N < resident ? N : resident, cl, smem,
-                         static_cast<cudaStream_t>(stream), args);
+  bool done = false;
+  st = launch_step(p, dt, sms, static_cast<cudaStream_t>(stream), &done);
+  if (st != SD_OK || done) return st;
+  return launch_rows<true>(p, dt, sms, static_cast<cudaStream_t>(stream));
 }

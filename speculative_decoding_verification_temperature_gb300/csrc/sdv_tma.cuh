@@ -126,4 +126,48 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity,
   return false;
 }
 
+// The same with a limit for one CTA: after a failure anywhere in it every
+// wait gives up at once (`abort` in its shared memory), so that all roles of
+// a warp-specialised kernel leave their loops.
+constexpr unsigned kRoleWaitLimit = 1u << 22;
+__device__ __forceinline__ bool role_wait(uint64_t *bar, uint32_t parity,
+                                          volatile int *abort,
+                                          int32_t *dev_status) {
+  for (unsigned it = 0; it < kRoleWaitLimit; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 255) == 255 && *abort) return false;
+  }
+  *abort = 1;
+  status_or(dev_status, SD_DEV_TIMEOUT);
+  return false;
+}
+
+// A position in a ring of n slots: the slot, and the parity of its filling.
+struct RingAt {
+  int slot, n;
+  uint32_t parity;
+  __device__ RingAt(int n_) : slot(0), n(n_), parity(0) {}
+  __device__ void next() {
+    if (++slot == n) slot = 0, parity ^= 1;
+  }
+};
+
+// Store two words to the same place in CTA `rank` of the cluster and count
+// their eight bytes on its barrier there.
+__device__ __forceinline__ void st_async_pair(void *here, uint64_t *bar,
+                                              int rank, float a, float b) {
+  uint32_t to, tb;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;"
+      : "=r"(to)
+      : "r"(smem_addr(here)), "r"(rank));
+  asm("mapa.shared::cluster.u32 %0, %1, %2;"
+      : "=r"(tb)
+      : "r"(smem_addr(bar)), "r"(rank));
+  asm volatile(
+      "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], "
+      "{%1, %2}, [%3];" ::"r"(to),
+      "f"(a), "f"(b), "r"(tb)
+      : "memory");
+}
+
 }  // namespace sdv

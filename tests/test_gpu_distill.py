@@ -61,7 +61,8 @@ def check(z, V, logit, ids, tl, w, T, *, status=0, out=None):
 @pytest.mark.parametrize("N,V,K,T", [
     (1, 1, 1, 1.0), (1, 7, 7, 0.7), (3, 1000, 5, 1.0), (5, 1001, 16, 0.7),
     (2, 32000, 64, 2.0), (33, 4096, 50, 1.0), (2, 152064, 32, 1.0),
-    (200, 515, 3, 0.5), (1, 128256, 256, 1.0), (700, 2048, 8, 1.0)])
+    (200, 515, 3, 0.5), (1, 128256, 256, 1.0), (700, 2048, 8, 1.0),
+    (90, 128256, 20, 1.0), (170, 75001, 7, 0.7), (160, 9, 9, 1.0)])
 def test_sizes(dtype, full, N, V, K, T):
     z, lg, ids, tl, w = make(N, V, K, dtype, T, seed=N + V, full=full)
     check(z, V, lg, ids, tl, w, T)
@@ -221,3 +222,43 @@ def test_from_the_fan_out():
     assert (np.abs(ref.f64(s["loss"]) - r["loss"]) <= r["loss_tol"]).all()
     tol = r["grad_tol"] + 2 * ref.U32 * np.abs(r["grad"]) + 1e-38
     assert (np.abs(ref.f64(s["grad"]) - r["grad"]) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("V,stride", [(20000, 20000), (90001, 90001),
+                                      (74000, 74008)])
+def test_step_over_many_rows(dtype, V, stride):
+    """Rows enough that every SM takes several, weights of 0 and unusable rows
+    among them: the step's gradient is the backward call's with the step's own
+    log-sum-exp, and in place it is the same bits."""
+    N, K = 400, 12
+    g = torch.Generator(device="cuda").manual_seed(V)
+    z = torch.randn(N, stride, generator=g, device="cuda").to(dtype)[:, :V]
+    top = torch.randn(N, V, generator=g, device="cuda").topk(K, 1)
+    a = (top.values.contiguous(), top.indices.to(torch.int32))
+    w = torch.rand(N, generator=g, device="cuda")
+    w[::7] = 0
+    z[5, 3] = float("nan")
+    z[14, 9] = float("inf")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    s = api.distill_topk_step(z, *a, w, 0.9, status=st)
+    f = api.distill_topk(z, *a, 0.9)
+    b = api.distill_topk_backward(z, s["lse"], *a, w, 0.9)
+    torch.cuda.synchronize()
+    assert int(st.item()) == api.DEV_NONFINITE
+    bad = torch.zeros(N, dtype=torch.bool, device="cuda")
+    bad[[5, 14]] = True
+    for k in ("loss", "lse"):
+        assert bool((torch.isnan(s[k]) == bad).all())
+        x, y = s[k][~bad], f[k][~bad]
+        # the two sum in another order
+        assert bool(((x - y).abs() <= 1e-4 * (1 + y.abs())).all()), k
+    assert bool((s["grad"][w == 0] == 0).all())
+    assert bool(torch.isnan(s["grad"][5]).all())
+    rows = (~bad) & (w != 0)
+    x, y = s["grad"][rows].float(), b[rows].float()
+    tol = 2 * ref.U[dtype] + 1e-5
+    assert bool(((x - y).abs() <= tol * y.abs() + 1e-12).all())
+    again = api.distill_topk_step(z, *a, w, 0.9, out=z)["grad"]
+    assert again is z
+    assert torch.equal(torch.nan_to_num(z), torch.nan_to_num(s["grad"]))
