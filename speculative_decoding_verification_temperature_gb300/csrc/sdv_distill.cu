@@ -420,13 +420,13 @@ distill_row_kernel(const __grid_constant__ DistillParams p) {
 // one CTA an SM, take rows in turn, a contiguous run of a row's slots each.
 // A row stays in shared memory from the pass that finds log sum exp to the
 // pass that writes the gradient, so HBM sees each byte once.  A loading warp
-// keeps a ring of 16 KB chunks full, across rows: while a row's sums are
+// keeps a ring of 32 KB chunks full, across rows: while a row's sums are
 // exchanged and its gradient is written, the next one arrives.  A second
 // warp has the teacher's entries of the next row ready; sixteen warps do the
 // two passes.
-constexpr int kChunk = 1024;      // slots
-constexpr int kRing = 13;         // chunks, 208 KB
-constexpr int kMostChunks = 9;    // of a run: the rest of the ring runs ahead
+constexpr int kChunk = 2048;      // slots
+constexpr int kRing = 6;          // chunks, 192 KB
+constexpr int kMostChunks = 4;    // of a run: the rest of the ring runs ahead
 constexpr int kStepWarps = 16;
 constexpr int kStepThreads = 32 * (kStepWarps + 2);
 
@@ -534,20 +534,26 @@ distill_step_kernel(const __grid_constant__ DistillParams p, int chunks) {
       for (int i = 0; i < chunks; ++i) {
         wait(&s.full[read.slot], read.parity);
         if (!fine) break;
-        const uint4 *src = ring + read.slot * kChunk;
-        const int n = min(kChunk, s1 - s0 - i * kChunk);
+        const uint4 *src = ring + read.slot * kChunk + tid;
+        const int lo = max(0, r.f0 - s0 - i * kChunk);
+        const int hi = min(kChunk, min(s1, r.f1) - s0 - i * kChunk);
 #pragma unroll
-        for (int k = 0; k < kChunk / (32 * kStepWarps); ++k) {
-          const int j = tid + k * 32 * kStepWarps;
-          if (j >= n) continue;
+        for (int k = 0; k < kChunk; k += 32 * kStepWarps) {
+          if (tid + k < lo || tid + k >= hi) continue;
           Raw<DT, VW> x;
-          if (r.full(s0 + i * kChunk + j)) x.w = src[j];
-          else x = load_partial(r, s0 + i * kChunk + j);
+          x.w = src[k];
           ms_add_v<DT, VW>(st, x, k2, vmax);
         }
         read.next();
       }
       if (!fine) break;
+      // a row's partial slots: its first, and the one after the whole ones
+      const int p0 = r.f0 > 0 && s0 == 0 && tid == 0 ? 0 : -1;
+      const int p1 = r.f1 < r.slots && r.f1 >= s0 && r.f1 < s1 && tid == 32
+                         ? r.f1 : -1;
+      if (p0 >= 0) ms_add_v<DT, VW>(st, load_partial(r, p0), k2, vmax);
+      if (p1 >= 0) ms_add_v<DT, VW>(st, load_partial(r, p1), k2, vmax);
+      __syncwarp();
       st = warp_down_ms(st, k2);
       if (lane == 0) s.part[warp] = st;
       wait(&s.t_full[two.slot], two.parity);
@@ -589,24 +595,42 @@ distill_step_kernel(const __grid_constant__ DistillParams p, int chunks) {
       const float c = ok ? w * p.inv_T : nan, nl2 = -(st.m * k2 + ls);
       const GradRow<DT> grad(p.grad, p.grad_stride, row, r);
       for (int i = 0; i < chunks; ++i) {
-        const uint4 *src = ring + write.slot * kChunk;
-        const int n = min(kChunk, s1 - s0 - i * kChunk);
+        const uint4 *src = ring + write.slot * kChunk + tid;
+        const int lo = max(0, r.f0 - s0 - i * kChunk);
+        const int hi = min(kChunk, min(s1, r.f1) - s0 - i * kChunk);
+        uint4 *dst = reinterpret_cast<uint4 *>(grad.slots) + s0 +
+                     i * kChunk + tid;
+        if (w != 0.f && grad.like) {
 #pragma unroll
-        for (int k = 0; k < kChunk / (32 * kStepWarps); ++k) {
-          const int j = tid + k * 32 * kStepWarps, at = s0 + i * kChunk + j;
-          if (j >= n) continue;
-          Raw<DT, VW> x;
-          if (r.full(at)) x.w = src[j];
-          else x = load_partial(r, at);
-          // a weight of 0: zeros, whatever the row holds
-          const uint4 g = slot_grad<DT>(x, c * P, k2, nl2);
-          grad.store(r, at, w == 0.f ? make_uint4(0, 0, 0, 0) : g);
+          for (int k = 0; k < kChunk; k += 32 * kStepWarps) {
+            if (tid + k < lo || tid + k >= hi) continue;
+            Raw<DT, VW> x;
+            x.w = src[k];
+            dst[k] = slot_grad<DT>(x, c * P, k2, nl2);
+          }
+        } else {
+          // zeros, whatever the row holds; or a gradient by the element
+          for (int k = 0; k < kChunk; k += 32 * kStepWarps) {
+            if (tid + k < lo || tid + k >= hi) continue;
+            Raw<DT, VW> x;
+            x.w = src[k];
+            const uint4 g = slot_grad<DT>(x, c * P, k2, nl2);
+            grad.store(r, s0 + i * kChunk + tid + k,
+                       w == 0.f ? make_uint4(0, 0, 0, 0) : g);
+          }
         }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.empty[write.slot]);
         write.next();
       }
+      for (int part : {p0, p1})
+        if (part >= 0) {
+          const uint4 g =
+              slot_grad<DT>(load_partial(r, part), c * P, k2, nl2);
+          grad.store(r, part, w == 0.f ? make_uint4(0, 0, 0, 0) : g);
+        }
+      __syncwarp();
       step_sync();
       if (w != 0.f)
         store_entries<DT>(p, t, grad.row, max(0, r.first_col(s0)),
