@@ -340,17 +340,32 @@ distill_row_kernel(const __grid_constant__ DistillParams p) {
   float vmax;
   for (int b = 0; b < batches; ++b) {
     const int n = b * RUN + tid;
+    if (s0 + b * RUN >= r.f0 && s0 + (b + 1) * RUN <= min(s1, r.f1)) {
+      const uint4 *src = reinterpret_cast<const uint4 *>(r.base) + s0 + n;
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (s0 + n + i * kRowThreads < s1)
-        x[i] = load_slot(r, s0 + n + i * kRowThreads);
+      for (int i = 0; i < kBatch; ++i) x[i].w = ld_v4(src + i * kRowThreads);
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      if (s0 + n + i * kRowThreads < s1) {
+      for (int i = 0; i < kBatch; ++i)
         ms_add_v<DT, VW>(st, x[i], k2, vmax);
-        if (STEP && n + i * kRowThreads < kKept && b + 1 < batches)
-          kept[n + i * kRowThreads] = x[i].w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int s = s0 + n + i * kRowThreads;
+        if (r.full(s) && s < s1) x[i].w = ld_v4(r.base + (long long)s * 16);
       }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int s = s0 + n + i * kRowThreads;
+        if (s >= s1) continue;
+        if (!r.full(s)) x[i] = load_partial(r, s);
+        ms_add_v<DT, VW>(st, x[i], k2, vmax);
+      }
+    }
+    if (STEP && b + 1 < batches) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (n + i * kRowThreads < kKept) kept[n + i * kRowThreads] = x[i].w;
+    }
   }
   st = warp_down_ms(st, k2);
   if (lane == 0) part[warp] = st;
@@ -425,9 +440,9 @@ distill_row_kernel(const __grid_constant__ DistillParams p) {
 // warp has the teacher's entries of the next row ready; sixteen warps do the
 // two passes.
 constexpr int kChunk = 2048;      // slots
-constexpr int kRing = 6;          // chunks, 192 KB
-constexpr int kMostChunks = 4;    // of a run: the rest of the ring runs ahead
-constexpr int kStepWarps = 16;
+constexpr int kRing = 3;          // chunks, 96 KB
+constexpr int kMostChunks = 2;    // of a run: the rest of the ring runs ahead
+constexpr int kStepWarps = 8;
 constexpr int kStepThreads = 32 * (kStepWarps + 2);
 
 struct StepShared {
@@ -444,7 +459,7 @@ __device__ __forceinline__ void step_sync() {  // the sixteen warps
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kStepThreads, 1)
+__global__ void __launch_bounds__(kStepThreads, 2)
 distill_step_kernel(const __grid_constant__ DistillParams p, int chunks) {
   constexpr int VW = vec_width<DT>();
   extern __shared__ __align__(16) char dyn[];
@@ -645,16 +660,24 @@ distill_step_kernel(const __grid_constant__ DistillParams p, int chunks) {
   cluster.sync();  // nothing is on its way to a CTA that has ended
 }
 
-// The backward call: a CTA per row and run of kThreads kBatch slots, all of
-// them on their way before the teacher's chain of loads.
+// The backward call: a CTA per row and span of up to `steps` runs of
+// kBackRun slots, each run loaded while the one before it is stored.  The
+// first is on its way before the teacher's chain of loads (ids, then the
+// student's logits there), which every CTA of a row goes through: a span is
+// as long as leaves CTAs enough to fill the GPU.
+constexpr int kBackBatch = 4;
+constexpr int kBackRun = kThreads * kBackBatch;
+constexpr int kBackSteps = 8;
+
 template <int DT>
-__global__ void __launch_bounds__(kThreads)
-distill_backward_kernel(const __grid_constant__ DistillParams p) {
-  constexpr int VW = vec_width<DT>(), RUN = kThreads * kBatch;
+__global__ void __launch_bounds__(kThreads, 4)
+distill_backward_kernel(const __grid_constant__ DistillParams p, int steps) {
+  constexpr int VW = vec_width<DT>();
   __shared__ Teacher t;
   const int row = blockIdx.x, tid = threadIdx.x;
   const SlotRow<DT> r(p.student, p.row_stride, row, p.V);
-  const int s0 = blockIdx.y * RUN, s1 = min(s0 + RUN, r.slots);
+  const int s0 = blockIdx.y * steps * kBackRun;
+  const int s1 = min(s0 + steps * kBackRun, r.slots);
   if (s0 >= s1) return;
   const GradRow<DT> grad(p.grad, p.grad_stride, row, r);
   const float w = __ldg(p.grad_loss + row);
@@ -663,11 +686,16 @@ distill_backward_kernel(const __grid_constant__ DistillParams p) {
       grad.store(r, s, make_uint4(0, 0, 0, 0));
     return;
   }
-  Raw<DT, VW> x[kBatch];
+  Raw<DT, VW> x[kBackBatch], y[kBackBatch];
+  // whole slots only; the others are read when they are written
+  auto fetch = [&](Raw<DT, VW> *v, int s) {
 #pragma unroll
-  for (int i = 0; i < kBatch; ++i)
-    if (s0 + tid + i * kThreads < s1)
-      x[i] = load_slot(r, s0 + tid + i * kThreads);
+    for (int i = 0; i < kBackBatch; ++i) {
+      const int at = s + tid + i * kThreads;
+      if (at < s1 && r.full(at)) v[i].w = ld_v4(r.base + (long long)at * 16);
+    }
+  };
+  fetch(x, s0);
   const int lo = max(0, r.first_col(s0)), hi = min(p.V, r.first_col(s1));
   if (tid < 32) load_teacher(p, row, t, r, lo, hi);
   const float lse = __ldg(p.lse_in + row);
@@ -677,10 +705,29 @@ distill_backward_kernel(const __grid_constant__ DistillParams p) {
   if (!ok && tid == 0) status_or(p.dev_status, SD_DEV_NONFINITE);
   const float c = ok ? w * p.inv_T : __int_as_float(0x7fc00000);
   const float nl2 = -lse * (1.f / kLn2);
+  auto store = [&](const Raw<DT, VW> *v, int s) {
 #pragma unroll
-  for (int i = 0; i < kBatch; ++i) {
-    const int s = s0 + tid + i * kThreads;
-    if (s < s1) grad.store(r, s, slot_grad<DT>(x[i], c * P, p.k2, nl2));
+    for (int i = 0; i < kBackBatch; ++i) {
+      const int at = s + tid + i * kThreads;
+      if (at < s1 && r.full(at) && grad.like)
+        *reinterpret_cast<uint4 *>(grad.slots + (long long)at * 16) =
+            slot_grad<DT>(v[i], c * P, p.k2, nl2);
+    }
+  };
+  for (int s = s0; s < s1; s += 2 * kBackRun) {
+    fetch(y, s + kBackRun);
+    store(x, s);
+    fetch(x, s + 2 * kBackRun);
+    store(y, s + kBackRun);
+  }
+  // a row's partial slots, and all of one whose gradient lies differently
+  if (!grad.like) {
+    for (int s = s0 + tid; s < s1; s += kThreads)
+      grad.store(r, s, slot_grad<DT>(load_slot(r, s), c * P, p.k2, nl2));
+  } else if (tid < 2) {
+    const int s = tid == 0 ? 0 : r.f1;
+    if (s >= s0 && s < s1 && !r.full(s) && (tid == 1 || r.f0 > 0))
+      grad.store(r, s, slot_grad<DT>(load_partial(r, s), c * P, p.k2, nl2));
   }
   __syncthreads();
   store_entries<DT>(p, t, grad.row, lo, hi, c, P, nl2, kThreads);
@@ -853,11 +900,15 @@ extern "C" sd_status sd_distill_topk_backward(
   p.grad_loss = grad_loss;
   p.grad = grad;
   p.grad_stride = grad_stride;
-  const int run = kThreads * kBatch;
-  const dim3 grid(N, (max_slots(V, dt) + run - 1) / run);
+  const int runs = (max_slots(V, dt) + kBackRun - 1) / kBackRun;
+  int steps = kBackSteps;
+  while (steps > 1 && (long long)N * ((runs + steps - 1) / steps) < 10LL * sms)
+    steps /= 2;
+  const dim3 grid(N, (runs + steps - 1) / steps);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dt == SD_F32) distill_backward_kernel<0><<<grid, kThreads, 0, s>>>(p);
-  else distill_backward_kernel<1><<<grid, kThreads, 0, s>>>(p);
+  if (dt == SD_F32)
+    distill_backward_kernel<0><<<grid, kThreads, 0, s>>>(p, steps);
+  else distill_backward_kernel<1><<<grid, kThreads, 0, s>>>(p, steps);
   SDV_CUDA(cudaGetLastError());
   return SD_OK;
 }
