@@ -1200,8 +1200,8 @@ extern "C" sd_status sd_paged_attention(
                   q_heads % cache->heads == 0,
               "q_heads=%d is not a multiple of the cache's %d heads", q_heads,
               cache->heads);
-  SDV_REQUIRE(scale > 0.f && std::isfinite(scale),
-              "scale must be finite and > 0");
+  SDV_REQUIRE(scale > 0.f && std::isfinite(scale * 1.5f),
+              "scale must be > 0, and scale log2(e) finite");
   SDV_REQUIRE(!tree_mask || mask_words >= 1, "mask_words < 1");
   if (D != 64 && D != 128)
     return fail(SD_ERR_UNSUPPORTED, "head_dim=%d is neither 64 nor 128", D);

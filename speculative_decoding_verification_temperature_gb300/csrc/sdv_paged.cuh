@@ -88,7 +88,7 @@ inline sd_status check_cache(const sd_paged_kv *c) {
   SDV_REQUIRE(c->num_pages >= 0, "num_pages < 0");
   SDV_REQUIRE(c->page_size >= 1, "page_size < 1");
   SDV_REQUIRE(c->max_pages >= 0, "max_pages < 0");
-  SDV_REQUIRE((long long)c->max_pages * c->page_size < (1LL << 31),
+  SDV_REQUIRE((long long)c->max_pages * c->page_size < (1LL << 31) - 256,
               "max_pages page_size = %lld does not fit 31 bits",
               (long long)c->max_pages * c->page_size);
   SDV_REQUIRE(c->heads >= 1 && c->heads <= 65535, "heads=%d outside [1, 65535]",
