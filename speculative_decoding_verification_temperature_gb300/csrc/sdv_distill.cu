@@ -193,7 +193,7 @@ template <int DT> struct GradRow {
 // p = 0 by a logit of -inf), p, log2 p, the student's logit at the id, and P
 // (NaN: unusable entries).
 struct Teacher {
-  int id[SD_MAX_DISTILL_K];
+  alignas(16) int id[SD_MAX_DISTILL_K];
   float p[SD_MAX_DISTILL_K];
   float log2p[SD_MAX_DISTILL_K];
   float at[SD_MAX_DISTILL_K];
@@ -267,6 +267,7 @@ __device__ void load_teacher(const DistillParams &p, int row, Teacher &t,
   for (int k = lane; k < p.K; k += 32)
     put_entry(p, t, k, __ldg(p.id + (long long)row * p.K + k),
               __ldg(p.logit + (long long)row * p.K + k));
+  if (lane < (-p.K & 3)) t.id[p.K + lane] = -1;  // read four at a time
   __syncwarp();
   constexpr int MOST = SD_MAX_DISTILL_K / 32;
   float z[MOST];  // on their way while the entries are normalised
@@ -282,6 +283,27 @@ __device__ void load_teacher(const DistillParams &p, int row, Teacher &t,
     if (lane + 32 * i < p.K) t.at[lane + 32 * i] = z[i];
 }
 
+// Whether entry k is the first of its id, and then the sum of p over all
+// entries with that id.
+__device__ __forceinline__ bool first_of_id(const Teacher &t, int K, int k,
+                                            float &sum) {
+  const int id = t.id[k];
+  bool first = true;
+  sum = 0.f;
+  for (int i = 0; i < K; i += 4) {
+    const int4 v = *reinterpret_cast<const int4 *>(t.id + i);
+    if (v.x != id && v.y != id && v.z != id && v.w != id) continue;
+    const int w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (w[e] == id) {
+        first = first && i + e >= k;
+        sum += t.p[i + e];
+      }
+  }
+  return first;
+}
+
 // The columns of the entries with ids in [lo, hi), over what the pass over
 // the row wrote: the first entry of an id writes for all that repeat it.
 template <int DT>
@@ -290,15 +312,8 @@ __device__ void store_entries(const DistillParams &p, const Teacher &t,
                               float nl2, int threads) {
   for (int k = threadIdx.x; k < p.K; k += threads) {
     const int id = t.id[k];
-    if (id < lo || id >= hi) continue;
-    float sum = 0.f;
-    bool first = true;
-    for (int i = 0; i < p.K; ++i)
-      if (t.id[i] == id) {
-        first = first && i >= k;
-        sum += t.p[i];
-      }
-    if (first)
+    float sum;
+    if (id >= lo && id < hi && first_of_id(t, p.K, k, sum))
       store_elt<DT>(grad, id, c * (P * ex2(fmaf(t.at[k], p.k2, nl2)) - sum));
   }
 }
@@ -432,29 +447,34 @@ distill_row_kernel(const __grid_constant__ DistillParams p) {
 }
 
 // The step where there are rows enough to fill the GPU: clusters of CL CTAs,
-// one CTA an SM, take rows in turn, a contiguous run of a row's slots each.
+// two CTAs an SM, take rows in turn, a contiguous run of a row's slots each.
 // A row stays in shared memory from the pass that finds log sum exp to the
 // pass that writes the gradient, so HBM sees each byte once.  A loading warp
 // keeps a ring of 32 KB chunks full, across rows: while a row's sums are
-// exchanged and its gradient is written, the next one arrives.  A second
-// warp has the teacher's entries of the next row ready; sixteen warps do the
-// two passes.
+// exchanged and its gradient is written, the next one arrives.  Two more
+// warps have the teacher's entries of the next rows ready; eight do the two
+// passes.
 constexpr int kChunk = 2048;      // slots
 constexpr int kRing = 3;          // chunks, 96 KB
 constexpr int kMostChunks = 2;    // of a run: the rest of the ring runs ahead
 constexpr int kStepWarps = 8;
-constexpr int kStepThreads = 32 * (kStepWarps + 2);
+constexpr int kStepThreads = 32 * (kStepWarps + 3);
 
 struct StepShared {
   uint64_t full[kRing], empty[kRing];
-  uint64_t t_full[2], t_empty[2], sum_full[2];
+  uint64_t t_full[2], t_empty[2], sum_full[2], row_full[2];
   volatile int abort;
   MS part[kStepWarps];
   alignas(8) MS sums[2][8];  // of the cluster's CTAs, two rows' worth
+  alignas(8) MS row[2];      // of the whole row
   Teacher t[2];
+  // a row's entries as its columns take them: the first of each id (others
+  // and unused ones -1), and the sum of p over the id
+  int col[2][SD_MAX_DISTILL_K];
+  float sum[2][SD_MAX_DISTILL_K];
 };
 
-__device__ __forceinline__ void step_sync() {  // the sixteen warps
+__device__ __forceinline__ void step_sync() {  // the warps of the passes
   asm volatile("bar.sync 1, %0;" ::"n"(32 * kStepWarps) : "memory");
 }
 
@@ -481,6 +501,7 @@ distill_step_kernel(const __grid_constant__ DistillParams p, int chunks) {
       mbar_init(&s.t_full[i], 1);
       mbar_init(&s.t_empty[i], kStepWarps);
       mbar_init(&s.sum_full[i], 1);
+      mbar_init(&s.row_full[i], 1);
     }
     s.abort = 0;
     fence_mbar_init();
@@ -523,19 +544,48 @@ distill_step_kernel(const __grid_constant__ DistillParams p, int chunks) {
         for (unsigned it = 0; it < (1u << 20); ++it)
           if (mbar_try_wait(&s.full[i], last & 1)) break;
       }
-  } else if (warp == kStepWarps + 1) {
+  } else if (warp > kStepWarps) {
     // ---- the teacher's entries, and the student's logits at their ids:
     // before the row's sums leave this CTA, so before any CTA writes to the
-    // row (the gradient may go to the student's own rows)
-    RingAt at(2);
-    for (int row = first; row < p.N; row += clusters) {
-      wait(&s.t_empty[at.slot], at.parity ^ 1);
+    // row (the gradient may go to the student's own rows).  Off the other
+    // warps' path, the loss.  A row's chain of loads takes longer than its
+    // two passes: two warps, every other row each.
+    const int me = warp - kStepWarps - 1;
+    uint32_t parity = 0;
+    Teacher &t = s.t[me];
+    for (int row = first + me * clusters; row < p.N; row += 2 * clusters) {
+      wait(&s.t_empty[me], parity ^ 1);
       if (!fine) break;
       const SlotRow<DT> r(p.student, p.row_stride, row, p.V);
-      load_teacher(p, row, s.t[at.slot], r, 0, p.V);
+      load_teacher(p, row, t, r, 0, p.V);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s.t_full[at.slot]);
-      at.next();
+      for (int k = lane; k < p.K; k += 32) {
+        float sum = 0.f;
+        const bool col = t.id[k] >= 0 && first_of_id(t, p.K, k, sum);
+        s.col[me][k] = col ? t.id[k] : -1;
+        s.sum[me][k] = sum;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.t_full[me]);
+      wait(&s.row_full[me], parity);
+      if (!fine) break;
+      if (rank == 0) {
+        const MS st = s.row[me];
+        const float ls = log2f(st.s);
+        const bool ok = ms_valid(st) && t.P == t.P;
+        float a = 0.f;
+        for (int k = lane; k < p.K; k += 32)
+          if (t.id[k] >= 0 && t.p[k] > 0.f)
+            a += t.p[k] * (t.log2p[k] - ((t.at[k] - st.m) * k2 - ls));
+        a = warp_down_sum(a);
+        if (lane == 0) {
+          p.loss[row] = ok ? a * kLn2 : nan;
+          p.lse[row] = ok ? (st.m * k2 + ls) * kLn2 : nan;
+          if (!ok) status_or(p.dev_status, SD_DEV_NONFINITE);
+        }
+        __syncwarp();
+      }
+      parity ^= 1;
     }
   } else {
     RingAt read(kRing), write(kRing), two(2);
@@ -543,6 +593,7 @@ distill_step_kernel(const __grid_constant__ DistillParams p, int chunks) {
       const SlotRow<DT> r(p.student, p.row_stride, row, p.V);
       const int s0 = (int)((long long)r.slots * rank / p.CL);
       const int s1 = (int)((long long)r.slots * (rank + 1) / p.CL);
+      const float w = __ldg(p.grad_loss + row);
       // ---- log sum exp
       MS st = ms_empty();
       float vmax;
@@ -591,21 +642,12 @@ distill_step_kernel(const __grid_constant__ DistillParams p, int chunks) {
       for (int i = 0; i < p.CL; ++i)
         st = ms_merge(st, s.sums[two.slot][i], k2);
       const Teacher &t = s.t[two.slot];
-      const float P = t.P, ls = log2f(st.s), w = __ldg(p.grad_loss + row);
-      const bool ok = ms_valid(st) && P == P;
-      if (rank == 0 && warp == 0) {
-        float a = 0.f;
-        for (int k = lane; k < p.K; k += 32)
-          if (t.id[k] >= 0 && t.p[k] > 0.f)
-            a += t.p[k] * (t.log2p[k] - ((t.at[k] - st.m) * k2 - ls));
-        a = warp_down_sum(a);
-        if (lane == 0) {
-          p.loss[row] = ok ? a * kLn2 : nan;
-          p.lse[row] = ok ? (st.m * k2 + ls) * kLn2 : nan;
-          if (!ok) status_or(p.dev_status, SD_DEV_NONFINITE);
-        }
-        __syncwarp();
+      if (tid == 0) {
+        s.row[two.slot] = st;
+        mbar_arrive(&s.row_full[two.slot]);
       }
+      const float P = t.P, ls = log2f(st.s);
+      const bool ok = ms_valid(st) && P == P;
       // ---- the gradient; each chunk is handed back as soon as it is used
       const float c = ok ? w * p.inv_T : nan, nl2 = -(st.m * k2 + ls);
       const GradRow<DT> grad(p.grad, p.grad_stride, row, r);
@@ -647,10 +689,17 @@ distill_step_kernel(const __grid_constant__ DistillParams p, int chunks) {
         }
       __syncwarp();
       step_sync();
-      if (w != 0.f)
-        store_entries<DT>(p, t, grad.row, max(0, r.first_col(s0)),
-                          min(p.V, r.first_col(s1)), c, P, nl2,
-                          32 * kStepWarps);
+      if (w != 0.f) {
+        const int lo = max(0, r.first_col(s0));
+        const int hi = min(p.V, r.first_col(s1));
+        for (int k = tid; k < p.K; k += 32 * kStepWarps) {
+          const int id = s.col[two.slot][k];
+          if (id >= lo && id < hi)
+            store_elt<DT>(grad.row, id,
+                          c * (P * ex2(fmaf(t.at[k], k2, nl2)) -
+                               s.sum[two.slot][k]));
+        }
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.t_empty[two.slot]);
       two.next();
