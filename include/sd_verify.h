@@ -665,17 +665,17 @@ sd_status sd_paged_attention(const void *q, long long q_stride, int q_heads,
  * lse [N]: log sum_j exp(student_j / T), an output of the forward calls and
  * an input of the backward one.
  * An entry with id < 0 is padding; one with id >= V is treated as padding
- * and sets SD_DEV_BAD_TOKEN (padding's logits are not looked at).  An entry with logit -inf has p = 0 and adds
- * nothing, whatever the student's logit.  Repeated ids each count.  A row
- * without usable entries has loss 0 and gradient 0.  A student logit of
- * -inf has q = 0.  A row (student's or teacher's) that holds NaN or +inf, a
- * teacher_lse that is not finite, or a student row without a logit above
- * -3e38, has loss and lse NaN, gradient NaN and sets SD_DEV_NONFINITE.  A row with grad_loss exactly 0 gets a gradient of
- * exactly 0 (its student row is not read by the backward call).
+ * and sets SD_DEV_BAD_TOKEN (padding's logits are not looked at).  An entry
+ * with logit -inf has p = 0 and adds nothing, whatever the student's logit.
+ * Repeated ids each count.  A row without usable entries has loss 0 and
+ * gradient 0.  A student logit of -inf has q = 0.  A row (student's or
+ * teacher's) that holds NaN or +inf, a teacher_lse that is not finite, or a
+ * student row without a logit above -3e38, has loss and lse NaN, gradient
+ * NaN and sets SD_DEV_NONFINITE (the backward call goes by the lse it is
+ * given).  A row with grad_loss exactly 0 gets a gradient of exactly 0 (its
+ * student row is not read by the backward call).
  * grad may be the student's own buffer (same pointer and stride).
- * sd_distill_topk_step is the forward and the backward call together; it
- * reads the student's rows once where one fits the shared memory of 16 SMs
- * (573,000 bf16 columns), and twice above.
+ * sd_distill_topk_step is the forward and the backward call together.
  * ------------------------------------------------------------------- */
 sd_status sd_distill_topk(const void *student, long long row_stride,
                           sd_dtype dt, const float *teacher_logit,

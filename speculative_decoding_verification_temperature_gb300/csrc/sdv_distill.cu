@@ -844,7 +844,7 @@ sd_status launch_rows(DistillParams &p, sd_dtype dt, int sms,
                       cudaStream_t s) {
   const int slots = max_slots(p.V, dt);
   int cl = 1;
-  while (cl < 8 && (long long)p.N * cl < 2LL * sms && slots / (2 * cl) >= 512)
+  while (cl < 8 && (long long)p.N * cl <= sms && slots / (2 * cl) >= 512)
     cl *= 2;
   p.CL = cl;
   const void *kernel = dt == SD_F32 ? (const void *)distill_row_kernel<0, STEP>
