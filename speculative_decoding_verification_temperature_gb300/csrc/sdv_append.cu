@@ -114,7 +114,8 @@ struct Double {
 };
 
 template <class T> __device__ __forceinline__ float2 unpack2(uint32_t u);
-template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t u) {
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t u) {
   return make_float2(__uint_as_float(u << 16),
                      __uint_as_float(u & 0xffff0000u));
 }
@@ -162,7 +163,8 @@ __device__ __forceinline__ Double turn(Double x, const float (&c)[8],
 // sines once.  Bound by HBM where there are many rows (each byte is read and
 // written once) and by the chain sequence -> page -> store where there are
 // few; a thread's first kAhead heads are on their way before it starts on
-// that chain.
+// that chain.  25k tokens of 48 heads of 128, fp16: 700 MB in 119 us, 0.88 of
+// the measured copy rate; one token 2.3 us, 288 tokens 3.3 us.
 constexpr int kAhead = 3;
 template <class T, bool NEIGHBOURS>
 __global__ void __launch_bounds__(kThreads)

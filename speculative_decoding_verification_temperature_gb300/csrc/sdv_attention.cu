@@ -14,14 +14,27 @@
 // is cut leaves partial sums in the workspace, which a second kernel joins
 // in key order.
 //
-// In a CTA, one warp loads key and value tiles by TMA through the block
-// table, one issues the tensor-core products, and two warpgroups ("streams")
+// In a CTA, two warps load key and value tiles by TMA through the block
+// table, two issue the tensor-core products, and two warpgroups ("streams")
 // turn scores into weights, a thread per row.  S = Q K^T goes to tensor
-// memory; the weights, rounded to 16 bits, go back there over S and are the
-// first operand of O += W V.  The streams take turns on the tensor cores:
-// with 256 rows each stream has 128 of them; with up to 128 rows (a few
+// memory; the weights, rounded to 16 bits (the tensor cores take two operands
+// of one type), go back there over S and are the first operand of O += W V.
+// With 256 rows each stream has 128 of them; with up to 128 rows (a few
 // drafts) both have the same rows and every other key tile, and their sums
-// are joined at the end of the unit.
+// are joined at the end of the unit.  The plain loop over keys with a warp
+// per (token, head) took 14 ms on 64 sequences of one token and 219 ms on
+// two prompt chunks; this takes 220 us and 555 us.
+//
+// What bounds it: HBM for a few rows a unit (1.41 GB of keys and values of 64
+// sequences in 220 us, 0.96 of the measured copy rate; a CTA keeps six tiles,
+// 192 KB, on their way), and for many rows the chain score product, softmax,
+// value product of a stream: 2750 cycles for two streams' 128 x 128 tiles
+// where the products alone take 2048 (1.47 PFLOP/s on chunks of 4096 and 2250
+// tokens, 0.77 of the measured bf16 rate).
+//
+// A wait that gives up (see role_wait) stops the loads and the products; all
+// other steps go on over meaningless data to the end of the share, so that
+// every barrier between warps is reached.
 #include <cuda.h>
 
 #include <atomic>
@@ -317,7 +330,6 @@ __device__ __forceinline__ void streams_sync() {
   asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 
-
 // 32 bytes, at a multiple of 32: whole sectors even where each lane writes
 // a row of its own.
 __device__ __forceinline__ void st_v8(void *to, const uint32_t *x) {
@@ -327,7 +339,8 @@ __device__ __forceinline__ void st_v8(void *to, const uint32_t *x) {
       : "memory");
 }
 
-template <class T> __device__ __forceinline__ uint32_t pack2(float lo, float hi);
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi);
 template <>
 __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
   uint32_t u;
@@ -468,7 +481,7 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
       }
       row.l *= f;
       if (hf || !first) {
-        // a half's sums are complete when the last half's before it are
+        // all sums before this half are complete when the last of them are
         const bool fine =
             role_wait(&o_full[hf ^ 1], parity ^ (hf ^ 1), abort, dev_status);
         if (!__all_sync(~0u, fine)) return false;
@@ -558,8 +571,8 @@ attention_kernel(const __grid_constant__ AttnParams p,
   const uint32_t tmem = s.tmem;
   bool fine = true;
 
-  // 384 threads start with 168 registers each; a softmax thread holds a row
-  // of 128 scores, a role next to nothing: 256 x 208 + 128 x 88 = 384 x 168
+  // 384 threads start with 168 registers each; a softmax thread holds much of
+  // a row, a role next to nothing: 256 x 208 + 128 x 88 = 384 x 168
   if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
   if (warp >= 8) {
@@ -624,137 +637,140 @@ attention_kernel(const __grid_constant__ AttnParams p,
           }
       }
     } else {
-    // ---- tensor-core products of stream st, a warp each: while one is held
-    // up issuing (products queue some 200 cycles deep) the other waits for
-    // its weights
-    const int st = warp - kMmaWarp;
-    constexpr uint32_t S_DESC = umma_idesc(BF16, false, kTile, kTile);
-    constexpr uint32_t O_DESC = umma_idesc(BF16, true, kTile, D);
-    constexpr uint32_t HI = umma_desc_hi(1024);
-    const uint32_t s_addr = tmem + st * kTile;
-    const uint32_t o_addr = tmem + 2 * kTile + st * D;
-    const uint32_t q_lo =
-        umma_desc_lo(q_tile + (PAIR ? st : 0) * L::kTileBytes, 16);
-    // where the stream reads keys and values next
-    const int kr = PAIR ? 0 : st, vr = PAIR ? 1 : st;
-    const uint32_t k_lo = umma_desc_lo(ring[kr], 16);
-    const uint32_t v_lo = umma_desc_lo(ring[vr], kTile * 128);
-    RingAt ring_k(kr ? L::kN1 : L::kN0), ring_v(L::kN1);
-    RingAt &k_at = ring_k, &v_at = PAIR ? ring_v : ring_k;
-    uint32_t wp = 0, qp = 0;
-    auto wait = [&](uint64_t *bar, uint32_t parity) {
-      fine = fine && role_wait(bar, parity, &s.abort, p.dev_status);
-    };
-    // S against the next key tile
-    auto wait_k = [&] { wait(&s.full[kr][k_at.slot], k_at.parity); };
-    auto scores = [&] {
-      if (fine && elect_one()) {
-        const uint32_t b = k_lo + k_at.slot * (L::kTileBytes / 16);
+      // ---- tensor-core products of stream st, a warp each: while one is held
+      // up issuing (products queue some 200 cycles deep) the other waits for
+      // its weights
+      const int st = warp - kMmaWarp;
+      constexpr uint32_t S_DESC = umma_idesc(BF16, false, kTile, kTile);
+      constexpr uint32_t O_DESC = umma_idesc(BF16, true, kTile, D);
+      constexpr uint32_t HI = umma_desc_hi(1024);
+      const uint32_t s_addr = tmem + st * kTile;
+      const uint32_t o_addr = tmem + 2 * kTile + st * D;
+      const uint32_t q_lo =
+          umma_desc_lo(q_tile + (PAIR ? st : 0) * L::kTileBytes, 16);
+      // where the stream reads keys and values next
+      const int kr = PAIR ? 0 : st, vr = PAIR ? 1 : st;
+      const uint32_t k_lo = umma_desc_lo(ring[kr], 16);
+      const uint32_t v_lo = umma_desc_lo(ring[vr], kTile * 128);
+      RingAt ring_k(kr ? L::kN1 : L::kN0), ring_v(L::kN1);
+      RingAt &k_at = ring_k, &v_at = PAIR ? ring_v : ring_k;
+      uint32_t wp = 0, qp = 0;
+      // After a wait that gives up nothing more is issued, but the loops go on
+      // to their ends: lanes may disagree about it, and elect_one() and
+      // __syncwarp() want them all.
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        fine = fine && role_wait(bar, parity, &s.abort, p.dev_status);
+      };
+      // S against the next key tile
+      auto wait_k = [&] { wait(&s.full[kr][k_at.slot], k_at.parity); };
+      auto scores = [&] {
+        if (elect_one() && fine) {
+          const uint32_t b = k_lo + k_at.slot * (L::kTileBytes / 16);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const int at = ((i / 4) * (kTile * 128) + (i % 4) * 32) / 16;
-          umma_ss<HI>(s_addr, q_lo + at, b + at, S_DESC, i > 0);
+          for (int i = 0; i < D / 16; ++i) {
+            const int at = ((i / 4) * (kTile * 128) + (i % 4) * 32) / 16;
+            umma_ss<HI>(s_addr, q_lo + at, b + at, S_DESC, i > 0);
+          }
+          umma_commit(&s.s_full[st]);
+          umma_commit(&s.empty[kr][k_at.slot]);
         }
-        umma_commit(&s.s_full[st]);
-        umma_commit(&s.empty[kr][k_at.slot]);
-      }
-      __syncwarp();
-      k_at.next();
-    };
-    // Wait for the value tile of key tile j.  What lies past the sequence's
-    // keys becomes zero, so that 0 x NaN of a stale page cannot reach the
-    // sums (both streams may write the same zeros).
-    auto wait_v = [&](int j) {
-      wait(&s.full[vr][v_at.slot], v_at.parity);
-      const int from = u.c.kv - j * kTile;
-      if (from < kTile) {
-        const int to = (from + p.box - 1) / p.box * p.box;
-        char *v = ring[vr] + v_at.slot * L::kTileBytes;
-        for (int i = lane; i < (to - from) * 8 * (D / 64); i += 32) {
-          const int row = from + i / 8 % (to - from);
-          const int half = i / 8 / (to - from);
-          *reinterpret_cast<uint4 *>(v + half * (kTile * 128) + row * 128 +
-                                     (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async();
         __syncwarp();
-      }
-    };
-    // O with that tile
-    // half hf of the tile's keys
-    auto values = [&](int hf, bool first) {
-      if (fine && elect_one()) {
-        const uint32_t b = v_lo + v_at.slot * (L::kTileBytes / 16) +
-                           hf * (kHalf * 128 / 16);
-        tmem_fence_after();
-#pragma unroll
-        for (int i = 0; i < kHalf / 16; ++i)
-          umma_ts<HI>(o_addr, s_addr + hf * (kHalf / 2) + i * 8,
-                      b + i * 16 * 128 / 16, O_DESC, !first || i > 0);
-        umma_commit(&s.o_full[st][hf]);
-        if (hf) umma_commit(&s.empty[vr][v_at.slot]);
-      }
-      __syncwarp();
-      if (hf) v_at.next();
-    };
-    // 256 rows: the streams take strict turns, a value and a score product
-    // at a time, so that one's softmax runs under the other's products
-    // (left to themselves they fall into step, and both wait for both)
-    uint32_t tp = st ^ 1;
-    auto take_turn = [&] {
-      wait(&s.turn[st], tp);
-      tp ^= 1;
-    };
-    auto pass_turn = [&] {
-      if (fine && elect_one()) mbar_arrive(&s.turn[st ^ 1]);
-      __syncwarp();
-    };
-    for (; u.left && fine; u.next()) {
-      const int cnt = u.j1 - u.j0;
-      if (PAIR && st == 1 && u.rows <= kTile) {
-        // no rows: let go of every tile as it comes
-        for (int i = 0; i < cnt && fine; ++i) {
-          wait(&s.full[kr][k_at.slot], k_at.parity);
-          if (fine && lane == 0) mbar_arrive(&s.empty[kr][k_at.slot]);
-          k_at.next();
-          wait(&s.full[vr][v_at.slot], v_at.parity);
-          if (fine && lane == 0) mbar_arrive(&s.empty[vr][v_at.slot]);
-          v_at.next();
+        k_at.next();
+      };
+      // Wait for the value tile of key tile j.  What lies past the sequence's
+      // keys becomes zero, so that 0 x NaN of a stale page cannot reach the
+      // sums (both streams may write the same zeros).
+      auto wait_v = [&](int j) {
+        wait(&s.full[vr][v_at.slot], v_at.parity);
+        const int from = u.c.kv - j * kTile;
+        if (from < kTile) {
+          const int to = (from + p.box - 1) / p.box * p.box;
+          char *v = ring[vr] + v_at.slot * L::kTileBytes;
+          for (int i = lane; i < (to - from) * 8 * (D / 64); i += 32) {
+            const int row = from + i / 8 % (to - from);
+            const int half = i / 8 / (to - from);
+            *reinterpret_cast<uint4 *>(v + half * (kTile * 128) + row * 128 +
+                                       (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+          __syncwarp();
         }
-        continue;
+      };
+      // O with half hf of that tile
+      auto values = [&](int hf, bool first) {
+        if (elect_one() && fine) {
+          const uint32_t b = v_lo + v_at.slot * (L::kTileBytes / 16) +
+                             hf * (kHalf * 128 / 16);
+          tmem_fence_after();
+#pragma unroll
+          for (int i = 0; i < kHalf / 16; ++i)
+            umma_ts<HI>(o_addr, s_addr + hf * (kHalf / 2) + i * 8,
+                        b + i * 16 * 128 / 16, O_DESC, !first || i > 0);
+          umma_commit(&s.o_full[st][hf]);
+          if (hf) umma_commit(&s.empty[vr][v_at.slot]);
+        }
+        __syncwarp();
+        if (hf) v_at.next();
+      };
+      // 256 rows: the streams take strict turns, a value and a score product
+      // at a time, so that one's softmax runs under the other's products
+      // (left to themselves they fall into step, and both wait for both)
+      uint32_t tp = st ^ 1;
+      auto take_turn = [&] {
+        wait(&s.turn[st], tp);
+        tp ^= 1;
+      };
+      auto pass_turn = [&] {
+        if (elect_one() && fine) mbar_arrive(&s.turn[st ^ 1]);
+        __syncwarp();
+      };
+      for (; u.left; u.next()) {
+        const int cnt = u.j1 - u.j0;
+        if (PAIR && st == 1 && u.rows <= kTile) {
+          // no rows: let go of every tile as it comes
+          for (int i = 0; i < cnt; ++i) {
+            wait(&s.full[kr][k_at.slot], k_at.parity);
+            if (fine && lane == 0) mbar_arrive(&s.empty[kr][k_at.slot]);
+            k_at.next();
+            wait(&s.full[vr][v_at.slot], v_at.parity);
+            if (fine && lane == 0) mbar_arrive(&s.empty[vr][v_at.slot]);
+            v_at.next();
+          }
+          continue;
+        }
+        wait(&s.q_full[PAIR ? st : 0], qp);
+        qp ^= 1;
+        const int i0 = PAIR ? 0 : st, step = PAIR ? 1 : 2;
+        const bool turns = PAIR && u.rows > kTile;
+        if (i0 < cnt) {
+          wait_k();
+          if (turns) take_turn();
+          tmem_fence_after();
+          scores();
+          if (turns) pass_turn();
+        }
+        for (int i = i0; i < cnt; i += step) {
+          const bool more = i + step < cnt;
+          wait_v(u.j0 + i);
+          if (PAIR && more) wait_k();
+          wait(&s.w_full[st][0], wp);
+          if (turns) take_turn();
+          values(0, i == i0);
+          wait(&s.w_full[st][1], wp);
+          wp ^= 1;
+          values(1, false);
+          if (!PAIR && more) wait_k();
+          if (more) scores();
+          if (turns) pass_turn();
+        }
       }
-      wait(&s.q_full[PAIR ? st : 0], qp);
-      qp ^= 1;
-      const int i0 = PAIR ? 0 : st, step = PAIR ? 1 : 2;
-      const bool turns = PAIR && u.rows > kTile;
-      if (i0 < cnt) {
-        wait_k();
-        if (turns) take_turn();
-        tmem_fence_after();
-        scores();
-        if (turns) pass_turn();
+      if (__any_sync(~0u, !fine)) {
+        // tensor memory is freed below: let products in flight end
+        if (elect_one()) umma_commit(&s.drain[st]);
+        __syncwarp();
+        for (unsigned it = 0; it < (1u << 20); ++it)
+          if (mbar_try_wait(&s.drain[st], 0)) break;
       }
-      for (int i = i0; i < cnt && fine; i += step) {
-        const bool more = i + step < cnt;
-        wait_v(u.j0 + i);
-        if (PAIR && more) wait_k();
-        wait(&s.w_full[st][0], wp);
-        if (turns) take_turn();
-        values(0, i == i0);
-        wait(&s.w_full[st][1], wp);
-        wp ^= 1;
-        values(1, false);
-        if (!PAIR && more) wait_k();
-        if (more) scores();
-        if (turns) pass_turn();
-      }
-    }
-    if (!fine) {  // tensor memory is freed below: let products in flight end
-      if (elect_one()) umma_commit(&s.drain[st]);
-      __syncwarp();
-      for (unsigned it = 0; it < (1u << 20); ++it)
-        if (mbar_try_wait(&s.drain[st], 0)) break;
-    }
     }
   } else {
     Units<ROWS> u(p, s.plan);
@@ -800,7 +816,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
       if (lane == 0) mbar_arrive(&s.q_full[PAIR ? st : 0]);
     };
     if (u.left) load_q(u);
-    while (u.left && fine) {
+    while (u.left) {
       if (tid == 0 && u.j0 == 0 && u.j1 < u.nk) {
         // this CTA's last unit goes on in the CTAs up to the one whose
         // share holds the unit's last tile
@@ -869,15 +885,13 @@ attention_kernel(const __grid_constant__ AttnParams p,
           mbar_arrive(&s.w_full[st][1]);
         }
       }
-      if (!fine) break;
       // ---- the end of the unit.  The last scores are out, so the next
       // unit's queries may replace this one's: its first scores are under
       // way while this one's rows are written
       if (PAIR && next.left) load_q(next);
       if (cnt > 0) {
-        fine = role_wait(&s.o_full[st][1], (tn - 1) & 1, &s.abort,
-                         p.dev_status);
-        if (!__all_sync(~0u, fine)) { fine = false; break; }
+        role_wait(&s.o_full[st][1], (tn - 1) & 1, &s.abort, p.dev_status);
+        __syncwarp();
         tmem_fence_after();
       }
       // the two streams' sums of the same rows are joined; stream st then

@@ -95,6 +95,13 @@ def test_one_token_of_one_sequence_and_many_tokens():
         128)
 
 
+def test_many_sequences():
+    r = np.random.default_rng(6)
+    n = r.integers(0, 3, 1100)
+    run(ref.Paged(n.tolist(), (n + r.integers(0, 20, 1100)).tolist(), 1, 64,
+                  8, torch.bfloat16, seed=21), 1, 64)
+
+
 def test_tree_positions():
     """Nodes of a token tree rotate by depth, not by slot."""
     P = ref.Paged([5, 3], [25, 3], 2, 64, 8, torch.bfloat16, seed=9)

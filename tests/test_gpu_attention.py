@@ -310,3 +310,33 @@ def test_many_calls_in_a_row_keep_their_bits(page):
     p = torch.softmax(kk @ q[b * n + t, h].double() * D ** -0.5, 0)
     err = (outs[0][b * n + t, h].double() - p @ vv).abs()
     assert bool((err <= 2.0 ** -7 * (p @ vv.abs()) + 1e-4).all())
+
+
+@pytest.mark.parametrize("hint", [1, 200])
+def test_many_sequences(hint):
+    """More sequences than a CTA looks over at once, empty ones and unusable
+    ones among them."""
+    r = np.random.default_rng(5)
+    B = 700
+    n = r.integers(0, 4, B)
+    kv = n + r.integers(0, 30, B)
+    n[300], kv[300] = 3, 400
+    P = ref.Paged(n.tolist(), kv.tolist(), 1, 64, 8, BF, seed=101)
+    run(P, 2, max_q=hint)
+    q = P.rows(2).cuda()
+    start, kvt = P.lengths()
+    cache = api.PagedKV(P.k.cuda(), P.v.cuda(), P.table.cuda())
+    want = api.paged_attention(q, cache, start, kvt, max_q=hint)["out"]
+    bad = [b for b in (10, 290, 600, 699) if n[b] > 0]
+    kvt[bad] = 10 ** 7
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = api.paged_attention(q, cache, start, kvt, max_q=hint,
+                              status=st)["out"]
+    assert int(st.item()) == (api.DEV_BAD_LENGTH if bad else 0)
+    rows = torch.zeros(P.total, dtype=torch.bool, device="cuda")
+    for b in bad:
+        rows[P.start[b]:P.start[b + 1]] = True
+    assert bool(torch.isnan(got[rows]).all())
+    # the shares move, so a unit may be cut elsewhere: another order of sums
+    err = (got[~rows].float() - want[~rows].float()).abs()
+    assert bool((err <= 2.0 ** -7 * want[~rows].float().abs() + 1e-3).all())

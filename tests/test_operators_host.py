@@ -81,7 +81,8 @@ def test_append_refusals(bad):
     dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
     dict(scale=float("inf")), dict(mask=P16, words=0), dict(q=None),
     dict(out=None), dict(q=P16 + 2), dict(qs=252), dict(qs=260),
-    dict(out=P16 + 8)])
+    dict(out=P16 + 8), dict(out=P16 + 16), dict(ws=None), dict(nws=1000),
+    dict(ws=P16 + 16), dict(scale=3e38), dict(total=1 << 30)])
 def test_attention_refusals(bad):
     assert attend(**bad) == api.SD_ERR_INVALID_ARG
 
