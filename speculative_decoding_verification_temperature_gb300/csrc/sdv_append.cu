@@ -158,13 +158,14 @@ __device__ __forceinline__ Double turn(Double x, const float (&c)[8],
 }
 
 // Heads whose parts are whole double chunks (D and rot_dim multiples of 16,
-// 16-byte aligned rows): a CTA per packed row, a thread for one double of
-// every (kThreads / doubles)-th head, so that it reads its eight cosines and
-// sines once.  Bound by HBM where there are many rows (each byte is read and
-// written once) and by the chain sequence -> page -> store where there are
-// few; a thread's first kAhead heads are on their way before it starts on
-// that chain.  25k tokens of 48 heads of 128, fp16: 700 MB in 119 us, 0.88 of
-// the measured copy rate; one token 2.3 us, 288 tokens 3.3 us.
+// 16-byte aligned rows): a CTA per packed row, as many threads as its doubles
+// need up to 256, a thread for one double of every (threads / doubles)-th
+// head, so that it reads its eight cosines and sines once.  Bound by HBM
+// where there are many rows (each byte is read and written once) and by the
+// chain sequence -> page -> store where there are few; a thread's first
+// kAhead heads are on their way before it starts on that chain.  25k tokens of
+// 48 heads of 128, fp16: 700 MB in 119 us, 0.88 of the measured copy rate; one
+// token 2.3 us, 288 tokens 3.3 us.
 constexpr int kAhead = 3;
 template <class T, bool NEIGHBOURS>
 __global__ void __launch_bounds__(kThreads)
@@ -173,7 +174,7 @@ append_kernel(const __grid_constant__ AppendParams p) {
   const int row = blockIdx.x, per = p.D / 16;
   const int first = div_by(threadIdx.x, p.by_half);
   const int i = threadIdx.x - first * per;
-  const int step = kThreads / per, heads = p.Hq + 2 * p.Hkv;
+  const int step = blockDim.x / per, heads = p.Hq + 2 * p.Hkv;
   const bool works = first < step;
   const bool turns = i * 16 < p.rot;
   // the double's chunks in a head: apart where pairs are, else neighbours
@@ -311,7 +312,12 @@ extern "C" sd_status sd_kv_append(
        cache->token_stride | cache->head_stride) % 8 == 0;
   const bool bf = cache->dt == SD_BF16;
   const void *kernel;
+  int threads = kThreads;
   if (wide) {
+    // few or small heads in small CTAs: 11k tokens of 6 heads of 64 take
+    // 9.4 us, with 256 threads a row 38.8
+    const long long all = (Hq + 2LL * cache->heads) * (D / 16);
+    if (all < kThreads) threads = (int)(all + 31) / 32 * 32;
     p.by_half = fast_div(D / 16);
     kernel = interleaved
                  ? (bf ? (const void *)append_kernel<__nv_bfloat16, true>
@@ -324,6 +330,6 @@ extern "C" sd_status sd_kv_append(
                 : (const void *)append_any_kernel<__half>;
   }
   void *args[] = {&p};
-  return launch_pdl(kernel, (unsigned)total, kThreads, 0,
+  return launch_pdl(kernel, (unsigned)total, threads, 0,
                     static_cast<cudaStream_t>(stream), args);
 }
