@@ -994,16 +994,11 @@ attention_kernel(const __grid_constant__ AttnParams p,
   if (warp == kMmaWarp) tmem_free_all(tmem);
 }
 
-// Joins the parts of cut units: a warp per row.  Block (x, y): the unit
-// that CTA x began, rows 8 y ...
-template <class T, int D, int ROWS>
-__global__ void __launch_bounds__(kThreads)
-attention_join_kernel(const __grid_constant__ AttnParams p) {
-  griddep_wait();
-  const CutUnit cut = p.cut[blockIdx.x];
-  const int r = blockIdx.y * kWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (cut.parts < 2 || r >= cut.rows) return;
+// A row of a cut unit from its parts (a warp), kAhead of them read at once.
+template <class T, int D, int ROWS, int kAhead>
+__device__ __forceinline__ void join_row(const AttnParams &p,
+                                         const CutUnit &cut, int r,
+                                         int lane) {
   auto slot = [&](int k) {
     return ((long long)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * ROWS + r;
   };
@@ -1025,10 +1020,10 @@ attention_join_kernel(const __grid_constant__ AttnParams p) {
                                   : ex2(ml.x - m);
     l += ml.y * w;
     const int n = min(cut.parts - k0, 32);
-    for (int k = 0; k < n; k += 2) {
-      float x[2][E];
+    for (int k = 0; k < n; k += kAhead) {
+      float x[kAhead][E];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kAhead; ++i) {
         const float *src =
             p.part_o + slot(min(k0 + k + i, cut.parts - 1)) * D + lane * E;
         if constexpr (E == 4) {
@@ -1040,7 +1035,7 @@ attention_join_kernel(const __grid_constant__ AttnParams p) {
         }
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kAhead; ++i) {
         const float wk = __shfl_sync(~0u, w, k + i);
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = fmaf(x[i][e], wk, o[e]);
@@ -1059,6 +1054,26 @@ attention_join_kernel(const __grid_constant__ AttnParams p) {
     dst[e / 2] = pack2<T>(o[e] * inv, o[e + 1] * inv);
   if (p.lse && lane == 0)
     p.lse[row] = l == 0.f ? -kInf : (m + log2f(l)) * kLn2;
+}
+
+// Joins the parts of cut units: a warp per row.  Block (x, y): the unit that
+// CTA x began, rows 8 y to 8 y + 7.  Where a long axis was cut into many parts
+// it is a chain of waits for L2: one head of 64 with 81 tokens behind 40k, the
+// whole call 50 us with parts read two at a time and 43 with sixteen.  Units
+// of two or three parts, which most are, would read more than they have that
+// way (64 tree nodes of 16 sequences: 73 us, two at a time 67).
+template <class T, int D, int ROWS>
+__global__ void __launch_bounds__(kThreads)
+attention_join_kernel(const __grid_constant__ AttnParams p) {
+  griddep_wait();
+  const CutUnit cut = p.cut[blockIdx.x];
+  const int r = blockIdx.y * kWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (cut.parts < 2 || r >= cut.rows) return;
+  if (cut.parts > 4)
+    join_row<T, D, ROWS, 16>(p, cut, r, lane);
+  else
+    join_row<T, D, ROWS, 2>(p, cut, r, lane);
 }
 
 // ------------------------------------------------------------------- host
