@@ -623,14 +623,15 @@ sd_status sd_kv_append(const sd_paged_kv *cache, const void *k,
  * page outside [0, num_pages) among the ones it reads (SD_DEV_BAD_PAGE),
  * get NaN.  Rows of no sequence are left as they are.  What the cache holds
  * at and past kv_len never reaches a result.  A NaN or an infinity in a
- * key or value before kv_len reaches the tokens that see it, and may reach
- * others of the sequence.
- * Products are of the cache's type with fp32 sums; the weights w_j are
- * rounded to the cache's type before they multiply v; maxima, sums and the
- * output's sum are fp32.
+ * key or value before kv_len reaches the tokens that see it (an infinite
+ * value perhaps as NaN), and may reach others of the sequence.
+ * Products are of the cache's type with fp32 sums; maxima, sums and the
+ * output's sum are fp32.  The weights w_j multiply v with twice the type's
+ * bits where max_q x q_heads / heads is at most 128, and rounded to the type
+ * beyond, which moves a result by about as much as its own rounding.
  *
- * max_q: the longest chunk, a hint: it picks the tile shape and never
- *     changes which results are computed.
+ * max_q: the longest chunk, a hint: it picks the tile shape (and with it the
+ *     weights' bits) and never changes which results are computed.
  * Workspace: sd_paged_attention_workspace(...) bytes with the same max_q.
  * ------------------------------------------------------------------- */
 size_t sd_paged_attention_workspace(int q_heads, int heads, int head_dim,

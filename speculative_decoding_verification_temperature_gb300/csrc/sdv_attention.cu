@@ -17,16 +17,27 @@
 // In a CTA, two warps load key and value tiles by TMA through the block
 // table, two issue the tensor-core products, and two warpgroups ("streams")
 // turn scores into weights, a thread per row.  S = Q K^T goes to tensor
-// memory; the weights, rounded to 16 bits (the tensor cores take two operands
+// memory; the weights, as 16-bit numbers (the tensor cores take two operands
 // of one type), go back there over S and are the first operand of O += W V.
 // With 256 rows each stream has 128 of them; with up to 128 rows (a few
 // drafts) both have the same rows and every other key tile, and their sums
-// are joined at the end of the unit.  The plain loop over keys with a warp
-// per (token, head) took 14 ms on 64 sequences of one token and 219 ms on
-// two prompt chunks; this takes 220 us and 555 us.
+// are joined at the end of the unit.
+//
+// With up to 128 rows a weight is the sum of two 16-bit numbers and O takes a
+// product of each: the tensor pipe is idle two thirds of the time there, and
+// the result is off by its own rounding alone.  Weights rounded once were
+// 0.0022 to 0.0026 off in bf16, by the inputs, where that rounding is 0.0017
+// (a few heavy keys of a few rows decide it); 9 tokens over 131072 keys took
+// 94 us so and take 96, 64 sequences of one token 220 and 229, 32 of nine 133
+// and 141.  With 256 rows, where the products are what it waits for, weights
+// are rounded once (0.0023).
+//
+// The plain loop over keys with a warp per (token, head) took 14 ms on 64
+// sequences of one token and 219 ms on two prompt chunks; this takes 229 us
+// and 555 us.
 //
 // What bounds it: HBM for a few rows a unit (1.41 GB of keys and values of 64
-// sequences in 220 us, 0.96 of the measured copy rate; a CTA keeps six tiles,
+// sequences in 229 us, 0.92 of the measured copy rate; a CTA keeps six tiles,
 // 192 KB, on their way), and for many rows the chain score product, softmax,
 // value product of a stream: 2750 cycles for two streams' 128 x 128 tiles
 // where the products alone take 2048 (1.47 PFLOP/s on chunks of 4096 and 2250
@@ -354,6 +365,30 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   return u;
 }
 
+// A pair as a sum of two 16-bit pairs.  bf16: the first is cut off, not
+// rounded (a byte permutation), and the second holds the 8 bits after it.
+template <class T>
+__device__ __forceinline__ void split2(float2 z, uint32_t &w, uint32_t &rest);
+template <>
+__device__ __forceinline__ void split2<__nv_bfloat16>(float2 z, uint32_t &w,
+                                                      uint32_t &rest) {
+  const uint32_t x = __float_as_uint(z.x), y = __float_as_uint(z.y);
+  w = __byte_perm(x, y, 0x7632);
+  const float2 r = fma2(make_float2(__uint_as_float(x & 0xffff0000u),
+                                    __uint_as_float(y & 0xffff0000u)),
+                        make_float2(-1.f, -1.f), z);
+  rest = pack2<__nv_bfloat16>(r.x, r.y);
+}
+template <>
+__device__ __forceinline__ void split2<__half>(float2 z, uint32_t &w,
+                                               uint32_t &rest) {
+  w = pack2<__half>(z.x, z.y);
+  const float2 r =
+      fma2(__half22float2(*reinterpret_cast<const __half2 *>(&w)),
+           make_float2(-1.f, -1.f), z);
+  rest = pack2<__half>(r.x, r.y);
+}
+
 // Bits of the 32 keys from `key` on that a row sees.  Causal: keys up to
 // `limit`.  Tree: the prefix, and the chunk's tokens in its mask.
 __device__ __forceinline__ uint32_t seen_bits(const AttnParams &p,
@@ -416,12 +451,12 @@ __device__ __forceinline__ float row_max(uint32_t s_addr, bool cuts,
   return m;
 }
 
-// 32 weights 2^(s sl + off), rounded and packed; their sums before the
-// rounding are added to `sum`.
-template <class T>
+// 32 weights 2^(s sl + off) as 16-bit pairs, with REST as two (see split2);
+// their sums before that are added to `sum`.
+template <class T, bool REST>
 __device__ __forceinline__ void weigh32(const uint32_t *x, float sl,
                                         float off, uint32_t *w,
-                                        float2 (&sum)[2]) {
+                                        uint32_t *rest, float2 (&sum)[2]) {
   const float2 k2 = make_float2(sl, sl), o2 = make_float2(off, off);
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
@@ -430,8 +465,16 @@ __device__ __forceinline__ void weigh32(const uint32_t *x, float sl,
     z.x = ex2(z.x);
     z.y = ex2(z.y);
     sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], z);
-    w[e >> 1] = pack2<T>(z.x, z.y);
+    if (REST) split2<T>(z, w[e >> 1], rest[e >> 1]);
+    else w[e >> 1] = pack2<T>(z.x, z.y);
   }
+}
+
+// Columns of the score tile where the weights of half a tile go: over the
+// scores of that half, which have been read by then.  With REST their second
+// numbers follow them.
+template <bool REST> constexpr int weight_col(int hf) {
+  return hf * (REST ? kHalf : kHalf / 2);
 }
 
 // A softmax thread's row: where its scores and sums lie, its reference m
@@ -449,7 +492,7 @@ struct Row {
 // ahead.  first: nothing is summed yet; parity: of the tile in the stream;
 // w_full, o_full: of the tile's halves.  Tiles that hide scores have a copy
 // of their own: a warp here runs on its scheduler's issue slots.
-template <class T, int D, bool HIDE>
+template <class T, int D, bool HIDE, bool REST>
 __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
                                            uint64_t *w_full, uint64_t *o_full,
                                            bool first, uint32_t parity,
@@ -459,7 +502,7 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
   tmem_ld32(row.s_addr, x[0]);
 #pragma unroll
   for (int hf = 0; hf < 2; ++hf) {
-    uint32_t w[kHalf / 2];
+    uint32_t w[kHalf / 2], rest[REST ? kHalf / 2 : 32];
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     float mt = -kInf;
     const float off = row.m == -kInf ? 0.f : -row.m * row.sl;
@@ -470,7 +513,8 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
       if (c < 3) tmem_ld32(row.s_addr + 32 * (c + 1), x[(c + 1) & 1]);
       if (HIDE) hide32(xc, seen[c]);
       mt = fmaxf(mt, max32(xc));
-      weigh32<T>(xc, row.sl, off, w + 16 * (c & 1), sum);
+      weigh32<T, REST>(xc, row.sl, off, w + 16 * (c & 1),
+                       rest + 16 * (c & 1), sum);
     }
     const bool raise = mt > -kInf && !((mt - row.m) * row.sl <= kSlack);
     if (__any_sync(~0u, raise)) {
@@ -505,11 +549,13 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
         tmem_ld32(row.s_addr + 32 * c, y);
         tmem_wait_ld();
         if (HIDE) hide32(y, seen[c]);
-        weigh32<T>(y, row.sl, to, w + 16 * (c & 1), sum);
+        weigh32<T, REST>(y, row.sl, to, w + 16 * (c & 1),
+                         rest + 16 * (c & 1), sum);
       }
       __syncwarp();
     }
-    tmem_st32(row.s_addr + hf * (kHalf / 2), w);
+    tmem_st32(row.s_addr + weight_col<REST>(hf), w);
+    if (REST) tmem_st32(row.s_addr + weight_col<REST>(hf) + kHalf / 2, rest);
     const float2 t = add2(sum[0], sum[1]);
     row.l += t.x + t.y;
     tmem_wait_st();
@@ -528,6 +574,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
                  const __grid_constant__ CUtensorMap v_map) {
   using L = Layout<D, PAIR>;
   constexpr int ROWS = L::kRows;
+  constexpr bool REST = !PAIR;
   constexpr bool BF16 = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ __align__(1024) char dyn[];  // swizzled tiles first
   Shared<D, PAIR> &s = *reinterpret_cast<Shared<D, PAIR> *>(dyn + L::kTiles);
@@ -701,11 +748,18 @@ attention_kernel(const __grid_constant__ AttnParams p,
         if (elect_one() && fine) {
           const uint32_t b = v_lo + v_at.slot * (L::kTileBytes / 16) +
                              hf * (kHalf * 128 / 16);
+          const uint32_t w = s_addr + weight_col<REST>(hf);
           tmem_fence_after();
 #pragma unroll
           for (int i = 0; i < kHalf / 16; ++i)
-            umma_ts<HI>(o_addr, s_addr + hf * (kHalf / 2) + i * 8,
-                        b + i * 16 * 128 / 16, O_DESC, !first || i > 0);
+            umma_ts<HI>(o_addr, w + i * 8, b + i * 16 * 128 / 16, O_DESC,
+                        !first || i > 0);
+          if (REST) {
+#pragma unroll
+            for (int i = 0; i < kHalf / 16; ++i)
+              umma_ts<HI>(o_addr, w + kHalf / 2 + i * 8,
+                          b + i * 16 * 128 / 16, O_DESC, true);
+          }
           umma_commit(&s.o_full[st][hf]);
           if (hf) umma_commit(&s.empty[vr][v_at.slot]);
         }
@@ -873,10 +927,10 @@ attention_kernel(const __grid_constant__ AttnParams p,
           }
           __syncwarp();
           if (i == 0) row.m = row_max(row.s_addr, cuts, seen);
-          fine = cuts ? weigh_tile<T, D, true>(row, seen, s.w_full[st],
+          fine = cuts ? weigh_tile<T, D, true, REST>(row, seen, s.w_full[st],
                                                s.o_full[st], i == 0, tn & 1,
                                                &s.abort, p.dev_status)
-                      : weigh_tile<T, D, false>(row, seen, s.w_full[st],
+                      : weigh_tile<T, D, false, REST>(row, seen, s.w_full[st],
                                                 s.o_full[st], i == 0, tn & 1,
                                                 &s.abort, p.dev_status);
           if (!fine) break;

@@ -111,9 +111,11 @@ def append_tol(exact, size, dtype):
         (2.0 ** -25 if dtype == torch.float16 else 0.0)
 
 
-def attention(P, q, scale, see=None):
+def attention(P, q, scale, see=None, split=False):
     """64-bit attention of a Paged batch: out, lse and the bounds of their
-    errors.  see: list of [n, n] truth tables of the chunk (None: causal)."""
+    errors.  see: list of [n, n] truth tables of the chunk (None: causal).
+    split: weights are sums of two numbers of the type, the first perhaps cut
+    off (2 u away at most) and the second rounded (u of that)."""
     q64 = f64(q)
     Hq, D = q64.shape[1:]
     G = Hq // P.heads
@@ -121,6 +123,7 @@ def attention(P, q, scale, see=None):
     lse = np.full((P.total, Hq), -np.inf)
     tol, ltol = np.zeros_like(out), np.zeros((P.total, Hq))
     u = U[P.dtype]
+    uw = 2 * u * u if split else u
     for b, (n, kv) in enumerate(zip(P.n, P.kv)):
         k, v = P.gather(P.k, b), P.gather(P.v, b)
         ok = np.zeros((n, kv), bool)
@@ -149,7 +152,7 @@ def attention(P, q, scale, see=None):
                 size = w @ np.abs(vh) / l
                 # weights rounded to the type (fp16 also in its subnormal
                 # range), their exponents off by d, the sums, the output
-                tol[r, h] = size * (u * 1.01 + 2 * d + 2 * kv * U32) + \
+                tol[r, h] = size * (uw * 1.01 + 2 * d + 2 * kv * U32) + \
                     u * np.abs(out[r, h]) * 1.01 + \
                     (ok[i].sum() * 2.0 ** -24 * np.abs(vh[ok[i]]).max()
                      + 2.0 ** -24 if P.dtype == torch.float16 else 0)

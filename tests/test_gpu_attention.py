@@ -59,6 +59,23 @@ def test_lengths(dtype, D, n, kv):
         max_q=max(n))
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,kv,Hq", [([1], [700], 4), ([9, 3], [260, 1000], 8),
+                                     ([64], [64], 4), ([5], [100], 2)])
+def test_few_rows_are_off_by_the_outputs_rounding(dtype, D, n, kv, Hq):
+    """With up to 128 rows a head the weights keep twice the type's bits."""
+    P = ref.Paged(n, kv, 2, D, 16, dtype, seed=sum(kv) + Hq)
+    q = P.rows(Hq, by=2.0)
+    start, lens = P.lengths()
+    got = api.paged_attention(
+        q.cuda(), api.PagedKV(P.to_gpu(P.k), P.to_gpu(P.v), P.table.cuda()),
+        start, lens, max_q=max(n), workspace=api.Workspace())
+    out, _, tol, _ = ref.attention(P, q, D ** -0.5, split=True)
+    assert (np.abs(ref.f64(got["out"] if isinstance(got, dict) else got)
+                   - out) <= tol).all()
+
+
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 1), (5, 5), (10, 2), (16, 1),
                                     (71, 1), (130, 1), (14, 2)])
 @pytest.mark.parametrize("n", [1, 4])
