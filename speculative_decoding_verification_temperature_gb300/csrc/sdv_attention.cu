@@ -24,13 +24,13 @@
 // are joined at the end of the unit.
 //
 // With up to 128 rows a weight is the sum of two 16-bit numbers and O takes a
-// product of each: the tensor pipe is idle two thirds of the time there, and
-// the result is off by its own rounding alone.  Weights rounded once were
-// 0.0022 to 0.0026 off in bf16, by the inputs, where that rounding is 0.0017
-// (a few heavy keys of a few rows decide it); 9 tokens over 131072 keys took
-// 94 us so and take 96, 64 sequences of one token 220 and 229, 32 of nine 133
-// and 141.  With 256 rows, where the products are what it waits for, weights
-// are rounded once (0.0023).
+// product of each (with one the tensor pipe is busy a third of the time, with
+// two 41 to 48 %), so that the result is off by its own rounding alone.
+// Weights rounded once were 0.0022 to 0.0026 off in bf16, by the inputs, where
+// that rounding is 0.0017 (a few heavy keys of a few rows decide it); 9 tokens
+// over 131072 keys took 94 us so and take 96, 64 sequences of one token 220
+// and 229, 32 of nine 133 and 141.  With 256 rows, where the products are what
+// it waits for, weights are rounded once (0.0023).
 //
 // The plain loop over keys with a warp per (token, head) took 14 ms on 64
 // sequences of one token and 219 ms on two prompt chunks; this takes 229 us
