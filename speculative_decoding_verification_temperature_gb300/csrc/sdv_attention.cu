@@ -326,6 +326,7 @@ template <int D, bool PAIR> struct Shared {
   uint64_t full[2][L::kN0], empty[2][L::kN0];
   uint64_t q_full[2], s_full[2], turn[2], drain[2];
   uint64_t w_full[2][2], o_full[2][2];  // of a stream's tile halves
+  uint64_t idle;  // stream 1 has no tile: its product warp saw the queries
   uint32_t tmem;
   volatile int abort;
   int bad[kBadRing];  // unit count whose pages were bad
@@ -598,6 +599,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
       }
       mbar_init(&s.turn[i], 1);
     }
+    mbar_init(&s.idle, 1);
     mbar_init(&s.drain[0], 1);
     mbar_init(&s.drain[1], 1);
     s.abort = 0;
@@ -802,6 +804,9 @@ attention_kernel(const __grid_constant__ AttnParams p,
           tmem_fence_after();
           scores();
           if (turns) pass_turn();
+        } else if (!PAIR) {
+          if (elect_one() && fine) mbar_arrive(&s.idle);
+          __syncwarp();
         }
         for (int i = i0; i < cnt; i += step) {
           const bool more = i + step < cnt;
@@ -833,6 +838,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 lanes << 16
     const float sl = p.scale_log2;
     unsigned tn = 0;  // tiles of this stream seen
+    uint32_t idle_p = 0;
     if (tid == 0) p.cut[blockIdx.x].parts = 0;
     const int base_row = PAIR ? st * kTile : 0;
     // a stream without rows takes no part in a unit
@@ -947,6 +953,14 @@ attention_kernel(const __grid_constant__ AttnParams p,
         role_wait(&s.o_full[st][1], (tn - 1) & 1, &s.abort, p.dev_status);
         __syncwarp();
         tmem_fence_after();
+      } else if (!PAIR) {
+        // One tile, and it is stream 0's: nothing else holds the queries back
+        // until product warp 1 has seen these.  Were they replaced twice
+        // before it looks, their barrier would show it the parity that it is
+        // waiting to see end.
+        role_wait(&s.idle, idle_p, &s.abort, p.dev_status);
+        idle_p ^= 1;
+        __syncwarp();
       }
       // the two streams' sums of the same rows are joined; stream st then
       // writes column half st.  256 rows: each its own rows, all columns.

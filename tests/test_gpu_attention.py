@@ -357,3 +357,29 @@ def test_many_sequences(hint):
     # the shares move, so a unit may be cut elsewhere: another order of sums
     err = (got[~rows].float() - want[~rows].float()).abs()
     assert bool((err <= 2.0 ** -7 * want[~rows].float().abs() + 1e-3).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("many", [False, True])
+def test_units_of_one_tile_among_longer_ones(D, many):
+    """Sequences of one key tile, of which one stream of a unit has nothing,
+    between sequences of two and more; several units an SM, calls queued
+    without waiting: no wait gives up, and every call has the same bits."""
+    r = np.random.default_rng(D + many)
+    B = 1200 if many else 300
+    kv = np.where(r.random(B) < 0.8, r.integers(1, 129, B),
+                  r.integers(129, 600, B)).tolist()
+    P = ref.Paged([1] * B, kv, 2, D, 64, BF, seed=D)
+    got = run(P, 4, max_q=1) if not many else None
+    cache = api.PagedKV(P.to_gpu(P.k), P.to_gpu(P.v), P.table.cuda())
+    q = P.rows(4, by=2.0).cuda()
+    start, lens = P.lengths()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = api.Workspace()
+    outs = [api.paged_attention(q, cache, start, lens, max_q=1, status=st,
+                                workspace=ws)["out"] for _ in range(60)]
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    assert bool(torch.isfinite(outs[0]).all())
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    assert many or got["out"].shape == outs[0].shape
