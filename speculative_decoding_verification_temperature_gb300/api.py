@@ -184,20 +184,40 @@ def _stream(device):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _raw_stream(device):
+    """The current stream's handle (without a Stream object around it where
+    torch has a call for that: 2 us less)."""
+    if _get_raw_stream is not None and device.index is not None:
+        return _get_raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
 class Workspace:
-    """Per-device scratch buffer for the library's work-queue counter.
-    Reused across calls on the same stream; give each concurrent stream its
-    own Workspace."""
+    """Scratch buffers of the calls that need one (work-queue counters, the
+    records and partial sums that one kernel of a call leaves to the next).
+
+    Each device, stream and host thread has its own, so calls on several
+    streams or from several threads share nothing; the default that calls
+    without ``workspace`` use is one of these.  A buffer that becomes too
+    small is kept beside the larger one, so that a captured CUDA graph never
+    writes to memory that something else has.  Graphs captured on one stream
+    by one thread do share a buffer: give those that are replayed at the same
+    time, or beside other calls on the capture's stream, a Workspace each."""
 
     def __init__(self):
         self._buf = {}
+        self._outgrown = []
 
     def get(self, device, nbytes):
-        b = self._buf.get(device)
+        key = device, _raw_stream(device), threading.get_ident()
+        b = self._buf.get(key)
         if b is None or b.numel() < nbytes:
+            if b is not None:  # doubled: what is kept stays below what is used
+                self._outgrown.append(b)
+                nbytes = max(nbytes, 2 * b.numel())
             b = torch.empty(max(nbytes, 256), dtype=torch.uint8,
                             device=device)
-            self._buf[device] = b
+            self._buf[key] = b
         return b
 
 
@@ -710,14 +730,6 @@ def _lengths(cache, q_start, kv_len):
     return B, qp, kp
 
 
-def _raw_stream(device):
-    """The current stream's handle (without a Stream object around it where
-    torch has a call for that: 2 us less)."""
-    if _get_raw_stream is not None and device.index is not None:
-        return _get_raw_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
-
-
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -772,7 +784,8 @@ def paged_attention(q, cache, q_start, kv_len, *, max_q=None, scale=None,
     int32.  tree_mask [total, words] int32 (None: causal): the tokens of its
     own chunk that each token sees, as bits.  max_q: the longest chunk, a
     hint that only picks the tile shape (default: the mean chunk).  scale
-    defaults to D ** -0.5.  Returns out [total, q_heads, D] (and lse [total,
+    defaults to D ** -0.5.  workspace: scratch between the call's two kernels
+    (default: the current stream's and thread's own).  Returns out [total, q_heads, D] (and lse [total,
     q_heads] float32 when want_lse)."""
     dev, D = cache.device, cache.head_dim
     total, Hq, qs = _rows(q, cache, "q")

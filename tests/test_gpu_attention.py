@@ -383,3 +383,57 @@ def test_units_of_one_tile_among_longer_ones(D, many):
     assert bool(torch.isfinite(outs[0]).all())
     assert all(torch.equal(o, outs[0]) for o in outs)
     assert many or got["out"].shape == outs[0].shape
+
+
+def test_two_streams_without_a_workspace():
+    """Calls of different shapes queued on two streams at once, whose units
+    are cut (each leaves records and partial sums to a second kernel)."""
+    calls = []
+    for n, kv, heads, D in (([9], [6000], 2, 64), ([2, 1], [3000, 900], 1, 128)):
+        P = ref.Paged(n, kv, heads, D, 16, BF, seed=D)
+        calls.append((P.rows(4 * heads).cuda(), api.PagedKV(
+            P.k.cuda(), P.v.cuda(), P.table.cuda()), *P.lengths()))
+    want = [api.paged_attention(*c)["out"] for c in calls]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(50):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(api.paged_attention(*calls[i])["out"])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in got[i])
+
+
+def test_a_graph_keeps_its_workspace():
+    """A captured call, replayed after a larger call on the same Workspace and
+    stream and after new tensors have taken what was free: the same bits, and
+    nothing is written into those tensors."""
+    small = ref.Paged([9], [3000], 1, 64, 16, BF, seed=3)
+    large = ref.Paged([80], [700], 2, 128, 16, BF, seed=4)
+
+    def args(P, Hq):
+        return (P.rows(Hq).cuda(), api.PagedKV(
+            P.k.cuda(), P.v.cuda(), P.table.cuda()), *P.lengths())
+    a, b = args(small, 4), args(large, 8)
+    ws, s = api.Workspace(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        want = api.paged_attention(*a, workspace=ws)["out"]
+        first = ws.get(a[1].device, 1)
+        size = first.numel()
+        del first
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            out = api.paged_attention(*a, workspace=ws)["out"]
+        api.paged_attention(*b, workspace=ws)
+        assert ws.get(a[1].device, 1).numel() > size
+        torch.cuda.synchronize()
+        taken = [torch.full((size,), 7, dtype=torch.uint8, device="cuda")
+                 for _ in range(4)]
+        for _ in range(3):
+            g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert all(bool((t == 7).all()) for t in taken)

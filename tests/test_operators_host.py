@@ -215,3 +215,32 @@ def test_formulas_against_torch():
             yb = y[r_][:, 1:8:2] if inter else y[r_][:, 4:8]
             np.testing.assert_allclose(ya + 1j * yb, w, atol=1e-14)
         np.testing.assert_array_equal(y[:, :, 8:], x[:, :, 8:])
+
+
+def test_workspace_buffers_are_not_shared(monkeypatch):
+    """A device, stream and thread each have their own buffer, and one that a
+    call outgrows stays allocated (a captured graph may write to it)."""
+    import gc
+    import threading
+    import weakref
+    stream = [1]
+    monkeypatch.setattr(api, "_raw_stream", lambda device: stream[0])
+    ws, dev = api.Workspace(), torch.device("cpu")
+    a = ws.get(dev, 1000)
+    assert ws.get(dev, 1000) is a and ws.get(dev, 10) is a
+    stream[0] = 2
+    b = ws.get(dev, 1000)
+    assert b.data_ptr() != a.data_ptr()
+    other = []
+    t = threading.Thread(target=lambda: other.append(ws.get(dev, 1000)))
+    t.start()
+    t.join()
+    assert other[0].data_ptr() not in (a.data_ptr(), b.data_ptr())
+    stream[0] = 1
+    assert ws.get(dev, 1000) is a
+    old = weakref.ref(a)
+    del a
+    c = ws.get(dev, 5000)
+    gc.collect()
+    assert c.numel() >= 5000 and old() is not None
+    assert ws.get(dev, 5000) is c
