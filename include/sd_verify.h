@@ -628,10 +628,13 @@ sd_status sd_kv_append(const sd_paged_kv *cache, const void *k,
  * Products are of the cache's type with fp32 sums; maxima, sums and the
  * output's sum are fp32.  The weights w_j multiply v with twice the type's
  * bits where max_q x q_heads / heads is at most 128, and rounded to the type
- * beyond, which moves a result by about as much as its own rounding.
+ * beyond, which moves a result by about as much as its own rounding.  fp16
+ * weights are also off by up to 2^-17 of the largest among the 64 keys of
+ * theirs (keys 64 i to 64 i + 63), and by 2^-28 of the row's largest beside
+ * that key and where the mask hides some of the 64.
  *
- * max_q: the longest chunk, a hint: it picks the tile shape (and with it the
- *     weights' bits) and never changes which results are computed.
+ * max_q: the longest chunk, a hint: it picks the tile shape, and with it the
+ *     weights' bits as above, never which results are computed.
  * Workspace: sd_paged_attention_workspace(...) bytes with the same max_q.
  * ------------------------------------------------------------------- */
 size_t sd_paged_attention_workspace(int q_heads, int heads, int head_dim,

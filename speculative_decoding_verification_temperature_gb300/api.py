@@ -783,7 +783,9 @@ def paged_attention(q, cache, q_start, kv_len, *, max_q=None, scale=None,
     q [total, q_heads, D], rows may be strided; q_start [B+1], kv_len [B]
     int32.  tree_mask [total, words] int32 (None: causal): the tokens of its
     own chunk that each token sees, as bits.  max_q: the longest chunk, a
-    hint that only picks the tile shape (default: the mean chunk).  scale
+    hint that picks the tile shape (default: the mean chunk), and with it
+    whether weights are rounded to the type before they multiply the values
+    (max_q x q_heads / heads above 128) or keep twice its bits.  scale
     defaults to D ** -0.5.  workspace: scratch between the call's two kernels
     (default: the current stream's and thread's own).  Returns out [total, q_heads, D] (and lse [total,
     q_heads] float32 when want_lse)."""

@@ -25,7 +25,8 @@
 //
 // With up to 128 rows a weight is the sum of two 16-bit numbers and O takes a
 // product of each (with one the tensor pipe is busy a third of the time, with
-// two 41 to 48 %), so that the result is off by its own rounding alone.
+// two 41 to 48 %), so that the result is off by little more than its own
+// rounding (fp16's range has its limits: see Scale).
 // Weights rounded once were 0.0022 to 0.0026 off in bf16, by the inputs, where
 // that rounding is 0.0017 (a few heavy keys of a few rows decide it); 9 tokens
 // over 131072 keys took 94 us so and take 96, 64 sequences of one token 220
@@ -63,11 +64,29 @@ constexpr int kAttnThreads = 384;  // two warpgroups of softmax, one of roles
 constexpr int kMmaWarp = 9;  // and 10; warps 8 and 11 load
 constexpr int kBadRing = 64;     // units whose bad-page mark is kept
 constexpr float kLn2 = 0.693147180559945f;
-// A row's reference moves only when its maximum is 2^15 above it: weights
-// stay inside fp16's range (bf16's is wider), their relative rounding is the
-// same at any scale, and hardly a tile rescales anything.  (At 2^8 the rows
-// of a prompt tile did so in one tile of ten, for half a tile's time each.)
-constexpr float kSlack = 15.f;
+// A row's weights are 2^kBias at its reference m, and m moves up only when the
+// scores' maximum is 2^kSlack above it: weights stay at or below 2^15, inside
+// fp16's range, and hardly a tile rescales anything.  (With a slack of 2^8 the
+// rows of a prompt tile did so in one tile of ten, for half a tile's time
+// each.)  bf16 has fp32's exponents: its weights keep their bits at any scale.
+// fp16 weights below 2^-14 lose bits and those below 2^-25 are gone, while l
+// counts them in full.  So in fp16 a reference is worth 2^3, and it moves DOWN
+// to the maximum of a half tile whose weights all lie 2^kDrop below it (one of
+// thousands, perhaps, that matter beside a key far above them).  A weight is
+// off by its own rounding, or by 2^-17 of the largest of its 64 keys; beside
+// a key that set the reference, and in a half that hides keys, by 2^-28 of the
+// reference's.  Sums grow by a move down, by 2^kMostUp at most, and once they
+// are kTop none is made: what lies below is then no part of the result's bits.
+// For this, fp16 takes 1 to 3 % more (without bias and moves down, two prompt
+// chunks of D = 128 took 559 us and take 578, 16 trees of 64 nodes 69 and 71,
+// 9 tokens over 131072 keys 97 and 99.5); a bias of 2^7 cost 6 to 7 %.
+template <class T> struct Scale {
+  static constexpr float kSlack = 15.f, kBias = 0.f, kDrop = kInf;
+};
+template <> struct Scale<__half> {
+  static constexpr float kSlack = 12.f, kBias = 3.f, kDrop = 11.f;
+};
+constexpr float kTop = 0x1p50f, kMostUp = 60.f;
 
 struct AttnParams {
   const void *q;
@@ -488,17 +507,18 @@ struct Row {
 // The weights of one row in one tile, half a tile at a time, so that the
 // values of one half are summed while the other is weighed.  They are taken
 // against the reference at hand while the scores' maximum is still being
-// found; where it turns out too far above (rare), the sums are scaled down
-// and the half is weighed once more.  Chunks of 32 scores are fetched one
-// ahead.  first: nothing is summed yet; parity: of the tile in the stream;
-// w_full, o_full: of the tile's halves.  Tiles that hide scores have a copy
-// of their own: a warp here runs on its scheduler's issue slots.
+// found; where it turns out too far above or, in fp16, below (both rare), the
+// sums are scaled and the half is weighed once more.  Chunks of 32 scores are
+// fetched one ahead.  first: nothing is summed yet; parity: of the tile in the
+// stream; w_full, o_full: of the tile's halves.  Tiles that hide scores have a
+// copy of their own: a warp here runs on its scheduler's issue slots.
 template <class T, int D, bool HIDE, bool REST>
 __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
                                            uint64_t *w_full, uint64_t *o_full,
                                            bool first, uint32_t parity,
                                            volatile int *abort,
                                            int32_t *dev_status) {
+  using S = Scale<T>;
   uint32_t x[2][32];
   tmem_ld32(row.s_addr, x[0]);
 #pragma unroll
@@ -506,7 +526,7 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
     uint32_t w[kHalf / 2], rest[REST ? kHalf / 2 : 32];
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     float mt = -kInf;
-    const float off = row.m == -kInf ? 0.f : -row.m * row.sl;
+    const float off = row.m == -kInf ? 0.f : S::kBias - row.m * row.sl;
 #pragma unroll
     for (int c = 2 * hf; c < 2 * hf + 2; ++c) {
       uint32_t *xc = x[c & 1];
@@ -517,11 +537,15 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
       weigh32<T, REST>(xc, row.sl, off, w + 16 * (c & 1),
                        rest + 16 * (c & 1), sum);
     }
-    const bool raise = mt > -kInf && !((mt - row.m) * row.sl <= kSlack);
-    if (__any_sync(~0u, raise)) {
+    constexpr bool DROPS = S::kDrop < kInf;
+    const float up = (mt - row.m) * row.sl;
+    bool move = mt > -kInf && !(up <= S::kSlack);
+    if (DROPS && (!HIDE || (seen[2 * hf] & seen[2 * hf + 1]) == ~0u))
+      move = move || (up < -S::kDrop && row.l < kTop);
+    if (__any_sync(~0u, move)) {
       float f = 1.f;
-      if (raise) {
-        f = row.m == -kInf ? 1.f : ex2((row.m - mt) * row.sl);
+      if (move) {
+        f = row.m == -kInf ? 1.f : ex2(DROPS ? fminf(-up, kMostUp) : -up);
         row.m = mt;
       }
       row.l *= f;
@@ -542,7 +566,7 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
           tmem_st32(row.o_addr + c, o);
         }
       }
-      const float to = row.m == -kInf ? 0.f : -row.m * row.sl;
+      const float to = row.m == -kInf ? 0.f : S::kBias - row.m * row.sl;
       sum[0] = sum[1] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int c = 2 * hf; c < 2 * hf + 2; ++c) {
@@ -996,9 +1020,11 @@ attention_kernel(const __grid_constant__ AttnParams p,
         const float inv = l == 0.f ? 0.f : 1.f / l;
         if (whole) f0 *= inv, f1 *= inv;
         if (mine && (PAIR || st == 0)) {
-          if (!whole) p.part_ml[part] = make_float2(m * sl, l);
+          // l counts 2^kBias for a weight of 1
+          const float ref = m * sl - Scale<T>::kBias;
+          if (!whole) p.part_ml[part] = make_float2(ref, l);
           else if (p.lse)
-            p.lse[to] = l == 0.f ? -kInf : (m * sl + log2f(l)) * kLn2;
+            p.lse[to] = l == 0.f ? -kInf : (ref + log2f(l)) * kLn2;
         }
         T *out = (T *)p.out + to * D + c_lo;
         float *part_o = p.part_o + part * D + c_lo;

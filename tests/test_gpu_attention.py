@@ -389,7 +389,8 @@ def test_two_streams_without_a_workspace():
     """Calls of different shapes queued on two streams at once, whose units
     are cut (each leaves records and partial sums to a second kernel)."""
     calls = []
-    for n, kv, heads, D in (([9], [6000], 2, 64), ([2, 1], [3000, 900], 1, 128)):
+    for n, kv, heads, D in (([9], [6000], 2, 64),
+                            ([2, 1], [3000, 900], 1, 128)):
         P = ref.Paged(n, kv, heads, D, 16, BF, seed=D)
         calls.append((P.rows(4 * heads).cuda(), api.PagedKV(
             P.k.cuda(), P.v.cuda(), P.table.cuda()), *P.lengths()))
@@ -437,3 +438,61 @@ def test_a_graph_keeps_its_workspace():
     torch.cuda.synchronize()
     assert torch.equal(out, want)
     assert all(bool((t == 7).all()) for t in taken)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("hint", [1, 400])
+@pytest.mark.parametrize("heavy", [(0,), (4095,), (0, 1700, 1701, 3000)])
+@pytest.mark.parametrize("below,size", [(11.5, 1.0), (17.3, 8.0),
+                                        (24.0, 4096.0)])
+def test_few_heavy_keys_of_no_value_over_thousands(D, hint, heavy, below,
+                                                   size):
+    """fp16, a few keys whose values are 0 and thousands of others `below`
+    nats under them (to 2^-34 of their weight), which are the whole result.
+
+    Bound: a weight is off by its rounding (u; as two numbers less) and by
+    2^-17 of the largest of its 64 keys, which lie within 2 nats of each other
+    unless a heavy one is among them: then by 2^-28 of that, and by no more
+    than itself; scores off by d; the sums; the output's rounding."""
+    B, H, G, kv, page = 20, 8, 2, 4096, 64
+    g = torch.Generator(device="cuda").manual_seed(D + hint)
+    score = torch.rand(B, kv, H, generator=g, device="cuda") * 2 - 1 - below
+    score[:, list(heavy)] = 0
+    k = torch.zeros(B, kv, H, D, device="cuda")
+    k[..., 3] = (score + 12) * 0.25
+    v = (torch.rand(B, kv, H, D, generator=g, device="cuda") + 0.5) * size
+    v[:, list(heavy)] = 0
+    k, v = k.to(HF), v.to(HF)
+    q = torch.zeros(B, G * H, D, device="cuda", dtype=HF)
+    q[..., 3] = 4.0
+    table = torch.randperm(B * kv // page, generator=g, device="cuda").to(
+        torch.int32)
+    pages = [torch.empty(B * kv // page, page, H, D, dtype=HF, device="cuda")
+             for _ in range(2)]
+    for p, x in zip(pages, (k, v)):
+        p[table.long()] = x.view(-1, page, H, D)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = api.paged_attention(
+        q, api.PagedKV(*pages, table.view(B, -1)),
+        torch.arange(B + 1, dtype=torch.int32, device="cuda"),
+        torch.full((B,), kv, dtype=torch.int32, device="cuda"), max_q=hint,
+        scale=1.0, want_lse=True, status=st, workspace=api.Workspace())
+    assert int(st.item()) == 0
+    s = torch.einsum("bhgd,bjhd->bhgj", q.view(B, H, G, D).double(),
+                     k.double())
+    lse = torch.logsumexp(s, -1)
+    w = torch.exp(s - lse[..., None])
+    out = torch.einsum("bhgj,bjhd->bhgd", w, v.double())
+    u = ref.U[HF]
+    top = s.abs().max().item()
+    d = 2 * ref.U32 * (D + 8) * top + 2.0 ** -20 + top * 4 * ref.U32
+    # v >= 0: out is also the sum of the terms' sizes
+    tol = out * (u * 1.01 + 2 * d + 2 * kv * ref.U32 + 2.0 ** -17 * np.e ** 2)
+    tol += 64 * len(heavy) * min(2.0 ** -28, np.exp(1 - below)) * \
+        v.max().item()
+    tol += u * 1.01 * out + 2.0 ** -24
+    err = (got["out"].view(B, H, G, D).double() - out).abs()
+    assert bool((err <= tol).all()), (err / out).max().item()
+    ltol = d + kv * ref.U32 + 128 * ref.U32
+    assert bool(((got["lse"].view(B, H, G).double() - lse).abs()
+                 <= ltol).all())
