@@ -672,12 +672,14 @@ sd_status sd_paged_attention(const void *q, long long q_stride, int q_heads,
  * and sets SD_DEV_BAD_TOKEN (padding's logits are not looked at).  An entry
  * with logit -inf has p = 0 and adds nothing, whatever the student's logit.
  * Repeated ids each count.  A row without usable entries has loss 0 and
- * gradient 0.  A student logit of -inf has q = 0.  A row (student's or
- * teacher's) that holds NaN or +inf, a teacher_lse that is not finite, or a
- * student row without a logit above -3e38, has loss and lse NaN, gradient
- * NaN and sets SD_DEV_NONFINITE (the backward call goes by the lse it is
- * given).  A row with grad_loss exactly 0 gets a gradient of exactly 0 (its
- * student row is not read by the backward call).
+ * gradient 0.  A student logit of -inf has q = 0, and so has any number far
+ * below the row's largest.  A row (student's or teacher's) that holds NaN or
+ * +inf, a teacher_lse that is not finite, or a student row without a logit
+ * above -1e38 and -1e9 T, has loss and lse NaN, gradient NaN and sets
+ * SD_DEV_NONFINITE (a student row whose largest logit is above 1e9 T may do
+ * so; logits below -2e38 T count as -inf; the backward call goes by the lse
+ * it is given).  A row with grad_loss exactly 0 gets a gradient of exactly 0
+ * (its student row is not read by the backward call).
  * grad may be the student's own buffer (same pointer and stride).
  * sd_distill_topk_step is the forward and the backward call together.
  * ------------------------------------------------------------------- */

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kThreads)
     a = block_reduce_am(a, ared);
     if (threadIdx.x == 0) p.apart[(size_t)rr * p.S + s] = a;
   } else {
-    MS st[1] = {ms_empty()};
+    MS st[1] = {ms_start(p.k2)};
     MS unused = ms_empty();
     stats_pass<DT, VW>(row, row, false, sl, p.k2, st[0], unused);
     block_reduce_ms<1>(st, p.k2, red);

@@ -142,10 +142,10 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 // ------------------------------------------------- online softmax state
 // Row statistics at temperature T with k2 = log2(e) / T:
 //   m = max_j z_j,  s = sum_j 2^(z_j k2 - m k2)
-// so that p_j = 2^(z_j k2 - m k2) / s.  The empty state holds m = kMEmpty
-// (finite, below any usable logit) so the hot loop needs no test for
-// "nothing seen yet": -inf entries add 2^-inf = 0.  NaN anywhere makes s
-// NaN; +inf makes m infinite; a row of only -inf leaves m at kMEmpty and
+// so that p_j = 2^(z_j k2 - m k2) / s.  A state's m starts finite and below any
+// usable logit (see ms_start; kMEmpty where states are only merged) so the
+// hot loop needs no test for "nothing seen yet": -inf entries add 2^-inf = 0.
+// NaN anywhere makes s NaN; +inf makes m infinite; a row of only -inf leaves
 // s = 0: all three are "invalid".
 constexpr float kMEmpty = -3.0e38f;
 
@@ -155,6 +155,15 @@ struct MS {
 };
 
 __device__ __forceinline__ MS ms_empty() { return {kMEmpty, 0.f}; }
+
+// The state that a pass over logits starts from: nothing seen, and m k2 =
+// -2^31.  Masked columns, -inf or any number further down, are then counted
+// against it and weigh nothing.  Counted against each other they could
+// overflow: -m k2 does from 3.4e38 on, and the rounding of m k2 alone is
+// hundreds where it is 2^32 and more.
+__device__ __forceinline__ MS ms_start(float k2) {
+  return {fmaxf(kMEmpty, __fdividef(-0x1p31f, k2)), 0.f};
+}
 
 __device__ __forceinline__ MS ms_merge(MS a, MS b, float k2) {
   const float m = fmaxf(a.m, b.m);
@@ -215,10 +224,7 @@ __device__ __forceinline__ void ms_add_v(MS &st, const Raw<DT, VW> &r,
     st.s *= ex2((st.m - vmax) * k2);
     st.m = vmax;
   }
-  // while nothing finite has been seen (m still the empty value, every
-  // element so far -inf) the offset would overflow (-m k2 = +inf, and
-  // -inf k2 + inf is NaN); 0 gives those elements their weight 0
-  const float mk = st.m > kMEmpty ? -st.m * k2 : 0.f;
+  const float mk = -st.m * k2;
   if constexpr (VW == 1) {
     st.s += ex2(fmaf(z[0], k2, mk));
   } else {

@@ -354,7 +354,7 @@ distill_row_kernel(const __grid_constant__ DistillParams p) {
   // before anything is written (the gradient may go to the student's rows)
   if (warp == WARPS - 1 && (rank == 0 || STEP))
     load_teacher(p, row, t, r, 0, p.V);
-  MS st = ms_empty();
+  MS st = ms_start(k2);
   float vmax;
   for (int b = 0; b < batches; ++b) {
     const int n = b * RUN + tid;
@@ -604,7 +604,7 @@ distill_step_kernel(const __grid_constant__ DistillParams p, int chunks) {
       const int s1 = (int)((long long)r.slots * (rank + 1) / p.CL);
       const float w = __ldg(p.grad_loss + row);
       // ---- log sum exp
-      MS st = ms_empty();
+      MS st = ms_start(k2);
       float vmax;
       for (int i = 0; i < chunks; ++i) {
         wait(&s.full[read.slot], read.parity);

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (tid == 0) sh.apart[par][r0 + 1] = c;
           }
         } else {
-          MS st[2] = {ms_empty(), ms_empty()};
+          MS st[2] = {ms_start(k2), ms_start(k2)};
           stats_pass<DT, VW>(ra, rb, two, sl, k2, st[0], st[1]);
           block_reduce_ms<2>(st, k2, sh.red);
           if (tid == 0) {
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           a = block_reduce_am(a, sh.ared);
           if (tid == 0) sh.apart[par][0] = a;
         } else {
-          MS st[2] = {ms_empty(), ms_empty()};
+          MS st[2] = {ms_start(k2), ms_start(k2)};
           stats_pass<DT, VW>(ra, ra, false, sl, k2, st[0], st[1]);
           block_reduce_ms<2>(st, k2, sh.red);
           if (tid == 0) sh.part[par][0] = st[0];

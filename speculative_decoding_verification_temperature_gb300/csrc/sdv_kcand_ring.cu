@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 4)
   // One row through the ring: per-thread online state, folded into the
   // per-warp partial of row r at the end.
   auto stream_row = [&](int r) {
-    MS st = ms_empty();
+    MS st = ms_start(k2);
     AM am = am_empty();
     for (int c = 0; c < nch; ++c) {
       const int v0 = sl.vbeg + c * kStageVecs;

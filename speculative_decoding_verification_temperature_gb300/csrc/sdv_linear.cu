@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, RING ? 4 : 2)
     } else {
       const bool has_d = j < gamma;
       const char *drow = has_d ? drow_of(s, j) : nullptr;
-      MS st[2] = {ms_empty(), ms_empty()};
+      MS st[2] = {ms_start(k2), ms_start(k2)};
       if constexpr (RING) {
         ring_stats<DT, VW>(rg, trow, drow, sl, k2, st[0], st[1]);
       } else {
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, RING ? 4 : 2)
   auto cand_stats = [&](int s, int j) -> uint4 {
     if constexpr (FAN && !GREEDY) {
       const char *trow = trow_of(s, j), *drow = drow_of(s, j);
-      MS st[2] = {ms_empty(), ms_empty()};
+      MS st[2] = {ms_start(k2), ms_start(k2)};
       VecTop<DT, VW> T;
       vec_top_init(T);
       ring_pass(rg, trow, drow, sl, [&](const uint4 *A, const uint4 *Bp,

@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
   WarpFilter wf;
   wf_init(wf, p.F);
-  MS st = ms_empty();
+  MS st = ms_start(p.k2);
   float worst = -__builtin_huge_valf();  // NaN-propagating max of v
   for (int vb = sl.vbeg + warp * 32 * kSelUF; vb < sl.vend;
        vb += kWarps * 32 * kSelUF) {  // warp-uniform

@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         a = block_reduce_am(a, sh.ared);
         if (tid == 0) sh.apart[par] = a;
       } else {
-        MS st[2] = {ms_empty(), ms_empty()};
+        MS st[2] = {ms_start(k2), ms_start(k2)};
         stats_pass<DT, VW>(ra, rb, has_q, sl, k2, st[0], st[1]);
         block_reduce_ms<2>(st, k2, sh.red);
         if (tid == 0) {

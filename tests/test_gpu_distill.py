@@ -262,3 +262,37 @@ def test_step_over_many_rows(dtype, V, stride):
     again = api.distill_topk_step(z, *a, w, 0.9, out=z)["grad"]
     assert again is z
     assert torch.equal(torch.nan_to_num(z), torch.nan_to_num(s["grad"]))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("N,V", [(4, 1000), (4, 64129), (200, 5000)])
+@pytest.mark.parametrize("mask,T", [(-2e38, 0.7), (-2e38, 2.0), (-1e38, 0.3),
+                                    (-2.9e38, 1.0), (-1e37, 0.7),
+                                    (-1e30, 1.0), (-1e10, 0.7), (-9e8, 0.7),
+                                    (-1e4, 0.7)])
+def test_finite_masks(dtype, N, V, mask, T):
+    """A mask far below every logit, finite or -inf, gives the same bits: the
+    first half of a row, all but its end, every other column."""
+    z, lg, ids, tl, w = make(N, V, 6, dtype, T, seed=V)
+    hide = torch.zeros(N, V, dtype=torch.bool)
+    hide[0, :V // 2] = True
+    hide[1, :V - 6] = True
+    hide[2, ::2] = True
+    ids[:] = torch.arange(V - 11, V + 1, 2, dtype=torch.int32)
+    ids[1] = torch.arange(V - 6, V, dtype=torch.int32)
+    ids[2] = torch.arange(1, 12, 2, dtype=torch.int32)
+    ids[ids >= V] = -1
+    a = (lg.cuda(), ids.cuda())
+    got = []
+    for m in (mask, -float("inf")):
+        zm = z.masked_fill(hide, m).cuda()
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        f = api.distill_topk(zm, *a, T, status=st)
+        s = api.distill_topk_step(zm, *a, w.cuda(), T, status=st)
+        g = api.distill_topk_backward(zm, f["lse"], *a, w.cuda(), T,
+                                      status=st)
+        torch.cuda.synchronize()
+        assert int(st.item()) == 0
+        got.append((f["loss"], f["lse"], s["loss"], s["lse"], s["grad"], g))
+    for x, y in zip(*got):
+        assert bool(torch.isfinite(x).all()) and torch.equal(x, y)

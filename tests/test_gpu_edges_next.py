@@ -117,3 +117,30 @@ def test_refused_arguments():
         api.branch_fork(torch.zeros((1, 64), device="cuda"),
                         torch.zeros(1, dtype=torch.int32, device="cuda"),
                         1.0, 65)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [1000, 5003, 64128])
+@pytest.mark.parametrize("low", [-2e38, -1e30, -1e10, -1e4])
+def test_finite_masks_verify_like_minus_infinity(dtype, V, low):
+    """Columns masked with a number (-2e38: past the fp32 range at T = 0.7):
+    the same outputs as with -inf."""
+    B, G, T = 6, 4, 0.7
+    g = torch.Generator().manual_seed(V)
+    z = torch.randn(B, G + 1, V, generator=g) * 3
+    d = z[:, :G] + torch.randn(B, G, V, generator=g)
+    tokens = (torch.randint(V - V // 2, (B, G), generator=g) + V // 2).to(
+        torch.int32).cuda()
+    u = (torch.rand(B, G + 1, generator=g) * 0.99 + 0.005).cuda()
+    got = []
+    for mask in (low, -float("inf")):
+        z[..., :V // 2] = mask
+        d[..., :V // 2] = mask
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        r = api.verify_linear(z.to(dtype).cuda(), d.to(dtype).cuda(), tokens,
+                              u, T, status=st)
+        assert int(st.item()) == 0
+        got.append(r)
+    for k in ("n", "tokens", "prob"):
+        assert torch.equal(got[0][k], got[1][k]), k
+    assert bool((got[0]["n"] >= 0).all())
