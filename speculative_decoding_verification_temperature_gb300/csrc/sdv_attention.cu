@@ -1016,9 +1016,10 @@ attention_kernel(const __grid_constant__ AttnParams p,
         const long long part =
             ((long long)blockIdx.x * 2 + (u.j0 == 0 ? 1 : 0)) * ROWS +
             base_row + r;
-        // no key seen: 0; a NaN sum stays NaN
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        if (whole) f0 *= inv, f1 *= inv;
+        // no key seen: 0, also where O has 0 times another row's infinity; a
+        // NaN sum stays NaN
+        if (l == 0.f) f0 = f1 = 0.f;
+        else if (whole) f0 *= 1.f / l, f1 *= 1.f / l;
         if (mine && (PAIR || st == 0)) {
           // l counts 2^kBias for a weight of 1
           const float ref = m * sl - Scale<T>::kBias;
@@ -1036,13 +1037,14 @@ attention_kernel(const __grid_constant__ AttnParams p,
           tmem_wait_ld();
           float o[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(a[e]) * f0;
+          for (int e = 0; e < 32; ++e)
+            o[e] = f0 == 0.f ? 0.f : __uint_as_float(a[e]) * f0;
           if (second) {
             tmem_ld32(o_addr + D + c, a);
             tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              o[e] = fmaf(__uint_as_float(a[e]), f1, o[e]);
+              o[e] = f1 == 0.f ? o[e] : fmaf(__uint_as_float(a[e]), f1, o[e]);
           }
           if (!mine) {
             // no such row

@@ -496,3 +496,31 @@ def test_few_heavy_keys_of_no_value_over_thousands(D, hint, heavy, below,
     ltol = d + kv * ref.U32 + 128 * ref.U32
     assert bool(((got["lse"].view(B, H, G).double() - lse).abs()
                  <= ltol).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("hint", [1, 200])
+@pytest.mark.parametrize("n", [40, 300])
+def test_empty_rows_beside_values_that_are_not_finite(D, hint, n):
+    """Rows that see no key give 0 and -inf whatever the values of other rows'
+    keys are: the mask leaves all rows empty but two, which see an infinity
+    and a NaN."""
+    P = ref.Paged([n, 3], [n, 20], 2, D, 16, BF, seed=n + D)
+    see = [np.zeros((n, n), bool), np.tril(np.ones((3, 3), bool))]
+    see[0][3, 0] = see[0][n - 1, n - 2] = True
+    for j, x in ((0, np.inf), (n - 2, np.nan)):
+        p, t = P.slot(0, j)
+        P.v[p, t] = x
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    r = api.paged_attention(
+        P.rows(8).cuda(), api.PagedKV(P.k.cuda(), P.v.cuda(), P.table.cuda()),
+        *P.lengths(), max_q=hint, tree_mask=ref.pack_mask(see), want_lse=True,
+        status=st, workspace=api.Workspace())
+    assert int(st.item()) == 0
+    empty = torch.ones(n + 3, dtype=torch.bool)
+    empty[[3, n - 1, n, n + 1, n + 2]] = False
+    assert bool((r["out"][empty.cuda()] == 0).all())
+    assert bool((r["lse"][empty.cuda()] == -float("inf")).all())
+    assert bool(torch.isinf(r["out"][3]).all() | torch.isnan(r["out"][3]).all())
+    assert bool(torch.isnan(r["out"][n - 1]).all())
+    assert bool(torch.isfinite(r["out"][n:]).all())
