@@ -734,6 +734,15 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _status(status, device):
+    """The address of the status word (None without one)."""
+    if status is None:
+        return None
+    if status.numel() < 1:
+        raise ValueError("status must hold one int32")
+    return _vec(status, device, torch.int32, "status")
+
+
 def kv_append(cache, k, v, q_start, kv_len, *, q=None, cos_sin=None,
               positions=None, interleaved=False, status=None):
     """Append new tokens' keys and values to a PagedKV, rotated by position
@@ -768,7 +777,7 @@ def kv_append(cache, k, v, q_start, kv_len, *, q=None, cos_sin=None,
     rc = lib().sd_kv_append(
         cache._addr, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, Hq, start,
         lens, pp, cp, max_pos, rot, 1 if interleaved else 0, B, total, op,
-        _ptr(status), _raw_stream(dev))
+        _status(status, dev), _raw_stream(dev))
     if rc != SD_OK:
         _check(rc)
     return out
@@ -787,8 +796,8 @@ def paged_attention(q, cache, q_start, kv_len, *, max_q=None, scale=None,
     whether weights are rounded to the type before they multiply the values
     (max_q x q_heads / heads above 128) or keep twice its bits.  scale
     defaults to D ** -0.5.  workspace: scratch between the call's two kernels
-    (default: the current stream's and thread's own).  Returns out [total, q_heads, D] (and lse [total,
-    q_heads] float32 when want_lse)."""
+    (default: the current stream's and thread's own).  Returns out [total,
+    q_heads, D] (and lse [total, q_heads] float32 when want_lse)."""
     dev, D = cache.device, cache.head_dim
     total, Hq, qs = _rows(q, cache, "q")
     B, start, lens = _lengths(cache, q_start, kv_len)
@@ -809,7 +818,8 @@ def paged_attention(q, cache, q_start, kv_len, *, max_q=None, scale=None,
     rc = L.sd_paged_attention(
         q.data_ptr(), qs, Hq, cache._addr, start, lens, mp, words, B, total,
         max_q, D ** -0.5 if scale is None else scale, out.data_ptr(),
-        _ptr(lse), _ptr(status), ws.data_ptr(), ws.numel(), _raw_stream(dev))
+        _ptr(lse), _status(status, dev), ws.data_ptr(), ws.numel(),
+        _raw_stream(dev))
     if rc != SD_OK:
         _check(rc)
     return {"out": out, "lse": lse} if want_lse else {"out": out}
@@ -871,7 +881,7 @@ def distill_topk(student, teacher_logit, teacher_id, T=1.0, *,
     lse = torch.empty(N, dtype=torch.float32, device=dev)
     rc = lib().sd_distill_topk(
         student.data_ptr(), rs, dt, lp, ip, tp, N, V, K, T, loss.data_ptr(),
-        lse.data_ptr(), _ptr(status), _raw_stream(dev))
+        lse.data_ptr(), _status(status, dev), _raw_stream(dev))
     if rc != SD_OK:
         _check(rc)
     return {"loss": loss, "lse": lse}
@@ -890,7 +900,7 @@ def distill_topk_backward(student, lse, teacher_logit, teacher_id, grad_loss,
     grad, gs = _grad_out(out, student, dev, N, V)
     rc = lib().sd_distill_topk_backward(
         student.data_ptr(), rs, dt, sp, lp, ip, tp, wp, N, V, K, T,
-        grad.data_ptr(), gs, _ptr(status), _raw_stream(dev))
+        grad.data_ptr(), gs, _status(status, dev), _raw_stream(dev))
     if rc != SD_OK:
         _check(rc)
     return grad
@@ -909,8 +919,8 @@ def distill_topk_step(student, teacher_logit, teacher_id, grad_loss, T=1.0,
     grad, gs = _grad_out(out, student, dev, N, V)
     rc = lib().sd_distill_topk_step(
         student.data_ptr(), rs, dt, lp, ip, tp, wp, N, V, K, T,
-        loss.data_ptr(), lse.data_ptr(), grad.data_ptr(), gs, _ptr(status),
-        _raw_stream(dev))
+        loss.data_ptr(), lse.data_ptr(), grad.data_ptr(), gs,
+        _status(status, dev), _raw_stream(dev))
     if rc != SD_OK:
         _check(rc)
     return {"loss": loss, "lse": lse, "grad": grad}

@@ -176,3 +176,29 @@ def test_another_stream():
     got = cache.k[P.table[0, :4].cuda().long()].reshape(64, 2, 64)
     want = x[:, :2] + (big[0, 0] * 0).to(x.dtype)
     assert torch.equal(torch.nan_to_num(got), torch.nan_to_num(want))
+
+
+@pytest.mark.parametrize("bad,err", [
+    (lambda: torch.zeros(1, dtype=torch.int32), ValueError),
+    (lambda: torch.zeros(1, dtype=torch.int64, device="cuda"), TypeError),
+    (lambda: torch.zeros(0, dtype=torch.int32, device="cuda"), ValueError),
+    (lambda: torch.zeros(4, dtype=torch.int32, device="cuda")[::2],
+     ValueError)])
+def test_status_words_are_checked(bad, err):
+    """By every call that this binding has around the verify step: the kernels
+    write to the status word's address."""
+    P = ref.Paged([1], [1], 1, 64, 8, torch.bfloat16, seed=1, fill=0.0)
+    cache = api.PagedKV(P.k.cuda(), P.v.cuda(), P.table.cuda())
+    x, st = P.rows(1).cuda(), bad()
+    z = torch.zeros(2, 50, device="cuda")
+    w = torch.zeros(2, device="cuda")
+    top = z[:, :3].contiguous(), torch.zeros(2, 3, dtype=torch.int32,
+                                             device="cuda")
+    for call in (lambda: api.kv_append(cache, x, x, *P.lengths(), status=st),
+                 lambda: api.paged_attention(x, cache, *P.lengths(),
+                                             status=st),
+                 lambda: api.distill_topk(z, *top, status=st),
+                 lambda: api.distill_topk_backward(z, w, *top, w, status=st),
+                 lambda: api.distill_topk_step(z, *top, w, status=st)):
+        with pytest.raises(err, match="status"):
+            call()
