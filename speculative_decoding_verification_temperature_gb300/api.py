@@ -655,7 +655,12 @@ class PagedKV:
     head-major page is ``t.transpose(1, 2)`` of [num_pages, heads,
     page_size, head_dim]); block_table [B, max_pages] int32, the page of
     each page_size keys of a sequence.  The tensors are kept, not copied:
-    the program may change them between calls."""
+    the program may change what they hold between calls.  Other tensors want
+    another PagedKV (k, v and block_table cannot be assigned)."""
+
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    block_table = property(lambda self: self._block_table)
 
     def __init__(self, k, v, block_table):
         dev = k.device
@@ -677,7 +682,7 @@ class PagedKV:
         _dev(block_table, dev, "block_table", torch.int32)
         if block_table.dim() != 2:
             raise ValueError("block_table must be [B, max_pages]")
-        self.k, self.v, self.block_table = k, v, block_table
+        self._k, self._v, self._block_table = k, v, block_table
         n, page, heads, dim = k.shape
         self.B, self.heads, self.head_dim = block_table.shape[0], heads, dim
         self.device, self.dtype = dev, k.dtype

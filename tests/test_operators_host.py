@@ -244,3 +244,12 @@ def test_workspace_buffers_are_not_shared(monkeypatch):
     gc.collect()
     assert c.numel() >= 5000 and old() is not None
     assert ws.get(dev, 5000) is c
+
+
+@pytest.mark.parametrize("name", ["k", "v", "block_table"])
+def test_a_cache_keeps_the_tensors_it_describes(name):
+    """Its C description holds their addresses: assigning another tensor would
+    leave the old address in use after the old tensor is gone."""
+    cache = api.PagedKV.__new__(api.PagedKV)
+    with pytest.raises(AttributeError):
+        setattr(cache, name, torch.zeros(1))
