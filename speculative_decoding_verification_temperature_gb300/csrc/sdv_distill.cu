@@ -823,7 +823,8 @@ sd_status launch_step(DistillParams &p, sd_dtype dt, int sms, cudaStream_t s,
                                     : (const void *)distill_step_kernel<1>;
   const size_t smem = (size_t)kRing * kChunk * 16 + sizeof(StepShared);
   int resident = 0;
-  const sd_status st = max_active_clusters(kernel, cl, smem, &resident);
+  const sd_status st =
+      max_active_clusters(kernel, cl, smem, &resident, kStepThreads);
   if (st != SD_OK) return st;
   p.CL = cl;
   const int clusters = p.N < resident ? p.N : resident;

@@ -105,7 +105,7 @@ sd_status check_device(int *sm_count) {
 }
 
 sd_status max_active_clusters(const void *kernel, int cl, size_t smem,
-                              int *out) {
+                              int *out, int threads) {
   int dev = 0;
   SDV_CUDA(cudaGetDevice(&dev));
   auto key = std::make_tuple(kernel, cl, smem, dev);
@@ -138,7 +138,7 @@ sd_status max_active_clusters(const void *kernel, int cl, size_t smem,
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(cl, 1, 1);
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -52,10 +52,10 @@ inline int choose_cluster(long long nvec) {
   return cl;
 }
 
-// Largest number of co-resident clusters of `cl` CTAs for a kernel (cached
-// per kernel, cluster size and shared-memory size).
+// Largest number of co-resident clusters of `cl` CTAs of `threads` threads
+// for a kernel (cached per kernel, cluster size and shared-memory size).
 sd_status max_active_clusters(const void *kernel, int cl, size_t smem,
-                              int *out);
+                              int *out, int threads = 256);
 
 // Launch `kernel` with a 1-D grid of nclusters * cl CTAs in clusters of cl.
 sd_status launch_clusters(const void *kernel, int nclusters, int cl,
