@@ -296,3 +296,57 @@ def test_finite_masks(dtype, N, V, mask, T):
         got.append((f["loss"], f["lse"], s["loss"], s["lse"], s["grad"], g))
     for x, y in zip(*got):
         assert bool(torch.isfinite(x).all()) and torch.equal(x, y)
+
+
+@pytest.mark.parametrize("N", [40, 200])
+@pytest.mark.parametrize("stride", [152064, 152065])
+def test_step_on_rows_longer_than_the_chip_keeps(N, stride):
+    """fp32 rows of 152064 columns, too long for eight CTAs to keep: with 40
+    rows clusters of four, with 200 single CTAs, each reads what it did not
+    keep a second time, in place from a row that it is overwriting; aligned
+    and off 16 bytes.  Against the formula in 64 bits (torch's log-softmax),
+    under the bounds of tests/operators_ref.py."""
+    V, K, T = 152064, 24, 0.9
+    g = torch.Generator(device="cuda").manual_seed(N)
+    z = torch.randn(N, stride, generator=g, device="cuda")[:, :V] * 3
+    z = torch.empty(N, stride, device="cuda")[:, :V].copy_(z)
+    top = torch.randn(N, V, generator=g, device="cuda").topk(K, 1)
+    a = (top.values.contiguous(), top.indices.to(torch.int32))
+    w = torch.rand(N, generator=g, device="cuda")
+    w[::9] = 0
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    s = api.distill_topk_step(z, *a, w, T, status=st)
+    f = api.distill_topk(z, *a, T, status=st)
+    back = api.distill_topk_backward(z, s["lse"], *a, w, T, status=st)
+    assert int(st.item()) == 0
+    u = ref.U32
+    for lo in range(0, N, 20):
+        r = slice(lo, lo + 20)
+        x = z[r].double() / T
+        lse = torch.logsumexp(x, 1)
+        logp = torch.log_softmax(top.values[r].double() / T, 1)
+        logq = x - lse[:, None]
+        p, size = logp.exp(), x.abs().amax(1)
+        loss = (p * (logp - logq.gather(1, top.indices[r]))).sum(1)
+        # as operators_ref.distill, with its largest terms for all
+        lse_tol = (V / 256 + 64) * u + 8 * u * (1 + size + lse.abs())
+        tsize = 2 * top.values[r].double().abs().amax(1) / T + 4
+        rel = 16 * u * (1 + tsize) + 256 * u
+        far = logq.abs().amax(1)
+        loss_tol = lse_tol + rel * (1 + tsize + far) + \
+            8 * u * (size + lse.abs())
+        for got in (s, f):
+            assert bool(((got["lse"][r] - lse).abs() <= lse_tol).all())
+            assert bool(((got["loss"][r] - loss).abs() <= loss_tol).all())
+        q = logq.exp()
+        pk = torch.zeros_like(q).scatter_add_(1, top.indices[r], p)
+        c = (w[r].double() / T)[:, None]
+        tol = c * (q * (rel + lse_tol)[:, None] + q * 16 * u * (1 + logq.abs())
+                   + pk * (rel[:, None] + 64 * u))
+        for got in (s["grad"], back):
+            d = (got[r].double() - c * (q - pk)).abs()
+            assert bool((d <= tol * 1.01 + u * (c * (q - pk)).abs()
+                         + 1e-38).all())
+    want = s["grad"].clone()
+    assert api.distill_topk_step(z, *a, w, T, out=z)["grad"] is z
+    assert torch.equal(z, want)
