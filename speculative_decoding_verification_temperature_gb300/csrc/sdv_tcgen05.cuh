@@ -43,9 +43,6 @@ __device__ __forceinline__ void tmem_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-#define SDV_R8(r, i)                                                     \
-  r[i], r[i + 1], r[i + 2], r[i + 3], r[i + 4], r[i + 5], r[i + 6],      \
-      r[i + 7]
 #define SDV_O8(r, i)                                                     \
   "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]),            \
       "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
@@ -70,13 +67,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
       "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::
           "r"(addr),
       SDV_I8(r, 0), SDV_I8(r, 8), SDV_I8(r, 16), SDV_I8(r, 24)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, "
-      "%6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
-      SDV_I8(r, 0), SDV_I8(r, 8)
       : "memory");
 }
 
