@@ -153,9 +153,8 @@ __device__ unsigned long long head_tiles(const AttnParams &p,
 // Starting and ending a unit costs a CTA about as much as this many key
 // tiles: it counts into the shares, so that many short units and few long
 // ones take the same time (two prompt chunks, one over 8192 cached keys and
-// one over 2385: 589 us by tiles alone, 549 with 8, 554 with 12).  Not where
-// the shares are themselves short: there every tile that another SM takes is
-// time saved.
+// one over 2385: 589 us by tiles alone, 549 with 8, 554 with 12; 8 trees of
+// 64 nodes 53 and 48, 8 prompts of up to 700 tokens 99 and 83).
 template <int ROWS> constexpr int unit_cost() { return ROWS == 256 ? 8 : 1; }
 
 // The plan of one CTA.  All units are laid end to end, each `extra` places
@@ -164,7 +163,6 @@ struct Plan {
   unsigned long long total, x0, x1;
   unsigned long long warp_sum[8], warp_units[8];
   int n, b, h, t, at;  // shares; the unit where x0 lies, and the place in it
-  int extra;
   int any_unusable;
 };
 
@@ -206,8 +204,7 @@ __device__ void make_plan(const AttnParams &p, Plan &s) {
       w += s.warp_sum[i];
       k += s.warp_units[i];
     }
-    s.extra = w >= 16ull * gridDim.x ? unit_cost<ROWS>() : 0;
-    w += k * s.extra;
+    w += k * unit_cost<ROWS>();
     s.total = w;
     s.any_unusable = any;
     s.n = w < gridDim.x ? (int)w : (int)gridDim.x;
@@ -219,7 +216,7 @@ __device__ void make_plan(const AttnParams &p, Plan &s) {
   }
   __syncthreads();
   if (s.x0 == s.x1) return;
-  const unsigned long long extra = s.extra;
+  constexpr unsigned long long extra = unit_cost<ROWS>();
   unsigned long long carry = 0;
   for (int base = 0; base < p.B; base += 256) {
     unsigned long long w = first_tiles + extra * first_units;
@@ -273,14 +270,15 @@ template <int ROWS> struct Units {
   const AttnParams &p;
   unsigned long long left;  // places of the share from `at` on
   Chunk c;
-  int b, h, t, T, at, extra;
+  static constexpr int extra = unit_cost<ROWS>();
+  int b, h, t, T, at;
   int j0, j1, nk;   // key tiles [j0, j1) of the unit's nk
   int rows;         // valid rows of the tile
   int count;        // units begun
 
   __device__ Units(const AttnParams &p_, const Plan &s)
       : p(p_), left(s.x1 - s.x0), b(s.b), h(s.h), t(s.t), T(0), at(s.at),
-        extra(s.extra), count(0) {
+        count(0) {
     if (!left) return;
     c = attn_chunk(p, b);
     T = row_tiles<ROWS>(p, c);
