@@ -75,18 +75,18 @@ constexpr float kLn2 = 0.693147180559945f;
 // thousands, perhaps, that matter beside a key far above them).  A weight is
 // off by its own rounding, or by 2^-17 of the largest of its 64 keys; beside
 // a key that set the reference, and in a half that hides keys, by 2^-28 of the
-// reference's.  Sums grow by a move down, by 2^kMostUp at most, and once they
-// are kTop none is made: what lies below is then no part of the result's bits.
-// For this, fp16 takes 1 to 3 % more (without bias and moves down, two prompt
-// chunks of D = 128 took 559 us and take 578, 16 trees of 64 nodes 69 and 71,
-// 9 tokens over 131072 keys 97 and 99.5); a bias of 2^7 cost 6 to 7 %.
+// reference's.  Sums grow by a move down, so none is made once they are kTop,
+// nor by more than 2^kMost: what lies below is then no part of the result.
+// For this, fp16 takes 2 to 5 % more (without bias and moves down, two prompt
+// chunks of D = 128 took 559 us and take 588, 16 trees of 64 nodes 69 and 72,
+// 9 tokens over 131072 keys 97 and 99).
 template <class T> struct Scale {
   static constexpr float kSlack = 15.f, kBias = 0.f, kDrop = kInf;
 };
 template <> struct Scale<__half> {
   static constexpr float kSlack = 12.f, kBias = 3.f, kDrop = 11.f;
 };
-constexpr float kTop = 0x1p50f, kMostUp = 60.f;
+constexpr float kTop = 0x1p50f, kMost = 60.f;
 
 struct AttnParams {
   const void *q;
@@ -539,11 +539,11 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
     const float up = (mt - row.m) * row.sl;
     bool move = mt > -kInf && !(up <= S::kSlack);
     if (DROPS && (!HIDE || (seen[2 * hf] & seen[2 * hf + 1]) == ~0u))
-      move = move || (up < -S::kDrop && row.l < kTop);
+      move = move || (up < -S::kDrop && up > -kMost && row.l < kTop);
     if (__any_sync(~0u, move)) {
       float f = 1.f;
       if (move) {
-        f = row.m == -kInf ? 1.f : ex2(DROPS ? fminf(-up, kMostUp) : -up);
+        f = row.m == -kInf ? 1.f : ex2(-up);
         row.m = mt;
       }
       row.l *= f;

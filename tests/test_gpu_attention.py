@@ -444,7 +444,8 @@ def test_a_graph_keeps_its_workspace():
 @pytest.mark.parametrize("hint", [1, 400])
 @pytest.mark.parametrize("heavy", [(0,), (4095,), (0, 1700, 1701, 3000)])
 @pytest.mark.parametrize("below,size", [(11.5, 1.0), (17.3, 8.0),
-                                        (24.0, 4096.0)])
+                                        (24.0, 4096.0), (36.0, 4096.0),
+                                        (60.0, 4096.0)])
 def test_few_heavy_keys_of_no_value_over_thousands(D, hint, heavy, below,
                                                    size):
     """fp16, a few keys whose values are 0 and thousands of others `below`
