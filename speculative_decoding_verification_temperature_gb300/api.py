@@ -879,7 +879,8 @@ def distill_topk(student, teacher_logit, teacher_id, T=1.0, *,
     strided), teacher_logit [N, K] float32, teacher_id [N, K] int32 (-1:
     padding), teacher_lse [N] float32 (None: the K probabilities are
     normalised among themselves).  Returns loss [N] and lse [N] (log sum
-    exp(student / T), which the backward call takes)."""
+    exp(student / T), which the backward call takes).  Neither is part of
+    torch's graph: the gradient is distill_topk_backward's."""
     dev, N, V, K, dt, rs, lp, ip, tp = _distill_rows(
         student, teacher_logit, teacher_id, teacher_lse)
     loss = torch.empty(N, dtype=torch.float32, device=dev)
@@ -896,8 +897,9 @@ def distill_topk_backward(student, lse, teacher_logit, teacher_id, grad_loss,
                           T=1.0, *, teacher_lse=None, out=None, status=None):
     """Gradient of sum_n grad_loss[n] loss[n] of distill_topk with respect to
     the student's logits (sd_distill_topk_backward); lse as distill_topk
-    returned it.  ``out`` may be the student itself.  Returns grad [N, V] of
-    the student's type."""
+    returned it.  ``out`` may be the student itself; torch does not see that
+    write (no version is counted, so nothing that autograd saved of the student
+    may be used after it).  Returns grad [N, V] of the student's type."""
     dev, N, V, K, dt, rs, lp, ip, tp = _distill_rows(
         student, teacher_logit, teacher_id, teacher_lse)
     sp = _row_vector(lse, dev, "lse", N)
@@ -914,8 +916,8 @@ def distill_topk_backward(student, lse, teacher_logit, teacher_id, grad_loss,
 def distill_topk_step(student, teacher_logit, teacher_id, grad_loss, T=1.0,
                       *, teacher_lse=None, out=None, status=None):
     """distill_topk and its gradient in one call (sd_distill_topk_step), for
-    a training step that knows the rows' weights beforehand.  Returns loss,
-    lse and grad."""
+    a training step that knows the rows' weights beforehand; ``out`` as in
+    distill_topk_backward.  Returns loss, lse and grad."""
     dev, N, V, K, dt, rs, lp, ip, tp = _distill_rows(
         student, teacher_logit, teacher_id, teacher_lse)
     wp = _row_vector(grad_loss, dev, "grad_loss", N)

@@ -59,7 +59,10 @@ __device__ __forceinline__ Place place_row(const AppendParams &p, int row) {
   return r;
 }
 
-// Any size and alignment: one CTA per packed row, one thread per pair.
+// Any size and alignment: one CTA per packed row, one thread per pair.  For
+// rotations and head sizes off the grid of 16 that models seldom have: loads
+// and stores by the element, angles read for every head (25k tokens of 48
+// heads of 96, rot_dim 20 or 24: 264 us, at HBM's rate 79).
 template <class T>
 __global__ void __launch_bounds__(kThreads)
 append_any_kernel(const __grid_constant__ AppendParams p) {
@@ -164,8 +167,8 @@ __device__ __forceinline__ Double turn(Double x, const float (&c)[8],
 // where there are many rows (each byte is read and written once) and by the
 // chain sequence -> page -> store where there are few; a thread's first
 // kAhead heads are on their way before it starts on that chain.  25k tokens of
-// 48 heads of 128, fp16: 700 MB in 119 us, 0.88 of the measured copy rate; one
-// token 2.3 us, 288 tokens 3.3 us.
+// 48 heads of 128, fp16: 700 MB in 120 us, 0.88 of the measured copy rate; one
+// token 2.1 us, 288 tokens 3.7 us.
 constexpr int kAhead = 3;
 template <class T, bool NEIGHBOURS>
 __global__ void __launch_bounds__(kThreads)

@@ -34,15 +34,16 @@
 // it waits for, weights are rounded once (0.0023).
 //
 // The plain loop over keys with a warp per (token, head) took 14 ms on 64
-// sequences of one token and 219 ms on two prompt chunks; this takes 229 us
-// and 555 us.
+// sequences of one token and 219 ms on two prompt chunks; this takes 230 us
+// and 561 us.
 //
 // What bounds it: HBM for a few rows a unit (1.41 GB of keys and values of 64
-// sequences in 229 us, 0.92 of the measured copy rate; a CTA keeps six tiles,
+// sequences in 230 us, 0.92 of the measured copy rate; a CTA keeps six tiles,
 // 192 KB, on their way), and for many rows the chain score product, softmax,
 // value product of a stream: 2750 cycles for two streams' 128 x 128 tiles
-// where the products alone take 2048 (1.47 PFLOP/s on chunks of 4096 and 2250
-// tokens, 0.77 of the measured bf16 rate).
+// where the products alone take 2048 (1.45 PFLOP/s on chunks of 4096 and 2250
+// tokens, 0.76 of the measured bf16 rate; with D = 64 the products halve, the
+// softmax stays, and the call takes 509 us).
 //
 // A wait that gives up (see role_wait) stops the loads and the products; all
 // other steps go on over meaningless data to the end of the share, so that

@@ -285,7 +285,9 @@ __device__ void load_teacher(const DistillParams &p, int row, Teacher &t,
 }
 
 // Whether entry k is the first of its id, and then the sum of p over all
-// entries with that id.
+// entries with that id: K x K comparisons a row, which the step hides up to
+// about K = 64 (2048 rows of 128256 bf16: 198 us; 251 with K = 128, 470 with
+// 256).
 __device__ __forceinline__ bool first_of_id(const Teacher &t, int K, int k,
                                             float &sum) {
   const int id = t.id[k];
@@ -327,8 +329,10 @@ __device__ void store_entries(const DistillParams &p, const Teacher &t,
 // (each thread its own, so nothing is waited for), and it reads the rest,
 // newest first, once more.  Two CTAs on an SM, each with a row, keep HBM
 // busy through each other's reductions.  288 rows of 32000 fp32 forward:
-// 7.0 us where reading them takes 5.5; the step takes this kernel where rows
-// are few (100 such rows: 8.4 us) or too long for distill_step_kernel.
+// 10.0 us where reading them from HBM takes 5.5 (7.0 us out of L2).  The step
+// takes this kernel where rows are few (100 such rows: 9.6 us) or too long
+// for distill_step_kernel; many of the latter have a CTA each, which reads
+// most of its row twice (2048 rows of 152064 fp32: 617 us, at HBM's rate 373).
 constexpr int kRowThreads = 512;
 constexpr int kKept = 6272;  // 98 KB a CTA
 
