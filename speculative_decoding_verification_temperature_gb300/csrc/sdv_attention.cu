@@ -52,19 +52,17 @@
 
 #include <atomic>
 
-#include "sdv_paged.cuh"
 #include "sdv_tcgen05.cuh"
+#include "sdv_units.cuh"
 
 namespace sdv {
 namespace {
 
-constexpr int kTile = 128;       // keys per tile, rows per stream
 constexpr int kHalf = kTile / 2;  // keys a softmax thread weighs at a time
 constexpr int kMaxGrid = 160;    // CTAs the workspace is laid out for
 constexpr int kAttnThreads = 384;  // two warpgroups of softmax, one of roles
 constexpr int kMmaWarp = 9;  // and 10; warps 8 and 11 load
 constexpr int kBadRing = 64;     // units whose bad-page mark is kept
-constexpr float kLn2 = 0.693147180559945f;
 // A row's weights are 2^kBias at its reference m, and m moves up only when the
 // scores' maximum is 2^kSlack above it: weights stay at or below 2^15, inside
 // fp16's range, and hardly a tile rescales anything.  (With a slack of 2^8 the
@@ -89,236 +87,12 @@ template <> struct Scale<__half> {
 };
 constexpr float kTop = 0x1p50f, kMost = 60.f;
 
-struct AttnParams {
+struct AttnParams : UnitParams {
   const void *q;
   long long q_stride;
-  const int32_t *q_start, *kv_len, *block_table, *mask;
-  int mask_words;
-  int B, total, Hq, Hkv, G;
-  FastDiv by_G, by_page;
-  int num_pages, page_size, max_pages;
+  int num_pages;
   int box;  // rows of one TMA box: a power of two that divides the page
   float scale_log2;  // scale x log2(e)
-  void *out;
-  float *lse;
-  int32_t *dev_status;
-  // workspace: records of cut units, (m, l) and O of the parts
-  struct CutUnit *cut;
-  float2 *part_ml;
-  float *part_o;
-};
-
-// A unit whose key range is cut: part 0 is slot 1 of the CTA that starts
-// it, part k slot 0 of the k-th CTA after it.
-struct CutUnit {
-  int parts, rows;     // rows: valid rows of the tile
-  int start, head;     // packed row of the sequence, cache head
-  int first;           // first row of the tile in (token, group) order
-};
-
-// ------------------------------------------------------------ work units
-__device__ __forceinline__ Chunk attn_chunk(const AttnParams &p, int b) {
-  Chunk c = load_chunk(p.q_start, p.kv_len, b, p.total,
-                       (long long)p.max_pages * p.page_size);
-  if (p.mask && c.n > 32LL * p.mask_words) c.usable = false;
-  return c;
-}
-
-template <int ROWS>
-__device__ __forceinline__ int row_tiles(const AttnParams &p,
-                                         const Chunk &c) {
-  return c.usable ? (c.n * p.G + ROWS - 1) / ROWS : 0;
-}
-
-// Key tiles that row tile t sees.
-template <int ROWS>
-__device__ __forceinline__ int key_tiles(const AttnParams &p, const Chunk &c,
-                                         int t) {
-  int last = c.kv - 1;
-  if (!p.mask) {
-    const int i = div_by((t + 1) * ROWS - 1, p.by_G);
-    if (i < c.n - 1) last = c.kv - c.n + i;
-  }
-  return last / kTile + 1;
-}
-
-template <int ROWS>
-__device__ unsigned long long head_tiles(const AttnParams &p,
-                                         const Chunk &c) {
-  const int T = row_tiles<ROWS>(p, c);
-  unsigned long long s = 0;
-  for (int t = 0; t < T; ++t) s += key_tiles<ROWS>(p, c, t);
-  return s;
-}
-
-// Starting and ending a unit costs a CTA about as much as this many key
-// tiles: it counts into the shares, so that many short units and few long
-// ones take the same time (two prompt chunks, one over 8192 cached keys and
-// one over 2385: 589 us by tiles alone, 549 with 8, 554 with 12; 8 trees of
-// 64 nodes 53 and 48, 8 prompts of up to 700 tokens 99 and 83).
-template <int ROWS> constexpr int unit_cost() { return ROWS == 256 ? 8 : 1; }
-
-// The plan of one CTA.  All units are laid end to end, each `extra` places
-// for itself and then one for each key tile; the CTA's share is [x0, x1).
-struct Plan {
-  unsigned long long total, x0, x1;
-  unsigned long long warp_sum[8], warp_units[8];
-  int n, b, h, t, at;  // shares; the unit where x0 lies, and the place in it
-  int any_unusable;
-};
-
-template <int ROWS>
-__device__ void make_plan(const AttnParams &p, Plan &s) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // key tiles and units of this thread's sequences; of its first one
-  unsigned long long tiles = 0, units = 0, first_tiles = 0, first_units = 0;
-  bool unusable = false;
-  if (tid < 256)
-    for (int b = tid; b < p.B; b += 256) {
-      const Chunk c = attn_chunk(p, b);
-      if (c.n > 0 && !c.usable) unusable = true;
-      if (!c.rows_ok) {
-        unusable = true;
-        if (blockIdx.x == 0) status_or(p.dev_status, SD_DEV_BAD_LENGTH);
-      }
-      const unsigned long long w = head_tiles<ROWS>(p, c) * p.Hkv;
-      const unsigned long long k =
-          (unsigned long long)row_tiles<ROWS>(p, c) * p.Hkv;
-      if (b == tid) first_tiles = w, first_units = k;
-      tiles += w;
-      units += k;
-    }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) {
-    tiles += __shfl_xor_sync(~0u, tiles, d);
-    units += __shfl_xor_sync(~0u, units, d);
-  }
-  if (lane == 0 && warp < 8) {
-    s.warp_sum[warp] = tiles;
-    s.warp_units[warp] = units;
-  }
-  if (tid == 0) s.b = -1;
-  const int any = __syncthreads_or(unusable);
-  if (tid == 0) {
-    unsigned long long w = 0, k = 0;
-    for (int i = 0; i < 8; ++i) {
-      w += s.warp_sum[i];
-      k += s.warp_units[i];
-    }
-    w += k * unit_cost<ROWS>();
-    s.total = w;
-    s.any_unusable = any;
-    s.n = w < gridDim.x ? (int)w : (int)gridDim.x;
-    s.x0 = s.x1 = 0;
-    if ((int)blockIdx.x < s.n) {
-      s.x0 = w * blockIdx.x / s.n;
-      s.x1 = w * (blockIdx.x + 1) / s.n;
-    }
-  }
-  __syncthreads();
-  if (s.x0 == s.x1) return;
-  constexpr unsigned long long extra = unit_cost<ROWS>();
-  unsigned long long carry = 0;
-  for (int base = 0; base < p.B; base += 256) {
-    unsigned long long w = first_tiles + extra * first_units;
-    if (base > 0) {
-      w = 0;
-      if (tid < 256 && base + tid < p.B) {
-        const Chunk c = attn_chunk(p, base + tid);
-        w = (head_tiles<ROWS>(p, c) + extra * row_tiles<ROWS>(p, c)) * p.Hkv;
-      }
-    }
-    unsigned long long inc = w;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const unsigned long long o = __shfl_up_sync(~0u, inc, d);
-      if (lane >= d) inc += o;
-    }
-    if (lane == 31 && warp < 8) s.warp_sum[warp] = inc;
-    __syncthreads();
-    unsigned long long all = 0, before = carry;
-    for (int i = 0; i < 8; ++i) {
-      if (i < warp) before += s.warp_sum[i];
-      all += s.warp_sum[i];
-    }
-    const unsigned long long lo = before + inc - w;
-    if (tid < 256 && s.x0 >= lo && s.x0 < lo + w) {
-      const Chunk c = attn_chunk(p, base + tid);
-      const unsigned long long per =
-          head_tiles<ROWS>(p, c) + extra * row_tiles<ROWS>(p, c);
-      unsigned long long r = s.x0 - lo;
-      s.h = (int)(r / per);
-      r %= per;
-      int t = 0;
-      for (;; ++t) {
-        const int k = key_tiles<ROWS>(p, c, t) + (int)extra;
-        if (r < (unsigned long long)k) break;
-        r -= k;
-      }
-      s.b = base + tid;
-      s.t = t;
-      s.at = (int)r;
-    }
-    carry += all;
-    __syncthreads();
-    if (s.b >= 0) break;
-  }
-}
-
-// Walks the units of a CTA's share that it has key tiles of; every warp
-// walks the same ones.
-template <int ROWS> struct Units {
-  const AttnParams &p;
-  unsigned long long left;  // places of the share from `at` on
-  Chunk c;
-  static constexpr int extra = unit_cost<ROWS>();
-  int b, h, t, T, at;
-  int j0, j1, nk;   // key tiles [j0, j1) of the unit's nk
-  int rows;         // valid rows of the tile
-  int count;        // units begun
-
-  __device__ Units(const AttnParams &p_, const Plan &s)
-      : p(p_), left(s.x1 - s.x0), b(s.b), h(s.h), t(s.t), T(0), at(s.at),
-        count(0) {
-    if (!left) return;
-    c = attn_chunk(p, b);
-    T = row_tiles<ROWS>(p, c);
-    set();
-    if (j0 == j1) next();
-  }
-  __device__ void to(const Units &o) {  // o walks the same share
-    left = o.left, c = o.c, b = o.b, h = o.h, t = o.t, T = o.T, at = o.at;
-    j0 = o.j0, j1 = o.j1, nk = o.nk, rows = o.rows, count = o.count;
-  }
-  __device__ int places() const {  // of the unit that are in the share
-    const int n = nk + extra - at;
-    return (unsigned long long)n < left ? n : (int)left;
-  }
-  __device__ void set() {
-    ++count;
-    nk = key_tiles<ROWS>(p, c, t);
-    j0 = max(0, at - extra);
-    j1 = max(0, at + places() - extra);
-    rows = min(c.n * p.G - t * ROWS, ROWS);
-  }
-  __device__ void next() {
-    do {  // past units of which the share has no tile
-      left -= places();
-      if (!left) return;
-      at = 0;
-      if (++t == T) {
-        t = 0;
-        if (++h == p.Hkv) {
-          h = 0;
-          do {  // left > 0: a later sequence has units
-            c = attn_chunk(p, ++b);
-            T = row_tiles<ROWS>(p, c);
-          } while (T == 0);
-        }
-      }
-      set();
-    } while (j0 == j1);
-  }
 };
 
 // --------------------------------------------------------- shared memory
@@ -360,30 +134,6 @@ __device__ __forceinline__ void streams_sync() {
   asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 
-// 32 bytes, at a multiple of 32: whole sectors even where each lane writes
-// a row of its own.
-__device__ __forceinline__ void st_v8(void *to, const uint32_t *x) {
-  asm volatile(
-      "st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to),
-      SDV_I8(x, 0)
-      : "memory");
-}
-
-template <class T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi);
-template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
-  uint32_t u;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
-  return u;
-}
-template <>
-__device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
-  uint32_t u;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(hi), "f"(lo));
-  return u;
-}
-
 // A pair as a sum of two 16-bit pairs.  bf16: the first is cut off, not
 // rounded (a byte permutation), and the second holds the 8 bits after it.
 template <class T>
@@ -406,31 +156,6 @@ __device__ __forceinline__ void split2<__half>(float2 z, uint32_t &w,
       fma2(__half22float2(*reinterpret_cast<const __half2 *>(&w)),
            make_float2(-1.f, -1.f), z);
   rest = pack2<__half>(r.x, r.y);
-}
-
-// Bits of the 32 keys from `key` on that a row sees.  Causal: keys up to
-// `limit`.  Tree: the prefix, and the chunk's tokens in its mask.
-__device__ __forceinline__ uint32_t seen_bits(const AttnParams &p,
-                                              const Chunk &c, int token,
-                                              int limit, int key) {
-  const int ctx = c.kv - c.n;
-  const int end = (p.mask ? c.kv - 1 : limit) - key;  // last bit in range
-  if (end < 0) return 0;
-  const uint32_t in = end >= 31 ? ~0u : (2u << end) - 1;
-  if (!p.mask) return in;
-  const int x = key - ctx;  // the chunk's token at bit 0
-  if (x <= -32) return in;
-  const int32_t *m = p.mask + (long long)(c.start + token) * p.mask_words;
-  uint32_t bits;
-  if (x < 0) {
-    bits = ((1u << -x) - 1) | (uint32_t)__ldg(m) << -x;
-  } else {
-    const int w = x >> 5;
-    const uint32_t lo = w < p.mask_words ? (uint32_t)__ldg(m + w) : 0;
-    const uint32_t hi = w + 1 < p.mask_words ? (uint32_t)__ldg(m + w + 1) : 0;
-    bits = __funnelshift_r(lo, hi, x & 31);
-  }
-  return bits & in;
 }
 
 __device__ __forceinline__ float max32(const uint32_t *x) {
@@ -1089,88 +814,6 @@ attention_kernel(const __grid_constant__ AttnParams p,
   if (warp == kMmaWarp) tmem_free_all(tmem);
 }
 
-// A row of a cut unit from its parts (a warp), kAhead of them read at once.
-template <class T, int D, int ROWS, int kAhead>
-__device__ __forceinline__ void join_row(const AttnParams &p,
-                                         const CutUnit &cut, int r,
-                                         int lane) {
-  auto slot = [&](int k) {
-    return ((long long)(blockIdx.x + k) * 2 + (k == 0 ? 1 : 0)) * ROWS + r;
-  };
-  constexpr int E = D / 32;
-  auto part = [&](int k) {
-    return k < cut.parts ? p.part_ml[slot(k)] : make_float2(-kInf, 0.f);
-  };
-  float2 ml = part(lane);
-  float m = ml.x;
-  for (int k = lane + 32; k < cut.parts; k += 32) m = fmaxf(m, part(k).x);
-#pragma unroll
-  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, d));
-  float l = 0.f, o[E] = {};
-  for (int k0 = 0; k0 < cut.parts; k0 += 32) {
-    if (k0) ml = part(k0 + lane);
-    // lane k has the weight of part k0 + k: 0 for one that saw nothing (or
-    // is none), NaN for one with a NaN sum
-    const float w = ml.x == -kInf ? (ml.y == ml.y ? 0.f : ml.y)
-                                  : ex2(ml.x - m);
-    l += ml.y * w;
-    const int n = min(cut.parts - k0, 32);
-    for (int k = 0; k < n; k += kAhead) {
-      float x[kAhead][E];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const float *src =
-            p.part_o + slot(min(k0 + k + i, cut.parts - 1)) * D + lane * E;
-        if constexpr (E == 4) {
-          const float4 v = *reinterpret_cast<const float4 *>(src);
-          x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
-        } else {
-          const float2 v = *reinterpret_cast<const float2 *>(src);
-          x[i][0] = v.x, x[i][1] = v.y;
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const float wk = __shfl_sync(~0u, w, k + i);
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(x[i][e], wk, o[e]);
-      }
-    }
-  }
-#pragma unroll
-  for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(~0u, l, d);
-  const int at = cut.first + r, tok = div_by(at, p.by_G);
-  const long long row = (long long)(cut.start + tok) * p.Hq +
-                        cut.head * p.G + (at - tok * p.G);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t *dst = reinterpret_cast<uint32_t *>((T *)p.out + row * D + lane * E);
-#pragma unroll
-  for (int e = 0; e < E; e += 2)
-    dst[e / 2] = pack2<T>(o[e] * inv, o[e + 1] * inv);
-  if (p.lse && lane == 0)
-    p.lse[row] = l == 0.f ? -kInf : (m + log2f(l)) * kLn2;
-}
-
-// Joins the parts of cut units: a warp per row.  Block (x, y): the unit that
-// CTA x began, rows 8 y to 8 y + 7.  Where a long axis was cut into many parts
-// it is a chain of waits for L2: one head of 64 with 81 tokens behind 40k, the
-// whole call 50 us with parts read two at a time and 43 with sixteen.  Units
-// of two or three parts, which most are, would read more than they have that
-// way (64 tree nodes of 16 sequences: 73 us, two at a time 67).
-template <class T, int D, int ROWS>
-__global__ void __launch_bounds__(kThreads)
-attention_join_kernel(const __grid_constant__ AttnParams p) {
-  griddep_wait();
-  const CutUnit cut = p.cut[blockIdx.x];
-  const int r = blockIdx.y * kWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (cut.parts < 2 || r >= cut.rows) return;
-  if (cut.parts > 4)
-    join_row<T, D, ROWS, 16>(p, cut, r, lane);
-  else
-    join_row<T, D, ROWS, 2>(p, cut, r, lane);
-}
-
 // ------------------------------------------------------------------- host
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType,
                                  cuuint32_t, void *, const cuuint64_t *,
@@ -1229,18 +872,6 @@ sd_status cache_map(const sd_paged_kv *c, void *base, int box,
   return SD_OK;
 }
 
-struct WsLayout {
-  size_t cut, ml, o, bytes;
-};
-WsLayout ws_layout(int rows, int D) {
-  WsLayout w;
-  w.cut = 0;
-  w.ml = (kMaxGrid * sizeof(CutUnit) + 255) / 256 * 256;
-  w.o = w.ml + (size_t)kMaxGrid * 2 * rows * sizeof(float2);
-  w.bytes = w.o + (size_t)kMaxGrid * 2 * rows * D * sizeof(float);
-  return w;
-}
-
 // 256 rows a unit where a chunk has more than 128 of them.
 bool pair_rows(int max_q, int G) { return (long long)max_q * G > kTile; }
 
@@ -1249,10 +880,7 @@ sd_status launch(AttnParams &p, const CUtensorMap &k_map,
                  const CUtensorMap &v_map, int sms, char *ws,
                  cudaStream_t s) {
   using L = Layout<D, PAIR>;
-  const WsLayout w = ws_layout(L::kRows, D);
-  p.cut = reinterpret_cast<CutUnit *>(ws + w.cut);
-  p.part_ml = reinterpret_cast<float2 *>(ws + w.ml);
-  p.part_o = reinterpret_cast<float *>(ws + w.o);
+  set_workspace(p, ws_layout(kMaxGrid, L::kRows, D), ws);
   const void *kernel = (const void *)attention_kernel<T, D, PAIR>;
   int dev = 0;
   SDV_CUDA(cudaGetDevice(&dev));
@@ -1269,21 +897,7 @@ sd_status launch(AttnParams &p, const CUtensorMap &k_map,
   sd_status st = launch_pdl(kernel, grid, kAttnThreads,
                             attn_smem<D, PAIR>(), s, args);
   if (st != SD_OK) return st;
-  // a sequence whose table holds one key tile has no unit that can be cut
-  if ((long long)p.max_pages * p.page_size <= kTile) return SD_OK;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, L::kRows / kWarps, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  void *jargs[] = {&p};
-  SDV_CUDA(cudaLaunchKernelExC(
-      &cfg, (const void *)attention_join_kernel<T, D, L::kRows>, jargs));
-  return SD_OK;
+  return launch_join<T, D, L::kRows>(p, grid, s);
 }
 
 template <class T>
@@ -1305,7 +919,8 @@ extern "C" size_t sd_paged_attention_workspace(int q_heads, int heads,
                                                int head_dim, int max_q) {
   if (heads < 1 || q_heads < heads || (head_dim != 64 && head_dim != 128))
     return 256;
-  return ws_layout(pair_rows(max_q, q_heads / heads) ? 256 : 128, head_dim)
+  return ws_layout(kMaxGrid, pair_rows(max_q, q_heads / heads) ? 256 : 128,
+                   head_dim)
       .bytes;
 }
 
