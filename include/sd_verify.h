@@ -40,7 +40,8 @@
  * sd_verify_linear_fanout, sd_presto_init, sd_presto_expand,
  * sd_branch_fork; each call with a workspace has a *_workspace query.
  * Around the verify step: sd_kv_append and sd_paged_attention (the target's
- * forward pass over a chunk of drafts and its paged cache) and
+ * forward pass over a chunk of drafts and its paged cache), sd_kv4_append,
+ * sd_kv4_read and sd_kv4_attention (the same over a cache in 4 bits) and
  * sd_distill_topk (and _backward, _step: training the drafter on the
  * target's top logits).
  *
@@ -647,6 +648,99 @@ sd_status sd_paged_attention(const void *q, long long q_stride, int q_heads,
                              float scale, void *out, float *lse,
                              int32_t *dev_status, void *workspace,
                              size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------
+ * The same cache in 4 bits (drafting over a long context costs the cache's
+ * bytes): groups of neighbours of a head's row share a scale.
+ *
+ * A group of 32, 64 or 128 neighbours (at most head_dim, which is 64 or 128)
+ * has a pair (a, b) of fp16 numbers and a code n in 0 .. 15 per element: the
+ * element is the fp16 number nearest to b + (64 + n) a.  Codes of head h,
+ * token t of page p are head_dim / 2 bytes at p page_stride + (h page_size +
+ * t) head_dim / 2; the pairs of its groups, a before b, are head_dim / group
+ * x 4 bytes at p scale_stride + (h page_size + t) head_dim / group x 4
+ * (strides in bytes, multiples of 16, the same for k and v; bases 16-byte
+ * aligned).  Of each four bytes, a little-endian word, the nibbles from the
+ * lowest on are elements 0, 2, 4, 6, 1, 3, 5, 7.  dt is the type of the rows
+ * that calls take and give.
+ * Sequences, chunks and the block table are those of sd_paged_kv.
+ * ------------------------------------------------------------------- */
+typedef struct {
+  void *k, *v;              /* device: codes */
+  void *k_scale, *v_scale;  /* device: pairs of fp16 */
+  sd_dtype dt;              /* SD_BF16 or SD_F16 */
+  int num_pages, page_size; /* page_size: a multiple of 8 */
+  int heads, head_dim;      /* of keys and values; head_dim: 64 or 128 */
+  int group;                /* 32, 64 or 128 */
+  long long page_stride, scale_stride; /* bytes */
+  const int32_t *block_table; /* device [B, max_pages] */
+  int max_pages;
+} sd_paged_kv4;
+
+/* ---------------------------------------------------------------------
+ * sd_kv_append into a 4-bit cache: keys (rotated, from fp32, not rounded to
+ * 16 bits first) and values are quantised as they are written.
+ *
+ * With lo and hi the least and the greatest of a group's values, kept inside
+ * -6144 .. 6144: a = fp16((hi - lo) c), b = fp16(lo - 64 a), n = rint((x - b)
+ * r) - 64 kept inside 0 .. 15 (0 where a is 0), in fp32, every operation
+ * rounded by itself, c = 1/15 and r = 1/a rounded too; the rotation's two
+ * products and their sum likewise.  An element is off by half a step (hi -
+ * lo) / 15, a sixteenth of a step more for b's rounding, and fp16's own
+ * rounding; values beyond 6144 are held as that.  A group that holds NaN or
+ * infinity reads as NaN.
+ *
+ * All arguments, and what happens to tokens that cannot be placed, as in
+ * sd_kv_append.
+ * ------------------------------------------------------------------- */
+sd_status sd_kv4_append(const sd_paged_kv4 *cache, const void *k,
+                        long long k_stride, const void *v, long long v_stride,
+                        const void *q, long long q_stride, int q_heads,
+                        const int32_t *q_start, const int32_t *kv_len,
+                        const int32_t *positions, const float *cos_sin,
+                        int max_pos, int rot_dim, int interleaved, int B,
+                        int total, void *q_out, int32_t *dev_status,
+                        void *stream);
+
+/* ---------------------------------------------------------------------
+ * Tokens of a 4-bit cache back as 16-bit rows (for a prompt's next part, or
+ * a check of what the cache stands for): rows q_start[b] .. q_start[b+1] - 1
+ * of k_out and v_out [total, heads, head_dim] get the last n = q_start[b+1] -
+ * q_start[b] of the first kv_len[b] keys and values of sequence b, so any
+ * range of a sequence can be read.  A token's heads are contiguous, tokens
+ * k_stride and v_stride elements apart (multiples of 16; bases 32-byte
+ * aligned).  bf16 rows are the fp16 numbers rounded once more.
+ * Rows of an unusable sequence, and of a page outside [0, num_pages)
+ * (SD_DEV_BAD_PAGE), are NaN.  Rows of no sequence are left as they are.
+ * ------------------------------------------------------------------- */
+sd_status sd_kv4_read(const sd_paged_kv4 *cache, const int32_t *q_start,
+                      const int32_t *kv_len, int B, int total, void *k_out,
+                      long long k_stride, void *v_out, long long v_stride,
+                      int32_t *dev_status, void *stream);
+
+/* ---------------------------------------------------------------------
+ * sd_paged_attention over a 4-bit cache, with the same arguments, masks and
+ * results: the keys and values are the fp16 numbers that the codes stand for,
+ * never rounded to bf16.
+ *
+ * Products are of fp16 numbers with fp32 sums; bf16 queries are brought to
+ * fp16 by a power of two a row, exactly but for elements 2^-28 of the row's
+ * largest and below.  A row of q with NaN or infinity gets NaN.  A group of
+ * the cache that reads as NaN reaches the tokens that see it, and may reach
+ * others of the sequence; what the cache holds at and past kv_len never does.
+ * max_q is a hint as there.
+ * Workspace: sd_kv4_attention_workspace(...) bytes with the same max_q.
+ * ------------------------------------------------------------------- */
+size_t sd_kv4_attention_workspace(int q_heads, int heads, int head_dim,
+                                  int max_q);
+
+sd_status sd_kv4_attention(const void *q, long long q_stride, int q_heads,
+                           const sd_paged_kv4 *cache, const int32_t *q_start,
+                           const int32_t *kv_len, const int32_t *tree_mask,
+                           int mask_words, int B, int total, int max_q,
+                           float scale, void *out, float *lse,
+                           int32_t *dev_status, void *workspace,
+                           size_t ws_bytes, void *stream);
 
 /* ---------------------------------------------------------------------
  * Distillation of a drafter from the target's top logits.

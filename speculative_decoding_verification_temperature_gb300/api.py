@@ -96,6 +96,12 @@ def _declare(L):
         "sd_paged_attention_workspace": ([I, I, I, I], Z),
         "sd_paged_attention": ([P, LL, I, P, P, P, P, I, I, I, I, F, P, P, P,
                                 P, Z, P], I),
+        "sd_kv4_append": ([P, P, LL, P, LL, P, LL, I, P, P, P, P, I, I, I, I,
+                           I, P, P, P], I),
+        "sd_kv4_read": ([P, P, P, I, I, P, LL, P, LL, P, P], I),
+        "sd_kv4_attention_workspace": ([I, I, I, I], Z),
+        "sd_kv4_attention": ([P, LL, I, P, P, P, P, I, I, I, I, F, P, P, P,
+                              P, Z, P], I),
         "sd_distill_topk": ([P, LL, I, P, P, P, I, I, I, F, P, P, P, P], I),
         "sd_distill_topk_backward": ([P, LL, I, P, P, P, P, P, I, I, I, F, P,
                                       LL, P, P], I),
@@ -693,6 +699,106 @@ class PagedKV:
         self._addr = ctypes.addressof(self._struct)
 
 
+class _PagedKV4Struct(ctypes.Structure):
+    """sd_paged_kv4 of include/sd_verify.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("dt", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("group", ctypes.c_int),
+                ("page_stride", ctypes.c_longlong),
+                ("scale_stride", ctypes.c_longlong),
+                ("block_table", ctypes.c_void_p),
+                ("max_pages", ctypes.c_int)]
+
+
+class PagedKV4:
+    """A paged cache of keys and values in 4 bits (sd_paged_kv4).
+
+    k, v [num_pages, heads, page_size, head_dim / 2] uint8: codes; k_scale,
+    v_scale [num_pages, heads, page_size, head_dim / group, 2] float16: a
+    pair for each group of 32, 64 or 128 elements.  Pages are contiguous;
+    they may lie apart (k and v alike, k_scale and v_scale alike).
+    block_table [B, max_pages] int32; dtype (bfloat16 or float16): of the
+    rows that calls take and give.  ``PagedKV4.empty`` allocates one.  The
+    tensors are kept, not copied, and cannot be assigned."""
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
+    block_table = property(lambda self: self._tensors[4])
+
+    def __init__(self, k, v, k_scale, v_scale, block_table, dtype):
+        dev = k.device
+        for t, name, want in ((k, "k", torch.uint8), (v, "v", torch.uint8),
+                              (k_scale, "k_scale", torch.float16),
+                              (v_scale, "v_scale", torch.float16)):
+            if not t.is_cuda:
+                raise ValueError("%s must be a CUDA tensor (there is no CPU "
+                                 "path)" % name)
+            if t.dtype != want:
+                raise TypeError("%s must be %s, got %s" %
+                                (name, want, t.dtype))
+            if t.device != dev:
+                raise ValueError("%s must live on %s" % (name, dev))
+        if dtype not in _CACHE_DT:
+            raise TypeError("dtype must be bfloat16 or float16, got %s" %
+                            dtype)
+        if k.dim() != 4:
+            raise ValueError("k must be [pages, heads, page_size, "
+                             "head_dim / 2]")
+        n, heads, page, half = k.shape
+        if k_scale.dim() != 5 or k_scale.shape[:3] != k.shape[:3] or \
+                k_scale.shape[4] != 2 or k_scale.shape[3] < 1 or \
+                2 * half % k_scale.shape[3]:
+            raise ValueError("k_scale must be [pages, heads, page_size, "
+                             "head_dim / group, 2]")
+        for a, b, name in ((k, v, "v"), (k_scale, v_scale, "v_scale")):
+            if b.shape != a.shape or n > 1 and b.stride(0) != a.stride(0):
+                raise ValueError("%s must have %s's shape and page stride" %
+                                 (name, name.replace("v", "k", 1)))
+            if n and not (a[0].is_contiguous() and b[0].is_contiguous()):
+                raise ValueError("pages must be contiguous")
+        _dev(block_table, dev, "block_table", torch.int32)
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [B, max_pages]")
+        self._tensors = k, v, k_scale, v_scale, block_table
+        self.B, self.heads, self.head_dim = \
+            block_table.shape[0], heads, 2 * half
+        self.group = 2 * half // k_scale.shape[3]
+        self.device, self.dtype = dev, dtype
+        self._struct = _PagedKV4Struct(
+            k.data_ptr(), v.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), _CACHE_DT[dtype], n, page, heads, 2 * half,
+            self.group, k.stride(0) if n > 1 else 0,
+            2 * k_scale.stride(0) if n > 1 else 0, block_table.data_ptr(),
+            block_table.shape[1])
+        self._addr = ctypes.addressof(self._struct)
+
+    @classmethod
+    def empty(cls, num_pages, page_size, heads, head_dim, block_table, dtype,
+              group=64):
+        """A cache of zeros on block_table's device."""
+        def zeros(*row, dt):
+            return torch.zeros((num_pages, heads, page_size) + row, dtype=dt,
+                               device=block_table.device)
+        if group not in (32, 64, 128) or head_dim % group:
+            raise ValueError("group must be 32, 64 or 128 and divide "
+                             "head_dim")
+        k, v = (zeros(head_dim // 2, dt=torch.uint8) for _ in range(2))
+        ks, vs = (zeros(head_dim // group, 2, dt=torch.float16)
+                  for _ in range(2))
+        return cls(k, v, ks, vs, block_table, dtype)
+
+
+def _in_4_bits(cache, want):
+    """Refuse a cache of the other kind."""
+    if isinstance(cache, PagedKV4) is not want:
+        raise TypeError("cache must be a %s" %
+                        ("PagedKV4" if want else "PagedKV"))
+
+
 # The checks below look at each property once: a call on a few tokens takes
 # less time on the GPU than its checks can take here.
 
@@ -748,16 +854,9 @@ def _status(status, device):
     return _vec(status, device, torch.int32, "status")
 
 
-def kv_append(cache, k, v, q_start, kv_len, *, q=None, cos_sin=None,
-              positions=None, interleaved=False, status=None):
-    """Append new tokens' keys and values to a PagedKV, rotated by position
-    (sd_kv_append).
-
-    k, v [total, heads, D] and q [total, q_heads, D] (optional), rows may be
-    strided; q_start [B+1] and kv_len [B] int32 (kv_len counts the new
-    tokens); cos_sin [max_pos, rot_dim] float32, cosines then sines (None:
-    no rotation); positions [total] int32 (None: the index in the sequence).
-    Returns the rotated queries (None without q)."""
+def _append(fn, cache, k, v, q_start, kv_len, q, cos_sin, positions,
+            interleaved, status):
+    """sd_kv_append or sd_kv4_append."""
     dev, D = cache.device, cache.head_dim
     total, _, ks = _rows(k, cache, "k", cache.heads)
     nv, _, vs = _rows(v, cache, "v", cache.heads)
@@ -779,13 +878,86 @@ def kv_append(cache, k, v, q_start, kv_len, *, q=None, cos_sin=None,
         pp = _vec(positions, dev, torch.int32, "positions")
         if positions.numel() != total:
             raise ValueError("positions must be [total]")
-    rc = lib().sd_kv_append(
+    rc = fn(
         cache._addr, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, Hq, start,
         lens, pp, cp, max_pos, rot, 1 if interleaved else 0, B, total, op,
         _status(status, dev), _raw_stream(dev))
     if rc != SD_OK:
         _check(rc)
     return out
+
+
+def kv_append(cache, k, v, q_start, kv_len, *, q=None, cos_sin=None,
+              positions=None, interleaved=False, status=None):
+    """Append new tokens' keys and values to a PagedKV, rotated by position
+    (sd_kv_append).
+
+    k, v [total, heads, D] and q [total, q_heads, D] (optional), rows may be
+    strided; q_start [B+1] and kv_len [B] int32 (kv_len counts the new
+    tokens); cos_sin [max_pos, rot_dim] float32, cosines then sines (None:
+    no rotation); positions [total] int32 (None: the index in the sequence).
+    Returns the rotated queries (None without q)."""
+    _in_4_bits(cache, False)
+    return _append(lib().sd_kv_append, cache, k, v, q_start, kv_len, q,
+                   cos_sin, positions, interleaved, status)
+
+
+def kv4_append(cache, k, v, q_start, kv_len, *, q=None, cos_sin=None,
+               positions=None, interleaved=False, status=None):
+    """kv_append to a PagedKV4: keys (rotated) and values are quantised to 4
+    bits as they are written (sd_kv4_append).  Arguments and result as in
+    kv_append."""
+    _in_4_bits(cache, True)
+    return _append(lib().sd_kv4_append, cache, k, v, q_start, kv_len, q,
+                   cos_sin, positions, interleaved, status)
+
+
+def kv4_read(cache, q_start, kv_len, total, *, status=None):
+    """Tokens of a PagedKV4 as 16-bit rows (sd_kv4_read): the last
+    q_start[b+1] - q_start[b] of the first kv_len[b] keys and values of
+    sequence b, at rows q_start[b] on.  q_start [B+1], kv_len [B] int32;
+    total: the rows of the result, q_start[-1] or more (rows of no sequence
+    are whatever the allocation held).  Returns k and v [total, heads, D]."""
+    _in_4_bits(cache, True)
+    dev, heads, D = cache.device, cache.heads, cache.head_dim
+    B, start, lens = _lengths(cache, q_start, kv_len)
+    k = torch.empty((total, heads, D), dtype=cache.dtype, device=dev)
+    v = torch.empty((total, heads, D), dtype=cache.dtype, device=dev)
+    rc = lib().sd_kv4_read(
+        cache._addr, start, lens, B, total, k.data_ptr(), heads * D,
+        v.data_ptr(), heads * D, _status(status, dev), _raw_stream(dev))
+    if rc != SD_OK:
+        _check(rc)
+    return {"k": k, "v": v}
+
+
+def _attention(fn, ws_bytes, q, cache, q_start, kv_len, max_q, scale,
+               tree_mask, want_lse, status, workspace):
+    """sd_paged_attention or sd_kv4_attention."""
+    dev, D = cache.device, cache.head_dim
+    total, Hq, qs = _rows(q, cache, "q")
+    B, start, lens = _lengths(cache, q_start, kv_len)
+    words, mp = 0, None
+    if tree_mask is not None:
+        mp = _vec(tree_mask, dev, torch.int32, "tree_mask")
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != total:
+            raise ValueError("tree_mask must be [total, words]")
+        words = tree_mask.shape[1]
+    if max_q is None:
+        max_q = -(-total // max(B, 1))
+    out = torch.empty((total, Hq, D), dtype=cache.dtype, device=dev)
+    lse = torch.empty((total, Hq), dtype=torch.float32,
+                      device=dev) if want_lse else None
+    nbytes = ws_bytes(Hq, cache.heads, D, max_q)
+    ws = (workspace or _default_ws).get(dev, nbytes)
+    rc = fn(
+        q.data_ptr(), qs, Hq, cache._addr, start, lens, mp, words, B, total,
+        max_q, D ** -0.5 if scale is None else scale, out.data_ptr(),
+        _ptr(lse), _status(status, dev), ws.data_ptr(), ws.numel(),
+        _raw_stream(dev))
+    if rc != SD_OK:
+        _check(rc)
+    return {"out": out, "lse": lse} if want_lse else {"out": out}
 
 
 def paged_attention(q, cache, q_start, kv_len, *, max_q=None, scale=None,
@@ -803,31 +975,25 @@ def paged_attention(q, cache, q_start, kv_len, *, max_q=None, scale=None,
     defaults to D ** -0.5.  workspace: scratch between the call's two kernels
     (default: the current stream's and thread's own).  Returns out [total,
     q_heads, D] (and lse [total, q_heads] float32 when want_lse)."""
-    dev, D = cache.device, cache.head_dim
-    total, Hq, qs = _rows(q, cache, "q")
-    B, start, lens = _lengths(cache, q_start, kv_len)
-    words, mp = 0, None
-    if tree_mask is not None:
-        mp = _vec(tree_mask, dev, torch.int32, "tree_mask")
-        if tree_mask.dim() != 2 or tree_mask.shape[0] != total:
-            raise ValueError("tree_mask must be [total, words]")
-        words = tree_mask.shape[1]
-    if max_q is None:
-        max_q = -(-total // max(B, 1))
-    out = torch.empty((total, Hq, D), dtype=cache.dtype, device=dev)
-    lse = torch.empty((total, Hq), dtype=torch.float32,
-                      device=dev) if want_lse else None
+    _in_4_bits(cache, False)
     L = lib()
-    nbytes = L.sd_paged_attention_workspace(Hq, cache.heads, D, max_q)
-    ws = (workspace or _default_ws).get(dev, nbytes)
-    rc = L.sd_paged_attention(
-        q.data_ptr(), qs, Hq, cache._addr, start, lens, mp, words, B, total,
-        max_q, D ** -0.5 if scale is None else scale, out.data_ptr(),
-        _ptr(lse), _status(status, dev), ws.data_ptr(), ws.numel(),
-        _raw_stream(dev))
-    if rc != SD_OK:
-        _check(rc)
-    return {"out": out, "lse": lse} if want_lse else {"out": out}
+    return _attention(L.sd_paged_attention, L.sd_paged_attention_workspace,
+                      q, cache, q_start, kv_len, max_q, scale, tree_mask,
+                      want_lse, status, workspace)
+
+
+def kv4_attention(q, cache, q_start, kv_len, *, max_q=None, scale=None,
+                  tree_mask=None, want_lse=False, status=None,
+                  workspace=None):
+    """Attention of a chunk of new tokens per sequence over a PagedKV4
+    (sd_kv4_attention); their keys and values are appended before.
+    Arguments and results as in paged_attention; keys and values are the
+    fp16 numbers that the codes stand for."""
+    _in_4_bits(cache, True)
+    L = lib()
+    return _attention(L.sd_kv4_attention, L.sd_kv4_attention_workspace, q,
+                      cache, q_start, kv_len, max_q, scale, tree_mask,
+                      want_lse, status, workspace)
 
 
 _LOGIT_DT = {torch.float32: SD_F32, torch.bfloat16: SD_BF16}

@@ -1,0 +1,103 @@
+// sdv_kv4.cuh -- the 4-bit cache: what its codes stand for, and the host's
+// checks of a description.
+//
+// A group's pair (a, b) of fp16 numbers makes its code n the fp16 number
+// nearest to b + (64 + n) a.  fp16 numbers from 64 on lie 2^-4 apart, so a
+// code's four bits at bits 4 to 7 of 0x5400 are the number 64 + n: a pair of
+// values is one logic operation and one fma of fp16 pairs, with a single
+// rounding, on every path that reads the cache.  (With b + n a the 64 would
+// cost a subtraction a pair: half as much again.)  b is coarser for it, a
+// sixteenth of a step, which the codes are chosen by; so are values beyond
+// kMost, which leaves 64 steps of a group inside fp16.
+//
+// A word of codes holds eight neighbours, elements 0, 2, 4, 6, 1, 3, 5, 7
+// from its lowest nibble on: a mask then finds neighbours (2 j, 2 j + 1).
+#pragma once
+
+#include "sdv_paged.cuh"
+
+namespace sdv {
+
+constexpr float kKv4Most = 6144.f;
+
+// Codes j and j + 4 of a word, which stand for elements 2 j and 2 j + 1, as
+// the fp16 pair (64 + n, 64 + n').
+__device__ __forceinline__ uint32_t kv4_codes(uint32_t w, int j) {
+  const uint32_t x = j == 0 ? w << 4 : w >> (4 * j - 4);
+  return (x & 0x00f000f0u) | 0x54005400u;
+}
+__device__ __forceinline__ uint32_t kv4_fma(uint32_t x, uint32_t a,
+                                            uint32_t b) {
+  uint32_t y;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(x), "r"(a), "r"(b));
+  return y;
+}
+// One number of a pair in both halves.
+__device__ __forceinline__ uint32_t both_lo(uint32_t x) {
+  return __byte_perm(x, x, 0x1010);
+}
+__device__ __forceinline__ uint32_t both_hi(uint32_t x) {
+  return __byte_perm(x, x, 0x3232);
+}
+
+// Where the codes and the pairs of a cache lie: in bytes, pages `stride`
+// apart, inside a page [heads][page_size] rows.
+struct Kv4Cache {
+  const char *k, *v, *k_scale, *v_scale;
+  long long page_stride, scale_stride;
+  int num_pages, row_bytes, scale_bytes;
+  int shift;  // log2 of the group
+};
+
+inline sd_status check_kv4(const sd_paged_kv4 *c) {
+  SDV_REQUIRE(c != nullptr, "cache is null");
+  SDV_REQUIRE(c->dt == SD_BF16 || c->dt == SD_F16, "bad cache dtype %d",
+              (int)c->dt);
+  SDV_REQUIRE(c->num_pages >= 0, "num_pages < 0");
+  SDV_REQUIRE(c->page_size >= 1, "page_size < 1");
+  SDV_REQUIRE(c->max_pages >= 0, "max_pages < 0");
+  SDV_REQUIRE((long long)c->max_pages * c->page_size < (1LL << 31) - 256,
+              "max_pages page_size = %lld does not fit 31 bits",
+              (long long)c->max_pages * c->page_size);
+  SDV_REQUIRE(c->heads >= 1 && c->heads <= 65535, "heads=%d outside [1, 65535]",
+              c->heads);
+  if (c->head_dim != 64 && c->head_dim != 128)
+    return fail(SD_ERR_UNSUPPORTED, "head_dim=%d is neither 64 nor 128",
+                c->head_dim);
+  SDV_REQUIRE((c->group == 32 || c->group == 64 || c->group == 128) &&
+                  c->group <= c->head_dim,
+              "group=%d is not 32, 64 or 128, or above head_dim=%d", c->group,
+              c->head_dim);
+  if (c->page_size % 8 != 0)
+    return fail(SD_ERR_UNSUPPORTED, "page_size=%d is not a multiple of 8",
+                c->page_size);
+  const long long rows = (long long)c->heads * c->page_size;
+  SDV_REQUIRE(c->num_pages <= 1 ||
+                  (c->page_stride >= rows * (c->head_dim / 2) &&
+                   c->scale_stride >= rows * (c->head_dim / c->group) * 4),
+              "pages overlap: a stride is below a page's bytes");
+  SDV_REQUIRE(c->page_stride >= 0 && c->scale_stride >= 0 &&
+                  c->page_stride % 16 == 0 && c->scale_stride % 16 == 0,
+              "page strides must be multiples of 16 bytes");
+  SDV_REQUIRE(aligned16(c->k) && aligned16(c->v) && aligned16(c->k_scale) &&
+                  aligned16(c->v_scale),
+              "codes and scales must be 16-byte aligned");
+  return SD_OK;
+}
+
+inline Kv4Cache kv4_cache(const sd_paged_kv4 *c) {
+  Kv4Cache r;
+  r.k = static_cast<const char *>(c->k);
+  r.v = static_cast<const char *>(c->v);
+  r.k_scale = static_cast<const char *>(c->k_scale);
+  r.v_scale = static_cast<const char *>(c->v_scale);
+  r.page_stride = c->page_stride;
+  r.scale_stride = c->scale_stride;
+  r.num_pages = c->num_pages;
+  r.row_bytes = c->head_dim / 2;
+  r.scale_bytes = c->head_dim / c->group * 4;
+  r.shift = c->group == 32 ? 5 : c->group == 64 ? 6 : 7;
+  return r;
+}
+
+}  // namespace sdv

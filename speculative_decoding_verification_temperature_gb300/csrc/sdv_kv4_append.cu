@@ -1,0 +1,480 @@
+// sdv_kv4_append.cu -- sd_kv4_append: new tokens' keys and values quantised
+// to 4 bits as they go into the paged cache, keys and queries rotated by
+// position on the way; sd_kv4_read: tokens of the cache back as 16-bit rows.
+//
+// With lo and hi the least and greatest of a group's values,
+//   a = fp16((hi - lo) / 15), b = fp16(lo - 64 a),
+//   n = rint((x - b) / a) - 64, kept inside 0 .. 15,
+// each step rounded to fp32 by itself (no contraction), 1 / 15 and 1 / a being
+// rounded first: the codes are the same numbers wherever they are computed.
+#include "sdv_kv4.cuh"
+
+namespace sdv {
+namespace {
+
+struct Append4Params {
+  const void *k, *v, *q;
+  long long k_stride, v_stride, q_stride;
+  const int32_t *q_start, *kv_len, *positions, *block_table;
+  const float *cos_sin;
+  int max_pos, rot, interleaved;
+  int B, total, Hq, Hkv;
+  int page_size, max_pages;
+  Kv4Cache c;
+  void *q_out;
+  int32_t *dev_status;
+};
+
+// Where one packed row goes: its page (negative: nowhere), token in the page
+// and row of the angles; st: the status bits it sets; owned: it belongs to a
+// sequence.
+struct Place {
+  int page, token, pos, st;
+  bool owned;
+};
+
+template <class P>
+__device__ __forceinline__ Place place_row(const P &p, int row) {
+  Place r{-1, 0, 0, 0, false};
+  const int b = warp_find_sequence(p.q_start, p.B, row);
+  const Chunk c = load_chunk(p.q_start, p.kv_len, b, p.total,
+                             (long long)p.max_pages * p.page_size);
+  if (!c.rows_ok) {
+    r.st = SD_DEV_BAD_LENGTH;
+    return r;
+  }
+  if (row < c.start || row >= c.start + c.n) return r;
+  r.owned = true;
+  if (!c.usable) {
+    r.st = SD_DEV_BAD_LENGTH;
+    return r;
+  }
+  r.pos = c.kv - c.n + (row - c.start);
+  const int page =
+      __ldg(p.block_table + (long long)b * p.max_pages + r.pos / p.page_size);
+  if (page < 0 || page >= p.c.num_pages) r.st = SD_DEV_BAD_PAGE;
+  else r.page = page;
+  r.token = r.pos % p.page_size;
+  return r;
+}
+
+template <class T> __device__ __forceinline__ float2 unpack2(uint32_t u);
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t u) {
+  return make_float2(__uint_as_float(u << 16),
+                     __uint_as_float(u & 0xffff0000u));
+}
+template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t u) {
+  return __half22float2(*reinterpret_cast<__half2 *>(&u));
+}
+template <class T> __device__ __forceinline__ uint32_t pack2(float2 x);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float2 x) {
+  const __nv_bfloat162 v = __float22bfloat162_rn(x);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float2 x) {
+  const __half2 v = __float22half2_rn(x);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// min and max that keep a NaN.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Codes of eight neighbours, one word, and their group's pair; `lanes`
+// neighbouring lanes hold a group.  The whole warp calls.
+__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], int lanes,
+                                              uint32_t &pair) {
+  float lo = x[0], hi = x[0];
+#pragma unroll
+  for (int e = 1; e < 8; ++e) lo = min_nan(lo, x[e]), hi = max_nan(hi, x[e]);
+  for (int d = 1; d < lanes; d <<= 1) {
+    lo = min_nan(lo, __shfl_xor_sync(~0u, lo, d));
+    hi = max_nan(hi, __shfl_xor_sync(~0u, hi, d));
+  }
+  if (!(lo > -kInf && hi < kInf)) {  // a group that holds NaN or infinity
+    pair = 0x7e007e00u;
+    return 0;
+  }
+  lo = fminf(fmaxf(lo, -kKv4Most), kKv4Most);
+  hi = fminf(fmaxf(hi, -kKv4Most), kKv4Most);
+  const __half a = __float2half_rn(__fmul_rn(__fsub_rn(hi, lo), 1.f / 15.f));
+  const float af = __half2float(a);
+  const __half b = __float2half_rn(__fsub_rn(lo, 64.f * af));
+  const float bf = __half2float(b);
+  const float inv = af > 0.f ? __frcp_rn(af) : 0.f;
+  uint32_t w = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float t = __fmul_rn(__fsub_rn(x[e], bf), inv);
+    t = fminf(fmaxf(t, 64.f), 79.f);
+    // 1.5 x 2^23 + t: t rounded to a whole number, its low bits the code
+    const uint32_t n = __float_as_uint(__fadd_rn(t, 12582912.f)) & 15;
+    w |= n << 4 * ((e & 1) * 4 + e / 2);
+  }
+  pair = (uint32_t)__half_as_ushort(b) << 16 | __half_as_ushort(a);
+  return w;
+}
+
+// A CTA per packed row; a thread takes eight neighbours of every (threads /
+// pieces)-th head, and the elements they are turned with: its own (WIDE,
+// interleaved), or a piece rot_dim / 2 away.  WIDE: rot_dim is a multiple of
+// 16 and rows are 16-byte aligned, so that pieces are whole 16-byte loads and
+// turn as a whole; otherwise elements are loaded one by one.
+constexpr int kAhead4 = 2;
+template <class T, int D, bool WIDE>
+__global__ void __launch_bounds__(kThreads)
+append4_kernel(const __grid_constant__ Append4Params p) {
+  griddep_wait();
+  constexpr int PER = D / 8;
+  const int row = blockIdx.x, i = threadIdx.x % PER;
+  const int first = threadIdx.x / PER, step = blockDim.x / PER;
+  const int heads = p.Hq + 2 * p.Hkv, half = p.rot / 2;
+  // element (or piece's first element) e is turned with other(e), by angle(e)
+  auto other = [&](int e) {
+    return p.interleaved ? e ^ 1 : e < half ? e + half : e - half;
+  };
+  const bool turns = 8 * i < p.rot;
+  const bool fetch = turns && !p.interleaved;
+  struct Piece {
+    uint4 own, other;
+  };
+  auto src_of = [&](int h) {
+    if (h < p.Hq) return (const T *)p.q + row * p.q_stride + (long long)h * D;
+    h -= p.Hq;
+    if (h < p.Hkv)
+      return (const T *)p.k + row * p.k_stride + (long long)h * D;
+    return (const T *)p.v + row * p.v_stride + (long long)(h - p.Hkv) * D;
+  };
+  auto load = [&](int h) {
+    Piece x;
+    x.own = x.other = make_uint4(0, 0, 0, 0);
+    if (h >= heads) return x;
+    const T *src = src_of(h);
+    const bool turned = h < p.Hq + p.Hkv;
+    if (WIDE) {
+      x.own = ld_nc_v4(src + 8 * i);
+      if (fetch && turned) x.other = ld_nc_v4(src + other(8 * i));
+    } else {
+      T own[8], oth[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int at = 8 * i + e;
+        own[e] = src[at];
+        oth[e] = turned && at < p.rot ? src[other(at)] : own[e];
+      }
+      x.own = *reinterpret_cast<const uint4 *>(own);
+      x.other = *reinterpret_cast<const uint4 *>(oth);
+    }
+    return x;
+  };
+  Piece ahead[kAhead4];
+#pragma unroll
+  for (int n = 0; n < kAhead4; ++n) ahead[n] = load(first + n * step);
+  Place pl = place_row(p, row);
+  if (pl.st == 0 && pl.owned && p.cos_sin) {
+    if (p.positions) pl.pos = __ldg(p.positions + row);
+    if (pl.pos < 0 || pl.pos >= p.max_pos) {
+      pl.st = SD_DEV_BAD_POSITION;
+      pl.page = -1;
+    }
+  }
+  if (threadIdx.x == 0) status_or(p.dev_status, pl.st);
+  if (!pl.owned) return;
+  // x' = x c + x_other s: the sine of the first of a pair is negative
+  float c[8], s[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int at = 8 * i + e;
+    c[e] = 1.f, s[e] = 0.f;
+    if (at < p.rot && pl.page >= 0) {
+      const bool head = p.interleaved ? !(at & 1) : at < half;
+      const int angle = p.interleaved ? at / 2 : head ? at : at - half;
+      const float *cs = p.cos_sin + (long long)pl.pos * p.rot + angle;
+      c[e] = __ldg(cs);
+      s[e] = head ? -__ldg(cs + half) : __ldg(cs + half);
+    }
+  }
+  const int lanes = 1 << (p.c.shift - 3);
+  auto put = [&](int h, const Piece &in) {
+    const bool is_q = h < p.Hq, turned = h < p.Hq + p.Hkv;
+    const uint32_t own[4] = {in.own.x, in.own.y, in.own.z, in.own.w};
+    const uint32_t oth[4] = {in.other.x, in.other.y, in.other.z, in.other.w};
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 u = unpack2<T>(own[e]);
+      x[2 * e] = u.x, x[2 * e + 1] = u.y;
+      if (turned && turns) {
+        float2 v = unpack2<T>(oth[e]);
+        if (WIDE && p.interleaved) v = make_float2(u.y, u.x);
+        const float y0 = __fadd_rn(__fmul_rn(u.x, c[2 * e]),
+                                   __fmul_rn(v.x, s[2 * e]));
+        const float y1 = __fadd_rn(__fmul_rn(u.y, c[2 * e + 1]),
+                                   __fmul_rn(v.y, s[2 * e + 1]));
+        // (an odd piece may end its turn in the middle)
+        if (WIDE || 8 * i + 2 * e < p.rot) x[2 * e] = y0;
+        if (WIDE || 8 * i + 2 * e + 1 < p.rot) x[2 * e + 1] = y1;
+      }
+    }
+    uint32_t pair;
+    const uint32_t word = quantise8(x, lanes, pair);  // the whole warp
+    if (h >= heads) return;
+    if (is_q) {
+      T *to = (T *)p.q_out + ((long long)row * p.Hq + h) * D + 8 * i;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (pl.page >= 0) {
+        w.x = pack2<T>(make_float2(x[0], x[1]));
+        w.y = pack2<T>(make_float2(x[2], x[3]));
+        w.z = pack2<T>(make_float2(x[4], x[5]));
+        w.w = pack2<T>(make_float2(x[6], x[7]));
+      }
+      if (WIDE) {
+        *reinterpret_cast<uint4 *>(to) = w;
+      } else {
+        const T *y = reinterpret_cast<const T *>(&w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) to[e] = y[e];
+      }
+    } else if (pl.page >= 0) {
+      const bool is_k = turned;
+      const int kh = h - p.Hq - (is_k ? 0 : p.Hkv);
+      const long long at = (long long)kh * p.page_size + pl.token;
+      char *codes = const_cast<char *>(is_k ? p.c.k : p.c.v) +
+                    pl.page * p.c.page_stride + at * (D / 2);
+      char *pairs = const_cast<char *>(is_k ? p.c.k_scale : p.c.v_scale) +
+                    pl.page * p.c.scale_stride + at * p.c.scale_bytes;
+      reinterpret_cast<uint32_t *>(codes)[i] = word;
+      if ((i & (lanes - 1)) == 0)
+        reinterpret_cast<uint32_t *>(pairs)[8 * i >> p.c.shift] = pair;
+    }
+  };
+  // every thread of a warp makes the same rounds
+  for (int h0 = 0; h0 < heads; h0 += kAhead4 * step) {
+#pragma unroll
+    for (int n = 0; n < kAhead4; ++n) {
+      const Piece now = ahead[n];
+      const int h = h0 + first + n * step;
+      if (h0 + (n + kAhead4) * step < heads) ahead[n] = load(h + kAhead4 * step);
+      put(h, now);
+    }
+  }
+}
+
+struct Read4Params {
+  const int32_t *q_start, *kv_len, *block_table;
+  int B, total, Hkv, page_size, max_pages;
+  Kv4Cache c;
+  void *k_out, *v_out;
+  long long k_stride, v_stride;
+  int32_t *dev_status;
+};
+
+// A warp per packed row, a lane for 16 elements of every (512 / D)-th head:
+// eight bytes of codes, the pair, and 32 bytes written.
+constexpr int kReadAhead = 4;
+template <class T, int D>
+__global__ void __launch_bounds__(kThreads)
+read4_kernel(const __grid_constant__ Read4Params p) {
+  griddep_wait();
+  constexpr int PER = D / 16, STEP = 32 / PER;
+  const int row = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (row >= p.total) return;  // the whole warp
+  const int lane = threadIdx.x & 31, i = lane % PER, first = lane / PER;
+  const Place pl = place_row(p, row);
+  if (lane == 0) status_or(p.dev_status, pl.st);
+  if (!pl.owned) return;
+  const int group = 16 * i >> p.c.shift;
+  for (int h0 = 0; h0 < 2 * p.Hkv; h0 += kReadAhead * STEP) {
+    uint2 w[kReadAhead];
+    uint32_t pair[kReadAhead];
+#pragma unroll
+    for (int n = 0; n < kReadAhead; ++n) {
+      const int h = h0 + n * STEP + first;
+      w[n] = make_uint2(0, 0);
+      pair[n] = 0x7e007e00u;  // NaN
+      if (h < 2 * p.Hkv && pl.page >= 0) {
+        const bool is_k = h < p.Hkv;
+        const long long at =
+            (long long)(is_k ? h : h - p.Hkv) * p.page_size + pl.token;
+        w[n] = __ldg(reinterpret_cast<const uint2 *>(
+            (is_k ? p.c.k : p.c.v) + pl.page * p.c.page_stride +
+            at * (D / 2) + 8 * i));
+        pair[n] = __ldg(reinterpret_cast<const uint32_t *>(
+            (is_k ? p.c.k_scale : p.c.v_scale) +
+            pl.page * p.c.scale_stride + at * p.c.scale_bytes + 4 * group));
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < kReadAhead; ++n) {
+      const int h = h0 + n * STEP + first;
+      if (h >= 2 * p.Hkv) continue;
+      const bool is_k = h < p.Hkv;
+      T *to = is_k ? (T *)p.k_out + row * p.k_stride + (long long)h * D
+                   : (T *)p.v_out + row * p.v_stride +
+                         (long long)(h - p.Hkv) * D;
+      const uint32_t a = both_lo(pair[n]), b = both_hi(pair[n]);
+      const uint32_t words[2] = {w[n].x, w[n].y};
+      uint32_t y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] = kv4_fma(kv4_codes(words[e / 4], e % 4), a, b);
+        if (!std::is_same<T, __half>::value)
+          y[e] = pack2<T>(unpack2<__half>(y[e]));
+      }
+      asm volatile(
+          "st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+              to + 16 * i),
+          "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(y[4]), "r"(y[5]),
+          "r"(y[6]), "r"(y[7])
+          : "memory");
+    }
+  }
+}
+
+template <class T, int D>
+const void *append_of(bool wide) {
+  return wide ? (const void *)append4_kernel<T, D, true>
+              : (const void *)append4_kernel<T, D, false>;
+}
+
+}  // namespace
+}  // namespace sdv
+
+using namespace sdv;
+
+extern "C" sd_status sd_kv4_append(
+    const sd_paged_kv4 *cache, const void *k, long long k_stride,
+    const void *v, long long v_stride, const void *q, long long q_stride,
+    int q_heads, const int32_t *q_start, const int32_t *kv_len,
+    const int32_t *positions, const float *cos_sin, int max_pos, int rot_dim,
+    int interleaved, int B, int total, void *q_out, int32_t *dev_status,
+    void *stream) {
+  sd_status st = check_kv4(cache);
+  if (st != SD_OK) return st;
+  SDV_REQUIRE(B >= 0 && total >= 0, "B < 0 or total < 0");
+  SDV_REQUIRE(q_heads >= 0 && q_heads <= 65535,
+              "q_heads=%d outside [0, 65535]", q_heads);
+  SDV_REQUIRE((q == nullptr) == (q_out == nullptr),
+              "q and q_out go together");
+  const int Hq = q ? q_heads : 0;
+  const int D = cache->head_dim;
+  if (cos_sin) {
+    SDV_REQUIRE(rot_dim >= 2 && rot_dim <= D && rot_dim % 2 == 0,
+                "rot_dim=%d is not even and in [2, %d]", rot_dim, D);
+    SDV_REQUIRE(max_pos >= 1, "max_pos < 1");
+  }
+  if (B == 0 || total == 0) return SD_OK;
+  SDV_REQUIRE(k && v && cache->k && cache->v && cache->k_scale &&
+                  cache->v_scale && q_start && kv_len,
+              "null pointer");
+  SDV_REQUIRE(cache->max_pages == 0 || cache->block_table,
+              "block_table is null");
+  SDV_REQUIRE(k_stride >= (long long)cache->heads * D &&
+                  v_stride >= (long long)cache->heads * D &&
+                  (!q || q_stride >= (long long)Hq * D),
+              "tokens overlap: a stride is below heads x head_dim");
+  int sms = 0;
+  st = check_device(&sms);
+  if (st != SD_OK) return st;
+  Append4Params p;
+  p.k = k;
+  p.v = v;
+  p.q = q;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_stride = q_stride;
+  p.q_start = q_start;
+  p.kv_len = kv_len;
+  p.positions = positions;
+  p.block_table = cache->block_table;
+  p.cos_sin = cos_sin;
+  p.max_pos = max_pos;
+  p.rot = cos_sin ? rot_dim : 0;
+  p.interleaved = interleaved;
+  p.B = B;
+  p.total = total;
+  p.Hq = Hq;
+  p.Hkv = cache->heads;
+  p.page_size = cache->page_size;
+  p.max_pages = cache->max_pages;
+  p.c = kv4_cache(cache);
+  p.q_out = q_out;
+  p.dev_status = dev_status;
+  const bool wide = p.rot % 16 == 0 && aligned16(k) && aligned16(v) &&
+                    aligned16(q) && aligned16(q_out) &&
+                    (k_stride | v_stride | (q ? q_stride : 0)) % 8 == 0;
+  const bool bf = cache->dt == SD_BF16;
+  const void *kernel =
+      D == 64 ? (bf ? append_of<__nv_bfloat16, 64>(wide)
+                    : append_of<__half, 64>(wide))
+              : (bf ? append_of<__nv_bfloat16, 128>(wide)
+                    : append_of<__half, 128>(wide));
+  const long long all = (Hq + 2LL * cache->heads) * (D / 8);
+  const int threads =
+      all < kThreads ? (int)(all + 31) / 32 * 32 : kThreads;
+  void *args[] = {&p};
+  return launch_pdl(kernel, (unsigned)total, threads, 0,
+                    static_cast<cudaStream_t>(stream), args);
+}
+
+extern "C" sd_status sd_kv4_read(const sd_paged_kv4 *cache,
+                                 const int32_t *q_start,
+                                 const int32_t *kv_len, int B, int total,
+                                 void *k_out, long long k_stride, void *v_out,
+                                 long long v_stride, int32_t *dev_status,
+                                 void *stream) {
+  sd_status st = check_kv4(cache);
+  if (st != SD_OK) return st;
+  const int D = cache->head_dim;
+  SDV_REQUIRE(B >= 0 && total >= 0, "B < 0 or total < 0");
+  if (B == 0 || total == 0) return SD_OK;
+  SDV_REQUIRE(cache->k && cache->v && cache->k_scale && cache->v_scale &&
+                  q_start && kv_len && k_out && v_out,
+              "null pointer");
+  SDV_REQUIRE(cache->max_pages == 0 || cache->block_table,
+              "block_table is null");
+  SDV_REQUIRE(k_stride >= (long long)cache->heads * D &&
+                  v_stride >= (long long)cache->heads * D,
+              "tokens overlap: a stride is below heads x head_dim");
+  SDV_REQUIRE((reinterpret_cast<uintptr_t>(k_out) & 31) == 0 &&
+                  (reinterpret_cast<uintptr_t>(v_out) & 31) == 0 &&
+                  k_stride % 16 == 0 && v_stride % 16 == 0,
+              "k_out and v_out must be 32-byte aligned, their strides "
+              "multiples of 16");
+  int sms = 0;
+  st = check_device(&sms);
+  if (st != SD_OK) return st;
+  Read4Params p;
+  p.q_start = q_start;
+  p.kv_len = kv_len;
+  p.block_table = cache->block_table;
+  p.B = B;
+  p.total = total;
+  p.Hkv = cache->heads;
+  p.page_size = cache->page_size;
+  p.max_pages = cache->max_pages;
+  p.c = kv4_cache(cache);
+  p.k_out = k_out;
+  p.v_out = v_out;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.dev_status = dev_status;
+  const bool bf = cache->dt == SD_BF16;
+  const void *kernel =
+      D == 64 ? (bf ? (const void *)read4_kernel<__nv_bfloat16, 64>
+                    : (const void *)read4_kernel<__half, 64>)
+              : (bf ? (const void *)read4_kernel<__nv_bfloat16, 128>
+                    : (const void *)read4_kernel<__half, 128>);
+  void *args[] = {&p};
+  return launch_pdl(kernel, (unsigned)((total + kWarps - 1LL) / kWarps),
+                    kThreads, 0, static_cast<cudaStream_t>(stream), args);
+}
