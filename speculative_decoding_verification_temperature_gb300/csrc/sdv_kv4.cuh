@@ -24,7 +24,11 @@ constexpr float kKv4Most = 6144.f;
 // the fp16 pair (64 + n, 64 + n').
 __device__ __forceinline__ uint32_t kv4_codes(uint32_t w, int j) {
   const uint32_t x = j == 0 ? w << 4 : w >> (4 * j - 4);
-  return (x & 0x00f000f0u) | 0x54005400u;
+  uint32_t y;  // x & 0x00f000f0 | 0x54005400, one operation
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;"
+      : "=r"(y)
+      : "r"(x), "r"(0x00f000f0u), "r"(0x54005400u));
+  return y;
 }
 __device__ __forceinline__ uint32_t kv4_fma(uint32_t x, uint32_t a,
                                             uint32_t b) {
@@ -72,6 +76,8 @@ inline sd_status check_kv4(const sd_paged_kv4 *c) {
     return fail(SD_ERR_UNSUPPORTED, "page_size=%d is not a multiple of 8",
                 c->page_size);
   const long long rows = (long long)c->heads * c->page_size;
+  SDV_REQUIRE(rows < (1LL << 31) - 256,
+              "heads page_size = %lld does not fit 31 bits", rows);
   SDV_REQUIRE(c->num_pages <= 1 ||
                   (c->page_stride >= rows * (c->head_dim / 2) &&
                    c->scale_stride >= rows * (c->head_dim / c->group) * 4),

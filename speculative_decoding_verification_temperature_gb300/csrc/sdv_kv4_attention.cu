@@ -18,18 +18,23 @@ struct Attn4Params : UnitParams {
 // ------------------------------------------------------- few rows a head
 //
 // Where a cache head has few rows (one token of a group of query heads), a
-// warp takes 16 keys at a time from the cache straight into registers and
-// makes them operands there, with the keys as the rows of the products:
+// warp takes 16 keys at a time, makes their codes operands in registers, and
+// has the keys as the rows of its products:
 //   S^T [16 keys x 8 rows] = K [16 x D] Q^T,   O^T [D x 8] += V^T [D x 16] W
-// so that 8 rows are not padded to more.  A thread's four neighbours hold one
-// key's row: which elements of it a step of a product takes is free as long
-// as the queries' operand takes the same.
+// so that 8 rows are not padded to more.  Four neighbouring threads hold a
+// key's row: which of its elements a step of a product takes is free as long
+// as the queries' operand takes the same.  Each warp has a ring of such blocks
+// in shared memory, which it fills itself with asynchronous copies, codes and
+// pairs as they lie: no other warp is waited for until a unit ends.  (A warp
+// that brought tiles of 128 keys by bulk copies, four a page, was held up by
+// their number: 56 cycles a copy, 154 us on 64 sequences of pages of 16.)
 //
 // A row's weights are fp16, 2^kBias at its reference m, which moves up only
 // when a score is 2^kSlack above it: at most 2^15, and a weight 2^-24 of the
 // reference's still has all its bits.
 constexpr float kBias = 10.f, kSlack = 5.f;
-constexpr int kBlock = 16;  // keys of a warp's step
+constexpr float kNone = 3e38f;  // in place of kBias - m: no reference yet
+constexpr int kBlock = 16;     // keys of a warp's step
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0,
                                          uint32_t a1, uint32_t a2,
@@ -48,213 +53,238 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-template <int D> struct Words {  // a thread's share of a key's row
-  uint32_t w[D / 32];
-};
-template <int D>
-__device__ __forceinline__ Words<D> ld_words(const char *p) {
-  Words<D> r;
-  if constexpr (D == 128) {
-    asm("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-        : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3])
-        : "l"(p));
+// A thread's share of a key's row: N words of shared memory.
+template <int N>
+__device__ __forceinline__ void lds_words(const char *p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 x = *reinterpret_cast<const uint4 *>(p);
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  } else if constexpr (N == 2) {
+    const uint2 x = *reinterpret_cast<const uint2 *>(p);
+    w[0] = x.x, w[1] = x.y;
   } else {
-    asm("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];"
-        : "=r"(r.w[0]), "=r"(r.w[1])
-        : "l"(p));
-  }
-  return r;
-}
-template <int D>
-__device__ __forceinline__ void ld_half_words(const char *p, uint32_t *w) {
-  if constexpr (D == 128) {
-    asm("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];"
-        : "=r"(w[0]), "=r"(w[1])
-        : "l"(p));
-  } else {
-    asm("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+    w[0] = *reinterpret_cast<const uint32_t *>(p);
   }
 }
 
-// 16 keys on their way: the thread's quarter of keys g and g + 8, and its
-// eighth of the values 2 t, 2 t + 1, 2 t + 8, 2 t + 9.
-template <int D> struct Stage {
-  Words<D> k[2];
-  uint32_t ks[2];
-  uint32_t v[4][D / 64];
-  uint32_t vs[4];
+// A part of a unit that a warp leaves to be joined with others: (m, l) and O
+// of its rows.
+template <int ROWS, int D> struct Part {
+  float2 ml[ROWS];
+  alignas(16) float o[ROWS][D + 4];
+};
+struct PartInfo {
+  int there;          // there is one
+  int begun, ended;   // it has the unit's first, its last key
+  int rows, start, head, first, ahead;  // ahead: places to the unit's end
 };
 
 template <int ROWS, int D, int WARPS> struct Shared4 {
   Plan plan;
-  int bad;
-  float q_scale[ROWS];
-  float2 ml[WARPS][ROWS];
-  uint32_t q[ROWS][D / 2 + 4];
-  alignas(16) float o[WARPS][ROWS][D + 4];
+  PartInfo info[WARPS][2];
+  Part<ROWS, D> part[WARPS];  // of the warp's first unit
 };
 
-// The queries of a unit as fp16 rows in shared memory (rows that are none:
-// zeros), bf16 ones times a power of two that takes the row's largest to
-// [2^14, 2^15): exact but for elements 2^-28 of that and below.  A row with
-// NaN or infinity gets a NaN factor.
-template <class T, int D, int ROWS, int WARPS>
-__device__ __forceinline__ void load_queries(const Attn4Params &p,
-                                             const Units<ROWS> &u,
-                                             Shared4<ROWS, D, WARPS> &s) {
-  constexpr int E = D / 64;  // words a lane
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = warp; r < ROWS; r += WARPS) {
-    uint32_t w[E] = {};
-    float f = p.scale_log2;
-    if (r < u.rows) {
-      const int at = u.t * ROWS + r, tok = div_by(at, p.by_G);
-      const T *src = (const T *)p.q + (u.c.start + tok) * p.q_stride +
-                     (long long)(u.h * p.G + at - tok * p.G) * D;
-      const uint32_t *x = reinterpret_cast<const uint32_t *>(src) + lane * E;
-      uint32_t top = 0;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        w[e] = __ldg(x + e);
-        top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-      }
-      top = __reduce_max_sync(~0u, top);
-      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        // exponents above -86: the power is a normal number
-        const int exp = max((int)(top >> 7), 41) - 127;
-        const float up = __uint_as_float((uint32_t)(14 - exp + 127) << 23);
-        f *= __uint_as_float((uint32_t)(exp - 14 + 127) << 23);
-        if (top >= 0x7f80u) f = __int_as_float(0x7fc00000);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          w[e] = pack2<__half>(__uint_as_float(w[e] << 16) * up,
-                               __uint_as_float(w[e] & 0xffff0000u) * up);
-      } else if (top >= 0x7c00u) {
-        f = __int_as_float(0x7fc00000);
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) s.q[r][lane * E + e] = w[e];
-    if (lane == 0) s.q_scale[r] = f;
-  }
+__device__ __forceinline__ void cp16(uint32_t to, const void *from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to),
+               "l"(from)
+               : "memory");
 }
+__device__ __forceinline__ void cp_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N> __device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A thread's part of a query row, D / 4 elements, as fp16 pairs, and the
+// factor of its scores.  bf16 rows are multiplied by the power of two that
+// takes the row's largest element to [2^14, 2^15): exact but for elements
+// 2^-28 of that and below.  A row with NaN or infinity gets a NaN factor.
+template <class T, int N>
+__device__ __forceinline__ float load_query(const T *src, bool valid,
+                                            float scale, uint32_t (&w)[N]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (valid) x = __ldg(reinterpret_cast<const uint4 *>(src) + i / 4);
+    w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+  top = max(top, __shfl_xor_sync(~0u, top, 1));
+  top = max(top, __shfl_xor_sync(~0u, top, 2));
+  float f = scale;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    // exponents above -86: the power is a normal number
+    const int exp = max((int)(top >> 7), 41) - 127;
+    const float up = __uint_as_float((uint32_t)(14 - exp + 127) << 23);
+    f *= __uint_as_float((uint32_t)(exp - 14 + 127) << 23);
+    if (top >= 0x7f80u) f = __int_as_float(0x7fc00000);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      w[i] = pack2<__half>(__uint_as_float(w[i] << 16) * up,
+                           __uint_as_float(w[i] & 0xffff0000u) * up);
+  } else if (top >= 0x7c00u) {
+    f = __int_as_float(0x7fc00000);
+  }
+  return f;
+}
+
+// Blocks of a warp's ring, one of them in use.
+template <int NT> constexpr int ring_depth() { return NT == 1 ? 3 : 4; }
+constexpr int kKeys = 2 * kBlock;  // keys of a place in the shares
 
 template <class T, int D, int NT, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 2 : 1)
 kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
   constexpr int ROWS = 8 * NT, W = D / 32;  // W: words of a key a thread
+  constexpr int CODES = kBlock * D / 2;     // bytes of a block's key codes
+  constexpr int kDepth = ring_depth<NT>();
+  static_assert(sizeof(Part<ROWS, D>) <= kDepth * (2 * CODES + 8 * kBlock),
+                "a part does not fit the smallest ring");
   using S = Shared4<ROWS, D, WARPS>;
-  extern __shared__ __align__(16) char dyn[];
+  using U = Units<ROWS, kKeys>;
+  extern __shared__ __align__(128) char dyn[];
   S &s = *reinterpret_cast<S *>(dyn);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, t = lane & 3;
+  const int g = lane >> 2, t = lane & 3, sb = p.c.scale_bytes;
+  const int slot_bytes = 2 * CODES + 2 * kBlock * sb;
+  auto ring_of = [&](int w) {
+    return dyn + (sizeof(S) + 127) / 128 * 128 + w * kDepth * slot_bytes;
+  };
+  char *ring = ring_of(warp);
   griddep_wait();
-  make_plan<ROWS>(p, s.plan);
-  if (tid == 0) {
-    s.bad = 0;
-    p.cut[blockIdx.x].parts = 0;
-  }
+  make_plan<ROWS, kKeys>(p, s.plan);
+  if (tid == 0) p.cut[blockIdx.x].parts = 0;
+  if (lane < 2) s.info[warp][lane].there = 0;
   __syncthreads();
-  Units<ROWS> u(p, s.plan);
-  const int k_group = (t * (D / 4)) >> p.c.shift;
-  const int v_group = (g * (D / 8)) >> p.c.shift;
-  for (; u.left; u.next()) {
-    if (tid == 0 && u.j0 == 0 && u.j1 < u.nk) {
-      // this CTA's last unit goes on in the CTAs up to the one whose share
-      // holds the unit's last tile
-      const unsigned long long end = s.plan.x1 + (unsigned)(u.nk - u.j1);
-      CutUnit cut;
-      cut.parts = (int)((end * s.plan.n - 1) / s.plan.total) -
-                  (int)blockIdx.x + 1;
-      cut.rows = u.rows;
-      cut.start = u.c.start;
-      cut.head = u.h;
-      cut.first = u.t * ROWS;
-      p.cut[blockIdx.x] = cut;
-    }
-    load_queries<T, D, ROWS, WARPS>(p, u, s);
-    __syncthreads();
-    const int32_t *table = p.block_table + (long long)u.b * p.max_pages;
-    const int end = min(u.j1 * kTile, u.c.kv);
-    bool bad = false;
 
-    auto page_of = [&](int key, int &tok) {  // key: a multiple of 8
+  // ---- the warp's blocks of a unit: where the next ones lie.  Lane 2 i + hf
+  // holds page and token of half hf of the i-th block of a batch of sixteen.
+  struct Pages {
+    int page, tok;
+  };
+  auto look_up = [&](const U &v, int first) {  // the batch's first block
+    const int key =
+        v.j0 * kKeys + (first + (lane >> 1)) * kBlock + 8 * (lane & 1);
+    Pages x{-1, 0};
+    if (key < min(v.j1 * kKeys, v.c.kv)) {
       const int n = div_by(key, p.by_page);
-      tok = key - n * p.page_size;
-      if (key >= end) return -1;
-      const int id = __ldg(table + n);
-      return id >= 0 && id < p.c.num_pages ? id : -2;
+      x.page = __ldg(p.block_table + (long long)v.b * p.max_pages + n);
+      x.tok = key - n * p.page_size;
+      if (x.page < 0 || x.page >= p.c.num_pages) x.page = -2;
+    }
+    return x;
+  };
+  // A lane's part of the copies of a block: 16 bytes of the codes of both
+  // halves (D = 64: of one), 16 bytes of pairs.
+  const uint32_t to = smem_addr(ring) + 16 * lane;
+  const int which = lane / sb, pair_hf = lane / (sb / 2) & 1;
+  const char *pairs = (which ? p.c.v_scale : p.c.k_scale) +
+                      16 * (lane & (sb / 2 - 1));
+  int fill = 0;  // slot to fill next
+  bool bad = false;
+  auto fetch = [&](const U &v, const Pages &x, int i) {
+    const int page[2] = {__shfl_sync(~0u, x.page, 2 * i),
+                         __shfl_sync(~0u, x.page, 2 * i + 1)};
+    const int tok[2] = {__shfl_sync(~0u, x.tok, 2 * i),
+                        __shfl_sync(~0u, x.tok, 2 * i + 1)};
+    const uint32_t at = to + fill * slot_bytes;
+    bad = bad || page[0] == -2 || page[1] == -2;
+    auto code_at = [&](int pg, int tk) {
+      const int row = v.h * p.page_size + tk;
+      return pg * p.c.page_stride + (long long)row * (D / 2);
     };
-    auto fetch = [&](int key, Stage<D> &x, const int (&page)[2],
-                     const int (&tok)[2]) {
+    if constexpr (D == 128) {
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        x.ks[hf] = x.vs[2 * hf] = x.vs[2 * hf + 1] = 0;
-#pragma unroll
-        for (int i = 0; i < W; ++i) x.k[hf].w[i] = 0;
-#pragma unroll
-        for (int i = 0; i < W / 2; ++i)
-          x.v[2 * hf][i] = x.v[2 * hf + 1][i] = 0;
+      for (int hf = 0; hf < 2; ++hf)
         if (page[hf] >= 0) {
-          const long long at = (long long)u.h * p.page_size + tok[hf];
-          const char *kc =
-              p.c.k + page[hf] * p.c.page_stride + at * (D / 2);
-          const char *vc =
-              p.c.v + page[hf] * p.c.page_stride + at * (D / 2);
-          const char *kp = p.c.k_scale + page[hf] * p.c.scale_stride +
-                           at * p.c.scale_bytes;
-          const char *vp = p.c.v_scale + page[hf] * p.c.scale_stride +
-                           at * p.c.scale_bytes;
-          x.k[hf] = ld_words<D>(kc + g * (D / 2) + t * (D / 8));
-          ld_half_words<D>(vc + 2 * t * (D / 2) + g * (D / 16), x.v[2 * hf]);
-          ld_half_words<D>(vc + (2 * t + 1) * (D / 2) + g * (D / 16),
-                           x.v[2 * hf + 1]);
-          // what lies past the sequence's keys counts as zeros
-          const int k0 = key + 8 * hf;
-          if (k0 + g < end)
-            x.ks[hf] = __ldg(reinterpret_cast<const uint32_t *>(
-                kp + g * p.c.scale_bytes + 4 * k_group));
-          if (k0 + 2 * t < end)
-            x.vs[2 * hf] = __ldg(reinterpret_cast<const uint32_t *>(
-                vp + 2 * t * p.c.scale_bytes + 4 * v_group));
-          if (k0 + 2 * t + 1 < end)
-            x.vs[2 * hf + 1] = __ldg(reinterpret_cast<const uint32_t *>(
-                vp + (2 * t + 1) * p.c.scale_bytes + 4 * v_group));
-        } else if (page[hf] == -2) {
-          bad = true;
+          const long long c = code_at(page[hf], tok[hf]) + 16 * lane;
+          cp16(at + 512 * hf, p.c.k + c);
+          cp16(at + CODES + 512 * hf, p.c.v + c);
         }
+    } else {
+      const int mine = lane < 16 ? page[0] : page[1];
+      if (mine >= 0) {
+        const long long c =
+            code_at(mine, lane < 16 ? tok[0] : tok[1]) + 16 * (lane & 15);
+        cp16(at, p.c.k + c);
+        cp16(at + CODES, p.c.v + c);
       }
-    };
+    }
+    const int pair_page = pair_hf ? page[1] : page[0];
+    if (which < 2 && pair_page >= 0) {
+      const int row = v.h * p.page_size + (pair_hf ? tok[1] : tok[0]);
+      cp16(at + 2 * CODES, pairs + pair_page * p.c.scale_stride +
+                               (long long)row * sb);
+    }
+    cp_commit();
+    if (++fill == kDepth) fill = 0;
+  };
+  // Row g of a product's keys is key (g >> 1) + 4 (g & 1) of eight, so that
+  // the two whose values a thread pairs are t and t + 4: four rows of 64
+  // bytes in a row, which share banks two by two instead of all four.
+  const int kg = (g >> 1) + 4 * (g & 1);
+  const int k_at = kg * (D / 2) + t * (D / 8);
+  const int ks_at = kg * sb + 4 * ((t * (D / 4)) >> p.c.shift);
+  const int v_at = t * (D / 2) + g * (D / 16);
+  const int vs_at = t * sb + 4 * ((g * (D / 8)) >> p.c.shift);
 
+  // the warp's share of the CTA's
+  const unsigned long long all = s.plan.x1 - s.plan.x0;
+  const unsigned long long from = all * warp / WARPS;
+  U u(p, s.plan, from, all * (warp + 1) / WARPS - from);
+  Pages now{-1, 0};
+  int slot = 0;  // slot to use next
+  if (u.left) {
+    now = look_up(u, 0);
+    for (int i = 0; i < kDepth - 1; ++i) fetch(u, now, i);
+  }
+  while (u.left) {
     // the queries' operand: the thread's quarter of rows g (and g + 8)
-    uint32_t qf[NT][2 * W * 2];
-    float rs[NT][2], m[NT][2], l[NT][2];
-    int limit[NT][2];
+    uint32_t qf[NT][4 * W];
+    float rs[NT][2], off[NT][2], l[NT][2];
     const int ctx = u.c.kv - u.c.n;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-#pragma unroll
-      for (int i = 0; i < 4 * W; ++i) qf[n][i] = s.q[8 * n + g][t * 4 * W + i];
+      const int r = u.t * ROWS + 8 * n + g, tok = div_by(r, p.by_G);
+      const float f = load_query<T, 4 * W>(
+          (const T *)p.q + (u.c.start + tok) * p.q_stride +
+              (long long)(u.h * p.G + r - tok * p.G) * D + t * (D / 4),
+          8 * n + g < u.rows, p.scale_log2, qf[n]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int r = 8 * n + 2 * t + e;
-        rs[n][e] = s.q_scale[r];
-        m[n][e] = -kInf;
+        rs[n][e] = __shfl_sync(~0u, f, 4 * (2 * t + e));  // of row 2 t + e
+        off[n][e] = kNone;
         l[n][e] = 0.f;
-        limit[n][e] =
-            ctx + div_by(u.t * ROWS + min(r, u.rows - 1), p.by_G);
       }
     }
-    float o[NT][W * 2][4];
+    float o[NT][2 * W][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 2 * W; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[n][i][e] = 0.f;
+    // keys that every row of the unit sees
     const int open = p.mask ? ctx : ctx + div_by(u.t * ROWS, p.by_G) + 1;
 
-    auto use = [&](int key, const Stage<D> &x) {
+    struct Block {  // the thread's part of 16 keys
+      uint32_t k[2][W], v[4][W / 2], ks[2], vs[4];
+    };
+    auto use = [&](auto hides, int key, Block &x) {
+      constexpr bool HIDE = decltype(hides)::value;
+      if (HIDE) {  // what lies past the sequence's keys counts as zeros
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          if (key + 8 * hf + kg >= u.c.kv) x.ks[hf] = 0;
+          if (key + 8 * hf + t >= u.c.kv) x.vs[2 * hf] = 0;
+          if (key + 8 * hf + t + 4 >= u.c.kv) x.vs[2 * hf + 1] = 0;
+        }
+      }
       float sc[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -266,60 +296,68 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
       for (int i = 0; i < W; ++i)
 #pragma unroll
         for (int j = 0; j < 4; j += 2) {
-          const uint32_t f0 = kv4_fma(kv4_codes(x.k[0].w[i], j), a0, b0);
-          const uint32_t f1 = kv4_fma(kv4_codes(x.k[1].w[i], j), a1, b1);
-          const uint32_t f2 = kv4_fma(kv4_codes(x.k[0].w[i], j + 1), a0, b0);
-          const uint32_t f3 = kv4_fma(kv4_codes(x.k[1].w[i], j + 1), a1, b1);
+          const uint32_t f0 = kv4_fma(kv4_codes(x.k[0][i], j), a0, b0);
+          const uint32_t f1 = kv4_fma(kv4_codes(x.k[1][i], j), a1, b1);
+          const uint32_t f2 = kv4_fma(kv4_codes(x.k[0][i], j + 1), a0, b0);
+          const uint32_t f3 = kv4_fma(kv4_codes(x.k[1][i], j + 1), a1, b1);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
             mma16816(sc[n], f0, f1, f2, f3, qf[n][4 * i + j],
                      qf[n][4 * i + j + 1]);
         }
-      // scores in powers of two; those a row does not see become -inf
+      // exponents of the weights; of keys a row does not see -inf
+      float y[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[n][e] *= rs[n][e & 1];
-      if (key + kBlock > open) {
+        for (int e = 0; e < 4; ++e)
+          y[n][e] = fmaf(sc[n][e], rs[n][e & 1], off[n][e & 1]);
+      if (HIDE) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int k = key + g + (e >> 1) * 8;
-            bool see = k <= limit[n][e & 1];
+            const int r = min(8 * n + 2 * t + (e & 1), u.rows - 1);
+            const int token = div_by(u.t * ROWS + r, p.by_G);
+            const int i = key + kg + (e >> 1) * 8 - ctx;
+            bool see = i <= token;
             if (p.mask) {
-              see = k < end;
-              const int i = k - ctx;
+              see = i < u.c.n;
               if (see && i >= 0)
-                see = i < 32 * p.mask_words &&
-                      (__ldg(p.mask +
-                             (long long)(u.c.start + limit[n][e & 1] - ctx) *
-                                 p.mask_words +
-                             (i >> 5)) >>
-                           (i & 31) &
-                       1);
+                see = __ldg(p.mask +
+                            (long long)(u.c.start + token) * p.mask_words +
+                            (i >> 5)) >>
+                          (i & 31) &
+                      1;
             }
-            if (!see) sc[n][e] = -kInf;
+            if (!see) y[n][e] = -kInf;
           }
       }
-      bool move = false;
+      float most = fmaxf(y[0][0], y[0][1]);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          move = move || fmaxf(sc[n][e], sc[n][e + 2]) > m[n][e] + kSlack;
-      if (__any_sync(~0u, move)) {
+      for (int n = 0; n < NT; ++n) {
+        if (n) most = max3f(most, y[n][0], y[n][1]);
+        most = max3f(most, y[n][2], y[n][3]);
+      }
+      if (__any_sync(~0u, most > kBias + kSlack)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = fmaxf(sc[n][e], sc[n][e + 2]);
+            // (from kNone the exponents say nothing but which keys count)
+            const float s0 =
+                y[n][e] == -kInf ? -kInf : sc[n][e] * rs[n][e];
+            const float s1 =
+                y[n][e + 2] == -kInf ? -kInf : sc[n][e + 2] * rs[n][e];
+            float top = fmaxf(s0, s1);
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1)
               top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-            if (top > m[n][e] + kSlack) {
-              const float f = ex2(m[n][e] - top);  // 0 from -inf
-              m[n][e] = top;
+            if (top + off[n][e] > kBias + kSlack) {
+              const float to = kBias - top, f = ex2(to - off[n][e]);
+              off[n][e] = to;
+              y[n][e] = s0 + to;
+              y[n][e + 2] = s1 + to;
               l[n][e] *= f;
 #pragma unroll
               for (int i = 0; i < 2 * W; ++i) {
@@ -335,14 +373,13 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
         float z[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float ref = m[n][e & 1];
-          z[e] = ex2(sc[n][e] - (ref == -kInf ? 0.f : ref - kBias));
+          z[e] = ex2(y[n][e]);
           l[n][e & 1] += z[e];
         }
         w[n][0] = transpose8(pack2<__half>(z[0], z[1]));
         w[n][1] = transpose8(pack2<__half>(z[2], z[3]));
       }
-      // values of two keys at a time: their codes are brought together first
+      // values of two keys at a time: their codes are brought together
       uint32_t va[2], vb[2];
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
@@ -371,36 +408,58 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
       }
     };
 
-    // a warp's blocks are WARPS apart; two are on their way, and the pages of
-    // a third
-    constexpr int STEP = WARPS * kBlock;
-    Stage<D> x[2];
-    int page[2], tok[2];
-    int key = u.j0 * kTile + warp * kBlock;
-    auto look = [&](int at) {
-      page[0] = page_of(at, tok[0]);
-      page[1] = page_of(at + 8, tok[1]);
-    };
-    look(key);
-    fetch(key, x[0], page, tok);
-    look(key + STEP);
-    while (key < end) {
-      fetch(key + STEP, x[1], page, tok);
-      look(key + 2 * STEP);
-      use(key, x[0]);
-      key += STEP;
-      if (key >= end) break;
-      fetch(key + STEP, x[0], page, tok);
-      look(key + 2 * STEP);
-      use(key, x[1]);
-      key += STEP;
+    const int key0 = u.j0 * kKeys;
+    const int blocks = (min(u.j1 * kKeys, u.c.kv) - key0 + kBlock - 1) /
+                       kBlock;
+    Pages later{-1, 0};  // pages of the next batch
+    for (int i = 0; i < blocks; ++i) {
+      const int in = i & 15;
+      if (in == 0) later = look_up(u, i + 16);
+      cp_wait<kDepth - 2>();
+      __syncwarp();
+      const int key = key0 + i * kBlock;
+      const char *c = ring + slot * slot_bytes, *y = c + 2 * CODES;
+      if (++slot == kDepth) slot = 0;
+      Block x;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        lds_words(c + k_at + 4 * D * hf, x.k[hf]);
+        lds_words(c + CODES + v_at + 4 * D * hf, x.v[2 * hf]);
+        lds_words(c + CODES + v_at + 4 * D * hf + 2 * D, x.v[2 * hf + 1]);
+        x.ks[hf] = *reinterpret_cast<const uint32_t *>(
+            y + ks_at + 8 * sb * hf);
+        x.vs[2 * hf] = *reinterpret_cast<const uint32_t *>(
+            y + kBlock * sb + vs_at + 8 * sb * hf);
+        x.vs[2 * hf + 1] = *reinterpret_cast<const uint32_t *>(
+            y + kBlock * sb + vs_at + 8 * sb * hf + 4 * sb);
+      }
+      // the slot used before this one is free
+      const int ahead = in + kDepth - 1;
+      if (ahead == 16) now = later;
+      fetch(u, now, ahead & 15);
+      if (key + kBlock > open) use(std::true_type{}, key, x);
+      else use(std::false_type{}, key, x);
     }
 
-    // ---- the warps' sums of the unit are joined
-    if (__any_sync(~0u, bad) && lane == 0) {
-      s.bad = 1;
-      status_or(p.dev_status, SD_DEV_BAD_PAGE);
+    // ---- the end of the part.  Blocks past it were fetched as empty ones:
+    // the next unit's take their place
+    cp_wait<0>();
+    fill = slot;
+    const bool was_bad = bad;
+    bad = false;
+    const bool begun = u.j0 == 0, ended = u.j1 == u.nk;
+    const int start = u.c.start, first = u.t * ROWS, head = u.h;
+    const int rows = u.rows, ahead = u.nk - u.j1;
+    u.next();
+    if (u.left) {
+      now = look_up(u, 0);
+      for (int i = 0; i < kDepth - 1; ++i) fetch(u, now, i);
     }
+    if (was_bad && lane == 0) status_or(p.dev_status, SD_DEV_BAD_PAGE);
+    // The last part may go where the ring was: nothing is on its way there.
+    Part<ROWS, D> &part =
+        begun ? *reinterpret_cast<Part<ROWS, D> *>(ring) : s.part[warp];
+    __syncwarp();
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -409,63 +468,124 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1)
           sum += __shfl_xor_sync(~0u, sum, d);
-        const int r = 8 * n + 2 * t + e;
-        if (g == 0) s.ml[warp][r] = make_float2(m[n][e], sum);
+        if (was_bad) sum = __int_as_float(0x7fc00000);
         // element 2 i of the thread's eighth is in o[i][e], 2 i + 1 in
         // o[i][e + 2]
+        const int r = 8 * n + 2 * t + e;
+        if (!begun || !ended) {
+          if (g == 0)
+            part.ml[r] = make_float2(
+                off[n][e] == kNone ? -kInf : -off[n][e], sum);
 #pragma unroll
-        for (int i = 0; i < 2 * W; i += 2)
-          *reinterpret_cast<float4 *>(
-              &s.o[warp][r][g * (D / 8) + 2 * i]) =
-              make_float4(o[n][i][e], o[n][i][e + 2], o[n][i + 1][e],
-                          o[n][i + 1][e + 2]);
-      }
-    __syncthreads();
-    const bool whole = u.j0 == 0 && u.j1 == u.nk;
-    constexpr int E = D / 32;
-    for (int r = warp; r < u.rows; r += WARPS) {
-      float top = -kInf, sum = 0.f, out[E] = {};
+          for (int i = 0; i < 2 * W; i += 2)
+            *reinterpret_cast<float4 *>(&part.o[r][g * (D / 8) + 2 * i]) =
+                make_float4(o[n][i][e], o[n][i][e + 2], o[n][i + 1][e],
+                            o[n][i + 1][e + 2]);
+        } else if (r < rows) {
+          const int tok = div_by(first + r, p.by_G);
+          const long long row = (long long)(start + tok) * p.Hq +
+                                head * p.G + first + r - tok * p.G;
+          // no key seen: 0, whatever O has of another row's infinity
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          uint32_t w[2 * W];
 #pragma unroll
-      for (int k = 0; k < WARPS; ++k) top = fmaxf(top, s.ml[k][r].x);
-#pragma unroll
-      for (int k = 0; k < WARPS; ++k) {
-        const float2 a = s.ml[k][r];
-        // 0 for a warp that saw nothing, NaN for one with a NaN sum
-        const float f = a.x == -kInf ? (a.y == a.y ? 0.f : a.y)
-                                     : ex2(a.x - top);
-        sum += a.y * f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float y = s.o[k][r][lane * E + e];
-          if (f != 0.f) out[e] = fmaf(y, f, out[e]);
+          for (int i = 0; i < 2 * W; ++i)
+            w[i] = sum == 0.f ? 0 : pack2<T>(o[n][i][e] * inv,
+                                             o[n][i][e + 2] * inv);
+          T *dst = (T *)p.out + row * D + g * (D / 8);
+          if constexpr (D == 128) {
+            st_v8(dst, w);
+          } else {
+            *reinterpret_cast<uint4 *>(dst) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (p.lse && g == 0)
+            p.lse[row] =
+                sum == 0.f ? -kInf : (log2f(sum) - off[n][e]) * kLn2;
         }
       }
-      if (s.bad) sum = __int_as_float(0x7fc00000);
-      const int at = u.t * ROWS + r, token = div_by(at, p.by_G);
-      if (whole) {
-        const long long to = (long long)(u.c.start + token) * p.Hq +
-                             u.h * p.G + at - token * p.G;
-        const float inv = 1.f / sum;
-        uint32_t *dst =
-            reinterpret_cast<uint32_t *>((T *)p.out + to * D + lane * E);
+    if (lane == 0 && (!begun || !ended))
+      s.info[warp][begun] = PartInfo{1,     begun, ended, rows,
+                                     start, head,  first, ahead};
+  }
+  __syncthreads();
+
+  // ---- parts of one unit lie in warps one after the other; what they make
+  // together is the unit, or the CTA's part of it.  A warp per row.
+  for (int w0 = 0; w0 < WARPS; ++w0)
+    for (int second = 0; second < 2; ++second) {
+      // where a chain of parts starts
+      const PartInfo &f = s.info[w0][second];
+      if (!f.there || (!second && all * w0 / WARPS > 0)) continue;
+      int w1 = w0;  // its last warp (some may have no share at all)
+      bool ended = f.ended;
+      for (int w = w0 + 1; w < WARPS && !ended; ++w)
+        if (s.info[w][0].there) {
+          w1 = w;
+          ended = s.info[w][0].ended;
+        }
+      const int ahead = s.info[w1][w1 == w0 ? second : 0].ahead;
+      if (tid == 0 && f.begun && !ended) {
+        // the unit goes on in the CTAs up to the one whose share holds its
+        // last key
+        const unsigned long long end = s.plan.x1 + (unsigned)ahead;
+        CutUnit cut;
+        cut.parts = (int)((end * s.plan.n - 1) / s.plan.total) -
+                    (int)blockIdx.x + 1;
+        cut.rows = f.rows;
+        cut.start = f.start;
+        cut.head = f.head;
+        cut.first = f.first;
+        p.cut[blockIdx.x] = cut;
+      }
+      constexpr int E = D / 32;
+      for (int r = warp; r < f.rows; r += WARPS) {
+        float top = -kInf, sum = 0.f, out[E] = {};
+        auto part_of = [&](int w) -> const Part<ROWS, D> & {
+          return w == w0 && second
+                     ? *reinterpret_cast<const Part<ROWS, D> *>(ring_of(w))
+                     : s.part[w];
+        };
+        for (int w = w0; w <= w1; ++w)
+          if (w == w0 || s.info[w][0].there)
+            top = fmaxf(top, part_of(w).ml[r].x);
+        for (int w = w0; w <= w1; ++w) {
+          if (w > w0 && !s.info[w][0].there) continue;
+          const Part<ROWS, D> &x = part_of(w);
+          const float2 a = x.ml[r];
+          // 0 for a part that saw nothing, NaN for one with a NaN sum
+          const float k = a.x == -kInf ? (a.y == a.y ? 0.f : a.y)
+                                       : ex2(a.x - top);
+          sum += a.y * k;
 #pragma unroll
-        for (int e = 0; e < E; e += 2)
-          dst[e / 2] = sum == 0.f ? 0 : pack2<T>(out[e] * inv,
-                                                 out[e + 1] * inv);
-        if (p.lse && lane == 0)
-          p.lse[to] = sum == 0.f ? -kInf : (top - kBias + log2f(sum)) * kLn2;
-      } else {
-        const long long part =
-            ((long long)blockIdx.x * 2 + (u.j0 == 0 ? 1 : 0)) * ROWS + r;
-        if (lane == 0) p.part_ml[part] = make_float2(top - kBias, sum);
+          for (int e = 0; e < E; ++e) {
+            const float y = x.o[r][lane * E + e];
+            if (k != 0.f) out[e] = fmaf(y, k, out[e]);
+          }
+        }
+        if (f.begun && ended) {
+          const int tok = div_by(f.first + r, p.by_G);
+          const long long row = (long long)(f.start + tok) * p.Hq +
+                                f.head * p.G + f.first + r - tok * p.G;
+          const float inv = 1.f / sum;
+          uint32_t *dst =
+              reinterpret_cast<uint32_t *>((T *)p.out + row * D + lane * E);
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-          p.part_o[part * D + lane * E + e] = out[e];
+          for (int e = 0; e < E; e += 2)
+            dst[e / 2] = sum == 0.f ? 0 : pack2<T>(out[e] * inv,
+                                                   out[e + 1] * inv);
+          if (p.lse && lane == 0)
+            p.lse[row] = sum == 0.f ? -kInf : (top + log2f(sum)) * kLn2;
+        } else {
+          const long long at =
+              ((long long)blockIdx.x * 2 + (f.begun ? 1 : 0)) * ROWS + r;
+          if (lane == 0) p.part_ml[at] = make_float2(top, sum);
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            p.part_o[at * D + lane * E + e] = out[e];
+        }
       }
     }
-    __syncthreads();
-    if (tid == 0) s.bad = 0;
-  }
 
   if (s.plan.any_unusable) {
     // NaN for the sequences that cannot be read
@@ -493,8 +613,10 @@ int rows_tile(int max_q, int G) {
 
 template <class T, int D, int NT>
 sd_status launch_rows(Attn4Params &p, int sms, void *ws, cudaStream_t s) {
-  constexpr int WARPS = 8;
-  constexpr size_t smem = sizeof(Shared4<8 * NT, D, WARPS>);
+  constexpr int WARPS = NT == 1 ? 8 : 12;
+  constexpr size_t shared =
+      (sizeof(Shared4<8 * NT, D, WARPS>) + 127) / 128 * 128;
+  constexpr size_t slots = WARPS * ring_depth<NT>() * kBlock;  // keys in the rings
   set_workspace(p, ws_layout(kMaxGrid4, 8 * NT, D), ws);
   const void *kernel = (const void *)kv4_rows_kernel<T, D, NT, WARPS>;
   int dev = 0;
@@ -502,14 +624,17 @@ sd_status launch_rows(Attn4Params &p, int sms, void *ws, cudaStream_t s) {
   static std::atomic<unsigned long long> ready{0};
   if (dev >= 64 || !(ready.load() >> dev & 1)) {
     SDV_CUDA(cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        (int)(shared + slots * (D + 2 * (D / 32) * 4))));
     if (dev < 64) ready.fetch_or(1ull << dev);
   }
   const int want = NT == 1 ? 2 * sms : sms;
   const unsigned grid = want < kMaxGrid4 ? want : kMaxGrid4;
   void *args[] = {&p};
-  const sd_status st = launch_pdl(kernel, grid, WARPS * 32, smem, s, args);
-  return st != SD_OK ? st : launch_join<T, D, 8 * NT>(p, grid, s);
+  const sd_status st =
+      launch_pdl(kernel, grid, WARPS * 32,
+                 shared + slots * (D + 2 * p.c.scale_bytes), s, args);
+  return st != SD_OK ? st : launch_join<T, D, 8 * NT, kKeys>(p, grid, s);
 }
 
 template <class T>

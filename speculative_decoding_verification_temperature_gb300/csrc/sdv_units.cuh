@@ -51,7 +51,7 @@ __device__ __forceinline__ int row_tiles(const UnitParams &p,
 }
 
 // Key tiles that row tile t sees.
-template <int ROWS>
+template <int ROWS, int KEYS = kTile>
 __device__ __forceinline__ int key_tiles(const UnitParams &p, const Chunk &c,
                                          int t) {
   int last = c.kv - 1;
@@ -59,15 +59,15 @@ __device__ __forceinline__ int key_tiles(const UnitParams &p, const Chunk &c,
     const int i = div_by((t + 1) * ROWS - 1, p.by_G);
     if (i < c.n - 1) last = c.kv - c.n + i;
   }
-  return last / kTile + 1;
+  return last / KEYS + 1;
 }
 
-template <int ROWS>
+template <int ROWS, int KEYS = kTile>
 __device__ unsigned long long head_tiles(const UnitParams &p,
                                          const Chunk &c) {
   const int T = row_tiles<ROWS>(p, c);
   unsigned long long s = 0;
-  for (int t = 0; t < T; ++t) s += key_tiles<ROWS>(p, c, t);
+  for (int t = 0; t < T; ++t) s += key_tiles<ROWS, KEYS>(p, c, t);
   return s;
 }
 
@@ -87,7 +87,7 @@ struct Plan {
   int any_unusable;
 };
 
-template <int ROWS>
+template <int ROWS, int KEYS = kTile>
 __device__ void make_plan(const UnitParams &p, Plan &s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // key tiles and units of this thread's sequences; of its first one
@@ -101,7 +101,7 @@ __device__ void make_plan(const UnitParams &p, Plan &s) {
         unusable = true;
         if (blockIdx.x == 0) status_or(p.dev_status, SD_DEV_BAD_LENGTH);
       }
-      const unsigned long long w = head_tiles<ROWS>(p, c) * p.Hkv;
+      const unsigned long long w = head_tiles<ROWS, KEYS>(p, c) * p.Hkv;
       const unsigned long long k =
           (unsigned long long)row_tiles<ROWS>(p, c) * p.Hkv;
       if (b == tid) first_tiles = w, first_units = k;
@@ -145,7 +145,7 @@ __device__ void make_plan(const UnitParams &p, Plan &s) {
       w = 0;
       if (tid < 256 && base + tid < p.B) {
         const Chunk c = attn_chunk(p, base + tid);
-        w = (head_tiles<ROWS>(p, c) + extra * row_tiles<ROWS>(p, c)) * p.Hkv;
+        w = (head_tiles<ROWS, KEYS>(p, c) + extra * row_tiles<ROWS>(p, c)) * p.Hkv;
       }
     }
     unsigned long long inc = w;
@@ -165,13 +165,13 @@ __device__ void make_plan(const UnitParams &p, Plan &s) {
     if (tid < 256 && s.x0 >= lo && s.x0 < lo + w) {
       const Chunk c = attn_chunk(p, base + tid);
       const unsigned long long per =
-          head_tiles<ROWS>(p, c) + extra * row_tiles<ROWS>(p, c);
+          head_tiles<ROWS, KEYS>(p, c) + extra * row_tiles<ROWS>(p, c);
       unsigned long long r = s.x0 - lo;
       s.h = (int)(r / per);
       r %= per;
       int t = 0;
       for (;; ++t) {
-        const int k = key_tiles<ROWS>(p, c, t) + (int)extra;
+        const int k = key_tiles<ROWS, KEYS>(p, c, t) + (int)extra;
         if (r < (unsigned long long)k) break;
         r -= k;
       }
@@ -187,7 +187,7 @@ __device__ void make_plan(const UnitParams &p, Plan &s) {
 
 // Walks the units of a CTA's share that it has key tiles of; every warp
 // walks the same ones.
-template <int ROWS> struct Units {
+template <int ROWS, int KEYS = kTile> struct Units {
   const UnitParams &p;
   unsigned long long left;  // places of the share from `at` on
   Chunk c;
@@ -206,6 +206,27 @@ template <int ROWS> struct Units {
     set();
     if (j0 == j1) next();
   }
+  // The part of the share from place `from` on, `n` places long.
+  __device__ Units(const UnitParams &p_, const Plan &s,
+                   unsigned long long from, unsigned long long n)
+      : p(p_), left(s.x1 - s.x0), b(s.b), h(s.h), t(s.t), T(0), at(s.at),
+        count(0) {
+    if (!n) left = 0;
+    if (!left) return;
+    c = attn_chunk(p, b);
+    T = row_tiles<ROWS>(p, c);
+    for (;;) {
+      set();
+      const int here = nk + extra - at;
+      if (from < (unsigned long long)here) break;
+      from -= here;
+      step();
+    }
+    at += (int)from;
+    left = n;
+    set();
+    if (j0 == j1) next();
+  }
   __device__ void to(const Units &o) {  // o walks the same share
     left = o.left, c = o.c, b = o.b, h = o.h, t = o.t, T = o.T, at = o.at;
     j0 = o.j0, j1 = o.j1, nk = o.nk, rows = o.rows, count = o.count;
@@ -216,26 +237,29 @@ template <int ROWS> struct Units {
   }
   __device__ void set() {
     ++count;
-    nk = key_tiles<ROWS>(p, c, t);
+    nk = key_tiles<ROWS, KEYS>(p, c, t);
     j0 = max(0, at - extra);
     j1 = max(0, at + places() - extra);
     rows = min(c.n * p.G - t * ROWS, ROWS);
+  }
+  __device__ void step() {  // to the start of the unit after this one
+    at = 0;
+    if (++t == T) {
+      t = 0;
+      if (++h == p.Hkv) {
+        h = 0;
+        do {  // there is one: a later sequence has units
+          c = attn_chunk(p, ++b);
+          T = row_tiles<ROWS>(p, c);
+        } while (T == 0);
+      }
+    }
   }
   __device__ void next() {
     do {  // past units of which the share has no tile
       left -= places();
       if (!left) return;
-      at = 0;
-      if (++t == T) {
-        t = 0;
-        if (++h == p.Hkv) {
-          h = 0;
-          do {  // left > 0: a later sequence has units
-            c = attn_chunk(p, ++b);
-            T = row_tiles<ROWS>(p, c);
-          } while (T == 0);
-        }
-      }
+      step();
       set();
     } while (j0 == j1);
   }
@@ -373,10 +397,10 @@ join_kernel(const __grid_constant__ UnitParams p) {
 }
 
 // The join after an attention kernel of `grid` CTAs.
-template <class T, int D, int ROWS>
+template <class T, int D, int ROWS, int KEYS = kTile>
 sd_status launch_join(UnitParams &p, unsigned grid, cudaStream_t s) {
   // a sequence whose table holds one key tile has no unit that can be cut
-  if ((long long)p.max_pages * p.page_size <= kTile) return SD_OK;
+  if ((long long)p.max_pages * p.page_size <= KEYS) return SD_OK;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, ROWS / kWarps, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
