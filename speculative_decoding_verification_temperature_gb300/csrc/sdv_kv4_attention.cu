@@ -13,6 +13,7 @@ struct Attn4Params : UnitParams {
   long long q_stride;
   Kv4Cache c;
   float scale_log2;  // scale x log2(e)
+  bool bf16;         // type of q and out; fp16 otherwise
 };
 
 // ------------------------------------------------------- few rows a head
@@ -40,7 +41,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0,
                                          uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
       "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -85,10 +86,13 @@ template <int ROWS, int D, int WARPS> struct Shared4 {
   Part<ROWS, D> part[WARPS];  // of the warp's first unit
 };
 
-__device__ __forceinline__ void cp16(uint32_t to, const void *from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to),
-               "l"(from)
-               : "memory");
+__device__ __forceinline__ void cp16(uint32_t to, const void *from,
+                                     bool there) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+      "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(to),
+      "l"(from), "r"((int)there)
+      : "memory");
 }
 __device__ __forceinline__ void cp_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -101,9 +105,10 @@ template <int N> __device__ __forceinline__ void cp_wait() {
 // factor of its scores.  bf16 rows are multiplied by the power of two that
 // takes the row's largest element to [2^14, 2^15): exact but for elements
 // 2^-28 of that and below.  A row with NaN or infinity gets a NaN factor.
-template <class T, int N>
-__device__ __forceinline__ float load_query(const T *src, bool valid,
-                                            float scale, uint32_t (&w)[N]) {
+template <int N>
+__device__ __forceinline__ float load_query(const void *src, bool valid,
+                                            bool bf16, float scale,
+                                            uint32_t (&w)[N]) {
   uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < N; i += 4) {
@@ -117,7 +122,7 @@ __device__ __forceinline__ float load_query(const T *src, bool valid,
   top = max(top, __shfl_xor_sync(~0u, top, 1));
   top = max(top, __shfl_xor_sync(~0u, top, 2));
   float f = scale;
-  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+  if (bf16) {
     // exponents above -86: the power is a normal number
     const int exp = max((int)(top >> 7), 41) - 127;
     const float up = __uint_as_float((uint32_t)(14 - exp + 127) << 23);
@@ -137,7 +142,7 @@ __device__ __forceinline__ float load_query(const T *src, bool valid,
 template <int NT> constexpr int ring_depth() { return NT == 1 ? 3 : 4; }
 constexpr int kKeys = 2 * kBlock;  // keys of a place in the shares
 
-template <class T, int D, int NT, int WARPS>
+template <int D, int SB, int NT, int WARPS>  // SB: bytes of a key's pairs
 __global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 2 : 1)
 kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
   constexpr int ROWS = 8 * NT, W = D / 32;  // W: words of a key a thread
@@ -150,8 +155,9 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
   extern __shared__ __align__(128) char dyn[];
   S &s = *reinterpret_cast<S *>(dyn);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = lane >> 2, t = lane & 3, sb = p.c.scale_bytes;
-  const int slot_bytes = 2 * CODES + 2 * kBlock * sb;
+  const int g = lane >> 2, t = lane & 3;
+  constexpr int sb = SB, slot_bytes = 2 * CODES + 2 * kBlock * SB;
+  constexpr int GROUP = 4 * D / SB;
   auto ring_of = [&](int w) {
     return dyn + (sizeof(S) + 127) / 128 * 128 + w * kDepth * slot_bytes;
   };
@@ -163,19 +169,27 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
   __syncthreads();
 
   // ---- the warp's blocks of a unit: where the next ones lie.  Lane 2 i + hf
-  // holds page and token of half hf of the i-th block of a batch of sixteen.
-  struct Pages {
-    int page, tok;
+  // holds the places in bytes of the codes and pairs of half hf of the i-th
+  // block of a batch of sixteen; negative: nothing to be had.
+  struct Places {
+    long long code, pair;
   };
+  bool bad = false;
   auto look_up = [&](const U &v, int first) {  // the batch's first block
     const int key =
         v.j0 * kKeys + (first + (lane >> 1)) * kBlock + 8 * (lane & 1);
-    Pages x{-1, 0};
+    Places x{-1, -1};
     if (key < min(v.j1 * kKeys, v.c.kv)) {
       const int n = div_by(key, p.by_page);
-      x.page = __ldg(p.block_table + (long long)v.b * p.max_pages + n);
-      x.tok = key - n * p.page_size;
-      if (x.page < 0 || x.page >= p.c.num_pages) x.page = -2;
+      const int page =
+          __ldg(p.block_table + (long long)v.b * p.max_pages + n);
+      if (page >= 0 && page < p.c.num_pages) {
+        const int row = (v.h - n) * p.page_size + key;
+        x.code = page * p.c.page_stride + (long long)row * (D / 2);
+        x.pair = page * p.c.scale_stride + (long long)row * sb;
+      } else {
+        bad = true;
+      }
     }
     return x;
   };
@@ -185,63 +199,46 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
   const int which = lane / sb, pair_hf = lane / (sb / 2) & 1;
   const char *pairs = (which ? p.c.v_scale : p.c.k_scale) +
                       16 * (lane & (sb / 2 - 1));
-  int fill = 0;  // slot to fill next
-  bool bad = false;
-  auto fetch = [&](const U &v, const Pages &x, int i) {
-    const int page[2] = {__shfl_sync(~0u, x.page, 2 * i),
-                         __shfl_sync(~0u, x.page, 2 * i + 1)};
-    const int tok[2] = {__shfl_sync(~0u, x.tok, 2 * i),
-                        __shfl_sync(~0u, x.tok, 2 * i + 1)};
-    const uint32_t at = to + fill * slot_bytes;
-    bad = bad || page[0] == -2 || page[1] == -2;
-    auto code_at = [&](int pg, int tk) {
-      const int row = v.h * p.page_size + tk;
-      return pg * p.c.page_stride + (long long)row * (D / 2);
-    };
-    if constexpr (D == 128) {
+  const char *k_codes = p.c.k + 16 * (lane & (D / 4 - 1));
+  const char *v_codes = p.c.v + 16 * (lane & (D / 4 - 1));
+  int fill = 0;  // where to fill next
+  auto fetch = [&](const Places &x, int i) {
+    const uint32_t at = to + fill;
+    constexpr int HALVES = D / 64;  // that a lane has a part of
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-        if (page[hf] >= 0) {
-          const long long c = code_at(page[hf], tok[hf]) + 16 * lane;
-          cp16(at + 512 * hf, p.c.k + c);
-          cp16(at + CODES + 512 * hf, p.c.v + c);
-        }
-    } else {
-      const int mine = lane < 16 ? page[0] : page[1];
-      if (mine >= 0) {
-        const long long c =
-            code_at(mine, lane < 16 ? tok[0] : tok[1]) + 16 * (lane & 15);
-        cp16(at, p.c.k + c);
-        cp16(at + CODES, p.c.v + c);
-      }
+    for (int hf = 0; hf < HALVES; ++hf) {
+      const int from = 2 * i + (HALVES == 2 ? hf : lane >> 4);
+      const long long c = __shfl_sync(~0u, x.code, from);
+      cp16(at + 512 * hf, k_codes + c, c >= 0);
+      cp16(at + CODES + 512 * hf, v_codes + c, c >= 0);
     }
-    const int pair_page = pair_hf ? page[1] : page[0];
-    if (which < 2 && pair_page >= 0) {
-      const int row = v.h * p.page_size + (pair_hf ? tok[1] : tok[0]);
-      cp16(at + 2 * CODES, pairs + pair_page * p.c.scale_stride +
-                               (long long)row * sb);
-    }
+    const long long c = __shfl_sync(~0u, x.pair, 2 * i + pair_hf);
+    cp16(at + 2 * CODES, pairs + c, which < 2 && c >= 0);
     cp_commit();
-    if (++fill == kDepth) fill = 0;
+    fill = fill == (kDepth - 1) * slot_bytes ? 0 : fill + slot_bytes;
   };
   // Row g of a product's keys is key (g >> 1) + 4 (g & 1) of eight, so that
   // the two whose values a thread pairs are t and t + 4: four rows of 64
   // bytes in a row, which share banks two by two instead of all four.
   const int kg = (g >> 1) + 4 * (g & 1);
   const int k_at = kg * (D / 2) + t * (D / 8);
-  const int ks_at = kg * sb + 4 * ((t * (D / 4)) >> p.c.shift);
+  const int ks_at = kg * sb + 4 * (t * (D / 4) / GROUP);
   const int v_at = t * (D / 2) + g * (D / 16);
-  const int vs_at = t * sb + 4 * ((g * (D / 8)) >> p.c.shift);
+  const int vs_at = t * sb + 4 * (g * (D / 8) / GROUP);
+
+  auto pack = [&](float a, float b) {
+    return p.bf16 ? pack2<__nv_bfloat16>(a, b) : pack2<__half>(a, b);
+  };
 
   // the warp's share of the CTA's
   const unsigned long long all = s.plan.x1 - s.plan.x0;
   const unsigned long long from = all * warp / WARPS;
   U u(p, s.plan, from, all * (warp + 1) / WARPS - from);
-  Pages now{-1, 0};
-  int slot = 0;  // slot to use next
+  Places now{-1, -1};
+  int slot = 0;  // where to use next
   if (u.left) {
     now = look_up(u, 0);
-    for (int i = 0; i < kDepth - 1; ++i) fetch(u, now, i);
+    for (int i = 0; i < kDepth - 1; ++i) fetch(now, i);
   }
   while (u.left) {
     // the queries' operand: the thread's quarter of rows g (and g + 8)
@@ -251,10 +248,10 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int r = u.t * ROWS + 8 * n + g, tok = div_by(r, p.by_G);
-      const float f = load_query<T, 4 * W>(
-          (const T *)p.q + (u.c.start + tok) * p.q_stride +
+      const float f = load_query<4 * W>(
+          (const uint16_t *)p.q + (u.c.start + tok) * p.q_stride +
               (long long)(u.h * p.G + r - tok * p.G) * D + t * (D / 4),
-          8 * n + g < u.rows, p.scale_log2, qf[n]);
+          8 * n + g < u.rows, p.bf16, p.scale_log2, qf[n]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         rs[n][e] = __shfl_sync(~0u, f, 4 * (2 * t + e));  // of row 2 t + e
@@ -275,21 +272,27 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
     struct Block {  // the thread's part of 16 keys
       uint32_t k[2][W], v[4][W / 2], ks[2], vs[4];
     };
-    auto use = [&](auto hides, int key, Block &x) {
+    const char *k_from = ring + k_at, *ks_from = ring + 2 * CODES + ks_at;
+    const char *v_from = ring + CODES + v_at;
+    const char *vs_from = ring + 2 * CODES + kBlock * SB + vs_at;
+    auto use = [&](auto hides, int key) {
       constexpr bool HIDE = decltype(hides)::value;
-      if (HIDE) {  // what lies past the sequence's keys counts as zeros
+      Block x;
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          if (key + 8 * hf + kg >= u.c.kv) x.ks[hf] = 0;
-          if (key + 8 * hf + t >= u.c.kv) x.vs[2 * hf] = 0;
-          if (key + 8 * hf + t + 4 >= u.c.kv) x.vs[2 * hf + 1] = 0;
-        }
+      for (int hf = 0; hf < 2; ++hf) {
+        lds_words(k_from + slot + 4 * D * hf, x.k[hf]);
+        x.ks[hf] = *reinterpret_cast<const uint32_t *>(
+            ks_from + slot + 8 * SB * hf);
       }
-      float sc[NT][4];
+      // what lies past the sequence's keys counts as zeros
+      if (HIDE && key + kg >= u.c.kv) x.ks[0] = 0;
+      if (HIDE && key + 8 + kg >= u.c.kv) x.ks[1] = 0;
+      // two sums a score: half the chain from product to product
+      float sc[NT][4], sd[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
+        for (int e = 0; e < 4; ++e) sc[n][e] = sd[n][e] = 0.f;
       const uint32_t a0 = both_lo(x.ks[0]), b0 = both_hi(x.ks[0]);
       const uint32_t a1 = both_lo(x.ks[1]), b1 = both_hi(x.ks[1]);
 #pragma unroll
@@ -302,9 +305,24 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
           const uint32_t f3 = kv4_fma(kv4_codes(x.k[1][i], j + 1), a1, b1);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
-            mma16816(sc[n], f0, f1, f2, f3, qf[n][4 * i + j],
+            mma16816(j ? sd[n] : sc[n], f0, f1, f2, f3, qf[n][4 * i + j],
                      qf[n][4 * i + j + 1]);
         }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[n][e] += sd[n][e];
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        lds_words(v_from + slot + 4 * D * hf, x.v[2 * hf]);
+        lds_words(v_from + slot + 4 * D * hf + 2 * D, x.v[2 * hf + 1]);
+        x.vs[2 * hf] = *reinterpret_cast<const uint32_t *>(
+            vs_from + slot + 8 * SB * hf);
+        x.vs[2 * hf + 1] = *reinterpret_cast<const uint32_t *>(
+            vs_from + slot + 8 * SB * hf + 4 * SB);
+        if (HIDE && key + 8 * hf + t >= u.c.kv) x.vs[2 * hf] = 0;
+        if (HIDE && key + 8 * hf + t + 4 >= u.c.kv) x.vs[2 * hf + 1] = 0;
+      }
       // exponents of the weights; of keys a row does not see -inf
       float y[NT][4];
 #pragma unroll
@@ -411,41 +429,24 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
     const int key0 = u.j0 * kKeys;
     const int blocks = (min(u.j1 * kKeys, u.c.kv) - key0 + kBlock - 1) /
                        kBlock;
-    Pages later{-1, 0};  // pages of the next batch
     for (int i = 0; i < blocks; ++i) {
-      const int in = i & 15;
-      if (in == 0) later = look_up(u, i + 16);
       cp_wait<kDepth - 2>();
       __syncwarp();
       const int key = key0 + i * kBlock;
-      const char *c = ring + slot * slot_bytes, *y = c + 2 * CODES;
-      if (++slot == kDepth) slot = 0;
-      Block x;
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        lds_words(c + k_at + 4 * D * hf, x.k[hf]);
-        lds_words(c + CODES + v_at + 4 * D * hf, x.v[2 * hf]);
-        lds_words(c + CODES + v_at + 4 * D * hf + 2 * D, x.v[2 * hf + 1]);
-        x.ks[hf] = *reinterpret_cast<const uint32_t *>(
-            y + ks_at + 8 * sb * hf);
-        x.vs[2 * hf] = *reinterpret_cast<const uint32_t *>(
-            y + kBlock * sb + vs_at + 8 * sb * hf);
-        x.vs[2 * hf + 1] = *reinterpret_cast<const uint32_t *>(
-            y + kBlock * sb + vs_at + 8 * sb * hf + 4 * sb);
-      }
       // the slot used before this one is free
-      const int ahead = in + kDepth - 1;
-      if (ahead == 16) now = later;
-      fetch(u, now, ahead & 15);
-      if (key + kBlock > open) use(std::true_type{}, key, x);
-      else use(std::false_type{}, key, x);
+      const int next = i + kDepth - 1;
+      if ((next & 15) == 0) now = look_up(u, next);
+      fetch(now, next & 15);
+      if (key + kBlock > open) use(std::true_type{}, key);
+      else use(std::false_type{}, key);
+      slot = slot == (kDepth - 1) * slot_bytes ? 0 : slot + slot_bytes;
     }
 
     // ---- the end of the part.  Blocks past it were fetched as empty ones:
     // the next unit's take their place
     cp_wait<0>();
     fill = slot;
-    const bool was_bad = bad;
+    const bool was_bad = __any_sync(~0u, bad);
     bad = false;
     const bool begun = u.j0 == 0, ended = u.j1 == u.nk;
     const int start = u.c.start, first = u.t * ROWS, head = u.h;
@@ -453,7 +454,7 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
     u.next();
     if (u.left) {
       now = look_up(u, 0);
-      for (int i = 0; i < kDepth - 1; ++i) fetch(u, now, i);
+      for (int i = 0; i < kDepth - 1; ++i) fetch(now, i);
     }
     if (was_bad && lane == 0) status_or(p.dev_status, SD_DEV_BAD_PAGE);
     // The last part may go where the ring was: nothing is on its way there.
@@ -490,9 +491,9 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
           uint32_t w[2 * W];
 #pragma unroll
           for (int i = 0; i < 2 * W; ++i)
-            w[i] = sum == 0.f ? 0 : pack2<T>(o[n][i][e] * inv,
-                                             o[n][i][e + 2] * inv);
-          T *dst = (T *)p.out + row * D + g * (D / 8);
+            w[i] = sum == 0.f ? 0
+                              : pack(o[n][i][e] * inv, o[n][i][e + 2] * inv);
+          uint16_t *dst = (uint16_t *)p.out + row * D + g * (D / 8);
           if constexpr (D == 128) {
             st_v8(dst, w);
           } else {
@@ -569,11 +570,12 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
                                 f.head * p.G + f.first + r - tok * p.G;
           const float inv = 1.f / sum;
           uint32_t *dst =
-              reinterpret_cast<uint32_t *>((T *)p.out + row * D + lane * E);
+              reinterpret_cast<uint32_t *>((uint16_t *)p.out + row * D +
+                                           lane * E);
 #pragma unroll
           for (int e = 0; e < E; e += 2)
-            dst[e / 2] = sum == 0.f ? 0 : pack2<T>(out[e] * inv,
-                                                   out[e + 1] * inv);
+            dst[e / 2] =
+                sum == 0.f ? 0 : pack(out[e] * inv, out[e + 1] * inv);
           if (p.lse && lane == 0)
             p.lse[row] = sum == 0.f ? -kInf : (top + log2f(sum)) * kLn2;
         } else {
@@ -596,7 +598,7 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
       const long long lo = (long long)c.start * p.Hq,
                       n = (long long)c.n * p.Hq;
       for (long long i = tid; i < n * D; i += WARPS * 32)
-        ((T *)p.out)[lo * D + i] = narrow<T>(__int_as_float(0x7fc00000));
+        ((uint16_t *)p.out)[lo * D + i] = 0x7fff;  // NaN of either type
       if (p.lse)
         for (long long i = tid; i < n; i += WARPS * 32)
           p.lse[lo + i] = __int_as_float(0x7fc00000);
@@ -611,40 +613,41 @@ int rows_tile(int max_q, int G) {
   return (long long)max_q * G <= 8 ? 1 : 2;
 }
 
-template <class T, int D, int NT>
+template <int D, int SB, int NT>
 sd_status launch_rows(Attn4Params &p, int sms, void *ws, cudaStream_t s) {
   constexpr int WARPS = NT == 1 ? 8 : 12;
-  constexpr size_t shared =
-      (sizeof(Shared4<8 * NT, D, WARPS>) + 127) / 128 * 128;
-  constexpr size_t slots = WARPS * ring_depth<NT>() * kBlock;  // keys in the rings
+  constexpr size_t smem =
+      (sizeof(Shared4<8 * NT, D, WARPS>) + 127) / 128 * 128 +
+      WARPS * ring_depth<NT>() * kBlock * (D + 2 * SB);
   set_workspace(p, ws_layout(kMaxGrid4, 8 * NT, D), ws);
-  const void *kernel = (const void *)kv4_rows_kernel<T, D, NT, WARPS>;
+  const void *kernel = (const void *)kv4_rows_kernel<D, SB, NT, WARPS>;
   int dev = 0;
   SDV_CUDA(cudaGetDevice(&dev));
   static std::atomic<unsigned long long> ready{0};
   if (dev >= 64 || !(ready.load() >> dev & 1)) {
     SDV_CUDA(cudaFuncSetAttribute(
-        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        (int)(shared + slots * (D + 2 * (D / 32) * 4))));
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
     if (dev < 64) ready.fetch_or(1ull << dev);
   }
   const int want = NT == 1 ? 2 * sms : sms;
   const unsigned grid = want < kMaxGrid4 ? want : kMaxGrid4;
   void *args[] = {&p};
-  const sd_status st =
-      launch_pdl(kernel, grid, WARPS * 32,
-                 shared + slots * (D + 2 * p.c.scale_bytes), s, args);
-  return st != SD_OK ? st : launch_join<T, D, 8 * NT, kKeys>(p, grid, s);
+  const sd_status st = launch_pdl(kernel, grid, WARPS * 32, smem, s, args);
+  if (st != SD_OK) return st;
+  return p.bf16 ? launch_join<__nv_bfloat16, D, 8 * NT, kKeys>(p, grid, s)
+                : launch_join<__half, D, 8 * NT, kKeys>(p, grid, s);
 }
 
-template <class T>
-sd_status dispatch4(Attn4Params &p, int D, int nt, int sms, void *ws,
+template <int NT>
+sd_status dispatch4(Attn4Params &p, int D, int sms, void *ws,
                     cudaStream_t s) {
+  const int sb = p.c.scale_bytes;
   if (D == 64)
-    return nt == 1 ? launch_rows<T, 64, 1>(p, sms, ws, s)
-                   : launch_rows<T, 64, 2>(p, sms, ws, s);
-  return nt == 1 ? launch_rows<T, 128, 1>(p, sms, ws, s)
-                 : launch_rows<T, 128, 2>(p, sms, ws, s);
+    return sb == 4 ? launch_rows<64, 4, NT>(p, sms, ws, s)
+                   : launch_rows<64, 8, NT>(p, sms, ws, s);
+  return sb == 4   ? launch_rows<128, 4, NT>(p, sms, ws, s)
+         : sb == 8 ? launch_rows<128, 8, NT>(p, sms, ws, s)
+                   : launch_rows<128, 16, NT>(p, sms, ws, s);
 }
 
 }  // namespace
@@ -723,8 +726,7 @@ extern "C" sd_status sd_kv4_attention(
   p.dev_status = dev_status;
   p.c = kv4_cache(cache);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int nt = rows_tile(max_q, p.G);
-  return cache->dt == SD_BF16
-             ? dispatch4<__nv_bfloat16>(p, D, nt, sms, workspace, s)
-             : dispatch4<__half>(p, D, nt, sms, workspace, s);
+  p.bf16 = cache->dt == SD_BF16;
+  return rows_tile(max_q, p.G) == 1 ? dispatch4<1>(p, D, sms, workspace, s)
+                                    : dispatch4<2>(p, D, sms, workspace, s);
 }
