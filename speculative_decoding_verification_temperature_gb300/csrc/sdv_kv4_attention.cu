@@ -19,7 +19,7 @@ struct Attn4Params : UnitParams {
 // ------------------------------------------------------- few rows a head
 //
 // Where a cache head has few rows (one token of a group of query heads), a
-// warp takes 16 keys at a time, makes their codes operands in registers, and
+// warp takes 32 keys at a time, makes their codes operands in registers, and
 // has the keys as the rows of its products:
 //   S^T [16 keys x 8 rows] = K [16 x D] Q^T,   O^T [D x 8] += V^T [D x 16] W
 // so that 8 rows are not padded to more.  Four neighbouring threads hold a
@@ -35,7 +35,7 @@ struct Attn4Params : UnitParams {
 // reference's still has all its bits.
 constexpr float kBias = 10.f, kSlack = 5.f;
 constexpr float kNone = 3e38f;  // in place of kBias - m: no reference yet
-constexpr int kBlock = 16;     // keys of a warp's step
+constexpr int kBlock = 32;  // keys of a warp's step, two products' rows
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0,
                                          uint32_t a1, uint32_t a2,
@@ -72,7 +72,7 @@ __device__ __forceinline__ void lds_words(const char *p, uint32_t (&w)[N]) {
 // of its rows.
 template <int ROWS, int D> struct Part {
   float2 ml[ROWS];
-  alignas(16) float o[ROWS][D + 4];
+  alignas(16) float o[ROWS][D];
 };
 struct PartInfo {
   int there;          // there is one
@@ -138,17 +138,14 @@ __device__ __forceinline__ float load_query(const void *src, bool valid,
   return f;
 }
 
-// Blocks of a warp's ring, one of them in use.
-template <int NT> constexpr int ring_depth() { return NT == 1 ? 3 : 4; }
-constexpr int kKeys = 2 * kBlock;  // keys of a place in the shares
+constexpr int kKeys = kBlock;  // keys of a place in the shares
 
 template <int D, int SB, int NT, int WARPS>  // SB: bytes of a key's pairs
-__global__ void __launch_bounds__(WARPS * 32, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1)
 kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
   constexpr int ROWS = 8 * NT, W = D / 32;  // W: words of a key a thread
   constexpr int CODES = kBlock * D / 2;     // bytes of a block's key codes
-  constexpr int kDepth = ring_depth<NT>();
-  static_assert(sizeof(Part<ROWS, D>) <= kDepth * (2 * CODES + 8 * kBlock),
+  static_assert(sizeof(Part<ROWS, D>) <= 2 * (2 * CODES + 8 * kBlock),
                 "a part does not fit the smallest ring");
   using S = Shared4<ROWS, D, WARPS>;
   using U = Units<ROWS, kKeys>;
@@ -159,7 +156,7 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
   constexpr int sb = SB, slot_bytes = 2 * CODES + 2 * kBlock * SB;
   constexpr int GROUP = 4 * D / SB;
   auto ring_of = [&](int w) {
-    return dyn + (sizeof(S) + 127) / 128 * 128 + w * kDepth * slot_bytes;
+    return dyn + (sizeof(S) + 127) / 128 * 128 + w * 2 * slot_bytes;
   };
   char *ring = ring_of(warp);
   griddep_wait();
@@ -168,16 +165,15 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
   if (lane < 2) s.info[warp][lane].there = 0;
   __syncthreads();
 
-  // ---- the warp's blocks of a unit: where the next ones lie.  Lane 2 i + hf
-  // holds the places in bytes of the codes and pairs of half hf of the i-th
-  // block of a batch of sixteen; negative: nothing to be had.
+  // ---- the warp's blocks of a unit: where the next ones lie.  Lane 4 i + o
+  // holds the places in bytes of the codes and pairs of keys 8 o to 8 o + 7 of
+  // the i-th block of a batch of eight; negative: nothing to be had.
   struct Places {
     long long code, pair;
   };
   bool bad = false;
   auto look_up = [&](const U &v, int first) {  // the batch's first block
-    const int key =
-        v.j0 * kKeys + (first + (lane >> 1)) * kBlock + 8 * (lane & 1);
+    const int key = v.j0 * kKeys + first * kBlock + 8 * lane;
     Places x{-1, -1};
     if (key < min(v.j1 * kKeys, v.c.kv)) {
       const int n = div_by(key, p.by_page);
@@ -193,29 +189,32 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
     }
     return x;
   };
-  // A lane's part of the copies of a block: 16 bytes of the codes of both
-  // halves (D = 64: of one), 16 bytes of pairs.
+  // A lane's part of the copies of a block: 16 bytes of the codes of each
+  // eight keys (D = 64: of every other eight), and of pairs.
   const uint32_t to = smem_addr(ring) + 16 * lane;
-  const int which = lane / sb, pair_hf = lane / (sb / 2) & 1;
+  constexpr int CHUNKS = 4 * SB;  // of 16 bytes of pairs, keys' first
+  const int which = lane / (2 * SB), pair_8 = lane / (SB / 2) & 3;
   const char *pairs = (which ? p.c.v_scale : p.c.k_scale) +
-                      16 * (lane & (sb / 2 - 1));
+                      16 * (lane & (SB / 2 - 1));
   const char *k_codes = p.c.k + 16 * (lane & (D / 4 - 1));
   const char *v_codes = p.c.v + 16 * (lane & (D / 4 - 1));
   int fill = 0;  // where to fill next
   auto fetch = [&](const Places &x, int i) {
     const uint32_t at = to + fill;
-    constexpr int HALVES = D / 64;  // that a lane has a part of
 #pragma unroll
-    for (int hf = 0; hf < HALVES; ++hf) {
-      const int from = 2 * i + (HALVES == 2 ? hf : lane >> 4);
-      const long long c = __shfl_sync(~0u, x.code, from);
-      cp16(at + 512 * hf, k_codes + c, c >= 0);
-      cp16(at + CODES + 512 * hf, v_codes + c, c >= 0);
+    for (int o = 0; o < D / 32; ++o) {
+      const long long c = __shfl_sync(
+          ~0u, x.code, 4 * i + (D == 128 ? o : 2 * o + (lane >> 4)));
+      cp16(at + 512 * o, k_codes + c, c >= 0);
+      cp16(at + CODES + 512 * o, v_codes + c, c >= 0);
     }
-    const long long c = __shfl_sync(~0u, x.pair, 2 * i + pair_hf);
-    cp16(at + 2 * CODES, pairs + c, which < 2 && c >= 0);
+    const long long c = __shfl_sync(~0u, x.pair, 4 * i + pair_8);
+    cp16(at + 2 * CODES, pairs + c, lane < CHUNKS && c >= 0);
+    if (CHUNKS > 32)  // the values' pairs: the same places
+      cp16(at + 2 * CODES + 512, p.c.v_scale + 16 * (lane & (SB / 2 - 1)) + c,
+           c >= 0);
     cp_commit();
-    fill = fill == (kDepth - 1) * slot_bytes ? 0 : fill + slot_bytes;
+    fill ^= slot_bytes;
   };
   // Row g of a product's keys is key (g >> 1) + 4 (g & 1) of eight, so that
   // the two whose values a thread pairs are t and t + 4: four rows of 64
@@ -238,7 +237,7 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
   int slot = 0;  // where to use next
   if (u.left) {
     now = look_up(u, 0);
-    for (int i = 0; i < kDepth - 1; ++i) fetch(now, i);
+    fetch(now, 0);
   }
   while (u.left) {
     // the queries' operand: the thread's quarter of rows g (and g + 8)
@@ -269,113 +268,108 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
     // keys that every row of the unit sees
     const int open = p.mask ? ctx : ctx + div_by(u.t * ROWS, p.by_G) + 1;
 
-    struct Block {  // the thread's part of 16 keys
-      uint32_t k[2][W], v[4][W / 2], ks[2], vs[4];
-    };
     const char *k_from = ring + k_at, *ks_from = ring + 2 * CODES + ks_at;
     const char *v_from = ring + CODES + v_at;
     const char *vs_from = ring + 2 * CODES + kBlock * SB + vs_at;
-    auto use = [&](auto hides, int key) {
+    // NB times 16 keys, from the b0-th of the block on.  With 16 rows there
+    // are no registers for both at once (188 us where this takes 147).
+    constexpr int NB = NT == 1 ? 2 : 1;
+    auto use = [&](auto hides, int key, int b0) {
       constexpr bool HIDE = decltype(hides)::value;
-      Block x;
+      // scores: [16 keys][rows]; two sums each, half the chain from product
+      // to product
+      float sc[NB][NT][4];
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        lds_words(k_from + slot + 4 * D * hf, x.k[hf]);
-        x.ks[hf] = *reinterpret_cast<const uint32_t *>(
-            ks_from + slot + 8 * SB * hf);
-      }
-      // what lies past the sequence's keys counts as zeros
-      if (HIDE && key + kg >= u.c.kv) x.ks[0] = 0;
-      if (HIDE && key + 8 + kg >= u.c.kv) x.ks[1] = 0;
-      // two sums a score: half the chain from product to product
-      float sc[NT][4], sd[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[n][e] = sd[n][e] = 0.f;
-      const uint32_t a0 = both_lo(x.ks[0]), b0 = both_hi(x.ks[0]);
-      const uint32_t a1 = both_lo(x.ks[1]), b1 = both_hi(x.ks[1]);
-#pragma unroll
-      for (int i = 0; i < W; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-          const uint32_t f0 = kv4_fma(kv4_codes(x.k[0][i], j), a0, b0);
-          const uint32_t f1 = kv4_fma(kv4_codes(x.k[1][i], j), a1, b1);
-          const uint32_t f2 = kv4_fma(kv4_codes(x.k[0][i], j + 1), a0, b0);
-          const uint32_t f3 = kv4_fma(kv4_codes(x.k[1][i], j + 1), a1, b1);
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-            mma16816(j ? sd[n] : sc[n], f0, f1, f2, f3, qf[n][4 * i + j],
-                     qf[n][4 * i + j + 1]);
-        }
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[n][e] += sd[n][e];
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        lds_words(v_from + slot + 4 * D * hf, x.v[2 * hf]);
-        lds_words(v_from + slot + 4 * D * hf + 2 * D, x.v[2 * hf + 1]);
-        x.vs[2 * hf] = *reinterpret_cast<const uint32_t *>(
-            vs_from + slot + 8 * SB * hf);
-        x.vs[2 * hf + 1] = *reinterpret_cast<const uint32_t *>(
-            vs_from + slot + 8 * SB * hf + 4 * SB);
-        if (HIDE && key + 8 * hf + t >= u.c.kv) x.vs[2 * hf] = 0;
-        if (HIDE && key + 8 * hf + t + 4 >= u.c.kv) x.vs[2 * hf + 1] = 0;
-      }
-      // exponents of the weights; of keys a row does not see -inf
-      float y[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          y[n][e] = fmaf(sc[n][e], rs[n][e & 1], off[n][e & 1]);
-      if (HIDE) {
+      for (int b = 0; b < NB; ++b) {
+        float sd[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int r = min(8 * n + 2 * t + (e & 1), u.rows - 1);
-            const int token = div_by(u.t * ROWS + r, p.by_G);
-            const int i = key + kg + (e >> 1) * 8 - ctx;
-            bool see = i <= token;
-            if (p.mask) {
-              see = i < u.c.n;
-              if (see && i >= 0)
-                see = __ldg(p.mask +
-                            (long long)(u.c.start + token) * p.mask_words +
-                            (i >> 5)) >>
-                          (i & 31) &
-                      1;
-            }
-            if (!see) y[n][e] = -kInf;
-          }
-      }
-      float most = fmaxf(y[0][0], y[0][1]);
+          for (int e = 0; e < 4; ++e) sc[b][n][e] = sd[n][e] = 0.f;
+        uint32_t k[2][W], a[2], c[2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (n) most = max3f(most, y[n][0], y[n][1]);
-        most = max3f(most, y[n][2], y[n][3]);
+        for (int hf = 0; hf < 2; ++hf) {
+          lds_words(k_from + slot + 8 * (D / 2) * (2 * (b0 + b) + hf), k[hf]);
+          uint32_t x = *reinterpret_cast<const uint32_t *>(
+              ks_from + slot + 8 * SB * (2 * (b0 + b) + hf));
+          // what lies past the sequence's keys counts as zeros
+          if (HIDE && key + 16 * (b0 + b) + 8 * hf + kg >= u.c.kv) x = 0;
+          a[hf] = both_lo(x);
+          c[hf] = both_hi(x);
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            const uint32_t f0 = kv4_fma(kv4_codes(k[0][i], j), a[0], c[0]);
+            const uint32_t f1 = kv4_fma(kv4_codes(k[1][i], j), a[1], c[1]);
+            const uint32_t f2 =
+                kv4_fma(kv4_codes(k[0][i], j + 1), a[0], c[0]);
+            const uint32_t f3 =
+                kv4_fma(kv4_codes(k[1][i], j + 1), a[1], c[1]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma16816(j ? sd[n] : sc[b][n], f0, f1, f2, f3,
+                       qf[n][4 * i + j], qf[n][4 * i + j + 1]);
+          }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[b][n][e] += sd[n][e];
       }
+      // exponents of the weights; of keys a row does not see -inf
+      float y[NB][NT][4];
+      float most = -kInf;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[b][n][e] = fmaf(sc[b][n][e], rs[n][e & 1], off[n][e & 1]);
+            if (HIDE) {
+              const int r = min(8 * n + 2 * t + (e & 1), u.rows - 1);
+              const int token = div_by(u.t * ROWS + r, p.by_G);
+              const int i = key + 16 * (b0 + b) + kg + (e >> 1) * 8 - ctx;
+              bool see = i <= token;
+              if (p.mask) {
+                see = i < u.c.n;
+                if (see && i >= 0)
+                  see = __ldg(p.mask +
+                              (long long)(u.c.start + token) * p.mask_words +
+                              (i >> 5)) >>
+                            (i & 31) &
+                        1;
+              }
+              if (!see) y[b][n][e] = -kInf;
+            }
+          }
+          most = max3f(most, y[b][n][0], y[b][n][1]);
+          most = max3f(most, y[b][n][2], y[b][n][3]);
+        }
       if (__any_sync(~0u, most > kBias + kSlack)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             // (from kNone the exponents say nothing but which keys count)
-            const float s0 =
-                y[n][e] == -kInf ? -kInf : sc[n][e] * rs[n][e];
-            const float s1 =
-                y[n][e + 2] == -kInf ? -kInf : sc[n][e + 2] * rs[n][e];
-            float top = fmaxf(s0, s1);
+            float x[2 * NB], top = -kInf;
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i) {
+              x[i] = y[i >> 1][n][e + 2 * (i & 1)];
+              if (x[i] != -kInf)
+                x[i] = sc[i >> 1][n][e + 2 * (i & 1)] * rs[n][e];
+              top = fmaxf(top, x[i]);
+            }
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1)
               top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
             if (top + off[n][e] > kBias + kSlack) {
-              const float to = kBias - top, f = ex2(to - off[n][e]);
-              off[n][e] = to;
-              y[n][e] = s0 + to;
-              y[n][e + 2] = s1 + to;
+              const float up = kBias - top, f = ex2(up - off[n][e]);
+              off[n][e] = up;
+#pragma unroll
+              for (int i = 0; i < 2 * NB; ++i)
+                y[i >> 1][n][e + 2 * (i & 1)] = x[i] + up;
               l[n][e] *= f;
 #pragma unroll
               for (int i = 0; i < 2 * W; ++i) {
@@ -385,65 +379,76 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
             }
           }
       }
-      uint32_t w[NT][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float z[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          z[e] = ex2(y[n][e]);
-          l[n][e & 1] += z[e];
-        }
-        w[n][0] = transpose8(pack2<__half>(z[0], z[1]));
-        w[n][1] = transpose8(pack2<__half>(z[2], z[3]));
-      }
-      // values of two keys at a time: their codes are brought together
-      uint32_t va[2], vb[2];
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        va[hf] = __byte_perm(x.vs[2 * hf], x.vs[2 * hf + 1], 0x5410);
-        vb[hf] = __byte_perm(x.vs[2 * hf], x.vs[2 * hf + 1], 0x7632);
-      }
-#pragma unroll
-      for (int i = 0; i < W / 2; ++i) {
-        uint32_t lo[2], hi[2];
+      for (int b = 0; b < NB; ++b) {
+        // values of two keys at a time: their codes are brought together
+        uint32_t v[4][W / 2], va[2], vc[2];
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          lo[hf] = __byte_perm(x.v[2 * hf][i], x.v[2 * hf + 1][i], 0x5410);
-          hi[hf] = __byte_perm(x.v[2 * hf][i], x.v[2 * hf + 1][i], 0x7632);
+          const char *from = v_from + slot + 8 * (D / 2) * (2 * (b0 + b) + hf);
+          lds_words(from, v[2 * hf]);
+          lds_words(from + 4 * (D / 2), v[2 * hf + 1]);
+          from = vs_from + slot + 8 * SB * (2 * (b0 + b) + hf);
+          uint32_t x = *reinterpret_cast<const uint32_t *>(from);
+          uint32_t z = *reinterpret_cast<const uint32_t *>(from + 4 * SB);
+          if (HIDE && key + 16 * (b0 + b) + 8 * hf + t >= u.c.kv) x = 0;
+          if (HIDE && key + 16 * (b0 + b) + 8 * hf + t + 4 >= u.c.kv) z = 0;
+          va[hf] = __byte_perm(x, z, 0x5410);
+          vc[hf] = __byte_perm(x, z, 0x7632);
+        }
+        uint32_t w[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float z[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            z[e] = ex2(y[b][n][e]);
+            l[n][e & 1] += z[e];
+          }
+          w[n][0] = transpose8(pack2<__half>(z[0], z[1]));
+          w[n][1] = transpose8(pack2<__half>(z[2], z[3]));
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          // elements 8 i + 2 j (rows g) and 8 i + 2 j + 1 (rows g + 8)
-          const uint32_t f0 = kv4_fma(kv4_codes(lo[0], j), va[0], vb[0]);
-          const uint32_t f1 = kv4_fma(kv4_codes(hi[0], j), va[0], vb[0]);
-          const uint32_t f2 = kv4_fma(kv4_codes(lo[1], j), va[1], vb[1]);
-          const uint32_t f3 = kv4_fma(kv4_codes(hi[1], j), va[1], vb[1]);
+        for (int i = 0; i < W / 2; ++i) {
+          uint32_t lo[2], hi[2];
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            mma16816(o[n][4 * i + j], f0, f1, f2, f3, w[n][0], w[n][1]);
+          for (int hf = 0; hf < 2; ++hf) {
+            lo[hf] = __byte_perm(v[2 * hf][i], v[2 * hf + 1][i], 0x5410);
+            hi[hf] = __byte_perm(v[2 * hf][i], v[2 * hf + 1][i], 0x7632);
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            // elements 8 i + 2 j (rows g) and 8 i + 2 j + 1 (rows g + 8)
+            const uint32_t f0 = kv4_fma(kv4_codes(lo[0], j), va[0], vc[0]);
+            const uint32_t f1 = kv4_fma(kv4_codes(hi[0], j), va[0], vc[0]);
+            const uint32_t f2 = kv4_fma(kv4_codes(lo[1], j), va[1], vc[1]);
+            const uint32_t f3 = kv4_fma(kv4_codes(hi[1], j), va[1], vc[1]);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma16816(o[n][4 * i + j], f0, f1, f2, f3, w[n][0], w[n][1]);
+          }
         }
       }
     };
-
     const int key0 = u.j0 * kKeys;
     const int blocks = (min(u.j1 * kKeys, u.c.kv) - key0 + kBlock - 1) /
                        kBlock;
     for (int i = 0; i < blocks; ++i) {
-      cp_wait<kDepth - 2>();
+      cp_wait<0>();
       __syncwarp();
+      // the next block goes where the one before this was
+      if (((i + 1) & 7) == 0) now = look_up(u, i + 1);
+      fetch(now, (i + 1) & 7);
       const int key = key0 + i * kBlock;
-      // the slot used before this one is free
-      const int next = i + kDepth - 1;
-      if ((next & 15) == 0) now = look_up(u, next);
-      fetch(now, next & 15);
-      if (key + kBlock > open) use(std::true_type{}, key);
-      else use(std::false_type{}, key);
-      slot = slot == (kDepth - 1) * slot_bytes ? 0 : slot + slot_bytes;
+#pragma unroll 1
+      for (int b0 = 0; b0 < 2; b0 += NB)
+        if (key + kBlock > open) use(std::true_type{}, key, b0);
+        else use(std::false_type{}, key, b0);
+      slot ^= slot_bytes;
     }
 
-    // ---- the end of the part.  Blocks past it were fetched as empty ones:
-    // the next unit's take their place
+    // ---- the end of the part.  The block past it was fetched as an empty
+    // one: the next unit's first takes its place
     cp_wait<0>();
     fill = slot;
     const bool was_bad = __any_sync(~0u, bad);
@@ -454,7 +459,7 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
     u.next();
     if (u.left) {
       now = look_up(u, 0);
-      for (int i = 0; i < kDepth - 1; ++i) fetch(now, i);
+      fetch(now, 0);
     }
     if (was_bad && lane == 0) status_or(p.dev_status, SD_DEV_BAD_PAGE);
     // The last part may go where the ring was: nothing is on its way there.
@@ -615,10 +620,12 @@ int rows_tile(int max_q, int G) {
 
 template <int D, int SB, int NT>
 sd_status launch_rows(Attn4Params &p, int sms, void *ws, cudaStream_t s) {
-  constexpr int WARPS = NT == 1 ? 8 : 12;
+  // Two CTAs of eight warps an SM where their shared memory lets them (200
+  // sequences of 300 keys take 29 us so, and 35 with one of sixteen).
+  constexpr int WARPS = NT == 2 ? 12 : D == 128 && SB == 16 ? 16 : 8;
   constexpr size_t smem =
       (sizeof(Shared4<8 * NT, D, WARPS>) + 127) / 128 * 128 +
-      WARPS * ring_depth<NT>() * kBlock * (D + 2 * SB);
+      WARPS * 2 * kBlock * (D + 2 * SB);
   set_workspace(p, ws_layout(kMaxGrid4, 8 * NT, D), ws);
   const void *kernel = (const void *)kv4_rows_kernel<D, SB, NT, WARPS>;
   int dev = 0;
@@ -629,7 +636,7 @@ sd_status launch_rows(Attn4Params &p, int sms, void *ws, cudaStream_t s) {
         kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
     if (dev < 64) ready.fetch_or(1ull << dev);
   }
-  const int want = NT == 1 ? 2 * sms : sms;
+  const int want = WARPS == 8 ? 2 * sms : sms;
   const unsigned grid = want < kMaxGrid4 ? want : kMaxGrid4;
   void *args[] = {&p};
   const sd_status st = launch_pdl(kernel, grid, WARPS * 32, smem, s, args);
