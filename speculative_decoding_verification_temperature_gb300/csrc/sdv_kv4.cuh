@@ -44,6 +44,36 @@ __device__ __forceinline__ uint32_t both_hi(uint32_t x) {
   return __byte_perm(x, x, 0x3232);
 }
 
+// 16 bytes from global to shared memory, asynchronously, if `there`.
+__device__ __forceinline__ void cp16(uint32_t to, const void *from,
+                                     bool there) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+      "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(to),
+      "l"(from), "r"((int)there)
+      : "memory");
+}
+__device__ __forceinline__ void cp_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N> __device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A thread's share of a key's row: N words of shared memory.
+template <int N>
+__device__ __forceinline__ void lds_words(const char *p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 x = *reinterpret_cast<const uint4 *>(p);
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  } else if constexpr (N == 2) {
+    const uint2 x = *reinterpret_cast<const uint2 *>(p);
+    w[0] = x.x, w[1] = x.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t *>(p);
+  }
+}
+
 // Where the codes and the pairs of a cache lie: in bytes, pages `stride`
 // apart, inside a page [heads][page_size] rows.
 struct Kv4Cache {

@@ -1,20 +1,9 @@
 // sdv_kv4_attention.cu -- sd_kv4_attention: a chunk of new tokens attends
 // over the 4-bit paged cache.
-#include <atomic>
-
-#include "sdv_kv4.cuh"
-#include "sdv_units.cuh"
+#include "sdv_attention.cuh"
 
 namespace sdv {
 namespace {
-
-struct Attn4Params : UnitParams {
-  const void *q;
-  long long q_stride;
-  Kv4Cache c;
-  float scale_log2;  // scale x log2(e)
-  bool bf16;         // type of q and out; fp16 otherwise
-};
 
 // ------------------------------------------------------- few rows a head
 //
@@ -54,20 +43,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
-// A thread's share of a key's row: N words of shared memory.
-template <int N>
-__device__ __forceinline__ void lds_words(const char *p, uint32_t (&w)[N]) {
-  if constexpr (N == 4) {
-    const uint4 x = *reinterpret_cast<const uint4 *>(p);
-    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-  } else if constexpr (N == 2) {
-    const uint2 x = *reinterpret_cast<const uint2 *>(p);
-    w[0] = x.x, w[1] = x.y;
-  } else {
-    w[0] = *reinterpret_cast<const uint32_t *>(p);
-  }
-}
-
 // A part of a unit that a warp leaves to be joined with others: (m, l) and O
 // of its rows.
 template <int ROWS, int D> struct Part {
@@ -85,21 +60,6 @@ template <int ROWS, int D, int WARPS> struct Shared4 {
   PartInfo info[WARPS][2];
   Part<ROWS, D> part[WARPS];  // of the warp's first unit
 };
-
-__device__ __forceinline__ void cp16(uint32_t to, const void *from,
-                                     bool there) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
-      "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(to),
-      "l"(from), "r"((int)there)
-      : "memory");
-}
-__device__ __forceinline__ void cp_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N> __device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 // A thread's part of a query row, D / 4 elements, as fp16 pairs, and the
 // factor of its scores.  bf16 rows are multiplied by the power of two that
@@ -142,7 +102,7 @@ constexpr int kKeys = kBlock;  // keys of a place in the shares
 
 template <int D, int SB, int NT, int WARPS>  // SB: bytes of a key's pairs
 __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1)
-kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
+kv4_rows_kernel(const __grid_constant__ AttnParams p) {
   constexpr int ROWS = 8 * NT, W = D / 32;  // W: words of a key a thread
   constexpr int CODES = kBlock * D / 2;     // bytes of a block's key codes
   static_assert(sizeof(Part<ROWS, D>) <= 2 * (2 * CODES + 8 * kBlock),
@@ -614,12 +574,18 @@ kv4_rows_kernel(const __grid_constant__ Attn4Params p) {
 // ------------------------------------------------------------------- host
 constexpr int kMaxGrid4 = 320;  // CTAs the workspace is laid out for
 
-int rows_tile(int max_q, int G) {
-  return (long long)max_q * G <= 8 ? 1 : 2;
+// The kernel of a call, by the rows a head has: 8 or 16 at a time in warps of
+// their own, 128 or 256 on the fifth-generation tensor cores.
+int rows_of(int max_q, int G) {
+  const long long n = (long long)max_q * G;
+  return n <= 8 ? 8 : n <= 16 ? 16 : n <= 128 ? 128 : 256;
+}
+size_t workspace_of(int rows, int D) {
+  return ws_layout(rows <= 16 ? kMaxGrid4 : kMaxGrid, rows, D).bytes;
 }
 
 template <int D, int SB, int NT>
-sd_status launch_rows(Attn4Params &p, int sms, void *ws, cudaStream_t s) {
+sd_status launch_rows(AttnParams &p, int sms, void *ws, cudaStream_t s) {
   // Two CTAs of eight warps an SM where their shared memory lets them (200
   // sequences of 300 keys take 29 us so, and 35 with one of sixteen).
   constexpr int WARPS = NT == 2 ? 12 : D == 128 && SB == 16 ? 16 : 8;
@@ -646,8 +612,8 @@ sd_status launch_rows(Attn4Params &p, int sms, void *ws, cudaStream_t s) {
 }
 
 template <int NT>
-sd_status dispatch4(Attn4Params &p, int D, int sms, void *ws,
-                    cudaStream_t s) {
+sd_status dispatch_rows(AttnParams &p, int D, int sms, void *ws,
+                        cudaStream_t s) {
   const int sb = p.c.scale_bytes;
   if (D == 64)
     return sb == 4 ? launch_rows<64, 4, NT>(p, sms, ws, s)
@@ -655,6 +621,16 @@ sd_status dispatch4(Attn4Params &p, int D, int sms, void *ws,
   return sb == 4   ? launch_rows<128, 4, NT>(p, sms, ws, s)
          : sb == 8 ? launch_rows<128, 8, NT>(p, sms, ws, s)
                    : launch_rows<128, 16, NT>(p, sms, ws, s);
+}
+
+template <bool PAIR>
+sd_status dispatch_tiles(AttnParams &p, int D, int sms, void *ws,
+                         cudaStream_t s) {
+  const CUtensorMap none = {};  // tiles are not loaded but made
+  char *at = static_cast<char *>(ws);
+  return D == 64
+             ? launch<__half, 64, PAIR, true>(p, none, none, sms, at, s)
+             : launch<__half, 128, PAIR, true>(p, none, none, sms, at, s);
 }
 
 }  // namespace
@@ -666,8 +642,7 @@ extern "C" size_t sd_kv4_attention_workspace(int q_heads, int heads,
                                              int head_dim, int max_q) {
   if (heads < 1 || q_heads < heads || (head_dim != 64 && head_dim != 128))
     return 256;
-  return ws_layout(kMaxGrid4, 8 * rows_tile(max_q, q_heads / heads), head_dim)
-      .bytes;
+  return workspace_of(rows_of(max_q, q_heads / heads), head_dim);
 }
 
 extern "C" sd_status sd_kv4_attention(
@@ -710,7 +685,7 @@ extern "C" sd_status sd_kv4_attention(
   int sms = 0;
   st = check_device(&sms);
   if (st != SD_OK) return st;
-  Attn4Params p;
+  AttnParams p;
   p.q = q;
   p.q_stride = q_stride;
   p.q_start = q_start;
@@ -734,6 +709,10 @@ extern "C" sd_status sd_kv4_attention(
   p.c = kv4_cache(cache);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   p.bf16 = cache->dt == SD_BF16;
-  return rows_tile(max_q, p.G) == 1 ? dispatch4<1>(p, D, sms, workspace, s)
-                                    : dispatch4<2>(p, D, sms, workspace, s);
+  switch (rows_of(max_q, p.G)) {
+    case 8: return dispatch_rows<1>(p, D, sms, workspace, s);
+    case 16: return dispatch_rows<2>(p, D, sms, workspace, s);
+    case 128: return dispatch_tiles<false>(p, D, sms, workspace, s);
+    default: return dispatch_tiles<true>(p, D, sms, workspace, s);
+  }
 }
