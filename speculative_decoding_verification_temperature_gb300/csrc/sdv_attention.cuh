@@ -63,9 +63,7 @@ namespace {
 
 constexpr int kHalf = kTile / 2;  // keys a softmax thread weighs at a time
 constexpr int kMaxGrid = 160;    // CTAs the workspace is laid out for
-// Two warpgroups of softmax, one of roles; over a cache in 4 bits one that
-// makes tiles of its codes.
-template <bool CODES> constexpr int attn_threads() { return CODES ? 512 : 384; }
+constexpr int kAttnThreads = 384;  // two warpgroups of softmax, one of roles
 constexpr int kMmaWarp = 9;  // and 10; warps 8 and 11 load
 constexpr int kBadRing = 64;     // units whose bad-page mark is kept
 // A row's weights are 2^kBias at its reference m, and m moves up only when the
@@ -123,13 +121,13 @@ template <int D, bool PAIR, bool CODES> struct Layout {
                              : D == 128 ? (PAIR ? 2 : 3)
                              : PAIR     ? 4
                                         : 5;
-  // CODES: each warp that makes tiles has a ring of what it makes them of,
-  // codes and pairs of 32 keys (or values).
-  static constexpr int kRaw = D == 128 ? (PAIR ? 3 : 5) : PAIR ? 4 : 8;
-  static constexpr int kRawBytes = 32 * (D / 2 + D / 8);
+  // CODES: a loading warp makes the tiles of its ring, of codes and pairs of
+  // 64 keys (or values) at a time, which it has a ring of.
+  static constexpr int kRaw = D == 128 ? (PAIR ? 3 : 4) : 6;
+  static constexpr int kRawBytes = 64 * (D / 2 + D / 8);
   static constexpr size_t kTiles =
       kQBytes + (size_t)kTileBytes * (kN0 + kN1) +
-      (CODES ? 4 * kRaw * kRawBytes : 0);
+      (CODES ? 2 * kRaw * kRawBytes : 0);
 };
 
 template <int D, bool PAIR, bool CODES> struct Shared {
@@ -154,7 +152,8 @@ __device__ __forceinline__ void streams_sync() {
   asm volatile("bar.sync 1, 256;" ::: "memory");
 }
 __device__ __forceinline__ void stream_sync(int st) {
-  asm volatile("bar.sync %0, 128;" ::"r"(2 + st) : "memory");
+  if (st) asm volatile("bar.sync 3, 128;" ::: "memory");
+  else asm volatile("bar.sync 2, 128;" ::: "memory");
 }
 
 // A pair as a sum of two 16-bit pairs.  bf16: the first is cut off, not
@@ -371,46 +370,56 @@ __device__ __forceinline__ float to_half_row(uint4 &x, bool bf16,
   return f;
 }
 
-// Tiles of 128 keys and of their values, as fp16 numbers in the swizzle, made
-// of a 4-bit cache by four warps, 32 keys each: a warp copies its codes and
-// pairs to a ring of its own, kRaw - 1 of them ahead, and turns a word of
-// codes, eight neighbours, into the 16 bytes of a chunk.  What lies past a
-// sequence's keys becomes zeros.
+// The tiles of ring `me`, as fp16 numbers in the swizzle, made of a 4-bit cache
+// by one warp: it copies codes and pairs of half a tile to a ring of its own,
+// kRaw - 1 halves ahead, and turns a word of codes, eight neighbours, into the
+// 16 bytes of a chunk.  What lies past a sequence's keys becomes zeros.
 template <int D, bool PAIR, int ROWS>
 __device__ __forceinline__ void make_tiles(const AttnParams &p,
                                            Shared<D, PAIR, true> &s,
                                            char *tiles, int me) {
   using L = Layout<D, PAIR, true>;
   constexpr int W = D / 32;  // words of a key a thread
-  constexpr int CODE_BYTES = 16 * D;
+  constexpr int CODE_BYTES = 32 * D;
+  // PAIR: keys or values of every tile; otherwise both of every other tile
+  constexpr int STEP = PAIR ? 1 : 2;
   const int lane = threadIdx.x & 31, sb = p.c.scale_bytes;
-  char *ring[2] = {tiles, tiles + L::kN0 * L::kTileBytes};
+  char *ring = tiles + (me ? L::kN0 * L::kTileBytes : 0);
   char *raw = tiles + (L::kN0 + L::kN1) * L::kTileBytes +
               me * L::kRaw * L::kRawBytes;
-  // ---- what is fetched next: keys (or, after them, values) of tile fj
+  // ---- what is fetched next: half fh of the keys, then of the values, of
+  // tile fj
   Units<ROWS> f(p, s.plan);
-  int fj = f.left ? f.j0 : 0, fill = 0;
-  bool f_values = false;
-  long long code = -1, pair = -1;  // of the lane's eight keys; negative: none
+  int fj = 0, fh = 0, fill = 0;
+  long long code = -1, pair = -1;  // of eight keys a lane; negative: none
   int id = 0;                      // and their page
-  auto look_up = [&] {
-    const int key = fj * kTile + 32 * me + 8 * (lane & 3);
+  auto look_up = [&] {  // lane: keys 8 (lane % 16) to + 7 of the tile
+    const int key = fj * kTile + 8 * (lane & 15);
     id = -1;
     if (key < f.c.kv)
       id = __ldg(p.block_table + (long long)f.b * p.max_pages +
                  div_by(key, p.by_page));
   };
-  if (f.left) look_up();
+  auto first_tile = [&] {  // of the ring in a unit; past units without one
+    for (; f.left; f.next()) {
+      fj = f.j0 + (PAIR ? 0 : me);
+      if (fj < f.j1) break;
+    }
+    if (f.left) look_up();
+  };
+  first_tile();
   const uint32_t to = smem_addr(raw) + 16 * lane;
-  const char *codes[2] = {p.c.k + 16 * (lane & (D / 4 - 1)),
-                          p.c.v + 16 * (lane & (D / 4 - 1))};
+  const char *k_codes = p.c.k + 16 * (lane & (D / 4 - 1));
+  const char *v_codes = p.c.v + 16 * (lane & (D / 4 - 1));
   const int pair_at = 16 * (lane & (sb / 2 - 1)), pair_8 = lane / (sb / 2);
   auto fetch = [&] {
     if (f.left) {
-      if (!f_values) {
-        const int key = fj * kTile + 32 * me + 8 * (lane & 3);
+      const bool values = PAIR ? me : fh >> 1;
+      const int hf = fh & 1;
+      if (fh == 0) {
+        const int key = fj * kTile + 8 * (lane & 15);
         code = pair = -1;
-        if (id >= 0 && id < p.c.num_pages) {
+        if (id >= 0 && id < p.num_pages) {
           const int row =
               (f.h - div_by(key, p.by_page)) * p.page_size + key;
           code = id * p.c.page_stride + (long long)row * (D / 2);
@@ -420,24 +429,30 @@ __device__ __forceinline__ void make_tiles(const AttnParams &p,
           status_or(p.dev_status, SD_DEV_BAD_PAGE);
         }
       }
-      const char *from = f_values ? codes[1] : codes[0];
+      const char *from = values ? v_codes : k_codes;
 #pragma unroll
-      for (int o = 0; o < D / 32; ++o) {
+      for (int o = 0; o < D / 16; ++o) {
         const long long c = __shfl_sync(
-            ~0u, code, D == 128 ? o : 2 * o + (lane >> 4));
+            ~0u, code, 8 * hf + (D == 128 ? o : 2 * o + (lane >> 4)));
         cp16(to + fill + 512 * o, from + c, c >= 0);
       }
-      const long long c = __shfl_sync(~0u, pair, pair_8 & 3);
-      cp16(to + fill + CODE_BYTES,
-           (f_values ? p.c.v_scale : p.c.k_scale) + pair_at + c,
-           pair_8 < 4 && c >= 0);
-      f_values = !f_values;
-      if (!f_values) {
-        if (++fj == f.j1) {
+      const char *pairs =
+          (values ? p.c.v_scale : p.c.k_scale) + pair_at;
+#pragma unroll
+      for (int o = 0; o < 2; ++o) {  // 64 / sb lanes hold eight keys' pairs
+        const int at = pair_8 + o * (64 / sb);
+        const long long c = __shfl_sync(~0u, pair, 8 * hf + (at & 7));
+        cp16(to + fill + CODE_BYTES + 512 * o, pairs + c, at < 8 && c >= 0);
+      }
+      if (++fh == (PAIR ? 2 : 4)) {
+        fh = 0;
+        fj += STEP;
+        if (fj >= f.j1) {
           f.next();
-          if (f.left) fj = f.j0;
+          first_tile();
+        } else {
+          look_up();
         }
-        if (f.left) look_up();
       }
     }
     cp_commit();
@@ -450,47 +465,49 @@ __device__ __forceinline__ void make_tiles(const AttnParams &p,
   const char *code_from = raw + row * (D / 2) + t * (D / 8);
   const char *pair_from =
       raw + CODE_BYTES + row * sb + 4 * ((t * (D / 4)) >> p.c.shift);
-  // chunk i of the thread's W lies in column half t / 2 (D = 128), and is the
-  // (W t + i)-th there.  A store's threads, two rows of four, would meet the
-  // same banks for both halves: the second half's take their words in another
+  // Chunk i of the thread's W is the (W t + i)-th of the row, eight to a
+  // column half.  A store's threads, two rows of four, would meet the same
+  // banks for both halves: the second half's take their words in another
   // order.
   const int turn = D == 128 ? t & 2 : 0;
-  const int dst_at =
-      (D == 128 ? (t >> 1) * (kTile * 128) : 0) + (32 * me + row) * 128;
+  char *const tile_at =
+      ring + (D == 128 ? (t >> 1) * (kTile * 128) : 0) + row * 128;
   int use = 0;
   bool fine = true;
-  RingAt at0(L::kN0), at1(L::kN1);
+  RingAt at(me ? L::kN1 : L::kN0);
   Units<ROWS> u(p, s.plan);
   for (; u.left && fine; u.next())
-    for (int j = u.j0; j < u.j1 && fine; ++j)
+    for (int j = u.j0 + (PAIR ? 0 : me); j < u.j1 && fine; j += STEP)
 #pragma unroll 1
-      for (int values = 0; values < 2 && fine; ++values) {
+      for (int n = 0; n < (PAIR ? 2 : 4); ++n) {  // halves of keys and values
         cp_wait<L::kRaw - 2>();
         __syncwarp();
-        fetch();  // to where the part before this one was
-        const bool second = PAIR ? values : (j - u.j0) & 1;
-        const int slot = second ? at1.slot : at0.slot;
-        const uint32_t parity = second ? at1.parity : at0.parity;
-        fine = role_wait(&s.empty[second][slot], parity ^ 1, &s.abort,
-                         p.dev_status);
-        if (!__all_sync(~0u, fine)) {
-          fine = false;
-          break;
+        fetch();  // to where the half before this one was
+        if (!(n & 1)) {
+          fine = role_wait(&s.empty[me][at.slot], at.parity ^ 1, &s.abort,
+                           p.dev_status);
+          if (!__all_sync(~0u, fine)) {
+            fine = false;
+            break;
+          }
         }
-        char *tile =
-            (second ? ring[1] : ring[0]) + slot * L::kTileBytes + dst_at;
-        const int left = u.c.kv - (j * kTile + 32 * me + row);
+        char *tile = tile_at + at.slot * L::kTileBytes + (n & 1) * 64 * 128;
+        const int left = u.c.kv - (j * kTile + 64 * (n & 1) + row);
+        // (all loads first: the compiler may not move one past a store)
+        uint32_t w[8][W], x[8];
 #pragma unroll
-        for (int o = 0; o < 4; ++o) {
-          uint32_t w[W];
-          lds_words(code_from + use + o * 8 * (D / 2), w);
-          uint32_t x = *reinterpret_cast<const uint32_t *>(
+        for (int o = 0; o < 8; ++o) {
+          lds_words(code_from + use + o * 8 * (D / 2), w[o]);
+          x[o] = *reinterpret_cast<const uint32_t *>(
               pair_from + use + o * 8 * sb);
-          if (8 * o >= left) x = 0;
-          const uint32_t a = both_lo(x), b = both_hi(x);
+        }
+#pragma unroll
+        for (int o = 0; o < 8; ++o) {
+          if (8 * o >= left) x[o] = 0;
+          const uint32_t a = both_lo(x[o]), b = both_hi(x[o]);
 #pragma unroll
           for (int i = 0; i < W; ++i) {
-            const uint32_t word = D == 128 && turn ? w[i ^ 2] : w[i];
+            const uint32_t word = D == 128 && turn ? w[o][i ^ 2] : w[o][i];
             const int chunk = ((W * t + (i ^ turn)) & 7) ^ row;
             uint4 y;
             y.x = kv4_fma(kv4_codes(word, 0), a, b);
@@ -500,12 +517,13 @@ __device__ __forceinline__ void make_tiles(const AttnParams &p,
             *reinterpret_cast<uint4 *>(tile + o * 8 * 128 + chunk * 16) = y;
           }
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.full[second][slot]);
-        if (second) at1.next();
-        else at0.next();
         use = use == (L::kRaw - 1) * L::kRawBytes ? 0 : use + L::kRawBytes;
+        if (n & 1) {
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.full[me][at.slot]);
+          at.next();
+        }
       }
   cp_wait<0>();
 }
@@ -514,7 +532,7 @@ __device__ __forceinline__ void make_tiles(const AttnParams &p,
 // T: type of the products.  CODES: the cache is in 4 bits, T is fp16, q and
 // out are of the type that p.bf16 says.
 template <class T, int D, bool PAIR, bool CODES>
-__global__ void __launch_bounds__(attn_threads<CODES>(), 1)
+__global__ void __launch_bounds__(kAttnThreads, 1)
 attention_kernel(const __grid_constant__ AttnParams p,
                  const __grid_constant__ CUtensorMap k_map,
                  const __grid_constant__ CUtensorMap v_map) {
@@ -533,7 +551,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
   if (tid == 0) {
     for (int i = 0; i < 2; ++i)
       for (int k = 0; k < L::kN0; ++k) {
-        mbar_init(&s.full[i][k], CODES ? 4 : 1);
+        mbar_init(&s.full[i][k], 1);
         mbar_init(&s.empty[i][k], PAIR ? 2 : 1);  // the streams that read it
       }
     for (int i = 0; i < 2; ++i) {
@@ -566,21 +584,23 @@ attention_kernel(const __grid_constant__ AttnParams p,
   const uint32_t tmem = s.tmem;
   bool fine = true;
 
-  // 384 threads start with 168 registers each, 512 with 128; a softmax thread
-  // holds much of a row, a role next to nothing: 256 x 208 + 128 x 88 = 384 x
-  // 168, and 256 x 168 + 256 x 88 = 512 x 128
+  // 384 threads start with 168 registers each; a softmax thread holds much of
+  // a row, a role next to nothing: 256 x 208 + 128 x 88 = 384 x 168
   if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  else if (CODES) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
   else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-  if (CODES && warp >= 12) {
-    if constexpr (CODES)
-      make_tiles<D, PAIR, ROWS>(p, s, q_tile + L::kQBytes,
-                                warp - 12);
-  } else if (CODES && (warp == 8 || warp == 11)) {
-    // nothing to load
-  } else if (warp >= 8) {
+  // (the branch has to be on the same condition: code that both kinds reach
+  // has the smaller number)
+  if (warp >= 8) {
+    const bool maker = CODES && (warp == 8 || warp == 11);
+    if constexpr (CODES) {
+      if (maker)
+        make_tiles<D, PAIR, ROWS>(p, s, q_tile + L::kQBytes,
+                                  warp == 8 ? 0 : 1);
+    }
     Units<ROWS> u(p, s.plan);
-    if (warp == 8 || warp == 11) {
+    if (maker) {
+      // done
+    } else if (!CODES && (warp == 8 || warp == 11)) {
       // ---- ring `me`, a box of page rows at a time
       const int me = warp == 8 ? 0 : 1;
       const int per = kTile / p.box;  // boxes of a tile and column half
@@ -1022,10 +1042,10 @@ attention_kernel(const __grid_constant__ AttnParams p,
       if (tid == 0) status_or(p.dev_status, SD_DEV_BAD_LENGTH);
       const long long lo = (long long)c.start * p.Hq,
                       n = (long long)c.n * p.Hq;
-      for (long long i = tid; i < n * D; i += blockDim.x)
+      for (long long i = tid; i < n * D; i += kAttnThreads)
         ((uint16_t *)p.out)[lo * D + i] = 0x7fff;  // NaN of either type
       if (p.lse)
-        for (long long i = tid; i < n; i += blockDim.x)
+        for (long long i = tid; i < n; i += kAttnThreads)
           p.lse[lo + i] = __int_as_float(0x7fc00000);
     }
   }
@@ -1056,7 +1076,7 @@ sd_status launch(AttnParams &p, const CUtensorMap &k_map,
   const unsigned grid = sms < kMaxGrid ? sms : kMaxGrid;
   void *args[] = {&p, const_cast<CUtensorMap *>(&k_map),
                   const_cast<CUtensorMap *>(&v_map)};
-  sd_status st = launch_pdl(kernel, grid, attn_threads<CODES>(),
+  sd_status st = launch_pdl(kernel, grid, kAttnThreads,
                             attn_smem<D, PAIR, CODES>(), s, args);
   if (st != SD_OK) return st;
   if (CODES && p.bf16)

@@ -706,6 +706,7 @@ extern "C" sd_status sd_kv4_attention(
   p.out = out;
   p.lse = lse;
   p.dev_status = dev_status;
+  p.num_pages = cache->num_pages;
   p.c = kv4_cache(cache);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   p.bf16 = cache->dt == SD_BF16;
