@@ -63,7 +63,9 @@ namespace {
 
 constexpr int kHalf = kTile / 2;  // keys a softmax thread weighs at a time
 constexpr int kMaxGrid = 160;    // CTAs the workspace is laid out for
-constexpr int kAttnThreads = 384;  // two warpgroups of softmax, one of roles
+// Two warpgroups of softmax, one of roles; over a cache in 4 bits one that
+// makes tiles of its codes.
+template <bool CODES> constexpr int attn_threads() { return CODES ? 512 : 384; }
 constexpr int kMmaWarp = 9;  // and 10; warps 8 and 11 load
 constexpr int kBadRing = 64;     // units whose bad-page mark is kept
 // A row's weights are 2^kBias at its reference m, and m moves up only when the
@@ -121,9 +123,9 @@ template <int D, bool PAIR, bool CODES> struct Layout {
                              : D == 128 ? (PAIR ? 2 : 3)
                              : PAIR     ? 4
                                         : 5;
-  // CODES: a loading warp makes the tiles of its ring, of codes and pairs of
-  // 64 keys (or values) at a time, which it has a ring of.
-  static constexpr int kRaw = D == 128 ? (PAIR ? 3 : 4) : 6;
+  // CODES: codes and pairs of 64 keys (or values), half a tile, in a ring of
+  // their own for each ring of tiles.
+  static constexpr int kRaw = D == 128 ? (PAIR ? 3 : 6) : 6;
   static constexpr int kRawBytes = 64 * (D / 2 + D / 8);
   static constexpr size_t kTiles =
       kQBytes + (size_t)kTileBytes * (kN0 + kN1) +
@@ -133,6 +135,7 @@ template <int D, bool PAIR, bool CODES> struct Layout {
 template <int D, bool PAIR, bool CODES> struct Shared {
   using L = Layout<D, PAIR, CODES>;
   uint64_t full[2][L::kN0], empty[2][L::kN0];
+  uint64_t raw_full[2][L::kRaw], raw_empty[2][L::kRaw];
   uint64_t q_full[2], s_full[2], turn[2], drain[2];
   uint64_t w_full[2][2], o_full[2][2];  // of a stream's tile halves
   uint64_t idle;  // stream 1 has no tile: its product warp saw the queries
@@ -370,97 +373,94 @@ __device__ __forceinline__ float to_half_row(uint4 &x, bool bf16,
   return f;
 }
 
-// The tiles of ring `me`, as fp16 numbers in the swizzle, made of a 4-bit cache
-// by one warp: it copies codes and pairs of half a tile to a ring of its own,
-// kRaw - 1 halves ahead, and turns a word of codes, eight neighbours, into the
-// 16 bytes of a chunk.  What lies past a sequence's keys becomes zeros.
+// Codes and pairs of the tiles of ring `me`, half a tile at a time, by one
+// warp.
 template <int D, bool PAIR, int ROWS>
-__device__ __forceinline__ void make_tiles(const AttnParams &p,
+__device__ __forceinline__ void load_codes(const AttnParams &p,
                                            Shared<D, PAIR, true> &s,
-                                           char *tiles, int me) {
+                                           char *raw, int me) {
   using L = Layout<D, PAIR, true>;
-  constexpr int W = D / 32;  // words of a key a thread
   constexpr int CODE_BYTES = 32 * D;
   // PAIR: keys or values of every tile; otherwise both of every other tile
   constexpr int STEP = PAIR ? 1 : 2;
   const int lane = threadIdx.x & 31, sb = p.c.scale_bytes;
-  char *ring = tiles + (me ? L::kN0 * L::kTileBytes : 0);
-  char *raw = tiles + (L::kN0 + L::kN1) * L::kTileBytes +
-              me * L::kRaw * L::kRawBytes;
-  // ---- what is fetched next: half fh of the keys, then of the values, of
-  // tile fj
-  Units<ROWS> f(p, s.plan);
-  int fj = 0, fh = 0, fill = 0;
-  long long code = -1, pair = -1;  // of eight keys a lane; negative: none
-  int id = 0;                      // and their page
-  auto look_up = [&] {  // lane: keys 8 (lane % 16) to + 7 of the tile
-    const int key = fj * kTile + 8 * (lane & 15);
-    id = -1;
-    if (key < f.c.kv)
-      id = __ldg(p.block_table + (long long)f.b * p.max_pages +
-                 div_by(key, p.by_page));
-  };
-  auto first_tile = [&] {  // of the ring in a unit; past units without one
-    for (; f.left; f.next()) {
-      fj = f.j0 + (PAIR ? 0 : me);
-      if (fj < f.j1) break;
-    }
-    if (f.left) look_up();
-  };
-  first_tile();
   const uint32_t to = smem_addr(raw) + 16 * lane;
-  const char *k_codes = p.c.k + 16 * (lane & (D / 4 - 1));
-  const char *v_codes = p.c.v + 16 * (lane & (D / 4 - 1));
+  const int chunk = 16 * (lane & (D / 4 - 1));
   const int pair_at = 16 * (lane & (sb / 2 - 1)), pair_8 = lane / (sb / 2);
-  auto fetch = [&] {
-    if (f.left) {
-      const bool values = PAIR ? me : fh >> 1;
-      const int hf = fh & 1;
-      if (fh == 0) {
-        const int key = fj * kTile + 8 * (lane & 15);
-        code = pair = -1;
-        if (id >= 0 && id < p.num_pages) {
-          const int row =
-              (f.h - div_by(key, p.by_page)) * p.page_size + key;
-          code = id * p.c.page_stride + (long long)row * (D / 2);
-          pair = id * p.c.scale_stride + (long long)row * sb;
-        } else if (key < f.c.kv) {
-          s.bad[f.count % kBadRing] = f.count;
-          status_or(p.dev_status, SD_DEV_BAD_PAGE);
+  bool fine = true;
+  RingAt at(L::kRaw);
+  Units<ROWS> u(p, s.plan);
+  for (; u.left && fine; u.next()) {
+    const int32_t *table = p.block_table + (long long)u.b * p.max_pages;
+    const int j0 = u.j0 + (PAIR ? 0 : me);
+    auto look_up = [&](int j) {  // page of keys 8 (lane % 16) to + 7 of tile j
+      const int key = j * kTile + 8 * (lane & 15);
+      return j < u.j1 && key < u.c.kv ? __ldg(table + div_by(key, p.by_page))
+                                      : -1;
+    };
+    int id = look_up(j0);
+    for (int j = j0; j < u.j1 && fine; j += STEP) {
+      const int key = j * kTile + 8 * (lane & 15);
+      long long code = -1, pair = -1;  // negative: none
+      if (id >= 0 && id < p.num_pages) {
+        const int row = (u.h - div_by(key, p.by_page)) * p.page_size + key;
+        code = id * p.c.page_stride + (long long)row * (D / 2);
+        pair = id * p.c.scale_stride + (long long)row * sb;
+      } else if (key < u.c.kv) {
+        s.bad[u.count % kBadRing] = u.count;
+        status_or(p.dev_status, SD_DEV_BAD_PAGE);
+      }
+      id = look_up(j + STEP);
+#pragma unroll 1
+      for (int n = 0; n < (PAIR ? 2 : 4); ++n) {  // halves of keys and values
+        const bool values = PAIR ? me : n >> 1;
+        const int first = 8 * (n & 1);
+        fine = role_wait(&s.raw_empty[me][at.slot], at.parity ^ 1, &s.abort,
+                         p.dev_status);
+        if (!__all_sync(~0u, fine)) {
+          fine = false;
+          break;
         }
-      }
-      const char *from = values ? v_codes : k_codes;
+        const char *from = (values ? p.c.v : p.c.k) + chunk;
+        const uint32_t dst = to + at.slot * L::kRawBytes;
+        long long c[D / 16];
 #pragma unroll
-      for (int o = 0; o < D / 16; ++o) {
-        const long long c = __shfl_sync(
-            ~0u, code, 8 * hf + (D == 128 ? o : 2 * o + (lane >> 4)));
-        cp16(to + fill + 512 * o, from + c, c >= 0);
-      }
-      const char *pairs =
-          (values ? p.c.v_scale : p.c.k_scale) + pair_at;
+        for (int o = 0; o < D / 16; ++o)
+          c[o] = __shfl_sync(
+              ~0u, code, first + (D == 128 ? o : 2 * o + (lane >> 4)));
+        const long long c0 = __shfl_sync(~0u, pair, first + (pair_8 & 7));
+        // 64 / sb lanes hold eight keys' pairs
+        const long long c1 =
+            __shfl_sync(~0u, pair, first + (pair_8 + 64 / sb & 7));
 #pragma unroll
-      for (int o = 0; o < 2; ++o) {  // 64 / sb lanes hold eight keys' pairs
-        const int at = pair_8 + o * (64 / sb);
-        const long long c = __shfl_sync(~0u, pair, 8 * hf + (at & 7));
-        cp16(to + fill + CODE_BYTES + 512 * o, pairs + c, at < 8 && c >= 0);
-      }
-      if (++fh == (PAIR ? 2 : 4)) {
-        fh = 0;
-        fj += STEP;
-        if (fj >= f.j1) {
-          f.next();
-          first_tile();
-        } else {
-          look_up();
-        }
+        for (int o = 0; o < D / 16; ++o)
+          cp16(dst + 512 * o, from + c[o], c[o] >= 0);
+        const char *pairs = (values ? p.c.v_scale : p.c.k_scale) + pair_at;
+        cp16(dst + CODE_BYTES, pairs + c0, pair_8 < 8 && c0 >= 0);
+        cp16(dst + CODE_BYTES + 512, pairs + c1,
+             pair_8 + 64 / sb < 8 && c1 >= 0);
+        cp_arrive(smem_addr(&s.raw_full[me][at.slot]));
+        at.next();
       }
     }
-    cp_commit();
-    fill = fill == (L::kRaw - 1) * L::kRawBytes ? 0 : fill + L::kRawBytes;
-  };
-  for (int i = 0; i < L::kRaw - 1; ++i) fetch();
+  }
+  cp_commit();
+  cp_wait<0>();
+}
 
-  // ---- and what is made of it
+// Half `hf` of the tiles of ring `me`, as fp16 numbers in the swizzle, by one
+// warp: a word of codes, eight neighbours, becomes the 16 bytes of a chunk.
+// What lies past a sequence's keys becomes zeros.
+template <int D, bool PAIR, int ROWS>
+__device__ __forceinline__ void make_tiles(const AttnParams &p,
+                                           Shared<D, PAIR, true> &s,
+                                           char *ring, const char *raw,
+                                           int me, int hf) {
+  using L = Layout<D, PAIR, true>;
+  constexpr int W = D / 32;  // words of a key a thread
+  constexpr int CODE_BYTES = 32 * D;
+  constexpr int STEP = PAIR ? 1 : 2;
+  const int lane = threadIdx.x & 31, sb = p.c.scale_bytes;
   const int row = lane >> 2, t = lane & 3;
   const char *code_from = raw + row * (D / 2) + t * (D / 8);
   const char *pair_from =
@@ -470,69 +470,80 @@ __device__ __forceinline__ void make_tiles(const AttnParams &p,
   // banks for both halves: the second half's take their words in another
   // order.
   const int turn = D == 128 ? t & 2 : 0;
-  char *const tile_at =
-      ring + (D == 128 ? (t >> 1) * (kTile * 128) : 0) + row * 128;
-  int use = 0;
+  char *const tile_at = ring + (D == 128 ? (t >> 1) * (kTile * 128) : 0) +
+                        (64 * hf + row) * 128;
+  int chunk[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+    chunk[i] = (((W * t + (i ^ turn)) & 7) ^ row) * 16;
   bool fine = true;
-  RingAt at(me ? L::kN1 : L::kN0);
+  RingAt at(me ? L::kN1 : L::kN0), from(L::kRaw);
+  if (hf) from.next();
   Units<ROWS> u(p, s.plan);
   for (; u.left && fine; u.next())
     for (int j = u.j0 + (PAIR ? 0 : me); j < u.j1 && fine; j += STEP)
 #pragma unroll 1
-      for (int n = 0; n < (PAIR ? 2 : 4); ++n) {  // halves of keys and values
-        cp_wait<L::kRaw - 2>();
-        __syncwarp();
-        fetch();  // to where the half before this one was
-        if (!(n & 1)) {
-          fine = role_wait(&s.empty[me][at.slot], at.parity ^ 1, &s.abort,
-                           p.dev_status);
-          if (!__all_sync(~0u, fine)) {
-            fine = false;
-            break;
-          }
+      for (int n = 0; n < (PAIR ? 1 : 2); ++n) {  // keys, values
+        fine = role_wait(&s.empty[me][at.slot], at.parity ^ 1, &s.abort,
+                         p.dev_status) &&
+               role_wait(&s.raw_full[me][from.slot], from.parity, &s.abort,
+                         p.dev_status);
+        if (!__all_sync(~0u, fine)) {
+          fine = false;
+          break;
         }
-        char *tile = tile_at + at.slot * L::kTileBytes + (n & 1) * 64 * 128;
-        const int left = u.c.kv - (j * kTile + 64 * (n & 1) + row);
-        // (all loads first: the compiler may not move one past a store)
-        uint32_t w[8][W], x[8];
-#pragma unroll
-        for (int o = 0; o < 8; ++o) {
-          lds_words(code_from + use + o * 8 * (D / 2), w[o]);
-          x[o] = *reinterpret_cast<const uint32_t *>(
-              pair_from + use + o * 8 * sb);
-        }
-#pragma unroll
-        for (int o = 0; o < 8; ++o) {
-          if (8 * o >= left) x[o] = 0;
-          const uint32_t a = both_lo(x[o]), b = both_hi(x[o]);
+        char *tile = tile_at + at.slot * L::kTileBytes;
+        const char *codes = code_from + from.slot * L::kRawBytes;
+        const char *pairs = pair_from + from.slot * L::kRawBytes;
+        const int left = u.c.kv - (j * kTile + 64 * hf + row);
+        // Eight keys at a time, the next ones' words loaded first (the
+        // compiler may not move a load past a store).
+        uint32_t w[2][W], x[2];
+        auto load = [&](int b, int o) {
+          lds_words(codes + o * 8 * (D / 2), w[b]);
+          x[b] = *reinterpret_cast<const uint32_t *>(pairs + o * 8 * sb);
+        };
+        auto make = [&](int k, int o) {
+          if (8 * o >= left) x[k] = 0;
+          const uint32_t a = both_lo(x[k]), b = both_hi(x[k]);
+          uint4 y[W];
 #pragma unroll
           for (int i = 0; i < W; ++i) {
-            const uint32_t word = D == 128 && turn ? w[o][i ^ 2] : w[o][i];
-            const int chunk = ((W * t + (i ^ turn)) & 7) ^ row;
-            uint4 y;
-            y.x = kv4_fma(kv4_codes(word, 0), a, b);
-            y.y = kv4_fma(kv4_codes(word, 1), a, b);
-            y.z = kv4_fma(kv4_codes(word, 2), a, b);
-            y.w = kv4_fma(kv4_codes(word, 3), a, b);
-            *reinterpret_cast<uint4 *>(tile + o * 8 * 128 + chunk * 16) = y;
+            const uint32_t word = D == 128 && turn ? w[k][i ^ 2] : w[k][i];
+            y[i].x = kv4_fma(kv4_codes(word, 0), a, b);
+            y[i].y = kv4_fma(kv4_codes(word, 1), a, b);
+            y[i].z = kv4_fma(kv4_codes(word, 2), a, b);
+            y[i].w = kv4_fma(kv4_codes(word, 3), a, b);
           }
+#pragma unroll
+          for (int i = 0; i < W; ++i)
+            *reinterpret_cast<uint4 *>(tile + o * 8 * 128 + chunk[i]) = y[i];
+        };
+        load(0, 0);
+#pragma unroll 1
+        for (int o = 0; o < 8; o += 2) {
+          load(1, o + 1);
+          make(0, o);
+          if (o < 6) load(0, o + 2);
+          make(1, o + 1);
         }
-        use = use == (L::kRaw - 1) * L::kRawBytes ? 0 : use + L::kRawBytes;
-        if (n & 1) {
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s.full[me][at.slot]);
-          at.next();
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&s.full[me][at.slot]);
+          mbar_arrive(&s.raw_empty[me][from.slot]);
         }
+        at.next();
+        from.next();
+        from.next();
       }
-  cp_wait<0>();
 }
 
 // ------------------------------------------------------------- the kernel
 // T: type of the products.  CODES: the cache is in 4 bits, T is fp16, q and
 // out are of the type that p.bf16 says.
 template <class T, int D, bool PAIR, bool CODES>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+__global__ void __launch_bounds__(attn_threads<CODES>(), 1)
 attention_kernel(const __grid_constant__ AttnParams p,
                  const __grid_constant__ CUtensorMap k_map,
                  const __grid_constant__ CUtensorMap v_map) {
@@ -551,8 +562,13 @@ attention_kernel(const __grid_constant__ AttnParams p,
   if (tid == 0) {
     for (int i = 0; i < 2; ++i)
       for (int k = 0; k < L::kN0; ++k) {
-        mbar_init(&s.full[i][k], 1);
+        mbar_init(&s.full[i][k], CODES ? 2 : 1);
         mbar_init(&s.empty[i][k], PAIR ? 2 : 1);  // the streams that read it
+      }
+    for (int i = 0; i < 2 && CODES; ++i)
+      for (int k = 0; k < L::kRaw; ++k) {
+        mbar_init(&s.raw_full[i][k], 32);
+        mbar_init(&s.raw_empty[i][k], 1);
       }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.q_full[i], PAIR ? 4 : 8);
@@ -584,18 +600,24 @@ attention_kernel(const __grid_constant__ AttnParams p,
   const uint32_t tmem = s.tmem;
   bool fine = true;
 
-  // 384 threads start with 168 registers each; a softmax thread holds much of
-  // a row, a role next to nothing: 256 x 208 + 128 x 88 = 384 x 168
+  // 384 threads start with 168 registers each, 512 with 128; a softmax thread
+  // holds much of a row, a role next to nothing: 256 x 208 + 128 x 88 = 384 x
+  // 168, and 256 x 168 + 256 x 88 = 512 x 128.
   if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  else if (CODES) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
   else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
   // (the branch has to be on the same condition: code that both kinds reach
   // has the smaller number)
   if (warp >= 8) {
-    const bool maker = CODES && (warp == 8 || warp == 11);
+    const bool maker = CODES && (warp == 8 || warp >= 11);
     if constexpr (CODES) {
-      if (maker)
-        make_tiles<D, PAIR, ROWS>(p, s, q_tile + L::kQBytes,
-                                  warp == 8 ? 0 : 1);
+      char *raw = q_tile + L::kQBytes + (L::kN0 + L::kN1) * L::kTileBytes;
+      const int me = warp == 8 || warp == 12 || warp == 13 ? 0 : 1;
+      raw += me * L::kRaw * L::kRawBytes;
+      if (warp == 8 || warp == 11)
+        load_codes<D, PAIR, ROWS>(p, s, raw, me);
+      else if (maker)
+        make_tiles<D, PAIR, ROWS>(p, s, ring[me], raw, me, warp & 1);
     }
     Units<ROWS> u(p, s.plan);
     if (maker) {
@@ -1042,10 +1064,10 @@ attention_kernel(const __grid_constant__ AttnParams p,
       if (tid == 0) status_or(p.dev_status, SD_DEV_BAD_LENGTH);
       const long long lo = (long long)c.start * p.Hq,
                       n = (long long)c.n * p.Hq;
-      for (long long i = tid; i < n * D; i += kAttnThreads)
+      for (long long i = tid; i < n * D; i += attn_threads<CODES>())
         ((uint16_t *)p.out)[lo * D + i] = 0x7fff;  // NaN of either type
       if (p.lse)
-        for (long long i = tid; i < n; i += kAttnThreads)
+        for (long long i = tid; i < n; i += attn_threads<CODES>())
           p.lse[lo + i] = __int_as_float(0x7fc00000);
     }
   }
@@ -1076,7 +1098,7 @@ sd_status launch(AttnParams &p, const CUtensorMap &k_map,
   const unsigned grid = sms < kMaxGrid ? sms : kMaxGrid;
   void *args[] = {&p, const_cast<CUtensorMap *>(&k_map),
                   const_cast<CUtensorMap *>(&v_map)};
-  sd_status st = launch_pdl(kernel, grid, kAttnThreads,
+  sd_status st = launch_pdl(kernel, grid, attn_threads<CODES>(),
                             attn_smem<D, PAIR, CODES>(), s, args);
   if (st != SD_OK) return st;
   if (CODES && p.bf16)

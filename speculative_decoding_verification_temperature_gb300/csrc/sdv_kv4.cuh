@@ -53,6 +53,12 @@ __device__ __forceinline__ void cp16(uint32_t to, const void *from,
       "l"(from), "r"((int)there)
       : "memory");
 }
+// Arrive on `bar` when the copies that this thread has begun are complete.
+__device__ __forceinline__ void cp_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                   bar)
+               : "memory");
+}
 __device__ __forceinline__ void cp_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
