@@ -110,8 +110,8 @@ template <int D, bool PAIR, bool CODES> struct Layout {
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kQBytes = (PAIR ? 2 : 1) * kTileBytes;
   // Two rings of tiles, as many as fit: what is in flight covers the latency
-  // of HBM.  PAIR: ring 0 holds the key tiles, ring 1 the value tiles, read
-  // by both streams.  Otherwise ring st holds stream st's tiles in the order
+  // of HBM.  PAIR and CODES: ring 0 holds the key tiles, ring 1 the value tiles,
+  // read by both streams.  Otherwise ring st holds stream st's tiles in the order
   // it uses them (key, value, key, ...): a ring with one writer and one
   // reader, so that a stream that is ahead never takes a slot's earlier
   // filling for its own.
@@ -137,7 +137,8 @@ template <int D, bool PAIR, bool CODES> struct Shared {
   uint64_t full[2][L::kN0], empty[2][L::kN0];
   uint64_t raw_full[2][L::kRaw], raw_empty[2][L::kRaw];
   uint64_t q_full[2], s_full[2], turn[2], drain[2];
-  uint64_t w_full[2][2], o_full[2][2];  // of a stream's tile halves
+  uint64_t w_full[2][2], o_full[2][2];  // of a stream's tile halves; SPLIT:
+                                        // w_full of its two buffers
   uint64_t idle;  // stream 1 has no tile: its product warp saw the queries
   uint32_t tmem;
   volatile int abort;
@@ -201,12 +202,13 @@ __device__ __forceinline__ void hide32(uint32_t *x, uint32_t seen) {
     if (!(seen >> e & 1)) x[e] = 0xff800000u;
 }
 
-// The largest of a row's 128 scores (of those it sees, where `cuts`).
+// The largest of a row's scores (of those it sees, where `cuts`).
+template <int KEYS>
 __device__ __forceinline__ float row_max(uint32_t s_addr, bool cuts,
                                          const uint32_t *seen) {
   float m = -kInf;
 #pragma unroll
-  for (int c = 0; c < kTile; c += 64) {
+  for (int c = 0; c < KEYS; c += 64) {
     uint32_t x[64];
     tmem_ld32(s_addr + c, x);
     tmem_ld32(s_addr + c + 32, x + 32);
@@ -261,7 +263,8 @@ struct Row {
 // fetched one ahead.  first: nothing is summed yet; parity: of the tile in the
 // stream; w_full, o_full: of the tile's halves.  Tiles that hide scores have a
 // copy of their own: a warp here runs on its scheduler's issue slots.
-template <class T, int D, bool HIDE, bool REST>
+// HALVES = 1: the stream has one half of each tile.
+template <class T, int D, bool HIDE, bool REST, int HALVES>
 __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
                                            uint64_t *w_full, uint64_t *o_full,
                                            bool first, uint32_t parity,
@@ -271,7 +274,7 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
   uint32_t x[2][32];
   tmem_ld32(row.s_addr, x[0]);
 #pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
+  for (int hf = 0; hf < HALVES; ++hf) {
     uint32_t w[kHalf / 2], rest[REST ? kHalf / 2 : 32];
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     float mt = -kInf;
@@ -280,7 +283,7 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
     for (int c = 2 * hf; c < 2 * hf + 2; ++c) {
       uint32_t *xc = x[c & 1];
       tmem_wait_ld();
-      if (c < 3) tmem_ld32(row.s_addr + 32 * (c + 1), x[(c + 1) & 1]);
+      if (c < 2 * HALVES - 1) tmem_ld32(row.s_addr + 32 * (c + 1), x[(c + 1) & 1]);
       if (HIDE) hide32(xc, seen[c]);
       mt = fmaxf(mt, max32(xc));
       weigh32<T, REST>(xc, row.sl, off, w + 16 * (c & 1),
@@ -301,7 +304,10 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
       if (hf || !first) {
         // all sums before this half are complete when the last of them are
         const bool fine =
-            role_wait(&o_full[hf ^ 1], parity ^ (hf ^ 1), abort, dev_status);
+            HALVES == 2
+                ? role_wait(&o_full[hf ^ 1], parity ^ (hf ^ 1), abort,
+                            dev_status)
+                : role_wait(&o_full[0], parity ^ 1, abort, dev_status);
         if (!__all_sync(~0u, fine)) return false;
         tmem_fence_after();
 #pragma unroll 1
@@ -373,16 +379,14 @@ __device__ __forceinline__ float to_half_row(uint4 &x, bool bf16,
   return f;
 }
 
-// Codes and pairs of the tiles of ring `me`, half a tile at a time, by one
-// warp.
+// Codes and pairs of the key tiles (ring 0) or value tiles (1), half a tile at
+// a time, by one warp.
 template <int D, bool PAIR, int ROWS>
 __device__ __forceinline__ void load_codes(const AttnParams &p,
                                            Shared<D, PAIR, true> &s,
                                            char *raw, int me) {
   using L = Layout<D, PAIR, true>;
   constexpr int CODE_BYTES = 32 * D;
-  // PAIR: keys or values of every tile; otherwise both of every other tile
-  constexpr int STEP = PAIR ? 1 : 2;
   const int lane = threadIdx.x & 31, sb = p.c.scale_bytes;
   const uint32_t to = smem_addr(raw) + 16 * lane;
   const int chunk = 16 * (lane & (D / 4 - 1));
@@ -392,14 +396,13 @@ __device__ __forceinline__ void load_codes(const AttnParams &p,
   Units<ROWS> u(p, s.plan);
   for (; u.left && fine; u.next()) {
     const int32_t *table = p.block_table + (long long)u.b * p.max_pages;
-    const int j0 = u.j0 + (PAIR ? 0 : me);
     auto look_up = [&](int j) {  // page of keys 8 (lane % 16) to + 7 of tile j
       const int key = j * kTile + 8 * (lane & 15);
       return j < u.j1 && key < u.c.kv ? __ldg(table + div_by(key, p.by_page))
                                       : -1;
     };
-    int id = look_up(j0);
-    for (int j = j0; j < u.j1 && fine; j += STEP) {
+    int id = look_up(u.j0);
+    for (int j = u.j0; j < u.j1 && fine; ++j) {
       const int key = j * kTile + 8 * (lane & 15);
       long long code = -1, pair = -1;  // negative: none
       if (id >= 0 && id < p.num_pages) {
@@ -410,18 +413,16 @@ __device__ __forceinline__ void load_codes(const AttnParams &p,
         s.bad[u.count % kBadRing] = u.count;
         status_or(p.dev_status, SD_DEV_BAD_PAGE);
       }
-      id = look_up(j + STEP);
+      id = look_up(j + 1);
 #pragma unroll 1
-      for (int n = 0; n < (PAIR ? 2 : 4); ++n) {  // halves of keys and values
-        const bool values = PAIR ? me : n >> 1;
-        const int first = 8 * (n & 1);
+      for (int first = 0; first < 16; first += 8) {  // halves of the tile
         fine = role_wait(&s.raw_empty[me][at.slot], at.parity ^ 1, &s.abort,
                          p.dev_status);
         if (!__all_sync(~0u, fine)) {
           fine = false;
           break;
         }
-        const char *from = (values ? p.c.v : p.c.k) + chunk;
+        const char *from = (me ? p.c.v : p.c.k) + chunk;
         const uint32_t dst = to + at.slot * L::kRawBytes;
         long long c[D / 16];
 #pragma unroll
@@ -435,7 +436,7 @@ __device__ __forceinline__ void load_codes(const AttnParams &p,
 #pragma unroll
         for (int o = 0; o < D / 16; ++o)
           cp16(dst + 512 * o, from + c[o], c[o] >= 0);
-        const char *pairs = (values ? p.c.v_scale : p.c.k_scale) + pair_at;
+        const char *pairs = (me ? p.c.v_scale : p.c.k_scale) + pair_at;
         cp16(dst + CODE_BYTES, pairs + c0, pair_8 < 8 && c0 >= 0);
         cp16(dst + CODE_BYTES + 512, pairs + c1,
              pair_8 + 64 / sb < 8 && c1 >= 0);
@@ -459,7 +460,6 @@ __device__ __forceinline__ void make_tiles(const AttnParams &p,
   using L = Layout<D, PAIR, true>;
   constexpr int W = D / 32;  // words of a key a thread
   constexpr int CODE_BYTES = 32 * D;
-  constexpr int STEP = PAIR ? 1 : 2;
   const int lane = threadIdx.x & 31, sb = p.c.scale_bytes;
   const int row = lane >> 2, t = lane & 3;
   const char *code_from = raw + row * (D / 2) + t * (D / 8);
@@ -481,62 +481,60 @@ __device__ __forceinline__ void make_tiles(const AttnParams &p,
   if (hf) from.next();
   Units<ROWS> u(p, s.plan);
   for (; u.left && fine; u.next())
-    for (int j = u.j0 + (PAIR ? 0 : me); j < u.j1 && fine; j += STEP)
-#pragma unroll 1
-      for (int n = 0; n < (PAIR ? 1 : 2); ++n) {  // keys, values
-        fine = role_wait(&s.empty[me][at.slot], at.parity ^ 1, &s.abort,
-                         p.dev_status) &&
-               role_wait(&s.raw_full[me][from.slot], from.parity, &s.abort,
-                         p.dev_status);
-        if (!__all_sync(~0u, fine)) {
-          fine = false;
-          break;
-        }
-        char *tile = tile_at + at.slot * L::kTileBytes;
-        const char *codes = code_from + from.slot * L::kRawBytes;
-        const char *pairs = pair_from + from.slot * L::kRawBytes;
-        const int left = u.c.kv - (j * kTile + 64 * hf + row);
-        // Eight keys at a time, the next ones' words loaded first (the
-        // compiler may not move a load past a store).
-        uint32_t w[2][W], x[2];
-        auto load = [&](int b, int o) {
-          lds_words(codes + o * 8 * (D / 2), w[b]);
-          x[b] = *reinterpret_cast<const uint32_t *>(pairs + o * 8 * sb);
-        };
-        auto make = [&](int k, int o) {
-          if (8 * o >= left) x[k] = 0;
-          const uint32_t a = both_lo(x[k]), b = both_hi(x[k]);
-          uint4 y[W];
-#pragma unroll
-          for (int i = 0; i < W; ++i) {
-            const uint32_t word = D == 128 && turn ? w[k][i ^ 2] : w[k][i];
-            y[i].x = kv4_fma(kv4_codes(word, 0), a, b);
-            y[i].y = kv4_fma(kv4_codes(word, 1), a, b);
-            y[i].z = kv4_fma(kv4_codes(word, 2), a, b);
-            y[i].w = kv4_fma(kv4_codes(word, 3), a, b);
-          }
-#pragma unroll
-          for (int i = 0; i < W; ++i)
-            *reinterpret_cast<uint4 *>(tile + o * 8 * 128 + chunk[i]) = y[i];
-        };
-        load(0, 0);
-#pragma unroll 1
-        for (int o = 0; o < 8; o += 2) {
-          load(1, o + 1);
-          make(0, o);
-          if (o < 6) load(0, o + 2);
-          make(1, o + 1);
-        }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&s.full[me][at.slot]);
-          mbar_arrive(&s.raw_empty[me][from.slot]);
-        }
-        at.next();
-        from.next();
-        from.next();
+    for (int j = u.j0; j < u.j1; ++j) {
+      fine = role_wait(&s.empty[me][at.slot], at.parity ^ 1, &s.abort,
+                       p.dev_status) &&
+             role_wait(&s.raw_full[me][from.slot], from.parity, &s.abort,
+                       p.dev_status);
+      if (!__all_sync(~0u, fine)) {
+        fine = false;
+        break;
       }
+      char *tile = tile_at + at.slot * L::kTileBytes;
+      const char *codes = code_from + from.slot * L::kRawBytes;
+      const char *pairs = pair_from + from.slot * L::kRawBytes;
+      const int left = u.c.kv - (j * kTile + 64 * hf + row);
+      // Eight keys at a time, the next ones' words loaded first (the
+      // compiler may not move a load past a store).
+      uint32_t w[2][W], x[2];
+      auto load = [&](int b, int o) {
+        lds_words(codes + o * 8 * (D / 2), w[b]);
+        x[b] = *reinterpret_cast<const uint32_t *>(pairs + o * 8 * sb);
+      };
+      auto make = [&](int k, int o) {
+        if (8 * o >= left) x[k] = 0;
+        const uint32_t a = both_lo(x[k]), b = both_hi(x[k]);
+        uint4 y[W];
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          const uint32_t word = D == 128 && turn ? w[k][i ^ 2] : w[k][i];
+          y[i].x = kv4_fma(kv4_codes(word, 0), a, b);
+          y[i].y = kv4_fma(kv4_codes(word, 1), a, b);
+          y[i].z = kv4_fma(kv4_codes(word, 2), a, b);
+          y[i].w = kv4_fma(kv4_codes(word, 3), a, b);
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+          *reinterpret_cast<uint4 *>(tile + o * 8 * 128 + chunk[i]) = y[i];
+      };
+      load(0, 0);
+#pragma unroll 1
+      for (int o = 0; o < 8; o += 2) {
+        load(1, o + 1);
+        make(0, o);
+        if (o < 6) load(0, o + 2);
+        make(1, o + 1);
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&s.full[me][at.slot]);
+        mbar_arrive(&s.raw_empty[me][from.slot]);
+      }
+      at.next();
+      from.next();
+      from.next();
+    }
 }
 
 // ------------------------------------------------------------- the kernel
@@ -550,6 +548,9 @@ attention_kernel(const __grid_constant__ AttnParams p,
   using L = Layout<D, PAIR, CODES>;
   constexpr int ROWS = L::kRows;
   constexpr bool REST = !PAIR && !CODES;
+  // Up to 128 rows over a 4-bit cache: both streams have every key tile, half
+  // of its keys each, and the next tile's scores are made meanwhile.
+  constexpr bool SPLIT = CODES && !PAIR;
   constexpr bool BF16 = sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value;
   extern __shared__ __align__(1024) char dyn[];  // swizzled tiles first
   using S = Shared<D, PAIR, CODES>;
@@ -680,6 +681,76 @@ attention_kernel(const __grid_constant__ AttnParams p,
             for (unsigned it = 0; it < (1u << 20); ++it)
               if (mbar_try_wait(&s.full[me][i], last & 1)) break;
           }
+      }
+    } else if constexpr (SPLIT) {
+      // ---- tensor-core products, all by one warp: the next tile's scores go
+      // out before this one's weights are waited for.  Products run in the
+      // order issued, so a buffer's scores are made after the values of the
+      // tile before last, whose weights it held.
+      constexpr uint32_t S_DESC = umma_idesc(BF16, false, kTile, kTile);
+      constexpr uint32_t O_DESC = umma_idesc(BF16, true, kTile, D);
+      constexpr uint32_t HI = umma_desc_hi(1024);
+      const uint32_t q_lo = umma_desc_lo(q_tile, 16);
+      const uint32_t k_lo = umma_desc_lo(ring[0], 16);
+      const uint32_t v_lo = umma_desc_lo(ring[1], kTile * 128);
+      RingAt k_at(L::kN0), v_at(L::kN1);
+      uint32_t qp = 0, wp = 0, buf = 0;
+      auto wait = [&](uint64_t *bar, uint32_t parity) {
+        fine = fine && role_wait(bar, parity, &s.abort, p.dev_status);
+      };
+      auto scores = [&](uint32_t to) {
+        wait(&s.full[0][k_at.slot], k_at.parity);
+        if (elect_one() && fine) {
+          const uint32_t b = k_lo + k_at.slot * (L::kTileBytes / 16);
+          tmem_fence_after();
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const int at = ((i / 4) * (kTile * 128) + (i % 4) * 32) / 16;
+            umma_ss<HI>(tmem + to * kTile, q_lo + at, b + at, S_DESC, i > 0);
+          }
+          umma_commit(&s.s_full[to]);
+          umma_commit(&s.empty[0][k_at.slot]);
+        }
+        __syncwarp();
+        k_at.next();
+      };
+      if (warp == kMmaWarp) {
+        for (; u.left; u.next()) {
+          const int cnt = u.j1 - u.j0;
+          wait(&s.q_full[0], qp);
+          qp ^= 1;
+          scores(buf);
+          for (int i = 0; i < cnt; ++i) {
+            if (i + 1 < cnt) scores(buf ^ 1);
+            wait(&s.full[1][v_at.slot], v_at.parity);
+            for (int st = 0; st < 2; ++st) {
+              wait(&s.w_full[st][buf], wp >> buf & 1);
+              if (elect_one() && fine) {
+                const uint32_t b = v_lo + v_at.slot * (L::kTileBytes / 16) +
+                                   st * (kHalf * 128 / 16);
+                const uint32_t w = tmem + buf * kTile + st * kHalf;
+                tmem_fence_after();
+#pragma unroll
+                for (int k = 0; k < kHalf / 16; ++k)
+                  umma_ts<HI>(tmem + 2 * kTile + st * D, w + k * 8,
+                              b + k * 16 * 128 / 16, O_DESC, i > 0 || k > 0);
+                umma_commit(&s.o_full[st][0]);
+                if (st) umma_commit(&s.empty[1][v_at.slot]);
+              }
+              __syncwarp();
+            }
+            wp ^= 1u << buf;  // (weights may be a buffer ahead of this)
+            v_at.next();
+            buf ^= 1;
+          }
+        }
+        if (__any_sync(~0u, !fine)) {
+          // tensor memory is freed below: let products in flight end
+          if (elect_one()) umma_commit(&s.drain[0]);
+          __syncwarp();
+          for (unsigned it = 0; it < (1u << 20); ++it)
+            if (mbar_try_wait(&s.drain[0], 0)) break;
+        }
       }
     } else {
       // ---- tensor-core products of stream st, a warp each: while one is held
@@ -913,8 +984,9 @@ attention_kernel(const __grid_constant__ AttnParams p,
         }
       }
       const int cnt_all = u.j1 - u.j0;
-      const int cnt =
-          !active(u) ? 0 : PAIR ? cnt_all : (cnt_all - st + 1) / 2;
+      const int cnt = !active(u)        ? 0
+                      : PAIR || SPLIT ? cnt_all
+                                      : (cnt_all - st + 1) / 2;
       const int row_at = u.t * ROWS + base_row + r;
       const bool mine = base_row + r < u.rows;
       const bool warp_rows = base_row + (warp & 3) * 32 < u.rows;
@@ -923,34 +995,40 @@ attention_kernel(const __grid_constant__ AttnParams p,
       Row row = {tmem + lanes + st * kTile,
                  tmem + lanes + 2 * kTile + st * D, sl, -kInf, 0.f};
       for (int i = 0; i < cnt; ++i, ++tn) {
-        const int j = u.j0 + (PAIR ? i : 2 * i + st);
-        fine = role_wait(&s.s_full[st], tn & 1, &s.abort, p.dev_status);
+        // SPLIT: tiles alternate between two buffers of scores
+        const int j = u.j0 + (PAIR || SPLIT ? i : 2 * i + st);
+        const int buf = SPLIT ? tn & 1 : st;
+        fine = role_wait(&s.s_full[buf], (SPLIT ? tn >> 1 : tn) & 1, &s.abort,
+                         p.dev_status);
         if (!__all_sync(~0u, fine)) { fine = false; break; }
+        constexpr int KEYS = SPLIT ? kHalf : kTile, HALVES = SPLIT ? 1 : 2;
+        if (SPLIT) row.s_addr = tmem + lanes + buf * kTile + st * kHalf;
         if (warp_rows) {
           tmem_fence_after();
           // only tiles past the row's last key hide anything
-          const int key = j * kTile;
+          const int key = j * kTile + (SPLIT ? st * kHalf : 0);
           const bool cuts = __any_sync(
-              ~0u, key + kTile - 1 > (p.mask ? ctx - 1 : limit));
-          uint32_t seen[kTile / 32] = {};
+              ~0u, key + KEYS - 1 > (p.mask ? ctx - 1 : limit));
+          uint32_t seen[KEYS / 32] = {};
           if (cuts) {
 #pragma unroll
-            for (int c = 0; c < kTile / 32; ++c)
+            for (int c = 0; c < KEYS / 32; ++c)
               seen[c] =
                   mine ? seen_bits(p, u.c, token, limit, key + 32 * c) : 0;
           }
           __syncwarp();
-          if (i == 0) row.m = row_max(row.s_addr, cuts, seen);
-          fine = cuts ? weigh_tile<T, D, true, REST>(row, seen, s.w_full[st],
-                                               s.o_full[st], i == 0, tn & 1,
-                                               &s.abort, p.dev_status)
-                      : weigh_tile<T, D, false, REST>(row, seen, s.w_full[st],
-                                                s.o_full[st], i == 0, tn & 1,
-                                                &s.abort, p.dev_status);
+          if (i == 0) row.m = row_max<KEYS>(row.s_addr, cuts, seen);
+          uint64_t *w_full = &s.w_full[st][SPLIT ? buf : 0];
+          fine = cuts ? weigh_tile<T, D, true, REST, HALVES>(
+                            row, seen, w_full, s.o_full[st], i == 0,
+                            tn & 1, &s.abort, p.dev_status)
+                      : weigh_tile<T, D, false, REST, HALVES>(
+                            row, seen, w_full, s.o_full[st], i == 0,
+                            tn & 1, &s.abort, p.dev_status);
           if (!fine) break;
         } else if (lane == 0) {
-          mbar_arrive(&s.w_full[st][0]);
-          mbar_arrive(&s.w_full[st][1]);
+          mbar_arrive(&s.w_full[st][SPLIT ? buf : 0]);
+          if (!SPLIT) mbar_arrive(&s.w_full[st][1]);
         }
       }
       // ---- the end of the unit.  The last scores are out, so the next
@@ -958,7 +1036,8 @@ attention_kernel(const __grid_constant__ AttnParams p,
       // way while this one's rows are written
       if (PAIR && next.left) load_q(next);
       if (cnt > 0) {
-        role_wait(&s.o_full[st][1], (tn - 1) & 1, &s.abort, p.dev_status);
+        role_wait(&s.o_full[st][SPLIT ? 0 : 1], (tn - 1) & 1, &s.abort,
+                  p.dev_status);
         __syncwarp();
         tmem_fence_after();
       } else if (!PAIR) {
@@ -993,7 +1072,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
       const int c_lo = PAIR ? 0 : st * (D / 2), c_n = PAIR ? D : D / 2;
       const uint32_t o_addr =
           tmem + lanes + 2 * kTile + (PAIR ? st * D : 0) + c_lo;
-      const bool second = !PAIR && cnt_all > 1;
+      const bool second = !PAIR && (SPLIT || cnt_all > 1);
       if (warp_rows) {
         const long long to = (long long)(u.c.start + token) * p.Hq +
                              u.h * p.G + (mine ? row_at - token * p.G : 0);
