@@ -462,17 +462,20 @@ __device__ __forceinline__ void make_tiles(const AttnParams &p,
   constexpr int CODE_BYTES = 32 * D;
   const int lane = threadIdx.x & 31, sb = p.c.scale_bytes;
   const int row = lane >> 2, t = lane & 3;
-  const char *code_from = raw + row * (D / 2) + t * (D / 8);
-  const char *pair_from =
-      raw + CODE_BYTES + row * sb + 4 * ((t * (D / 4)) >> p.c.shift);
   // Chunk i of the thread's W is the (W t + i)-th of the row, eight to a
   // column half.  A store's threads, two rows of four, would meet the same
   // banks for both halves: the second half's take their words in another
-  // order.
+  // order.  (Addresses of shared memory as such: a pointer that may be to
+  // either ring would be a generic one.)
   const int turn = D == 128 ? t & 2 : 0;
-  char *const tile_at = ring + (D == 128 ? (t >> 1) * (kTile * 128) : 0) +
-                        (64 * hf + row) * 128;
-  int chunk[W];
+  const uint32_t code_from =
+      smem_addr(raw) + row * (D / 2) + t * (D / 8) + 4 * turn;
+  const uint32_t pair_from = smem_addr(raw) + CODE_BYTES + row * sb +
+                             4 * ((t * (D / 4)) >> p.c.shift);
+  const uint32_t tile_at = smem_addr(ring) +
+                           (D == 128 ? (t >> 1) * (kTile * 128) : 0) +
+                           (64 * hf + row) * 128;
+  uint32_t chunk[W];
 #pragma unroll
   for (int i = 0; i < W; ++i)
     chunk[i] = (((W * t + (i ^ turn)) & 7) ^ row) * 16;
@@ -490,16 +493,18 @@ __device__ __forceinline__ void make_tiles(const AttnParams &p,
         fine = false;
         break;
       }
-      char *tile = tile_at + at.slot * L::kTileBytes;
-      const char *codes = code_from + from.slot * L::kRawBytes;
-      const char *pairs = pair_from + from.slot * L::kRawBytes;
+      const uint32_t tile = tile_at + at.slot * L::kTileBytes;
+      const uint32_t codes = code_from + from.slot * L::kRawBytes;
+      const uint32_t pairs = pair_from + from.slot * L::kRawBytes;
       const int left = u.c.kv - (j * kTile + 64 * hf + row);
       // Eight keys at a time, the next ones' words loaded first (the
       // compiler may not move a load past a store).
       uint32_t w[2][W], x[2];
       auto load = [&](int b, int o) {
-        lds_words(codes + o * 8 * (D / 2), w[b]);
-        x[b] = *reinterpret_cast<const uint32_t *>(pairs + o * 8 * sb);
+        const uint32_t at = codes + o * 8 * (D / 2);
+        lds_pair(at, w[b]);
+        if (D == 128) lds_pair(at + 8 - 8 * turn, w[b] + W - 2);
+        x[b] = lds_word(pairs + o * 8 * sb);
       };
       auto make = [&](int k, int o) {
         if (8 * o >= left) x[k] = 0;
@@ -507,15 +512,14 @@ __device__ __forceinline__ void make_tiles(const AttnParams &p,
         uint4 y[W];
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-          const uint32_t word = D == 128 && turn ? w[k][i ^ 2] : w[k][i];
-          y[i].x = kv4_fma(kv4_codes(word, 0), a, b);
-          y[i].y = kv4_fma(kv4_codes(word, 1), a, b);
-          y[i].z = kv4_fma(kv4_codes(word, 2), a, b);
-          y[i].w = kv4_fma(kv4_codes(word, 3), a, b);
+          y[i].x = kv4_fma(kv4_codes(w[k][i], 0), a, b);
+          y[i].y = kv4_fma(kv4_codes(w[k][i], 1), a, b);
+          y[i].z = kv4_fma(kv4_codes(w[k][i], 2), a, b);
+          y[i].w = kv4_fma(kv4_codes(w[k][i], 3), a, b);
         }
 #pragma unroll
         for (int i = 0; i < W; ++i)
-          *reinterpret_cast<uint4 *>(tile + o * 8 * 128 + chunk[i]) = y[i];
+          sts_v4(tile + o * 8 * 128 + chunk[i], y[i]);
       };
       load(0, 0);
 #pragma unroll 1

@@ -66,6 +66,23 @@ template <int N> __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Shared memory by its own addresses.
+__device__ __forceinline__ uint32_t lds_word(uint32_t at) {
+  uint32_t x;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
+__device__ __forceinline__ void lds_pair(uint32_t at, uint32_t *x) {
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+               : "=r"(x[0]), "=r"(x[1])
+               : "r"(at)
+               : "memory");
+}
+__device__ __forceinline__ void sts_v4(uint32_t at, uint4 x) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x.x),
+               "r"(x.y), "r"(x.z), "r"(x.w)
+               : "memory");
+}
 // A thread's share of a key's row: N words of shared memory.
 template <int N>
 __device__ __forceinline__ void lds_words(const char *p, uint32_t (&w)[N]) {
