@@ -20,7 +20,9 @@ struct Append4Params {
   int max_pos, rot, interleaved;
   int B, total, Hq, Hkv;
   int page_size, max_pages;
+  FastDiv by_page;
   Kv4Cache c;
+  bool angles_wide;  // cos_sin can be read 16 bytes at a time
   void *q_out;
   int32_t *dev_status;
 };
@@ -50,11 +52,11 @@ __device__ __forceinline__ Place place_row(const P &p, int row) {
     return r;
   }
   r.pos = c.kv - c.n + (row - c.start);
-  const int page =
-      __ldg(p.block_table + (long long)b * p.max_pages + r.pos / p.page_size);
+  const int n = div_by(r.pos, p.by_page);
+  const int page = __ldg(p.block_table + (long long)b * p.max_pages + n);
   if (page < 0 || page >= p.c.num_pages) r.st = SD_DEV_BAD_PAGE;
   else r.page = page;
-  r.token = r.pos % p.page_size;
+  r.token = r.pos - n * p.page_size;
   return r;
 }
 
@@ -78,27 +80,34 @@ template <> __device__ __forceinline__ uint32_t pack2<__half>(float2 x) {
 }
 
 // min and max that keep a NaN.
-__device__ __forceinline__ float min_nan(float a, float b) {
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
   float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  return __fmul2_rn(a, b);
 }
 
 // Codes of eight neighbours, one word, and their group's pair; `lanes`
 // neighbouring lanes hold a group.  The whole warp calls.
-__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], int lanes,
+__device__ __forceinline__ uint32_t quantise8(const float2 (&x)[4], int lanes,
                                               uint32_t &pair) {
-  float lo = x[0], hi = x[0];
-#pragma unroll
-  for (int e = 1; e < 8; ++e) lo = min_nan(lo, x[e]), hi = max_nan(hi, x[e]);
+  float lo = min_nan(x[0].x, x[0].y, x[1].x), hi = max_nan(x[0].x, x[0].y,
+                                                           x[1].x);
+  lo = min_nan(lo, x[1].y, x[2].x), hi = max_nan(hi, x[1].y, x[2].x);
+  lo = min_nan(lo, x[2].y, x[3].x), hi = max_nan(hi, x[2].y, x[3].x);
+  lo = min_nan(lo, x[3].y, x[3].y), hi = max_nan(hi, x[3].y, x[3].y);
   for (int d = 1; d < lanes; d <<= 1) {
-    lo = min_nan(lo, __shfl_xor_sync(~0u, lo, d));
-    hi = max_nan(hi, __shfl_xor_sync(~0u, hi, d));
+    const float a = __shfl_xor_sync(~0u, lo, d);
+    const float b = __shfl_xor_sync(~0u, hi, d);
+    lo = min_nan(lo, a, a);
+    hi = max_nan(hi, b, b);
   }
   if (!(lo > -kInf && hi < kInf)) {  // a group that holds NaN or infinity
     pair = 0x7e007e00u;
@@ -111,58 +120,54 @@ __device__ __forceinline__ uint32_t quantise8(const float (&x)[8], int lanes,
   const __half b = __float2half_rn(__fsub_rn(lo, 64.f * af));
   const float bf = __half2float(b);
   const float inv = af > 0.f ? __frcp_rn(af) : 0.f;
-  uint32_t w = 0;
+  // 1.5 x 2^23 + t is t rounded to a whole number, in the low bits: added up
+  // with their shifts, what lies above the codes is a constant modulo 2^32
+  const float2 minus_b = make_float2(-bf, -bf), inv2 = make_float2(inv, inv);
+  const float2 magic = make_float2(12582912.f, 12582912.f);
+  uint32_t w = 0u - (0x4b400000u + 64) * 0x11111111u;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    float t = __fmul_rn(__fsub_rn(x[e], bf), inv);
-    t = fminf(fmaxf(t, 64.f), 79.f);
-    // 1.5 x 2^23 + t: t rounded to a whole number, its low bits the code
-    const uint32_t n = __float_as_uint(__fadd_rn(t, 12582912.f)) & 15;
-    w |= n << 4 * ((e & 1) * 4 + e / 2);
+  for (int e = 0; e < 4; ++e) {
+    float2 t = mul2(add2(x[e], minus_b), inv2);
+    t.x = fminf(fmaxf(t.x, 64.f), 79.f);
+    t.y = fminf(fmaxf(t.y, 64.f), 79.f);
+    t = add2(t, magic);
+    w += __float_as_uint(t.x) << 4 * e;
+    w += __float_as_uint(t.y) << 4 * (e + 4);
   }
   pair = (uint32_t)__half_as_ushort(b) << 16 | __half_as_ushort(a);
   return w;
 }
 
+// Eight neighbours of a head, and the elements they are turned with.
+struct Piece {
+  uint4 own, other;
+};
+
 // A CTA per packed row; a thread takes eight neighbours of every (threads /
-// pieces)-th head, and the elements they are turned with: its own (WIDE,
-// interleaved), or a piece rot_dim / 2 away.  WIDE: rot_dim is a multiple of
-// 16 and rows are 16-byte aligned, so that pieces are whole 16-byte loads and
-// turn as a whole; otherwise elements are loaded one by one.
-constexpr int kAhead4 = 2;
+// pieces)-th head, so that it reads its cosines and sines once.  Queries first,
+// which are only turned, then keys and values; a thread's first pieces of both
+// are on their way before it looks for the row's place.  WIDE: rot_dim is a
+// multiple of 16 and rows are 16-byte aligned, so that pieces are whole 16-byte
+// loads and turn as a whole; otherwise elements are loaded one by one.
 template <class T, int D, bool WIDE>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 append4_kernel(const __grid_constant__ Append4Params p) {
   griddep_wait();
   constexpr int PER = D / 8;
   const int row = blockIdx.x, i = threadIdx.x % PER;
   const int first = threadIdx.x / PER, step = blockDim.x / PER;
-  const int heads = p.Hq + 2 * p.Hkv, half = p.rot / 2;
-  // element (or piece's first element) e is turned with other(e), by angle(e)
+  const int half = p.rot / 2;
+  // element (or piece's first element) e is turned with other(e)
   auto other = [&](int e) {
     return p.interleaved ? e ^ 1 : e < half ? e + half : e - half;
   };
   const bool turns = 8 * i < p.rot;
-  const bool fetch = turns && !p.interleaved;
-  struct Piece {
-    uint4 own, other;
-  };
-  auto src_of = [&](int h) {
-    if (h < p.Hq) return (const T *)p.q + row * p.q_stride + (long long)h * D;
-    h -= p.Hq;
-    if (h < p.Hkv)
-      return (const T *)p.k + row * p.k_stride + (long long)h * D;
-    return (const T *)p.v + row * p.v_stride + (long long)(h - p.Hkv) * D;
-  };
-  auto load = [&](int h) {
+  auto load = [&](const T *src, bool turned) {
     Piece x;
-    x.own = x.other = make_uint4(0, 0, 0, 0);
-    if (h >= heads) return x;
-    const T *src = src_of(h);
-    const bool turned = h < p.Hq + p.Hkv;
     if (WIDE) {
       x.own = ld_nc_v4(src + 8 * i);
-      if (fetch && turned) x.other = ld_nc_v4(src + other(8 * i));
+      x.other = x.own;
+      if (turned && !p.interleaved) x.other = ld_nc_v4(src + other(8 * i));
     } else {
       T own[8], oth[8];
 #pragma unroll
@@ -176,9 +181,22 @@ append4_kernel(const __grid_constant__ Append4Params p) {
     }
     return x;
   };
-  Piece ahead[kAhead4];
-#pragma unroll
-  for (int n = 0; n < kAhead4; ++n) ahead[n] = load(first + n * step);
+  auto load_q = [&](int h) {
+    Piece x{};
+    if (h < p.Hq)
+      x = load((const T *)p.q + row * p.q_stride + (long long)h * D, turns);
+    return x;
+  };
+  auto load_kv = [&](int h) {  // keys, then values
+    Piece x{};
+    if (h < p.Hkv)
+      x = load((const T *)p.k + row * p.k_stride + (long long)h * D, turns);
+    else if (h < 2 * p.Hkv)
+      x = load((const T *)p.v + row * p.v_stride + (long long)(h - p.Hkv) * D,
+               false);
+    return x;
+  };
+  Piece q = load_q(first), kv = load_kv(first);
   Place pl = place_row(p, row);
   if (pl.st == 0 && pl.owned && p.cos_sin) {
     if (p.positions) pl.pos = __ldg(p.positions + row);
@@ -190,88 +208,109 @@ append4_kernel(const __grid_constant__ Append4Params p) {
   if (threadIdx.x == 0) status_or(p.dev_status, pl.st);
   if (!pl.owned) return;
   // x' = x c + x_other s: the sine of the first of a pair is negative
-  float c[8], s[8];
+  float2 c[4], s[4];
+  const float *cs = p.cos_sin + (long long)pl.pos * p.rot;
+  if (WIDE && turns && pl.page >= 0 && p.angles_wide) {
+    const bool head = 8 * i < half;
+    const int angle = p.interleaved ? 4 * i : head ? 8 * i : 8 * i - half;
+    float4 a = __ldg(reinterpret_cast<const float4 *>(cs + angle));
+    float4 b = __ldg(reinterpret_cast<const float4 *>(cs + half + angle));
+    if (p.interleaved) {
+      c[0] = make_float2(a.x, a.x), s[0] = make_float2(-b.x, b.x);
+      c[1] = make_float2(a.y, a.y), s[1] = make_float2(-b.y, b.y);
+      c[2] = make_float2(a.z, a.z), s[2] = make_float2(-b.z, b.z);
+      c[3] = make_float2(a.w, a.w), s[3] = make_float2(-b.w, b.w);
+    } else {
+      const float4 u =
+          __ldg(reinterpret_cast<const float4 *>(cs + angle + 4));
+      const float4 v =
+          __ldg(reinterpret_cast<const float4 *>(cs + half + angle + 4));
+      const float k = head ? -1.f : 1.f;
+      c[0] = make_float2(a.x, a.y), s[0] = make_float2(k * b.x, k * b.y);
+      c[1] = make_float2(a.z, a.w), s[1] = make_float2(k * b.z, k * b.w);
+      c[2] = make_float2(u.x, u.y), s[2] = make_float2(k * v.x, k * v.y);
+      c[3] = make_float2(u.z, u.w), s[3] = make_float2(k * v.z, k * v.w);
+    }
+  } else {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int at = 8 * i + e;
-    c[e] = 1.f, s[e] = 0.f;
-    if (at < p.rot && pl.page >= 0) {
-      const bool head = p.interleaved ? !(at & 1) : at < half;
-      const int angle = p.interleaved ? at / 2 : head ? at : at - half;
-      const float *cs = p.cos_sin + (long long)pl.pos * p.rot + angle;
-      c[e] = __ldg(cs);
-      s[e] = head ? -__ldg(cs + half) : __ldg(cs + half);
+    for (int e = 0; e < 8; ++e) {
+      const int at = 8 * i + e;
+      float x = 1.f, y = 0.f;
+      if (at < p.rot && pl.page >= 0) {
+        const bool head = p.interleaved ? !(at & 1) : at < half;
+        const int angle = p.interleaved ? at / 2 : head ? at : at - half;
+        x = __ldg(cs + angle);
+        y = head ? -__ldg(cs + half + angle) : __ldg(cs + half + angle);
+      }
+      if (e & 1) c[e / 2].y = x, s[e / 2].y = y;
+      else c[e / 2].x = x, s[e / 2].x = y;
     }
   }
-  const int lanes = 1 << (p.c.shift - 3);
-  auto put = [&](int h, const Piece &in) {
-    const bool is_q = h < p.Hq, turned = h < p.Hq + p.Hkv;
+  auto turn = [&](const Piece &in, bool turned, float2 (&x)[4]) {
     const uint32_t own[4] = {in.own.x, in.own.y, in.own.z, in.own.w};
     const uint32_t oth[4] = {in.other.x, in.other.y, in.other.z, in.other.w};
-    float x[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float2 u = unpack2<T>(own[e]);
-      x[2 * e] = u.x, x[2 * e + 1] = u.y;
-      if (turned && turns) {
-        float2 v = unpack2<T>(oth[e]);
-        if (WIDE && p.interleaved) v = make_float2(u.y, u.x);
-        const float y0 = __fadd_rn(__fmul_rn(u.x, c[2 * e]),
-                                   __fmul_rn(v.x, s[2 * e]));
-        const float y1 = __fadd_rn(__fmul_rn(u.y, c[2 * e + 1]),
-                                   __fmul_rn(v.y, s[2 * e + 1]));
-        // (an odd piece may end its turn in the middle)
-        if (WIDE || 8 * i + 2 * e < p.rot) x[2 * e] = y0;
-        if (WIDE || 8 * i + 2 * e + 1 < p.rot) x[2 * e + 1] = y1;
-      }
-    }
-    uint32_t pair;
-    const uint32_t word = quantise8(x, lanes, pair);  // the whole warp
-    if (h >= heads) return;
-    if (is_q) {
-      T *to = (T *)p.q_out + ((long long)row * p.Hq + h) * D + 8 * i;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (pl.page >= 0) {
-        w.x = pack2<T>(make_float2(x[0], x[1]));
-        w.y = pack2<T>(make_float2(x[2], x[3]));
-        w.z = pack2<T>(make_float2(x[4], x[5]));
-        w.w = pack2<T>(make_float2(x[6], x[7]));
-      }
-      if (WIDE) {
-        *reinterpret_cast<uint4 *>(to) = w;
-      } else {
-        const T *y = reinterpret_cast<const T *>(&w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) to[e] = y[e];
-      }
-    } else if (pl.page >= 0) {
-      const bool is_k = turned;
-      const int kh = h - p.Hq - (is_k ? 0 : p.Hkv);
-      const long long at = (long long)kh * p.page_size + pl.token;
-      char *codes = const_cast<char *>(is_k ? p.c.k : p.c.v) +
-                    pl.page * p.c.page_stride + at * (D / 2);
-      char *pairs = const_cast<char *>(is_k ? p.c.k_scale : p.c.v_scale) +
-                    pl.page * p.c.scale_stride + at * p.c.scale_bytes;
-      reinterpret_cast<uint32_t *>(codes)[i] = word;
-      if ((i & (lanes - 1)) == 0)
-        reinterpret_cast<uint32_t *>(pairs)[8 * i >> p.c.shift] = pair;
+      x[e] = unpack2<T>(own[e]);
+      if (!turned) continue;
+      const float2 v = WIDE && p.interleaved ? make_float2(x[e].y, x[e].x)
+                                             : unpack2<T>(oth[e]);
+      const float2 y = add2(mul2(x[e], c[e]), mul2(v, s[e]));
+      // (an odd piece may end its turn in the middle)
+      if (WIDE || 8 * i + 2 * e < p.rot) x[e].x = y.x;
+      if (WIDE || 8 * i + 2 * e + 1 < p.rot) x[e].y = y.y;
     }
   };
-  // every thread of a warp makes the same rounds
-  for (int h0 = 0; h0 < heads; h0 += kAhead4 * step) {
-#pragma unroll
-    for (int n = 0; n < kAhead4; ++n) {
-      const Piece now = ahead[n];
-      const int h = h0 + first + n * step;
-      if (h0 + (n + kAhead4) * step < heads) ahead[n] = load(h + kAhead4 * step);
-      put(h, now);
+  for (int h = first; h < p.Hq; h += step) {
+    const Piece now = q;
+    q = load_q(h + step);
+    float2 x[4];
+    turn(now, turns, x);
+    T *to = (T *)p.q_out + ((long long)row * p.Hq + h) * D + 8 * i;
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (pl.page >= 0) {
+      w.x = pack2<T>(x[0]);
+      w.y = pack2<T>(x[1]);
+      w.z = pack2<T>(x[2]);
+      w.w = pack2<T>(x[3]);
     }
+    if (WIDE) {
+      *reinterpret_cast<uint4 *>(to) = w;
+    } else {
+      const T *y = reinterpret_cast<const T *>(&w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) to[e] = y[e];
+    }
+  }
+  if (pl.page < 0) return;  // the whole CTA
+  const int lanes = 1 << (p.c.shift - 3);
+  // every thread of a warp makes the same rounds
+  for (int h0 = 0; h0 < 2 * p.Hkv; h0 += step) {
+    const int h = h0 + first;
+    const Piece now = kv;
+    if (h0 + step < 2 * p.Hkv) kv = load_kv(h + step);
+    const bool is_k = h < p.Hkv;
+    float2 x[4];
+    turn(now, turns && is_k, x);
+    uint32_t pair;
+    const uint32_t word = quantise8(x, lanes, pair);  // the whole warp
+    if (h >= 2 * p.Hkv) continue;
+    const long long at =
+        (long long)(is_k ? h : h - p.Hkv) * p.page_size + pl.token;
+    char *codes = const_cast<char *>(is_k ? p.c.k : p.c.v) +
+                  pl.page * p.c.page_stride + at * (D / 2);
+    char *pairs = const_cast<char *>(is_k ? p.c.k_scale : p.c.v_scale) +
+                  pl.page * p.c.scale_stride + at * p.c.scale_bytes;
+    reinterpret_cast<uint32_t *>(codes)[i] = word;
+    if ((i & (lanes - 1)) == 0)
+      reinterpret_cast<uint32_t *>(pairs)[8 * i >> p.c.shift] = pair;
   }
 }
 
 struct Read4Params {
   const int32_t *q_start, *kv_len, *block_table;
   int B, total, Hkv, page_size, max_pages;
+  FastDiv by_page;
   Kv4Cache c;
   void *k_out, *v_out;
   long long k_stride, v_stride;
@@ -405,8 +444,10 @@ extern "C" sd_status sd_kv4_append(
   p.Hq = Hq;
   p.Hkv = cache->heads;
   p.page_size = cache->page_size;
+  p.by_page = fast_div(cache->page_size);
   p.max_pages = cache->max_pages;
   p.c = kv4_cache(cache);
+  p.angles_wide = aligned16(cos_sin);
   p.q_out = q_out;
   p.dev_status = dev_status;
   const bool wide = p.rot % 16 == 0 && aligned16(k) && aligned16(v) &&
@@ -418,7 +459,8 @@ extern "C" sd_status sd_kv4_append(
                     : append_of<__half, 64>(wide))
               : (bf ? append_of<__nv_bfloat16, 128>(wide)
                     : append_of<__half, 128>(wide));
-  const long long all = (Hq + 2LL * cache->heads) * (D / 8);
+  const long long most = Hq > 2 * cache->heads ? Hq : 2 * cache->heads;
+  const long long all = most * (D / 8);
   const int threads =
       all < kThreads ? (int)(all + 31) / 32 * 32 : kThreads;
   void *args[] = {&p};
@@ -461,6 +503,7 @@ extern "C" sd_status sd_kv4_read(const sd_paged_kv4 *cache,
   p.total = total;
   p.Hkv = cache->heads;
   p.page_size = cache->page_size;
+  p.by_page = fast_div(cache->page_size);
   p.max_pages = cache->max_pages;
   p.c = kv4_cache(cache);
   p.k_out = k_out;
