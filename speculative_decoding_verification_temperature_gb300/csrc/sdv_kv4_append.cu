@@ -17,7 +17,7 @@ struct Append4Params {
   long long k_stride, v_stride, q_stride;
   const int32_t *q_start, *kv_len, *positions, *block_table;
   const float *cos_sin;
-  int max_pos, rot, interleaved;
+  int max_pos, rot, warps;
   int B, total, Hq, Hkv;
   int page_size, max_pages;
   FastDiv by_page;
@@ -143,23 +143,28 @@ struct Piece {
   uint4 own, other;
 };
 
-// A CTA per packed row; a thread takes eight neighbours of every (threads /
-// pieces)-th head, so that it reads its cosines and sines once.  Queries first,
-// which are only turned, then keys and values; a thread's first pieces of both
-// are on their way before it looks for the row's place.  WIDE: rot_dim is a
-// multiple of 16 and rows are 16-byte aligned, so that pieces are whole 16-byte
-// loads and turn as a whole; otherwise elements are loaded one by one.
-template <class T, int D, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 4)
+// p.warps warps per packed row (one where there are many rows, up to eight
+// where there are few); a thread takes eight neighbours of every step-th head,
+// so that it reads its cosines and sines once.  Queries first, which are only
+// turned, then keys and values, kBatch heads at a time; the first ones are on
+// their way before the row's place is looked for.  WIDE: rot_dim is a multiple
+// of 16 and rows are 16-byte aligned, so that pieces are whole 16-byte loads
+// and turn as a whole; otherwise elements are loaded one by one.
+constexpr int kBatch = 4;
+template <class T, int D, bool WIDE, bool NEIGHBOURS>
+__global__ void __launch_bounds__(kThreads, 3)
 append4_kernel(const __grid_constant__ Append4Params p) {
   griddep_wait();
   constexpr int PER = D / 8;
-  const int row = blockIdx.x, i = threadIdx.x % PER;
-  const int first = threadIdx.x / PER, step = blockDim.x / PER;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x * (kWarps / p.warps) + warp / p.warps;
+  if (row >= p.total) return;  // the whole warp
+  const int at = warp % p.warps * 32 + lane;
+  const int i = lane % PER, first = at / PER, step = p.warps * 32 / PER;
   const int half = p.rot / 2;
   // element (or piece's first element) e is turned with other(e)
   auto other = [&](int e) {
-    return p.interleaved ? e ^ 1 : e < half ? e + half : e - half;
+    return NEIGHBOURS ? e ^ 1 : e < half ? e + half : e - half;
   };
   const bool turns = 8 * i < p.rot;
   auto load = [&](const T *src, bool turned) {
@@ -167,36 +172,42 @@ append4_kernel(const __grid_constant__ Append4Params p) {
     if (WIDE) {
       x.own = ld_nc_v4(src + 8 * i);
       x.other = x.own;
-      if (turned && !p.interleaved) x.other = ld_nc_v4(src + other(8 * i));
+      if (turned && !NEIGHBOURS) x.other = ld_nc_v4(src + other(8 * i));
     } else {
       T own[8], oth[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int at = 8 * i + e;
-        own[e] = src[at];
-        oth[e] = turned && at < p.rot ? src[other(at)] : own[e];
+        const int n = 8 * i + e;
+        own[e] = src[n];
+        oth[e] = turned && n < p.rot ? src[other(n)] : own[e];
       }
       x.own = *reinterpret_cast<const uint4 *>(own);
       x.other = *reinterpret_cast<const uint4 *>(oth);
     }
     return x;
   };
-  auto load_q = [&](int h) {
-    Piece x{};
-    if (h < p.Hq)
-      x = load((const T *)p.q + row * p.q_stride + (long long)h * D, turns);
-    return x;
+  const T *q_row = (const T *)p.q + row * p.q_stride;
+  const T *k_row = (const T *)p.k + row * p.k_stride;
+  const T *v_row = (const T *)p.v + row * p.v_stride;
+  Piece x[kBatch];
+  auto load_q = [&](int h0) {
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n) {
+      const int h = h0 + n * step + first;
+      if (h < p.Hq) x[n] = load(q_row + h * D, turns);
+    }
   };
-  auto load_kv = [&](int h) {  // keys, then values
-    Piece x{};
-    if (h < p.Hkv)
-      x = load((const T *)p.k + row * p.k_stride + (long long)h * D, turns);
-    else if (h < 2 * p.Hkv)
-      x = load((const T *)p.v + row * p.v_stride + (long long)(h - p.Hkv) * D,
-               false);
-    return x;
+  auto load_kv = [&](int h0) {  // keys, then values
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n) {
+      const int h = h0 + n * step + first;
+      if (h < 2 * p.Hkv)
+        x[n] = load(h < p.Hkv ? k_row + h * D : v_row + (h - p.Hkv) * D,
+                    turns && h < p.Hkv);
+    }
   };
-  Piece q = load_q(first), kv = load_kv(first);
+  if (p.Hq > 0) load_q(0);
+  else load_kv(0);
   Place pl = place_row(p, row);
   if (pl.st == 0 && pl.owned && p.cos_sin) {
     if (p.positions) pl.pos = __ldg(p.positions + row);
@@ -205,17 +216,17 @@ append4_kernel(const __grid_constant__ Append4Params p) {
       pl.page = -1;
     }
   }
-  if (threadIdx.x == 0) status_or(p.dev_status, pl.st);
+  if (at == 0) status_or(p.dev_status, pl.st);
   if (!pl.owned) return;
   // x' = x c + x_other s: the sine of the first of a pair is negative
   float2 c[4], s[4];
   const float *cs = p.cos_sin + (long long)pl.pos * p.rot;
   if (WIDE && turns && pl.page >= 0 && p.angles_wide) {
     const bool head = 8 * i < half;
-    const int angle = p.interleaved ? 4 * i : head ? 8 * i : 8 * i - half;
+    const int angle = NEIGHBOURS ? 4 * i : head ? 8 * i : 8 * i - half;
     float4 a = __ldg(reinterpret_cast<const float4 *>(cs + angle));
     float4 b = __ldg(reinterpret_cast<const float4 *>(cs + half + angle));
-    if (p.interleaved) {
+    if (NEIGHBOURS) {
       c[0] = make_float2(a.x, a.x), s[0] = make_float2(-b.x, b.x);
       c[1] = make_float2(a.y, a.y), s[1] = make_float2(-b.y, b.y);
       c[2] = make_float2(a.z, a.z), s[2] = make_float2(-b.z, b.z);
@@ -234,76 +245,85 @@ append4_kernel(const __grid_constant__ Append4Params p) {
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int at = 8 * i + e;
-      float x = 1.f, y = 0.f;
-      if (at < p.rot && pl.page >= 0) {
-        const bool head = p.interleaved ? !(at & 1) : at < half;
-        const int angle = p.interleaved ? at / 2 : head ? at : at - half;
-        x = __ldg(cs + angle);
-        y = head ? -__ldg(cs + half + angle) : __ldg(cs + half + angle);
+      const int n = 8 * i + e;
+      float u = 1.f, v = 0.f;
+      if (n < p.rot && pl.page >= 0) {
+        const bool head = NEIGHBOURS ? !(n & 1) : n < half;
+        const int angle = NEIGHBOURS ? n / 2 : head ? n : n - half;
+        u = __ldg(cs + angle);
+        v = head ? -__ldg(cs + half + angle) : __ldg(cs + half + angle);
       }
-      if (e & 1) c[e / 2].y = x, s[e / 2].y = y;
-      else c[e / 2].x = x, s[e / 2].x = y;
+      if (e & 1) c[e / 2].y = u, s[e / 2].y = v;
+      else c[e / 2].x = u, s[e / 2].x = v;
     }
   }
-  auto turn = [&](const Piece &in, bool turned, float2 (&x)[4]) {
+  auto turn = [&](const Piece &in, bool turned, float2 (&y)[4]) {
     const uint32_t own[4] = {in.own.x, in.own.y, in.own.z, in.own.w};
     const uint32_t oth[4] = {in.other.x, in.other.y, in.other.z, in.other.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      x[e] = unpack2<T>(own[e]);
+      y[e] = unpack2<T>(own[e]);
       if (!turned) continue;
-      const float2 v = WIDE && p.interleaved ? make_float2(x[e].y, x[e].x)
-                                             : unpack2<T>(oth[e]);
-      const float2 y = add2(mul2(x[e], c[e]), mul2(v, s[e]));
+      const float2 v = WIDE && NEIGHBOURS ? make_float2(y[e].y, y[e].x)
+                                          : unpack2<T>(oth[e]);
+      const float2 z = add2(mul2(y[e], c[e]), mul2(v, s[e]));
       // (an odd piece may end its turn in the middle)
-      if (WIDE || 8 * i + 2 * e < p.rot) x[e].x = y.x;
-      if (WIDE || 8 * i + 2 * e + 1 < p.rot) x[e].y = y.y;
+      if (WIDE || 8 * i + 2 * e < p.rot) y[e].x = z.x;
+      if (WIDE || 8 * i + 2 * e + 1 < p.rot) y[e].y = z.y;
     }
   };
-  for (int h = first; h < p.Hq; h += step) {
-    const Piece now = q;
-    q = load_q(h + step);
-    float2 x[4];
-    turn(now, turns, x);
-    T *to = (T *)p.q_out + ((long long)row * p.Hq + h) * D + 8 * i;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (pl.page >= 0) {
-      w.x = pack2<T>(x[0]);
-      w.y = pack2<T>(x[1]);
-      w.z = pack2<T>(x[2]);
-      w.w = pack2<T>(x[3]);
-    }
-    if (WIDE) {
-      *reinterpret_cast<uint4 *>(to) = w;
-    } else {
-      const T *y = reinterpret_cast<const T *>(&w);
+  T *q_to = (T *)p.q_out + (long long)row * p.Hq * D + 8 * i;
+  for (int h0 = 0; h0 < p.Hq; h0 += kBatch * step) {
+    if (h0) load_q(h0);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) to[e] = y[e];
+    for (int n = 0; n < kBatch; ++n) {
+      const int h = h0 + n * step + first;
+      if (h >= p.Hq) break;
+      uint4 w = x[n].own;  // where nothing turns it is copied
+      if (turns) {
+        float2 y[4];
+        turn(x[n], true, y);
+        w = make_uint4(pack2<T>(y[0]), pack2<T>(y[1]), pack2<T>(y[2]),
+                       pack2<T>(y[3]));
+      }
+      if (pl.page < 0) w = make_uint4(0, 0, 0, 0);
+      T *to = q_to + h * D;
+      if (WIDE) {
+        *reinterpret_cast<uint4 *>(to) = w;
+      } else {
+        const T *y = reinterpret_cast<const T *>(&w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) to[e] = y[e];
+      }
     }
   }
-  if (pl.page < 0) return;  // the whole CTA
+  if (pl.page < 0) return;  // the whole warp
   const int lanes = 1 << (p.c.shift - 3);
-  // every thread of a warp makes the same rounds
-  for (int h0 = 0; h0 < 2 * p.Hkv; h0 += step) {
-    const int h = h0 + first;
-    const Piece now = kv;
-    if (h0 + step < 2 * p.Hkv) kv = load_kv(h + step);
-    const bool is_k = h < p.Hkv;
-    float2 x[4];
-    turn(now, turns && is_k, x);
-    uint32_t pair;
-    const uint32_t word = quantise8(x, lanes, pair);  // the whole warp
-    if (h >= 2 * p.Hkv) continue;
-    const long long at =
-        (long long)(is_k ? h : h - p.Hkv) * p.page_size + pl.token;
-    char *codes = const_cast<char *>(is_k ? p.c.k : p.c.v) +
-                  pl.page * p.c.page_stride + at * (D / 2);
-    char *pairs = const_cast<char *>(is_k ? p.c.k_scale : p.c.v_scale) +
-                  pl.page * p.c.scale_stride + at * p.c.scale_bytes;
-    reinterpret_cast<uint32_t *>(codes)[i] = word;
-    if ((i & (lanes - 1)) == 0)
-      reinterpret_cast<uint32_t *>(pairs)[8 * i >> p.c.shift] = pair;
+  const long long page_c = pl.page * p.c.page_stride + 4 * i;
+  const long long page_s =
+      pl.page * p.c.scale_stride + 4 * (8 * i >> p.c.shift);
+  // every lane makes the same rounds
+  for (int h0 = 0; h0 < 2 * p.Hkv; h0 += kBatch * step) {
+    if (h0 || p.Hq > 0) load_kv(h0);
+#pragma unroll
+    for (int n = 0; n < kBatch; ++n) {
+      if (h0 + n * step >= 2 * p.Hkv) break;
+      const int h = h0 + n * step + first;
+      const bool is_k = h < p.Hkv;
+      float2 y[4];
+      turn(x[n], turns && is_k, y);
+      uint32_t pair;
+      const uint32_t word = quantise8(y, lanes, pair);  // the whole warp
+      if (h >= 2 * p.Hkv) continue;
+      const int slot = (is_k ? h : h - p.Hkv) * p.page_size + pl.token;
+      char *codes = const_cast<char *>(is_k ? p.c.k : p.c.v);
+      char *pairs = const_cast<char *>(is_k ? p.c.k_scale : p.c.v_scale);
+      *reinterpret_cast<uint32_t *>(codes + page_c +
+                                    (long long)slot * (D / 2)) = word;
+      if ((i & (lanes - 1)) == 0)
+        *reinterpret_cast<uint32_t *>(
+            pairs + page_s + (long long)slot * p.c.scale_bytes) = pair;
+    }
   }
 }
 
@@ -380,9 +400,12 @@ read4_kernel(const __grid_constant__ Read4Params p) {
 }
 
 template <class T, int D>
-const void *append_of(bool wide) {
-  return wide ? (const void *)append4_kernel<T, D, true>
-              : (const void *)append4_kernel<T, D, false>;
+const void *append_of(bool wide, bool neighbours) {
+  if (neighbours)
+    return wide ? (const void *)append4_kernel<T, D, true, true>
+                : (const void *)append4_kernel<T, D, false, true>;
+  return wide ? (const void *)append4_kernel<T, D, true, false>
+              : (const void *)append4_kernel<T, D, false, false>;
 }
 
 }  // namespace
@@ -438,7 +461,6 @@ extern "C" sd_status sd_kv4_append(
   p.cos_sin = cos_sin;
   p.max_pos = max_pos;
   p.rot = cos_sin ? rot_dim : 0;
-  p.interleaved = interleaved;
   p.B = B;
   p.total = total;
   p.Hq = Hq;
@@ -454,18 +476,22 @@ extern "C" sd_status sd_kv4_append(
                     aligned16(q) && aligned16(q_out) &&
                     (k_stride | v_stride | (q ? q_stride : 0)) % 8 == 0;
   const bool bf = cache->dt == SD_BF16;
+  const bool nb = interleaved != 0;
   const void *kernel =
-      D == 64 ? (bf ? append_of<__nv_bfloat16, 64>(wide)
-                    : append_of<__half, 64>(wide))
-              : (bf ? append_of<__nv_bfloat16, 128>(wide)
-                    : append_of<__half, 128>(wide));
+      D == 64 ? (bf ? append_of<__nv_bfloat16, 64>(wide, nb)
+                    : append_of<__half, 64>(wide, nb))
+              : (bf ? append_of<__nv_bfloat16, 128>(wide, nb)
+                    : append_of<__half, 128>(wide, nb));
+  // as many warps a row as find a place, but no more than it has work for
   const long long most = Hq > 2 * cache->heads ? Hq : 2 * cache->heads;
-  const long long all = most * (D / 8);
-  const int threads =
-      all < kThreads ? (int)(all + 31) / 32 * 32 : kThreads;
+  p.warps = 1;
+  while (p.warps < kWarps && (long long)total * p.warps < 32 * sms &&
+         p.warps * 32 < most * (D / 8))
+    p.warps *= 2;
+  const unsigned rows = kWarps / p.warps;
   void *args[] = {&p};
-  return launch_pdl(kernel, (unsigned)total, threads, 0,
-                    static_cast<cudaStream_t>(stream), args);
+  return launch_pdl(kernel, (unsigned)((total + rows - 1LL) / rows), kThreads,
+                    0, static_cast<cudaStream_t>(stream), args);
 }
 
 extern "C" sd_status sd_kv4_read(const sd_paged_kv4 *cache,
