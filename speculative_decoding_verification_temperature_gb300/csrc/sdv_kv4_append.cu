@@ -152,7 +152,7 @@ struct Piece {
 // and turn as a whole; otherwise elements are loaded one by one.
 constexpr int kBatch = 4;
 template <class T, int D, bool WIDE, bool NEIGHBOURS>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(kThreads, 4)
 append4_kernel(const __grid_constant__ Append4Params p) {
   griddep_wait();
   constexpr int PER = D / 8;
