@@ -257,6 +257,7 @@ append4_kernel(const __grid_constant__ Append4Params p) {
       else c[e / 2].x = u, s[e / 2].x = v;
     }
   }
+  // Products and sums are rounded one by one: packed ones would be fused.
   auto turn = [&](const Piece &in, bool turned, float2 (&y)[4]) {
     const uint32_t own[4] = {in.own.x, in.own.y, in.own.z, in.own.w};
     const uint32_t oth[4] = {in.other.x, in.other.y, in.other.z, in.other.w};
@@ -266,7 +267,11 @@ append4_kernel(const __grid_constant__ Append4Params p) {
       if (!turned) continue;
       const float2 v = WIDE && NEIGHBOURS ? make_float2(y[e].y, y[e].x)
                                           : unpack2<T>(oth[e]);
-      const float2 z = add2(mul2(y[e], c[e]), mul2(v, s[e]));
+      const float2 z =
+          make_float2(__fadd_rn(__fmul_rn(y[e].x, c[e].x),
+                                __fmul_rn(v.x, s[e].x)),
+                      __fadd_rn(__fmul_rn(y[e].y, c[e].y),
+                                __fmul_rn(v.y, s[e].y)));
       // (an odd piece may end its turn in the middle)
       if (WIDE || 8 * i + 2 * e < p.rot) y[e].x = z.x;
       if (WIDE || 8 * i + 2 * e + 1 < p.rot) y[e].y = z.y;

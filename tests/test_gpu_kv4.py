@@ -142,6 +142,48 @@ def test_append_positions_and_odd_rows():
         np.testing.assert_array_equal(x, y)
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,group,rot", [(128, 64, 128), (64, 32, 32)])
+def test_append_many_rows_bit_for_bit(dtype, interleaved, D, group, rot):
+    """Millions of elements: no product of the rotation is fused with its sum
+    (a code in 10^5 would change), on one to eight warps a row."""
+    H, page = 8, 64
+    for total in (40, 700, 3001, 9000):
+        cols = -(-total // page)
+        g = torch.Generator(device="cuda").manual_seed(total)
+        table = torch.randperm(cols, generator=g,
+                               device="cuda").int().view(1, cols)
+        cache = api.PagedKV4.empty(cols, page, H, D, table, dtype, group)
+        x = torch.randn((total, 2 * H, D), generator=g,
+                        device="cuda").to(dtype)
+        tab = oref.cos_sin_table(total, rot).cuda()
+        start, kv = lengths([total], [total])
+        api.kv4_append(cache, x[:, :H], x[:, H:], start, kv, cos_sin=tab,
+                       interleaved=interleaved)
+        y = x.float()
+        c, s = (t[:, None] for t in tab.split(rot // 2, 1))
+        at = torch.arange(rot // 2, device="cuda")
+        i, j = (2 * at, 2 * at + 1) if interleaved else (at, at + rot // 2)
+        a, b = y[:, :H, i], y[:, :H, j]
+        y[:, :H, i], y[:, :H, j] = a * c - b * s, a * s + b * c
+        y = y.unflatten(-1, (-1, group))
+        lo, hi = y.amin(-1, keepdim=True), y.amax(-1, keepdim=True)
+        step = ((hi - lo) * float(np.float32(1 / 15))).half()
+        base = (lo - step.float() * 64).half()
+        n = ((y - base.float()) * step.float().reciprocal()).round() - 64
+        n = n.clamp(0, 15).to(torch.uint8).flatten(-2)
+        w = n.unflatten(-1, (-1, 8))[..., torch.tensor(ref.ORDER).cuda()]
+        codes = (w[..., 0::2] | w[..., 1::2] << 4).flatten(-2)
+        pos = torch.arange(total, device="cuda")
+        p, t = table[0, pos // page].long(), pos % page
+        pair = torch.cat([step, base], -1)
+        for got, want in ((cache.k, codes[:, :H]), (cache.v, codes[:, H:]),
+                          (cache.k_scale, pair[:, :H]),
+                          (cache.v_scale, pair[:, H:])):
+            assert torch.equal(got[p, :, t], want)
+
+
 def test_append_numbers_at_the_ends():
     """One number a group, NaN, infinities, numbers beyond 6144 and below
     fp16's least, groups far from zero."""
