@@ -21,13 +21,22 @@ namespace sdv {
 constexpr float kKv4Most = 6144.f;
 
 // Codes j and j + 4 of a word, which stand for elements 2 j and 2 j + 1, as
-// the fp16 pair (64 + n, 64 + n').
+// the fp16 pair (64 + n, 64 + n').  Those at bits 0 to 3 of a half are made
+// 1024 + n and 960 subtracted (exactly): a shift less for the pipe of integers
+// and logic, which is the fuller one, and an addition more for the other.
 __device__ __forceinline__ uint32_t kv4_codes(uint32_t w, int j) {
-  const uint32_t x = j == 0 ? w << 4 : w >> (4 * j - 4);
-  uint32_t y;  // x & 0x00f000f0 | 0x54005400, one operation
-  asm("lop3.b32 %0, %1, %2, %3, 0xea;"
-      : "=r"(y)
-      : "r"(x), "r"(0x00f000f0u), "r"(0x54005400u));
+  const uint32_t x = j < 2 ? w : w >> 8;
+  uint32_t y;  // x & mask | magic, one operation
+  if (j & 1) {
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;"
+        : "=r"(y)
+        : "r"(x), "r"(0x00f000f0u), "r"(0x54005400u));
+  } else {
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;"
+        : "=r"(y)
+        : "r"(x), "r"(0x000f000fu), "r"(0x64006400u));
+    asm("add.rn.f16x2 %0, %0, %1;" : "+r"(y) : "r"(0xe380e380u));  // -960
+  }
   return y;
 }
 __device__ __forceinline__ uint32_t kv4_fma(uint32_t x, uint32_t a,
