@@ -109,7 +109,7 @@ kv4_rows_kernel(const __grid_constant__ AttnParams p) {
                 "a part does not fit the smallest ring");
   using S = Shared4<ROWS, D, WARPS>;
   using U = Units<ROWS, kKeys>;
-  extern __shared__ __align__(128) char dyn[];
+  extern __shared__ __align__(1024) char dyn[];
   S &s = *reinterpret_cast<S *>(dyn);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
