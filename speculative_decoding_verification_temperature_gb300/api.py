@@ -198,6 +198,21 @@ def _raw_stream(device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
+_devices = None  # how many there are, once a call has asked
+
+
+def _call(device, fn, *args):
+    """fn(*args) with the tensors' device as the current one (launches go to
+    the current device's context)."""
+    global _devices
+    if _devices is None:
+        _devices = torch.cuda.device_count()
+    if _devices > 1 and device.index is not None:
+        with torch.cuda.device(device):
+            return fn(*args)
+    return fn(*args)
+
+
 class Workspace:
     """Scratch buffers of the calls that need one (work-queue counters, the
     records and partial sums that one kernel of a call leaves to the next).
@@ -878,10 +893,10 @@ def _append(fn, cache, k, v, q_start, kv_len, q, cos_sin, positions,
         pp = _vec(positions, dev, torch.int32, "positions")
         if positions.numel() != total:
             raise ValueError("positions must be [total]")
-    rc = fn(
-        cache._addr, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, Hq, start,
-        lens, pp, cp, max_pos, rot, 1 if interleaved else 0, B, total, op,
-        _status(status, dev), _raw_stream(dev))
+    rc = _call(
+        dev, fn, cache._addr, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, Hq,
+        start, lens, pp, cp, max_pos, rot, 1 if interleaved else 0, B, total,
+        op, _status(status, dev), _raw_stream(dev))
     if rc != SD_OK:
         _check(rc)
     return out
@@ -923,9 +938,10 @@ def kv4_read(cache, q_start, kv_len, total, *, status=None):
     B, start, lens = _lengths(cache, q_start, kv_len)
     k = torch.empty((total, heads, D), dtype=cache.dtype, device=dev)
     v = torch.empty((total, heads, D), dtype=cache.dtype, device=dev)
-    rc = lib().sd_kv4_read(
-        cache._addr, start, lens, B, total, k.data_ptr(), heads * D,
-        v.data_ptr(), heads * D, _status(status, dev), _raw_stream(dev))
+    rc = _call(
+        dev, lib().sd_kv4_read, cache._addr, start, lens, B, total,
+        k.data_ptr(), heads * D, v.data_ptr(), heads * D,
+        _status(status, dev), _raw_stream(dev))
     if rc != SD_OK:
         _check(rc)
     return {"k": k, "v": v}
@@ -950,9 +966,9 @@ def _attention(fn, ws_bytes, q, cache, q_start, kv_len, max_q, scale,
                       device=dev) if want_lse else None
     nbytes = ws_bytes(Hq, cache.heads, D, max_q)
     ws = (workspace or _default_ws).get(dev, nbytes)
-    rc = fn(
-        q.data_ptr(), qs, Hq, cache._addr, start, lens, mp, words, B, total,
-        max_q, D ** -0.5 if scale is None else scale, out.data_ptr(),
+    rc = _call(
+        dev, fn, q.data_ptr(), qs, Hq, cache._addr, start, lens, mp, words, B,
+        total, max_q, D ** -0.5 if scale is None else scale, out.data_ptr(),
         _ptr(lse), _status(status, dev), ws.data_ptr(), ws.numel(),
         _raw_stream(dev))
     if rc != SD_OK:

@@ -696,3 +696,51 @@ def test_drafting_from_a_4_bit_copy(dtype, group):
         # 4 bits: a step is a fifteenth of a group's range, about 5; scores
         # move by a tenth or two, values by 0.1
         assert float((got.float() - near.float()).abs().mean()) < 0.2
+
+
+def test_offsets_past_32_bits():
+    """Pages more than 4 GB into the cache: the same bits as at its start."""
+    H, D, page, n = 8, 128, 64, 140000
+    shape = (n, H, page, D // 2)
+    k, v = (torch.empty(shape, dtype=torch.uint8, device="cuda")
+            for _ in range(2))
+    ks, vs = (torch.empty((n, H, page, 2, 2), dtype=torch.float16,
+                          device="cuda") for _ in range(2))
+    g = torch.Generator(device="cuda").manual_seed(9)
+    total = 300
+    x = torch.randn((total, 2 * H + 32, D), generator=g, device="cuda").to(BF)
+    start, kv = lengths([total], [total])
+    out = []
+    for first in (0, n - 8):
+        table = (first + torch.arange(8, device="cuda")).int().view(1, 8)
+        cache = api.PagedKV4(k, v, ks, vs, table, BF)
+        api.kv4_append(cache, x[:, :H], x[:, H:2 * H], start, kv)
+        r = [*api.kv4_read(cache, start, kv, total).values()]
+        for m in (1, 3, 9, 300):  # each kernel
+            s0, kv0 = lengths([m], [total])
+            q = x[:m, 2 * H:].contiguous()
+            r.append(api.kv4_attention(q, cache, s0, kv0, max_q=m)["out"])
+        out.append(r)
+    for a, b in zip(*out):
+        assert torch.equal(a, b) and bool(torch.isfinite(a).all())
+
+
+def test_calls_on_two_streams_at_once():
+    """Calls that overlap on the GPU share nothing."""
+    P = ref.Paged4([9, 9, 1], [900, 400, 2000], 2, 128, 16, BF, 81, 64)
+    cache = P.cache(api)
+    start, kv = P.lengths()
+    qs = [P.rows(h).cuda() for h in (4, 16, 128)]
+    want = [api.kv4_attention(q, cache, start, kv, max_q=9)["out"]
+            for q in qs]
+    side = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for q, s in zip(qs, side):
+            with torch.cuda.stream(s):
+                got.append(api.kv4_attention(q, cache, start, kv,
+                                             max_q=9)["out"])
+    torch.cuda.synchronize()
+    for i, a in enumerate(got):
+        assert torch.equal(a, want[i % 3])
