@@ -263,8 +263,11 @@ struct Row {
 // fetched one ahead.  first: nothing is summed yet; parity: of the tile in the
 // stream; w_full, o_full: of the tile's halves.  Tiles that hide scores have a
 // copy of their own: a warp here runs on its scheduler's issue slots.
-// HALVES = 1: the stream has one half of each tile.
-template <class T, int D, bool HIDE, bool REST, int HALVES>
+// HALVES = 1: the stream has one half of each tile.  CODES: the halves in a
+// loop, since with the warps that make tiles an SM runs four kinds of code at
+// a time and waits for instructions (two prompt chunks 804 us, so 681; with
+// 16-bit keys 557 and 574).
+template <class T, int D, bool HIDE, bool REST, int HALVES, bool CODES>
 __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
                                            uint64_t *w_full, uint64_t *o_full,
                                            bool first, uint32_t parity,
@@ -273,7 +276,7 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
   using S = Scale<T>;
   uint32_t x[2][32];
   tmem_ld32(row.s_addr, x[0]);
-#pragma unroll
+#pragma unroll (CODES && !HIDE ? 1 : 2)
   for (int hf = 0; hf < HALVES; ++hf) {
     uint32_t w[kHalf / 2], rest[REST ? kHalf / 2 : 32];
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -1023,10 +1026,10 @@ attention_kernel(const __grid_constant__ AttnParams p,
           __syncwarp();
           if (i == 0) row.m = row_max<KEYS>(row.s_addr, cuts, seen);
           uint64_t *w_full = &s.w_full[st][SPLIT ? buf : 0];
-          fine = cuts ? weigh_tile<T, D, true, REST, HALVES>(
+          fine = cuts ? weigh_tile<T, D, true, REST, HALVES, CODES>(
                             row, seen, w_full, s.o_full[st], i == 0,
                             tn & 1, &s.abort, p.dev_status)
-                      : weigh_tile<T, D, false, REST, HALVES>(
+                      : weigh_tile<T, D, false, REST, HALVES, CODES>(
                             row, seen, w_full, s.o_full[st], i == 0,
                             tn & 1, &s.abort, p.dev_status);
           if (!fine) break;
