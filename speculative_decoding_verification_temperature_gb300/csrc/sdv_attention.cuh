@@ -45,6 +45,20 @@
 // tokens, 0.76 of the measured bf16 rate; with D = 64 the products halve, the
 // softmax stays, and the call takes 509 us).
 //
+// Over a 4-bit cache (CODES) two warps load codes and pairs as they lie, half a
+// tile of 64 keys at a time, and four more make fp16 tiles of them in the same
+// swizzle; products are of fp16 numbers, bf16 queries are scaled to them, and
+// weights are rounded once.  Up to 128 rows (SPLIT): both streams have every
+// tile, a half of its keys each, and one warp issues all products, so that the
+// next tile's scores are made beside this one's weights (32 chunks of 9 tokens
+// 131 us with every other tile a stream, so 122).  One warp that loaded and
+// made a tile took 6400 cycles for it, half of them loading (246 us); 2000
+// cycles of makers, 1900 of softmax and 1700 of products, in rings of two
+// tiles, make 3000 a tile now, where the tile's bytes take 700.  With 256 rows
+// 680 us on the two prompt chunks (1.2 PFLOP/s), where 16-bit keys take 557:
+// the warps wait for instructions (1.9 of 8 stalled at a time against 1.1), not
+// for the makers, which could make a quarter as much in the same time.
+//
 // A wait that gives up (see role_wait) stops the loads and the products; all
 // other steps go on over meaningless data to the end of the share, so that
 // every barrier between warps is reached.
@@ -110,8 +124,8 @@ template <int D, bool PAIR, bool CODES> struct Layout {
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kQBytes = (PAIR ? 2 : 1) * kTileBytes;
   // Two rings of tiles, as many as fit: what is in flight covers the latency
-  // of HBM.  PAIR and CODES: ring 0 holds the key tiles, ring 1 the value tiles,
-  // read by both streams.  Otherwise ring st holds stream st's tiles in the order
+  // of HBM.  PAIR and CODES: ring 0 holds the key tiles, ring 1 the value
+  // tiles, read by both streams.  Otherwise ring st holds stream st's tiles in the order
   // it uses them (key, value, key, ...): a ring with one writer and one
   // reader, so that a stream that is ahead never takes a slot's earlier
   // filling for its own.
@@ -286,7 +300,8 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
     for (int c = 2 * hf; c < 2 * hf + 2; ++c) {
       uint32_t *xc = x[c & 1];
       tmem_wait_ld();
-      if (c < 2 * HALVES - 1) tmem_ld32(row.s_addr + 32 * (c + 1), x[(c + 1) & 1]);
+      if (c < 2 * HALVES - 1)
+        tmem_ld32(row.s_addr + 32 * (c + 1), x[(c + 1) & 1]);
       if (HIDE) hide32(xc, seen[c]);
       mt = fmaxf(mt, max32(xc));
       weigh32<T, REST>(xc, row.sl, off, w + 16 * (c & 1),

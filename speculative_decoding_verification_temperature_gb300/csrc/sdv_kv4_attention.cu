@@ -1,5 +1,11 @@
 // sdv_kv4_attention.cu -- sd_kv4_attention: a chunk of new tokens attends
 // over the 4-bit paged cache.
+//
+// With more than 16 rows a head, the kernel of sdv_attention.cuh; with up to 8
+// or 16, the one below, whose products are small ones of a warp's own: tiles
+// of 128 rows there would be written to and read from shared memory as 16-bit
+// numbers, four times the cache's bytes, and take 2.2 times as long for 8 rows
+// (64 sequences of up to 8192 keys: 89 us here; 16 rows 147, and 203 there).
 #include "sdv_attention.cuh"
 
 namespace sdv {
@@ -18,6 +24,18 @@ namespace {
 // pairs as they lie: no other warp is waited for until a unit ends.  (A warp
 // that brought tiles of 128 keys by bulk copies, four a page, was held up by
 // their number: 56 cycles a copy, 154 us on 64 sequences of pages of 16.)
+//
+// What bounds it: making numbers of codes.  32 values of a key are 4 masks, 2
+// shifts, 2 subtractions and 4 fmas for each 8, and 16 keys of 128 take 348
+// instructions in all, 87 cycles of an SM's issue slots, where their bytes take
+// 89 at HBM's rate.  Four warps a scheduler fill 0.6 of the slots: 89 us on 64
+// sequences (0.40 GB, 4.5 TB/s, 0.67 of the measured copy rate), 66 us and a
+// join of 8 on one token behind 262144 keys.
+//
+// The units' shares are per warp, in places of 32 keys; what the warps of a CTA
+// have of one unit they join in shared memory at the end, what CTAs have of one
+// the join kernel.  (With a share a CTA, whose warps joined at every unit's
+// end, 200 sequences of up to 300 keys took 49 us; this takes 30.)
 //
 // A row's weights are fp16, 2^kBias at its reference m, which moves up only
 // when a score is 2^kSlack above it: at most 2^15, and a weight 2^-24 of the
@@ -575,7 +593,8 @@ kv4_rows_kernel(const __grid_constant__ AttnParams p) {
 constexpr int kMaxGrid4 = 320;  // CTAs the workspace is laid out for
 
 // The kernel of a call, by the rows a head has: 8 or 16 at a time in warps of
-// their own, 128 or 256 on the fifth-generation tensor cores.
+// their own, 128 or 256 in tiles.  Measured on 64 sequences of up to 8192 keys:
+// 16 rows 147 us in warps and 203 in tiles, 32 rows 280 and 203.
 int rows_of(int max_q, int G) {
   const long long n = (long long)max_q * G;
   return n <= 8 ? 8 : n <= 16 ? 16 : n <= 128 ? 128 : 256;

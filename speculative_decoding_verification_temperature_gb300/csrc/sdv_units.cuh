@@ -145,7 +145,8 @@ __device__ void make_plan(const UnitParams &p, Plan &s) {
       w = 0;
       if (tid < 256 && base + tid < p.B) {
         const Chunk c = attn_chunk(p, base + tid);
-        w = (head_tiles<ROWS, KEYS>(p, c) + extra * row_tiles<ROWS>(p, c)) * p.Hkv;
+        w = (head_tiles<ROWS, KEYS>(p, c) + extra * row_tiles<ROWS>(p, c)) *
+            p.Hkv;
       }
     }
     unsigned long long inc = w;

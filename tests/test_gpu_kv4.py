@@ -9,6 +9,7 @@ import torch
 from speculative_decoding_verification_temperature_gb300 import api
 from tests import kv4_ref as ref
 from tests import operators_ref as oref
+from tests.test_gpu_canaries import GuardedTorch
 
 pytestmark = pytest.mark.gpu
 
@@ -122,7 +123,12 @@ def test_append_head_layouts(Hkv, Hq):
 @pytest.mark.parametrize("page", [8, 24, 64, 320])
 def test_append_pages_apart(page):
     P = ref.Paged4([30, 1], [90, 200], 2, 64, page, BF, 8, 32, apart=48)
-    run_append(P, 2, 32)
+    cache, _ = run_append(P, 2, 32)
+    for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+        between = t._base[:, t[0].numel():]
+        assert between.numel() * between.element_size() == 48 * t.shape[0]
+        assert bool((between == 255).all() if t.dtype == torch.uint8
+                    else torch.isnan(between).all())
 
 
 def test_append_positions_and_odd_rows():
@@ -744,3 +750,24 @@ def test_calls_on_two_streams_at_once():
     torch.cuda.synchronize()
     for i, a in enumerate(got):
         assert torch.equal(a, want[i % 3])
+
+
+@pytest.mark.parametrize("n,kv,Hq", [([3, 1], [3000, 70], 4),
+                                     ([3, 1], [3000, 70], 8),
+                                     ([9, 1], [3000, 70], 6),
+                                     ([200], [300], 6)])
+@pytest.mark.parametrize("D,group", [(64, 64), (128, 32)])
+def test_no_write_outside_the_buffers(monkeypatch, n, kv, Hq, D, group):
+    """Outputs and workspaces lie between guards."""
+    P = ref.Paged4(n, kv, 2, D, 16, BF, 91, group)
+    cache, q = P.cache(api), P.rows(Hq).cuda()
+    start, lens = P.lengths()
+    x = P.rows(4).cuda()
+    guard = GuardedTorch()
+    monkeypatch.setattr(api, "torch", guard)
+    api.kv4_attention(q, cache, start, lens, max_q=max(n), want_lse=True,
+                      workspace=api.Workspace())
+    assert guard.check() == 3
+    api.kv4_append(cache, x[:, :2], x[:, 2:], start, lens, q=q)
+    api.kv4_read(cache, start, lens, P.total)
+    assert guard.check() == 3
