@@ -216,13 +216,12 @@ __device__ __forceinline__ void hide32(uint32_t *x, uint32_t seen) {
     if (!(seen >> e & 1)) x[e] = 0xff800000u;
 }
 
-// The largest of a row's scores (of those it sees, where `cuts`).
-template <int KEYS>
+// The largest of a row's 128 scores (of those it sees, where `cuts`).
 __device__ __forceinline__ float row_max(uint32_t s_addr, bool cuts,
                                          const uint32_t *seen) {
   float m = -kInf;
 #pragma unroll
-  for (int c = 0; c < KEYS; c += 64) {
+  for (int c = 0; c < kTile; c += 64) {
     uint32_t x[64];
     tmem_ld32(s_addr + c, x);
     tmem_ld32(s_addr + c + 32, x + 32);
@@ -277,11 +276,10 @@ struct Row {
 // fetched one ahead.  first: nothing is summed yet; parity: of the tile in the
 // stream; w_full, o_full: of the tile's halves.  Tiles that hide scores have a
 // copy of their own: a warp here runs on its scheduler's issue slots.
-// HALVES = 1: the stream has one half of each tile.  CODES: the halves in a
-// loop, since with the warps that make tiles an SM runs four kinds of code at
-// a time and waits for instructions (two prompt chunks 804 us, so 681; with
-// 16-bit keys 557 and 574).
-template <class T, int D, bool HIDE, bool REST, int HALVES, bool CODES>
+// CODES: the halves in a loop, since with the warps that make tiles an SM runs
+// four kinds of code at a time and waits for instructions (two prompt chunks
+// 804 us, so 681; with 16-bit keys 557 and 574).
+template <class T, int D, bool HIDE, bool REST, bool CODES>
 __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
                                            uint64_t *w_full, uint64_t *o_full,
                                            bool first, uint32_t parity,
@@ -291,7 +289,7 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
   uint32_t x[2][32];
   tmem_ld32(row.s_addr, x[0]);
 #pragma unroll (CODES && !HIDE ? 1 : 2)
-  for (int hf = 0; hf < HALVES; ++hf) {
+  for (int hf = 0; hf < 2; ++hf) {
     uint32_t w[kHalf / 2], rest[REST ? kHalf / 2 : 32];
     float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
     float mt = -kInf;
@@ -300,8 +298,7 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
     for (int c = 2 * hf; c < 2 * hf + 2; ++c) {
       uint32_t *xc = x[c & 1];
       tmem_wait_ld();
-      if (c < 2 * HALVES - 1)
-        tmem_ld32(row.s_addr + 32 * (c + 1), x[(c + 1) & 1]);
+      if (c < 3) tmem_ld32(row.s_addr + 32 * (c + 1), x[(c + 1) & 1]);
       if (HIDE) hide32(xc, seen[c]);
       mt = fmaxf(mt, max32(xc));
       weigh32<T, REST>(xc, row.sl, off, w + 16 * (c & 1),
@@ -322,10 +319,7 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
       if (hf || !first) {
         // all sums before this half are complete when the last of them are
         const bool fine =
-            HALVES == 2
-                ? role_wait(&o_full[hf ^ 1], parity ^ (hf ^ 1), abort,
-                            dev_status)
-                : role_wait(&o_full[0], parity ^ 1, abort, dev_status);
+            role_wait(&o_full[hf ^ 1], parity ^ (hf ^ 1), abort, dev_status);
         if (!__all_sync(~0u, fine)) return false;
         tmem_fence_after();
 #pragma unroll 1
@@ -361,6 +355,77 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&w_full[hf]);
   }
+  return true;
+}
+
+// The weights of one row in half a tile, where the stream has a half of each
+// (SPLIT): the maximum first, then the weights in a second pass over the
+// scores, in loops as short as they can be, for the same reason (32 chunks of
+// 9 tokens 117 us; weighed while the maximum is being found 122).
+template <class T, int D>
+__device__ __forceinline__ bool weigh_half(Row &row, bool cuts,
+                                           const uint32_t (&seen)[2],
+                                           uint64_t *w_full, uint64_t *o_full,
+                                           bool first, uint32_t parity,
+                                           volatile int *abort,
+                                           int32_t *dev_status) {
+  using S = Scale<T>;
+  float mt = -kInf;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t x[32];
+    tmem_ld32(row.s_addr + 32 * c, x);
+    tmem_wait_ld();
+    if (cuts) hide32(x, seen[c]);
+    mt = fmaxf(mt, max32(x));
+  }
+  const float up = (mt - row.m) * row.sl;
+  bool move = mt > -kInf && !(up <= S::kSlack);
+  if (!cuts || (seen[0] & seen[1]) == ~0u)
+    move = move || (up < -S::kDrop && up > -kMost && row.l < kTop);
+  if (__any_sync(~0u, move)) {
+    float f = 1.f;
+    if (move) {
+      f = row.m == -kInf ? 1.f : ex2(-up);
+      row.m = mt;
+    }
+    row.l *= f;
+    if (!first) {
+      // all sums before this half are complete when the last of them are
+      const bool fine = role_wait(o_full, parity ^ 1, abort, dev_status);
+      if (!__all_sync(~0u, fine)) return false;
+      tmem_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(row.o_addr + c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+        tmem_st32(row.o_addr + c, o);
+      }
+    }
+    __syncwarp();
+  }
+  const float off = row.m == -kInf ? 0.f : S::kBias - row.m * row.sl;
+  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    uint32_t x[32], w[16];
+    tmem_ld32(row.s_addr + 32 * c, x);
+    tmem_wait_ld();
+    if (cuts) hide32(x, c ? seen[1] : seen[0]);
+    weigh32<T, false>(x, row.sl, off, w, w, sum);
+    // over scores that have been read
+    tmem_st16(row.s_addr + 16 * c, w);
+  }
+  const float2 t = add2(sum[0], sum[1]);
+  row.l += t.x + t.y;
+  tmem_wait_st();
+  tmem_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(w_full);
   return true;
 }
 
@@ -1023,7 +1088,7 @@ attention_kernel(const __grid_constant__ AttnParams p,
         fine = role_wait(&s.s_full[buf], (SPLIT ? tn >> 1 : tn) & 1, &s.abort,
                          p.dev_status);
         if (!__all_sync(~0u, fine)) { fine = false; break; }
-        constexpr int KEYS = SPLIT ? kHalf : kTile, HALVES = SPLIT ? 1 : 2;
+        constexpr int KEYS = SPLIT ? kHalf : kTile;
         if (SPLIT) row.s_addr = tmem + lanes + buf * kTile + st * kHalf;
         if (warp_rows) {
           tmem_fence_after();
@@ -1039,14 +1104,19 @@ attention_kernel(const __grid_constant__ AttnParams p,
                   mine ? seen_bits(p, u.c, token, limit, key + 32 * c) : 0;
           }
           __syncwarp();
-          if (i == 0) row.m = row_max<KEYS>(row.s_addr, cuts, seen);
-          uint64_t *w_full = &s.w_full[st][SPLIT ? buf : 0];
-          fine = cuts ? weigh_tile<T, D, true, REST, HALVES, CODES>(
-                            row, seen, w_full, s.o_full[st], i == 0,
-                            tn & 1, &s.abort, p.dev_status)
-                      : weigh_tile<T, D, false, REST, HALVES, CODES>(
-                            row, seen, w_full, s.o_full[st], i == 0,
-                            tn & 1, &s.abort, p.dev_status);
+          if constexpr (SPLIT) {
+            fine = weigh_half<T, D>(row, cuts, seen, &s.w_full[st][buf],
+                                    &s.o_full[st][0], i == 0, tn & 1,
+                                    &s.abort, p.dev_status);
+          } else {
+            if (i == 0) row.m = row_max(row.s_addr, cuts, seen);
+            fine = cuts ? weigh_tile<T, D, true, REST, CODES>(
+                              row, seen, s.w_full[st], s.o_full[st], i == 0,
+                              tn & 1, &s.abort, p.dev_status)
+                        : weigh_tile<T, D, false, REST, CODES>(
+                              row, seen, s.w_full[st], s.o_full[st], i == 0,
+                              tn & 1, &s.abort, p.dev_status);
+          }
           if (!fine) break;
         } else if (lane == 0) {
           mbar_arrive(&s.w_full[st][SPLIT ? buf : 0]);

@@ -254,16 +254,14 @@ kv4_rows_kernel(const __grid_constant__ AttnParams p) {
     constexpr int NB = NT == 1 ? 2 : 1;
     auto use = [&](auto hides, int key, int b0) {
       constexpr bool HIDE = decltype(hides)::value;
-      // scores: [16 keys][rows]; two sums each, half the chain from product
-      // to product
+      // scores: [16 keys][rows]
       float sc[NB][NT][4];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        float sd[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[b][n][e] = sd[n][e] = 0.f;
+          for (int e = 0; e < 4; ++e) sc[b][n][e] = 0.f;
         uint32_t k[2][W], a[2], c[2];
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
@@ -287,13 +285,9 @@ kv4_rows_kernel(const __grid_constant__ AttnParams p) {
                 kv4_fma(kv4_codes(k[1][i], j + 1), a[1], c[1]);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-              mma16816(j ? sd[n] : sc[b][n], f0, f1, f2, f3,
-                       qf[n][4 * i + j], qf[n][4 * i + j + 1]);
+              mma16816(sc[b][n], f0, f1, f2, f3, qf[n][4 * i + j],
+                       qf[n][4 * i + j + 1]);
           }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[b][n][e] += sd[n][e];
       }
       // exponents of the weights; of keys a row does not see -inf
       float y[NB][NT][4];
