@@ -51,10 +51,10 @@
 // weights are rounded once.  Up to 128 rows (SPLIT): both streams have every
 // tile, a half of its keys each, and one warp issues all products, so that the
 // next tile's scores are made beside this one's weights (32 chunks of 9 tokens
-// 131 us with every other tile a stream, so 122).  One warp that loaded and
+// 131 us with every other tile a stream, so 116).  One warp that loaded and
 // made a tile took 6400 cycles for it, half of them loading (246 us); 2000
-// cycles of makers, 1900 of softmax and 1700 of products, in rings of two
-// tiles, make 3000 a tile now, where the tile's bytes take 700.  With 256 rows
+// cycles of makers, 1800 of softmax and 1700 of products, in rings of two
+// tiles, make 2800 a tile now, where the tile's bytes take 700.  With 256 rows
 // 680 us on the two prompt chunks (1.2 PFLOP/s), where 16-bit keys take 557:
 // the warps wait for instructions (1.9 of 8 stalled at a time against 1.1), not
 // for the makers, which could make a quarter as much in the same time.

@@ -5,7 +5,7 @@
 // or 16, the one below, whose products are small ones of a warp's own: tiles
 // of 128 rows there would be written to and read from shared memory as 16-bit
 // numbers, four times the cache's bytes, and take 2.2 times as long for 8 rows
-// (64 sequences of up to 8192 keys: 89 us here; 16 rows 147, and 203 there).
+// (64 sequences of up to 8192 keys: 88 us here; 16 rows 136, and 195 there).
 #include "sdv_attention.cuh"
 
 namespace sdv {
@@ -26,9 +26,9 @@ namespace {
 // their number: 56 cycles a copy, 154 us on 64 sequences of pages of 16.)
 //
 // What bounds it: making numbers of codes.  32 values of a key are 4 masks, 2
-// shifts, 2 subtractions and 4 fmas for each 8, and 16 keys of 128 take 348
-// instructions in all, 87 cycles of an SM's issue slots, where their bytes take
-// 89 at HBM's rate.  Four warps a scheduler fill 0.6 of the slots: 89 us on 64
+// shifts, 2 subtractions and 4 fmas for each 8, and 16 keys of 128 take 345
+// instructions in all, 86 cycles of an SM's issue slots, where their bytes take
+// 89 at HBM's rate.  Four warps a scheduler fill 0.6 of the slots: 88 us on 64
 // sequences (0.40 GB, 4.5 TB/s, 0.67 of the measured copy rate), 66 us and a
 // join of 8 on one token behind 262144 keys.
 //
@@ -250,7 +250,7 @@ kv4_rows_kernel(const __grid_constant__ AttnParams p) {
     const char *v_from = ring + CODES + v_at;
     const char *vs_from = ring + 2 * CODES + kBlock * SB + vs_at;
     // NB times 16 keys, from the b0-th of the block on.  With 16 rows there
-    // are no registers for both at once (188 us where this takes 147).
+    // are no registers for both at once (188 us where 147 were taken so).
     constexpr int NB = NT == 1 ? 2 : 1;
     auto use = [&](auto hides, int key, int b0) {
       constexpr bool HIDE = decltype(hides)::value;
@@ -588,7 +588,7 @@ constexpr int kMaxGrid4 = 320;  // CTAs the workspace is laid out for
 
 // The kernel of a call, by the rows a head has: 8 or 16 at a time in warps of
 // their own, 128 or 256 in tiles.  Measured on 64 sequences of up to 8192 keys:
-// 16 rows 147 us in warps and 203 in tiles, 32 rows 280 and 203.
+// 16 rows 136 us in warps and 195 in tiles, 32 rows 260 and 195.
 int rows_of(int max_q, int G) {
   const long long n = (long long)max_q * G;
   return n <= 8 ? 8 : n <= 16 ? 16 : n <= 128 ? 128 : 256;
