@@ -111,7 +111,7 @@ __device__ __forceinline__ void lds_words(const char *p, uint32_t (&w)[N]) {
 struct Kv4Cache {
   const char *k, *v, *k_scale, *v_scale;
   long long page_stride, scale_stride;
-  int num_pages, row_bytes, scale_bytes;
+  int num_pages, scale_bytes;
   int shift;  // log2 of the group
 };
 
@@ -162,7 +162,6 @@ inline Kv4Cache kv4_cache(const sd_paged_kv4 *c) {
   r.page_stride = c->page_stride;
   r.scale_stride = c->scale_stride;
   r.num_pages = c->num_pages;
-  r.row_bytes = c->head_dim / 2;
   r.scale_bytes = c->head_dim / c->group * 4;
   r.shift = c->group == 32 ? 5 : c->group == 64 ? 6 : 7;
   return r;
