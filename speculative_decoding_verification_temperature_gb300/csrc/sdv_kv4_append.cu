@@ -182,7 +182,7 @@ append4_kernel(const __grid_constant__ Append4Params p) {
       x.other = x.own;
       if (turned && !NEIGHBOURS) x.other = ld_nc_v4(src + other(8 * i));
     } else {
-      T own[8], oth[8];
+      alignas(16) T own[8], oth[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int n = 8 * i + e;
