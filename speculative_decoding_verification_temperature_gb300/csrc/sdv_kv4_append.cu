@@ -8,11 +8,10 @@
 // each step rounded to fp32 by itself (no contraction), 1 / 15 and 1 / a being
 // rounded first: the codes are the same numbers wherever they are computed.
 //
-// What bounds them: HBM, less than half of it reached where rows are few (25k
-// tokens of 48 heads of 128, fp16, are 608 MB in 129 us, 0.70 of the measured
-// copy rate, with 0.57 of the issue slots; 99k tokens of 8 heads are read back,
-// 0.52 GB, in 88 us, 0.88), and for one token the chain sequence -> page ->
-// store.
+// What bounds them: HBM where rows are many (28k tokens of 48 heads of 128,
+// fp16, are 608 MB in 128 us, 0.70 of the measured copy rate, with 0.57 of the
+// issue slots; 99k tokens of 8 heads are read back, 0.52 GB, in 88 us, 0.88),
+// and the chain sequence -> page -> store where they are few.
 #include "sdv_kv4.cuh"
 
 namespace sdv {
@@ -157,7 +156,7 @@ struct Piece {
 // of 16 and rows are 16-byte aligned, so that pieces are whole 16-byte loads
 // and turn as a whole; otherwise elements are loaded one by one.  (A CTA a row
 // looked up the row's place and read its angles in each of eight warps: 208 us
-// on the 25k tokens, and 128 with a warp a row.)
+// on the 28k tokens, and 128 with a warp a row.)
 constexpr int kBatch = 4;
 template <class T, int D, bool WIDE, bool NEIGHBOURS>
 __global__ void __launch_bounds__(kThreads, 4)
