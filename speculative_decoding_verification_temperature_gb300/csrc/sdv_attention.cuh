@@ -429,33 +429,33 @@ __device__ __forceinline__ bool weigh_half(Row &row, bool cuts,
   return true;
 }
 
-// Eight elements of a query row that CH neighbouring lanes hold, to fp16
+// A thread's part of a query row that LANES neighbouring lanes hold, to fp16
 // pairs; returns the factor of the row's scores.  bf16 rows are multiplied by
 // the power of two that takes the row's largest element to [2^14, 2^15): exact
-// but for elements 2^-28 of that and below.  A row with NaN or infinity gets a
-// NaN factor.
-template <int CH>
-__device__ __forceinline__ float to_half_row(uint4 &x, bool bf16,
-                                             float scale) {
-  uint32_t w[4] = {x.x, x.y, x.z, x.w}, top = 0;
+// but for elements 2^-28 of that and below.  The power stops at 2^126, whose
+// inverse is still a normal number: rows below 2^-112 are taken to below 2^14,
+// where bf16's least number, 2^-133, is 2^-7, and nothing is lost at all.  A
+// row with NaN or infinity gets a NaN factor.
+template <int LANES, int N>
+__device__ __forceinline__ float fit_query(uint32_t (&w)[N], bool bf16,
+                                           float scale) {
+  uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < N; ++i)
     top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
 #pragma unroll
-  for (int d = 1; d < CH; d <<= 1)
+  for (int d = 1; d < LANES; d <<= 1)
     top = max(top, __shfl_xor_sync(~0u, top, d));
   float f = scale;
   if (bf16) {
-    // exponents above -86: the power is a normal number
-    const int exp = max((int)(top >> 7), 41) - 127;
+    const int exp = max((int)(top >> 7), 15) - 127;
     const float up = __uint_as_float((uint32_t)(14 - exp + 127) << 23);
     f *= __uint_as_float((uint32_t)(exp - 14 + 127) << 23);
     if (top >= 0x7f80u) f = __int_as_float(0x7fc00000);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < N; ++i)
       w[i] = pack2<__half>(__uint_as_float(w[i] << 16) * up,
                            __uint_as_float(w[i] & 0xffff0000u) * up);
-    x = make_uint4(w[0], w[1], w[2], w[3]);
   } else if (top >= 0x7c00u) {
     f = __int_as_float(0x7fc00000);
   }
@@ -1024,7 +1024,9 @@ attention_kernel(const __grid_constant__ AttnParams p,
       for (int i = 0; i < kTile * CH / NT; ++i) {
         const int n = me / CH + i * (NT / CH);
         if constexpr (CODES) {
-          const float f = to_half_row<CH>(x[i], p.bf16, p.scale_log2);
+          uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          const float f = fit_query<CH>(w, p.bf16, p.scale_log2);
+          x[i] = make_uint4(w[0], w[1], w[2], w[3]);
           if (ch == 0) s.q_sl[sl_at][base_row + n] = f;
         }
         *reinterpret_cast<uint4 *>(dst + n * 128 +

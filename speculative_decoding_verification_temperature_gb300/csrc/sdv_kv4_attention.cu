@@ -80,40 +80,18 @@ template <int ROWS, int D, int WARPS> struct Shared4 {
 };
 
 // A thread's part of a query row, D / 4 elements, as fp16 pairs, and the
-// factor of its scores.  bf16 rows are multiplied by the power of two that
-// takes the row's largest element to [2^14, 2^15): exact but for elements
-// 2^-28 of that and below.  A row with NaN or infinity gets a NaN factor.
+// factor of its scores (see fit_query).
 template <int N>
 __device__ __forceinline__ float load_query(const void *src, bool valid,
                                             bool bf16, float scale,
                                             uint32_t (&w)[N]) {
-  uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < N; i += 4) {
     uint4 x = make_uint4(0, 0, 0, 0);
     if (valid) x = __ldg(reinterpret_cast<const uint4 *>(src) + i / 4);
     w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
   }
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    top = max(top, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-  top = max(top, __shfl_xor_sync(~0u, top, 1));
-  top = max(top, __shfl_xor_sync(~0u, top, 2));
-  float f = scale;
-  if (bf16) {
-    // exponents above -86: the power is a normal number
-    const int exp = max((int)(top >> 7), 41) - 127;
-    const float up = __uint_as_float((uint32_t)(14 - exp + 127) << 23);
-    f *= __uint_as_float((uint32_t)(exp - 14 + 127) << 23);
-    if (top >= 0x7f80u) f = __int_as_float(0x7fc00000);
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      w[i] = pack2<__half>(__uint_as_float(w[i] << 16) * up,
-                           __uint_as_float(w[i] & 0xffff0000u) * up);
-  } else if (top >= 0x7c00u) {
-    f = __int_as_float(0x7fc00000);
-  }
-  return f;
+  return fit_query<4>(w, bf16, scale);
 }
 
 constexpr int kKeys = kBlock;  // keys of a place in the shares
