@@ -435,7 +435,8 @@ __device__ __forceinline__ bool weigh_half(Row &row, bool cuts,
 // but for elements 2^-28 of that and below.  The power stops at 2^126, whose
 // inverse is still a normal number: rows below 2^-112 are taken to below 2^14,
 // where bf16's least number, 2^-133, is 2^-7, and nothing is lost at all.  A
-// row with NaN or infinity gets a NaN factor.
+// factor beyond fp32's numbers becomes the greatest of them: times a score of
+// 0 it has to be 0.  A row with NaN or infinity gets a NaN factor.
 template <int LANES, int N>
 __device__ __forceinline__ float fit_query(uint32_t (&w)[N], bool bf16,
                                            float scale) {
@@ -451,6 +452,7 @@ __device__ __forceinline__ float fit_query(uint32_t (&w)[N], bool bf16,
     const int exp = max((int)(top >> 7), 15) - 127;
     const float up = __uint_as_float((uint32_t)(14 - exp + 127) << 23);
     f *= __uint_as_float((uint32_t)(exp - 14 + 127) << 23);
+    f = fminf(f, 0x1.fffffep127f);
     if (top >= 0x7f80u) f = __int_as_float(0x7fc00000);
 #pragma unroll
     for (int i = 0; i < N; ++i)

@@ -25,3 +25,14 @@ def test_attention_queries_near_the_least_numbers(n, Hq, by):
     """bf16 rows down to its subnormal numbers, scores of a usual size."""
     P = ref.Paged4([n, 1], [n + 150, 30], 1, 64, 16, BF, 45, 32)
     run(P, Hq, scale=0.3 / by, q=P.rows(Hq, by=by), max_q=n)
+
+
+@pytest.mark.parametrize("n,Hq", SHAPES)
+def test_attention_a_factor_beyond_32_bits(n, Hq):
+    """Scale times the queries' power of two is above 3.4e38, the scores are
+    0: every key seen counts alike."""
+    P = ref.Paged4([n, 1], [n + 150, 30], 1, 64, 16, BF, 46, 32)
+    P.kn[:], P.kp[:] = ref.quantise(np.zeros_like(P.kn, np.float64), 32)
+    P.k = torch.tensor(ref.values(P.kn, P.kp))
+    q = torch.full((P.total, Hq, 64), 2.0 ** 127, dtype=BF)
+    run(P, Hq, scale=2.0 ** 20, q=q, max_q=n)
