@@ -681,9 +681,10 @@ typedef struct {
  * sd_kv_append into a 4-bit cache: keys (rotated, from fp32, not rounded to
  * 16 bits first) and values are quantised as they are written.
  *
- * With lo and hi the least and the greatest of a group's values, kept inside
- * -6144 .. 6144: a = fp16((hi - lo) c), b = fp16(lo - 64 a), n = rint((x - b)
- * r) - 64 kept inside 0 .. 15 (0 where a is 0), in fp32, every operation
+ * With lo and hi the least and the greatest of a group's values x, all of
+ * them first kept inside -6144 .. 6144: a = fp16((hi - lo) c), b = fp16(lo -
+ * 64 a), n = rint((x - b) r) - 64 kept inside 0 .. 15 (0 where a is 0), in
+ * fp32, every operation
  * rounded by itself, c = 1/15 and r = 1/a rounded too; the rotation's two
  * products and their sum likewise.  An element is off by half a step (hi -
  * lo) / 15, a sixteenth of a step more for b's rounding, and fp16's own

@@ -5,7 +5,7 @@
 // With lo and hi the least and greatest of a group's values,
 //   a = fp16((hi - lo) / 15), b = fp16(lo - 64 a),
 //   n = rint((x - b) / a) - 64, kept inside 0 .. 15,
-// each step rounded to fp32 by itself (no contraction), 1 / 15 and 1 / a being
+// values, lo and hi first brought inside -6144 .. 6144, and each step rounded to fp32 by itself (no contraction), 1 / 15 and 1 / a being
 // rounded first: the codes are the same numbers wherever they are computed.
 //
 // What bounds them: HBM where rows are many (28k tokens of 48 heads of 128,
@@ -129,12 +129,18 @@ __device__ __forceinline__ uint32_t quantise8(const float2 (&x)[4], int lanes,
   // with their shifts, what lies above the codes is a constant modulo 2^32
   const float2 minus_b = make_float2(-bf, -bf), inv2 = make_float2(inv, inv);
   const float2 magic = make_float2(12582912.f, 12582912.f);
+  // Numbers beyond lo and hi count as these: every step here keeps the order,
+  // so their places are the limits, two a group for two operations a number.
+  auto place = [&](float y) {
+    return fminf(fmaxf(__fmul_rn(__fadd_rn(y, -bf), inv), 64.f), 79.f);
+  };
+  const float least = place(lo), most = place(hi);
   uint32_t w = 0u - (0x4b400000u + 64) * 0x11111111u;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     float2 t = mul2(add2(x[e], minus_b), inv2);
-    t.x = fminf(fmaxf(t.x, 64.f), 79.f);
-    t.y = fminf(fmaxf(t.y, 64.f), 79.f);
+    t.x = fminf(fmaxf(t.x, least), most);
+    t.y = fminf(fmaxf(t.y, least), most);
     t = add2(t, magic);
     w += __float_as_uint(t.x) << 4 * e;
     w += __float_as_uint(t.y) << 4 * (e + 4);

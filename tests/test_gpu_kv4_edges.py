@@ -36,3 +36,38 @@ def test_attention_a_factor_beyond_32_bits(n, Hq):
     P.k = torch.tensor(ref.values(P.kn, P.kp))
     q = torch.full((P.total, Hq, 64), 2.0 ** 127, dtype=BF)
     run(P, Hq, scale=2.0 ** 20, q=q, max_q=n)
+
+
+# ------------------------------------------------------------------ append
+def inside(x):
+    """x as a group of finite numbers holds it."""
+    return np.clip(x, -ref.MOST, ref.MOST)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 64), (128, 128)])
+@pytest.mark.parametrize("at", [6144, -6144])
+def test_append_beyond_the_end_in_narrow_groups(dtype, D, group, at):
+    """Numbers near +-6144 and some beyond: the codes are those of the numbers
+    kept inside, and what is held stays within their own rounding of them."""
+    sign = 1 if at > 0 else -1
+    P = ref.Paged4([16], [16], 1, D, 16, dtype, 12, group)
+    g = np.random.default_rng(3)
+    x = sign * (6144 - g.integers(0, 9, (16, 2, D)) * g.integers(
+        0, 9, (16, 1, 1)).astype(np.float64))
+    beyond = g.random((16, 2, D)) < 0.1
+    x[beyond] = sign * g.choice([6150.0, 7000.0, 60000.0], beyond.sum())
+    x[3] = np.where(g.random((2, D)) < 0.5, 7000.0, -60000.0)
+    t = torch.tensor(x).to(dtype)
+    cache = P.cache(api)
+    start, kv = P.lengths()
+    api.kv4_append(cache, t[:, :1].cuda(), t[:, 1:].cuda(), start, kv)
+    y = inside(oref.f64(t))
+    for i, (codes, pairs) in enumerate(((cache.k, cache.k_scale),
+                                        (cache.v, cache.v_scale))):
+        want, pair = ref.quantise(y[:, i], group)
+        p = P.table[0, 0]
+        np.testing.assert_array_equal(pairs.cpu().numpy()[p, 0],
+                                      pair.astype(np.float16))
+        np.testing.assert_array_equal(codes.cpu().numpy()[p, 0],
+                                      ref.pack(want))
