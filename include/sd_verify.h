@@ -727,10 +727,14 @@ sd_status sd_kv4_read(const sd_paged_kv4 *cache, const int32_t *q_start,
  * Products are of fp16 numbers with fp32 sums; bf16 queries are brought to
  * fp16 by a power of two a row, exactly but for elements 2^-28 of the row's
  * largest and below (in rows that lie below 2^-112 exactly, whatever their
- * elements are, bf16's subnormal numbers among them).  The weights multiply v rounded to fp16 once, and are off
+ * elements are, bf16's subnormal numbers among them).  A weight multiplies v
+ * as the sum of two fp16 numbers where dt is SD_F16 and max_q x q_heads / heads
+ * is up to 128, otherwise rounded to fp16 once (2^-11 relative: beside bf16's
+ * own rounding, 2^-8 of the result, or as in sd_paged_attention).  It is off
  * by up to 2^-28 of the row's largest besides (with more than 16 rows a head
- * by up to 2^-17 of the largest among the 64 keys of theirs, as there).  A row of q with NaN or infinity gets NaN.  A group of
- * the cache that reads as NaN reaches the tokens that see it, and may reach
+ * by up to 2^-17 of the largest among the 64 keys of theirs, as there).  A row
+ * of q with NaN or infinity gets NaN.  A group of the cache that reads as NaN
+ * reaches the tokens that see it, and may reach
  * others of the sequence; what the cache holds at and past kv_len never does.
  * max_q is a hint as there.
  * Workspace: sd_kv4_attention_workspace(...) bytes with the same max_q.

@@ -63,14 +63,15 @@ sd_status cache_map(const sd_paged_kv *c, void *base, int box,
   return SD_OK;
 }
 
+// With up to 128 rows a weight is two numbers.
 template <class T>
 sd_status dispatch(AttnParams &p, int D, bool pair, const CUtensorMap &km,
                    const CUtensorMap &vm, int sms, char *ws, cudaStream_t s) {
   if (D == 64)
-    return pair ? launch<T, 64, true, false>(p, km, vm, sms, ws, s)
-                : launch<T, 64, false, false>(p, km, vm, sms, ws, s);
-  return pair ? launch<T, 128, true, false>(p, km, vm, sms, ws, s)
-              : launch<T, 128, false, false>(p, km, vm, sms, ws, s);
+    return pair ? launch<T, 64, true, false, false>(p, km, vm, sms, ws, s)
+                : launch<T, 64, false, false, true>(p, km, vm, sms, ws, s);
+  return pair ? launch<T, 128, true, false, false>(p, km, vm, sms, ws, s)
+              : launch<T, 128, false, false, true>(p, km, vm, sms, ws, s);
 }
 
 }  // namespace

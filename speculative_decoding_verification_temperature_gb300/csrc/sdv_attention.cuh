@@ -47,11 +47,13 @@
 //
 // Over a 4-bit cache (CODES) two warps load codes and pairs as they lie, half a
 // tile of 64 keys at a time, and four more make fp16 tiles of them in the same
-// swizzle; products are of fp16 numbers, bf16 queries are scaled to them, and
-// weights are rounded once.  Up to 128 rows (SPLIT): both streams have every
-// tile, a half of its keys each, and one warp issues all products, so that the
-// next tile's scores are made beside this one's weights (32 chunks of 9 tokens
-// 131 us with every other tile a stream, so 116).  One warp that loaded and
+// swizzle; products are of fp16 numbers, bf16 queries are scaled to them.  Up
+// to 128 rows (SPLIT): both streams have every tile, a half of its keys each,
+// and one warp issues all products, so that the next tile's scores are made
+// beside this one's weights (32 chunks of 9 tokens 131 us with every other tile
+// a stream, so 116).  Beside fp16 rows a weight there is two numbers as above;
+// beside bf16 rows fp16's bits are enough (0.00167 off, with two 0.00166; the
+// chunks of 9 tokens take 116 us and would take 131).  One warp that loaded and
 // made a tile took 6400 cycles for it, half of them loading (246 us); 2000
 // cycles of makers, 1800 of softmax and 1700 of products, in rings of two
 // tiles, make 2800 a tile now, where the tile's bytes take 700.  With 256 rows
@@ -362,7 +364,7 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
 // (SPLIT): the maximum first, then the weights in a second pass over the
 // scores, in loops as short as they can be, for the same reason (32 chunks of
 // 9 tokens 117 us; weighed while the maximum is being found 122).
-template <class T, int D>
+template <class T, int D, bool REST>
 __device__ __forceinline__ bool weigh_half(Row &row, bool cuts,
                                            const uint32_t (&seen)[2],
                                            uint64_t *w_full, uint64_t *o_full,
@@ -412,13 +414,14 @@ __device__ __forceinline__ bool weigh_half(Row &row, bool cuts,
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
   for (int c = 0; c < 2; ++c) {
-    uint32_t x[32], w[16];
+    uint32_t x[32], w[16], rest[16];
     tmem_ld32(row.s_addr + 32 * c, x);
     tmem_wait_ld();
     if (cuts) hide32(x, c ? seen[1] : seen[0]);
-    weigh32<T, false>(x, row.sl, off, w, w, sum);
-    // over scores that have been read
-    tmem_st16(row.s_addr + 16 * c, w);
+    weigh32<T, REST>(x, row.sl, off, w, rest, sum);
+    // over the scores that they are the weights of
+    tmem_st16(row.s_addr + 32 * c, w);
+    if (REST) tmem_st16(row.s_addr + 32 * c + 16, rest);
   }
   const float2 t = add2(sum[0], sum[1]);
   row.l += t.x + t.y;
@@ -628,15 +631,14 @@ __device__ __forceinline__ void make_tiles(const AttnParams &p,
 
 // ------------------------------------------------------------- the kernel
 // T: type of the products.  CODES: the cache is in 4 bits, T is fp16, q and
-// out are of the type that p.bf16 says.
-template <class T, int D, bool PAIR, bool CODES>
+// out are of the type that p.bf16 says.  REST: weights are two numbers each.
+template <class T, int D, bool PAIR, bool CODES, bool REST>
 __global__ void __launch_bounds__(attn_threads<CODES>(), 1)
 attention_kernel(const __grid_constant__ AttnParams p,
                  const __grid_constant__ CUtensorMap k_map,
                  const __grid_constant__ CUtensorMap v_map) {
   using L = Layout<D, PAIR, CODES>;
   constexpr int ROWS = L::kRows;
-  constexpr bool REST = !PAIR && !CODES;
   // Up to 128 rows over a 4-bit cache: both streams have every key tile, half
   // of its keys each, and the next tile's scores are made meanwhile.
   constexpr bool SPLIT = CODES && !PAIR;
@@ -821,8 +823,12 @@ attention_kernel(const __grid_constant__ AttnParams p,
                 tmem_fence_after();
 #pragma unroll
                 for (int k = 0; k < kHalf / 16; ++k)
-                  umma_ts<HI>(tmem + 2 * kTile + st * D, w + k * 8,
-                              b + k * 16 * 128 / 16, O_DESC, i > 0 || k > 0);
+#pragma unroll
+                  for (int rest = 0; rest < (REST ? 2 : 1); ++rest)
+                    umma_ts<HI>(tmem + 2 * kTile + st * D,
+                                w + k / 2 * 32 + k % 2 * 8 + rest * 16,
+                                b + k * 16 * 128 / 16, O_DESC,
+                                i > 0 || k > 0 || rest > 0);
                 umma_commit(&s.o_full[st][0]);
                 if (st) umma_commit(&s.empty[1][v_at.slot]);
               }
@@ -1109,9 +1115,9 @@ attention_kernel(const __grid_constant__ AttnParams p,
           }
           __syncwarp();
           if constexpr (SPLIT) {
-            fine = weigh_half<T, D>(row, cuts, seen, &s.w_full[st][buf],
-                                    &s.o_full[st][0], i == 0, tn & 1,
-                                    &s.abort, p.dev_status);
+            fine = weigh_half<T, D, REST>(
+                row, cuts, seen, &s.w_full[st][buf], &s.o_full[st][0], i == 0,
+                tn & 1, &s.abort, p.dev_status);
           } else {
             if (i == 0) row.m = row_max(row.s_addr, cuts, seen);
             fine = cuts ? weigh_tile<T, D, true, REST, CODES>(
@@ -1254,13 +1260,13 @@ attention_kernel(const __grid_constant__ AttnParams p,
 // 256 rows a unit where a chunk has more than 128 of them.
 bool pair_rows(int max_q, int G) { return (long long)max_q * G > kTile; }
 
-template <class T, int D, bool PAIR, bool CODES>
+template <class T, int D, bool PAIR, bool CODES, bool REST>
 sd_status launch(AttnParams &p, const CUtensorMap &k_map,
                  const CUtensorMap &v_map, int sms, char *ws,
                  cudaStream_t s) {
   using L = Layout<D, PAIR, CODES>;
   set_workspace(p, ws_layout(kMaxGrid, L::kRows, D), ws);
-  const void *kernel = (const void *)attention_kernel<T, D, PAIR, CODES>;
+  const void *kernel = (const void *)attention_kernel<T, D, PAIR, CODES, REST>;
   int dev = 0;
   SDV_CUDA(cudaGetDevice(&dev));
   static std::atomic<unsigned long long> ready{0};

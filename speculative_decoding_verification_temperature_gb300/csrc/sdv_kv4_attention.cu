@@ -39,7 +39,13 @@ namespace {
 //
 // A row's weights are fp16, 2^kBias at its reference m, which moves up only
 // when a score is 2^kSlack above it: at most 2^15, and a weight 2^-24 of the
-// reference's still has all its bits.
+// reference's still has all its bits.  Beside rows in fp16 a weight is the sum
+// of two such numbers and O takes a product of each (REST), so that the result
+// is off by little more than its own rounding; one would be as coarse as that
+// (0.00029 off where the rounding is 0.00021).  Beside bf16 rows one number has
+// four times the result's bits to spare: two are 0.00165 off and one 0.00166,
+// and 64 sequences take 99 us with two and 89 with one, one token behind
+// 262144 keys 83 and 76.
 constexpr float kBias = 10.f, kSlack = 5.f;
 constexpr float kNone = 3e38f;  // in place of kBias - m: no reference yet
 constexpr int kBlock = 32;  // keys of a warp's step, two products' rows
@@ -96,7 +102,8 @@ __device__ __forceinline__ float load_query(const void *src, bool valid,
 
 constexpr int kKeys = kBlock;  // keys of a place in the shares
 
-template <int D, int SB, int NT, int WARPS>  // SB: bytes of a key's pairs
+// SB: bytes of a key's pairs.  REST: weights are two numbers each.
+template <int D, int SB, int NT, int WARPS, bool REST>
 __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 2 : 1)
 kv4_rows_kernel(const __grid_constant__ AttnParams p) {
   constexpr int ROWS = 8 * NT, W = D / 32;  // W: words of a key a thread
@@ -346,18 +353,23 @@ kv4_rows_kernel(const __grid_constant__ AttnParams p) {
           va[hf] = __byte_perm(x, z, 0x5410);
           vc[hf] = __byte_perm(x, z, 0x7632);
         }
-        uint32_t w[NT][2];
+        uint32_t w[NT][2], rest[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float z[4];
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            z[e] = ex2(y[b][n][e]);
-            l[n][e & 1] += z[e];
+          for (int hf = 0; hf < 2; ++hf) {
+            const float2 z = make_float2(ex2(y[b][n][2 * hf]),
+                                         ex2(y[b][n][2 * hf + 1]));
+            l[n][0] += z.x;
+            l[n][1] += z.y;
+            if (REST) {
+              split2<__half>(z, w[n][hf], rest[n][hf]);
+              rest[n][hf] = transpose8(rest[n][hf]);
+            } else {
+              w[n][hf] = pack2<__half>(z.x, z.y);
+            }
+            w[n][hf] = transpose8(w[n][hf]);
           }
-          w[n][0] = transpose8(pack2<__half>(z[0], z[1]));
-          w[n][1] = transpose8(pack2<__half>(z[2], z[3]));
-        }
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) {
           uint32_t lo[2], hi[2];
@@ -374,8 +386,12 @@ kv4_rows_kernel(const __grid_constant__ AttnParams p) {
             const uint32_t f2 = kv4_fma(kv4_codes(lo[1], j), va[1], vc[1]);
             const uint32_t f3 = kv4_fma(kv4_codes(hi[1], j), va[1], vc[1]);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) {
               mma16816(o[n][4 * i + j], f0, f1, f2, f3, w[n][0], w[n][1]);
+              if (REST)
+                mma16816(o[n][4 * i + j], f0, f1, f2, f3, rest[n][0],
+                         rest[n][1]);
+            }
           }
         }
       }
@@ -575,7 +591,7 @@ size_t workspace_of(int rows, int D) {
   return ws_layout(rows <= 16 ? kMaxGrid4 : kMaxGrid, rows, D).bytes;
 }
 
-template <int D, int SB, int NT>
+template <int D, int SB, int NT, bool REST>
 sd_status launch_rows(AttnParams &p, int sms, void *ws, cudaStream_t s) {
   // Two CTAs of eight warps an SM where their shared memory lets them (200
   // sequences of 300 keys take 29 us so, and 35 with one of sixteen).
@@ -584,7 +600,7 @@ sd_status launch_rows(AttnParams &p, int sms, void *ws, cudaStream_t s) {
       (sizeof(Shared4<8 * NT, D, WARPS>) + 127) / 128 * 128 +
       WARPS * 2 * kBlock * (D + 2 * SB);
   set_workspace(p, ws_layout(kMaxGrid4, 8 * NT, D), ws);
-  const void *kernel = (const void *)kv4_rows_kernel<D, SB, NT, WARPS>;
+  const void *kernel = (const void *)kv4_rows_kernel<D, SB, NT, WARPS, REST>;
   int dev = 0;
   SDV_CUDA(cudaGetDevice(&dev));
   static std::atomic<unsigned long long> ready{0};
@@ -602,26 +618,35 @@ sd_status launch_rows(AttnParams &p, int sms, void *ws, cudaStream_t s) {
                 : launch_join<__half, D, 8 * NT, kKeys>(p, grid, s);
 }
 
-template <int NT>
+template <int NT, bool REST>
 sd_status dispatch_rows(AttnParams &p, int D, int sms, void *ws,
                         cudaStream_t s) {
   const int sb = p.c.scale_bytes;
   if (D == 64)
-    return sb == 4 ? launch_rows<64, 4, NT>(p, sms, ws, s)
-                   : launch_rows<64, 8, NT>(p, sms, ws, s);
-  return sb == 4   ? launch_rows<128, 4, NT>(p, sms, ws, s)
-         : sb == 8 ? launch_rows<128, 8, NT>(p, sms, ws, s)
-                   : launch_rows<128, 16, NT>(p, sms, ws, s);
+    return sb == 4 ? launch_rows<64, 4, NT, REST>(p, sms, ws, s)
+                   : launch_rows<64, 8, NT, REST>(p, sms, ws, s);
+  return sb == 4   ? launch_rows<128, 4, NT, REST>(p, sms, ws, s)
+         : sb == 8 ? launch_rows<128, 8, NT, REST>(p, sms, ws, s)
+                   : launch_rows<128, 16, NT, REST>(p, sms, ws, s);
 }
 
-template <bool PAIR>
+template <bool PAIR, bool REST>
 sd_status dispatch_tiles(AttnParams &p, int D, int sms, void *ws,
                          cudaStream_t s) {
   const CUtensorMap none = {};  // tiles are not loaded but made
   char *at = static_cast<char *>(ws);
-  return D == 64
-             ? launch<__half, 64, PAIR, true>(p, none, none, sms, at, s)
-             : launch<__half, 128, PAIR, true>(p, none, none, sms, at, s);
+  return D == 64 ? launch<__half, 64, PAIR, true, REST>(p, none, none, sms, at,
+                                                        s)
+                 : launch<__half, 128, PAIR, true, REST>(p, none, none, sms,
+                                                         at, s);
+}
+
+template <bool REST>
+sd_status dispatch_up_to_128(AttnParams &p, int rows, int D, int sms, void *ws,
+                        cudaStream_t s) {
+  return rows == 8    ? dispatch_rows<1, REST>(p, D, sms, ws, s)
+         : rows == 16 ? dispatch_rows<2, REST>(p, D, sms, ws, s)
+                      : dispatch_tiles<false, REST>(p, D, sms, ws, s);
 }
 
 }  // namespace
@@ -701,10 +726,8 @@ extern "C" sd_status sd_kv4_attention(
   p.c = kv4_cache(cache);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   p.bf16 = cache->dt == SD_BF16;
-  switch (rows_of(max_q, p.G)) {
-    case 8: return dispatch_rows<1>(p, D, sms, workspace, s);
-    case 16: return dispatch_rows<2>(p, D, sms, workspace, s);
-    case 128: return dispatch_tiles<false>(p, D, sms, workspace, s);
-    default: return dispatch_tiles<true>(p, D, sms, workspace, s);
-  }
+  const int rows = rows_of(max_q, p.G);
+  if (rows == 256) return dispatch_tiles<true, false>(p, D, sms, workspace, s);
+  return p.bf16 ? dispatch_up_to_128<false>(p, rows, D, sms, workspace, s)
+                : dispatch_up_to_128<true>(p, rows, D, sms, workspace, s);
 }

@@ -38,6 +38,48 @@ def test_attention_a_factor_beyond_32_bits(n, Hq):
     run(P, Hq, scale=2.0 ** 20, q=q, max_q=n)
 
 
+def weight_bound(P, q, scale):
+    """out, and a bound with weights that keep 22 bits (2^-21 of their own
+    size counts twice that) and 2^-28 of the row's largest: what is left is
+    the scores' and sums' 32 bits and the output's own rounding."""
+    u, u32, D = oref.U[P.dtype], oref.U32, P.dim
+    q64 = oref.f64(q)
+    Hq = q64.shape[1]
+    out, tol = np.zeros((P.total, Hq, D)), np.zeros((P.total, Hq, D))
+    for b, (n, kv) in enumerate(zip(P.n, P.kv)):
+        k, v = P.gather(P.k, b), P.gather(P.v, b)
+        for i in range(n):
+            m, r = kv - n + i + 1, P.start[b] + i
+            for h in range(Hq):
+                kh, vh = (x[:m, h // (Hq // P.heads)] for x in (k, v))
+                s = kh @ q64[r, h] * scale
+                w = np.exp(s - s.max())
+                w /= w.sum()
+                d = scale * 2 * u32 * (D + 8) * \
+                    (np.abs(kh) @ np.abs(q64[r, h])).max() + 2.0 ** -20 + \
+                    np.abs(s).max() * 4 * u32
+                out[r, h] = w @ vh
+                tol[r, h] = w @ np.abs(vh) * (2.0 ** -21 + 2 * d +
+                                              2 * m * u32) + \
+                    u * np.abs(out[r, h]) * 1.01 + 2.0 ** -24 + \
+                    m * 2.0 ** -28 * np.abs(vh).max()
+    return out, tol
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,Hq", SHAPES[:3])
+def test_attention_weights_keep_more_bits_than_the_type(n, Hq, D):
+    """Up to 128 rows a head a weight is two fp16 numbers: where values cancel
+    the result is off by less than one would leave."""
+    P = ref.Paged4([n, n], [n + 2, n + 40], 1, D, 16, HF, 47, 32)
+    q = P.rows(Hq, by=0.5)
+    start, kv = P.lengths()
+    got = oref.f64(api.kv4_attention(q.cuda(), P.cache(api), start, kv,
+                                     max_q=n)["out"])
+    out, tol = weight_bound(P, q, D ** -0.5)
+    assert (np.abs(got - out) <= tol).all(), (np.abs(got - out) / tol).max()
+
+
 # ------------------------------------------------------------------ append
 def inside(x):
     """x as a group of finite numbers holds it."""
