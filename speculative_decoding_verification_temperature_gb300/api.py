@@ -203,11 +203,12 @@ _devices = None  # how many there are, once a call has asked
 
 def _call(device, fn, *args):
     """fn(*args) with the tensors' device as the current one (launches go to
-    the current device's context)."""
+    the current device's context).  It is entered where it is not that already:
+    to enter and leave one costs as much as a small call's checks."""
     global _devices
     if _devices is None:
         _devices = torch.cuda.device_count()
-    if _devices > 1 and device.index is not None:
+    if _devices > 1 and device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
             return fn(*args)
     return fn(*args)
