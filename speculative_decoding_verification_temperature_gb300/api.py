@@ -285,7 +285,8 @@ def verify_linear(target, draft, tokens, uniforms, T, *, want_accept=False,
     L = lib()
     nbytes = L.sd_verify_linear_workspace(B, gamma, V, _dt(target))
     ws = (workspace or _default_ws).get(dev, nbytes)
-    _check(L.sd_verify_linear(
+    _check(_call(
+        dev, L.sd_verify_linear,
         _p(target), _p(draft), _dt(target), _p(tokens), _p(uniforms), B,
         gamma, V, float(T), _p(n), _p(toks), _p(prob), _p(acc), _p(res),
         _p(status), _p(ws), ws.numel(), _stream(dev)))
@@ -317,7 +318,8 @@ def verify_linear_static(target, draft, tokens, uniforms, T, *,
     prob = torch.empty(B, dtype=torch.float32, device=dev)
     acc = torch.empty((B, max(gamma, 1)), dtype=torch.float32,
                       device=dev) if want_accept else None
-    _check(lib().sd_verify_linear_static(
+    _check(_call(
+        dev, lib().sd_verify_linear_static,
         _p(target), _p(draft), _dt(target), _p(tokens), _p(uniforms), B,
         gamma, V, float(T), _p(n), _p(toks), _p(prob), _p(acc), None,
         _p(status), _stream(dev)))
@@ -353,7 +355,8 @@ def verify_linear_filtered(target, draft, tokens, uniforms, T, top_k,
     L = lib()
     nbytes = L.sd_verify_linear_filtered_workspace(B, gamma, V, _dt(target))
     ws = (workspace or _default_ws).get(dev, nbytes)
-    _check(L.sd_verify_linear_filtered(
+    _check(_call(
+        dev, L.sd_verify_linear_filtered,
         _p(target), _p(draft), _dt(target), _p(tokens), _p(uniforms), B,
         gamma, V, float(T), int(top_k), float(top_p), _p(n), _p(toks),
         _p(prob), _p(keep), _p(status), _p(ws), ws.numel(), _stream(dev)))
@@ -387,7 +390,8 @@ def verify_kcand(target, draft, tokens, uniforms, T, *, status=None,
     L = lib()
     nbytes = L.sd_verify_kcand_workspace(B, K, gamma, V, _dt(target))
     ws = (workspace or _default_ws).get(dev, nbytes)
-    _check(L.sd_verify_kcand(
+    _check(_call(
+        dev, L.sd_verify_kcand,
         _p(target), _p(draft), _dt(target), _p(tokens), _p(uniforms), B, K,
         gamma, V, float(T), _p(n), _p(ks), _p(toks), _p(npc), _p(prob),
         _p(status), _p(ws), ws.numel(), _stream(dev)))
@@ -417,7 +421,8 @@ def verify_kcand_trie(target, draft, tokens, uniforms, T, *, status=None,
     L = lib()
     nbytes = L.sd_verify_kcand_trie_workspace(B, K, gamma, V, _dt(target))
     ws = (workspace or _default_ws).get(dev, nbytes)
-    _check(L.sd_verify_kcand_trie(
+    _check(_call(
+        dev, L.sd_verify_kcand_trie,
         _p(target), _p(draft), _dt(target), _p(tokens), _p(uniforms), B, K,
         gamma, V, float(T), _p(n), _p(ks), _p(toks), _p(prob), _p(status),
         _p(ws), ws.numel(), _stream(dev)))
@@ -445,7 +450,8 @@ def verify_tree(target, draft, parent, node_tokens, uniforms, T, *,
     L = lib()
     nbytes = L.sd_verify_tree_workspace(B, N, V, _dt(target))
     ws = (workspace or _default_ws).get(dev, nbytes)
-    _check(L.sd_verify_tree(
+    _check(_call(
+        dev, L.sd_verify_tree,
         _p(target), _p(draft), _dt(target), _p(parent), _p(node_tokens),
         _p(uniforms), B, N, V, float(T), _p(n), _p(toks), _p(nodes),
         _p(prob), _p(status), _p(ws), ws.numel(), _stream(dev)))
@@ -470,7 +476,8 @@ def verify_tree_det(target, parent, node_tokens, uniforms, T, *,
     L = lib()
     nbytes = L.sd_verify_tree_det_workspace(B, N, V, _dt(target))
     ws = (workspace or _default_ws).get(dev, nbytes)
-    _check(L.sd_verify_tree_det(
+    _check(_call(
+        dev, L.sd_verify_tree_det,
         _p(target), _dt(target), _p(parent), _p(node_tokens), _p(uniforms),
         B, N, V, float(T), _p(n), _p(toks), _p(nodes), _p(prob), _p(status),
         _p(ws), ws.numel(), _stream(dev)))
@@ -494,11 +501,13 @@ class PrestoTree:
         self.node_score = torch.empty((B, budget), **f32)
         self.frontier_node = torch.empty((B, W), **i32)
         self.frontier_score = torch.empty((B, W), **f32)
-        _check(lib().sd_presto_init(
+        dev = self.n_nodes.device
+        _check(_call(
+            dev, lib().sd_presto_init,
             B, W, budget, _p(self.n_nodes), _p(self.parent),
             _p(self.node_tokens), _p(self.node_score),
             _p(self.frontier_node), _p(self.frontier_score),
-            _stream(torch.device(device))))
+            _stream(dev)))
 
 
 def presto_expand(tree, q_logits, log_rho, T, lam, b_top, *, status=None,
@@ -519,7 +528,8 @@ def presto_expand(tree, q_logits, log_rho, T, lam, b_top, *, status=None,
     nbytes = L.sd_presto_expand_workspace(B, tree.W, V, int(b_top),
                                           _dt(q_logits))
     ws = (workspace or _default_ws).get(dev, nbytes)
-    _check(L.sd_presto_expand(
+    _check(_call(
+        dev, L.sd_presto_expand,
         _p(q_logits), q_logits.stride(0), _p(log_rho), _dt(q_logits), B,
         tree.W, V, float(T), float(lam), int(b_top), tree.budget,
         _p(tree.n_nodes), _p(tree.parent), _p(tree.node_tokens),
@@ -541,9 +551,10 @@ def branch_fork(draft, x_b, T, k_max, *, status=None, workspace=None):
     L = lib()
     nbytes = L.sd_branch_fork_workspace(B, V, int(k_max), _dt(draft))
     ws = (workspace or _default_ws).get(dev, nbytes)
-    _check(L.sd_branch_fork(_p(draft), _dt(draft), _p(x_b), B, V, float(T),
-                            int(k_max), _p(k), _p(toks), _p(status), _p(ws),
-                            ws.numel(), _stream(dev)))
+    _check(_call(
+        dev, L.sd_branch_fork, _p(draft), _dt(draft), _p(x_b), B, V, float(T),
+        int(k_max), _p(k), _p(toks), _p(status), _p(ws), ws.numel(),
+        _stream(dev)))
     return {"k": k, "tokens": toks}
 
 
@@ -554,8 +565,8 @@ def selftest_bounded_wait(polls, device="cuda"):
     dev = torch.device(device)
     st = torch.zeros(1, dtype=torch.int32, device=dev)
     out = torch.zeros(2, dtype=torch.int32, device=dev)
-    _check(lib().sd_selftest_bounded_wait(int(polls), _p(st), _p(out),
-                                          _stream(dev)))
+    _check(_call(st.device, lib().sd_selftest_bounded_wait, int(polls),
+                 _p(st), _p(out), _stream(dev)))
     torch.cuda.synchronize(dev)
     o = out.tolist()
     return int(st.item()), o[0], o[1]
@@ -586,7 +597,8 @@ def fanout_topk(draft, F, *, want_logit=False, status=None, workspace=None):
     L = lib()
     nbytes = L.sd_fanout_topk_workspace(B, K1 - 1, V, _dt(draft))
     ws = (workspace or _default_ws).get(dev, nbytes)
-    _check(L.sd_fanout_topk(
+    _check(_call(
+        dev, L.sd_fanout_topk,
         _p(draft), _dt(draft), B, K1 - 1, V, ctypes.cast(Fh, ctypes.c_void_p),
         _p(toks), _p(lg), _p(status), _p(ws), ws.numel(), _stream(dev)))
     r = {"tokens": toks[:, :total]}
@@ -612,9 +624,9 @@ def fanout_hits(n, tokens, fan_tokens, F):
         raise ValueError("fan_tokens must be [B, sum F]")
     Fh = (ctypes.c_int32 * K1)(*F)
     hit = torch.empty(B, dtype=torch.int32, device=dev)
-    _check(lib().sd_fanout_hits(_p(n), _p(tokens), _p(fan_tokens), B, K1 - 1,
-                                ctypes.cast(Fh, ctypes.c_void_p), _p(hit),
-                                _stream(dev)))
+    _check(_call(
+        dev, lib().sd_fanout_hits, _p(n), _p(tokens), _p(fan_tokens), B,
+        K1 - 1, ctypes.cast(Fh, ctypes.c_void_p), _p(hit), _stream(dev)))
     return hit
 
 
@@ -644,7 +656,8 @@ def verify_linear_fanout(target, draft, tokens, uniforms, T, F, *,
     L = lib()
     nbytes = L.sd_verify_linear_fanout_workspace(B, gamma, V, _dt(target))
     ws = (workspace or _default_ws).get(dev, nbytes)
-    _check(L.sd_verify_linear_fanout(
+    _check(_call(
+        dev, L.sd_verify_linear_fanout,
         _p(target), _p(draft), _dt(target), _p(tokens), _p(uniforms), B,
         gamma, V, float(T), ctypes.cast(Fh, ctypes.c_void_p), _p(n),
         _p(toks), _p(prob), _p(ftok), _p(flog), _p(status), _p(ws),
@@ -1068,7 +1081,8 @@ def distill_topk(student, teacher_logit, teacher_id, T=1.0, *,
         student, teacher_logit, teacher_id, teacher_lse)
     loss = torch.empty(N, dtype=torch.float32, device=dev)
     lse = torch.empty(N, dtype=torch.float32, device=dev)
-    rc = lib().sd_distill_topk(
+    rc = _call(
+        dev, lib().sd_distill_topk,
         student.data_ptr(), rs, dt, lp, ip, tp, N, V, K, T, loss.data_ptr(),
         lse.data_ptr(), _status(status, dev), _raw_stream(dev))
     if rc != SD_OK:
@@ -1088,7 +1102,8 @@ def distill_topk_backward(student, lse, teacher_logit, teacher_id, grad_loss,
     sp = _row_vector(lse, dev, "lse", N)
     wp = _row_vector(grad_loss, dev, "grad_loss", N)
     grad, gs = _grad_out(out, student, dev, N, V)
-    rc = lib().sd_distill_topk_backward(
+    rc = _call(
+        dev, lib().sd_distill_topk_backward,
         student.data_ptr(), rs, dt, sp, lp, ip, tp, wp, N, V, K, T,
         grad.data_ptr(), gs, _status(status, dev), _raw_stream(dev))
     if rc != SD_OK:
@@ -1107,7 +1122,8 @@ def distill_topk_step(student, teacher_logit, teacher_id, grad_loss, T=1.0,
     loss = torch.empty(N, dtype=torch.float32, device=dev)
     lse = torch.empty(N, dtype=torch.float32, device=dev)
     grad, gs = _grad_out(out, student, dev, N, V)
-    rc = lib().sd_distill_topk_step(
+    rc = _call(
+        dev, lib().sd_distill_topk_step,
         student.data_ptr(), rs, dt, lp, ip, tp, wp, N, V, K, T,
         loss.data_ptr(), lse.data_ptr(), grad.data_ptr(), gs,
         _status(status, dev), _raw_stream(dev))

@@ -1,5 +1,8 @@
 """The device that a call of the binding launches on (no GPU: torch's calls
 are replaced)."""
+import ast
+import inspect
+
 import torch
 
 import pytest
@@ -53,3 +56,21 @@ def test_one_device_is_never_asked_for(devices, monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", None)
     api._call(torch.device("cuda", 0), launch(devices))
     assert devices == [("call", ())]
+
+
+def test_every_launch_goes_to_its_tensors_device():
+    """Each call that takes a stream is made through _call."""
+    tree = ast.parse(inspect.getsource(api))
+    made = direct = 0
+    for node in ast.walk(tree):
+        if not isinstance(node, ast.Call):
+            continue
+        if not any(isinstance(a, ast.Call) and isinstance(a.func, ast.Name)
+                   and a.func.id in ("_stream", "_raw_stream")
+                   for a in node.args):
+            continue
+        if ast.unparse(node.func) == "_call":
+            made += 1
+        else:
+            direct += 1
+    assert made >= 20 and direct == 0
