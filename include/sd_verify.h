@@ -684,12 +684,14 @@ typedef struct {
  * With lo and hi the least and the greatest of a group's values x, all of
  * them first kept inside -6144 .. 6144: a = fp16((hi - lo) c), b = fp16(lo -
  * 64 a), n = rint((x - b) r) - 64 kept inside 0 .. 15 (0 where a is 0), in
- * fp32, every operation
- * rounded by itself, c = 1/15 and r = 1/a rounded too; the rotation's two
- * products and their sum likewise.  An element is off by half a step (hi -
- * lo) / 15, a sixteenth of a step more for b's rounding, and fp16's own
- * rounding; values beyond 6144 are held as that.  A group that holds NaN or
- * infinity reads as NaN.
+ * fp32, every operation rounded by itself, c = 1/15 and r = 1/a rounded too;
+ * the rotation's two products and their sum likewise.  An element is off by
+ * up to half a step (hi - lo) / 15; by half the distance of fp16 numbers at
+ * lo - 64 a, b's rounding (1/32 of a step in groups about zero, 2^-11 |lo -
+ * 64 a| at most, which is several steps of a narrow group far from zero); by
+ * a's rounding, 15 steps x 2^-11, or 15 x 2^-25 near fp16's least numbers; and
+ * by fp16's own rounding.  Values beyond 6144 count as that.  A group that
+ * holds NaN or infinity reads as NaN.
  *
  * All arguments, and what happens to tokens that cannot be placed, as in
  * sd_kv_append.

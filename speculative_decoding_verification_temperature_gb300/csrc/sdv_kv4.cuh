@@ -6,9 +6,11 @@
 // code's four bits at bits 4 to 7 of 0x5400 are the number 64 + n: a pair of
 // values is one logic operation and one fma of fp16 pairs, with a single
 // rounding, on every path that reads the cache.  (With b + n a the 64 would
-// cost a subtraction a pair: half as much again.)  b is coarser for it, a
-// sixteenth of a step, which the codes are chosen by; so are values beyond
-// kMost, which leaves 64 steps of a group inside fp16.
+// cost a subtraction a pair: half as much again.)  b is coarser for it: fp16
+// numbers at lo - 64 a lie up to a sixteenth of a step apart in groups about
+// zero, and 2^-10 of the offset in those far from it; the codes are chosen by
+// the b that is kept.  Values beyond kMost count as that, so that 79 steps of
+// a group stay inside fp16.
 //
 // A word of codes holds eight neighbours, elements 0, 2, 4, 6, 1, 3, 5, 7
 // from its lowest nibble on: a mask then finds neighbours (2 j, 2 j + 1).
