@@ -9,8 +9,8 @@
 // cost a subtraction a pair: half as much again.)  b is coarser for it: fp16
 // numbers at lo - 64 a lie up to a sixteenth of a step apart in groups about
 // zero, and 2^-10 of the offset in those far from it; the codes are chosen by
-// the b that is kept.  Values beyond kMost count as that, so that 79 steps of
-// a group stay inside fp16.
+// the b that is kept.  Values beyond kMost count as that, so that b, 64 steps
+// below a group, stays inside fp16.
 //
 // A word of codes holds eight neighbours, elements 0, 2, 4, 6, 1, 3, 5, 7
 // from its lowest nibble on: a mask then finds neighbours (2 j, 2 j + 1).

@@ -8,7 +8,7 @@ import torch
 from speculative_decoding_verification_temperature_gb300 import api
 from tests import kv4_ref as ref
 from tests import operators_ref as oref
-from tests.test_gpu_kv4 import i32, lengths, run, run_append
+from tests.test_gpu_kv4 import run
 
 pytestmark = pytest.mark.gpu
 
@@ -80,6 +80,25 @@ def test_attention_weights_keep_more_bits_than_the_type(n, Hq, D):
     assert (np.abs(got - out) <= tol).all(), (np.abs(got - out) / tol).max()
 
 
+@pytest.mark.parametrize("hint", [2, 4, 30, 100])
+@pytest.mark.parametrize("masked", [False, True])
+def test_attention_more_sequences_than_a_block_takes_at_once(hint, masked):
+    """601 short ragged sequences, some of them empty, planned 256 at a time;
+    hints that pick each kernel."""
+    r = np.random.default_rng(8)
+    n = r.integers(0, 4, 601)
+    n[::7] = 0
+    kv = n + r.integers(0, 90, 601)
+    kv[5::50] += 300
+    P = ref.Paged4(n.tolist(), kv.tolist(), 2, 64, 16, BF, 48, 32)
+    see = None
+    if masked:
+        see = [np.tril(np.ones((m, m), bool)) for m in n]
+        for t in see[::3]:
+            t[:, :-1] = False  # the last token sees itself, others only keys
+    run(P, 8, max_q=hint, see=see)
+
+
 # ------------------------------------------------------------------ append
 def inside(x):
     """x as a group of finite numbers holds it."""
@@ -113,3 +132,51 @@ def test_append_beyond_the_end_in_narrow_groups(dtype, D, group, at):
                                       pair.astype(np.float16))
         np.testing.assert_array_equal(codes.cpu().numpy()[p, 0],
                                       ref.pack(want))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,rot", [(64, 64), (128, 128), (128, 48)])
+def test_append_an_angle_table_at_any_address(interleaved, D, rot):
+    """A table that starts 4, 8 or 12 bytes past 16-byte alignment: the bits
+    of the aligned one, keys, values and queries."""
+    P = ref.Paged4([40, 1, 7], [90, 30, 7], 2, D, 16, BF, 13, 32)
+    x = P.rows(8).cuda()
+    start, kv = P.lengths()
+    tab = oref.cos_sin_table(90, rot).cuda()
+
+    def call(table):
+        cache = P.cache(api)
+        q = api.kv4_append(cache, x[:, 4:6], x[:, 6:], start, kv, q=x[:, :4],
+                           cos_sin=table, interleaved=interleaved)
+        return [q, cache.k, cache.v, cache.k_scale.view(torch.int16),
+                cache.v_scale.view(torch.int16)]
+
+    want = call(tab)
+    for off in (1, 2, 3):
+        store = torch.full((tab.numel() + 4,), float("nan"), device="cuda")
+        odd = store[off:off + tab.numel()].view(tab.shape)
+        odd.copy_(tab)
+        assert odd.data_ptr() % 16 == 4 * off
+        for a, b in zip(call(odd), want):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rot", [64, 32, 34])
+def test_append_rotated_rows_at_any_address(dtype, interleaved, rot):
+    """Rows that are not 16-byte aligned, turned: the bits of aligned ones."""
+    P = ref.Paged4([30, 2], [70, 9], 2, 64, 8, dtype, 14, 32)
+    start, kv = P.lengths()
+    tab = oref.cos_sin_table(70, rot).cuda()
+    wide = torch.randn((32, 8 * 64 + 3), device="cuda").to(dtype)
+    odd = wide[:, 1:513].unflatten(1, (8, 64))
+    got = []
+    for x in (odd, odd.contiguous()):
+        cache = P.cache(api)
+        q = api.kv4_append(cache, x[:, 4:6], x[:, 6:], start, kv, q=x[:, :4],
+                           cos_sin=tab, interleaved=interleaved)
+        got.append([q, cache.k, cache.v, cache.k_scale.view(torch.int16),
+                    cache.v_scale.view(torch.int16)])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
