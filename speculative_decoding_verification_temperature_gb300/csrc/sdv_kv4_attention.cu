@@ -525,9 +525,7 @@ kv4_rows_kernel(const __grid_constant__ AttnParams p) {
           if (w > w0 && !s.info[w][0].there) continue;
           const Part<ROWS, D> &x = part_of(w);
           const float2 a = x.ml[r];
-          // 0 for a part that saw nothing, NaN for one with a NaN sum
-          const float k = a.x == -kInf ? (a.y == a.y ? 0.f : a.y)
-                                       : ex2(a.x - top);
+          const float k = part_weight(a, top);
           sum += a.y * k;
 #pragma unroll
           for (int e = 0; e < E; ++e) {

@@ -315,6 +315,12 @@ __device__ __forceinline__ uint32_t pack2<__half>(float lo, float hi) {
   return u;
 }
 
+// What a part with reference ml.x and sum ml.y counts beside a reference m: 0
+// if it saw nothing (or is none), NaN if its sum is NaN.
+__device__ __forceinline__ float part_weight(float2 ml, float m) {
+  return ml.x == -kInf ? (ml.y == ml.y ? 0.f : ml.y) : ex2(ml.x - m);
+}
+
 // A row of a cut unit from its parts (a warp), kAhead of them read at once.
 template <class T, int D, int ROWS, int kAhead>
 __device__ __forceinline__ void join_row(const UnitParams &p,
@@ -335,10 +341,7 @@ __device__ __forceinline__ void join_row(const UnitParams &p,
   float l = 0.f, o[E] = {};
   for (int k0 = 0; k0 < cut.parts; k0 += 32) {
     if (k0) ml = part(k0 + lane);
-    // lane k has the weight of part k0 + k: 0 for one that saw nothing (or
-    // is none), NaN for one with a NaN sum
-    const float w = ml.x == -kInf ? (ml.y == ml.y ? 0.f : ml.y)
-                                  : ex2(ml.x - m);
+    const float w = part_weight(ml, m);  // of part k0 + lane
     l += ml.y * w;
     const int n = min(cut.parts - k0, 32);
     for (int k = 0; k < n; k += kAhead) {
