@@ -56,10 +56,10 @@
 // chunks of 9 tokens take 116 us and would take 131).  One warp that loaded and
 // made a tile took 6400 cycles for it, half of them loading (246 us); 2000
 // cycles of makers, 1800 of softmax and 1700 of products, in rings of two
-// tiles, make 2800 a tile now, where the tile's bytes take 700.  With 256 rows
-// 680 us on the two prompt chunks (1.2 PFLOP/s), where 16-bit keys take 557:
-// the warps wait for instructions (1.9 of 8 stalled at a time against 1.1), not
-// for the makers, which could make a quarter as much in the same time.
+// tiles, make 2800 a tile now, where the tile's bytes take 700: the stages wait
+// for one another.  With 256 rows 690 us on the two prompt chunks (1.2 PFLOP/s,
+// tensor pipe 0.50), where 16-bit keys take 557: not for the makers, which
+// could make a quarter as much in the same time.
 //
 // A wait that gives up (see role_wait) stops the loads and the products; all
 // other steps go on over meaningless data to the end of the share, so that
@@ -140,7 +140,8 @@ template <int D, bool PAIR, bool CODES> struct Layout {
                              : PAIR     ? 4
                                         : 5;
   // CODES: codes and pairs of 64 keys (or values), half a tile, in a ring of
-  // their own for each ring of tiles.
+  // their own for each ring of tiles: six halves where they fit (32 chunks of 9
+  // tokens 115 us, with three 119), three beside 256 rows of queries.
   static constexpr int kRaw = D == 128 ? (PAIR ? 3 : 6) : 6;
   static constexpr int kRawBytes = 64 * (D / 2 + D / 8);
   static constexpr size_t kTiles =
@@ -363,7 +364,7 @@ __device__ __forceinline__ bool weigh_tile(Row &row, const uint32_t *seen,
 // The weights of one row in half a tile, where the stream has a half of each
 // (SPLIT): the maximum first, then the weights in a second pass over the
 // scores, in loops as short as they can be, for the same reason (32 chunks of
-// 9 tokens 117 us; weighed while the maximum is being found 122).
+// 9 tokens 116 us; weighed while the maximum is being found 122).
 template <class T, int D, bool REST>
 __device__ __forceinline__ bool weigh_half(Row &row, bool cuts,
                                            const uint32_t (&seen)[2],

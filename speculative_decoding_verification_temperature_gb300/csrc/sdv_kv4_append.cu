@@ -8,10 +8,14 @@
 // values, lo and hi first brought inside -6144 .. 6144, and each step rounded to fp32 by itself (no contraction), 1 / 15 and 1 / a being
 // rounded first: the codes are the same numbers wherever they are computed.
 //
-// What bounds them: HBM where rows are many (28k tokens of 48 heads of 128,
-// fp16, are 608 MB in 128 us, 0.70 of the measured copy rate, with 0.57 of the
-// issue slots; 99k tokens of 8 heads are read back, 0.52 GB, in 88 us, 0.88),
-// and the chain sequence -> page -> store where they are few.
+// Where rows are many, what they wait for is HBM: 28k tokens of 48 heads of
+// 128, fp16, neighbours turned, are 611 MB in 133 us, 0.69 of the measured copy
+// rate, with 0.6 of the issue slots; of 12.2 warps at an issue 6.4 wait for a
+// load, and registers are all taken.  Halves turned take 186 us (a second load
+// a piece, which the registers do not hold: 112 bytes of spills, and 8.5 of
+// 14.4 warps wait), none turned 164; rows that are not whole 16-byte pieces
+// 302.  99k tokens of 8 heads are read back, 0.52 GB, in 87 us, 0.89.  Where
+// rows are few it is the chain sequence -> page -> store.
 #include "sdv_kv4.cuh"
 
 namespace sdv {
@@ -162,7 +166,9 @@ struct Piece {
 // of 16 and rows are 16-byte aligned, so that pieces are whole 16-byte loads
 // and turn as a whole; otherwise elements are loaded one by one.  (A CTA a row
 // looked up the row's place and read its angles in each of eight warps: 208 us
-// on the 28k tokens, and 128 with a warp a row.)
+// on the 28k tokens, and 133 with a warp a row.)  Four CTAs an SM: with three,
+// where no instance of whole pieces spills, neighbours take 143 us, halves 195
+// and rows without a turn 179; with two 143, 259 and 238.
 constexpr int kBatch = 4;
 template <class T, int D, bool WIDE, bool NEIGHBOURS>
 __global__ void __launch_bounds__(kThreads, 4)
@@ -500,7 +506,9 @@ extern "C" sd_status sd_kv4_append(
                     : append_of<__half, 64>(wide, nb))
               : (bf ? append_of<__nv_bfloat16, 128>(wide, nb)
                     : append_of<__half, 128>(wide, nb));
-  // as many warps a row as find a place, but no more than it has work for
+  // as many warps a row as find a place (32 an SM are resident at a time), but
+  // no more than it has work for: 1216 tokens, halves turned, take 10.8 us with
+  // four warps a row, 14.5 with two and 12.9 with eight
   const long long most = Hq > 2 * cache->heads ? Hq : 2 * cache->heads;
   p.warps = 1;
   while (p.warps < kWarps && (long long)total * p.warps < 32 * sms &&

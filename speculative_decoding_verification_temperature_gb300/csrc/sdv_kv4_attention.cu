@@ -25,12 +25,14 @@ namespace {
 // that brought tiles of 128 keys by bulk copies, four a page, was held up by
 // their number: 56 cycles a copy, 154 us on 64 sequences of pages of 16.)
 //
-// What bounds it: making numbers of codes.  32 values of a key are 4 masks, 2
-// shifts, 2 subtractions and 4 fmas for each 8, and 16 keys of 128 take 345
-// instructions in all, 86 cycles of an SM's issue slots, where their bytes take
-// 89 at HBM's rate.  Four warps a scheduler fill 0.6 of the slots: 88 us on 64
-// sequences (0.40 GB, 4.5 TB/s, 0.67 of the measured copy rate), 66 us and a
-// join of 8 on one token behind 262144 keys.
+// What it spends its time on: making numbers of codes.  A word, eight values,
+// is 4 masks, a shift, 2 subtractions and 4 fmas; 16 keys of 128 are 16 words a
+// lane and 340 instructions in all, 41 ns of an SM's issue slots (2.07 GHz),
+// where their bytes take 52 at the measured copy rate.  No pipe is full: four
+// warps a scheduler issue in 0.6 of the slots, and of 6.1 warps at an issue 1.3
+// wait for the result before, 1.0 for a pipe and 0.7 to be dispatched, 0.3 for
+// memory.  88 us on 64 sequences (0.40 GB, 4.5 TB/s, 0.67 of the copy rate), 67
+// us and a join of 8 on one token behind 262144 keys.
 //
 // The units' shares are per warp, in places of 32 keys; what the warps of a CTA
 // have of one unit they join in shared memory at the end, what CTAs have of one
@@ -42,10 +44,10 @@ namespace {
 // reference's still has all its bits.  Beside rows in fp16 a weight is the sum
 // of two such numbers and O takes a product of each (REST), so that the result
 // is off by little more than its own rounding; one would be as coarse as that
-// (0.00029 off where the rounding is 0.00021).  Beside bf16 rows one number has
-// four times the result's bits to spare: two are 0.00165 off and one 0.00166,
-// and 64 sequences take 99 us with two and 89 with one, one token behind
-// 262144 keys 83 and 76.
+// (0.00029 off where the rounding is 0.00021).  Beside bf16 rows one number's
+// rounding is an eighth of the result's: two are 0.00165 off and one 0.00166,
+// and 64 sequences take 98 us with two and 88 with one, one token behind
+// 262144 keys 82 and 75.
 constexpr float kBias = 10.f, kSlack = 5.f;
 constexpr float kNone = 3e38f;  // in place of kBias - m: no reference yet
 constexpr int kBlock = 32;  // keys of a warp's step, two products' rows
@@ -592,7 +594,12 @@ size_t workspace_of(int rows, int D) {
 template <int D, int SB, int NT, bool REST>
 sd_status launch_rows(AttnParams &p, int sms, void *ws, cudaStream_t s) {
   // Two CTAs of eight warps an SM where their shared memory lets them (200
-  // sequences of 300 keys take 29 us so, and 35 with one of sixteen).
+  // sequences of 300 keys take 29 us so, and 35 with one of sixteen); with
+  // pairs of 32 elements at D = 128 it does not, and one of sixteen takes 92 us
+  // on 64 sequences, one of eight 110.  16 rows a head hold twice as much a
+  // warp: one CTA of twelve, as many as shared memory holds at D = 128: 137
+  // us on 64 sequences (its spills of 200 bytes included; eight warps, which
+  // spill nothing, take 132, ten 153), at D = 64 81 (eight 88, sixteen 81).
   constexpr int WARPS = NT == 2 ? 12 : D == 128 && SB == 16 ? 16 : 8;
   constexpr size_t smem =
       (sizeof(Shared4<8 * NT, D, WARPS>) + 127) / 128 * 128 +
