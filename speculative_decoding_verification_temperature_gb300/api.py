@@ -1018,7 +1018,9 @@ def kv4_attention(q, cache, q_start, kv_len, *, max_q=None, scale=None,
     """Attention of a chunk of new tokens per sequence over a PagedKV4
     (sd_kv4_attention); their keys and values are appended before.
     Arguments and results as in paged_attention; keys and values are the
-    fp16 numbers that the codes stand for."""
+    fp16 numbers that the codes stand for.  Weights multiply them as fp16
+    numbers: float16 rows have two a weight unless max_q x q_heads / heads is
+    above 128, bfloat16 rows one."""
     _in_4_bits(cache, True)
     L = lib()
     return _attention(L.sd_kv4_attention, L.sd_kv4_attention_workspace, q,
