@@ -736,9 +736,8 @@ sd_status sd_kv4_read(const sd_paged_kv4 *cache, const int32_t *q_start,
  * by up to 2^-28 of the row's largest besides (with more than 16 rows a head
  * by up to 2^-17 of the largest among the 64 keys of theirs, as there).  A row
  * of q with NaN or infinity gets NaN.  A group of the cache that reads as NaN
- * reaches the tokens that see it, and may reach
- * others of the sequence; what the cache holds at and past kv_len never does.
- * max_q is a hint as there.
+ * reaches the tokens that see it, and may reach others of the sequence; what
+ * the cache holds at and past kv_len never does.  max_q is a hint as there.
  * Workspace: sd_kv4_attention_workspace(...) bytes with the same max_q.
  * ------------------------------------------------------------------- */
 size_t sd_kv4_attention_workspace(int q_heads, int heads, int head_dim,
